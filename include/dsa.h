@@ -520,6 +520,94 @@ int dsa_forward_host(const dsa_forward_buffers* b, int n_docs, int T, int Hi, in
                      int H, int Dqk, int Dv, float scale, int chunks, cudaStream_t compute,
                      cudaStream_t copy);
 
+/* ---- 8-bit block cache.  Keys and values kept as E4M3 codes with one scale
+ * per (block of tokens, head):
+ *   cache uint8 [n_blocks, block, Hc, D], scale fp32 [n_blocks, Hc]; the value
+ *   of a code is e4m3(code) * scale[its block, its head].
+ * Where a batch's rows live: sequence b holds packed tokens cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 (int32 [n_seqs + 1], from 0, non-decreasing; tokens from
+ * cu_seqlens[n_seqs] to T-1 are padding) at positions pos[b] + local index.
+ *   block_table int32 [n_seqs, max_blocks]: position p of sequence b is row
+ *       block_table[b, p / block] * block + p % block; an entry outside [0,
+ *       n_blocks) means "not mapped".
+ *   block_table NULL: position p is cache row p (max_blocks is ignored).
+ *   pos int32 [n_seqs] or NULL: NULL is 0 with a table and cu_seqlens[b]
+ *       without one (row t of the batch is row t of the cache).
+ * With block = 1, no table and pos NULL a call quantises plain rows: one
+ * positive fp32 scale per (row, head), the codes and descales that
+ * dsa_indexer_scores_fp8 / dsa_indexer_topk_fp8 take for qi8 (Hc = Hi) and
+ * ki8 (Hc = 1).
+ * Shapes: block a power of two <= DSA_KV8_MAX_BLOCK, D a multiple of 16 <=
+ * DSA_KV8_MAX_DIM, 1 <= Hc <= DSA_KV8_MAX_HEADS, n_blocks * block < 2^31;
+ * cache and bf16 rows 16-byte aligned. */
+#define DSA_KV8_MAX_BLOCK 256
+#define DSA_KV8_MAX_DIM 1024
+#define DSA_KV8_MAX_HEADS 1024
+
+/* Quantises rows as they are written into the cache.
+ *   src bf16 [T, Hc, D]; cache, scale (in, out).
+ * For every (block, head) that receives rows, with a the largest |x| over
+ * their finite values: s_new = 2^e, e the smallest integer with a <= 448 * 2^e,
+ * not below -126.  If the first new row is the block's first row, its scale
+ * becomes s_new.  Otherwise the rows before it are the sequence's own earlier
+ * ones: the scale becomes s = max(s_old, s_new), and where it grew they are
+ * rescaled, code = e4m3(value(code) * (s_old / s)).  New codes are e4m3(x / s),
+ * to nearest even; infinities become +-448, NaN stays NaN.  s is a power of
+ * two whenever every earlier scale was, and then reading back gives the bf16
+ * of a code exactly.  Rows behind the new ones, blocks that receive none and
+ * tokens whose position is not mapped are left alone.
+ * Contract (not checked, device data): a block receives rows from one
+ * sequence per call, through one table entry.  Other uses leave the codes and
+ * the scale of that block unspecified.
+ * Errors: DSA_ERR_VALUE. */
+int dsa_kv8_write(const void* src, const int32_t* cu_seqlens, const int32_t* pos, const int32_t* block_table,
+                  int n_seqs, int T, int Hc, int D, int block, int n_blocks, int max_blocks, void* cache,
+                  float* scale, cudaStream_t stream);
+
+/* Reads rows back, packed: out bf16 [T, Hc, D] (out), out[t] = e4m3(code) *
+ * scale in fp32, rounded to bf16 (exact for the writer's power-of-two scales),
+ * for each token's row, 0 where its position is not mapped.  Padding tokens'
+ * rows of out are left as they were.  Positions may be shared between sequences.
+ * Errors: DSA_ERR_VALUE. */
+int dsa_kv8_read(const void* cache, const float* scale, const int32_t* cu_seqlens, const int32_t* pos,
+                 const int32_t* block_table, int n_seqs, int T, int Hc, int D, int block, int n_blocks,
+                 int max_blocks, void* out, cudaStream_t stream);
+
+/* Sparse attention forward over the 8-bit cache: dsa_sparse_attn_fwd with K
+ * and V read as codes, and with Hc KV heads (query head h reads KV head
+ * h / (H / Hc)).  For row t, head h and valid slot j (as there: j <
+ * clamp(topk_length[t], 0, K) and a mapped id), r_j its cache row, b_j its block:
+ *   s_j = scale * kv_scale[b_j, kvh] * sum_c q[t,h,c] * e4m3(kv8[r_j, kvh, c]),
+ *   Z = sum_j exp(s_j) + exp(sink[h]),
+ *   out[t,h,:] = sum_j exp(s_j) * V_j / Z,
+ * V_j = v_scale[b_j, kvh] * e4m3(v8[r_j, kvh, :]), or the first Dv values of
+ * the kv8 row when v8 is NULL.
+ *   q bf16 [T, H, Dqk]; kv8 uint8 [n_blocks, block, Hc, Dqk], kv_scale fp32
+ *   [n_blocks, Hc]; v8 uint8 [n_blocks, block, Hc, Dv] and v_scale, or both NULL;
+ *   idx int32 [T, K]: cache rows without a block table; with one, positions
+ *   in the sequence of token t (cu_seqlens over the T query rows), and rows
+ *   t >= cu_seqlens[n_seqs] of the outputs are left as they were.  Without a
+ *   table cu_seqlens, n_seqs and max_blocks are ignored.
+ *   topk_length, sink, out, lse, lse_kv, max_logits as dsa_sparse_attn_fwd
+ *   (empty rows too: out 0, lse sink or -inf, lse_kv +inf, max_logits -inf).
+ *   Scales must be positive and finite (device contract).  Codes of rows that
+ *   no valid slot names are never used, whatever they hold.
+ *   workspace: dsa_sparse_attn_fwd_kv8_workspace_size bytes (0 for many
+ *   shapes: then it may be NULL), 256-byte aligned, contents ignored on
+ *   entry; calls that may overlap need one each.
+ * Accumulation is fp32.  Results are bitwise reproducible.
+ * Shapes: (Dqk, Dv) in {(576, 512), (512, 512)} without v8, or (256, 256) with
+ * it; H a multiple of Hc, H / Hc <= 128; K >= 0; scale finite > 0; q, kv8, v8,
+ * out 16-byte aligned.
+ * Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
+size_t dsa_sparse_attn_fwd_kv8_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K);
+int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const float* kv_scale, const void* v8,
+                            const float* v_scale, const int32_t* idx, const int32_t* topk_length,
+                            const float* sink, const int32_t* cu_seqlens, const int32_t* block_table, int n_seqs,
+                            int T, int H, int Hc, int Dqk, int Dv, int K, int block, int n_blocks, int max_blocks,
+                            float scale, void* out, float* lse, float* lse_kv, float* max_logits,
+                            void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* Route packing ([NeMo-QSA] _pack_indices): routes int32 [B, S, W] hold
  * batch-local ids; out int32 [B*S, Wp] with Wp = ceil(W/4)*4 receives
  * b*S + id for 0 <= id < S and -1 otherwise (including slots W..Wp-1).

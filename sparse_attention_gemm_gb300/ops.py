@@ -71,6 +71,10 @@ _SIGNATURES = {
     "dsa_sparse_attn_bwd_workspace_size": ([I, I, I, I], SZ),
     "dsa_sparse_attn_bwd": ([P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, SZ, P], I),
     "dsa_sparse_attn_bwd_workspace_size_ex": ([I, I, I, I, I], SZ),
+    "dsa_kv8_write": ([P, P, P, P, I, I, I, I, I, I, I, P, P, P], I),
+    "dsa_kv8_read": ([P, P, P, P, P, I, I, I, I, I, I, I, P, P], I),
+    "dsa_sparse_attn_fwd_kv8_workspace_size": ([I, I, I, I, I, I], SZ),
+    "dsa_sparse_attn_fwd_kv8": ([P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
     "dsa_sparse_attn_bwd_ex": ([P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, I, P, SZ, P], I),
 }
 
@@ -602,3 +606,141 @@ def sparse_attn_bwd(q, kv, out, dout, lse_kv, idx, scale: float, topk_length=Non
                                         _p(d_sink), 1 if deterministic else 0, _p(workspace),
                                         workspace.numel() * workspace.element_size(), _stream()))
     return {"dq": dq, "dkv": dkv, "d_sink": d_sink}
+
+
+def _need_here(**tensors):
+    """The call goes to the current device's current stream: so do its tensors."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _kv8_cache(cache, scale, name="cache"):
+    _need(cache, name, torch.uint8, 4)
+    _need(scale, f"{name}_scale", torch.float32, 2)
+    n_blocks, block, heads, dim = cache.shape
+    if scale.shape[0] != n_blocks or scale.shape[1] != heads:
+        raise ValueError(f"{name}_scale must be [{n_blocks}, {heads}], got {tuple(scale.shape)}")
+    return n_blocks, block, heads, dim
+
+
+def _kv8_sequences(cu_seqlens, pos, block_table):
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    n_seqs = cu_seqlens.shape[0] - 1
+    if pos is not None:
+        _need(pos, "pos", torch.int32, 1)
+        if pos.shape[0] != n_seqs:
+            raise ValueError(f"pos must have {n_seqs} entries, got {pos.shape[0]}")
+    width = 0
+    if block_table is not None:
+        _need(block_table, "block_table", torch.int32, 2)
+        if block_table.shape[0] != n_seqs:
+            raise ValueError(f"block_table must have {n_seqs} rows, got {block_table.shape[0]}")
+        width = block_table.shape[1]
+    return n_seqs, width
+
+
+def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
+    """Quantises the bf16 rows src [T, Hc, D] into the E4M3 block cache (uint8
+    [n_blocks, block, Hc, D], scale fp32 [n_blocks, Hc]), in place; returns both."""
+    _need(src, "src", torch.bfloat16, 3)
+    n_blocks, block, heads, dim = _kv8_cache(cache, cache_scale)
+    n_seqs, width = _kv8_sequences(cu_seqlens, pos, block_table)
+    T = src.shape[0]
+    if src.shape[1] != heads or src.shape[2] != dim:
+        raise ValueError(f"src must be [T, {heads}, {dim}], got {tuple(src.shape)}")
+    _need_here(src=src, cache=cache, cache_scale=cache_scale, cu_seqlens=cu_seqlens, pos=pos, block_table=block_table)
+    _check("dsa_kv8_write", lib().dsa_kv8_write(_p(src), _p(cu_seqlens), _p(pos), _p(block_table), n_seqs, T, heads,
+                                                dim, block, n_blocks, width, _p(cache), _p(cache_scale), _stream()))
+    return cache, cache_scale
+
+
+def kv8_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None, out=None):
+    """Rows of the 8-bit block cache back to packed bf16 [T, Hc, D] (rows of an
+    `out` that is given stay as they are behind the last sequence)."""
+    n_blocks, block, heads, dim = _kv8_cache(cache, cache_scale)
+    n_seqs, width = _kv8_sequences(cu_seqlens, pos, block_table)
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=cache.device)
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape[0] != T or out.shape[1] != heads or out.shape[2] != dim:
+            raise ValueError(f"out must be [{T}, {heads}, {dim}], got {tuple(out.shape)}")
+    _need_here(cache=cache, cache_scale=cache_scale, cu_seqlens=cu_seqlens, pos=pos, block_table=block_table, out=out)
+    _check("dsa_kv8_read", lib().dsa_kv8_read(_p(cache), _p(cache_scale), _p(cu_seqlens), _p(pos), _p(block_table),
+                                              n_seqs, T, heads, dim, block, n_blocks, width, _p(out), _stream()))
+    return out
+
+
+def sparse_attn_fwd_kv8_workspace_size(T: int, H: int, Hc: int, Dqk: int, Dv: int, K: int) -> int:
+    return int(lib().dsa_sparse_attn_fwd_kv8_workspace_size(T, H, Hc, Dqk, Dv, K))
+
+
+def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, sink=None, v8=None, v_scale=None,
+                        cu_seqlens=None, block_table=None, want_lse_kv: bool = False, want_max_logits: bool = False,
+                        out=None, lse=None, workspace=None):
+    """Sparse attention forward over the 8-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
+    idx holds cache rows, or, with block_table and cu_seqlens, positions in the row's sequence."""
+    _need(q, "q", torch.bfloat16, 3)
+    n_blocks, block, heads, dim = _kv8_cache(kv8, kv_scale, "kv8")
+    _need(idx, "idx", torch.int32, 2)
+    T, H, Dqk = q.shape
+    K = idx.shape[1]
+    if dim != Dqk:
+        raise ValueError(f"kv8 rows must have the query's {Dqk} dims, got {dim}")
+    if idx.shape[0] != T:
+        raise ValueError(f"idx must have {T} rows, got {idx.shape[0]}")
+    if topk_length is not None:
+        _need(topk_length, "topk_length", torch.int32, 1)
+        if topk_length.shape[0] != T:
+            raise ValueError(f"topk_length must have {T} entries, got {topk_length.shape[0]}")
+    if sink is not None:
+        _need(sink, "sink", torch.float32, 1)
+        if sink.shape[0] != H:
+            raise ValueError(f"sink must have {H} entries, got {sink.shape[0]}")
+    Dv = 512
+    if v8 is not None:
+        if v_scale is None:
+            raise ValueError("v8 needs v_scale")
+        if _kv8_cache(v8, v_scale, "v8")[:3] != (n_blocks, block, heads):
+            raise ValueError("v8 must have the blocks and heads of kv8")
+        Dv = v8.shape[3]
+    elif v_scale is not None:
+        raise ValueError("v_scale needs v8")
+    n_seqs, width = 0, 0
+    if block_table is not None:
+        if cu_seqlens is None:
+            raise ValueError("block_table needs cu_seqlens")
+        n_seqs, width = _kv8_sequences(cu_seqlens, None, block_table)
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=dev)
+    elif _need(out, "out", torch.bfloat16, 3).shape != (T, H, Dv):
+        raise ValueError(f"out must be [{T}, {H}, {Dv}], got {tuple(out.shape)}")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    elif _need(lse, "lse", torch.float32, 2).shape != (T, H):
+        raise ValueError(f"lse must be [{T}, {H}], got {tuple(lse.shape)}")
+    lse_kv = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse_kv else None
+    ml = torch.empty((T, H), dtype=torch.float32, device=dev) if want_max_logits else None
+    if workspace is None:
+        need = sparse_attn_fwd_kv8_workspace_size(T, H, heads, Dqk, Dv, K)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need_here(q=q, kv8=kv8, kv8_scale=kv_scale, idx=idx, topk_length=topk_length, sink=sink, v8=v8, v8_scale=v_scale,
+               cu_seqlens=cu_seqlens if block_table is not None else None, block_table=block_table, out=out, lse=lse,
+               workspace=workspace)
+    _check("dsa_sparse_attn_fwd_kv8",
+           lib().dsa_sparse_attn_fwd_kv8(_p(q), _p(kv8), _p(kv_scale), _p(v8), _p(v_scale), _p(idx), _p(topk_length),
+                                         _p(sink), _p(cu_seqlens) if block_table is not None else None,
+                                         _p(block_table), n_seqs, T, H, heads, Dqk, Dv, K, block, n_blocks, width,
+                                         float(scale), _p(out), _p(lse), _p(lse_kv), _p(ml), _p(workspace),
+                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                         _stream()))
+    res = {"out": out, "lse": lse}
+    if lse_kv is not None:
+        res["lse_kv"] = lse_kv
+    if ml is not None:
+        res["max_logits"] = ml
+    return res
