@@ -1,26 +1,80 @@
-// attention_kv8.cu -- sparse attention over the 8-bit block cache.
+// attention_kv8.cu -- sparse attention over the 8-bit block cache, on tcgen05.
 //
-// For row t, head h (of KV head h / (H / Hc)) and valid slot j, with row r_j
-// in block b_j: s_j = scale * k_scale[b_j] * (q . e4m3(kv8[r_j])),
-// out = sum_j exp(s_j) v_scale[b_j] e4m3(v8[r_j]) / (sum_j exp(s_j) + exp(sink)).
+// For row t, head h (of KV head kvh = h / (H / Hc)) and valid slot j, with
+// cache row r_j in block b_j:
+//   s_j = scale * k_scale[b_j] * (q . e4m3(kv8[r_j])),
+//   out = sum_j exp(s_j) v_scale[b_j] e4m3(v8[r_j]) / (sum_j exp(s_j) + exp(sink)).
+//
+// Both products run on the codes as they lie in the cache (kind::f8f6f4): a
+// block's scale is one number per key, so it multiplies the key's scores and
+// weights afterwards and no code is ever widened in shared memory.  The other
+// operand of each product is split into two E4M3 terms:
+//   query:   q / s = hi + lo / 16, s the power of two that brings the head's
+//            largest element to (224, 448].  A bf16 significand has 8 bits, two
+//            E4M3 terms hold 4 each: exact down to 2^-14 of the scaled units.
+//   weights: w = C * exp(s_j - m) * v_scale / 2^E as hi + lo: relative error
+//            2^-8, what rounding to bf16 costs, and at least 2^-10 / C of the
+//            largest weight (the smaller term's smallest step).
+// Against the bf16 kernel a tile of 64 keys costs half the gather and 34
+// instructions instead of 52; hi and lo of the query are the two halves of
+// one N = 128 operand, hi and lo of the weights two instructions into the same sums.
+//
+// Work item = (token, KV head, group of 64 query heads, split of its slots).
+// Products ("swap AB"):
+//   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T   (M = 64 keys, N = 128)
+//   MMA2  O^T[dim, head] += V^T[dim, key] . (Phi + Plo)^T[key, head] (M = 128 dims, N = 64)
+// S^T (two buffers) and O^T fill TMEM.  Tiles are gathered with cp.async into
+// 128-byte-swizzled rows by eight warps, two tiles in flight, three or four buffers.
+// Softmax: as in the bf16 kernel, one reference maximum per head that moves
+// when a tile passes it by 2^kTheta, and a reference exponent E of the value
+// scales that moves when a block's scale passes 2^E; both move the running sums.
+//
+// Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
+// MMA1, 17 MMA2, 18..19 idle (they fill the fifth warpgroup).
 #include <climits>
 
 #include "kv8.cuh"
 
 namespace {
 
+constexpr int kKeys = 64;  // keys per tile
+constexpr int kHG = 64;    // query heads per group
+constexpr int kGatherWarps = 8;
+constexpr int kGatherThreads = kGatherWarps * 32;
+constexpr int kGatherKeys = kGatherThreads / 8;   // keys one gather step covers
+constexpr int kGatherSteps = kKeys / kGatherKeys;
+constexpr int kSoftWarp0 = kGatherWarps;
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
+constexpr int kMma2Warp = kMmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 4) * 32;  // five warpgroups
+// Registers: launched at kLaunchRegs per thread, moved from the lean
+// warpgroups to the softmax ones.
+constexpr int kLaunchRegs = 96, kLeanRegs = 56, kSoftRegs = 152;
+static_assert(3 * 128 * kLeanRegs + 2 * 128 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
+constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
+constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
+constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
+constexpr uint32_t kPBytes = 2 * kPPart;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kKeys = 32;    // keys per tile, one per lane
-constexpr int kHeads = 8;    // heads per CTA, one per warp
-constexpr int kThreads = kHeads * 32;
-constexpr int kPad = 16;     // bytes added to a staged row (bank conflicts)
+// Weights reach 2^kTheta before the reference moves; kWeight = 2^(8 - kTheta)
+// puts that at 256, below E4M3's 448, and leaves 2^-10 / kWeight = 2^-14 as the
+// smallest step of a weight.
+constexpr float kTheta = 4.0f;
+constexpr float kWeight = 16.0f;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSCol = 0;    // S^T buffers at columns 0 and 128 (hi 64, lo 64)
+constexpr int kOCol = 256;  // O^T blocks at 256 + 64 m
+constexpr int kPlanSms = 152;
+constexpr int kMaxSplits = 32;
 
 struct Params {
   const __nv_bfloat16* q;
   const uint8_t* k8;
   const float* k_scale;
-  const uint8_t* v8;  // == k8 when V is the first Dv dims of the row
+  const uint8_t* v8;  // separate V, or unused
   const float* v_scale;
   const int32_t* idx;
   const int32_t* topk_length;
@@ -30,123 +84,810 @@ struct Params {
   float* lse;
   float* lse_kv;
   float* max_logits;
-  int H, Hc, Dqk, Dv, K;
-  bool separate;
+  float* part_o;   // [T, H, splits, Dv], splits > 1
+  float4* part_s;  // [T, H, splits]: reference, sum, maximum
+  uint32_t* status;
+  int H, Hc, G, K, splits, n_items;  // G: 64-head groups per KV head
   float scale_log2;
 };
 
-__global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const Params p) {
-  extern __shared__ uint8_t smem[];
-  __shared__ int rows[kKeys];
-  __shared__ float ks[kKeys], vs[kKeys];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = p.H / p.Hc, per = (group + kHeads - 1) / kHeads;
-  const int kvh = blockIdx.y / per, hg = (blockIdx.y - kvh * per) * kHeads + warp;
-  const bool real = hg < group;
-  const int h = kvh * group + min(hg, group - 1);
-  if (p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs)) return;
-  const int b = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, t) : 0;
-  const int kst = p.Dqk + kPad, vst = p.separate ? p.Dv + kPad : 0;
-  uint8_t* kt = smem;
-  uint8_t* vt = p.separate ? smem + kKeys * kst : smem;
-  const int vld = p.separate ? vst : kst;
-  float* qs = reinterpret_cast<float*>(smem + kKeys * (kst + vst)) + warp * p.Dqk;
-  const int64_t orow = static_cast<int64_t>(t) * p.H + h;
-  for (int c = lane; c < p.Dqk; c += 32) qs[c] = __bfloat162float(p.q[orow * p.Dqk + c]);
+template <int DQK, int DV, bool SEP>
+struct Shape {
+  static constexpr int kNqk = (DQK + 127) / 128;           // 128-code chunks of a key row
+  static constexpr int kNv = DV / 128;
+  static constexpr int kTail = DQK % 128 ? (DQK % 128) / 32 : 4;  // K = 32 steps of the last chunk
+  static constexpr int kChunks = kNqk + (SEP ? kNv : 0);
+  static constexpr int kVFirst = SEP ? kNqk : 0;
+  static constexpr int kStages = DQK == 576 ? 3 : 4;
+  static constexpr uint32_t kBuf = kChunks * kChunkBytes;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kKv = kQ + kNqk * kQChunkBytes;
+  static constexpr uint32_t kP = kKv + kStages * kBuf;
+  static constexpr uint32_t kSmall = kP + 2 * kPBytes;
+  // wmax, red [4][64]; alpha, mref, fac [64]; qsc [3][64]; svm [4]; exflag [2][8]
+  static constexpr uint32_t kSmallBytes = (2 * 256 + 3 * 64 + 3 * 64 + 4 + 16) * 4;
+  static constexpr uint32_t kBars = kSmall + kSmallBytes;
+  static constexpr uint32_t kMisc = kBars + 24 * 8;
+  static constexpr uint32_t kTotal = kMisc + 16;
+  static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kSmallBytes % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ int ord_f32(float f) {
+  int i = __float_as_int(f);
+  return i >= 0 ? i : (i ^ 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unord_f32(int i) { return __int_as_float(i >= 0 ? i : (i ^ 0x7FFFFFFF)); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool elect_sync() {
+  uint32_t is = 0;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(is));
+  return is != 0;
+}
+
+__device__ __forceinline__ void named_bar(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(src_bytes), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 h2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint2 pack4(const uint16_t (&c)[4]) {
+  return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
+}
+
+// Smallest power of two >= x (x >= 0 finite), within [2^-126, 2^126].
+__device__ __forceinline__ float pow2_ceil(float x) {
+  const uint32_t u = __float_as_uint(x);
+  uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) ? 1u : 0u);
+  e = e < 1u ? 1u : (e > 253u ? 253u : e);
+  return __uint_as_float(e << 23);
+}
+
+// One work item: the tiles [i0, i1) of row t.
+struct Item {
+  int t, kvh, h0, hv;  // first query head and how many of the group's are real
+  int split, i0, i1, len;
+  bool dead;           // a padding row of a batch with a block table
+};
+
+__device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
+  Item w;
+  int u = p.n_items - 1 - it;  // longest rows first (they are the last of a packed prompt)
+  w.split = u % p.splits;
+  u /= p.splits;
+  const int per = p.Hc * p.G, group = p.H / p.Hc;
+  w.t = u / per;
+  const int r = u - w.t * per;
+  w.kvh = r / p.G;
+  const int g = r - w.kvh * p.G;
+  w.h0 = w.kvh * group + g * kHG;
+  w.hv = min(kHG, group - g * kHG);
+  w.dead = w.t >= t_end;
   int len = p.K;
-  if (p.topk_length) len = min(max(__ldg(p.topk_length + t), 0), p.K);
-  float m = -INFINITY, l = 0.f, acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < len; j0 += kKeys) {
-    __syncthreads();
-    if (threadIdx.x < kKeys) {
-      const int j = j0 + threadIdx.x;
-      const int id = j < len ? __ldg(p.idx + static_cast<int64_t>(t) * p.K + j) : -1;
-      const int r = id >= 0 ? dsa::kv8_row(p.g, b, id) : -1;
-      rows[threadIdx.x] = r;
-      const int64_t sb = static_cast<int64_t>(r >> p.g.lb) * p.Hc + kvh;
-      ks[threadIdx.x] = r >= 0 ? __ldg(p.k_scale + sb) : 0.f;
-      vs[threadIdx.x] = r >= 0 ? __ldg(p.v_scale + sb) : 0.f;
+  if (p.topk_length) {
+    len = __ldg(p.topk_length + w.t);
+    len = len < 0 ? 0 : (len > p.K ? p.K : len);
+  }
+  if (w.dead) len = 0;
+  const int nt = (len + kKeys - 1) / kKeys;
+  w.len = len;
+  w.i0 = static_cast<int>(static_cast<int64_t>(nt) * w.split / p.splits);
+  w.i1 = static_cast<int>(static_cast<int64_t>(nt) * (w.split + 1) / p.splits);
+  return w;
+}
+
+template <int DQK, int DV, bool SEP>
+__global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
+  using S = Shape<DQK, DV, SEP>;
+  constexpr int ST = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = dsa::smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  int* wmax = reinterpret_cast<int*>(smem + S::kSmall);  // [4 quarters][64 heads]
+  float* red = reinterpret_cast<float*>(wmax + 256);     // [4][64]
+  float* alpha = red + 256;                              // [64]
+  float* mref = alpha + 64;                              // [64]
+  float* fac = mref + 64;                                // [64]
+  // Query scales (times scale * log2(e)) of three items in turn: the gather
+  // warps convert item n + 3's query after MMA1 of item n + 2 has run, which
+  // needed the S buffer of item n, which the softmax hands back after reading these.
+  float* qsc = fac + 64;                                 // [3][64]
+  float* svm = qsc + 192;                                // [4]
+  int* exflag = reinterpret_cast<int*>(svm + 4);         // [2][8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* kv_full = bars;        // [4]
+  uint64_t* kv_empty = bars + 4;   // [4]
+  uint64_t* s_full = bars + 8;     // [2]
+  uint64_t* s_empty = bars + 10;   // [2]
+  uint64_t* p_full = bars + 12;    // [2]
+  uint64_t* p_empty = bars + 14;   // [2]: MMA2 of the tile has run
+  uint64_t* q_full = bars + 16;
+  uint64_t* q_empty = bars + 17;
+  uint64_t* drain = bars + 18;     // [2]: the MMA issuers' exit commits
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < ST; ++b) {
+      dsa::mbar_init(&kv_full[b], kGatherWarps);
+      dsa::mbar_init(&kv_empty[b], 1);
     }
-    __syncthreads();
-    const int pk = p.Dqk >> 4, pv = p.separate ? p.Dv >> 4 : 0;
-    for (int i = threadIdx.x; i < kKeys * (pk + pv); i += kThreads) {
-      const int j = i / (pk + pv), c = i - j * (pk + pv);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (rows[j] >= 0) {
-        const int64_t rh = static_cast<int64_t>(rows[j]) * p.Hc + kvh;
-        v = c < pk ? __ldg(reinterpret_cast<const uint4*>(p.k8 + rh * p.Dqk) + c)
-                   : __ldg(reinterpret_cast<const uint4*>(p.v8 + rh * p.Dv) + (c - pk));
+    for (int b = 0; b < 2; ++b) {
+      dsa::mbar_init(&s_full[b], 1);
+      dsa::mbar_init(&s_empty[b], kSoftWarps);
+      dsa::mbar_init(&p_full[b], kSoftWarps);
+      dsa::mbar_init(&p_empty[b], 1);
+      dsa::mbar_init(&drain[b], 1);
+    }
+    dsa::mbar_init(q_full, kGatherWarps);
+    dsa::mbar_init(q_empty, 1);
+    *abort_flag = 0;
+    dsa::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) dsa::tmem_alloc(tmem_slot, kTmemCols);
+  dsa::tc_fence_before();
+  __syncthreads();
+  dsa::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const dsa::Waiter wt = dsa::make_waiter(abort_flag, p.status);
+  const int t_end = p.g.table ? __ldg(p.g.cu + p.g.n_seqs) : INT_MAX;
+
+  if (warp < kGatherWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
+    // ------------------------------------------------------------ gather
+    // Thread gt covers piece (gt & 7) (16 codes) of keys (gt >> 3) + 32 kg of
+    // every chunk.  A row's place depends on its id and the block table: ids
+    // are read two tiles ahead, the table one tile ahead.
+    const int gt = threadIdx.x, piece = gt & 7;
+    const uint64_t keep = dsa::l2_policy_evict_last();  // rows are selected by many queries
+    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
+    int tile_ctr = 0, item_ctr = 0;
+    int pend = -1;  // stage whose copies are in flight
+    bool ok = true;
+    auto signal = [&](int stage) {
+      dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
+    };
+    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+      const Item w = get_item(p, it, t_end);
+      if (w.i0 >= w.i1) continue;
+      const int b = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, w.t) : 0;
+      const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
+      auto load_id = [&](int i, int kg) {
+        const int j = i * kKeys + kg * kGatherKeys + (gt >> 3);
+        return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
+      };
+      int row[kGatherSteps], nid[kGatherSteps];
+#pragma unroll
+      for (int kg = 0; kg < kGatherSteps; ++kg) {
+        nid[kg] = load_id(w.i0 + 1, kg);
+        const int id = load_id(w.i0, kg);
+        row[kg] = id >= 0 ? dsa::kv8_row(p.g, b, id) : -1;
       }
-      *reinterpret_cast<uint4*>(c < pk ? kt + j * kst + c * 16 : vt + j * vst + (c - pk) * 16) = v;
-    }
-    __syncthreads();
-    float dot = 0.f;
-    for (int c = 0; c < p.Dqk; c += 4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(kt + lane * kst + c);
-      const float2 a = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w)), e = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w >> 16));
-      const float4 qv = *reinterpret_cast<const float4*>(qs + c);
-      dot = fmaf(qv.x, a.x, fmaf(qv.y, a.y, fmaf(qv.z, e.x, fmaf(qv.w, e.y, dot))));
-    }
-    const bool valid = rows[lane] >= 0;
-    const float x = valid ? dot * (ks[lane] * p.scale_log2) : -INFINITY;
-    float mx = x;
+      for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+        const int stage = tile_ctr % ST;
+        int cur[kGatherSteps];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float mr = mn == -INFINITY ? 0.f : mn;
-    const float alpha = exp2f(m - mr);
-    const float e = valid ? exp2f(x - mr) : 0.f;
-    float sum = e;
+        for (int kg = 0; kg < kGatherSteps; ++kg) {
+          cur[kg] = row[kg];
+          row[kg] = nid[kg] >= 0 ? dsa::kv8_row(p.g, b, nid[kg]) : -1;
+          nid[kg] = load_id(i + 2, kg);
+        }
+        const uint32_t ph = ((tile_ctr / ST) & 1) ^ 1;
+        if (pend >= 0 && !__all_sync(0xffffffffu, dsa::mbar_test_wait(&kv_empty[stage], ph))) {
+          // no free buffer: do not hold back the tile that may have landed
+          cp_async_wait<0>();
+          signal(pend);
+          pend = -1;
+        }
+        if (!dsa::mbar_wait_warp(&kv_empty[stage], ph, wt)) {
+          ok = false;
+          break;
+        }
+        const uint32_t buf = kv_addr + stage * S::kBuf;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * alpha + sum;
-    m = mn;
-    const float w = valid ? e * vs[lane] : 0.f;
+        for (int kg = 0; kg < kGatherSteps; ++kg) {
+          const int key = kg * kGatherKeys + (gt >> 3);
+          const uint32_t nbytes = cur[kg] >= 0 ? 16u : 0u;
+          const int64_t rh = static_cast<int64_t>(cur[kg] >= 0 ? cur[kg] : 0) * p.Hc + w.kvh;
+          // checked build: the row is inside the cache
+          if (!dsa::check(cur[kg] < (p.g.n_blocks << p.g.lb), p.status)) continue;
+          const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
+          const uint32_t dst = buf + dsa::sw128_offset(key, piece * 16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] *= alpha;
-    for (int j = 0; j < kKeys; ++j) {
-      if (rows[j] < 0) continue;
-      const float wj = __shfl_sync(0xffffffffu, w, j);
+          for (int c = 0; c < S::kNqk; ++c)
+            if (c * 128 + piece * 16 < DQK) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes, keep);
+          if (SEP) {
+            const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = i * 128 + lane * 4;
-        if (d < p.Dv) {
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(vt + j * vld + d);
-          const float2 a = dsa::f2_of_e4m3x2(static_cast<uint16_t>(u)), c = dsa::f2_of_e4m3x2(static_cast<uint16_t>(u >> 16));
-          acc[4 * i] = fmaf(wj, a.x, acc[4 * i]);
-          acc[4 * i + 1] = fmaf(wj, a.y, acc[4 * i + 1]);
-          acc[4 * i + 2] = fmaf(wj, c.x, acc[4 * i + 2]);
-          acc[4 * i + 3] = fmaf(wj, c.y, acc[4 * i + 3]);
+            for (int c = 0; c < S::kNv; ++c)
+              cp_async16(dst + (S::kNqk + c) * kChunkBytes, vrow + c * 128, nbytes, keep);
+          }
+        }
+        cp_async_commit();
+        if (pend >= 0) {
+          cp_async_wait<1>();
+          signal(pend);
+        }
+        pend = stage;
+        if (i == w.i0) {
+          // The item's query, once MMA1 of the item before has run: its tiles
+          // must all be signalled before this waits for them.
+          cp_async_wait<0>();
+          signal(pend);
+          pend = -1;
+          if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) {
+            ok = false;
+            break;
+          }
+          // four threads per head, 16-byte pieces sub, sub + 4, ...
+          const int hq = gt >> 2, sub = gt & 3;
+          const bool real = hq < w.hv;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK) + sub;
+          uint32_t m = 0;
+#pragma unroll 6
+          for (int k = 0; k < DQK / 32; ++k) {
+            const uint4 v = __ldg(src + 4 * k);
+            m = max(m, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
+            m = max(m, max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu)));
+          }
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          // a head with infinity or NaN: its scores are NaN
+          const bool finite = m < 0x7F80u;
+          const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
+          const float inv = real ? 1.f / s : 0.f;
+          if (sub == 0)
+            qsc[(item_ctr % 3) * 64 + hq] = !real ? 0.f : (finite ? s * p.scale_log2 : __uint_as_float(0x7FC00000u));
+          // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
+          // which gives each softmax thread eight consecutive heads
+          const int hr = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
+          uint8_t* qb = smem + S::kQ;
+#pragma unroll 3
+          for (int k = 0; k < DQK / 32; ++k) {
+            const uint4 v = __ldg(src + 4 * k);
+            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const __half2 h = __floats2half2_rn(__uint_as_float(wd[n] << 16) * inv,
+                                                  __uint_as_float(wd[n] & 0xFFFF0000u) * inv);
+              hi[n] = dsa::e4m3x2_h2(h2_bits(h));
+              lo[n] = dsa::e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(hi[n]))), __float2half2_rn(16.f))));
+            }
+            const int el = (sub + 4 * k) * 8;
+            const uint32_t off = (el >> 7) * kQChunkBytes + dsa::sw128_offset(hr, (el & 127) & ~15) + (el & 8);
+            *reinterpret_cast<uint2*>(qb + off) = pack4(hi);
+            *reinterpret_cast<uint2*>(qb + off + kHG * 128) = pack4(lo);
+          }
+          dsa::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) dsa::mbar_arrive(q_full);
+          ++item_ctr;
         }
       }
     }
-  }
-  if (!real) return;
-  const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
-  const bool any = m > -INFINITY || l != 0.f;  // l != 0 also when it is NaN
-  const float M = fmaxf(m, sk), Mr = M == -INFINITY ? 0.f : M;
-  const float a = any ? exp2f(m - Mr) : 0.f;
-  const float z = l * a + exp2f(sk - Mr);
-  const float f = any ? a / z : 0.f;
+    cp_async_wait<0>();  // nothing of this thread is in flight when it leaves
+    if (pend >= 0) signal(pend);
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
+    if (warp != kMmaWarp && warp != kMma2Warp) goto done;
+    // ------------------------------------------------------------ MMA issue
+    // Two warps, one per product, each converged with one elected issuer.
+    const bool leader = elect_sync();
+    const uint32_t base = dsa::smem_u32(smem);
+    int tile_ctr = 0;
+    bool ok = true;
+    if (warp == kMmaWarp) {
+      constexpr uint32_t idesc1 = dsa::idesc_e4m3(kKeys, 2 * kHG);
+      const uint64_t q_desc = dsa::smem_desc(base + S::kQ, 16, 1024, dsa::kSwizzle128B);
+      const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
+      int item_ctr = 0;
+      for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+        const Item w = get_item(p, it, t_end);
+        if (w.i0 >= w.i1) continue;
+        if (!dsa::mbar_wait_warp(q_full, item_ctr & 1, wt)) break;
+        for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+          const int b = tile_ctr & 1, stage = tile_ctr % ST;
+          const bool got = dsa::mbar_wait(&s_empty[b], ((tile_ctr >> 1) & 1) ^ 1, wt) &&
+                           dsa::mbar_wait(&kv_full[stage], (tile_ctr / ST) & 1, wt);
+          dsa::tc_fence_after();
+          const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
+          const uint32_t d = tmem_base + kSCol + b * 128;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int d = (i >> 2) * 128 + lane * 4 + (i & 3);
-    if (d < p.Dv) p.out[orow * p.Dv + d] = __float2bfloat16_rn(acc[i] * f);
+          for (int c = 0; c < S::kNqk; ++c) {
+            const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < (c + 1 < S::kNqk ? 4 : S::kTail); ++kk)
+              dsa::umma_f8_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
+          }
+          if (leader && got) dsa::umma_commit(&s_full[b]);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
+        if (leader) dsa::umma_commit(q_empty);
+        __syncwarp();
+        ++item_ctr;
+      }
+      if (leader) dsa::umma_drain(&drain[0], p.status);
+      __syncwarp();
+    } else {
+      constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kHG) | (1u << 15) | (1u << 16);  // both MN-major
+      const uint64_t v_desc =
+          dsa::smem_desc(base + S::kKv + S::kVFirst * kChunkBytes, kChunkBytes, 1024, dsa::kSwizzle128B);
+      // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
+      const uint64_t p_desc = dsa::smem_desc(base + S::kP, kPPart, 512, dsa::kSwizzle64B);
+      for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+        const Item w = get_item(p, it, t_end);
+        for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+          const int b = tile_ctr & 1, stage = tile_ctr % ST;
+          const bool got = dsa::mbar_wait(&p_full[b], (tile_ctr >> 1) & 1, wt);
+          dsa::tc_fence_after();
+          const uint64_t a0 = v_desc + stage * (S::kBuf >> 4), b0 = p_desc + b * (kPBytes >> 4);
+#pragma unroll
+          for (int mb = 0; mb < S::kNv; ++mb) {
+            const uint32_t d = tmem_base + kOCol + mb * kHG;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 32; ++kk) {
+              const uint64_t a = a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4);
+              const uint64_t bp = b0 + kk * (32 * kHG >> 4);
+              dsa::umma_f8_if(leader && got, d, a, bp, idesc2, (i > w.i0 || kk > 0) ? 1u : 0u);
+              dsa::umma_f8_if(leader && got, d, a, bp + (kPPart >> 4), idesc2, 1u);
+            }
+          }
+          if (leader && got) {
+            dsa::umma_commit(&p_empty[b]);
+            dsa::umma_commit(&kv_empty[stage]);
+          }
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+        }
+      }
+      if (leader) dsa::umma_drain(&drain[1], p.status);
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------ softmax + epilogue
+    const int sw = warp - kSoftWarp0;
+    const int st = threadIdx.x - kSoftWarp0 * 32;
+    const int quarter = warp & 3;  // TMEM lane quarter
+    const int hh = sw >> 2;        // head half
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    // S^T registers 4j + e (key kA) and 4j + 2 + e (key kB) hold head hb + 2j + e
+    const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
+    const int hb = hh * 32 + 8 * (lane & 3);
+    const bool want_max = p.max_logits != nullptr;
+    int tile_ctr = 0, item_ctr = 0;
+    bool ok = true;
+    // A wait of this thread gave up: the eight warps leave together, at a
+    // point that reduces the flag (see the bf16 kernel).
+    bool failed = false;
+    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+      const Item w = get_item(p, it, t_end);
+      if (w.dead) continue;
+      const int64_t orow = static_cast<int64_t>(w.t) * p.H + w.h0;
+      if (w.i0 >= w.i1) {
+        if (p.splits > 1) {
+          if (st < w.hv) p.part_s[(orow + st) * p.splits + w.split] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        } else {
+          for (int h = 0; h < w.hv; ++h)
+            for (int d = st; d < DV; d += kSoftThreads) p.out[(orow + h) * DV + d] = __float2bfloat16_rn(0.f);
+          if (st < w.hv) {
+            p.lse[orow + st] = p.sink ? __ldg(p.sink + w.h0 + st) : -INFINITY;
+            if (p.lse_kv) p.lse_kv[orow + st] = INFINITY;
+            if (p.max_logits) p.max_logits[orow + st] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      float l_part[8], qs[8];
+      float m_max = -INFINITY;
+      float ref = __uint_as_float(1u << 23);  // 2^E of the value scales so far
+      float inv = 0.f;                        // 2^-E
+#pragma unroll
+      for (int h = 0; h < 8; ++h) l_part[h] = 0.f;
+      const int b_seq = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, w.t) : 0;
+      const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
+      auto load_id = [&](int i, int k) {
+        const int j = i * kKeys + k;
+        return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
+      };
+      auto block_of = [&](int id) { return id >= 0 ? dsa::kv8_block(p.g, b_seq, id >> p.g.lb) : -1; };
+      auto scale_of = [&](const float* s, int blk) {
+        return blk >= 0 ? __ldg(s + static_cast<int64_t>(blk) * p.Hc + w.kvh) : 0.f;
+      };
+      // each key's id, block and scales are read three, two and one tiles ahead
+      int blA = block_of(load_id(w.i0, kA)), blB = block_of(load_id(w.i0, kB));
+      int nblA = block_of(load_id(w.i0 + 1, kA)), nblB = block_of(load_id(w.i0 + 1, kB));
+      int idA = load_id(w.i0 + 2, kA), idB = load_id(w.i0 + 2, kB);
+      float nskA = scale_of(p.k_scale, blA), nskB = scale_of(p.k_scale, blB);
+      float nsvA = SEP ? scale_of(p.v_scale, blA) : nskA, nsvB = SEP ? scale_of(p.v_scale, blB) : nskB;
+      for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+        const int b = tile_ctr & 1;
+        const uint32_t ph = (tile_ctr >> 1) & 1;
+        const bool vA = blA >= 0, vB = blB >= 0;
+        const float skA = nskA, skB = nskB, svA = nsvA, svB = nsvB;
+        blA = nblA;
+        blB = nblB;
+        nskA = scale_of(p.k_scale, blA);
+        nskB = scale_of(p.k_scale, blB);
+        nsvA = SEP ? scale_of(p.v_scale, blA) : nskA;
+        nsvB = SEP ? scale_of(p.v_scale, blB) : nskB;
+        nblA = block_of(idA);
+        nblB = block_of(idB);
+        idA = load_id(i + 3, kA);
+        idB = load_id(i + 3, kB);
+        if (!failed) failed = !dsa::mbar_wait(&s_full[b], ph, wt);
+        dsa::tc_fence_after();
+        float x[16];
+        {
+          uint32_t v[16], lo[16];
+          const uint32_t ta = tmem_base + lane_off + kSCol + b * 128 + hh * 32;
+          dsa::tmem_ld16x256b_x4(ta, v);
+          dsa::tmem_ld16x256b_x4(ta + 64, lo);
+          dsa::tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
+        }
+        if (i == w.i0) {
+          const float4 a = *reinterpret_cast<const float4*>(qsc + (item_ctr % 3) * 64 + hb),
+                       c = *reinterpret_cast<const float4*>(qsc + (item_ctr % 3) * 64 + hb + 4);
+          qs[0] = a.x, qs[1] = a.y, qs[2] = a.z, qs[3] = a.w;
+          qs[4] = c.x, qs[5] = c.y, qs[6] = c.z, qs[7] = c.w;
+          ++item_ctr;
+        }
+        dsa::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
+        // x: scores in powers of two; y: against the reference m of each head
+        float y[16];
+        bool ex = svA > ref || svB > ref;
+        {
+          const float4 ma = *reinterpret_cast<const float4*>(mref + hb), mb = *reinterpret_cast<const float4*>(mref + hb + 4);
+          const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[4 * j + e] *= qs[2 * j + e] * skA;
+              x[4 * j + 2 + e] *= qs[2 * j + e] * skB;
+              y[4 * j + e] = vA ? x[4 * j + e] - m[2 * j + e] : -INFINITY;
+              y[4 * j + 2 + e] = vB ? x[4 * j + 2 + e] - m[2 * j + e] : -INFINITY;
+              ex |= (y[4 * j + e] > kTheta) || (y[4 * j + 2 + e] > kTheta);
+            }
+          }
+        }
+        const uint32_t wflags = __reduce_or_sync(0xffffffffu, (ex ? 1u : 0u) | (failed ? 2u : 0u));
+        if (lane == 0) exflag[b * 8 + sw] = static_cast<int>(wflags);
+        named_bar(1, kSoftThreads);
+        const bool first = i == w.i0;  // always sets the references (mref holds the item before's)
+        bool reduce = want_max || first;
+        int any_failed = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int f = exflag[b * 8 + k];
+          reduce |= (f & 1) != 0;
+          any_failed |= f & 2;
+        }
+        if (any_failed) {  // every softmax thread read the same flags
+          ok = false;
+          break;
+        }
+        bool need_rescale = false;
+        float ratio = 1.f;  // of the old to the new 2^E
+        if (reduce) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(vA ? x[4 * j + e] : -INFINITY, vB ? x[4 * j + 2 + e] : -INFINITY);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              if (lane < 4) wmax[quarter * 64 + hb + 2 * j + e] = ord_f32(mx);
+            }
+          }
+          float sv = fmaxf(svA, svB);
+          sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 4));
+          sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
+          sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
+          if (lane == 0 && hh == 0) svm[quarter] = sv;
+          named_bar(1, kSoftThreads);
+          const float rn = fmaxf(ref, pow2_ceil(fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]))));
+          inv = 1.f / rn;
+          ratio = ref * inv;
+          ref = rn;
+          if (st < 64) {
+            const int r = max(max(wmax[st], wmax[64 + st]), max(wmax[128 + st], wmax[192 + st]));
+            const float tmax = unord_f32(r);
+            const float mo = first ? -INFINITY : mref[st];
+            const float mn = (tmax > mo + kTheta) ? tmax : mo;
+            alpha[st] = (mn == mo) ? 1.f : ex2(mo - mn);
+            mref[st] = mn;
+            m_max = fmaxf(m_max, tmax);
+          }
+          named_bar(1, kSoftThreads);
+          const float4 aa = *reinterpret_cast<const float4*>(alpha + hb), ab = *reinterpret_cast<const float4*>(alpha + hb + 4);
+          const float4 ma = *reinterpret_cast<const float4*>(mref + hb), mb = *reinterpret_cast<const float4*>(mref + hb + 4);
+          const float a[8] = {aa.x, aa.y, aa.z, aa.w, ab.x, ab.y, ab.z, ab.w};
+          const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+          bool moved = ratio != 1.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              moved |= a[2 * j + e] != 1.f;
+              l_part[2 * j + e] *= a[2 * j + e];
+              y[4 * j + e] = vA ? x[4 * j + e] - m[2 * j + e] : -INFINITY;
+              y[4 * j + 2 + e] = vB ? x[4 * j + 2 + e] - m[2 * j + e] : -INFINITY;
+            }
+          }
+          need_rescale = __any_sync(0xffffffffu, moved) && !first;
+        }
+        // P^T rows kA and kB, both terms: the thread's eight heads are bytes
+        // hb .. hb + 7 of the 64-byte rows (64-byte swizzle: 16-byte unit ^ (key >> 1 & 3))
+        if (!failed) failed = !dsa::mbar_wait(&p_empty[b], ph ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
+        {
+          uint8_t* pb = smem + S::kP + b * kPBytes;
+          const int unit = hb >> 4, in = hb & 8;
+          const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int key = k ? kB : kA;
+            const float wk = k ? wB : wA;
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float p0 = ex2(y[4 * j + 2 * k]), p1 = ex2(y[4 * j + 2 * k + 1]);
+              l_part[2 * j] += p0;
+              l_part[2 * j + 1] += p1;
+              const __half2 h = __floats2half2_rn(p0 * wk, p1 * wk);
+              hi[j] = dsa::e4m3x2_h2(h2_bits(h));
+              lo[j] = dsa::e4m3x2_h2(h2_bits(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(hi[j])))));
+            }
+            uint8_t* at = pb + key * kHG + ((unit ^ ((key >> 1) & 3)) << 4) + in;
+            *reinterpret_cast<uint2*>(at) = pack4(hi);
+            *reinterpret_cast<uint2*>(at + kPPart) = pack4(lo);
+          }
+        }
+        if (need_rescale) {
+          // MMA2 of the previous tile must have landed before O^T is scaled
+          if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((tile_ctr - 1) >> 1) & 1, wt);
+          dsa::tc_fence_after();
+          const float* a32 = alpha + hh * 32;
+#pragma unroll 1
+          for (int mb = 0; mb < S::kNv; ++mb) {
+            const uint32_t ta = tmem_base + lane_off + kOCol + mb * kHG + hh * 32;
+            uint32_t v[32];
+            dsa::tmem_ld32(ta, v);
+            dsa::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * (a32[c] * ratio));
+            dsa::tmem_st32(ta, v);
+          }
+          dsa::tmem_wait_st();
+        }
+        dsa::fence_proxy_async_smem();
+        dsa::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dsa::mbar_arrive(&p_full[b]);
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------- epilogue
+      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
+      // been waited for in turn, so the parity names that tile)
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[(tile_ctr - 1) & 1], ((tile_ctr - 1) >> 1) & 1, wt);
+      dsa::tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        float v = l_part[h];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (lane < 4) red[quarter * 64 + hb + h] = v;
+      }
+      named_bar(1, kSoftThreads);
+      const float unscale = ref * (1.f / kWeight);
+      if (st < 64) {
+        const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
+        const float mc = mref[st];
+        const bool any = l != 0.f;  // true for NaN too
+        float f = unscale;
+        if (p.splits > 1) {
+          if (st < w.hv) p.part_s[(orow + st) * p.splits + w.split] = make_float4(mc, l, m_max, 0.f);
+        } else {
+          const float sink = (p.sink && st < w.hv) ? __ldg(p.sink + w.h0 + st) : -INFINITY;
+          const float sk = sink * kLog2e;
+          float lse_v = sink, lkv = INFINITY;
+          f = 0.f;
+          if (any) {
+            const float M = fmaxf(mc, sk);
+            const float a = exp2f(mc - M);
+            const float z = l * a + exp2f(sk - M);
+            f = a / z * unscale;
+            lse_v = (M + log2f(z)) * kLn2;
+            lkv = (mc + log2f(l)) * kLn2;
+          }
+          if (st < w.hv) {
+            p.lse[orow + st] = lse_v;
+            if (p.lse_kv) p.lse_kv[orow + st] = lkv;
+            if (p.max_logits) p.max_logits[orow + st] = any ? m_max * kLn2 : -INFINITY;
+          }
+        }
+        fac[st] = f;
+      }
+      named_bar(1, kSoftThreads);
+      {
+        const float* f32 = fac + hh * 32;
+        const int hcount = min(32, w.hv - hh * 32);
+#pragma unroll 1
+        for (int mb = 0; mb < S::kNv; ++mb) {
+          uint32_t v[32];
+          dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kHG + hh * 32, v);
+          dsa::tmem_wait_ld();
+          const int d = mb * 128 + quarter * 32 + lane;
+          if (p.splits > 1) {
+            float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + d;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (c < hcount) *o = __uint_as_float(v[c]) * f32[c];
+              o += static_cast<int64_t>(p.splits) * DV;
+            }
+          } else {
+            __nv_bfloat16* o = p.out + (orow + hh * 32) * DV + d;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (c < hcount) __stcs(o, __float2bfloat16_rn(__uint_as_float(v[c]) * f32[c]));
+              o += DV;
+            }
+          }
+        }
+      }
+      dsa::tc_fence_before();
+      if (dsa::named_bar_any(1, kSoftThreads, failed)) {  // the item's last barrier: the group leaves together
+        ok = false;
+        break;
+      }
+    }
   }
-  if (lane == 0) {
-    p.lse[orow] = any ? (Mr + log2f(z)) * kLn2 : sink;
-    if (p.lse_kv) p.lse_kv[orow] = any ? (m + log2f(l)) * kLn2 : INFINITY;
-    if (p.max_logits) p.max_logits[orow] = m * kLn2;
+
+done:
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    dsa::tc_fence_after();
+    dsa::tmem_dealloc(tmem_base, kTmemCols);
   }
+}
+
+// Joins the splits of one (token, head) per CTA: with M the largest reference,
+// z = sum_s 2^(m_s - M) l_s + 2^(sink - M), out = sum_s 2^(m_s - M) O_s / z.
+template <int DV>
+__global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
+  const int64_t row = blockIdx.x;
+  const int t = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<int64_t>(t) * p.H);
+  if (p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs)) return;
+  const int lane = threadIdx.x & 31;
+  float4 s = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  if (lane < p.splits) s = p.part_s[row * p.splits + lane];
+  const bool have = s.y != 0.f;  // a split without a valid slot wrote no O
+  float m = have ? s.x : -INFINITY, mx = have ? s.z : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
+  const bool any = __any_sync(0xffffffffu, have);
+  const float M = fmaxf(m, sk);
+  const float a = have ? exp2f(s.x - M) : 0.f;
+  float l = have ? s.y * a : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float z = any ? l + exp2f(sk - M) : 1.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.splits * DV) + threadIdx.x;
+  for (int k = 0; k < p.splits; ++k) {
+    const float ak = __shfl_sync(0xffffffffu, a, k);
+    if (__shfl_sync(0xffffffffu, have, k)) {
+      const float4 v = __ldcs(o + k * (DV / 4));
+      acc.x = fmaf(ak, v.x, acc.x);
+      acc.y = fmaf(ak, v.y, acc.y);
+      acc.z = fmaf(ak, v.z, acc.z);
+      acc.w = fmaf(ak, v.w, acc.w);
+    }
+  }
+  const float f = 1.f / z;
+  const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+  reinterpret_cast<uint2*>(p.out + row * DV)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
+  if (threadIdx.x == 0) {
+    p.lse[row] = any ? (M + log2f(z)) * kLn2 : sink;
+    if (p.lse_kv) p.lse_kv[row] = any ? (M + log2f(l)) * kLn2 : INFINITY;
+    if (p.max_logits) p.max_logits[row] = any ? mx * kLn2 : -INFINITY;
+  }
+}
+
+// Splits of each row's slots: the number that makes the longest CTA shortest,
+// counting a wave of CTAs as its tiles plus kItemTiles tiles for the query's
+// conversion, the first gather and the epilogue, and joining as kJoinTiles
+// tiles plus one per 16 splits.
+constexpr int kItemTiles = 3, kJoinTiles = 3;
+
+int plan_splits(int64_t units, int K) {
+  const int nt = (K + kKeys - 1) / kKeys;
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits && s <= nt; ++s) {
+    const int64_t waves = (units * s + kPlanSms - 1) / kPlanSms;
+    const int64_t c = 16 * (waves * ((nt + s - 1) / s + kItemTiles) + (s > 1 ? kJoinTiles : 0)) + (s > 1 ? s : 0);
+    if (c < cost) cost = c, best = s;
+  }
+  return best;
+}
+
+bool known_shape(int T, int H, int Hc, int Dqk, int Dv, int K) {
+  const bool form = ((Dqk == 576 || Dqk == 512) && Dv == 512) || (Dqk == 256 && Dv == 256);
+  return form && T >= 1 && H >= 1 && Hc >= 1 && H % Hc == 0 && K >= 1;
+}
+
+int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * ((H / Hc + kHG - 1) / kHG); }
+
+size_t part_bytes(int T, int H, int splits) {
+  return (static_cast<size_t>(T) * H * splits * sizeof(float4) + 255) / 256 * 256;
+}
+
+template <int DQK, int DV, bool SEP>
+int launch(const Params& p, int T, int sms, cudaStream_t stream) {
+  using S = Shape<DQK, DV, SEP>;
+  constexpr int smem = S::kTotal + 1024;
+  auto kernel = attn_kv8_kernel<DQK, DV, SEP>;
+  // the register split assumes the launch count it was sized for
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
+    return dsa::set_error(DSA_ERR_CUDA, "attn_kv8_kernel: compiled with %d registers per thread, expected %d", fa.numRegs,
+                          kLaunchRegs);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return dsa::launch_error("attn_kv8_kernel smem attribute");
+  kernel<<<p.n_items < sms ? p.n_items : sms, kThreads, smem, stream>>>(p);
+  int rc = dsa::launch_error("attn_kv8_kernel");
+  if (rc != DSA_OK || p.splits == 1) return rc;
+  attn_kv8_join_kernel<DV><<<static_cast<unsigned>(T) * p.H, DV / 4, 0, stream>>>(p);
+  return dsa::launch_error("attn_kv8_join_kernel");
 }
 
 }  // namespace
 
 extern "C" size_t dsa_sparse_attn_fwd_kv8_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
-  (void)T, (void)H, (void)Hc, (void)Dqk, (void)Dv, (void)K;
-  return 0;
+  if (!known_shape(T, H, Hc, Dqk, Dv, K)) return 0;
+  const int s = plan_splits(units_of(T, H, Hc), K);
+  return s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
 }
 
 extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const float* kv_scale, const void* v8,
@@ -166,6 +907,9 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   if (T < 0 || H < 1 || Hc < 1 || Hc > DSA_KV8_MAX_HEADS || H % Hc != 0 || H / Hc > 128 || K < 0)
     return dsa::set_error(DSA_ERR_VALUE, "%s: need T >= 0, K >= 0, 1 <= Hc <= %d, H a multiple of Hc, H / Hc <= 128", fn,
                           DSA_KV8_MAX_HEADS);
+  const int64_t units = T > 0 ? units_of(T, H, Hc) : 0;
+  if (units * kMaxSplits > INT_MAX || static_cast<int64_t>(T) * H > INT_MAX)
+    return dsa::set_error(DSA_ERR_VALUE, "%s: T * H exceeds the int32 range of work items", fn);
   if (n_blocks < 1 || block < 1 || block > DSA_KV8_MAX_BLOCK || (block & (block - 1)) != 0)
     return dsa::set_error(DSA_ERR_VALUE, "%s: need n_blocks >= 1 and block a power of two in [1, %d]", fn, DSA_KV8_MAX_BLOCK);
   if (static_cast<int64_t>(n_blocks) * block > INT_MAX)
@@ -181,7 +925,8 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   if (need > 0 && (!workspace || ws_bytes < need || !dsa::aligned(workspace, 256)))
     return dsa::set_error(DSA_ERR_WORKSPACE, "%s: needs a 256-byte aligned workspace of %zu bytes, got %zu", fn, need,
                           workspace ? ws_bytes : static_cast<size_t>(0));
-  int rc = dsa::check_device(nullptr);
+  int sms = 0;
+  int rc = dsa::check_device(&sms);
   if (rc != DSA_OK) return rc;
   if (T == 0) return DSA_OK;
   int lb = 0;
@@ -202,13 +947,16 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   p.max_logits = max_logits;
   p.H = H;
   p.Hc = Hc;
-  p.Dqk = Dqk;
-  p.Dv = Dv;
   p.K = K;
-  p.separate = separate;
+  p.G = (H / Hc + kHG - 1) / kHG;
+  p.splits = need > 0 ? plan_splits(units, K) : 1;
+  p.n_items = static_cast<int>(units * p.splits);
+  p.status = dsa::device_status_ptr();
+  if (need > 0) {
+    p.part_s = static_cast<float4*>(workspace);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(T, H, p.splits));
+  }
   p.scale_log2 = scale * kLog2e;
-  const int per = (H / Hc + kHeads - 1) / kHeads;
-  const int smem = kKeys * (Dqk + kPad + (separate ? Dv + kPad : 0)) + kHeads * Dqk * 4;
-  attn_kv8_kernel<<<dim3(T, Hc * per), kThreads, smem, stream>>>(p);
-  return dsa::launch_error("attn_kv8_kernel");
+  if (separate) return launch<256, 256, true>(p, T, sms, stream);
+  return Dqk == 576 ? launch<576, 512, false>(p, T, sms, stream) : launch<512, 512, false>(p, T, sms, stream);
 }

@@ -458,6 +458,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t start, uint32_t lbo, uint
   return d;
 }
 constexpr uint32_t kSwizzle128B = 2;
+constexpr uint32_t kSwizzle64B = 4;
 
 // (d0, d1) = (a0 * b0 + d0, a1 * b1 + d1): two fp32 fmas with round to
 // nearest in one packed instruction (fma.rn.f32x2); each lane is exactly
