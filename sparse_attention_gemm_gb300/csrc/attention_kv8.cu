@@ -31,6 +31,7 @@
 //
 // Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
 // MMA1, 17 MMA2, 18..19 idle (they fill the fifth warpgroup).
+#include <atomic>
 #include <climits>
 
 #include "kv8.cuh"
@@ -56,7 +57,6 @@ static_assert(3 * 128 * kLeanRegs + 2 * 128 * kSoftRegs <= kThreads * kLaunchReg
 constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
-constexpr uint32_t kPBytes = 2 * kPPart;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Weights reach 2^kTheta before the reference moves; kWeight = 2^(8 - kTheta)
@@ -91,33 +91,36 @@ struct Params {
   float scale_log2;
 };
 
+// A key row is kFull chunks of 128 codes (128-byte swizzle) and, at 576 dims,
+// a tail of 64 (64-byte swizzle).  MMA2 does not read the tail, so once a
+// tile's scores are done its space takes the first term of the tile's P^T; that is
+// what makes four buffers fit.
 template <int DQK, int DV, bool SEP>
 struct Shape {
-  static constexpr int kNqk = (DQK + 127) / 128;           // 128-code chunks of a key row
+  static constexpr int kFull = DQK / 128;
+  static constexpr bool kTail = DQK % 128 != 0;
+  static_assert(DQK % 128 == 0 || DQK % 128 == 64, "tail of 64 codes");
   static constexpr int kNv = DV / 128;
-  static constexpr int kTail = DQK % 128 ? (DQK % 128) / 32 : 4;  // K = 32 steps of the last chunk
-  static constexpr int kChunks = kNqk + (SEP ? kNv : 0);
-  static constexpr int kVFirst = SEP ? kNqk : 0;
-  static constexpr int kStages = DQK == 576 ? 3 : 4;
-  static constexpr uint32_t kBuf = kChunks * kChunkBytes;
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kKv = kQ + kNqk * kQChunkBytes;
-  static constexpr uint32_t kP = kKv + kStages * kBuf;
-  static constexpr uint32_t kSmall = kP + 2 * kPBytes;
-  // wmax, red [4][64]; alpha, mref, fac [64]; qsc [3][64]; svm [4]; exflag [2][8]
-  static constexpr uint32_t kSmallBytes = (2 * 256 + 3 * 64 + 3 * 64 + 4 + 16) * 4;
-  static constexpr uint32_t kBars = kSmall + kSmallBytes;
+  static constexpr uint32_t kVOff = SEP ? kFull * kChunkBytes : 0;  // V inside a tile buffer
+  static constexpr uint32_t kTailOff = kFull * kChunkBytes;
+  static constexpr uint32_t kBuf = (kFull + (SEP ? kNv : 0)) * kChunkBytes + (kTail ? kKeys * 64 : 0);
+  static constexpr int kStages = SEP ? 5 : 4;
+  static constexpr uint32_t kQTail = kFull * kQChunkBytes;
+  static constexpr uint32_t kQBytes = kQTail + (kTail ? 2 * kHG * 64 : 0);
+  static constexpr uint32_t kKv = kQBytes;
+  static constexpr uint32_t kPLo = kKv + kStages * kBuf;               // [2]
+  static constexpr uint32_t kPHi = kTail ? kKv + kTailOff : kPLo + 2 * kPPart;  // stage by stage, or [2]
+  static constexpr uint32_t kPHiStep = kTail ? kBuf : kPPart;
+  static constexpr uint32_t kWmax = kPLo + (kTail ? 2 : 4) * kPPart;   // float [4][64]
+  static constexpr uint32_t kAlpha = kWmax + 1024;                     // float [8][32]
+  static constexpr uint32_t kQsc = kAlpha + 1024;                      // float [3][64]
+  static constexpr uint32_t kSvm = kQsc + 768;                         // float [4]
+  static constexpr uint32_t kBars = kSvm + 16;
   static constexpr uint32_t kMisc = kBars + 24 * 8;
   static constexpr uint32_t kTotal = kMisc + 16;
-  static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
-  static_assert(kSmallBytes % 8 == 0, "alignment");
+  static_assert(kTotal <= 227 * 1024, "shared memory");
+  static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kPLo % 1024 == 0, "alignment");
 };
-
-__device__ __forceinline__ int ord_f32(float f) {
-  int i = __float_as_int(f);
-  return i >= 0 ? i : (i ^ 0x7FFFFFFF);
-}
-__device__ __forceinline__ float unord_f32(int i) { return __int_as_float(i >= 0 ? i : (i ^ 0x7FFFFFFF)); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -146,6 +149,8 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 h2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint2 pack4(const uint16_t (&c)[4]) {
@@ -158,6 +163,26 @@ __device__ __forceinline__ float pow2_ceil(float x) {
   uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) ? 1u : 0u);
   e = e < 1u ? 1u : (e > 253u ? 253u : e);
   return __uint_as_float(e << 23);
+}
+
+// Byte offset of 16-byte unit `u` of row `r` in rows of 64 bytes, 64-byte swizzle.
+__device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t u) { return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4); }
+
+// Combines v[0..7] (one value per head hb + i) over the 8 lanes that share
+// lane & 3, halving the values at each step: lane keeps head hb + own_head(lane).
+__device__ __forceinline__ int own_head(int lane) { return ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1); }
+template <class F>
+__device__ __forceinline__ float fold8(float (&v)[8], int lane, F f) {
+#pragma unroll
+  for (int n = 4, bit = 16; n > 0; n >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+    }
+  }
+  return v[0];
 }
 
 // One work item: the tiles [i0, i1) of row t.
@@ -197,30 +222,27 @@ template <int DQK, int DV, bool SEP>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   using S = Shape<DQK, DV, SEP>;
   constexpr int ST = S::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = dsa::smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  int* wmax = reinterpret_cast<int*>(smem + S::kSmall);  // [4 quarters][64 heads]
-  float* red = reinterpret_cast<float*>(wmax + 256);     // [4][64]
-  float* alpha = red + 256;                              // [64]
-  float* mref = alpha + 64;                              // [64]
-  float* fac = mref + 64;                                // [64]
+  extern __shared__ __align__(1024) uint8_t smem[];  // the kernel has no other shared memory
+  if (dsa::smem_u32(smem) & 1023u) {                 // would break every swizzle
+    if (threadIdx.x == 0) atomicOr(p.status, DSA_STATUS_CHECK_FAILED);
+    return;
+  }
+  float* wmax = reinterpret_cast<float*>(smem + S::kWmax);  // [4 quarters][64 heads]
   // Query scales (times scale * log2(e)) of three items in turn: the gather
   // warps convert item n + 3's query after MMA1 of item n + 2 has run, which
   // needed the S buffer of item n, which the softmax hands back after reading these.
-  float* qsc = fac + 64;                                 // [3][64]
-  float* svm = qsc + 192;                                // [4]
-  int* exflag = reinterpret_cast<int*>(svm + 4);         // [2][8]
+  float* qsc = reinterpret_cast<float*>(smem + S::kQsc);  // [3][64]
+  float* svm = reinterpret_cast<float*>(smem + S::kSvm);  // [4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  uint64_t* kv_full = bars;        // [4]
-  uint64_t* kv_empty = bars + 4;   // [4]
-  uint64_t* s_full = bars + 8;     // [2]
-  uint64_t* s_empty = bars + 10;   // [2]
-  uint64_t* p_full = bars + 12;    // [2]
-  uint64_t* p_empty = bars + 14;   // [2]: MMA2 of the tile has run
-  uint64_t* q_full = bars + 16;
-  uint64_t* q_empty = bars + 17;
-  uint64_t* drain = bars + 18;     // [2]: the MMA issuers' exit commits
+  uint64_t* kv_full = bars;        // [5]
+  uint64_t* kv_empty = bars + 5;   // [5]
+  uint64_t* s_full = bars + 10;    // [2]
+  uint64_t* s_empty = bars + 12;   // [2]
+  uint64_t* p_full = bars + 14;    // [2]
+  uint64_t* p_empty = bars + 16;   // [2]: MMA2 of the tile has run
+  uint64_t* q_full = bars + 18;
+  uint64_t* q_empty = bars + 19;
+  uint64_t* drain = bars + 20;     // [2]: the MMA issuers' exit commits
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
@@ -258,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // are read two tiles ahead, the table one tile ahead.
     const int gt = threadIdx.x, piece = gt & 7;
     const uint64_t keep = dsa::l2_policy_evict_last();  // rows are selected by many queries
+    const uint64_t once = dsa::l2_policy_evict_first();
     const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
     int tile_ctr = 0, item_ctr = 0;
     int pend = -1;  // stage whose copies are in flight
@@ -266,6 +289,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
       __syncwarp();
       if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
+    };
+    // The query: four threads per head, each with 16-byte units sub, sub + 4, ...
+    // of its two operand rows.  A unit pair (hi, lo) is as large as the 16 bf16
+    // values it is made of: they land there and are converted in place.
+    const int hq = gt >> 2, sub = gt & 3;
+    // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
+    // which gives each softmax thread eight consecutive heads
+    const int hr = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
+    auto q_unit = [&](int u, int lo) {
+      const int r = hr + lo * kHG;
+      return u < S::kFull * 8 ? (u >> 3) * kQChunkBytes + dsa::sw128_offset(r, (u & 7) * 16)
+                              : S::kQTail + sw64_offset(r, u - S::kFull * 8);
+    };
+    auto send_query = [&](const Item& w) {
+      const bool real = hq < w.hv;
+      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK;
+      const uint32_t qa = dsa::smem_u32(smem);
+#pragma unroll
+      for (int k = 0; k < DQK / 64; ++k) {
+        const int u = sub + 4 * k;
+        cp_async16(qa + q_unit(u, 0), src + u * 16, real ? 16u : 0u, once);
+        cp_async16(qa + q_unit(u, 1), src + u * 16 + 8, real ? 16u : 0u, once);
+      }
+      cp_async_commit();
+    };
+    auto convert_query = [&](const Item& w, int n_item) {
+      uint32_t m = 0;
+#pragma unroll 3
+      for (int k = 0; k < DQK / 64; ++k) {
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo) {
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, lo));
+          m = max(m, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
+          m = max(m, max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu)));
+        }
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // a head with infinity or NaN: its scores are NaN
+      const bool finite = m < 0x7F80u;
+      const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
+      const float inv = 1.f / s;
+      if (sub == 0) qsc[(n_item % 3) * 64 + hq] = finite ? s * p.scale_log2 : __uint_as_float(0x7FC00000u);
+#pragma unroll 1
+      for (int k = 0; k < DQK / 64; ++k) {
+        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 0)),
+                        reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 1))};
+        const uint4 v0 = *at[0], v1 = *at[1];
+        const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint16_t h2[2], l2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t u = wd[2 * n + e];
+            const __half2 h = __floats2half2_rn(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xFFFF0000u) * inv);
+            h2[e] = dsa::e4m3x2_h2(h2_bits(h));
+            l2[e] = dsa::e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(h2[e]))), __float2half2_rn(16.f))));
+          }
+          hi[n] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
+          lo[n] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
+        }
+        *at[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *at[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      dsa::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(q_full);
+    };
+    // L2 prefetch of a later item's query and ids
+    auto prefetch_item = [&](int it) {
+      if (it >= p.n_items) return;
+      const Item w = get_item(p, it, t_end);
+      if (w.i0 >= w.i1) return;
+      const uint8_t* q0 = reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK);
+      for (int o = gt * 128; o < w.hv * DQK * 2; o += kGatherThreads * 128) l2_prefetch(q0 + o);
+      const int j = w.i0 * kKeys + gt * 32;
+      if (j < min(w.i1 * kKeys, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
     };
     for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
       const Item w = get_item(p, it, t_end);
@@ -276,6 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         const int j = i * kKeys + kg * kGatherKeys + (gt >> 3);
         return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
       };
+      // the query first where its buffer is free already (a CTA's first item)
+      const bool q_sent = __all_sync(0xffffffffu, dsa::mbar_test_wait(q_empty, (item_ctr & 1) ^ 1));
+      if (q_sent) send_query(w);
       int row[kGatherSteps], nid[kGatherSteps];
 #pragma unroll
       for (int kg = 0; kg < kGatherSteps; ++kg) {
@@ -314,13 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
           const uint32_t dst = buf + dsa::sw128_offset(key, piece * 16);
 #pragma unroll
-          for (int c = 0; c < S::kNqk; ++c)
-            if (c * 128 + piece * 16 < DQK) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes, keep);
+          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes, keep);
+          if (S::kTail && piece < 4)
+            cp_async16(buf + S::kTailOff + sw64_offset(key, piece), krow + S::kFull * 128, nbytes, keep);
           if (SEP) {
             const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
 #pragma unroll
             for (int c = 0; c < S::kNv; ++c)
-              cp_async16(dst + (S::kNqk + c) * kChunkBytes, vrow + c * 128, nbytes, keep);
+              cp_async16(dst + S::kVOff + c * kChunkBytes, vrow + c * 128, nbytes, keep);
           }
         }
         cp_async_commit();
@@ -330,60 +436,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         pend = stage;
         if (i == w.i0) {
-          // The item's query, once MMA1 of the item before has run: its tiles
-          // must all be signalled before this waits for them.
-          cp_async_wait<0>();
-          signal(pend);
-          pend = -1;
-          if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) {
-            ok = false;
-            break;
-          }
-          // four threads per head, 16-byte pieces sub, sub + 4, ...
-          const int hq = gt >> 2, sub = gt & 3;
-          const bool real = hq < w.hv;
-          const uint4* src =
-              reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK) + sub;
-          uint32_t m = 0;
-#pragma unroll 6
-          for (int k = 0; k < DQK / 32; ++k) {
-            const uint4 v = __ldg(src + 4 * k);
-            m = max(m, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
-            m = max(m, max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu)));
-          }
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          // a head with infinity or NaN: its scores are NaN
-          const bool finite = m < 0x7F80u;
-          const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
-          const float inv = real ? 1.f / s : 0.f;
-          if (sub == 0)
-            qsc[(item_ctr % 3) * 64 + hq] = !real ? 0.f : (finite ? s * p.scale_log2 : __uint_as_float(0x7FC00000u));
-          // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
-          // which gives each softmax thread eight consecutive heads
-          const int hr = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
-          uint8_t* qb = smem + S::kQ;
-#pragma unroll 3
-          for (int k = 0; k < DQK / 32; ++k) {
-            const uint4 v = __ldg(src + 4 * k);
-            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-            uint16_t hi[4], lo[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const __half2 h = __floats2half2_rn(__uint_as_float(wd[n] << 16) * inv,
-                                                  __uint_as_float(wd[n] & 0xFFFF0000u) * inv);
-              hi[n] = dsa::e4m3x2_h2(h2_bits(h));
-              lo[n] = dsa::e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(hi[n]))), __float2half2_rn(16.f))));
+          if (!q_sent) {
+            // MMA1 of the item before must have run: its tiles (and this one,
+            // so that nothing waits for it later) are signalled first
+            cp_async_wait<0>();
+            signal(pend);
+            pend = -1;
+            if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) {
+              ok = false;
+              break;
             }
-            const int el = (sub + 4 * k) * 8;
-            const uint32_t off = (el >> 7) * kQChunkBytes + dsa::sw128_offset(hr, (el & 127) & ~15) + (el & 8);
-            *reinterpret_cast<uint2*>(qb + off) = pack4(hi);
-            *reinterpret_cast<uint2*>(qb + off + kHG * 128) = pack4(lo);
+            send_query(w);
           }
-          dsa::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) dsa::mbar_arrive(q_full);
+          cp_async_wait<0>();
+          if (pend >= 0) signal(pend);
+          pend = -1;
+          convert_query(w, item_ctr);
           ++item_ctr;
+          prefetch_item(it + gridDim.x);
         }
       }
     }
@@ -400,8 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     bool ok = true;
     if (warp == kMmaWarp) {
       constexpr uint32_t idesc1 = dsa::idesc_e4m3(kKeys, 2 * kHG);
-      const uint64_t q_desc = dsa::smem_desc(base + S::kQ, 16, 1024, dsa::kSwizzle128B);
+      const uint64_t q_desc = dsa::smem_desc(base, 16, 1024, dsa::kSwizzle128B);
       const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
+      const uint64_t qt_desc = dsa::smem_desc(base + S::kQTail, 16, 512, dsa::kSwizzle64B);
+      const uint64_t kt_desc = dsa::smem_desc(base + S::kKv + S::kTailOff, 16, 512, dsa::kSwizzle64B);
       int item_ctr = 0;
       for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
         const Item w = get_item(p, it, t_end);
@@ -415,11 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
           const uint32_t d = tmem_base + kSCol + b * 128;
 #pragma unroll
-          for (int c = 0; c < S::kNqk; ++c) {
+          for (int c = 0; c < S::kFull; ++c) {
             const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < (c + 1 < S::kNqk ? 4 : S::kTail); ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               dsa::umma_f8_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
+          }
+          if (S::kTail) {
+            const uint64_t at = kt_desc + stage * (S::kBuf >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) dsa::umma_f8_if(leader && got, d, at + kk * 2, qt_desc + kk * 2, idesc1, 1u);
           }
           if (leader && got) dsa::umma_commit(&s_full[b]);
           if (!__all_sync(0xffffffffu, got)) {
@@ -437,25 +514,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     } else {
       constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kHG) | (1u << 15) | (1u << 16);  // both MN-major
       const uint64_t v_desc =
-          dsa::smem_desc(base + S::kKv + S::kVFirst * kChunkBytes, kChunkBytes, 1024, dsa::kSwizzle128B);
+          dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
       // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
-      const uint64_t p_desc = dsa::smem_desc(base + S::kP, kPPart, 512, dsa::kSwizzle64B);
+      const uint64_t ph_desc = dsa::smem_desc(base + S::kPHi, kPPart, 512, dsa::kSwizzle64B);
+      const uint64_t pl_desc = dsa::smem_desc(base + S::kPLo, kPPart, 512, dsa::kSwizzle64B);
       for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
         const Item w = get_item(p, it, t_end);
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
           const int b = tile_ctr & 1, stage = tile_ctr % ST;
           const bool got = dsa::mbar_wait(&p_full[b], (tile_ctr >> 1) & 1, wt);
           dsa::tc_fence_after();
-          const uint64_t a0 = v_desc + stage * (S::kBuf >> 4), b0 = p_desc + b * (kPBytes >> 4);
+          const uint64_t a0 = v_desc + stage * (S::kBuf >> 4);
+          const uint64_t bh = ph_desc + (S::kTail ? stage : b) * (S::kPHiStep >> 4), bl = pl_desc + b * (kPPart >> 4);
 #pragma unroll
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t d = tmem_base + kOCol + mb * kHG;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 32; ++kk) {
               const uint64_t a = a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4);
-              const uint64_t bp = b0 + kk * (32 * kHG >> 4);
-              dsa::umma_f8_if(leader && got, d, a, bp, idesc2, (i > w.i0 || kk > 0) ? 1u : 0u);
-              dsa::umma_f8_if(leader && got, d, a, bp + (kPPart >> 4), idesc2, 1u);
+              dsa::umma_f8_if(leader && got, d, a, bh + kk * (32 * kHG >> 4), idesc2, (i > w.i0 || kk > 0) ? 1u : 0u);
+              dsa::umma_f8_if(leader && got, d, a, bl + kk * (32 * kHG >> 4), idesc2, 1u);
             }
           }
           if (leader && got) {
@@ -483,6 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
     const int hb = hh * 32 + 8 * (lane & 3);
     const bool want_max = p.max_logits != nullptr;
+    float* alpha = reinterpret_cast<float*>(smem + S::kAlpha) + sw * 32;  // this warp's factors of O^T
+    // epilogue scratch, in P^T's second term (free once MMA2 has run)
+    float* red = reinterpret_cast<float*>(smem + S::kPLo);  // [4][64] sums
+    float* redm = red + 256;                                // [4][64] maxima
+    float* mref = redm + 256;                               // [64]
+    float* fac = mref + 64;                                 // [64]
     int tile_ctr = 0, item_ctr = 0;
     bool ok = true;
     // A wait of this thread gave up: the eight warps leave together, at a
@@ -506,12 +590,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         continue;
       }
-      float l_part[8], qs[8];
-      float m_max = -INFINITY;
-      float ref = __uint_as_float(1u << 23);  // 2^E of the value scales so far
-      float inv = 0.f;                        // 2^-E
+      // Per head hb + h: the reference, this thread's keys' sum and (for
+      // max_logits) maximum.  kNone is below every score, so that the first
+      // valid key moves the reference and -inf - kNone is -inf, not NaN.
+      constexpr float kNone = -3e38f;
+      float m[8], l_part[8], qs[8], top[8];
+      float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
+      float inv = __uint_as_float(253u << 23);  // 2^-E
 #pragma unroll
-      for (int h = 0; h < 8; ++h) l_part[h] = 0.f;
+      for (int h = 0; h < 8; ++h) l_part[h] = 0.f, m[h] = kNone, top[h] = -INFINITY;
       const int b_seq = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, w.t) : 0;
       const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
       auto load_id = [&](int i, int k) {
@@ -530,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       float nsvA = SEP ? scale_of(p.v_scale, blA) : nskA, nsvB = SEP ? scale_of(p.v_scale, blB) : nskB;
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
         const int b = tile_ctr & 1;
-        const uint32_t ph = (tile_ctr >> 1) & 1;
+        const uint32_t par = (tile_ctr >> 1) & 1;
         const bool vA = blA >= 0, vB = blB >= 0;
         const float skA = nskA, skB = nskB, svA = nsvA, svB = nsvB;
         blA = nblA;
@@ -543,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         nblB = block_of(idB);
         idA = load_id(i + 3, kA);
         idB = load_id(i + 3, kB);
-        if (!failed) failed = !dsa::mbar_wait(&s_full[b], ph, wt);
+        if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
         dsa::tc_fence_after();
         float x[16];
         {
@@ -565,54 +652,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         dsa::tc_fence_before();
         __syncwarp();
         if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
-        // x: scores in powers of two; y: against the reference m of each head
-        float y[16];
+        // scores in powers of two; -inf where the slot is not valid
         bool ex = svA > ref || svB > ref;
-        {
-          const float4 ma = *reinterpret_cast<const float4*>(mref + hb), mb = *reinterpret_cast<const float4*>(mref + hb + 4);
-          const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[4 * j + e] *= qs[2 * j + e] * skA;
-              x[4 * j + 2 + e] *= qs[2 * j + e] * skB;
-              y[4 * j + e] = vA ? x[4 * j + e] - m[2 * j + e] : -INFINITY;
-              y[4 * j + 2 + e] = vB ? x[4 * j + 2 + e] - m[2 * j + e] : -INFINITY;
-              ex |= (y[4 * j + e] > kTheta) || (y[4 * j + 2 + e] > kTheta);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const int h = 2 * j + e;
+            float& xa = x[4 * j + e];
+            float& xb = x[4 * j + 2 + e];
+            xa = vA ? xa * (qs[h] * skA) : -INFINITY;
+            xb = vB ? xb * (qs[h] * skB) : -INFINITY;
+            ex |= xa - m[h] > kTheta || xb - m[h] > kTheta;
+            if (want_max) top[h] = fmaxf(top[h], fmaxf(xa, xb));
           }
         }
-        const uint32_t wflags = __reduce_or_sync(0xffffffffu, (ex ? 1u : 0u) | (failed ? 2u : 0u));
-        if (lane == 0) exflag[b * 8 + sw] = static_cast<int>(wflags);
-        named_bar(1, kSoftThreads);
-        const bool first = i == w.i0;  // always sets the references (mref holds the item before's)
-        bool reduce = want_max || first;
-        int any_failed = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int f = exflag[b * 8 + k];
-          reduce |= (f & 1) != 0;
-          any_failed |= f & 2;
-        }
-        if (any_failed) {  // every softmax thread read the same flags
-          ok = false;
-          break;
-        }
+        const bool first = i == w.i0;
         bool need_rescale = false;
         float ratio = 1.f;  // of the old to the new 2^E
-        if (reduce) {
+        if (dsa::named_bar_any(1, kSoftThreads, ex || failed)) {
+          if (dsa::named_bar_any(1, kSoftThreads, failed)) {  // the group leaves together
+            ok = false;
+            break;
+          }
+          // move the references: the tile's maximum per head over its 64 keys
+          float v[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(vA ? x[4 * j + e] : -INFINITY, vB ? x[4 * j + 2 + e] : -INFINITY);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              if (lane < 4) wmax[quarter * 64 + hb + 2 * j + e] = ord_f32(mx);
-            }
+            v[2 * j] = fmaxf(x[4 * j], x[4 * j + 2]);
+            v[2 * j + 1] = fmaxf(x[4 * j + 1], x[4 * j + 3]);
           }
+          const float mx = fold8(v, lane, [](float a, float c) { return fmaxf(a, c); });
+          wmax[quarter * 64 + hb + own_head(lane)] = mx;
           float sv = fmaxf(svA, svB);
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 4));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
@@ -623,39 +694,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           inv = 1.f / rn;
           ratio = ref * inv;
           ref = rn;
-          if (st < 64) {
-            const int r = max(max(wmax[st], wmax[64 + st]), max(wmax[128 + st], wmax[192 + st]));
-            const float tmax = unord_f32(r);
-            const float mo = first ? -INFINITY : mref[st];
-            const float mn = (tmax > mo + kTheta) ? tmax : mo;
-            alpha[st] = (mn == mo) ? 1.f : ex2(mo - mn);
-            mref[st] = mn;
-            m_max = fmaxf(m_max, tmax);
-          }
-          named_bar(1, kSoftThreads);
-          const float4 aa = *reinterpret_cast<const float4*>(alpha + hb), ab = *reinterpret_cast<const float4*>(alpha + hb + 4);
-          const float4 ma = *reinterpret_cast<const float4*>(mref + hb), mb = *reinterpret_cast<const float4*>(mref + hb + 4);
-          const float a[8] = {aa.x, aa.y, aa.z, aa.w, ab.x, ab.y, ab.z, ab.w};
-          const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
           bool moved = ratio != 1.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int g4 = 0; g4 < 2; ++g4) {
+            float4 t4 = *reinterpret_cast<const float4*>(wmax + hb + 4 * g4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              moved |= a[2 * j + e] != 1.f;
-              l_part[2 * j + e] *= a[2 * j + e];
-              y[4 * j + e] = vA ? x[4 * j + e] - m[2 * j + e] : -INFINITY;
-              y[4 * j + 2 + e] = vB ? x[4 * j + 2 + e] - m[2 * j + e] : -INFINITY;
+            for (int q4 = 1; q4 < 4; ++q4) {
+              const float4 o = *reinterpret_cast<const float4*>(wmax + q4 * 64 + hb + 4 * g4);
+              t4.x = fmaxf(t4.x, o.x), t4.y = fmaxf(t4.y, o.y), t4.z = fmaxf(t4.z, o.z), t4.w = fmaxf(t4.w, o.w);
+            }
+            const float tm[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int h = 4 * g4 + k;
+              const float mn = tm[k] > m[h] + kTheta ? tm[k] : m[h];
+              const float a = ex2(m[h] - mn);
+              moved |= mn != m[h];
+              l_part[h] *= a;
+              m[h] = mn;
+              if (lane < 4) alpha[hb - hh * 32 + h] = a * ratio;
             }
           }
           need_rescale = __any_sync(0xffffffffu, moved) && !first;
         }
-        // P^T rows kA and kB, both terms: the thread's eight heads are bytes
-        // hb .. hb + 7 of the 64-byte rows (64-byte swizzle: 16-byte unit ^ (key >> 1 & 3))
-        if (!failed) failed = !dsa::mbar_wait(&p_empty[b], ph ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
+        // P^T rows kA and kB, both terms: the thread's eight heads are bytes hb .. hb + 7 of the 64-byte rows
+        if (!failed) failed = !dsa::mbar_wait(&p_empty[b], par ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
         {
-          uint8_t* pb = smem + S::kP + b * kPBytes;
-          const int unit = hb >> 4, in = hb & 8;
+          uint8_t* ph = smem + S::kPHi + (S::kTail ? tile_ctr % ST : b) * S::kPHiStep;
+          uint8_t* pl = smem + S::kPLo + b * kPPart;
           const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -664,23 +730,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             uint16_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float p0 = ex2(y[4 * j + 2 * k]), p1 = ex2(y[4 * j + 2 * k + 1]);
+              const float p0 = ex2(x[4 * j + 2 * k] - m[2 * j]), p1 = ex2(x[4 * j + 2 * k + 1] - m[2 * j + 1]);
               l_part[2 * j] += p0;
               l_part[2 * j + 1] += p1;
               const __half2 h = __floats2half2_rn(p0 * wk, p1 * wk);
               hi[j] = dsa::e4m3x2_h2(h2_bits(h));
               lo[j] = dsa::e4m3x2_h2(h2_bits(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(hi[j])))));
             }
-            uint8_t* at = pb + key * kHG + ((unit ^ ((key >> 1) & 3)) << 4) + in;
-            *reinterpret_cast<uint2*>(at) = pack4(hi);
-            *reinterpret_cast<uint2*>(at + kPPart) = pack4(lo);
+            const uint32_t at = sw64_offset(key, hb >> 4) + (hb & 8);
+            *reinterpret_cast<uint2*>(ph + at) = pack4(hi);
+            *reinterpret_cast<uint2*>(pl + at) = pack4(lo);
           }
         }
         if (need_rescale) {
           // MMA2 of the previous tile must have landed before O^T is scaled
           if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((tile_ctr - 1) >> 1) & 1, wt);
           dsa::tc_fence_after();
-          const float* a32 = alpha + hh * 32;
+          __syncwarp();  // alpha, written by four lanes of this warp
 #pragma unroll 1
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t ta = tmem_base + lane_off + kOCol + mb * kHG + hh * 32;
@@ -688,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             dsa::tmem_ld32(ta, v);
             dsa::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * (a32[c] * ratio));
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha[c]);
             dsa::tmem_st32(ta, v);
           }
           dsa::tmem_wait_st();
@@ -705,19 +771,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       // been waited for in turn, so the parity names that tile)
       if (!failed) failed = !dsa::mbar_wait(&p_empty[(tile_ctr - 1) & 1], ((tile_ctr - 1) >> 1) & 1, wt);
       dsa::tc_fence_after();
+      if (quarter == 0 && lane < 4) {
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        float v = l_part[h];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (lane < 4) red[quarter * 64 + hb + h] = v;
+        for (int h = 0; h < 8; ++h) mref[hb + h] = m[h];
       }
+      red[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
+      if (want_max)
+        redm[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
       named_bar(1, kSoftThreads);
       const float unscale = ref * (1.f / kWeight);
       if (st < 64) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
         const float mc = mref[st];
+        const float m_max = want_max ? fmaxf(fmaxf(redm[st], redm[64 + st]), fmaxf(redm[128 + st], redm[192 + st])) : 0.f;
         const bool any = l != 0.f;  // true for NaN too
         float f = unscale;
         if (p.splits > 1) {
@@ -866,15 +932,22 @@ size_t part_bytes(int T, int H, int splits) {
 template <int DQK, int DV, bool SEP>
 int launch(const Params& p, int T, int sms, cudaStream_t stream) {
   using S = Shape<DQK, DV, SEP>;
-  constexpr int smem = S::kTotal + 1024;
+  constexpr int smem = S::kTotal;
   auto kernel = attn_kv8_kernel<DQK, DV, SEP>;
-  // the register split assumes the launch count it was sized for
-  cudaFuncAttributes fa{};
-  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
-    return dsa::set_error(DSA_ERR_CUDA, "attn_kv8_kernel: compiled with %d registers per thread, expected %d", fa.numRegs,
-                          kLaunchRegs);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return dsa::launch_error("attn_kv8_kernel smem attribute");
+  // once per device: the register split assumes the launch count it was sized
+  // for, and the kernel needs its shared memory allowed
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaGetDevice(&dev);  // below 64: check_device
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
+      return dsa::set_error(DSA_ERR_CUDA, "attn_kv8_kernel: compiled with %d registers per thread, expected %d", fa.numRegs,
+                            kLaunchRegs);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return dsa::launch_error("attn_kv8_kernel smem attribute");
+    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
   kernel<<<p.n_items < sms ? p.n_items : sms, kThreads, smem, stream>>>(p);
   int rc = dsa::launch_error("attn_kv8_kernel");
   if (rc != DSA_OK || p.splits == 1) return rc;

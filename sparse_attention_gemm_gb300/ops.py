@@ -608,68 +608,101 @@ def sparse_attn_bwd(q, kv, out, dout, lse_kv, idx, scale: float, topk_length=Non
     return {"dq": dq, "dkv": dkv, "d_sink": d_sink}
 
 
-def _need_here(**tensors):
-    """The call goes to the current device's current stream: so do its tensors."""
-    here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+# The calls on the 8-bit cache are made once or twice per layer of a decode
+# step, whose kernels run for a few microseconds: their arguments are checked
+# in one pass each, and pointers and the stream go to ctypes as plain integers
+# (kv8_read from Python: 15.2 us a call with the helpers above, 8 us so).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _kv8_cache(cache, scale, name="cache"):
-    _need(cache, name, torch.uint8, 4)
-    _need(scale, f"{name}_scale", torch.float32, 2)
-    n_blocks, block, heads, dim = cache.shape
-    if scale.shape[0] != n_blocks or scale.shape[1] != heads:
-        raise ValueError(f"{name}_scale must be [{n_blocks}, {heads}], got {tuple(scale.shape)}")
-    return n_blocks, block, heads, dim
+def _arg(t, name, dtype, dim, device):
+    """Pointer of a tensor argument on `device` (None stays None); raises as _need does."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim or not t.is_contiguous() or
+            t.get_device() != device):
+        _need(t, name, dtype, dim)
+        raise ValueError(f"{name} is on {t.device}, other arguments are on cuda:{device}")
+    return t.data_ptr()
 
 
-def _kv8_sequences(cu_seqlens, pos, block_table):
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+def _required(t, name, dtype, dim, device):
+    p = _arg(t, name, dtype, dim, device)
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return p
+
+
+def _device_of(t, name, dtype, dim):
+    """Device index of the first argument; the call goes to the current device's current stream."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _need(t, name, dtype, dim)
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _kv8_scale(scale, name, n_blocks, heads, device):
+    p = _required(scale, name, torch.float32, 2, device)
+    if scale.shape != (n_blocks, heads):
+        raise ValueError(f"{name} must be [{n_blocks}, {heads}], got {tuple(scale.shape)}")
+    return p
+
+
+def _kv8_sequences(cu_seqlens, pos, block_table, device):
+    """(n_seqs, table width, pointers of cu_seqlens, pos, block_table)"""
+    pc = _required(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
     n_seqs = cu_seqlens.shape[0] - 1
-    if pos is not None:
-        _need(pos, "pos", torch.int32, 1)
-        if pos.shape[0] != n_seqs:
-            raise ValueError(f"pos must have {n_seqs} entries, got {pos.shape[0]}")
+    pp = _arg(pos, "pos", torch.int32, 1, device)
+    if pos is not None and pos.shape[0] != n_seqs:
+        raise ValueError(f"pos must have {n_seqs} entries, got {pos.shape[0]}")
+    pt = _arg(block_table, "block_table", torch.int32, 2, device)
     width = 0
     if block_table is not None:
-        _need(block_table, "block_table", torch.int32, 2)
-        if block_table.shape[0] != n_seqs:
-            raise ValueError(f"block_table must have {n_seqs} rows, got {block_table.shape[0]}")
-        width = block_table.shape[1]
-    return n_seqs, width
+        rows, width = block_table.shape
+        if rows != n_seqs:
+            raise ValueError(f"block_table must have {n_seqs} rows, got {rows}")
+    return n_seqs, width, pc, pp, pt
 
 
 def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
     """Quantises the bf16 rows src [T, Hc, D] into the E4M3 block cache (uint8
     [n_blocks, block, Hc, D], scale fp32 [n_blocks, Hc]), in place; returns both."""
-    _need(src, "src", torch.bfloat16, 3)
-    n_blocks, block, heads, dim = _kv8_cache(cache, cache_scale)
-    n_seqs, width = _kv8_sequences(cu_seqlens, pos, block_table)
+    dev = _device_of(cache, "cache", torch.uint8, 4)
+    pk = _required(cache, "cache", torch.uint8, 4, dev)
+    n_blocks, block, heads, dim = cache.shape
+    ps = _kv8_scale(cache_scale, "cache_scale", n_blocks, heads, dev)
+    n_seqs, width, pc, pp, pt = _kv8_sequences(cu_seqlens, pos, block_table, dev)
+    px = _required(src, "src", torch.bfloat16, 3, dev)
     T = src.shape[0]
-    if src.shape[1] != heads or src.shape[2] != dim:
+    if src.shape != (T, heads, dim):
         raise ValueError(f"src must be [T, {heads}, {dim}], got {tuple(src.shape)}")
-    _need_here(src=src, cache=cache, cache_scale=cache_scale, cu_seqlens=cu_seqlens, pos=pos, block_table=block_table)
-    _check("dsa_kv8_write", lib().dsa_kv8_write(_p(src), _p(cu_seqlens), _p(pos), _p(block_table), n_seqs, T, heads,
-                                                dim, block, n_blocks, width, _p(cache), _p(cache_scale), _stream()))
+    rc = (_lib or lib()).dsa_kv8_write(px, pc, pp, pt, n_seqs, T, heads, dim, block, n_blocks, width, pk, ps,
+                                       _raw_stream(dev))
+    if rc:
+        _check("dsa_kv8_write", rc)
     return cache, cache_scale
 
 
 def kv8_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None, out=None):
     """Rows of the 8-bit block cache back to packed bf16 [T, Hc, D] (rows of an
     `out` that is given stay as they are behind the last sequence)."""
-    n_blocks, block, heads, dim = _kv8_cache(cache, cache_scale)
-    n_seqs, width = _kv8_sequences(cu_seqlens, pos, block_table)
+    dev = _device_of(cache, "cache", torch.uint8, 4)
+    pk = _required(cache, "cache", torch.uint8, 4, dev)
+    n_blocks, block, heads, dim = cache.shape
+    ps = _kv8_scale(cache_scale, "cache_scale", n_blocks, heads, dev)
+    n_seqs, width, pc, pp, pt = _kv8_sequences(cu_seqlens, pos, block_table, dev)
     if out is None:
         out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=cache.device)
-    else:
-        _need(out, "out", torch.bfloat16, 3)
-        if out.shape[0] != T or out.shape[1] != heads or out.shape[2] != dim:
-            raise ValueError(f"out must be [{T}, {heads}, {dim}], got {tuple(out.shape)}")
-    _need_here(cache=cache, cache_scale=cache_scale, cu_seqlens=cu_seqlens, pos=pos, block_table=block_table, out=out)
-    _check("dsa_kv8_read", lib().dsa_kv8_read(_p(cache), _p(cache_scale), _p(cu_seqlens), _p(pos), _p(block_table),
-                                              n_seqs, T, heads, dim, block, n_blocks, width, _p(out), _stream()))
+    po = _required(out, "out", torch.bfloat16, 3, dev)
+    if out.shape != (T, heads, dim):
+        raise ValueError(f"out must be [{T}, {heads}, {dim}], got {tuple(out.shape)}")
+    rc = (_lib or lib()).dsa_kv8_read(pk, ps, pc, pp, pt, n_seqs, T, heads, dim, block, n_blocks, width, po,
+                                      _raw_stream(dev))
+    if rc:
+        _check("dsa_kv8_read", rc)
     return out
 
 
@@ -682,62 +715,61 @@ def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, s
                         out=None, lse=None, workspace=None):
     """Sparse attention forward over the 8-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
     idx holds cache rows, or, with block_table and cu_seqlens, positions in the row's sequence."""
-    _need(q, "q", torch.bfloat16, 3)
-    n_blocks, block, heads, dim = _kv8_cache(kv8, kv_scale, "kv8")
-    _need(idx, "idx", torch.int32, 2)
+    dev = _device_of(q, "q", torch.bfloat16, 3)
+    pq = _required(q, "q", torch.bfloat16, 3, dev)
     T, H, Dqk = q.shape
-    K = idx.shape[1]
+    pk = _required(kv8, "kv8", torch.uint8, 4, dev)
+    n_blocks, block, heads, dim = kv8.shape
+    pks = _kv8_scale(kv_scale, "kv_scale", n_blocks, heads, dev)
+    pi = _required(idx, "idx", torch.int32, 2, dev)
+    rows, K = idx.shape
     if dim != Dqk:
         raise ValueError(f"kv8 rows must have the query's {Dqk} dims, got {dim}")
-    if idx.shape[0] != T:
-        raise ValueError(f"idx must have {T} rows, got {idx.shape[0]}")
-    if topk_length is not None:
-        _need(topk_length, "topk_length", torch.int32, 1)
-        if topk_length.shape[0] != T:
-            raise ValueError(f"topk_length must have {T} entries, got {topk_length.shape[0]}")
-    if sink is not None:
-        _need(sink, "sink", torch.float32, 1)
-        if sink.shape[0] != H:
-            raise ValueError(f"sink must have {H} entries, got {sink.shape[0]}")
-    Dv = 512
+    if rows != T:
+        raise ValueError(f"idx must have {T} rows, got {rows}")
+    pl = _arg(topk_length, "topk_length", torch.int32, 1, dev)
+    if topk_length is not None and topk_length.shape[0] != T:
+        raise ValueError(f"topk_length must have {T} entries, got {topk_length.shape[0]}")
+    psk = _arg(sink, "sink", torch.float32, 1, dev)
+    if sink is not None and sink.shape[0] != H:
+        raise ValueError(f"sink must have {H} entries, got {sink.shape[0]}")
+    if (v8 is None) != (v_scale is None):
+        raise ValueError("v8 and v_scale go together")
+    Dv, pv, pvs = 512, None, None
     if v8 is not None:
-        if v_scale is None:
-            raise ValueError("v8 needs v_scale")
-        if _kv8_cache(v8, v_scale, "v8")[:3] != (n_blocks, block, heads):
-            raise ValueError("v8 must have the blocks and heads of kv8")
+        pv = _required(v8, "v8", torch.uint8, 4, dev)
         Dv = v8.shape[3]
-    elif v_scale is not None:
-        raise ValueError("v_scale needs v8")
-    n_seqs, width = 0, 0
+        if v8.shape != (n_blocks, block, heads, Dv):
+            raise ValueError("v8 must have the blocks and heads of kv8")
+        pvs = _kv8_scale(v_scale, "v_scale", n_blocks, heads, dev)
+    n_seqs, width, pc, pt = 0, 0, None, None
     if block_table is not None:
         if cu_seqlens is None:
             raise ValueError("block_table needs cu_seqlens")
-        n_seqs, width = _kv8_sequences(cu_seqlens, None, block_table)
-    dev = q.device
+        n_seqs, width, pc, _, pt = _kv8_sequences(cu_seqlens, None, block_table, dev)
     if out is None:
-        out = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=dev)
-    elif _need(out, "out", torch.bfloat16, 3).shape != (T, H, Dv):
+        out = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != (T, H, Dv):
         raise ValueError(f"out must be [{T}, {H}, {Dv}], got {tuple(out.shape)}")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    elif _need(lse, "lse", torch.float32, 2).shape != (T, H):
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, H):
         raise ValueError(f"lse must be [{T}, {H}], got {tuple(lse.shape)}")
-    lse_kv = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse_kv else None
-    ml = torch.empty((T, H), dtype=torch.float32, device=dev) if want_max_logits else None
+    po, ple = _required(out, "out", torch.bfloat16, 3, dev), _required(lse, "lse", torch.float32, 2, dev)
+    lse_kv = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_lse_kv else None
+    ml = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_max_logits else None
+    L = _lib or lib()
     if workspace is None:
-        need = sparse_attn_fwd_kv8_workspace_size(T, H, heads, Dqk, Dv, K)
+        need = L.dsa_sparse_attn_fwd_kv8_workspace_size(T, H, heads, Dqk, Dv, K)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _need_here(q=q, kv8=kv8, kv8_scale=kv_scale, idx=idx, topk_length=topk_length, sink=sink, v8=v8, v8_scale=v_scale,
-               cu_seqlens=cu_seqlens if block_table is not None else None, block_table=block_table, out=out, lse=lse,
-               workspace=workspace)
-    _check("dsa_sparse_attn_fwd_kv8",
-           lib().dsa_sparse_attn_fwd_kv8(_p(q), _p(kv8), _p(kv_scale), _p(v8), _p(v_scale), _p(idx), _p(topk_length),
-                                         _p(sink), _p(cu_seqlens) if block_table is not None else None,
-                                         _p(block_table), n_seqs, T, H, heads, Dqk, Dv, K, block, n_blocks, width,
-                                         float(scale), _p(out), _p(lse), _p(lse_kv), _p(ml), _p(workspace),
-                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                         _stream()))
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    pw = _arg(workspace, "workspace", torch.uint8, 1, dev)
+    rc = L.dsa_sparse_attn_fwd_kv8(pq, pk, pks, pv, pvs, pi, pl, psk, pc, pt, n_seqs, T, H, heads, Dqk, Dv, K, block,
+                                   n_blocks, width, scale, po, ple, None if lse_kv is None else lse_kv.data_ptr(),
+                                   None if ml is None else ml.data_ptr(), pw,
+                                   0 if workspace is None else workspace.shape[0], _raw_stream(dev))
+    if rc:
+        _check("dsa_sparse_attn_fwd_kv8", rc)
     res = {"out": out, "lse": lse}
     if lse_kv is not None:
         res["lse_kv"] = lse_kv
