@@ -111,10 +111,13 @@ struct Shape {
   static constexpr uint32_t kPLo = kKv + kStages * kBuf;               // [2]
   static constexpr uint32_t kPHi = kTail ? kKv + kTailOff : kPLo + 2 * kPPart;  // stage by stage, or [2]
   static constexpr uint32_t kPHiStep = kTail ? kBuf : kPPart;
-  static constexpr uint32_t kWmax = kPLo + (kTail ? 2 : 4) * kPPart;   // float [4][64]
-  static constexpr uint32_t kAlpha = kWmax + 1024;                     // float [8][32]
-  static constexpr uint32_t kQsc = kAlpha + 1024;                      // float [3][64]
-  static constexpr uint32_t kSvm = kQsc + 768;                         // float [4]
+  // key and value scale of each slot of a stage (one number where they are one); -1: no slot
+  static constexpr uint32_t kMeta = kPLo + (kTail ? 2 : 4) * kPPart;
+  static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
+  static constexpr uint32_t kWmax = kMeta + kStages * kMetaStep;       // float [4][64]
+  static constexpr uint32_t kAlpha = kWmax + 1024;                     // float [64]
+  static constexpr uint32_t kQexp = kAlpha + 256;                      // uint8 [3][64]
+  static constexpr uint32_t kSvm = kQexp + 192;                        // float [4]
   static constexpr uint32_t kBars = kSvm + 16;
   static constexpr uint32_t kMisc = kBars + 24 * 8;
   static constexpr uint32_t kTotal = kMisc + 16;
@@ -228,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     return;
   }
   float* wmax = reinterpret_cast<float*>(smem + S::kWmax);  // [4 quarters][64 heads]
-  // Query scales (times scale * log2(e)) of three items in turn: the gather
+  // Exponents of the query scales (biased; 255: not finite) of three items in turn: the gather
   // warps convert item n + 3's query after MMA1 of item n + 2 has run, which
   // needed the S buffer of item n, which the softmax hands back after reading these.
-  float* qsc = reinterpret_cast<float*>(smem + S::kQsc);  // [3][64]
+  uint8_t* qexp = smem + S::kQexp;                        // [3][64]
   float* svm = reinterpret_cast<float*>(smem + S::kSvm);  // [4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* kv_full = bars;        // [5]
@@ -284,8 +287,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
     int tile_ctr = 0, item_ctr = 0;
     int pend = -1;  // stage whose copies are in flight
+    float psk[kGatherSteps], psv[kGatherSteps];  // and its keys' scales
     bool ok = true;
     auto signal = [&](int stage) {
+      if (piece == 0) {
+#pragma unroll
+        for (int kg = 0; kg < kGatherSteps; ++kg) {
+          const int key = kg * kGatherKeys + (gt >> 3);
+          if (SEP)
+            reinterpret_cast<float2*>(smem + S::kMeta + stage * S::kMetaStep)[key] = make_float2(psk[kg], psv[kg]);
+          else
+            reinterpret_cast<float*>(smem + S::kMeta + stage * S::kMetaStep)[key] = psk[kg];
+        }
+      }
       dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
       __syncwarp();
       if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
@@ -318,22 +332,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       uint32_t m = 0;
 #pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
-#pragma unroll
-        for (int lo = 0; lo < 2; ++lo) {
-          const uint4 v = *reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, lo));
-          m = max(m, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
-          m = max(m, max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu)));
-        }
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, 0)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, 1)), m);
       }
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
       // a head with infinity or NaN: its scores are NaN
       const bool finite = m < 0x7F80u;
       const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
-      const float inv = 1.f / s;
-      if (sub == 0) qsc[(n_item % 3) * 64 + hq] = finite ? s * p.scale_log2 : __uint_as_float(0x7FC00000u);
-#pragma unroll 1
+      const float inv = dsa::pow2_inverse(s);
+      if (sub == 0) qexp[(n_item % 3) * 64 + hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
+      // (rows of padding heads are zeros in either form)
+#pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
+        if (hq >= w.hv) break;
         uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 0)),
                         reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 1))};
         const uint4 v0 = *at[0], v1 = *at[1];
@@ -409,6 +421,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           break;
         }
         const uint32_t buf = kv_addr + stage * S::kBuf;
+        float nsk[kGatherSteps], nsv[kGatherSteps];
+#pragma unroll
+        for (int kg = 0; kg < kGatherSteps; ++kg) {
+          nsk[kg] = nsv[kg] = -1.f;
+          if (piece == 0 && cur[kg] >= 0) {
+            const int64_t at = static_cast<int64_t>(cur[kg] >> p.g.lb) * p.Hc + w.kvh;
+            nsk[kg] = __ldg(p.k_scale + at);
+            if (SEP) nsv[kg] = __ldg(p.v_scale + at);
+          }
+        }
 #pragma unroll
         for (int kg = 0; kg < kGatherSteps; ++kg) {
           const int key = kg * kGatherKeys + (gt >> 3);
@@ -435,6 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           signal(pend);
         }
         pend = stage;
+#pragma unroll
+        for (int kg = 0; kg < kGatherSteps; ++kg) psk[kg] = nsk[kg], psv[kg] = nsv[kg];
         if (i == w.i0) {
           if (!q_sent) {
             // MMA1 of the item before must have run: its tiles (and this one,
@@ -561,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
     const int hb = hh * 32 + 8 * (lane & 3);
     const bool want_max = p.max_logits != nullptr;
-    float* alpha = reinterpret_cast<float*>(smem + S::kAlpha) + sw * 32;  // this warp's factors of O^T
+    // factors of O^T per head (the four warps of a head half write the same ones)
+    float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
     // epilogue scratch, in P^T's second term (free once MMA2 has run)
     float* red = reinterpret_cast<float*>(smem + S::kPLo);  // [4][64] sums
     float* redm = red + 256;                                // [4][64] maxima
@@ -590,46 +615,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         continue;
       }
-      // Per head hb + h: the reference, this thread's keys' sum and (for
-      // max_logits) maximum.  kNone is below every score, so that the first
-      // valid key moves the reference and -inf - kNone is -inf, not NaN.
-      constexpr float kNone = -3e38f;
+      // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
       float m[8], l_part[8], qs[8], top[8];
+      bool unset = true;                        // no valid slot so far
       float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
       float inv = __uint_as_float(253u << 23);  // 2^-E
 #pragma unroll
-      for (int h = 0; h < 8; ++h) l_part[h] = 0.f, m[h] = kNone, top[h] = -INFINITY;
-      const int b_seq = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, w.t) : 0;
-      const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
-      auto load_id = [&](int i, int k) {
-        const int j = i * kKeys + k;
-        return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
-      };
-      auto block_of = [&](int id) { return id >= 0 ? dsa::kv8_block(p.g, b_seq, id >> p.g.lb) : -1; };
-      auto scale_of = [&](const float* s, int blk) {
-        return blk >= 0 ? __ldg(s + static_cast<int64_t>(blk) * p.Hc + w.kvh) : 0.f;
-      };
-      // each key's id, block and scales are read three, two and one tiles ahead
-      int blA = block_of(load_id(w.i0, kA)), blB = block_of(load_id(w.i0, kB));
-      int nblA = block_of(load_id(w.i0 + 1, kA)), nblB = block_of(load_id(w.i0 + 1, kB));
-      int idA = load_id(w.i0 + 2, kA), idB = load_id(w.i0 + 2, kB);
-      float nskA = scale_of(p.k_scale, blA), nskB = scale_of(p.k_scale, blB);
-      float nsvA = SEP ? scale_of(p.v_scale, blA) : nskA, nsvB = SEP ? scale_of(p.v_scale, blB) : nskB;
+      for (int h = 0; h < 8; ++h) l_part[h] = 0.f, m[h] = 0.f, top[h] = -INFINITY;
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
         const int b = tile_ctr & 1;
         const uint32_t par = (tile_ctr >> 1) & 1;
-        const bool vA = blA >= 0, vB = blB >= 0;
-        const float skA = nskA, skB = nskB, svA = nsvA, svB = nsvB;
-        blA = nblA;
-        blB = nblB;
-        nskA = scale_of(p.k_scale, blA);
-        nskB = scale_of(p.k_scale, blB);
-        nsvA = SEP ? scale_of(p.v_scale, blA) : nskA;
-        nsvB = SEP ? scale_of(p.v_scale, blB) : nskB;
-        nblA = block_of(idA);
-        nblB = block_of(idB);
-        idA = load_id(i + 3, kA);
-        idB = load_id(i + 3, kB);
+        const int stage = tile_ctr % ST;
+        // the slots' scales come with the gathered tile
+        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (tile_ctr / ST) & 1, wt);
+        float skA, skB, svA, svB;
+        if (SEP) {
+          const float2* meta = reinterpret_cast<const float2*>(smem + S::kMeta + stage * S::kMetaStep);
+          const float2 ma = meta[kA], mb = meta[kB];
+          skA = ma.x, svA = ma.y, skB = mb.x, svB = mb.y;
+        } else {
+          const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
+          svA = skA = meta[kA];
+          svB = skB = meta[kB];
+        }
+        const bool vA = skA >= 0.f, vB = skB >= 0.f;
         if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
         dsa::tc_fence_after();
         float x[16];
@@ -643,28 +652,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           for (int r = 0; r < 16; ++r) x[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
         }
         if (i == w.i0) {
-          const float4 a = *reinterpret_cast<const float4*>(qsc + (item_ctr % 3) * 64 + hb),
-                       c = *reinterpret_cast<const float4*>(qsc + (item_ctr % 3) * 64 + hb + 4);
-          qs[0] = a.x, qs[1] = a.y, qs[2] = a.z, qs[3] = a.w;
-          qs[4] = c.x, qs[5] = c.y, qs[6] = c.z, qs[7] = c.w;
+          const uint8_t* e = qexp + (item_ctr % 3) * 64 + hb;
+#pragma unroll
+          for (int h = 0; h < 8; ++h)  // (255: a head with infinity or NaN)
+            qs[h] = __uint_as_float(static_cast<uint32_t>(e[h]) << 23) * (e[h] == 255 ? NAN : p.scale_log2);
           ++item_ctr;
         }
         dsa::tc_fence_before();
         __syncwarp();
         if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
-        // scores in powers of two; -inf where the slot is not valid
-        bool ex = svA > ref || svB > ref;
+        // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int h = 2 * j + e;
-            float& xa = x[4 * j + e];
-            float& xb = x[4 * j + 2 + e];
-            xa = vA ? xa * (qs[h] * skA) : -INFINITY;
-            xb = vB ? xb * (qs[h] * skB) : -INFINITY;
-            ex |= xa - m[h] > kTheta || xb - m[h] > kTheta;
-            if (want_max) top[h] = fmaxf(top[h], fmaxf(xa, xb));
+            x[4 * j + e] = fmaf(x[4 * j + e], qs[h] * skA, -m[h]);
+            x[4 * j + 2 + e] = fmaf(x[4 * j + 2 + e], qs[h] * skB, -m[h]);
+          }
+        }
+        if (!vA) {
+          svA = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * j] = x[4 * j + 1] = -INFINITY;
+        }
+        if (!vB) {
+          svB = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * j + 2] = x[4 * j + 3] = -INFINITY;
+        }
+        float most = x[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) most = fmaxf(most, x[r]);
+        const bool ex = unset || most > kTheta || svA > ref || svB > ref;
+        if (want_max) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              top[2 * j + e] = fmaxf(top[2 * j + e], fmaxf(x[4 * j + e], x[4 * j + 2 + e]) + m[2 * j + e]);
           }
         }
         const bool first = i == w.i0;
@@ -690,8 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
           if (lane == 0 && hh == 0) svm[quarter] = sv;
           named_bar(1, kSoftThreads);
-          const float rn = fmaxf(ref, pow2_ceil(fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]))));
-          inv = 1.f / rn;
+          const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
+          const float rn = fmaxf(ref, pow2_ceil(sv_max));
+          inv = dsa::pow2_inverse(rn);
           ratio = ref * inv;
           ref = rn;
           bool moved = ratio != 1.f;
@@ -707,20 +734,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int h = 4 * g4 + k;
-              const float mn = tm[k] > m[h] + kTheta ? tm[k] : m[h];
-              const float a = ex2(m[h] - mn);
-              moved |= mn != m[h];
+              // by how much the reference moves: to the tile's maximum, if that
+              // passes it by kTheta or is the first
+              const float up = (unset ? tm[k] > -INFINITY : tm[k] > kTheta) ? tm[k] : 0.f;
+              const float a = unset ? 1.f : ex2(-up);
+              moved |= up != 0.f;
               l_part[h] *= a;
-              m[h] = mn;
-              if (lane < 4) alpha[hb - hh * 32 + h] = a * ratio;
+              m[h] += up;
+              x[4 * (h >> 1) + (h & 1)] -= up;
+              x[4 * (h >> 1) + 2 + (h & 1)] -= up;
+              if (lane < 4) alpha[hb + h] = a * ratio;
             }
           }
+          unset = unset && !(sv_max > 0.f);
           need_rescale = __any_sync(0xffffffffu, moved) && !first;
         }
         // P^T rows kA and kB, both terms: the thread's eight heads are bytes hb .. hb + 7 of the 64-byte rows
         if (!failed) failed = !dsa::mbar_wait(&p_empty[b], par ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
         {
-          uint8_t* ph = smem + S::kPHi + (S::kTail ? tile_ctr % ST : b) * S::kPHiStep;
+          uint8_t* ph = smem + S::kPHi + (S::kTail ? stage : b) * S::kPHiStep;
           uint8_t* pl = smem + S::kPLo + b * kPPart;
           const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
 #pragma unroll
@@ -730,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             uint16_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float p0 = ex2(x[4 * j + 2 * k] - m[2 * j]), p1 = ex2(x[4 * j + 2 * k + 1] - m[2 * j + 1]);
+              const float p0 = ex2(x[4 * j + 2 * k]), p1 = ex2(x[4 * j + 2 * k + 1]);
               l_part[2 * j] += p0;
               l_part[2 * j + 1] += p1;
               const __half2 h = __floats2half2_rn(p0 * wk, p1 * wk);
@@ -747,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((tile_ctr - 1) >> 1) & 1, wt);
           dsa::tc_fence_after();
           __syncwarp();  // alpha, written by four lanes of this warp
+          const float* a32 = alpha + hh * 32;
 #pragma unroll 1
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t ta = tmem_base + lane_off + kOCol + mb * kHG + hh * 32;
@@ -754,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             dsa::tmem_ld32(ta, v);
             dsa::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha[c]);
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a32[c]);
             dsa::tmem_st32(ta, v);
           }
           dsa::tmem_wait_st();
@@ -815,23 +848,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         const int hcount = min(32, w.hv - hh * 32);
 #pragma unroll 1
         for (int mb = 0; mb < S::kNv; ++mb) {
+          if (hcount <= 0) break;
           uint32_t v[32];
           dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kHG + hh * 32, v);
           dsa::tmem_wait_ld();
-          const int d = mb * 128 + quarter * 32 + lane;
+          const int d = mb * 128 + quarter * 32;
           if (p.splits > 1) {
-            float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + d;
+            float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + d + lane;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               if (c < hcount) *o = __uint_as_float(v[c]) * f32[c];
               o += static_cast<int64_t>(p.splits) * DV;
             }
           } else {
-            __nv_bfloat16* o = p.out + (orow + hh * 32) * DV + d;
+            // lane = dim and register = head: lanes exchange with their
+            // neighbours until each holds four dims of one head of four
+            __nv_bfloat16* o = p.out + (orow + hh * 32 + (lane & 3)) * DV + d + (lane & ~3);
+            const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c < hcount) __stcs(o, __float2bfloat16_rn(__uint_as_float(v[c]) * f32[c]));
-              o += DV;
+            for (int c = 0; c < 32; c += 4) {
+              if (c < hcount) {
+                uint32_t two[2];  // dims (lane & ~1) + {0, 1} of head c + 2 k + odd
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float a = __uint_as_float(v[c + 2 * k]) * f32[c + 2 * k];
+                  const float e = __uint_as_float(v[c + 2 * k + 1]) * f32[c + 2 * k + 1];
+                  const float got = __shfl_xor_sync(0xffffffffu, odd ? a : e, 1);
+                  const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(got, e) : __floats2bfloat162_rn(a, got);
+                  two[k] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? two[0] : two[1], 2);
+                if (c + (lane & 3) < hcount)
+                  __stcs(reinterpret_cast<uint2*>(o + c * DV), upper ? make_uint2(got, two[1]) : make_uint2(two[0], got));
+              }
             }
           }
         }
@@ -856,6 +905,7 @@ done:
 // z = sum_s 2^(m_s - M) l_s + 2^(sink - M), out = sum_s 2^(m_s - M) O_s / z.
 template <int DV>
 __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
   const int64_t row = blockIdx.x;
   const int t = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<int64_t>(t) * p.H);
   if (p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs)) return;
@@ -951,8 +1001,18 @@ int launch(const Params& p, int T, int sms, cudaStream_t stream) {
   kernel<<<p.n_items < sms ? p.n_items : sms, kThreads, smem, stream>>>(p);
   int rc = dsa::launch_error("attn_kv8_kernel");
   if (rc != DSA_OK || p.splits == 1) return rc;
-  attn_kv8_join_kernel<DV><<<static_cast<unsigned>(T) * p.H, DV / 4, 0, stream>>>(p);
-  return dsa::launch_error("attn_kv8_join_kernel");
+  // launched while the splits' kernel drains, so that its start-up hides behind it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(T) * p.H);
+  cfg.blockDim = dim3(DV / 4);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<DV>, p) != cudaSuccess) return dsa::launch_error("attn_kv8_join_kernel");
+  return DSA_OK;
 }
 
 }  // namespace

@@ -13,28 +13,55 @@
 
 namespace {
 
-constexpr int kWriteThreads = 256;
-constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 32;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowPieces = 4;  // 16-byte pieces in flight per lane of the row writer
 
-// What one CTA of the write kernel works on: a block that receives rows.
+constexpr uint32_t kInfinity = 0x7F80u;  // bf16 bits
+
+// Largest finite magnitude of a piece, as bf16 bits (dsa::amax_bf16x8 takes a
+// third of the instructions: this is for the rare block that holds infinity or NaN).
+__device__ __forceinline__ uint32_t finite_max(uint4 v, uint32_t m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = w[k] & 0x7FFFu, b = (w[k] >> 16) & 0x7FFFu;
+    m = max(m, a < 0x7F80u ? a : 0u);
+    m = max(m, b < 0x7F80u ? b : 0u);
+  }
+  return m;
+}
+
+// Codes of x / s: a product for a power of two s (every scale that the writer makes), else divided.
+template <bool kPow2>
+__device__ __forceinline__ uint2 codes_of(uint4 v, float s) {
+  const bool exact = kPow2 || (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  const float inv = dsa::pow2_inverse(s);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint16_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xFFFF0000u);
+    o[k] = exact ? dsa::e4m3x2(a * inv, b * inv) : dsa::e4m3x2(a / s, b / s);
+  }
+  return make_uint2(o[0] | (static_cast<uint32_t>(o[1]) << 16), o[2] | (static_cast<uint32_t>(o[3]) << 16));
+}
+
+// What one CTA of the block writer works on: a block that receives rows.
 struct WriteItem {
-  int t0;     // packed token of the first new row
-  int rows;   // new rows
-  int first;  // their first row inside the block
-  int block;  // physical block, -1 when there is none
+  int seq, t0;  // sequence, packed token of the first new row
+  int rows;     // new rows
+  int first;    // their first row inside the block
+  int64_t page; // logical block
 };
 
-// The item-th block that receives rows, counted through the sequences.
+// The item-th block that receives rows, counted through the sequences.  Every
+// warp looks for itself, 32 sequences at a time: no barrier before the rows are read.
 __device__ bool find_item(const dsa::Kv8Geom& g, int item, WriteItem* out) {
-  __shared__ int wsum[kWriteThreads / 32];
-  __shared__ int s_found;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int size = 1 << g.lb;
-  if (tid == 0) s_found = 0;
+  const int lane = threadIdx.x & 31;
   int base = 0;
-  for (int b0 = 0; b0 < g.n_seqs; b0 += kWriteThreads) {
-    const int b = b0 + tid;
+  for (int b0 = 0; b0 < g.n_seqs; b0 += 32) {
+    const int b = b0 + lane;
     int c0 = 0, n = 0, count = 0;
     int64_t p0 = 0;
     if (b < g.n_seqs) {
@@ -49,142 +76,264 @@ __device__ bool find_item(const dsa::Kv8Geom& g, int item, WriteItem* out) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int before = base, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWriteThreads / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    inc += before;
-    if (item >= inc - count && item < inc) {
-      const int64_t page = (p0 >> g.lb) + (item - (inc - count));
-      const int64_t lo = max(p0, page << g.lb), hi = min(p0 + n, (page << g.lb) + size);
-      out->t0 = c0 + static_cast<int>(lo - p0);
+    inc += base;
+    const uint32_t hit = __ballot_sync(0xffffffffu, item >= inc - count && item < inc);
+    if (hit) {
+      const int from = __ffs(hit) - 1;
+      const int64_t first_pos = __shfl_sync(0xffffffffu, p0, from);
+      const int64_t page = (first_pos >> g.lb) + (item - __shfl_sync(0xffffffffu, inc - count, from));
+      const int64_t lo = max(first_pos, page << g.lb);
+      const int64_t hi = min(first_pos + __shfl_sync(0xffffffffu, n, from), (page + 1) << g.lb);
+      out->seq = b0 + from;
+      out->t0 = __shfl_sync(0xffffffffu, c0, from) + static_cast<int>(lo - first_pos);
       out->rows = static_cast<int>(hi - lo);
       out->first = static_cast<int>(lo - (page << g.lb));
-      out->block = kv8_block(g, b, page);
-      s_found = 1;
+      out->page = page;
+      return true;
     }
-    base += total;
-    if (base > item) break;
+    base = __shfl_sync(0xffffffffu, inc, 31);
   }
-  __syncthreads();
-  return s_found != 0;
+  return false;
 }
 
-__global__ void __launch_bounds__(kWriteThreads)
+// One CTA per (block that receives rows, head): a warp per row, the rows' pieces
+// read once and kept in registers until the block's scale is known (rows
+// beyond what fits are read again).  NP: pieces of a lane and row, kRows: rows
+// that a warp keeps -- few for small blocks, so that more CTAs are resident.
+template <int NP, int kRows>
+__global__ void __launch_bounds__(kThreads)
     kv8_write_kernel(const __nv_bfloat16* __restrict__ src, const dsa::Kv8Geom g, int Hc, int D,
                      uint8_t* __restrict__ cache, float* __restrict__ scale) {
-  __shared__ WriteItem it;
-  __shared__ uint32_t wmax[kWriteThreads / 32];
-  if (!find_item(g, blockIdx.x, &it) || it.block < 0) return;
-  const int h = blockIdx.y, tid = threadIdx.x;
-  const int p8 = D >> 3;  // 16-byte pieces of a bf16 row
+  __shared__ uint32_t wmax[kWarps];
+  WriteItem it;
+  if (!find_item(g, blockIdx.x, &it)) return;
+  const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int p8 = D >> 3;
   const int64_t ld = static_cast<int64_t>(Hc) * D;
   const __nv_bfloat16* s0 = src + it.t0 * ld + static_cast<int64_t>(h) * D;
-  // largest finite magnitude, as bf16 bits without the sign (monotonic)
+  const int block = dsa::kv8_block(g, it.seq, it.page);
+  auto load = [&](int r, int k) {
+    const int c = k * 32 + lane;
+    return c < p8 ? __ldg(reinterpret_cast<const uint4*>(s0 + r * ld) + c) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 v[kRows][NP];
   uint32_t m = 0;
-  for (int i = tid; i < it.rows * p8; i += kWriteThreads) {
-    const int r = i / p8, c = i - r * p8;
-    const uint4 v = *reinterpret_cast<const uint4*>(s0 + r * ld + c * 8);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t a = w[k] & 0x7FFFu, b = (w[k] >> 16) & 0x7FFFu;
-      m = max(m, a < 0x7F80u ? a : 0u);
-      m = max(m, b < 0x7F80u ? b : 0u);
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + i * kWarps;
+    if (r < it.rows) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) v[i][k] = load(r, k);
     }
   }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((tid & 31) == 0) wmax[tid >> 5] = m;
-  float* sp = scale + static_cast<int64_t>(it.block) * Hc + h;
-  const float s_old = it.first > 0 ? *sp : 0.f;
-  __syncthreads();  // every thread has read the old scale before it is replaced
+  float* sp = scale + static_cast<int64_t>(block < 0 ? 0 : block) * Hc + h;
+  const float s_old = it.first > 0 && block >= 0 ? *sp : 0.f;
 #pragma unroll
-  for (int w = 0; w < kWriteThreads / 32; ++w) m = max(m, wmax[w]);
+  for (int i = 0; i < kRows; ++i) {
+    if (warp + i * kWarps < it.rows) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) m = dsa::amax_bf16x8(v[i][k], m);
+    }
+  }
+  for (int r = warp + kRows * kWarps; r < it.rows; r += kWarps) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) m = dsa::amax_bf16x8(load(r, k), m);
+  }
+  auto block_max = [&](uint32_t x) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if (lane == 0) wmax[warp] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x = max(x, wmax[w]);
+    return x;
+  };
+  m = block_max(dsa::larger_half(m));  // (behind its barrier every thread has read the old scale)
+  if (block < 0) return;
+  if (m >= kInfinity) {
+    m = 0;
+    for (int r = warp; r < it.rows; r += kWarps) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) m = finite_max(load(r, k), m);
+    }
+    __syncthreads();
+    m = block_max(m);
+  }
   const float s = fmaxf(s_old, dsa::kv8_scale_of(__uint_as_float(m << 16)));
-  if (tid == 0) *sp = s;
-  uint8_t* c0 = cache + (static_cast<int64_t>(it.block) << g.lb) * ld + static_cast<int64_t>(h) * D;
-  const int p16 = D >> 4;
+  if (threadIdx.x == 0) *sp = s;
+  uint8_t* c0 = cache + (static_cast<int64_t>(block) << g.lb) * ld + static_cast<int64_t>(h) * D;
   if (it.first > 0 && s > s_old) {
     const float ratio = s_old / s;
-    for (int i = tid; i < it.first * p16; i += kWriteThreads) {
-      const int r = i / p16, c = i - r * p16;
-      uint4* p = reinterpret_cast<uint4*>(c0 + r * ld + c * 16);
-      uint4 v = *p;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    for (int r = warp; r < it.first; r += kWarps) {
+      for (int c = lane; c < D >> 4; c += 32) {
+        uint4* p = reinterpret_cast<uint4*>(c0 + r * ld) + c;
+        uint4 u = *p;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 a = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k])),
-                     b = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
-        w[k] = dsa::e4m3x2(a.x * ratio, a.y * ratio) | (static_cast<uint32_t>(dsa::e4m3x2(b.x * ratio, b.y * ratio)) << 16);
+        for (int k = 0; k < 4; ++k) {
+          const float2 a = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k])),
+                       b = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+          w[k] = dsa::e4m3x2(a.x * ratio, a.y * ratio) | (static_cast<uint32_t>(dsa::e4m3x2(b.x * ratio, b.y * ratio)) << 16);
+        }
+        *p = u;
       }
-      *p = v;
     }
   }
-  for (int i = tid; i < it.rows * p8; i += kWriteThreads) {
-    const int r = i / p8, c = i - r * p8;
-    const uint4 v = *reinterpret_cast<const uint4*>(s0 + r * ld + c * 8);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint16_t o[4];
+  uint8_t* o0 = c0 + it.first * ld;
+  auto store = [&](int r, int k, uint4 u) {
+    const int c = k * 32 + lane;
+    if (c < p8) *(reinterpret_cast<uint2*>(o0 + r * ld) + c) = codes_of<false>(u, s);
+  };
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o[k] = dsa::e4m3x2(__uint_as_float(w[k] << 16) / s, __uint_as_float(w[k] & 0xFFFF0000u) / s);
-    uint2 q;
-    q.x = o[0] | (static_cast<uint32_t>(o[1]) << 16);
-    q.y = o[2] | (static_cast<uint32_t>(o[3]) << 16);
-    *reinterpret_cast<uint2*>(c0 + (it.first + r) * ld + c * 8) = q;
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + i * kWarps;
+    if (r < it.rows) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) store(r, k, v[i][k]);
+    }
+  }
+  for (int r = warp + kRows * kWarps; r < it.rows; r += kWarps) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) store(r, k, load(r, k));
   }
 }
 
-// One CTA per kReadTokens packed tokens: their rows and sequences are looked
-// up once, then the threads stream the rows' 16-byte pieces.
-__global__ void __launch_bounds__(kReadThreads)
-    kv8_read_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ scale, const dsa::Kv8Geom g, int Hc,
-                    int D, __nv_bfloat16* __restrict__ out) {
-  __shared__ int rows[kReadTokens];  // cache row, -1 unmapped, -2 behind the last sequence
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kReadTokens;
-  if (threadIdx.x < kReadTokens) {
-    const int64_t t = t0 + threadIdx.x;
-    int row = -2;
-    if (t < g.T && t >= __ldg(g.cu) && t < __ldg(g.cu + g.n_seqs)) {
-      const int b = dsa::kv8_seq(g.cu, g.n_seqs, static_cast<int>(t));
-      const int c = __ldg(g.cu + b);
-      row = dsa::kv8_row(g, b, kv8_pos0(g, b, c) + (t - c));
-    }
-    rows[threadIdx.x] = row;
-  }
+// Cache row of packed token t; -1 not mapped, -2 behind the last sequence.
+__device__ __forceinline__ int row_of_token(const dsa::Kv8Geom& g, int64_t t) {
+  if (t >= g.T || t < __ldg(g.cu) || t >= __ldg(g.cu + g.n_seqs)) return -2;
+  const int b = dsa::kv8_seq(g.cu, g.n_seqs, static_cast<int>(t));
+  const int c = __ldg(g.cu + b);
+  return dsa::kv8_row(g, b, kv8_pos0(g, b, c) + (t - c));
+}
+
+// n / d for n * d < 2^32, magic = magic_of(d): n * (2^32 / d + 1) exceeds n / d *
+// 2^32 by at most n, less than the 2^32 / d that would reach the next quotient.
+// 0 stands for d = 1, and 1 gives 0 for every n.
+__device__ __forceinline__ int fast_div(int n, uint32_t magic) {
+  return magic ? static_cast<int>(__umulhi(n, magic)) : n;
+}
+uint32_t magic_of(int d) { return d == 1 ? 0 : static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(d)) + 1; }
+
+// block = 1: a (token, head) row has its own scale.  G lanes per row, NP pieces
+// each, kRowPieces / NP rows at a time; `tokens` tokens per CTA, whose cache
+// rows are looked up first.
+constexpr int kMaxTokens = 64;
+
+template <int G, int NP>
+__global__ void __launch_bounds__(kThreads)
+    kv8_write_rows_kernel(const __nv_bfloat16* __restrict__ src, const dsa::Kv8Geom g, int Hc, int D, int tokens,
+                          uint32_t magic_hc, uint8_t* __restrict__ cache, float* __restrict__ scale) {
+  constexpr int kRows = kRowPieces / NP, kGroups = kThreads / G;
+  __shared__ int rows[kMaxTokens];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  if (threadIdx.x < tokens) rows[threadIdx.x] = row_of_token(g, t0 + threadIdx.x);
   __syncthreads();
-  const int p16 = D >> 4, per = Hc * p16;
-  const int64_t ld = static_cast<int64_t>(Hc) * D;
-  for (int i = threadIdx.x; i < kReadTokens * per; i += kReadThreads) {
-    const int k = i / per, c = i - k * per;
-    const int row = rows[k];
-    if (row == -2) continue;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (row >= 0) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(cache + row * ld) + c);
-      const float s = __ldg(scale + static_cast<int64_t>(row >> g.lb) * Hc + c / p16);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[8];
+  const int sub = threadIdx.x % G, p8 = D >> 3;
+  const int n = min(static_cast<int64_t>(tokens), g.T - t0) * Hc;
+  const __nv_bfloat16* s0 = src + t0 * Hc * D;
+  // every lane takes part in the reductions: all groups make the same trips
+  const int first = threadIdx.x / G;
+  for (int i0 = 0; i0 < n; i0 += kGroups * kRows) {
+    uint4 v[kRows][NP];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[j])),
-                     y = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[j] >> 16));
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x.x * s, x.y * s), u = __floats2bfloat162_rn(y.x * s, y.y * s);
-        o[2 * j] = *reinterpret_cast<const uint32_t*>(&l);
-        o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&u);
+    for (int r = 0; r < kRows; ++r) {
+      const int i = i0 + first + r * kGroups;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = k * G + sub;
+        v[r][k] = i < n && c < p8 ? __ldcs(reinterpret_cast<const uint4*>(s0 + static_cast<int64_t>(i) * D) + c)
+                                  : make_uint4(0, 0, 0, 0);
       }
-      a = make_uint4(o[0], o[1], o[2], o[3]);
-      b = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    uint4* p = reinterpret_cast<uint4*>(out + (t0 + k) * ld) + 2 * c;
-    p[0] = a;
-    p[1] = b;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int i = i0 + first + r * kGroups;
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) m = dsa::amax_bf16x8(v[r][k], m);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = dsa::larger_half(m);
+      if (__any_sync(0xffffffffu, m >= kInfinity)) {
+        m = 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) m = finite_max(v[r][k], m);
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
+      if (i >= n) continue;
+      const int t = fast_div(i, magic_hc);
+      const int row = rows[t];
+      if (row < 0) continue;
+      const float s = dsa::kv8_scale_of(__uint_as_float(m << 16));
+      const int64_t rh = static_cast<int64_t>(row) * Hc + (i - t * Hc);
+      if (sub == 0) scale[rh] = s;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = k * G + sub;
+        if (c < p8) *(reinterpret_cast<uint2*>(cache + rh * D) + c) = codes_of<true>(v[r][k], s);
+      }
+    }
   }
+}
+
+// `tokens` packed tokens per CTA: their cache rows are looked up once, then the
+// threads stream the rows' pieces of 8 codes (a warp's store covers 512
+// consecutive bytes), kReadPieces of them in flight each.
+constexpr int kReadPieces = 8;
+
+__global__ void __launch_bounds__(kThreads)
+    kv8_read_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ scale, const dsa::Kv8Geom g, int Hc,
+                    int D, int tokens, uint32_t magic_row, uint32_t magic_head, __nv_bfloat16* __restrict__ out) {
+  __shared__ int rows[kMaxTokens];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  if (threadIdx.x < tokens) rows[threadIdx.x] = row_of_token(g, t0 + threadIdx.x);
+  __syncthreads();
+  const int p8 = D >> 3, per = Hc * p8;
+  const int64_t ld = static_cast<int64_t>(Hc) * D;
+  const int n = min(static_cast<int64_t>(tokens), g.T - t0) * per;
+  uint4* o0 = reinterpret_cast<uint4*>(out + t0 * ld);
+  for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kReadPieces) {
+    uint2 v[kReadPieces];
+    float s[kReadPieces];
+    uint32_t live = 0;  // pieces that are written
+#pragma unroll
+    for (int j = 0; j < kReadPieces; ++j) {
+      const int i = i0 + j * kThreads;
+      v[j] = make_uint2(0, 0);
+      s[j] = 0.f;
+      if (i < n) {
+        const int k = fast_div(i, magic_row), c = i - k * per;
+        const int row = rows[k];
+        if (row != -2) live |= 1u << j;
+        if (row >= 0) {
+          v[j] = __ldcs(reinterpret_cast<const uint2*>(cache + row * ld) + c);
+          s[j] = __ldg(scale + static_cast<int64_t>(row >> g.lb) * Hc + fast_div(c, magic_head));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kReadPieces; ++j) {
+      const uint32_t w[2] = {v[j].x, v[j].y};
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 x = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k])),
+                     y = dsa::f2_of_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x.x * s[j], x.y * s[j]), u = __floats2bfloat162_rn(y.x * s[j], y.y * s[j]);
+        o[2 * k] = *reinterpret_cast<const uint32_t*>(&l);
+        o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&u);
+      }
+      if (live >> j & 1) o0[i0 + j * kThreads] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// Tokens per CTA: enough for 16 KB of codes, fewer where the batch would not
+// fill the device twice, and few enough for 16-bit piece numbers.
+int tokens_per_cta(int T, int Hc, int D, int sms) {
+  int n = std::max(1, std::min(kMaxTokens, 16384 / (Hc * D)));
+  n = std::max(1, std::min(n, T / (2 * sms)));
+  return n;
 }
 
 // Checks of the two calls; fills the geometry.
@@ -221,13 +370,34 @@ extern "C" int dsa_kv8_write(const void* src, const int32_t* cu_seqlens, const i
   int rc = check_args("dsa_kv8_write", src, cache, scale, cu_seqlens, pos, block_table, n_seqs, T, Hc, D, block,
                       n_blocks, max_blocks, &g);
   if (rc != DSA_OK) return rc;
-  rc = dsa::check_device(nullptr);
+  int sms = 0;
+  rc = dsa::check_device(&sms);
   if (rc != DSA_OK) return rc;
   if (T == 0) return DSA_OK;
+  const auto* x = static_cast<const __nv_bfloat16*>(src);
+  auto* c = static_cast<uint8_t*>(cache);
+  if (block == 1) {
+    const int tokens = tokens_per_cta(T, Hc, D, sms);
+    const unsigned grid = static_cast<unsigned>((T + tokens - 1) / tokens);
+    const uint32_t magic = magic_of(Hc);
+    if (D <= 128)
+      kv8_write_rows_kernel<16, 1><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
+    else if (D <= 256)
+      kv8_write_rows_kernel<32, 1><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
+    else if (D <= 512)
+      kv8_write_rows_kernel<32, 2><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
+    else
+      kv8_write_rows_kernel<32, 4><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
+    return dsa::launch_error("kv8_write_rows_kernel");
+  }
   // a sequence of n rows touches at most n / block + 2 blocks, and at most n
-  const int64_t items = std::min<int64_t>(T, T / block + 2ll * n_seqs);
-  kv8_write_kernel<<<dim3(static_cast<unsigned>(items), Hc), kWriteThreads, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(src), g, Hc, D, static_cast<uint8_t*>(cache), scale);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(T, T / block + 2ll * n_seqs)), Hc);
+  const int np = (D + 255) / 256;
+  auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(x, g, Hc, D, c, scale); };
+  if (block <= 16)
+    launch(np == 1 ? kv8_write_kernel<1, 2> : np == 2 ? kv8_write_kernel<2, 2> : np == 3 ? kv8_write_kernel<3, 2> : kv8_write_kernel<4, 2>);
+  else
+    launch(np == 1 ? kv8_write_kernel<1, 8> : np == 2 ? kv8_write_kernel<2, 8> : np == 3 ? kv8_write_kernel<3, 8> : kv8_write_kernel<4, 6>);
   return dsa::launch_error("kv8_write_kernel");
 }
 
@@ -239,10 +409,13 @@ extern "C" int dsa_kv8_read(const void* cache, const float* scale, const int32_t
   int rc = check_args("dsa_kv8_read", out, cache, scale, cu_seqlens, pos, block_table, n_seqs, T, Hc, D, block,
                       n_blocks, max_blocks, &g);
   if (rc != DSA_OK) return rc;
-  rc = dsa::check_device(nullptr);
+  int sms = 0;
+  rc = dsa::check_device(&sms);
   if (rc != DSA_OK) return rc;
   if (T == 0) return DSA_OK;
-  kv8_read_kernel<<<(T + kReadTokens - 1) / kReadTokens, kReadThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(cache), scale, g, Hc, D, static_cast<__nv_bfloat16*>(out));
+  const int tokens = tokens_per_cta(T, Hc, D, sms);
+  kv8_read_kernel<<<static_cast<unsigned>((T + tokens - 1) / tokens), kThreads, 0, stream>>>(
+      static_cast<const uint8_t*>(cache), scale, g, Hc, D, tokens, tokens == 1 ? 1 : magic_of(Hc * (D / 8)), magic_of(D / 8),
+      static_cast<__nv_bfloat16*>(out));
   return dsa::launch_error("kv8_read_kernel");
 }

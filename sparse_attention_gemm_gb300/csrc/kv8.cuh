@@ -64,6 +64,25 @@ __device__ __forceinline__ float kv8_scale_of(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// 1 / s of a power of two s in [2^-126, 2^126], exactly.
+__device__ __forceinline__ float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// Larger of two pairs of 16-bit unsigned numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Largest magnitudes of the eight bf16 values of a piece, kept in two lanes as
+// bits without the sign (monotonic; 0x7F80 and above: infinity or NaN).
+__device__ __forceinline__ uint32_t amax_bf16x8(uint4 v, uint32_t m) {
+  m = max_u16x2(m, v.x & 0x7FFF7FFFu);
+  m = max_u16x2(m, v.y & 0x7FFF7FFFu);
+  m = max_u16x2(m, v.z & 0x7FFF7FFFu);
+  return max_u16x2(m, v.w & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ uint32_t larger_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
 // Two values -> two E4M3 codes (x0 in the low byte), to nearest even, beyond
 // +-448 the largest code of that sign, NaN stays NaN.
 __device__ __forceinline__ uint16_t e4m3x2(float x0, float x1) {
