@@ -13,8 +13,8 @@
 //            largest element to (224, 448].  A bf16 significand has 8 bits, two
 //            E4M3 terms hold 4 each: exact down to 2^-14 of the scaled units.
 //   weights: w = C * exp(s_j - m) * v_scale / 2^E as hi + lo: relative error
-//            2^-8, what rounding to bf16 costs, and at least 2^-10 / C of the
-//            largest weight (the smaller term's smallest step).
+//            2^-8, what rounding to bf16 costs, and never less than 2^-10 / C
+//            (half the smaller term's smallest step).
 // Against the bf16 kernel a tile of 64 keys costs half the gather and 34
 // instructions instead of 52; hi and lo of the query are the two halves of
 // one N = 128 operand, hi and lo of the weights two instructions into the same sums.
@@ -52,18 +52,20 @@ constexpr int kMma2Warp = kMmaWarp + 1;
 constexpr int kThreads = (kMmaWarp + 4) * 32;  // five warpgroups
 // Registers: launched at kLaunchRegs per thread, moved from the lean
 // warpgroups to the softmax ones.
-constexpr int kLaunchRegs = 96, kLeanRegs = 56, kSoftRegs = 152;
+constexpr int kLaunchRegs = 96, kLeanRegs = 64, kSoftRegs = 144;
 static_assert(3 * 128 * kLeanRegs + 2 * 128 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Weights reach 2^kTheta before the reference moves; kWeight = 2^(8 - kTheta)
-// puts that at 256, below E4M3's 448, and leaves 2^-10 / kWeight = 2^-14 as the
-// smallest step of a weight.
-constexpr float kTheta = 4.0f;
-constexpr float kWeight = 16.0f;
+// Weights reach 2^kTheta before the reference moves; kWeight puts that at
+// E4M3's largest, 448, and leaves an error of 2^-10 / kWeight < 2^-13.8 of a
+// weight of 1 where the smaller term's step ends.  (kTheta = 4, kWeight = 16:
+// the reference of some head moved in a third of the tiles of the drawn
+// prompts, at 2K cycles a time.)
+constexpr float kTheta = 5.0f;
+constexpr float kWeight = 14.0f;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 0;    // S^T buffers at columns 0 and 128 (hi 64, lo 64)
 constexpr int kOCol = 256;  // O^T blocks at 256 + 64 m
@@ -311,18 +313,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
     // which gives each softmax thread eight consecutive heads
     const int hr = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
+    // (odd heads take the halves of a 128-byte row in the other order: eight
+    // lanes then touch all banks once)
     auto q_unit = [&](int u, int lo) {
       const int r = hr + lo * kHG;
       return u < S::kFull * 8 ? (u >> 3) * kQChunkBytes + dsa::sw128_offset(r, (u & 7) * 16)
                               : S::kQTail + sw64_offset(r, u - S::kFull * 8);
     };
+    auto unit_of = [&](int k) { return (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0); };
     auto send_query = [&](const Item& w) {
       const bool real = hq < w.hv;
       const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK;
       const uint32_t qa = dsa::smem_u32(smem);
 #pragma unroll
       for (int k = 0; k < DQK / 64; ++k) {
-        const int u = sub + 4 * k;
+        const int u = unit_of(k);
         cp_async16(qa + q_unit(u, 0), src + u * 16, real ? 16u : 0u, once);
         cp_async16(qa + q_unit(u, 1), src + u * 16 + 8, real ? 16u : 0u, once);
       }
@@ -332,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       uint32_t m = 0;
 #pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, 0)), m);
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(sub + 4 * k, 1)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(unit_of(k), 0)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(unit_of(k), 1)), m);
       }
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
@@ -346,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
         if (hq >= w.hv) break;
-        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 0)),
-                        reinterpret_cast<uint4*>(smem + q_unit(sub + 4 * k, 1))};
+        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(unit_of(k), 0)),
+                        reinterpret_cast<uint4*>(smem + q_unit(unit_of(k), 1))};
         const uint4 v0 = *at[0], v1 = *at[1];
         const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         uint32_t hi[4], lo[4];
@@ -393,20 +398,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       // the query first where its buffer is free already (a CTA's first item)
       const bool q_sent = __all_sync(0xffffffffu, dsa::mbar_test_wait(q_empty, (item_ctr & 1) ^ 1));
       if (q_sent) send_query(w);
-      int row[kGatherSteps], nid[kGatherSteps];
+      const int32_t* trow = p.g.table ? p.g.table + static_cast<int64_t>(b) * p.g.max_blocks : nullptr;
+      auto load_block = [&](int id) {  // as the table holds it; -1 beyond the table
+        const int page = id >> p.g.lb;
+        return !trow || id < 0 ? page : page < p.g.max_blocks ? __ldg(trow + page) : -1;
+      };
+      // id of this tile's and the next tile's keys, table entry of this tile's:
+      // loaded one tile before they are looked at
+      int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
 #pragma unroll
       for (int kg = 0; kg < kGatherSteps; ++kg) {
         nid[kg] = load_id(w.i0 + 1, kg);
-        const int id = load_id(w.i0, kg);
-        row[kg] = id >= 0 ? dsa::kv8_row(p.g, b, id) : -1;
+        id[kg] = load_id(w.i0, kg);
+        blk[kg] = load_block(id[kg]);
       }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
         const int stage = tile_ctr % ST;
         int cur[kGatherSteps];
 #pragma unroll
         for (int kg = 0; kg < kGatherSteps; ++kg) {
-          cur[kg] = row[kg];
-          row[kg] = nid[kg] >= 0 ? dsa::kv8_row(p.g, b, nid[kg]) : -1;
+          cur[kg] = id[kg] >= 0 && blk[kg] >= 0 && blk[kg] < p.g.n_blocks
+                        ? (blk[kg] << p.g.lb) + (id[kg] & ((1 << p.g.lb) - 1))
+                        : -1;
+          id[kg] = nid[kg];
+          blk[kg] = load_block(nid[kg]);
           nid[kg] = load_id(i + 2, kg);
         }
         const uint32_t ph = ((tile_ctr / ST) & 1) ^ 1;
@@ -640,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         const bool vA = skA >= 0.f, vB = skB >= 0.f;
         if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
+        __syncwarp();
         dsa::tc_fence_after();
         float x[16];
         {
@@ -777,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (need_rescale) {
           // MMA2 of the previous tile must have landed before O^T is scaled
           if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((tile_ctr - 1) >> 1) & 1, wt);
+          __syncwarp();
           dsa::tc_fence_after();
           __syncwarp();  // alpha, written by four lanes of this warp
           const float* a32 = alpha + hh * 32;
@@ -803,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       // O^T is complete with the last tile's MMA2 (each phase of p_empty has
       // been waited for in turn, so the parity names that tile)
       if (!failed) failed = !dsa::mbar_wait(&p_empty[(tile_ctr - 1) & 1], ((tile_ctr - 1) >> 1) & 1, wt);
+      __syncwarp();
       dsa::tc_fence_after();
       if (quarter == 0 && lane < 4) {
 #pragma unroll
@@ -861,26 +879,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
               o += static_cast<int64_t>(p.splits) * DV;
             }
           } else {
-            // lane = dim and register = head: lanes exchange with their
-            // neighbours until each holds four dims of one head of four
-            __nv_bfloat16* o = p.out + (orow + hh * 32 + (lane & 3)) * DV + d + (lane & ~3);
-            const bool odd = lane & 1, upper = lane & 2;
+            // (two bytes a lane: exchanging values between lanes for wider
+            // stores made the kernel 2.5% slower, the shuffles cost more)
+            __nv_bfloat16* o = p.out + (orow + hh * 32) * DV + d + lane;
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              if (c < hcount) {
-                uint32_t two[2];  // dims (lane & ~1) + {0, 1} of head c + 2 k + odd
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float a = __uint_as_float(v[c + 2 * k]) * f32[c + 2 * k];
-                  const float e = __uint_as_float(v[c + 2 * k + 1]) * f32[c + 2 * k + 1];
-                  const float got = __shfl_xor_sync(0xffffffffu, odd ? a : e, 1);
-                  const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(got, e) : __floats2bfloat162_rn(a, got);
-                  two[k] = *reinterpret_cast<const uint32_t*>(&r);
-                }
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? two[0] : two[1], 2);
-                if (c + (lane & 3) < hcount)
-                  __stcs(reinterpret_cast<uint2*>(o + c * DV), upper ? make_uint2(got, two[1]) : make_uint2(two[0], got));
-              }
+            for (int c = 0; c < 32; ++c) {
+              if (c < hcount) __stcs(o, __float2bfloat16_rn(__uint_as_float(v[c]) * f32[c]));
+              o += DV;
             }
           }
         }

@@ -105,8 +105,8 @@ def attention(q, kv8, kv_scale, idx, sm, length=None, sink=None, v8=None, v_scal
     2^-24 of the sum of their magnitudes, a query kept to 2^-21 of its largest
     element, and a few fp32 roundings (2^-21 relative): d_j.  Weights: exp is a
     few ulp (2^-20), and a weight enters the value product as two E4M3 terms of
-    a half: relative 2^-8 + 2^-11, and at least 2^-14 of the largest weight times
-    the largest scale (what the smaller term resolves).  out is rounded to bf16 (2^-8)."""
+    a half: relative 2^-8 + 2^-11, and at least 2^-10 / 14 of the largest weight times
+    the largest scale (half the smaller term's step, weights being held as 14 times themselves).  out is rounded to bf16 (2^-8)."""
     T, H, dqk = q.shape
     n_blocks, block, heads, _ = kv8.shape
     group, K = H // heads, idx.shape[1]
@@ -151,6 +151,6 @@ def attention(q, kv8, kv_scale, idx, sm, length=None, sink=None, v8=None, v_scal
             out[t, hs], lse_kv[t, hs], lse[t, hs], mx[t, hs] = o, m + np.log(z), m + np.log(zs), m
             ltol[t, hs] = dm + 2.0 ** -21 * (np.abs(m) + 16)
             top = 2.0 ** np.ceil(np.log2(sv.max()))
-            floor = 2.0 ** -14 * top * np.abs(vc).sum(0)[None, :] / zs[:, None]
+            floor = 2.0 ** -10 / 14 * top * np.abs(vc).sum(0)[None, :] / zs[:, None]
             tol[t, hs] = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -11 + 2 * dm[:, None]) * (p @ np.abs(v)) + floor
     return {"out": out, "lse": lse, "lse_kv": lse_kv, "max_logits": mx, "out_tol": tol, "lse_tol": ltol, "done": done}
