@@ -30,7 +30,7 @@
 // scales that moves when a block's scale passes 2^E; both move the running sums.
 //
 // Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
-// MMA1, 17 MMA2, 18..19 idle (they fill the fifth warpgroup).
+// MMA1, 17 MMA2.
 #include <atomic>
 #include <climits>
 
@@ -49,11 +49,11 @@ constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
 constexpr int kMma2Warp = kMmaWarp + 1;
-constexpr int kThreads = (kMmaWarp + 4) * 32;  // five warpgroups
-// Registers: launched at kLaunchRegs per thread, moved from the lean
-// warpgroups to the softmax ones.
-constexpr int kLaunchRegs = 96, kLeanRegs = 64, kSoftRegs = 144;
-static_assert(3 * 128 * kLeanRegs + 2 * 128 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
+constexpr int kThreads = (kMma2Warp + 1) * 32;
+// 18 warps: 96 registers a thread.  Moving registers from the gather and MMA
+// warps to the softmax ones (setmaxnreg) is not done here: builds whose gather
+// branch came near its limit stopped with an illegal instruction, always at
+// the same place of the same build.
 constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
@@ -139,8 +139,17 @@ __device__ __forceinline__ bool elect_sync() {
   return is != 0;
 }
 
-__device__ __forceinline__ void named_bar(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+// The softmax warps' barrier, plain and with an OR over the group.  The
+// instructions want converged warps (.aligned), and lanes part at waits and
+// at `if (lane == 0)` or `if (!valid)` before them: each warp is brought
+// together first.  The same goes for tcgen05.ld / st: __syncwarp before each.
+__device__ __forceinline__ void group_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ bool group_any(bool x) {
+  __syncwarp();
+  return dsa::named_bar_any(1, kSoftThreads, x);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
@@ -218,8 +227,9 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
   if (w.dead) len = 0;
   const int nt = (len + kKeys - 1) / kKeys;
   w.len = len;
-  w.i0 = static_cast<int>(static_cast<int64_t>(nt) * w.split / p.splits);
-  w.i1 = static_cast<int>(static_cast<int64_t>(nt) * (w.split + 1) / p.splits);
+  // (nt <= 2^25 and at most 32 splits: the products fit)
+  w.i0 = static_cast<int>(static_cast<uint32_t>(nt) * static_cast<uint32_t>(w.split) / static_cast<uint32_t>(p.splits));
+  w.i1 = static_cast<int>(static_cast<uint32_t>(nt) * static_cast<uint32_t>(w.split + 1) / static_cast<uint32_t>(p.splits));
   return w;
 }
 
@@ -278,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   const int t_end = p.g.table ? __ldg(p.g.cu + p.g.n_seqs) : INT_MAX;
 
   if (warp < kGatherWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
     // ------------------------------------------------------------ gather
     // Thread gt covers piece (gt & 7) (16 codes) of keys (gt >> 3) + 32 kg of
     // every chunk.  A row's place depends on its id and the block table: ids
@@ -306,30 +315,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       __syncwarp();
       if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
     };
-    // The query: four threads per head, each with 16-byte units sub, sub + 4, ...
-    // of its two operand rows.  A unit pair (hi, lo) is as large as the 16 bf16
-    // values it is made of: they land there and are converted in place.
+    // The query.  A warp loads and converts eight heads: a unit pair (hi, lo) of
+    // the operand's rows is as large as the 16 bf16 values it is made of, so
+    // they land there (a warp instruction copies 512 consecutive bytes) and
+    // are converted in place, four threads per head, units sub, sub + 4, ...
+    // Odd heads take the halves of a 128-byte row in the other order: eight
+    // lanes then touch all banks once.
     const int hq = gt >> 2, sub = gt & 3;
     // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
     // which gives each softmax thread eight consecutive heads
-    const int hr = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
-    // (odd heads take the halves of a 128-byte row in the other order: eight
-    // lanes then touch all banks once)
-    auto q_unit = [&](int u, int lo) {
-      const int r = hr + lo * kHG;
+    auto row_of = [](int h) { return (h & 32) + ((h & 6) << 2) + ((h >> 2) & 6) + (h & 1); };
+    auto q_addr = [](int r, int u) {
       return u < S::kFull * 8 ? (u >> 3) * kQChunkBytes + dsa::sw128_offset(r, (u & 7) * 16)
                               : S::kQTail + sw64_offset(r, u - S::kFull * 8);
     };
-    auto unit_of = [&](int k) { return (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0); };
+    auto q_unit = [&](int k, int lo) {
+      return q_addr(row_of(hq) + lo * kHG, (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0));
+    };
     auto send_query = [&](const Item& w) {
-      const bool real = hq < w.hv;
-      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK;
+      constexpr int kPieces = DQK / 8;  // of 16 bytes, per head
+      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
       const uint32_t qa = dsa::smem_u32(smem);
-#pragma unroll
-      for (int k = 0; k < DQK / 64; ++k) {
-        const int u = unit_of(k);
-        cp_async16(qa + q_unit(u, 0), src + u * 16, real ? 16u : 0u, once);
-        cp_async16(qa + q_unit(u, 1), src + u * 16 + 8, real ? 16u : 0u, once);
+#pragma unroll 6
+      for (int k = 0; k < 8 * kPieces / 32; ++k) {
+        const int x = k * 32 + lane, h = warp * 8 + x / kPieces, c = x % kPieces;
+        const bool real = h < w.hv;
+        cp_async16(qa + q_addr(row_of(h) + (c & 1) * kHG, c >> 1), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u, once);
       }
       cp_async_commit();
     };
@@ -337,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       uint32_t m = 0;
 #pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(unit_of(k), 0)), m);
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(unit_of(k), 1)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(k, 0)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(k, 1)), m);
       }
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
@@ -351,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll 3
       for (int k = 0; k < DQK / 64; ++k) {
         if (hq >= w.hv) break;
-        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(unit_of(k), 0)),
-                        reinterpret_cast<uint4*>(smem + q_unit(unit_of(k), 1))};
+        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(k, 0)),
+                        reinterpret_cast<uint4*>(smem + q_unit(k, 1))};
         const uint4 v0 = *at[0], v1 = *at[1];
         const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         uint32_t hi[4], lo[4];
@@ -488,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             send_query(w);
           }
           cp_async_wait<0>();
+          __syncwarp();
           if (pend >= 0) signal(pend);
           pend = -1;
           convert_query(w, item_ctr);
@@ -499,8 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     cp_async_wait<0>();  // nothing of this thread is in flight when it leaves
     if (pend >= 0) signal(pend);
   } else if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
-    if (warp != kMmaWarp && warp != kMma2Warp) goto done;
     // ------------------------------------------------------------ MMA issue
     // Two warps, one per product, each converged with one elected issuer.
     const bool leader = elect_sync();
@@ -522,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           const int b = tile_ctr & 1, stage = tile_ctr % ST;
           const bool got = dsa::mbar_wait(&s_empty[b], ((tile_ctr >> 1) & 1) ^ 1, wt) &&
                            dsa::mbar_wait(&kv_full[stage], (tile_ctr / ST) & 1, wt);
+          __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
           const uint32_t d = tmem_base + kSCol + b * 128;
@@ -562,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
           const int b = tile_ctr & 1, stage = tile_ctr % ST;
           const bool got = dsa::mbar_wait(&p_full[b], (tile_ctr >> 1) & 1, wt);
+          __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = v_desc + stage * (S::kBuf >> 4);
           const uint64_t bh = ph_desc + (S::kTail ? stage : b) * (S::kPHiStep >> 4), bl = pl_desc + b * (kPPart >> 4);
@@ -589,7 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------------------ softmax + epilogue
     const int sw = warp - kSoftWarp0;
     const int st = threadIdx.x - kSoftWarp0 * 32;
@@ -712,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         const bool first = i == w.i0;
         bool need_rescale = false;
         float ratio = 1.f;  // of the old to the new 2^E
-        if (dsa::named_bar_any(1, kSoftThreads, ex || failed)) {
-          if (dsa::named_bar_any(1, kSoftThreads, failed)) {  // the group leaves together
+        if (group_any(ex || failed)) {
+          if (group_any(failed)) {  // the group leaves together
             ok = false;
             break;
           }
@@ -731,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
           if (lane == 0 && hh == 0) svm[quarter] = sv;
-          named_bar(1, kSoftThreads);
+          group_sync();
           const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
           const float rn = fmaxf(ref, pow2_ceil(sv_max));
           inv = dsa::pow2_inverse(rn);
@@ -801,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t ta = tmem_base + lane_off + kOCol + mb * kHG + hh * 32;
             uint32_t v[32];
+            __syncwarp();
             dsa::tmem_ld32(ta, v);
             dsa::tmem_wait_ld();
 #pragma unroll
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       red[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
       if (want_max)
         redm[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
-      named_bar(1, kSoftThreads);
+      group_sync();
       const float unscale = ref * (1.f / kWeight);
       if (st < 64) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         fac[st] = f;
       }
-      named_bar(1, kSoftThreads);
+      group_sync();
       {
         const float* f32 = fac + hh * 32;
         const int hcount = min(32, w.hv - hh * 32);
@@ -868,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         for (int mb = 0; mb < S::kNv; ++mb) {
           if (hcount <= 0) break;
           uint32_t v[32];
+          __syncwarp();
           dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kHG + hh * 32, v);
           dsa::tmem_wait_ld();
           const int d = mb * 128 + quarter * 32;
@@ -891,14 +904,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
       }
       dsa::tc_fence_before();
-      if (dsa::named_bar_any(1, kSoftThreads, failed)) {  // the item's last barrier: the group leaves together
+      if (group_any(failed)) {  // the item's last barrier: the group leaves together
         ok = false;
         break;
       }
     }
   }
 
-done:
+  __syncwarp();
   __syncthreads();
   if (warp == kMmaWarp) {
     dsa::tc_fence_after();
@@ -989,16 +1002,10 @@ int launch(const Params& p, int T, int sms, cudaStream_t stream) {
   using S = Shape<DQK, DV, SEP>;
   constexpr int smem = S::kTotal;
   auto kernel = attn_kv8_kernel<DQK, DV, SEP>;
-  // once per device: the register split assumes the launch count it was sized
-  // for, and the kernel needs its shared memory allowed
-  static std::atomic<uint64_t> ready{0};
+  static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
   int dev = 0;
   cudaGetDevice(&dev);  // below 64: check_device
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs)
-      return dsa::set_error(DSA_ERR_CUDA, "attn_kv8_kernel: compiled with %d registers per thread, expected %d", fa.numRegs,
-                            kLaunchRegs);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return dsa::launch_error("attn_kv8_kernel smem attribute");
     ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
