@@ -233,7 +233,8 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
   return w;
 }
 
-template <int DQK, int DV, bool SEP>
+// kMax: max_logits is asked for (eight registers a softmax thread).
+template <int DQK, int DV, bool SEP, bool kMax>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   using S = Shape<DQK, DV, SEP>;
   constexpr int ST = S::kStages;
@@ -610,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // S^T registers 4j + e (key kA) and 4j + 2 + e (key kB) hold head hb + 2j + e
     const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
     const int hb = hh * 32 + 8 * (lane & 3);
-    const bool want_max = p.max_logits != nullptr;
     // factors of O^T per head (the four warps of a head half write the same ones)
     float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
     // epilogue scratch, in P^T's second term (free once MMA2 has run)
@@ -642,12 +642,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         continue;
       }
       // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
-      float m[8], l_part[8], qs[8], top[8];
+      float m[8], l_part[8], qs[8];
+      [[maybe_unused]] float top[8];
       bool unset = true;                        // no valid slot so far
       float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
       float inv = __uint_as_float(253u << 23);  // 2^-E
 #pragma unroll
-      for (int h = 0; h < 8; ++h) l_part[h] = 0.f, m[h] = 0.f, top[h] = -INFINITY;
+      for (int h = 0; h < 8; ++h) {
+        l_part[h] = 0.f, m[h] = 0.f;
+        if (kMax) top[h] = -INFINITY;
+      }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
         const int b = tile_ctr & 1;
         const uint32_t par = (tile_ctr >> 1) & 1;
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll
         for (int r = 1; r < 16; ++r) most = fmaxf(most, x[r]);
         const bool ex = unset || most > kTheta || svA > ref || svB > ref;
-        if (want_max) {
+        if constexpr (kMax) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -839,14 +843,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         for (int h = 0; h < 8; ++h) mref[hb + h] = m[h];
       }
       red[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
-      if (want_max)
+      if constexpr (kMax)
         redm[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
       group_sync();
       const float unscale = ref * (1.f / kWeight);
       if (st < 64) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
         const float mc = mref[st];
-        const float m_max = want_max ? fmaxf(fmaxf(redm[st], redm[64 + st]), fmaxf(redm[128 + st], redm[192 + st])) : 0.f;
+        const float m_max = kMax ? fmaxf(fmaxf(redm[st], redm[64 + st]), fmaxf(redm[128 + st], redm[192 + st])) : 0.f;
         const bool any = l != 0.f;  // true for NaN too
         float f = unscale;
         if (p.splits > 1) {
@@ -867,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           if (st < w.hv) {
             p.lse[orow + st] = lse_v;
             if (p.lse_kv) p.lse_kv[orow + st] = lkv;
-            if (p.max_logits) p.max_logits[orow + st] = any ? m_max * kLn2 : -INFINITY;
+            if (kMax) p.max_logits[orow + st] = any ? m_max * kLn2 : -INFINITY;
           }
         }
         fac[st] = f;
@@ -997,11 +1001,11 @@ size_t part_bytes(int T, int H, int splits) {
   return (static_cast<size_t>(T) * H * splits * sizeof(float4) + 255) / 256 * 256;
 }
 
-template <int DQK, int DV, bool SEP>
-int launch(const Params& p, int T, int sms, cudaStream_t stream) {
+template <int DQK, int DV, bool SEP, bool kMax>
+int launch_form(const Params& p, int T, int sms, cudaStream_t stream) {
   using S = Shape<DQK, DV, SEP>;
   constexpr int smem = S::kTotal;
-  auto kernel = attn_kv8_kernel<DQK, DV, SEP>;
+  auto kernel = attn_kv8_kernel<DQK, DV, SEP, kMax>;
   static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
   int dev = 0;
   cudaGetDevice(&dev);  // below 64: check_device
@@ -1025,6 +1029,12 @@ int launch(const Params& p, int T, int sms, cudaStream_t stream) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<DV>, p) != cudaSuccess) return dsa::launch_error("attn_kv8_join_kernel");
   return DSA_OK;
+}
+
+template <int DQK, int DV, bool SEP>
+int launch(const Params& p, int T, int sms, cudaStream_t stream) {
+  return p.max_logits ? launch_form<DQK, DV, SEP, true>(p, T, sms, stream)
+                      : launch_form<DQK, DV, SEP, false>(p, T, sms, stream);
 }
 
 }  // namespace
