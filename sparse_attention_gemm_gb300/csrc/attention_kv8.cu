@@ -44,16 +44,15 @@ constexpr int kGatherWarps = 8;
 constexpr int kGatherThreads = kGatherWarps * 32;
 constexpr int kGatherKeys = kGatherThreads / 8;   // keys one gather step covers
 constexpr int kGatherSteps = kKeys / kGatherKeys;
+static_assert(kGatherSteps == 2, "a thread gathers two keys of a tile");
 constexpr int kSoftWarp0 = kGatherWarps;
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
 constexpr int kMma2Warp = kMmaWarp + 1;
 constexpr int kThreads = (kMma2Warp + 1) * 32;
-// 18 warps: 96 registers a thread.  Moving registers from the gather and MMA
-// warps to the softmax ones (setmaxnreg) is not done here: builds whose gather
-// branch came near its limit stopped with an illegal instruction, always at
-// the same place of the same build.
+// 18 warps: 96 registers a thread; moving some from the gather and MMA warps
+// to the softmax ones (setmaxnreg) is not needed: no role is short of any in its loop.
 constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
@@ -152,10 +151,11 @@ __device__ __forceinline__ bool group_any(bool x) {
   return dsa::named_bar_any(1, kSoftThreads, x);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
-               "r"(src_bytes), "l"(policy)
-               : "memory");
+// 16-byte global -> shared copy; src_bytes = 0 fills zeros without reading.  No
+// cache policy: it is a uniform operand of the instruction, and with the tail
+// copied by half a warp's lanes some builds stopped at an illegal instruction.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -294,8 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // every chunk.  A row's place depends on its id and the block table: ids
     // are read two tiles ahead, the table one tile ahead.
     const int gt = threadIdx.x, piece = gt & 7;
-    const uint64_t keep = dsa::l2_policy_evict_last();  // rows are selected by many queries
-    const uint64_t once = dsa::l2_policy_evict_first();
     const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
     int tile_ctr = 0, item_ctr = 0;
     int pend = -1;  // stage whose copies are in flight
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       for (int k = 0; k < 8 * kPieces / 32; ++k) {
         const int x = k * 32 + lane, h = warp * 8 + x / kPieces, c = x % kPieces;
         const bool real = h < w.hv;
-        cp_async16(qa + q_addr(row_of(h) + (c & 1) * kHG, c >> 1), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u, once);
+        cp_async16(qa + q_addr(row_of(h) + (c & 1) * kHG, c >> 1), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u);
       }
       cp_async_commit();
     };
@@ -468,15 +466,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
           const uint32_t dst = buf + dsa::sw128_offset(key, piece * 16);
 #pragma unroll
-          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes, keep);
-          if (S::kTail && piece < 4)
-            cp_async16(buf + S::kTailOff + sw64_offset(key, piece), krow + S::kFull * 128, nbytes, keep);
+          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes);
           if (SEP) {
             const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
 #pragma unroll
             for (int c = 0; c < S::kNv; ++c)
-              cp_async16(dst + S::kVOff + c * kChunkBytes, vrow + c * 128, nbytes, keep);
+              cp_async16(dst + S::kVOff + c * kChunkBytes, vrow + c * 128, nbytes);
           }
+        }
+        if (S::kTail) {
+          // the tail's four pieces: lanes with piece 0..3 take the first key's, the others the second's
+          const bool second = piece >= 4;
+          const int key = (second ? kGatherKeys : 0) + (gt >> 3), r = second ? cur[1] : cur[0];
+          const int64_t rh = static_cast<int64_t>(r >= 0 ? r : 0) * p.Hc + w.kvh;
+          if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
+            cp_async16(buf + S::kTailOff + sw64_offset(key, piece & 3), p.k8 + rh * DQK + S::kFull * 128 + (piece & 3) * 16,
+                       r >= 0 ? 16u : 0u);
         }
         cp_async_commit();
         if (pend >= 0) {
