@@ -609,77 +609,69 @@ def sparse_attn_bwd(q, kv, out, dout, lse_kv, idx, scale: float, topk_length=Non
 
 
 # The calls on the 8-bit cache are made once or twice per layer of a decode
-# step, whose kernels run for a few microseconds: their arguments are checked
-# in one pass each, and pointers and the stream go to ctypes as plain integers
-# (kv8_read from Python: 15.2 us a call with the helpers above, 8 us so).
+# step, whose kernels run for a few microseconds.  Their arguments are checked
+# by one condition each call; only when it fails are they looked at one by one
+# for the error to raise.  Pointers and the stream go to ctypes as plain integers.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch.cuda.current_device
+_Tensor, _U8, _I32, _F32, _BF16 = torch.Tensor, torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
-def _arg(t, name, dtype, dim, device):
-    """Pointer of a tensor argument on `device` (None stays None); raises as _need does."""
-    if t is None:
-        return None
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim or not t.is_contiguous() or
-            t.get_device() != device):
+def _ok(t, dtype, dim, device):
+    """Whether t is a contiguous tensor of this kind on this device."""
+    return (isinstance(t, _Tensor) and t.dtype == dtype and t.dim() == dim and t.is_contiguous() and
+            t.get_device() == device)
+
+
+def _refuse(device, *args):
+    """Raises for the first of (tensor, name, dtype, dim, shape or None) that is not as it has to be."""
+    for t, name, dtype, dim, shape in args:
         _need(t, name, dtype, dim)
-        raise ValueError(f"{name} is on {t.device}, other arguments are on cuda:{device}")
-    return t.data_ptr()
+        if t.get_device() != device or device != _current_device():
+            raise ValueError(f"{name} is on {t.device}: the tensors of a call are on the current device, "
+                             f"cuda:{_current_device()}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError("inconsistent arguments")
 
 
-def _required(t, name, dtype, dim, device):
-    p = _arg(t, name, dtype, dim, device)
-    if t is None:
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return p
-
-
-def _device_of(t, name, dtype, dim):
-    """Device index of the first argument; the call goes to the current device's current stream."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        _need(t, name, dtype, dim)
-    device = t.get_device()
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return device
-
-
-def _kv8_scale(scale, name, n_blocks, heads, device):
-    p = _required(scale, name, torch.float32, 2, device)
-    if scale.shape != (n_blocks, heads):
-        raise ValueError(f"{name} must be [{n_blocks}, {heads}], got {tuple(scale.shape)}")
-    return p
-
-
-def _kv8_sequences(cu_seqlens, pos, block_table, device):
-    """(n_seqs, table width, pointers of cu_seqlens, pos, block_table)"""
-    pc = _required(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+def _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T):
+    _need(cache, "cache", _U8, 4)
+    _need(cu_seqlens, "cu_seqlens", _I32, 1)
+    n_blocks, _, heads, dim = cache.shape
     n_seqs = cu_seqlens.shape[0] - 1
-    pp = _arg(pos, "pos", torch.int32, 1, device)
-    if pos is not None and pos.shape[0] != n_seqs:
-        raise ValueError(f"pos must have {n_seqs} entries, got {pos.shape[0]}")
-    pt = _arg(block_table, "block_table", torch.int32, 2, device)
-    width = 0
+    device = cache.get_device()
+    args = [(cache, "cache", _U8, 4, None), (cache_scale, "cache_scale", _F32, 2, (n_blocks, heads)),
+            (cu_seqlens, "cu_seqlens", _I32, 1, None)]
+    if pos is not None:
+        args.append((pos, "pos", _I32, 1, (n_seqs,)))
     if block_table is not None:
-        rows, width = block_table.shape
-        if rows != n_seqs:
-            raise ValueError(f"block_table must have {n_seqs} rows, got {rows}")
-    return n_seqs, width, pc, pp, pt
+        _need(block_table, "block_table", _I32, 2)
+        args.append((block_table, "block_table", _I32, 2, (n_seqs, block_table.shape[1])))
+    args.append((rows, rows_name, _BF16, 3, (T, heads, dim)))
+    _refuse(device, *args)
 
 
 def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
     """Quantises the bf16 rows src [T, Hc, D] into the E4M3 block cache (uint8
     [n_blocks, block, Hc, D], scale fp32 [n_blocks, Hc]), in place; returns both."""
-    dev = _device_of(cache, "cache", torch.uint8, 4)
-    pk = _required(cache, "cache", torch.uint8, 4, dev)
+    dev = cache.get_device() if isinstance(cache, _Tensor) else -1
+    if not (dev >= 0 and dev == _current_device() and _ok(cache, _U8, 4, dev) and
+            _ok(cache_scale, _F32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev) and
+            _ok(src, _BF16, 3, dev) and (pos is None or _ok(pos, _I32, 1, dev)) and
+            (block_table is None or _ok(block_table, _I32, 2, dev))):
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", src.shape[0])
     n_blocks, block, heads, dim = cache.shape
-    ps = _kv8_scale(cache_scale, "cache_scale", n_blocks, heads, dev)
-    n_seqs, width, pc, pp, pt = _kv8_sequences(cu_seqlens, pos, block_table, dev)
-    px = _required(src, "src", torch.bfloat16, 3, dev)
     T = src.shape[0]
-    if src.shape != (T, heads, dim):
-        raise ValueError(f"src must be [T, {heads}, {dim}], got {tuple(src.shape)}")
-    rc = (_lib or lib()).dsa_kv8_write(px, pc, pp, pt, n_seqs, T, heads, dim, block, n_blocks, width, pk, ps,
+    n_seqs = cu_seqlens.shape[0] - 1
+    rows, width = (n_seqs, 0) if block_table is None else block_table.shape
+    if (src.shape != (T, heads, dim) or cache_scale.shape != (n_blocks, heads) or rows != n_seqs or
+            (pos is not None and pos.shape[0] != n_seqs)):
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", T)
+    rc = (_lib or lib()).dsa_kv8_write(src.data_ptr(), cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(),
+                                       None if block_table is None else block_table.data_ptr(), n_seqs, T, heads, dim,
+                                       block, n_blocks, width, cache.data_ptr(), cache_scale.data_ptr(),
                                        _raw_stream(dev))
     if rc:
         _check("dsa_kv8_write", rc)
@@ -689,18 +681,24 @@ def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
 def kv8_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None, out=None):
     """Rows of the 8-bit block cache back to packed bf16 [T, Hc, D] (rows of an
     `out` that is given stay as they are behind the last sequence)."""
-    dev = _device_of(cache, "cache", torch.uint8, 4)
-    pk = _required(cache, "cache", torch.uint8, 4, dev)
+    dev = cache.get_device() if isinstance(cache, _Tensor) else -1
+    if out is None and dev >= 0 and _ok(cache, _U8, 4, dev):
+        out = torch.empty((T, cache.shape[2], cache.shape[3]), dtype=_BF16, device=cache.device)
+    if not (dev >= 0 and dev == _current_device() and _ok(cache, _U8, 4, dev) and
+            _ok(cache_scale, _F32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev) and
+            _ok(out, _BF16, 3, dev) and (pos is None or _ok(pos, _I32, 1, dev)) and
+            (block_table is None or _ok(block_table, _I32, 2, dev))):
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, out, "out", T)
     n_blocks, block, heads, dim = cache.shape
-    ps = _kv8_scale(cache_scale, "cache_scale", n_blocks, heads, dev)
-    n_seqs, width, pc, pp, pt = _kv8_sequences(cu_seqlens, pos, block_table, dev)
-    if out is None:
-        out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=cache.device)
-    po = _required(out, "out", torch.bfloat16, 3, dev)
-    if out.shape != (T, heads, dim):
-        raise ValueError(f"out must be [{T}, {heads}, {dim}], got {tuple(out.shape)}")
-    rc = (_lib or lib()).dsa_kv8_read(pk, ps, pc, pp, pt, n_seqs, T, heads, dim, block, n_blocks, width, po,
-                                      _raw_stream(dev))
+    n_seqs = cu_seqlens.shape[0] - 1
+    rows, width = (n_seqs, 0) if block_table is None else block_table.shape
+    if (out.shape != (T, heads, dim) or cache_scale.shape != (n_blocks, heads) or rows != n_seqs or
+            (pos is not None and pos.shape[0] != n_seqs)):
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, out, "out", T)
+    rc = (_lib or lib()).dsa_kv8_read(cache.data_ptr(), cache_scale.data_ptr(), cu_seqlens.data_ptr(),
+                                      None if pos is None else pos.data_ptr(),
+                                      None if block_table is None else block_table.data_ptr(), n_seqs, T, heads, dim,
+                                      block, n_blocks, width, out.data_ptr(), _raw_stream(dev))
     if rc:
         _check("dsa_kv8_read", rc)
     return out
@@ -710,64 +708,83 @@ def sparse_attn_fwd_kv8_workspace_size(T: int, H: int, Hc: int, Dqk: int, Dv: in
     return int(lib().dsa_sparse_attn_fwd_kv8_workspace_size(T, H, Hc, Dqk, Dv, K))
 
 
+def _attn_refuse(q, kv8, kv_scale, idx, topk_length, sink, v8, v_scale, cu_seqlens, block_table, out, lse, workspace):
+    _need(q, "q", _BF16, 3)
+    _need(kv8, "kv8", _U8, 4)
+    T, H, Dqk = q.shape
+    n_blocks, block, heads, _ = kv8.shape
+    if (v8 is None) != (v_scale is None):
+        raise ValueError("v8 and v_scale go together")
+    if block_table is not None and cu_seqlens is None:
+        raise ValueError("block_table needs cu_seqlens")
+    args = [(q, "q", _BF16, 3, None), (kv8, "kv8", _U8, 4, (n_blocks, block, heads, Dqk)),
+            (kv_scale, "kv_scale", _F32, 2, (n_blocks, heads))]
+    _need(idx, "idx", _I32, 2)
+    args.append((idx, "idx", _I32, 2, (T, idx.shape[1])))
+    Dv = 512
+    if v8 is not None:
+        _need(v8, "v8", _U8, 4)
+        Dv = v8.shape[3]
+        args += [(v8, "v8", _U8, 4, (n_blocks, block, heads, Dv)), (v_scale, "v_scale", _F32, 2, (n_blocks, heads))]
+    if block_table is not None:
+        _need(block_table, "block_table", _I32, 2)
+        args += [(block_table, "block_table", _I32, 2, None),
+                 (cu_seqlens, "cu_seqlens", _I32, 1, (block_table.shape[0] + 1,))]
+    args += [a for a in ((topk_length, "topk_length", _I32, 1, (T,)), (sink, "sink", _F32, 1, (H,)),
+                         (out, "out", _BF16, 3, (T, H, Dv)), (lse, "lse", _F32, 2, (T, H)),
+                         (workspace, "workspace", _U8, 1, None)) if a[0] is not None]
+    _refuse(q.get_device(), *args)
+
+
 def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, sink=None, v8=None, v_scale=None,
                         cu_seqlens=None, block_table=None, want_lse_kv: bool = False, want_max_logits: bool = False,
                         out=None, lse=None, workspace=None):
     """Sparse attention forward over the 8-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
     idx holds cache rows, or, with block_table and cu_seqlens, positions in the row's sequence."""
-    dev = _device_of(q, "q", torch.bfloat16, 3)
-    pq = _required(q, "q", torch.bfloat16, 3, dev)
+    dev = q.get_device() if isinstance(q, _Tensor) else -1
+    paged = block_table is not None
+    if not (dev >= 0 and dev == _current_device() and _ok(q, _BF16, 3, dev) and _ok(kv8, _U8, 4, dev) and
+            _ok(kv_scale, _F32, 2, dev) and
+            _ok(idx, _I32, 2, dev) and (topk_length is None or _ok(topk_length, _I32, 1, dev)) and
+            (sink is None or _ok(sink, _F32, 1, dev)) and
+            (v8 is None if v_scale is None else _ok(v8, _U8, 4, dev) and _ok(v_scale, _F32, 2, dev)) and
+            (not paged or _ok(block_table, _I32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev)) and
+            (out is None or _ok(out, _BF16, 3, dev)) and (lse is None or _ok(lse, _F32, 2, dev)) and
+            (workspace is None or _ok(workspace, _U8, 1, dev))):
+        _attn_refuse(q, kv8, kv_scale, idx, topk_length, sink, v8, v_scale, cu_seqlens, block_table, out, lse,
+                     workspace)
     T, H, Dqk = q.shape
-    pk = _required(kv8, "kv8", torch.uint8, 4, dev)
     n_blocks, block, heads, dim = kv8.shape
-    pks = _kv8_scale(kv_scale, "kv_scale", n_blocks, heads, dev)
-    pi = _required(idx, "idx", torch.int32, 2, dev)
-    rows, K = idx.shape
-    if dim != Dqk:
-        raise ValueError(f"kv8 rows must have the query's {Dqk} dims, got {dim}")
-    if rows != T:
-        raise ValueError(f"idx must have {T} rows, got {rows}")
-    pl = _arg(topk_length, "topk_length", torch.int32, 1, dev)
-    if topk_length is not None and topk_length.shape[0] != T:
-        raise ValueError(f"topk_length must have {T} entries, got {topk_length.shape[0]}")
-    psk = _arg(sink, "sink", torch.float32, 1, dev)
-    if sink is not None and sink.shape[0] != H:
-        raise ValueError(f"sink must have {H} entries, got {sink.shape[0]}")
-    if (v8 is None) != (v_scale is None):
-        raise ValueError("v8 and v_scale go together")
-    Dv, pv, pvs = 512, None, None
-    if v8 is not None:
-        pv = _required(v8, "v8", torch.uint8, 4, dev)
-        Dv = v8.shape[3]
-        if v8.shape != (n_blocks, block, heads, Dv):
-            raise ValueError("v8 must have the blocks and heads of kv8")
-        pvs = _kv8_scale(v_scale, "v_scale", n_blocks, heads, dev)
-    n_seqs, width, pc, pt = 0, 0, None, None
-    if block_table is not None:
-        if cu_seqlens is None:
-            raise ValueError("block_table needs cu_seqlens")
-        n_seqs, width, pc, _, pt = _kv8_sequences(cu_seqlens, None, block_table, dev)
+    K = idx.shape[1]
+    Dv = 512 if v8 is None else v8.shape[3]
+    n_seqs, width = (0, 0) if not paged else block_table.shape
+    if (dim != Dqk or kv_scale.shape != (n_blocks, heads) or idx.shape[0] != T or
+            (topk_length is not None and topk_length.shape[0] != T) or (sink is not None and sink.shape[0] != H) or
+            (v8 is not None and (v8.shape != (n_blocks, block, heads, Dv) or v_scale.shape != (n_blocks, heads))) or
+            (paged and cu_seqlens.shape[0] != n_seqs + 1) or (out is not None and out.shape != (T, H, Dv)) or
+            (lse is not None and lse.shape != (T, H))):
+        _attn_refuse(q, kv8, kv_scale, idx, topk_length, sink, v8, v_scale, cu_seqlens, block_table, out, lse,
+                     workspace)
     if out is None:
-        out = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != (T, H, Dv):
-        raise ValueError(f"out must be [{T}, {H}, {Dv}], got {tuple(out.shape)}")
+        out = q.new_empty((T, H, Dv))
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse.shape != (T, H):
-        raise ValueError(f"lse must be [{T}, {H}], got {tuple(lse.shape)}")
-    po, ple = _required(out, "out", torch.bfloat16, 3, dev), _required(lse, "lse", torch.float32, 2, dev)
-    lse_kv = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_lse_kv else None
-    ml = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_max_logits else None
+        lse = kv_scale.new_empty((T, H))
+    lse_kv = kv_scale.new_empty((T, H)) if want_lse_kv else None
+    ml = kv_scale.new_empty((T, H)) if want_max_logits else None
     L = _lib or lib()
     if workspace is None:
         need = L.dsa_sparse_attn_fwd_kv8_workspace_size(T, H, heads, Dqk, Dv, K)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    pw = _arg(workspace, "workspace", torch.uint8, 1, dev)
-    rc = L.dsa_sparse_attn_fwd_kv8(pq, pk, pks, pv, pvs, pi, pl, psk, pc, pt, n_seqs, T, H, heads, Dqk, Dv, K, block,
-                                   n_blocks, width, scale, po, ple, None if lse_kv is None else lse_kv.data_ptr(),
-                                   None if ml is None else ml.data_ptr(), pw,
-                                   0 if workspace is None else workspace.shape[0], _raw_stream(dev))
+            workspace = kv8.new_empty(need)
+    rc = L.dsa_sparse_attn_fwd_kv8(
+        q.data_ptr(), kv8.data_ptr(), kv_scale.data_ptr(), None if v8 is None else v8.data_ptr(),
+        None if v8 is None else v_scale.data_ptr(), idx.data_ptr(),
+        None if topk_length is None else topk_length.data_ptr(), None if sink is None else sink.data_ptr(),
+        cu_seqlens.data_ptr() if paged else None, block_table.data_ptr() if paged else None, n_seqs, T, H, heads, Dqk,
+        Dv, K, block, n_blocks, width, scale, out.data_ptr(), lse.data_ptr(),
+        None if lse_kv is None else lse_kv.data_ptr(), None if ml is None else ml.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
+        _raw_stream(dev))
     if rc:
         _check("dsa_sparse_attn_fwd_kv8", rc)
     res = {"out": out, "lse": lse}
