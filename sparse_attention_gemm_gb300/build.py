@@ -21,8 +21,8 @@ BUILD_CHECKED = os.path.join(HERE, "_build_checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "libdsa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "small_ops.cu", "topk.cu", "indexer.cu", "attention.cu", "attention_bwd.cu", "pipeline.cu",
-           "kv8.cu", "attention_kv8.cu"]
-HEADERS = ["common.cuh", "block_sort.cuh", "topk_select.cuh", "kv8.cuh"]
+           "kv8.cu", "attention_kv8.cu", "attention_kv8_narrow.cu"]
+HEADERS = ["common.cuh", "block_sort.cuh", "topk_select.cuh", "kv8.cuh", "attention_kv8.cuh"]
 
 
 def _nvcc() -> str:

@@ -31,14 +31,12 @@
 //
 // Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
 // MMA1, 17 MMA2.
-#include <atomic>
-#include <climits>
-
-#include "kv8.cuh"
+#include "attention_kv8.cuh"
 
 namespace {
 
-constexpr int kKeys = 64;  // keys per tile
+using namespace dsa::kv8_attn;
+
 constexpr int kHG = 64;    // query heads per group
 constexpr int kGatherWarps = 8;
 constexpr int kGatherThreads = kGatherWarps * 32;
@@ -53,44 +51,12 @@ constexpr int kMma2Warp = kMmaWarp + 1;
 constexpr int kThreads = (kMma2Warp + 1) * 32;
 // 18 warps: 96 registers a thread; moving some from the gather and MMA warps
 // to the softmax ones (setmaxnreg) is not needed: no role is short of any in its loop.
-constexpr uint32_t kChunkBytes = kKeys * 128;     // 64 keys x 128 codes
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// Weights reach 2^kTheta before the reference moves; kWeight puts that at
-// E4M3's largest, 448, and leaves an error of 2^-10 / kWeight < 2^-13.8 of a
-// weight of 1 where the smaller term's step ends.  (kTheta = 4, kWeight = 16:
-// the reference of some head moved in a third of the tiles of the drawn
-// prompts, at 2K cycles a time.)
-constexpr float kTheta = 5.0f;
-constexpr float kWeight = 14.0f;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 0;    // S^T buffers at columns 0 and 128 (hi 64, lo 64)
 constexpr int kOCol = 256;  // O^T blocks at 256 + 64 m
-constexpr int kPlanSms = 152;
 constexpr int kMaxSplits = 32;
-
-struct Params {
-  const __nv_bfloat16* q;
-  const uint8_t* k8;
-  const float* k_scale;
-  const uint8_t* v8;  // separate V, or unused
-  const float* v_scale;
-  const int32_t* idx;
-  const int32_t* topk_length;
-  const float* sink;
-  dsa::Kv8Geom g;
-  __nv_bfloat16* out;
-  float* lse;
-  float* lse_kv;
-  float* max_logits;
-  float* part_o;   // [T, H, splits, Dv], splits > 1
-  float4* part_s;  // [T, H, splits]: reference, sum, maximum
-  uint32_t* status;
-  int H, Hc, G, K, splits, n_items;  // G: 64-head groups per KV head
-  float scale_log2;
-};
 
 // A key row is kFull chunks of 128 codes (128-byte swizzle) and, at 576 dims,
 // a tail of 64 (64-byte swizzle).  MMA2 does not read the tail, so once a
@@ -126,18 +92,6 @@ struct Shape {
   static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kPLo % 1024 == 0, "alignment");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ bool elect_sync() {
-  uint32_t is = 0;
-  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(is));
-  return is != 0;
-}
-
 // The softmax warps' barrier, plain and with an OR over the group.  The
 // instructions want converged warps (.aligned), and lanes part at waits and
 // at `if (lane == 0)` or `if (!valid)` before them: each warp is brought
@@ -150,37 +104,6 @@ __device__ __forceinline__ bool group_any(bool x) {
   __syncwarp();
   return dsa::named_bar_any(1, kSoftThreads, x);
 }
-
-// 16-byte global -> shared copy; src_bytes = 0 fills zeros without reading.  No
-// cache policy: it is a uniform operand of the instruction, and with the tail
-// copied by half a warp's lanes some builds stopped at an illegal instruction.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-__device__ __forceinline__ __half2 h2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
-__device__ __forceinline__ uint2 pack4(const uint16_t (&c)[4]) {
-  return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
-}
-
-// Smallest power of two >= x (x >= 0 finite), within [2^-126, 2^126].
-__device__ __forceinline__ float pow2_ceil(float x) {
-  const uint32_t u = __float_as_uint(x);
-  uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) ? 1u : 0u);
-  e = e < 1u ? 1u : (e > 253u ? 253u : e);
-  return __uint_as_float(e << 23);
-}
-
-// Byte offset of 16-byte unit `u` of row `r` in rows of 64 bytes, 64-byte swizzle.
-__device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t u) { return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4); }
 
 // Combines v[0..7] (one value per head hb + i) over the 8 lanes that share
 // lane & 3, halving the values at each step: lane keeps head hb + own_head(lane).
@@ -370,12 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         for (int n = 0; n < 4; ++n) {
           uint16_t h2[2], l2[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t u = wd[2 * n + e];
-            const __half2 h = __floats2half2_rn(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xFFFF0000u) * inv);
-            h2[e] = dsa::e4m3x2_h2(h2_bits(h));
-            l2[e] = dsa::e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(h2[e]))), __float2half2_rn(16.f))));
-          }
+          for (int e = 0; e < 2; ++e) split_query(wd[2 * n + e], inv, h2[e], l2[e]);
           hi[n] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
           lo[n] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
         }
@@ -801,9 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
               const float p0 = ex2(x[4 * j + 2 * k]), p1 = ex2(x[4 * j + 2 * k + 1]);
               l_part[2 * j] += p0;
               l_part[2 * j + 1] += p1;
-              const __half2 h = __floats2half2_rn(p0 * wk, p1 * wk);
-              hi[j] = dsa::e4m3x2_h2(h2_bits(h));
-              lo[j] = dsa::e4m3x2_h2(h2_bits(__hsub2(h, h2_of(dsa::h2_of_e4m3x2(hi[j])))));
+              split_weights(p0 * wk, p1 * wk, hi[j], lo[j]);
             }
             const uint32_t at = sw64_offset(key, hb >> 4) + (hb & 8);
             *reinterpret_cast<uint2*>(ph + at) = pack4(hi);
@@ -1045,7 +961,7 @@ int launch(const Params& p, int T, int sms, cudaStream_t stream) {
 }  // namespace
 
 extern "C" size_t dsa_sparse_attn_fwd_kv8_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
-  if (!known_shape(T, H, Hc, Dqk, Dv, K)) return 0;
+  if (!known_shape(T, H, Hc, Dqk, Dv, K) || narrow_takes(T, H, Hc, K)) return 0;
   const int s = plan_splits(units_of(T, H, Hc), K);
   return s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
 }
@@ -1112,11 +1028,12 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   p.splits = need > 0 ? plan_splits(units, K) : 1;
   p.n_items = static_cast<int>(units * p.splits);
   p.status = dsa::device_status_ptr();
+  p.scale_log2 = scale * kLog2e;
+  if (narrow_takes(T, H, Hc, K)) return launch_narrow(p, T, Dqk, stream);
   if (need > 0) {
     p.part_s = static_cast<float4*>(workspace);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(T, H, p.splits));
   }
-  p.scale_log2 = scale * kLog2e;
   if (separate) return launch<256, 256, true>(p, T, sms, stream);
   return Dqk == 576 ? launch<576, 512, false>(p, T, sms, stream) : launch<512, 512, false>(p, T, sms, stream);
 }

@@ -1,0 +1,109 @@
+// attention_kv8.cuh -- what the two kernels of the attention over the 8-bit
+// block cache share: the arguments, the weights' range and small helpers.
+#pragma once
+
+#include <atomic>
+#include <climits>
+
+#include "kv8.cuh"
+
+namespace dsa {
+namespace kv8_attn {
+
+constexpr int kKeys = 64;  // keys per tile
+constexpr uint32_t kChunkBytes = kKeys * 128;  // 64 keys x 128 codes
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Weights reach 2^kTheta before the reference moves; kWeight puts that at
+// E4M3's largest, 448, and leaves an error of 2^-10 / kWeight < 2^-13.8 of a
+// weight of 1 where the smaller term's step ends.  (kTheta = 4, kWeight = 16:
+// the reference of some head moved in a third of the tiles of the drawn
+// prompts, at 2K cycles a time.)
+constexpr float kTheta = 5.0f;
+constexpr float kWeight = 14.0f;
+constexpr int kPlanSms = 152;
+
+struct Params {
+  const __nv_bfloat16* q;
+  const uint8_t* k8;
+  const float* k_scale;
+  const uint8_t* v8;  // separate V, or unused
+  const float* v_scale;
+  const int32_t* idx;
+  const int32_t* topk_length;
+  const float* sink;
+  dsa::Kv8Geom g;
+  __nv_bfloat16* out;
+  float* lse;
+  float* lse_kv;
+  float* max_logits;
+  float* part_o;   // [T, H, splits, Dv], splits > 1
+  float4* part_s;  // [T, H, splits]: reference, sum, maximum
+  uint32_t* status;
+  int H, Hc, G, K, splits, n_items;  // G: 64-head groups per KV head
+  float scale_log2;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool elect_sync() {
+  uint32_t is = 0;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(is));
+  return is != 0;
+}
+
+// 16-byte global -> shared copy; src_bytes = 0 fills zeros without reading.  No
+// cache policy: it is a uniform operand of the instruction, and with the tail
+// copied by half a warp's lanes some builds stopped at an illegal instruction.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 h2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint2 pack4(const uint16_t (&c)[4]) {
+  return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
+}
+
+// Smallest power of two >= x (x >= 0 finite), within [2^-126, 2^126].
+__device__ __forceinline__ float pow2_ceil(float x) {
+  const uint32_t u = __float_as_uint(x);
+  uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) ? 1u : 0u);
+  e = e < 1u ? 1u : (e > 253u ? 253u : e);
+  return __uint_as_float(e << 23);
+}
+
+// Byte offset of 16-byte unit `u` of row `r` in rows of 64 bytes, 64-byte swizzle.
+__device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t u) { return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4); }
+
+// The two terms of a pair of query values (bf16x2): x / s = hi + lo / 16, inv = 1 / s.
+__device__ __forceinline__ void split_query(uint32_t u, float inv, uint16_t& hi, uint16_t& lo) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xFFFF0000u) * inv);
+  hi = e4m3x2_h2(h2_bits(h));
+  lo = e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(h2_of_e4m3x2(hi))), __float2half2_rn(16.f))));
+}
+// The two terms of a pair of weights.
+__device__ __forceinline__ void split_weights(float w0, float w1, uint16_t& hi, uint16_t& lo) {
+  const __half2 h = __floats2half2_rn(w0, w1);
+  hi = e4m3x2_h2(h2_bits(h));
+  lo = e4m3x2_h2(h2_bits(__hsub2(h, h2_of(h2_of_e4m3x2(hi)))));
+}
+
+// Attention in groups of 16 heads (attention_kv8_narrow.cu): whether it takes
+// a call, and the launch.
+bool narrow_takes(int T, int H, int Hc, int K);
+int launch_narrow(Params p, int T, int Dqk, cudaStream_t stream);
+
+}  // namespace kv8_attn
+}  // namespace dsa

@@ -1,0 +1,764 @@
+// attention_kv8_narrow.cu -- sparse attention over the 8-bit block cache in
+// groups of 16 query heads: the mathematics of attention_kv8.cu (scores from
+// the codes, query and weights as two E4M3 terms, one moving reference), for
+// calls whose KV heads serve at most 16 query heads and for calls of few rows.
+//
+// One work item (token, KV head, 16 heads, split of its slots) per CTA, two
+// CTAs on an SM: with 16 heads a tile's products, softmax and query are a
+// quarter of the 64-head kernel's, so an item is a chain of latencies (ids,
+// table, gather, scores, weights, sums), and what hides one CTA's is the other.
+//   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T  (M = 64 keys, N = 32)
+//   MMA2  O^T[dim, hi|lo head] += V^T[dim, key] . P^T[key, hi|lo head]  (M = 128 dims, N = 32)
+// Hi and lo of the weights are the two halves of one operand; the halves of O^T
+// are added when it is read, which costs 16 columns of TMEM instead of an instruction.
+// Splits of a row are the CTAs of a cluster: each leaves its sums in its own
+// shared memory, and each joins the dims of its rank from everyone's.  No
+// second kernel, no workspace, and the order of the sum is the ranks'.
+//
+// Warps: 0..3 gather, 4..7 query conversion, softmax and epilogue, 8 MMA1, 9 MMA2.
+#include "attention_kv8.cuh"
+
+namespace {
+
+using namespace dsa::kv8_attn;
+
+constexpr int kHG = 16;
+constexpr int kGatherWarps = 4;
+constexpr int kGatherThreads = kGatherWarps * 32;
+constexpr int kGatherKeys = kGatherThreads / 8;  // keys one gather step covers
+constexpr int kGatherSteps = kKeys / kGatherKeys;
+constexpr int kSoftWarps = 4;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kMmaWarp = kGatherWarps + kSoftWarps;
+constexpr int kThreads = (kMmaWarp + 2) * 32;
+constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 16 heads x 128 codes
+constexpr uint32_t kPBytes = kKeys * 2 * kHG;     // both E4M3 terms of P^T
+constexpr uint32_t kSwizzle32B = 6;
+constexpr int kCols = 2 * kHG;  // TMEM columns of one S^T buffer or one block of O^T
+constexpr int kOCol = 2 * kCols;
+constexpr int kMaxCluster = 8;
+
+template <int DQK, int DV, bool SEP>
+struct Shape {
+  static constexpr int kFull = DQK / 128;
+  static constexpr bool kTail = DQK % 128 != 0;
+  static constexpr int kNv = DV / 128;
+  static constexpr uint32_t kVOff = SEP ? kFull * kChunkBytes : 0;
+  static constexpr uint32_t kTailOff = kFull * kChunkBytes;
+  static constexpr uint32_t kBuf = (kFull + (SEP ? kNv : 0)) * kChunkBytes + (kTail ? kKeys * 64 : 0);
+  static constexpr int kStages = SEP ? 3 : 2;  // what two CTAs of an SM have room for
+  static constexpr uint32_t kTmem = kOCol + kNv * kCols <= 128 ? 128 : 256;
+  static constexpr uint32_t kKv = 0;
+  static constexpr uint32_t kQ = kStages * kBuf;
+  static constexpr uint32_t kQTail = kQ + kFull * kQChunkBytes;
+  static constexpr uint32_t kP = kQTail + (kTail ? 2 * kHG * 64 : 0);  // [2]
+  // key and value scale of each slot of a stage (one number where they are one); -1: no slot
+  static constexpr uint32_t kMeta = kP + 2 * kPBytes;
+  static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
+  static constexpr uint32_t kWmax = kMeta + kStages * kMetaStep;  // float [4][16]
+  static constexpr uint32_t kRed = kWmax + 256;                   // float [4][16] sums
+  static constexpr uint32_t kRedM = kRed + 256;                   // float [4][16] maxima
+  static constexpr uint32_t kAlpha = kRedM + 256;                 // float [16]
+  static constexpr uint32_t kFac = kAlpha + 64;                   // float [16]
+  static constexpr uint32_t kStats = kFac + 64;                   // float4 [16]: reference, sum, maximum
+  static constexpr uint32_t kSvm = kStats + 256;                  // float [4]
+  static constexpr uint32_t kQexp = kSvm + 16;                    // uint8 [16]
+  static constexpr uint32_t kBars = kQexp + 16;
+  static constexpr uint32_t kMisc = kBars + 18 * 8;
+  static constexpr uint32_t kTotal = kMisc + 16;
+  static constexpr uint32_t kPart = kKv;  // float [16][DV]: a split's sums, once its products have run
+  static_assert(kTotal <= (228 * 1024) / 2 - 1024, "two CTAs' shared memory");
+  static_assert(kHG * DV * 4 <= kStages * kBuf, "a split's sums fit");
+  static_assert(kBuf % 1024 == 0 && kQ % 1024 == 0 && kP % 1024 == 0, "alignment");
+};
+
+__device__ __forceinline__ void group_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ bool group_any(bool x) {
+  __syncwarp();
+  return dsa::named_bar_any(1, kSoftThreads, x);
+}
+// Every thread of every CTA of the cluster arrives, on every path.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t smem_addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte unit `u` of row `r` in rows of 32 bytes, 32-byte swizzle.
+__device__ __forceinline__ uint32_t sw32_offset(uint32_t r, uint32_t u) { return r * 32u + ((u ^ ((r >> 2) & 1u)) << 4); }
+
+// Combines v[0..3] (one value per head hb + i) over the 8 lanes that share
+// lane & 3: lane keeps head hb + own_head(lane).
+__device__ __forceinline__ int own_head(int lane) { return ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1); }
+template <class F>
+__device__ __forceinline__ float fold4(const float (&v)[4], int lane, F f) {
+  const bool up = (lane & 16) != 0;
+  const float a = f(up ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16));
+  const float b = f(up ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16));
+  const bool up2 = (lane & 8) != 0;
+  const float c = f(up2 ? b : a, __shfl_xor_sync(0xffffffffu, up2 ? a : b, 8));
+  return f(c, __shfl_xor_sync(0xffffffffu, c, 4));
+}
+
+// What the sums of a head give: the factor of its weighted values and the statistics.
+struct Norm {
+  float f, lse, lse_kv;
+};
+__device__ __forceinline__ Norm norm_of(float m, float l, float sink) {
+  Norm n{0.f, sink, INFINITY};
+  if (l != 0.f) {  // true for NaN too
+    const float sk = sink * kLog2e, M = fmaxf(m, sk);
+    const float a = exp2f(m - M);
+    const float z = l * a + exp2f(sk - M);
+    n.f = a / z;
+    n.lse = (M + log2f(z)) * kLn2;
+    n.lse_kv = (m + log2f(l)) * kLn2;
+  }
+  return n;
+}
+
+template <int DQK, int DV, bool SEP>
+__global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Params p) {
+  using S = Shape<DQK, DV, SEP>;
+  constexpr int ST = S::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the kernel has no other shared memory
+
+  // the item: longest rows first (they are the last of a packed prompt)
+  const int unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
+  const int u = p.n_items - 1 - unit;
+  const int per = p.Hc * p.G, group = p.H / p.Hc;
+  const int t = u / per, r0 = u - t * per, kvh = r0 / p.G, g0 = (r0 - kvh * p.G) * kHG;
+  const int h0 = kvh * group + g0, hv = min(kHG, group - g0);
+  if (p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs)) return;  // a padding row: its whole cluster leaves
+  const bool aligned = (dsa::smem_u32(smem) & 1023u) == 0;   // else every swizzle breaks
+  if (!aligned && threadIdx.x == 0) atomicOr(p.status, DSA_STATUS_CHECK_FAILED);
+  int len = p.K;
+  if (p.topk_length) {
+    len = __ldg(p.topk_length + t);
+    len = len < 0 ? 0 : (len > p.K ? p.K : len);
+  }
+  const int nt = aligned ? (len + kKeys - 1) / kKeys : 0;
+  // (nt <= 2^25 and at most 8 splits: the products fit)
+  const int i0 = static_cast<int>(static_cast<uint32_t>(nt) * split / p.splits);
+  const int i1 = static_cast<int>(static_cast<uint32_t>(nt) * (split + 1) / p.splits);
+
+  float* wmax = reinterpret_cast<float*>(smem + S::kWmax);
+  float* red = reinterpret_cast<float*>(smem + S::kRed);
+  float* redm = reinterpret_cast<float*>(smem + S::kRedM);
+  float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
+  float* fac = reinterpret_cast<float*>(smem + S::kFac);
+  float4* stats = reinterpret_cast<float4*>(smem + S::kStats);
+  float* svm = reinterpret_cast<float*>(smem + S::kSvm);
+  uint8_t* qexp = smem + S::kQexp;  // exponents of the query scales (biased; 255: not finite)
+  float* part = reinterpret_cast<float*>(smem + S::kPart);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* kv_full = bars;       // [3]
+  uint64_t* kv_empty = bars + 3;  // [3]
+  uint64_t* s_full = bars + 6;    // [2]
+  uint64_t* s_empty = bars + 8;   // [2]
+  uint64_t* p_full = bars + 10;   // [2]
+  uint64_t* p_empty = bars + 12;  // [2]: MMA2 of the tile has run
+  uint64_t* q_full = bars + 14;
+  uint64_t* drain = bars + 15;    // [2]: the MMA issuers' exit commits
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (aligned) {
+    if (threadIdx.x == 0) {
+      for (int b = 0; b < ST; ++b) {
+        dsa::mbar_init(&kv_full[b], kGatherWarps);
+        dsa::mbar_init(&kv_empty[b], 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        dsa::mbar_init(&s_full[b], 1);
+        dsa::mbar_init(&s_empty[b], kSoftWarps);
+        dsa::mbar_init(&p_full[b], kSoftWarps);
+        dsa::mbar_init(&p_empty[b], 1);
+        dsa::mbar_init(&drain[b], 1);
+      }
+      dsa::mbar_init(q_full, kSoftWarps);
+      *abort_flag = 0;
+      dsa::fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == kMmaWarp) dsa::tmem_alloc(tmem_slot, S::kTmem);
+  }
+  dsa::tc_fence_before();
+  __syncthreads();
+  dsa::tc_fence_after();
+  const uint32_t tmem_base = aligned ? *tmem_slot : 0;
+  const dsa::Waiter wt = dsa::make_waiter(abort_flag, p.status);
+  const int64_t orow = static_cast<int64_t>(t) * p.H + h0;
+
+  if (i0 >= i1) {
+    // no slots: sums of nothing
+    if (threadIdx.x < kHG) stats[threadIdx.x] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (p.splits == 1) {
+      for (int h = 0; h < hv; ++h)
+        for (int d = threadIdx.x; d < DV; d += kThreads) p.out[(orow + h) * DV + d] = __float2bfloat16_rn(0.f);
+      if (threadIdx.x < hv) {
+        p.lse[orow + threadIdx.x] = p.sink ? __ldg(p.sink + h0 + threadIdx.x) : -INFINITY;
+        if (p.lse_kv) p.lse_kv[orow + threadIdx.x] = INFINITY;
+        if (p.max_logits) p.max_logits[orow + threadIdx.x] = -INFINITY;
+      }
+    }
+  } else if (warp < kGatherWarps) {
+    // ------------------------------------------------------------ gather
+    // Thread gt covers piece (gt & 7) (16 codes) of keys (gt >> 3) + 16 kg of
+    // every chunk.  A row's place depends on its id and the block table: ids
+    // are read two tiles ahead, the table one tile ahead.
+    const int gt = threadIdx.x, piece = gt & 7, key0 = gt >> 3;
+    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
+    const int32_t* irow = p.idx + static_cast<int64_t>(t) * p.K;
+    auto load_id = [&](int i, int kg) {
+      const int j = i * kKeys + kg * kGatherKeys + key0;
+      return i < i1 && j < len ? __ldg(irow + j) : -1;
+    };
+    int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
+#pragma unroll
+    for (int kg = 0; kg < kGatherSteps; ++kg) {
+      id[kg] = load_id(i0, kg);
+      nid[kg] = load_id(i0 + 1, kg);
+    }
+    const int32_t* trow =
+        p.g.table ? p.g.table + static_cast<int64_t>(dsa::kv8_seq(p.g.cu, p.g.n_seqs, t)) * p.g.max_blocks : nullptr;
+    auto load_block = [&](int x) {  // as the table holds it; -1 beyond the table
+      const int page = x >> p.g.lb;
+      return !trow || x < 0 ? page : page < p.g.max_blocks ? __ldg(trow + page) : -1;
+    };
+#pragma unroll
+    for (int kg = 0; kg < kGatherSteps; ++kg) blk[kg] = load_block(id[kg]);
+    int pend = -1;  // stage whose copies are in flight
+    float psk[kGatherSteps], psv[kGatherSteps];  // and its keys' scales
+    auto signal = [&](int stage) {
+      if (piece == 0) {
+#pragma unroll
+        for (int kg = 0; kg < kGatherSteps; ++kg) {
+          const int key = kg * kGatherKeys + key0;
+          if (SEP)
+            reinterpret_cast<float2*>(smem + S::kMeta + stage * S::kMetaStep)[key] = make_float2(psk[kg], psv[kg]);
+          else
+            reinterpret_cast<float*>(smem + S::kMeta + stage * S::kMetaStep)[key] = psk[kg];
+        }
+      }
+      dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
+    };
+    for (int i = i0, ctr = 0; i < i1; ++i, ++ctr) {
+      const int stage = ctr % ST;
+      int cur[kGatherSteps];
+#pragma unroll
+      for (int kg = 0; kg < kGatherSteps; ++kg) {
+        cur[kg] = id[kg] >= 0 && blk[kg] >= 0 && blk[kg] < p.g.n_blocks
+                      ? (blk[kg] << p.g.lb) + (id[kg] & ((1 << p.g.lb) - 1))
+                      : -1;
+        id[kg] = nid[kg];
+        blk[kg] = load_block(nid[kg]);
+        nid[kg] = load_id(i + 2, kg);
+      }
+      const uint32_t ph = ((ctr / ST) & 1) ^ 1;
+      if (pend >= 0 && !__all_sync(0xffffffffu, dsa::mbar_test_wait(&kv_empty[stage], ph))) {
+        // no free buffer: do not hold back the tile that may have landed
+        cp_async_wait<0>();
+        signal(pend);
+        pend = -1;
+      }
+      if (!dsa::mbar_wait_warp(&kv_empty[stage], ph, wt)) break;
+      const uint32_t buf = kv_addr + stage * S::kBuf;
+      float nsk[kGatherSteps], nsv[kGatherSteps];
+#pragma unroll
+      for (int kg = 0; kg < kGatherSteps; ++kg) {
+        nsk[kg] = nsv[kg] = -1.f;
+        if (piece == 0 && cur[kg] >= 0) {
+          const int64_t at = static_cast<int64_t>(cur[kg] >> p.g.lb) * p.Hc + kvh;
+          nsk[kg] = __ldg(p.k_scale + at);
+          if (SEP) nsv[kg] = __ldg(p.v_scale + at);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int kg = 0; kg < kGatherSteps; ++kg) {
+        const int key = kg * kGatherKeys + key0;
+        const uint32_t nbytes = cur[kg] >= 0 ? 16u : 0u;
+        const int64_t rh = static_cast<int64_t>(cur[kg] >= 0 ? cur[kg] : 0) * p.Hc + kvh;
+        // checked build: the row is inside the cache
+        if (!dsa::check(cur[kg] < (p.g.n_blocks << p.g.lb), p.status)) continue;
+        const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
+        const uint32_t dst = buf + dsa::sw128_offset(key, piece * 16);
+#pragma unroll
+        for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes);
+        if (SEP) {
+          const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
+#pragma unroll
+          for (int c = 0; c < S::kNv; ++c) cp_async16(dst + S::kVOff + c * kChunkBytes, vrow + c * 128, nbytes);
+        }
+      }
+      if (S::kTail) {
+        // the tail's four pieces: lanes with piece 0..3 take the even steps' keys, the others the odd ones'
+#pragma unroll
+        for (int kg = 0; kg < kGatherSteps; kg += 2) {
+          const bool second = piece >= 4;
+          const int key = (second ? kg + 1 : kg) * kGatherKeys + key0, r = second ? cur[kg + 1] : cur[kg];
+          const int64_t rh = static_cast<int64_t>(r >= 0 ? r : 0) * p.Hc + kvh;
+          if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
+            cp_async16(buf + S::kTailOff + sw64_offset(key, piece & 3), p.k8 + rh * DQK + S::kFull * 128 + (piece & 3) * 16,
+                       r >= 0 ? 16u : 0u);
+        }
+      }
+      cp_async_commit();
+      if (pend >= 0) {
+        cp_async_wait<1>();
+        signal(pend);
+      }
+      pend = stage;
+#pragma unroll
+      for (int kg = 0; kg < kGatherSteps; ++kg) psk[kg] = nsk[kg], psv[kg] = nsv[kg];
+    }
+    cp_async_wait<0>();  // nothing of this thread is in flight when it leaves
+    if (pend >= 0) signal(pend);
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    // Two warps, one per product, each converged with one elected issuer.
+    const bool leader = elect_sync();
+    const uint32_t base = dsa::smem_u32(smem);
+    if (warp == kMmaWarp) {
+      constexpr uint32_t idesc1 = dsa::idesc_e4m3(kKeys, kCols);
+      const uint64_t q_desc = dsa::smem_desc(base + S::kQ, 16, 1024, dsa::kSwizzle128B);
+      const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
+      const uint64_t qt_desc = dsa::smem_desc(base + S::kQTail, 16, 512, dsa::kSwizzle64B);
+      const uint64_t kt_desc = dsa::smem_desc(base + S::kKv + S::kTailOff, 16, 512, dsa::kSwizzle64B);
+      const bool go = dsa::mbar_wait_warp(q_full, 0, wt);
+      for (int i = i0, ctr = 0; i < i1 && go; ++i, ++ctr) {
+        const int b = ctr & 1, stage = ctr % ST;
+        const bool got = dsa::mbar_wait(&s_empty[b], ((ctr >> 1) & 1) ^ 1, wt) &&
+                         dsa::mbar_wait(&kv_full[stage], (ctr / ST) & 1, wt);
+        __syncwarp();
+        dsa::tc_fence_after();
+        const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
+        const uint32_t d = tmem_base + b * kCols;
+#pragma unroll
+        for (int c = 0; c < S::kFull; ++c) {
+          const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            dsa::umma_f8_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
+        }
+        if (S::kTail) {
+          const uint64_t at = kt_desc + stage * (S::kBuf >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) dsa::umma_f8_if(leader && got, d, at + kk * 2, qt_desc + kk * 2, idesc1, 1u);
+        }
+        if (leader && got) dsa::umma_commit(&s_full[b]);
+        if (!__all_sync(0xffffffffu, got)) break;
+      }
+      if (leader) dsa::umma_drain(&drain[0], p.status);
+      __syncwarp();
+    } else {
+      constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kCols) | (1u << 15) | (1u << 16);  // both MN-major
+      const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
+      // P^T rows are 32 bytes (hi and lo of 16 heads): 32-byte swizzle, groups of 8 keys 256 bytes apart
+      const uint64_t p_desc = dsa::smem_desc(base + S::kP, kPBytes, 256, kSwizzle32B);
+      for (int i = i0, ctr = 0; i < i1; ++i, ++ctr) {
+        const int b = ctr & 1, stage = ctr % ST;
+        const bool got = dsa::mbar_wait(&p_full[b], (ctr >> 1) & 1, wt);
+        __syncwarp();
+        dsa::tc_fence_after();
+        const uint64_t a0 = v_desc + stage * (S::kBuf >> 4), b0 = p_desc + b * (kPBytes >> 4);
+#pragma unroll
+        for (int mb = 0; mb < S::kNv; ++mb) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            dsa::umma_f8_if(leader && got, tmem_base + kOCol + mb * kCols,
+                            a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4), b0 + kk * (32 * kCols >> 4), idesc2,
+                            (i > i0 || kk > 0) ? 1u : 0u);
+        }
+        if (leader && got) {
+          dsa::umma_commit(&p_empty[b]);
+          dsa::umma_commit(&kv_empty[stage]);
+        }
+        if (!__all_sync(0xffffffffu, got)) break;
+      }
+      if (leader) dsa::umma_drain(&drain[1], p.status);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ query, softmax, epilogue
+    const int st = threadIdx.x - kGatherThreads;
+    const int quarter = warp & 3;  // TMEM lane quarter
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    // the query: eight threads per head, pieces of 8 values sub, sub + 8, ...
+    // Head 4 c + 2 j + e is row 8 j + 2 c + e of the operand (its second term
+    // 16 rows on), which gives each softmax thread four consecutive heads.
+    {
+      const int hq = st >> 3, sub = st & 7;
+      const int row = ((hq >> 1) & 1) * 8 + (hq >> 2) * 2 + (hq & 1);
+      constexpr int kPieces = DQK / 64;
+      uint4 v[kPieces];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (orow + hq) * DQK) + sub;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) v[k] = hq < hv ? __ldg(src + 8 * k) : make_uint4(0, 0, 0, 0);
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) m = dsa::amax_bf16x8(v[k], m);
+      m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 4)));
+      // a head with infinity or NaN: its scores are NaN
+      const bool finite = m < 0x7F80u;
+      const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
+      const float inv = dsa::pow2_inverse(s);
+      if (sub == 0) qexp[hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) split_query(wd[n], inv, hi[n], lo[n]);
+        const int unit16 = (sub + 8 * k) >> 1;  // 16 codes of the row
+        const uint32_t half = (sub & 1) * 8;
+        const bool tail = unit16 >= S::kFull * 8;
+        const uint32_t at = tail ? S::kQTail + sw64_offset(row, unit16 - S::kFull * 8)
+                                 : S::kQ + (unit16 >> 3) * kQChunkBytes + dsa::sw128_offset(row, (unit16 & 7) * 16);
+        // (16 rows on leaves either swizzle's phase as it is)
+        *reinterpret_cast<uint2*>(smem + at + half) = pack4(hi);
+        *reinterpret_cast<uint2*>(smem + at + half + kHG * (tail ? 64 : 128)) = pack4(lo);
+      }
+      dsa::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(q_full);
+    }
+    // S^T registers 4j + e (key kA) and 4j + 2 + e (key kB) hold head hb + 2j + e
+    const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
+    const int hb = 4 * (lane & 3);
+    // Per head hb + h: the reference, this thread's keys' sum and maximum.
+    float m[4], l_part[4], qs[4], top[4];
+    bool unset = true;                        // no valid slot so far
+    float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
+    float inv = __uint_as_float(253u << 23);  // 2^-E
+#pragma unroll
+    for (int h = 0; h < 4; ++h) l_part[h] = 0.f, m[h] = 0.f, qs[h] = 0.f, top[h] = -INFINITY;
+    bool ok = true;
+    // A wait of this thread gave up: the four warps leave together, at a
+    // point that reduces the flag (see the bf16 kernel).
+    bool failed = false;
+    int ctr = 0;
+    for (int i = i0; i < i1; ++i, ++ctr) {
+      const int b = ctr & 1, stage = ctr % ST;
+      const uint32_t par = (ctr >> 1) & 1;
+      // the slots' scales come with the gathered tile
+      if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (ctr / ST) & 1, wt);
+      float skA, skB, svA, svB;
+      if (SEP) {
+        const float2* meta = reinterpret_cast<const float2*>(smem + S::kMeta + stage * S::kMetaStep);
+        const float2 ma = meta[kA], mb = meta[kB];
+        skA = ma.x, svA = ma.y, skB = mb.x, svB = mb.y;
+      } else {
+        const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
+        svA = skA = meta[kA];
+        svB = skB = meta[kB];
+      }
+      const bool vA = skA >= 0.f, vB = skB >= 0.f;
+      if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
+      __syncwarp();
+      dsa::tc_fence_after();
+      float x[8];
+      {
+        uint32_t v[16];
+        dsa::tmem_ld16x256b_x4(tmem_base + lane_off + b * kCols, v);
+        dsa::tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
+      }
+      if (i == i0) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {  // (255: a head with infinity or NaN)
+          const uint8_t e = qexp[hb + h];
+          qs[h] = __uint_as_float(static_cast<uint32_t>(e) << 23) * (e == 255 ? NAN : p.scale_log2);
+        }
+      }
+      dsa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
+      // scores in powers of two against the references; -inf where there is no slot
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 2 * j + e;
+          x[4 * j + e] = vA ? fmaf(x[4 * j + e], qs[h] * skA, -m[h]) : -INFINITY;
+          x[4 * j + 2 + e] = vB ? fmaf(x[4 * j + 2 + e], qs[h] * skB, -m[h]) : -INFINITY;
+        }
+      }
+      svA = vA ? svA : 0.f;
+      svB = vB ? svB : 0.f;
+      float most = x[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) most = fmaxf(most, x[r]);
+      const bool ex = unset || most > kTheta || svA > ref || svB > ref;
+      float v[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        v[h] = fmaxf(x[4 * (h >> 1) + (h & 1)], x[4 * (h >> 1) + 2 + (h & 1)]);
+        top[h] = fmaxf(top[h], v[h] + m[h]);
+      }
+      bool need_rescale = false;
+      if (group_any(ex || failed)) {
+        if (group_any(failed)) {  // the group leaves together
+          ok = false;
+          break;
+        }
+        // move the references: the tile's maximum per head over its 64 keys
+        wmax[quarter * kHG + hb + own_head(lane)] = fold4(v, lane, [](float a, float c) { return fmaxf(a, c); });
+        float sv = fmaxf(svA, svB);
+        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 4));
+        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
+        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
+        if (lane == 0) svm[quarter] = sv;
+        group_sync();
+        const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
+        const float rn = fmaxf(ref, pow2_ceil(sv_max));
+        inv = dsa::pow2_inverse(rn);
+        const float ratio = ref * inv;  // of the old to the new 2^E
+        ref = rn;
+        bool moved = ratio != 1.f;
+        float4 t4 = *reinterpret_cast<const float4*>(wmax + hb);
+#pragma unroll
+        for (int q4 = 1; q4 < 4; ++q4) {
+          const float4 o = *reinterpret_cast<const float4*>(wmax + q4 * kHG + hb);
+          t4.x = fmaxf(t4.x, o.x), t4.y = fmaxf(t4.y, o.y), t4.z = fmaxf(t4.z, o.z), t4.w = fmaxf(t4.w, o.w);
+        }
+        const float tm[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          // by how much the reference moves: to the tile's maximum, if that
+          // passes it by kTheta or is the first
+          const float up = (unset ? tm[h] > -INFINITY : tm[h] > kTheta) ? tm[h] : 0.f;
+          const float a = unset ? 1.f : ex2(-up);
+          moved |= up != 0.f;
+          l_part[h] *= a;
+          m[h] += up;
+          x[4 * (h >> 1) + (h & 1)] -= up;
+          x[4 * (h >> 1) + 2 + (h & 1)] -= up;
+          if (lane < 4) alpha[hb + h] = a * ratio;  // (the four warps write the same ones)
+        }
+        unset = unset && !(sv_max > 0.f);
+        need_rescale = __any_sync(0xffffffffu, moved) && i > i0;
+      }
+      // P^T rows kA and kB, both terms: the thread's four heads are bytes hb .. hb + 3 of each half
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[b], par ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
+      {
+        uint8_t* pb = smem + S::kP + b * kPBytes;
+        const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int key = k ? kB : kA;
+          const float wk = k ? wB : wA;
+          uint16_t hi[2], lo[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float p0 = ex2(x[4 * j + 2 * k]), p1 = ex2(x[4 * j + 2 * k + 1]);
+            l_part[2 * j] += p0;
+            l_part[2 * j + 1] += p1;
+            split_weights(p0 * wk, p1 * wk, hi[j], lo[j]);
+          }
+          *reinterpret_cast<uint32_t*>(pb + sw32_offset(key, 0) + hb) = hi[0] | (static_cast<uint32_t>(hi[1]) << 16);
+          *reinterpret_cast<uint32_t*>(pb + sw32_offset(key, 1) + hb) = lo[0] | (static_cast<uint32_t>(lo[1]) << 16);
+        }
+      }
+      if (need_rescale) {
+        // MMA2 of the previous tile must have landed before O^T is scaled
+        if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((ctr - 1) >> 1) & 1, wt);
+        __syncwarp();  // (and alpha, written by four lanes of this warp)
+        dsa::tc_fence_after();
+#pragma unroll 1
+        for (int mb = 0; mb < S::kNv; ++mb) {
+          const uint32_t ta = tmem_base + lane_off + kOCol + mb * kCols;
+          uint32_t o[32];
+          __syncwarp();
+          dsa::tmem_ld32(ta, o);
+          dsa::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c & 15]);
+          dsa::tmem_st32(ta, o);
+        }
+        dsa::tmem_wait_st();
+      }
+      dsa::fence_proxy_async_smem();
+      dsa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dsa::mbar_arrive(&p_full[b]);
+    }
+
+    // ---------------------------------------------------------- epilogue
+    if (ok) {
+      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
+      // been waited for in turn, so the parity names that tile)
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[(ctr - 1) & 1], ((ctr - 1) >> 1) & 1, wt);
+      __syncwarp();
+      dsa::tc_fence_after();
+      red[quarter * kHG + hb + own_head(lane)] = fold4(l_part, lane, [](float a, float c) { return a + c; });
+      redm[quarter * kHG + hb + own_head(lane)] = fold4(top, lane, [](float a, float c) { return fmaxf(a, c); });
+      if (quarter == 0 && lane < 4) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) alpha[hb + h] = m[h];
+      }
+      group_sync();
+      const float unscale = ref * (1.f / kWeight);
+      if (st < kHG) {
+        const float l = red[st] + red[kHG + st] + red[2 * kHG + st] + red[3 * kHG + st];
+        const float mc = alpha[st];
+        const float mx = fmaxf(fmaxf(redm[st], redm[kHG + st]), fmaxf(redm[2 * kHG + st], redm[3 * kHG + st]));
+        stats[st] = make_float4(mc, l, mx, 0.f);
+        fac[st] = unscale;
+        if (p.splits == 1) {
+          const Norm n = norm_of(mc, l, p.sink && st < hv ? __ldg(p.sink + h0 + st) : -INFINITY);
+          fac[st] = n.f * unscale;
+          if (st < hv) {
+            p.lse[orow + st] = n.lse;
+            if (p.lse_kv) p.lse_kv[orow + st] = n.lse_kv;
+            if (p.max_logits) p.max_logits[orow + st] = l != 0.f ? mx * kLn2 : -INFINITY;
+          }
+        }
+      }
+      group_sync();
+#pragma unroll 1
+      for (int mb = 0; mb < S::kNv; ++mb) {
+        uint32_t v[32];
+        __syncwarp();
+        dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kCols, v);
+        dsa::tmem_wait_ld();
+        const int d = mb * 128 + quarter * 32 + lane;
+#pragma unroll
+        for (int h = 0; h < kHG; ++h) {
+          const float o = (__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * fac[h];
+          if (h < hv) {
+            if (p.splits > 1) part[h * DV + d] = o;
+            else p.out[(orow + h) * DV + d] = __float2bfloat16_rn(o);
+          }
+        }
+      }
+      dsa::tc_fence_before();
+    }
+  }
+
+  __syncwarp();
+  if (p.splits > 1) {
+    // Joins the splits: with M the largest reference, out = sum_s 2^(m_s - M) O_s / z.
+    cluster_sync();
+    const int dims = DV / p.splits, quads = dims / 4, d0 = split * dims;
+    const uint32_t stats_at = dsa::smem_u32(stats), part_at = dsa::smem_u32(part);
+    for (int x = threadIdx.x; x < hv * quads; x += kThreads) {
+      const int h = x / quads, d = d0 + (x - h * quads) * 4;
+      float4 sm[kMaxCluster];
+      float M = -INFINITY, mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s) {
+        sm[s] = s < p.splits ? ld_cluster(of_rank(stats_at + h * 16, s)) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (sm[s].y != 0.f) M = fmaxf(M, sm[s].x), mx = fmaxf(mx, sm[s].z);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s) {
+        if (sm[s].y == 0.f) continue;  // a split without a valid slot
+        const float a = exp2f(sm[s].x - M);
+        const float4 v = ld_cluster(of_rank(part_at + (h * DV + d) * 4, s));
+        l = fmaf(sm[s].y, a, l);
+        acc.x = fmaf(a, v.x, acc.x), acc.y = fmaf(a, v.y, acc.y), acc.z = fmaf(a, v.z, acc.z), acc.w = fmaf(a, v.w, acc.w);
+      }
+      const Norm n = norm_of(M, l, p.sink ? __ldg(p.sink + h0 + h) : -INFINITY);
+      const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc.x * n.f, acc.y * n.f),
+                           o1 = __floats2bfloat162_rn(acc.z * n.f, acc.w * n.f);
+      *reinterpret_cast<uint2*>(p.out + (orow + h) * DV + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+      if (d == 0) {
+        p.lse[orow + h] = n.lse;
+        if (p.lse_kv) p.lse_kv[orow + h] = n.lse_kv;
+        if (p.max_logits) p.max_logits[orow + h] = l != 0.f ? mx * kLn2 : -INFINITY;
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == kMmaWarp && aligned) {
+    dsa::tc_fence_after();
+    dsa::tmem_dealloc(tmem_base, S::kTmem);
+  }
+  if (p.splits > 1) cluster_sync();  // the others have read this CTA's sums
+}
+
+int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * ((H / Hc + kHG - 1) / kHG); }
+
+// Splits of each row's slots, one to eight: the number that makes the busiest SM's work shortest,
+// counting an item as its tiles plus kItemTiles for what happens once.
+constexpr int kItemTiles = 4;
+
+int plan_splits(int64_t units, int K) {
+  const int nt = (K + kKeys - 1) / kKeys;
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= kMaxCluster && s <= nt; s *= 2) {
+    const int64_t waves = (units * s + 2 * kPlanSms - 1) / (2 * kPlanSms);
+    const int64_t c = 4 * waves * ((nt + s - 1) / s + kItemTiles) + (s > 1 ? 2 + s : 0);
+    if (c < cost) cost = c, best = s;
+  }
+  return best;
+}
+
+template <int DQK, int DV, bool SEP>
+int launch_form(const Params& p, cudaStream_t stream) {
+  using S = Shape<DQK, DV, SEP>;
+  auto kernel = attn_kv8_narrow_kernel<DQK, DV, SEP>;
+  static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
+  int dev = 0;
+  cudaGetDevice(&dev);  // below 64: check_device
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal) != cudaSuccess)
+      return dsa::launch_error("attn_kv8_narrow_kernel smem attribute");
+    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_items) * p.splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return dsa::launch_error("attn_kv8_narrow_kernel");
+  return DSA_OK;
+}
+
+}  // namespace
+
+namespace dsa {
+namespace kv8_attn {
+
+bool narrow_takes(int T, int H, int Hc, int) { return H / Hc <= kHG || units_of(T, H, Hc) <= 16; }
+
+int launch_narrow(Params p, int T, int Dqk, cudaStream_t stream) {
+  p.G = (p.H / p.Hc + kHG - 1) / kHG;
+  const int64_t units = units_of(T, p.H, p.Hc);
+  p.splits = plan_splits(units, p.K);
+  p.n_items = static_cast<int>(units);
+  if (Dqk == 256) return launch_form<256, 256, true>(p, stream);
+  return Dqk == 576 ? launch_form<576, 512, false>(p, stream) : launch_form<512, 512, false>(p, stream);
+}
+
+}  // namespace kv8_attn
+}  // namespace dsa
