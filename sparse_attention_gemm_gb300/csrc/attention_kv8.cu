@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
       const Item w = get_item(p, it, t_end);
       if (w.i0 >= w.i1) continue;
-      const int b = p.g.table ? dsa::kv8_seq(p.g.cu, p.g.n_seqs, w.t) : 0;
+      const int b = p.g.table ? dsa::kv8_seq_warp(p.g.cu, p.g.n_seqs, w.t) : 0;
       const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
       auto load_id = [&](int i, int kg) {
         const int j = i * kKeys + kg * kGatherKeys + (gt >> 3);
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           svA = skA = meta[kA];
           svB = skB = meta[kB];
         }
-        const bool vA = skA >= 0.f, vB = skB >= 0.f;
+        const bool vA = skA > 0.f, vB = skB > 0.f;
         if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
         __syncwarp();
         dsa::tc_fence_after();

@@ -52,7 +52,7 @@ struct Shape {
   static constexpr uint32_t kQ = kStages * kBuf;
   static constexpr uint32_t kQTail = kQ + kFull * kQChunkBytes;
   static constexpr uint32_t kP = kQTail + (kTail ? 2 * kHG * 64 : 0);  // [2]
-  // key and value scale of each slot of a stage (one number where they are one); -1: no slot
+  // scale of each slot's key and, behind them, value (one number where they are one); 0: no slot
   static constexpr uint32_t kMeta = kP + 2 * kPBytes;
   static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
   static constexpr uint32_t kWmax = kMeta + kStages * kMetaStep;  // float [4][16]
@@ -60,7 +60,7 @@ struct Shape {
   static constexpr uint32_t kRedM = kRed + 256;                   // float [4][16] maxima
   static constexpr uint32_t kAlpha = kRedM + 256;                 // float [16]
   static constexpr uint32_t kFac = kAlpha + 64;                   // float [16]
-  static constexpr uint32_t kStats = kFac + 64;                   // float4 [16]: reference, sum, maximum
+  static constexpr uint32_t kStats = kFac + 64;                   // float4 [16]: reference, sum, maximum, sink
   static constexpr uint32_t kSvm = kStats + 256;                  // float [4]
   static constexpr uint32_t kQexp = kSvm + 16;                    // uint8 [16]
   static constexpr uint32_t kBars = kQexp + 16;
@@ -81,9 +81,8 @@ __device__ __forceinline__ bool group_any(bool x) {
   return dsa::named_bar_any(1, kSoftThreads, x);
 }
 // Every thread of every CTA of the cluster arrives, on every path.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t of_rank(uint32_t smem_addr, int rank) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
@@ -140,17 +139,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   const int per = p.Hc * p.G, group = p.H / p.Hc;
   const int t = u / per, r0 = u - t * per, kvh = r0 / p.G, g0 = (r0 - kvh * p.G) * kHG;
   const int h0 = kvh * group + g0, hv = min(kHG, group - g0);
-  if (p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs)) return;  // a padding row: its whole cluster leaves
-  const bool aligned = (dsa::smem_u32(smem) & 1023u) == 0;   // else every swizzle breaks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool aligned = (dsa::smem_u32(smem) & 1023u) == 0;  // else every swizzle breaks
   if (!aligned && threadIdx.x == 0) atomicOr(p.status, DSA_STATUS_CHECK_FAILED);
+  // a row of padding behind the last sequence: nothing is read or written for it
+  const bool dead = p.g.table && t >= __ldg(p.g.cu + p.g.n_seqs);
   int len = p.K;
   if (p.topk_length) {
     len = __ldg(p.topk_length + t);
     len = len < 0 ? 0 : (len > p.K ? p.K : len);
   }
-  const int nt = aligned ? (len + kKeys - 1) / kKeys : 0;
+  const int nt = aligned && !dead ? (len + kKeys - 1) / kKeys : 0;
   // (nt <= 2^25 and at most 8 splits: the products fit)
-  const int i0 = static_cast<int>(static_cast<uint32_t>(nt) * split / p.splits);
+  const int i0 = split == 0 ? 0 : static_cast<int>(static_cast<uint32_t>(nt) * split / p.splits);
   const int i1 = static_cast<int>(static_cast<uint32_t>(nt) * (split + 1) / p.splits);
 
   float* wmax = reinterpret_cast<float*>(smem + S::kWmax);
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   float* svm = reinterpret_cast<float*>(smem + S::kSvm);
   uint8_t* qexp = smem + S::kQexp;  // exponents of the query scales (biased; 255: not finite)
   float* part = reinterpret_cast<float*>(smem + S::kPart);
+  __nv_bfloat16* row16 = reinterpret_cast<__nv_bfloat16*>(smem + S::kPart);  // [16][DV]: the results of an undivided row
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* kv_full = bars;       // [3]
   uint64_t* kv_empty = bars + 3;  // [3]
@@ -174,11 +176,44 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // First loads, before the barriers and TMEM are there: the gather warps'
+  // ids of two tiles and table entries of one, the softmax warps' query.
+  static_assert(kGatherThreads == 8 * kHG, "eight threads a head");
+  const int64_t orow = static_cast<int64_t>(t) * p.H + h0;
+  const int32_t* irow = p.idx + static_cast<int64_t>(t) * p.K;
+  auto slot_of = [&](int i, int kg) { return i * kKeys + kg * kGatherKeys + static_cast<int>(threadIdx.x >> 3); };
+  const int32_t* trow = nullptr;
+  auto load_block = [&](int x) {  // as the table holds it; -1 beyond the table
+    const int page = x >> p.g.lb;
+    return !trow || x < 0 ? page : page < p.g.max_blocks ? __ldg(trow + page) : -1;
+  };
+  int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
+  constexpr int kPieces = DQK / 64;  // 16-byte pieces of a head's row a thread converts
+  const int st = threadIdx.x - kGatherThreads, hq = st >> 3, sub = st & 7;
+  uint4 qv[kPieces];
+  if (warp < kGatherWarps) {
+#pragma unroll
+    for (int kg = 0; kg < kGatherSteps; ++kg) {
+      id[kg] = slot_of(i0, kg) < p.K ? __ldg(irow + slot_of(i0, kg)) : -1;
+      nid[kg] = slot_of(i0 + 1, kg) < p.K ? __ldg(irow + slot_of(i0 + 1, kg)) : -1;
+    }
+    if (p.g.table) trow = p.g.table + static_cast<int64_t>(dsa::kv8_seq_warp(p.g.cu, p.g.n_seqs, t)) * p.g.max_blocks;
+#pragma unroll
+    for (int kg = 0; kg < kGatherSteps; ++kg) {
+      id[kg] = slot_of(i0, kg) < len ? id[kg] : -1;
+      nid[kg] = i0 + 1 < i1 && slot_of(i0 + 1, kg) < len ? nid[kg] : -1;
+      blk[kg] = load_block(id[kg]);
+    }
+  } else if (warp < kMmaWarp) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (orow + hq) * DQK) + sub;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) qv[k] = hq < hv ? __ldg(src + 8 * k) : make_uint4(0, 0, 0, 0);
+  }
+
   if (aligned) {
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kThreads - 32) {  // (a warp that has nothing else to do)
       for (int b = 0; b < ST; ++b) {
-        dsa::mbar_init(&kv_full[b], kGatherWarps);
+        dsa::mbar_init(&kv_full[b], kGatherThreads);
         dsa::mbar_init(&kv_empty[b], 1);
       }
       for (int b = 0; b < 2; ++b) {
@@ -200,12 +235,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   dsa::tc_fence_after();
   const uint32_t tmem_base = aligned ? *tmem_slot : 0;
   const dsa::Waiter wt = dsa::make_waiter(abort_flag, p.status);
-  const int64_t orow = static_cast<int64_t>(t) * p.H + h0;
 
   if (i0 >= i1) {
     // no slots: sums of nothing
-    if (threadIdx.x < kHG) stats[threadIdx.x] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    if (p.splits == 1) {
+    if (threadIdx.x < kHG)
+      stats[threadIdx.x] = make_float4(-INFINITY, 0.f, -INFINITY, p.sink && threadIdx.x < hv ? __ldg(p.sink + h0 + threadIdx.x) : -INFINITY);
+    if (p.splits == 1 && !dead) {
       for (int h = 0; h < hv; ++h)
         for (int d = threadIdx.x; d < DV; d += kThreads) p.out[(orow + h) * DV + d] = __float2bfloat16_rn(0.f);
       if (threadIdx.x < hv) {
@@ -220,43 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
     // every chunk.  A row's place depends on its id and the block table: ids
     // are read two tiles ahead, the table one tile ahead.
     const int gt = threadIdx.x, piece = gt & 7, key0 = gt >> 3;
-    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
-    const int32_t* irow = p.idx + static_cast<int64_t>(t) * p.K;
-    auto load_id = [&](int i, int kg) {
-      const int j = i * kKeys + kg * kGatherKeys + key0;
-      return i < i1 && j < len ? __ldg(irow + j) : -1;
-    };
-    int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
-#pragma unroll
-    for (int kg = 0; kg < kGatherSteps; ++kg) {
-      id[kg] = load_id(i0, kg);
-      nid[kg] = load_id(i0 + 1, kg);
-    }
-    const int32_t* trow =
-        p.g.table ? p.g.table + static_cast<int64_t>(dsa::kv8_seq(p.g.cu, p.g.n_seqs, t)) * p.g.max_blocks : nullptr;
-    auto load_block = [&](int x) {  // as the table holds it; -1 beyond the table
-      const int page = x >> p.g.lb;
-      return !trow || x < 0 ? page : page < p.g.max_blocks ? __ldg(trow + page) : -1;
-    };
-#pragma unroll
-    for (int kg = 0; kg < kGatherSteps; ++kg) blk[kg] = load_block(id[kg]);
-    int pend = -1;  // stage whose copies are in flight
-    float psk[kGatherSteps], psv[kGatherSteps];  // and its keys' scales
-    auto signal = [&](int stage) {
-      if (piece == 0) {
-#pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) {
-          const int key = kg * kGatherKeys + key0;
-          if (SEP)
-            reinterpret_cast<float2*>(smem + S::kMeta + stage * S::kMetaStep)[key] = make_float2(psk[kg], psv[kg]);
-          else
-            reinterpret_cast<float*>(smem + S::kMeta + stage * S::kMetaStep)[key] = psk[kg];
-        }
-      }
-      dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
-      __syncwarp();
-      if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
-    };
+    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv, meta_addr = dsa::smem_u32(smem) + S::kMeta;
     for (int i = i0, ctr = 0; i < i1; ++i, ++ctr) {
       const int stage = ctr % ST;
       int cur[kGatherSteps];
@@ -267,28 +266,22 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
                       : -1;
         id[kg] = nid[kg];
         blk[kg] = load_block(nid[kg]);
-        nid[kg] = load_id(i + 2, kg);
+        nid[kg] = i + 2 < i1 && slot_of(i + 2, kg) < len ? __ldg(irow + slot_of(i + 2, kg)) : -1;
       }
       const uint32_t ph = ((ctr / ST) & 1) ^ 1;
-      if (pend >= 0 && !__all_sync(0xffffffffu, dsa::mbar_test_wait(&kv_empty[stage], ph))) {
-        // no free buffer: do not hold back the tile that may have landed
-        cp_async_wait<0>();
-        signal(pend);
-        pend = -1;
-      }
       if (!dsa::mbar_wait_warp(&kv_empty[stage], ph, wt)) break;
       const uint32_t buf = kv_addr + stage * S::kBuf;
-      float nsk[kGatherSteps], nsv[kGatherSteps];
+      {
+        // the scales: lanes with piece kg and kg + 4 take key kg's (with V, its key scale and its value scale)
+        int r = cur[0];
 #pragma unroll
-      for (int kg = 0; kg < kGatherSteps; ++kg) {
-        nsk[kg] = nsv[kg] = -1.f;
-        if (piece == 0 && cur[kg] >= 0) {
-          const int64_t at = static_cast<int64_t>(cur[kg] >> p.g.lb) * p.Hc + kvh;
-          nsk[kg] = __ldg(p.k_scale + at);
-          if (SEP) nsv[kg] = __ldg(p.v_scale + at);
-        }
+        for (int kg = 1; kg < kGatherSteps; ++kg) r = (piece & 3) == kg ? cur[kg] : r;
+        const int64_t at = static_cast<int64_t>((r >= 0 ? r : 0) >> p.g.lb) * p.Hc + kvh;
+        const bool value = SEP && piece >= 4;
+        if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
+          cp_async4(meta_addr + stage * S::kMetaStep + (value ? kKeys * 4 : 0) + ((piece & 3) * kGatherKeys + key0) * 4,
+                    (value ? p.v_scale : p.k_scale) + at, r >= 0 ? 4u : 0u);
       }
-      __syncwarp();
 #pragma unroll
       for (int kg = 0; kg < kGatherSteps; ++kg) {
         const int key = kg * kGatherKeys + key0;
@@ -318,17 +311,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
                        r >= 0 ? 16u : 0u);
         }
       }
-      cp_async_commit();
-      if (pend >= 0) {
-        cp_async_wait<1>();
-        signal(pend);
-      }
-      pend = stage;
-#pragma unroll
-      for (int kg = 0; kg < kGatherSteps; ++kg) psk[kg] = nsk[kg], psv[kg] = nsv[kg];
+      cp_async_arrive(&kv_full[stage]);
     }
-    cp_async_wait<0>();  // nothing of this thread is in flight when it leaves
-    if (pend >= 0) signal(pend);
+    cp_async_wait_all();  // nothing of this thread is in flight when it leaves
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // Two warps, one per product, each converged with one elected issuer.
@@ -345,6 +330,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         const int b = ctr & 1, stage = ctr % ST;
         const bool got = dsa::mbar_wait(&s_empty[b], ((ctr >> 1) & 1) ^ 1, wt) &&
                          dsa::mbar_wait(&kv_full[stage], (ctr / ST) & 1, wt);
+        // the gathered codes, before the tensor core reads them (MMA2's come
+        // with the softmax warps' arrival, behind a fence of theirs)
+        dsa::fence_proxy_async_smem();
         __syncwarp();
         dsa::tc_fence_after();
         const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
@@ -396,23 +384,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
     }
   } else {
     // ------------------------------------------------------------ query, softmax, epilogue
-    const int st = threadIdx.x - kGatherThreads;
     const int quarter = warp & 3;  // TMEM lane quarter
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // the query: eight threads per head, pieces of 8 values sub, sub + 8, ...
     // Head 4 c + 2 j + e is row 8 j + 2 c + e of the operand (its second term
     // 16 rows on), which gives each softmax thread four consecutive heads.
     {
-      const int hq = st >> 3, sub = st & 7;
       const int row = ((hq >> 1) & 1) * 8 + (hq >> 2) * 2 + (hq & 1);
-      constexpr int kPieces = DQK / 64;
-      uint4 v[kPieces];
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (orow + hq) * DQK) + sub;
-#pragma unroll
-      for (int k = 0; k < kPieces; ++k) v[k] = hq < hv ? __ldg(src + 8 * k) : make_uint4(0, 0, 0, 0);
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) m = dsa::amax_bf16x8(v[k], m);
+      for (int k = 0; k < kPieces; ++k) m = dsa::amax_bf16x8(qv[k], m);
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
       m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 4)));
@@ -423,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       if (sub == 0) qexp[hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
-        const uint32_t wd[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        const uint32_t wd[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
         uint16_t hi[4], lo[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) split_query(wd[n], inv, hi[n], lo[n]);
@@ -460,17 +441,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       const uint32_t par = (ctr >> 1) & 1;
       // the slots' scales come with the gathered tile
       if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (ctr / ST) & 1, wt);
-      float skA, skB, svA, svB;
-      if (SEP) {
-        const float2* meta = reinterpret_cast<const float2*>(smem + S::kMeta + stage * S::kMetaStep);
-        const float2 ma = meta[kA], mb = meta[kB];
-        skA = ma.x, svA = ma.y, skB = mb.x, svB = mb.y;
-      } else {
-        const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
-        svA = skA = meta[kA];
-        svB = skB = meta[kB];
-      }
-      const bool vA = skA >= 0.f, vB = skB >= 0.f;
+      const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
+      const float skA = meta[kA], skB = meta[kB];
+      const bool vA = skA > 0.f, vB = skB > 0.f;
+      const float svA = vA ? (SEP ? meta[kKeys + kA] : skA) : 0.f, svB = vB ? (SEP ? meta[kKeys + kB] : skB) : 0.f;
       if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
       __syncwarp();
       dsa::tc_fence_after();
@@ -502,8 +476,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
           x[4 * j + 2 + e] = vB ? fmaf(x[4 * j + 2 + e], qs[h] * skB, -m[h]) : -INFINITY;
         }
       }
-      svA = vA ? svA : 0.f;
-      svB = vB ? svB : 0.f;
       float most = x[0];
 #pragma unroll
       for (int r = 1; r < 8; ++r) most = fmaxf(most, x[r]);
@@ -515,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         top[h] = fmaxf(top[h], v[h] + m[h]);
       }
       bool need_rescale = false;
-      if (group_any(ex || failed)) {
+      if (i == i0 || group_any(ex || failed)) {
         if (group_any(failed)) {  // the group leaves together
           ok = false;
           break;
@@ -606,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
     if (ok) {
       // O^T is complete with the last tile's MMA2 (each phase of p_empty has
       // been waited for in turn, so the parity names that tile)
+      const float sink = p.sink && st < hv ? __ldg(p.sink + h0 + st) : -INFINITY;
       if (!failed) failed = !dsa::mbar_wait(&p_empty[(ctr - 1) & 1], ((ctr - 1) >> 1) & 1, wt);
       __syncwarp();
       dsa::tc_fence_after();
@@ -621,10 +594,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         const float l = red[st] + red[kHG + st] + red[2 * kHG + st] + red[3 * kHG + st];
         const float mc = alpha[st];
         const float mx = fmaxf(fmaxf(redm[st], redm[kHG + st]), fmaxf(redm[2 * kHG + st], redm[3 * kHG + st]));
-        stats[st] = make_float4(mc, l, mx, 0.f);
+        stats[st] = make_float4(mc, l, mx, sink);
         fac[st] = unscale;
         if (p.splits == 1) {
-          const Norm n = norm_of(mc, l, p.sink && st < hv ? __ldg(p.sink + h0 + st) : -INFINITY);
+          const Norm n = norm_of(mc, l, sink);
           fac[st] = n.f * unscale;
           if (st < hv) {
             p.lse[orow + st] = n.lse;
@@ -634,6 +607,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         }
       }
       group_sync();
+      float f[kHG];
+#pragma unroll
+      for (int h = 0; h < kHG; h += 4) {
+        const float4 f4 = *reinterpret_cast<const float4*>(fac + h);
+        f[h] = f4.x, f[h + 1] = f4.y, f[h + 2] = f4.z, f[h + 3] = f4.w;
+      }
 #pragma unroll 1
       for (int mb = 0; mb < S::kNv; ++mb) {
         uint32_t v[32];
@@ -641,14 +620,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kCols, v);
         dsa::tmem_wait_ld();
         const int d = mb * 128 + quarter * 32 + lane;
+        if (p.splits > 1) {
 #pragma unroll
-        for (int h = 0; h < kHG; ++h) {
-          const float o = (__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * fac[h];
-          if (h < hv) {
-            if (p.splits > 1) part[h * DV + d] = o;
-            else p.out[(orow + h) * DV + d] = __float2bfloat16_rn(o);
-          }
+          for (int h = 0; h < kHG; ++h) part[h * DV + d] = (__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * f[h];
+        } else {
+#pragma unroll
+          for (int h = 0; h < kHG; ++h)
+            row16[h * DV + d] = __float2bfloat16_rn((__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * f[h]);
         }
+      }
+      if (p.splits == 1) {
+        // through shared memory: 16 bytes a lane (two bytes a lane straight to memory took 7K cycles of 16K)
+        group_sync();
+        uint4* o = reinterpret_cast<uint4*>(p.out + orow * DV);
+        for (int x = st; x < hv * (DV / 8); x += kSoftThreads) __stcs(o + x, reinterpret_cast<const uint4*>(row16)[x]);
       }
       dsa::tc_fence_before();
     }
@@ -657,32 +642,39 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   __syncwarp();
   if (p.splits > 1) {
     // Joins the splits: with M the largest reference, out = sum_s 2^(m_s - M) O_s / z.
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     const int dims = DV / p.splits, quads = dims / 4, d0 = split * dims;
     const uint32_t stats_at = dsa::smem_u32(stats), part_at = dsa::smem_u32(part);
-    for (int x = threadIdx.x; x < hv * quads; x += kThreads) {
+    for (int x = threadIdx.x; x < (dead ? 0 : hv * quads); x += kThreads) {
       const int h = x / quads, d = d0 + (x - h * quads) * 4;
-      float4 sm[kMaxCluster];
-      float M = -INFINITY, mx = -INFINITY, l = 0.f;
+      float4 sm[kMaxCluster], o[kMaxCluster];
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) {
-        sm[s] = s < p.splits ? ld_cluster(of_rank(stats_at + h * 16, s)) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (sm[s].y != 0.f) M = fmaxf(M, sm[s].x), mx = fmaxf(mx, sm[s].z);
+        if (s < p.splits) {
+          sm[s] = ld_cluster(of_rank(stats_at + h * 16, s));
+          o[s] = ld_cluster(of_rank(part_at + (h * DV + d) * 4, s));
+        } else {
+          sm[s] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        }
       }
+      float M = -INFINITY, mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s)
+        if (sm[s].y != 0.f) M = fmaxf(M, sm[s].x), mx = fmaxf(mx, sm[s].z);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) {
-        if (sm[s].y == 0.f) continue;  // a split without a valid slot
+        if (sm[s].y == 0.f) continue;  // a split without a valid slot: it may have left no sums
         const float a = exp2f(sm[s].x - M);
-        const float4 v = ld_cluster(of_rank(part_at + (h * DV + d) * 4, s));
         l = fmaf(sm[s].y, a, l);
-        acc.x = fmaf(a, v.x, acc.x), acc.y = fmaf(a, v.y, acc.y), acc.z = fmaf(a, v.z, acc.z), acc.w = fmaf(a, v.w, acc.w);
+        acc.x = fmaf(a, o[s].x, acc.x), acc.y = fmaf(a, o[s].y, acc.y), acc.z = fmaf(a, o[s].z, acc.z), acc.w = fmaf(a, o[s].w, acc.w);
       }
-      const Norm n = norm_of(M, l, p.sink ? __ldg(p.sink + h0 + h) : -INFINITY);
-      const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc.x * n.f, acc.y * n.f),
-                           o1 = __floats2bfloat162_rn(acc.z * n.f, acc.w * n.f);
+      const Norm n = norm_of(M, l, sm[0].w);
+      const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * n.f, acc.y * n.f),
+                           r1 = __floats2bfloat162_rn(acc.z * n.f, acc.w * n.f);
       *reinterpret_cast<uint2*>(p.out + (orow + h) * DV + d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+          make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
       if (d == 0) {
         p.lse[orow + h] = n.lse;
         if (p.lse_kv) p.lse_kv[orow + h] = n.lse_kv;
@@ -690,13 +682,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       }
     }
   }
+  if (p.splits > 1) cluster_arrive();  // this thread has read the others' sums
   __syncwarp();
   __syncthreads();
   if (warp == kMmaWarp && aligned) {
     dsa::tc_fence_after();
     dsa::tmem_dealloc(tmem_base, S::kTmem);
   }
-  if (p.splits > 1) cluster_sync();  // the others have read this CTA's sums
+  if (p.splits > 1) cluster_wait();
 }
 
 int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * ((H / Hc + kHG - 1) / kHG); }
@@ -739,7 +732,7 @@ int launch_form(const Params& p, cudaStream_t stream) {
   attr.val.clusterDim.x = p.splits;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return dsa::launch_error("attn_kv8_narrow_kernel");
   return DSA_OK;
 }

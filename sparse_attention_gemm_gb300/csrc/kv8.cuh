@@ -53,6 +53,20 @@ __device__ __forceinline__ int kv8_seq(const int32_t* __restrict__ cu, int n_seq
   return lo;
 }
 
+// The same by a converged warp, 32 probes a step: a load's latency per factor of 32 in n_seqs.
+__device__ __forceinline__ int kv8_seq_warp(const int32_t* __restrict__ cu, int n_seqs, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_seqs;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at < n && __ldg(cu + lo + at) <= t);
+    const int k = le ? (31 - __clz(le)) * step : 0;
+    lo += k;
+    n = min(step, n - k);
+  }
+  return lo;
+}
+
 // Scale of values up to `amax` (>= 0, finite): 2^e with the smallest e that
 // keeps amax <= 448 * 2^e, at least 2^-126.  448 = 1.75 * 2^8, so e follows
 // from the exponent and from whether the significand exceeds 1.75.  Powers
