@@ -52,7 +52,8 @@ constexpr int kThreads = (kMma2Warp + 1) * 32;
 // 18 warps: 96 registers a thread; moving some from the gather and MMA warps
 // to the softmax ones (setmaxnreg) is not needed: no role is short of any in its loop.
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
-constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T
+constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T, 64 keys
+constexpr int kTile = 2 * kKeys;                  // keys per tile: M of the score product
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 0;    // S^T buffers at columns 0 and 128 (hi 64, lo 64)
 constexpr int kOCol = 256;  // O^T blocks at 256 + 64 m
@@ -68,25 +69,25 @@ struct Shape {
   static constexpr bool kTail = DQK % 128 != 0;
   static_assert(DQK % 128 == 0 || DQK % 128 == 64, "tail of 64 codes");
   static constexpr int kNv = DV / 128;
-  static constexpr uint32_t kVOff = SEP ? kFull * kChunkBytes : 0;  // V inside a tile buffer
-  static constexpr uint32_t kTailOff = kFull * kChunkBytes;
-  static constexpr uint32_t kBuf = (kFull + (SEP ? kNv : 0)) * kChunkBytes + (kTail ? kKeys * 64 : 0);
-  static constexpr int kStages = SEP ? 5 : 4;
+  static constexpr uint32_t kVOff = SEP ? kFull * 2 * kChunkBytes : 0;  // V inside a tile buffer
+  static constexpr uint32_t kTailOff = kFull * 2 * kChunkBytes;
+  static constexpr uint32_t kBuf = 2 * ((kFull + (SEP ? kNv : 0)) * kChunkBytes + (kTail ? kKeys * 64 : 0));
   static constexpr uint32_t kQTail = kFull * kQChunkBytes;
   static constexpr uint32_t kQBytes = kQTail + (kTail ? 2 * kHG * 64 : 0);
-  static constexpr uint32_t kKv = kQBytes;
-  static constexpr uint32_t kPLo = kKv + kStages * kBuf;               // [2]
-  static constexpr uint32_t kPHi = kTail ? kKv + kTailOff : kPLo + 2 * kPPart;  // stage by stage, or [2]
-  static constexpr uint32_t kPHiStep = kTail ? kBuf : kPPart;
-  // key and value scale of each slot of a stage (one number where they are one); -1: no slot
+  static constexpr uint32_t kKv = kQBytes;                          // [2] tiles
+  static constexpr uint32_t kPLo = kKv + 2 * kBuf;                  // [2] halves of a tile
+  static constexpr uint32_t kPHi = kTail ? kKv + kTailOff : kPLo + 2 * kPPart;  // [2] halves; of each tile buffer, or
+  static constexpr uint32_t kPHiStep = kTail ? kBuf : 0;                        // of the one in turn
+  // scale of each slot's key and, behind them, value (one number where they are one), per half of a tile; 0: no slot
   static constexpr uint32_t kMeta = kPLo + (kTail ? 2 : 4) * kPPart;
   static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
-  static constexpr uint32_t kWmax = kMeta + kStages * kMetaStep;       // float [4][64]
+  static constexpr uint32_t kWmax = kMeta + 4 * kMetaStep;             // float [4][64]
   static constexpr uint32_t kAlpha = kWmax + 1024;                     // float [64]
-  static constexpr uint32_t kQexp = kAlpha + 256;                      // uint8 [3][64]
+  static constexpr uint32_t kFac = kAlpha + 256;                       // float [64]
+  static constexpr uint32_t kQexp = kFac + 256;                        // uint8 [3][64]
   static constexpr uint32_t kSvm = kQexp + 192;                        // float [4]
   static constexpr uint32_t kBars = kSvm + 16;
-  static constexpr uint32_t kMisc = kBars + 24 * 8;
+  static constexpr uint32_t kMisc = kBars + 20 * 8;
   static constexpr uint32_t kTotal = kMisc + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
   static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kPLo % 1024 == 0, "alignment");
@@ -122,6 +123,12 @@ __device__ __forceinline__ float fold8(float (&v)[8], int lane, F f) {
   return v[0];
 }
 
+// Index of a thread's score of its key k (0..3) and head h (0..7), and the largest of a head's.
+__device__ __forceinline__ constexpr int at(int k, int h) { return 16 * (k >> 1) + 4 * (h >> 1) + 2 * (k & 1) + (h & 1); }
+__device__ __forceinline__ float most_of(const float (&x)[32], int h) {
+  return fmaxf(fmaxf(x[at(0, h)], x[at(1, h)]), fmaxf(x[at(2, h)], x[at(3, h)]));
+}
+
 // One work item: the tiles [i0, i1) of row t.
 struct Item {
   int t, kvh, h0, hv;  // first query head and how many of the group's are real
@@ -148,9 +155,9 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
     len = len < 0 ? 0 : (len > p.K ? p.K : len);
   }
   if (w.dead) len = 0;
-  const int nt = (len + kKeys - 1) / kKeys;
+  const int nt = (len + kTile - 1) / kTile;
   w.len = len;
-  // (nt <= 2^25 and at most 32 splits: the products fit)
+  // (nt <= 2^24 and at most 32 splits: the products fit)
   w.i0 = static_cast<int>(static_cast<uint32_t>(nt) * static_cast<uint32_t>(w.split) / static_cast<uint32_t>(p.splits));
   w.i1 = static_cast<int>(static_cast<uint32_t>(nt) * static_cast<uint32_t>(w.split + 1) / static_cast<uint32_t>(p.splits));
   return w;
@@ -160,7 +167,6 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
 template <int DQK, int DV, bool SEP, bool kMax>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   using S = Shape<DQK, DV, SEP>;
-  constexpr int ST = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];  // the kernel has no other shared memory
   if (dsa::smem_u32(smem) & 1023u) {                 // would break every swizzle
     if (threadIdx.x == 0) atomicOr(p.status, DSA_STATUS_CHECK_FAILED);
@@ -173,31 +179,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   uint8_t* qexp = smem + S::kQexp;                        // [3][64]
   float* svm = reinterpret_cast<float*>(smem + S::kSvm);  // [4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  uint64_t* kv_full = bars;        // [5]
-  uint64_t* kv_empty = bars + 5;   // [5]
-  uint64_t* s_full = bars + 10;    // [2]
-  uint64_t* s_empty = bars + 12;   // [2]
-  uint64_t* p_full = bars + 14;    // [2]
-  uint64_t* p_empty = bars + 16;   // [2]: MMA2 of the tile has run
-  uint64_t* q_full = bars + 18;
-  uint64_t* q_empty = bars + 19;
-  uint64_t* drain = bars + 20;     // [2]: the MMA issuers' exit commits
+  uint64_t* kv_full = bars;        // [4]: halves of the two tile buffers
+  uint64_t* kv_empty = bars + 4;   // [4]
+  uint64_t* s_full = bars + 8;     // [2]
+  uint64_t* s_empty = bars + 10;   // [2]
+  uint64_t* p_empty = bars + 12;   // [2]: MMA2 of the half of a tile has run
+  uint64_t* drain = bars + 14;     // [2]: the MMA issuers' exit commits
+  uint64_t* p_full = bars + 16;    // of the whole tile: its first half's products already meet rescaled sums
+  uint64_t* q_full = bars + 17;
+  uint64_t* q_empty = bars + 18;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < ST; ++b) {
-      dsa::mbar_init(&kv_full[b], kGatherWarps);
+    for (int b = 0; b < 4; ++b) {
+      dsa::mbar_init(&kv_full[b], kGatherThreads);
       dsa::mbar_init(&kv_empty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
       dsa::mbar_init(&s_full[b], 1);
       dsa::mbar_init(&s_empty[b], kSoftWarps);
-      dsa::mbar_init(&p_full[b], kSoftWarps);
       dsa::mbar_init(&p_empty[b], 1);
       dsa::mbar_init(&drain[b], 1);
     }
+    dsa::mbar_init(p_full, kSoftWarps);
     dsa::mbar_init(q_full, kGatherWarps);
     dsa::mbar_init(q_empty, 1);
     *abort_flag = 0;
@@ -217,61 +223,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // every chunk.  A row's place depends on its id and the block table: ids
     // are read two tiles ahead, the table one tile ahead.
     const int gt = threadIdx.x, piece = gt & 7;
-    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv;
-    int tile_ctr = 0, item_ctr = 0;
-    int pend = -1;  // stage whose copies are in flight
-    float psk[kGatherSteps], psv[kGatherSteps];  // and its keys' scales
+    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv, meta_addr = dsa::smem_u32(smem) + S::kMeta;
+    int half_ctr = 0, item_ctr = 0;  // (here a unit of work is half a tile)
     bool ok = true;
-    auto signal = [&](int stage) {
-      if (piece == 0) {
-#pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) {
-          const int key = kg * kGatherKeys + (gt >> 3);
-          if (SEP)
-            reinterpret_cast<float2*>(smem + S::kMeta + stage * S::kMetaStep)[key] = make_float2(psk[kg], psv[kg]);
-          else
-            reinterpret_cast<float*>(smem + S::kMeta + stage * S::kMetaStep)[key] = psk[kg];
-        }
-      }
-      dsa::fence_proxy_async_smem();  // the copies, before the tensor core reads them
-      __syncwarp();
-      if (lane == 0) dsa::mbar_arrive(&kv_full[stage]);
-    };
-    // The query.  A warp loads and converts eight heads: a unit pair (hi, lo) of
-    // the operand's rows is as large as the 16 bf16 values it is made of, so
-    // they land there (a warp instruction copies 512 consecutive bytes) and
-    // are converted in place, four threads per head, units sub, sub + 4, ...
-    // Odd heads take the halves of a 128-byte row in the other order: eight
-    // lanes then touch all banks once.
+    // The query: eight heads a warp, four threads a head, units (16 values)
+    // sub, sub + 4, ...; odd heads take the halves of a 128-byte row in the
+    // other order, so that eight lanes touch all banks once.  It is read twice,
+    // for the head's largest element while the item before still uses the
+    // operand, and for the terms: between the two items' scores stand only the
+    // conversions and what of the loads they do not hide.
     const int hq = gt >> 2, sub = gt & 3;
+    constexpr int kUnits = DQK / 64;
+    constexpr int kAhead = 3;  // units loaded ahead of the one converted
     // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
     // which gives each softmax thread eight consecutive heads
-    auto row_of = [](int h) { return (h & 32) + ((h & 6) << 2) + ((h >> 2) & 6) + (h & 1); };
-    auto q_addr = [](int r, int u) {
-      return u < S::kFull * 8 ? (u >> 3) * kQChunkBytes + dsa::sw128_offset(r, (u & 7) * 16)
-                              : S::kQTail + sw64_offset(r, u - S::kFull * 8);
-    };
-    auto q_unit = [&](int k, int lo) {
-      return q_addr(row_of(hq) + lo * kHG, (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0));
-    };
-    auto send_query = [&](const Item& w) {
-      constexpr int kPieces = DQK / 8;  // of 16 bytes, per head
-      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
-      const uint32_t qa = dsa::smem_u32(smem);
-#pragma unroll 6
-      for (int k = 0; k < 8 * kPieces / 32; ++k) {
-        const int x = k * 32 + lane, h = warp * 8 + x / kPieces, c = x % kPieces;
-        const bool real = h < w.hv;
-        cp_async16(qa + q_addr(row_of(h) + (c & 1) * kHG, c >> 1), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u);
-      }
-      cp_async_commit();
-    };
+    const int qrow = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
+    auto unit_of = [&](int k) { return (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0); };
     auto convert_query = [&](const Item& w, int n_item) {
+      const bool real = hq < w.hv;
+      // (a padding head: any)
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK);
       uint32_t m = 0;
 #pragma unroll 3
-      for (int k = 0; k < DQK / 64; ++k) {
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(k, 0)), m);
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(smem + q_unit(k, 1)), m);
+      for (int k = 0; k < kUnits; ++k) {
+        const int u = unit_of(k);
+        const uint4 v0 = __ldg(src + 2 * u), v1 = __ldg(src + 2 * u + 1);
+        m = dsa::amax_bf16x8(v1, dsa::amax_bf16x8(v0, m));
       }
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
@@ -279,30 +256,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const bool finite = m < 0x7F80u;
       const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
       const float inv = dsa::pow2_inverse(s);
+      uint4 v[kAhead + 1][2];
+      auto load = [&](int k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[k % (kAhead + 1)][e] = __ldg(src + 2 * unit_of(k) + e);
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) load(k);
+      if (!dsa::mbar_wait_warp(q_empty, (n_item & 1) ^ 1, wt)) return false;
       if (sub == 0) qexp[(n_item % 3) * 64 + hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
-      // (rows of padding heads are zeros in either form)
-#pragma unroll 3
-      for (int k = 0; k < DQK / 64; ++k) {
-        if (hq >= w.hv) break;
-        uint4* at[2] = {reinterpret_cast<uint4*>(smem + q_unit(k, 0)),
-                        reinterpret_cast<uint4*>(smem + q_unit(k, 1))};
-        const uint4 v0 = *at[0], v1 = *at[1];
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        if (k + kAhead < kUnits) load(k + kAhead);
+        const int u = unit_of(k);
+        const uint4 v0 = v[k % (kAhead + 1)][0], v1 = v[k % (kAhead + 1)][1];
         const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int j = 0; j < 4; ++j) {
           uint16_t h2[2], l2[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) split_query(wd[2 * n + e], inv, h2[e], l2[e]);
-          hi[n] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
-          lo[n] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
+          for (int e = 0; e < 2; ++e) split_query(real ? wd[2 * j + e] : 0, inv, h2[e], l2[e]);
+          hi[j] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
+          lo[j] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
         }
-        *at[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *at[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const bool tail = k >= S::kFull * 2;
+        const uint32_t at = tail ? S::kQTail + sw64_offset(qrow, u - S::kFull * 8)
+                                 : (u >> 3) * kQChunkBytes + dsa::sw128_offset(qrow, (u & 7) * 16);
+        // (64 rows on leaves either swizzle's phase as it is)
+        *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + at + kHG * (tail ? 64 : 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       dsa::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) dsa::mbar_arrive(q_full);
+      return true;
     };
     // L2 prefetch of a later item's query and ids
     auto prefetch_item = [&](int it) {
@@ -311,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       if (w.i0 >= w.i1) return;
       const uint8_t* q0 = reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK);
       for (int o = gt * 128; o < w.hv * DQK * 2; o += kGatherThreads * 128) l2_prefetch(q0 + o);
-      const int j = w.i0 * kKeys + gt * 32;
-      if (j < min(w.i1 * kKeys, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
+      const int j = w.i0 * kTile + gt * 32;
+      if (j < min(w.i1 * kTile, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
     };
     for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
       const Item w = get_item(p, it, t_end);
@@ -321,11 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
       auto load_id = [&](int i, int kg) {
         const int j = i * kKeys + kg * kGatherKeys + (gt >> 3);
-        return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
+        return j < w.len ? __ldg(irow + j) : -1;
       };
-      // the query first where its buffer is free already (a CTA's first item)
-      const bool q_sent = __all_sync(0xffffffffu, dsa::mbar_test_wait(q_empty, (item_ctr & 1) ^ 1));
-      if (q_sent) send_query(w);
       const int32_t* trow = p.g.table ? p.g.table + static_cast<int64_t>(b) * p.g.max_blocks : nullptr;
       auto load_block = [&](int id) {  // as the table holds it; -1 beyond the table
         const int page = id >> p.g.lb;
@@ -336,12 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
 #pragma unroll
       for (int kg = 0; kg < kGatherSteps; ++kg) {
-        nid[kg] = load_id(w.i0 + 1, kg);
-        id[kg] = load_id(w.i0, kg);
+        nid[kg] = load_id(2 * w.i0 + 1, kg);
+        id[kg] = load_id(2 * w.i0, kg);
         blk[kg] = load_block(id[kg]);
       }
-      for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-        const int stage = tile_ctr % ST;
+      // The query comes behind the first tile's copies, whose buffer does not
+      // wait for it; a CTA's first query behind those of half of it.
+      const int q_at = 2 * w.i0 + (item_ctr == 0 ? 0 : 1);
+      for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
+        const int stage = half_ctr & 3;
         int cur[kGatherSteps];
 #pragma unroll
         for (int kg = 0; kg < kGatherSteps; ++kg) {
@@ -350,29 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
                         : -1;
           id[kg] = nid[kg];
           blk[kg] = load_block(nid[kg]);
-          nid[kg] = load_id(i + 2, kg);
+          nid[kg] = i + 2 < 2 * w.i1 ? load_id(i + 2, kg) : -1;
         }
-        const uint32_t ph = ((tile_ctr / ST) & 1) ^ 1;
-        if (pend >= 0 && !__all_sync(0xffffffffu, dsa::mbar_test_wait(&kv_empty[stage], ph))) {
-          // no free buffer: do not hold back the tile that may have landed
-          cp_async_wait<0>();
-          signal(pend);
-          pend = -1;
-        }
-        if (!dsa::mbar_wait_warp(&kv_empty[stage], ph, wt)) {
+        if (!dsa::mbar_wait_warp(&kv_empty[stage], ((half_ctr >> 2) & 1) ^ 1, wt)) {
           ok = false;
           break;
         }
-        const uint32_t buf = kv_addr + stage * S::kBuf;
-        float nsk[kGatherSteps], nsv[kGatherSteps];
-#pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) {
-          nsk[kg] = nsv[kg] = -1.f;
-          if (piece == 0 && cur[kg] >= 0) {
-            const int64_t at = static_cast<int64_t>(cur[kg] >> p.g.lb) * p.Hc + w.kvh;
-            nsk[kg] = __ldg(p.k_scale + at);
-            if (SEP) nsv[kg] = __ldg(p.v_scale + at);
-          }
+        const uint32_t buf = kv_addr + (stage >> 1) * S::kBuf, half = stage & 1;
+        {
+          // the scales: lanes of even and odd pieces take the two keys' (with V, those of pieces 2, 3, 6, 7 the value's)
+          const int r = piece & 1 ? cur[1] : cur[0];
+          const int64_t at = static_cast<int64_t>((r >= 0 ? r : 0) >> p.g.lb) * p.Hc + w.kvh;
+          const bool value = SEP && (piece & 2);
+          if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
+            cp_async4(meta_addr + stage * S::kMetaStep + (value ? kKeys * 4 : 0) + ((piece & 1) * kGatherKeys + (gt >> 3)) * 4,
+                      (value ? p.v_scale : p.k_scale) + at, r >= 0 ? 4u : 0u);
         }
 #pragma unroll
         for (int kg = 0; kg < kGatherSteps; ++kg) {
@@ -382,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           // checked build: the row is inside the cache
           if (!dsa::check(cur[kg] < (p.g.n_blocks << p.g.lb), p.status)) continue;
           const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
-          const uint32_t dst = buf + dsa::sw128_offset(key, piece * 16);
+          const uint32_t dst = buf + half * kChunkBytes + dsa::sw128_offset(key, piece * 16);
 #pragma unroll
-          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * kChunkBytes, krow + c * 128, nbytes);
+          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * 2 * kChunkBytes, krow + c * 128, nbytes);
           if (SEP) {
             const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
 #pragma unroll
             for (int c = 0; c < S::kNv; ++c)
-              cp_async16(dst + S::kVOff + c * kChunkBytes, vrow + c * 128, nbytes);
+              cp_async16(dst + S::kVOff + c * 2 * kChunkBytes, vrow + c * 128, nbytes);
           }
         }
         if (S::kTail) {
@@ -398,77 +378,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           const int key = (second ? kGatherKeys : 0) + (gt >> 3), r = second ? cur[1] : cur[0];
           const int64_t rh = static_cast<int64_t>(r >= 0 ? r : 0) * p.Hc + w.kvh;
           if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
-            cp_async16(buf + S::kTailOff + sw64_offset(key, piece & 3), p.k8 + rh * DQK + S::kFull * 128 + (piece & 3) * 16,
+            cp_async16(buf + S::kTailOff + half * (kKeys * 64) + sw64_offset(key, piece & 3), p.k8 + rh * DQK + S::kFull * 128 + (piece & 3) * 16,
                        r >= 0 ? 16u : 0u);
         }
-        cp_async_commit();
-        if (pend >= 0) {
-          cp_async_wait<1>();
-          signal(pend);
-        }
-        pend = stage;
-#pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) psk[kg] = nsk[kg], psv[kg] = nsv[kg];
-        if (i == w.i0) {
-          if (!q_sent) {
-            // MMA1 of the item before must have run: its tiles (and this one,
-            // so that nothing waits for it later) are signalled first
-            cp_async_wait<0>();
-            signal(pend);
-            pend = -1;
-            if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) {
-              ok = false;
-              break;
-            }
-            send_query(w);
+        cp_async_arrive(&kv_full[stage]);
+        if (i == q_at) {
+          if (!convert_query(w, item_ctr)) {
+            ok = false;
+            break;
           }
-          cp_async_wait<0>();
-          __syncwarp();
-          if (pend >= 0) signal(pend);
-          pend = -1;
-          convert_query(w, item_ctr);
           ++item_ctr;
           prefetch_item(it + gridDim.x);
         }
       }
     }
-    cp_async_wait<0>();  // nothing of this thread is in flight when it leaves
-    if (pend >= 0) signal(pend);
+    cp_async_wait_all();  // nothing of this thread is in flight when it leaves
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // Two warps, one per product, each converged with one elected issuer.
     const bool leader = elect_sync();
     const uint32_t base = dsa::smem_u32(smem);
-    int tile_ctr = 0;
     bool ok = true;
     if (warp == kMmaWarp) {
-      constexpr uint32_t idesc1 = dsa::idesc_e4m3(kKeys, 2 * kHG);
+      constexpr uint32_t idesc1 = dsa::idesc_e4m3(kTile, 2 * kHG);
       const uint64_t q_desc = dsa::smem_desc(base, 16, 1024, dsa::kSwizzle128B);
       const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
       const uint64_t qt_desc = dsa::smem_desc(base + S::kQTail, 16, 512, dsa::kSwizzle64B);
       const uint64_t kt_desc = dsa::smem_desc(base + S::kKv + S::kTailOff, 16, 512, dsa::kSwizzle64B);
-      int item_ctr = 0;
+      int tile_ctr = 0, item_ctr = 0;
       for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
         const Item w = get_item(p, it, t_end);
         if (w.i0 >= w.i1) continue;
         if (!dsa::mbar_wait_warp(q_full, item_ctr & 1, wt)) break;
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-          const int b = tile_ctr & 1, stage = tile_ctr % ST;
-          const bool got = dsa::mbar_wait(&s_empty[b], ((tile_ctr >> 1) & 1) ^ 1, wt) &&
-                           dsa::mbar_wait(&kv_full[stage], (tile_ctr / ST) & 1, wt);
+          const int b = tile_ctr & 1;  // of the tile buffers and of those of S^T
+          const uint32_t par = (tile_ctr >> 1) & 1;
+          const bool got = dsa::mbar_wait(&s_empty[b], par ^ 1, wt) && dsa::mbar_wait(&kv_full[2 * b], par, wt) &&
+                           dsa::mbar_wait(&kv_full[2 * b + 1], par, wt);
+          // the gathered codes, before the tensor core reads them (MMA2's come
+          // with the softmax warps' arrival, behind a fence of theirs)
+          dsa::fence_proxy_async_smem();
           __syncwarp();
           dsa::tc_fence_after();
-          const uint64_t a0 = kv_desc + stage * (S::kBuf >> 4);
+          const uint64_t a0 = kv_desc + b * (S::kBuf >> 4);
           const uint32_t d = tmem_base + kSCol + b * 128;
 #pragma unroll
           for (int c = 0; c < S::kFull; ++c) {
-            const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
+            const uint64_t ac = a0 + c * (2 * kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               dsa::umma_f8_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
           }
           if (S::kTail) {
-            const uint64_t at = kt_desc + stage * (S::kBuf >> 4);
+            const uint64_t at = kt_desc + b * (S::kBuf >> 4);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) dsa::umma_f8_if(leader && got, d, at + kk * 2, qt_desc + kk * 2, idesc1, 1u);
           }
@@ -487,33 +449,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       __syncwarp();
     } else {
       constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kHG) | (1u << 15) | (1u << 16);  // both MN-major
-      const uint64_t v_desc =
-          dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
+      int half_ctr = 0;
+      const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, 2 * kChunkBytes, 1024, dsa::kSwizzle128B);
       // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
       const uint64_t ph_desc = dsa::smem_desc(base + S::kPHi, kPPart, 512, dsa::kSwizzle64B);
       const uint64_t pl_desc = dsa::smem_desc(base + S::kPLo, kPPart, 512, dsa::kSwizzle64B);
       for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
         const Item w = get_item(p, it, t_end);
-        for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-          const int b = tile_ctr & 1, stage = tile_ctr % ST;
-          const bool got = dsa::mbar_wait(&p_full[b], (tile_ctr >> 1) & 1, wt);
+        for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
+          const int half = half_ctr & 1, b = (half_ctr >> 1) & 1;
+          const bool got = half == 1 || dsa::mbar_wait(p_full, b, wt);
           __syncwarp();
           dsa::tc_fence_after();
-          const uint64_t a0 = v_desc + stage * (S::kBuf >> 4);
-          const uint64_t bh = ph_desc + (S::kTail ? stage : b) * (S::kPHiStep >> 4), bl = pl_desc + b * (kPPart >> 4);
+          const uint64_t a0 = v_desc + b * (S::kBuf >> 4) + half * (kChunkBytes >> 4);
+          const uint64_t bh = ph_desc + b * (S::kPHiStep >> 4) + half * (kPPart >> 4), bl = pl_desc + half * (kPPart >> 4);
 #pragma unroll
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t d = tmem_base + kOCol + mb * kHG;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 32; ++kk) {
-              const uint64_t a = a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4);
-              dsa::umma_f8_if(leader && got, d, a, bh + kk * (32 * kHG >> 4), idesc2, (i > w.i0 || kk > 0) ? 1u : 0u);
+              const uint64_t a = a0 + mb * (2 * kChunkBytes >> 4) + kk * (32 * 128 >> 4);
+              dsa::umma_f8_if(leader && got, d, a, bh + kk * (32 * kHG >> 4), idesc2, (i > 2 * w.i0 || kk > 0) ? 1u : 0u);
               dsa::umma_f8_if(leader && got, d, a, bl + kk * (32 * kHG >> 4), idesc2, 1u);
             }
           }
           if (leader && got) {
-            dsa::umma_commit(&p_empty[b]);
-            dsa::umma_commit(&kv_empty[stage]);
+            dsa::umma_commit(&p_empty[half]);
+            dsa::umma_commit(&kv_empty[half_ctr & 3]);
           }
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
@@ -531,8 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const int quarter = warp & 3;  // TMEM lane quarter
     const int hh = sw >> 2;        // head half
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // S^T registers 4j + e (key kA) and 4j + 2 + e (key kB) hold head hb + 2j + e
-    const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
+    // Of S^T a thread holds four keys' scores of eight heads: key k of them is
+    // row key0 + 8 k of its half of the tile, head hb + 2j + e of it is x[16 (k / 2) + 4j + 2 (k % 2) + e]
+    const int half = quarter >> 1, key0 = (quarter & 1) * 32 + (lane >> 2);
     const int hb = hh * 32 + 8 * (lane & 3);
     // factors of O^T per head (the four warps of a head half write the same ones)
     float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
@@ -540,17 +503,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     float* red = reinterpret_cast<float*>(smem + S::kPLo);  // [4][64] sums
     float* redm = red + 256;                                // [4][64] maxima
     float* mref = redm + 256;                               // [64]
-    float* fac = mref + 64;                                 // [64]
+    float* fac = reinterpret_cast<float*>(smem + S::kFac);  // [64]
+    uint8_t* rows = smem + S::kPLo + sw * 1024;             // this warp's: 16 heads x 32 dims of the result
     int tile_ctr = 0, item_ctr = 0;
     bool ok = true;
     // A wait of this thread gave up: the eight warps leave together, at a
     // point that reduces the flag (see the bf16 kernel).
     bool failed = false;
+    Item next = get_item(p, blockIdx.x, t_end);
     for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
-      const Item w = get_item(p, it, t_end);
+      const Item w = next;
+      const bool empty = w.dead || w.i0 >= w.i1;
+      if (empty && it + gridDim.x < p.n_items) next = get_item(p, it + gridDim.x, t_end);
       if (w.dead) continue;
       const int64_t orow = static_cast<int64_t>(w.t) * p.H + w.h0;
-      if (w.i0 >= w.i1) {
+      if (empty) {
         if (p.splits > 1) {
           if (st < w.hv) p.part_s[(orow + st) * p.splits + w.split] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
         } else {
@@ -576,34 +543,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (kMax) top[h] = -INFINITY;
       }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-        const int b = tile_ctr & 1;
+        const int b = tile_ctr & 1, stage = 2 * b + half;
         const uint32_t par = (tile_ctr >> 1) & 1;
-        const int stage = tile_ctr % ST;
         // the slots' scales come with the gathered tile
-        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (tile_ctr / ST) & 1, wt);
-        float skA, skB, svA, svB;
-        if (SEP) {
-          const float2* meta = reinterpret_cast<const float2*>(smem + S::kMeta + stage * S::kMetaStep);
-          const float2 ma = meta[kA], mb = meta[kB];
-          skA = ma.x, svA = ma.y, skB = mb.x, svB = mb.y;
-        } else {
-          const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
-          svA = skA = meta[kA];
-          svB = skB = meta[kB];
-        }
-        const bool vA = skA > 0.f, vB = skB > 0.f;
+        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], par, wt);
+        const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep) + key0;
+        float sk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sk[k] = meta[8 * k] > 0.f ? meta[8 * k] : 0.f;
         if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
         __syncwarp();
         dsa::tc_fence_after();
-        float x[16];
-        {
+        float x[32];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
           uint32_t v[16], lo[16];
-          const uint32_t ta = tmem_base + lane_off + kSCol + b * 128 + hh * 32;
+          const uint32_t ta = tmem_base + lane_off + (static_cast<uint32_t>(g * 16) << 16) + kSCol + b * 128 + hh * 32;
           dsa::tmem_ld16x256b_x4(ta, v);
           dsa::tmem_ld16x256b_x4(ta + 64, lo);
           dsa::tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
+          for (int r = 0; r < 16; ++r) x[16 * g + r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
         }
         if (i == w.i0) {
           const uint8_t* e = qexp + (item_ctr % 3) * 64 + hb;
@@ -617,40 +577,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
         // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int k = 0; k < 4; ++k) {
+          const bool valid = sk[k] > 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int h = 2 * j + e;
-            x[4 * j + e] = fmaf(x[4 * j + e], qs[h] * skA, -m[h]);
-            x[4 * j + 2 + e] = fmaf(x[4 * j + 2 + e], qs[h] * skB, -m[h]);
+          for (int h = 0; h < 8; ++h) {
+            float& s = x[at(k, h)];
+            s = valid ? fmaf(s, qs[h] * sk[k], -m[h]) : -INFINITY;
           }
         }
-        if (!vA) {
-          svA = 0.f;
+        float most = x[0], sv_most = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[4 * j] = x[4 * j + 1] = -INFINITY;
+        for (int r = 1; r < 32; ++r) most = fmaxf(most, x[r]);
+        if (SEP) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sk[k] = sk[k] > 0.f ? meta[kKeys + 8 * k] : 0.f;  // from here on the values' scales
         }
-        if (!vB) {
-          svB = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[4 * j + 2] = x[4 * j + 3] = -INFINITY;
-        }
-        float most = x[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) most = fmaxf(most, x[r]);
-        const bool ex = unset || most > kTheta || svA > ref || svB > ref;
+        for (int k = 0; k < 4; ++k) sv_most = fmaxf(sv_most, sk[k]);
+        const bool ex = unset || most > kTheta || sv_most > ref;
         if constexpr (kMax) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              top[2 * j + e] = fmaxf(top[2 * j + e], fmaxf(x[4 * j + e], x[4 * j + 2 + e]) + m[2 * j + e]);
-          }
+          for (int h = 0; h < 8; ++h) top[h] = fmaxf(top[h], most_of(x, h) + m[h]);
         }
         const bool first = i == w.i0;
         bool need_rescale = false;
         float ratio = 1.f;  // of the old to the new 2^E
-        if (group_any(ex || failed)) {
+        if (first || group_any(ex || failed)) {
           if (group_any(failed)) {  // the group leaves together
             ok = false;
             break;
@@ -658,14 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           // move the references: the tile's maximum per head over its 64 keys
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[2 * j] = fmaxf(x[4 * j], x[4 * j + 2]);
-            v[2 * j + 1] = fmaxf(x[4 * j + 1], x[4 * j + 3]);
-          }
+          for (int h = 0; h < 8; ++h) v[h] = most_of(x, h);
           const float mx = fold8(v, lane, [](float a, float c) { return fmaxf(a, c); });
           wmax[quarter * 64 + hb + own_head(lane)] = mx;
-          float sv = fmaxf(svA, svB);
-          sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 4));
+          float sv = fmaxf(sv_most, __shfl_xor_sync(0xffffffffu, sv_most, 4));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
           if (lane == 0 && hh == 0) svm[quarter] = sv;
@@ -686,49 +634,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             }
             const float tm[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int h = 4 * g4 + k;
+            for (int n = 0; n < 4; ++n) {
+              const int h = 4 * g4 + n;
               // by how much the reference moves: to the tile's maximum, if that
               // passes it by kTheta or is the first
-              const float up = (unset ? tm[k] > -INFINITY : tm[k] > kTheta) ? tm[k] : 0.f;
+              const float up = (unset ? tm[n] > -INFINITY : tm[n] > kTheta) ? tm[n] : 0.f;
               const float a = unset ? 1.f : ex2(-up);
               moved |= up != 0.f;
               l_part[h] *= a;
               m[h] += up;
-              x[4 * (h >> 1) + (h & 1)] -= up;
-              x[4 * (h >> 1) + 2 + (h & 1)] -= up;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[at(k, h)] -= up;
               if (lane < 4) alpha[hb + h] = a * ratio;
             }
           }
           unset = unset && !(sv_max > 0.f);
           need_rescale = __any_sync(0xffffffffu, moved) && !first;
         }
-        // P^T rows kA and kB, both terms: the thread's eight heads are bytes hb .. hb + 7 of the 64-byte rows
-        if (!failed) failed = !dsa::mbar_wait(&p_empty[b], par ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
+        // P^T rows key0 + 8 k, both terms: the thread's eight heads are bytes hb .. hb + 7 of the 64-byte rows
+        if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr & 1) ^ 1, wt);  // MMA2 of the tile before has read it
         {
-          uint8_t* ph = smem + S::kPHi + (S::kTail ? stage : b) * S::kPHiStep;
-          uint8_t* pl = smem + S::kPLo + b * kPPart;
-          const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
+          uint8_t* ph = smem + S::kPHi + b * S::kPHiStep + half * kPPart;
+          uint8_t* pl = smem + S::kPLo + half * kPPart;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int key = k ? kB : kA;
-            const float wk = k ? wB : wA;
+          for (int k = 0; k < 4; ++k) {
+            const float wk = sk[k] * inv * kWeight;  // (2^-E alone stays in range)
             uint16_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float p0 = ex2(x[4 * j + 2 * k]), p1 = ex2(x[4 * j + 2 * k + 1]);
+              const float p0 = ex2(x[at(k, 2 * j)]), p1 = ex2(x[at(k, 2 * j + 1)]);
               l_part[2 * j] += p0;
               l_part[2 * j + 1] += p1;
               split_weights(p0 * wk, p1 * wk, hi[j], lo[j]);
             }
-            const uint32_t at = sw64_offset(key, hb >> 4) + (hb & 8);
-            *reinterpret_cast<uint2*>(ph + at) = pack4(hi);
-            *reinterpret_cast<uint2*>(pl + at) = pack4(lo);
+            const uint32_t to = sw64_offset(key0 + 8 * k, hb >> 4) + (hb & 8);
+            *reinterpret_cast<uint2*>(ph + to) = pack4(hi);
+            *reinterpret_cast<uint2*>(pl + to) = pack4(lo);
           }
         }
         if (need_rescale) {
           // MMA2 of the previous tile must have landed before O^T is scaled
-          if (!failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((tile_ctr - 1) >> 1) & 1, wt);
+          if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr & 1) ^ 1, wt);
           __syncwarp();
           dsa::tc_fence_after();
           __syncwarp();  // alpha, written by four lanes of this warp
@@ -749,14 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         dsa::fence_proxy_async_smem();
         dsa::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dsa::mbar_arrive(&p_full[b]);
+        if (lane == 0) dsa::mbar_arrive(p_full);
       }
       if (!ok) break;
 
       // ---------------------------------------------------------- epilogue
+      if (it + gridDim.x < p.n_items) next = get_item(p, it + gridDim.x, t_end);
+      const float sink = p.sink && st < w.hv ? __ldg(p.sink + w.h0 + st) : -INFINITY;
       // O^T is complete with the last tile's MMA2 (each phase of p_empty has
       // been waited for in turn, so the parity names that tile)
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[(tile_ctr - 1) & 1], ((tile_ctr - 1) >> 1) & 1, wt);
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr - 1) & 1, wt);
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr - 1) & 1, wt);
       __syncwarp();
       dsa::tc_fence_after();
       if (quarter == 0 && lane < 4) {
@@ -777,7 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (p.splits > 1) {
           if (st < w.hv) p.part_s[(orow + st) * p.splits + w.split] = make_float4(mc, l, m_max, 0.f);
         } else {
-          const float sink = (p.sink && st < w.hv) ? __ldg(p.sink + w.h0 + st) : -INFINITY;
           const float sk = sink * kLog2e;
           float lse_v = sink, lkv = INFINITY;
           f = 0.f;
@@ -817,13 +765,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
               o += static_cast<int64_t>(p.splits) * DV;
             }
           } else {
-            // (two bytes a lane: exchanging values between lanes for wider
-            // stores made the kernel 2.5% slower, the shuffles cost more)
-            __nv_bfloat16* o = p.out + (orow + hh * 32) * DV + d + lane;
+            // through shared memory, 16 heads at a time: 64 consecutive bytes a
+            // head (two bytes a lane straight to memory: 7K cycles an item)
+            __nv_bfloat16* o = p.out + (orow + hh * 32 + (lane >> 2)) * DV + d + (lane & 3) * 8;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c < hcount) __stcs(o, __float2bfloat16_rn(__uint_as_float(v[c]) * f32[c]));
-              o += DV;
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) {
+                const float4 f4 = *reinterpret_cast<const float4*>(f32 + half * 16 + c);
+                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {  // (one conversion of two: they run at an eighth of the multiplies' rate)
+                  const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[half * 16 + c + e]) * f[e],
+                                                                 __uint_as_float(v[half * 16 + c + e + 1]) * f[e + 1]);
+                  reinterpret_cast<__nv_bfloat16*>(rows)[(c + e) * 32 + lane] = r.x;
+                  reinterpret_cast<__nv_bfloat16*>(rows)[(c + e + 1) * 32 + lane] = r.y;
+                }
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int c = half * 16 + k * 8;
+                if (c + (lane >> 2) < hcount)
+                  __stcs(reinterpret_cast<uint4*>(o + c * DV), reinterpret_cast<const uint4*>(rows)[k * 32 + lane]);
+              }
+              __syncwarp();
             }
           }
         }
@@ -900,7 +866,7 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
 constexpr int kItemTiles = 3, kJoinTiles = 3;
 
 int plan_splits(int64_t units, int K) {
-  const int nt = (K + kKeys - 1) / kKeys;
+  const int nt = (K + kTile - 1) / kTile;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxSplits && s <= nt; ++s) {
