@@ -499,12 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const int hb = hh * 32 + 8 * (lane & 3);
     // factors of O^T per head (the four warps of a head half write the same ones)
     float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
-    // epilogue scratch, in P^T's second term (free once MMA2 has run)
-    float* red = reinterpret_cast<float*>(smem + S::kPLo);  // [4][64] sums
-    float* redm = red + 256;                                // [4][64] maxima
-    float* mref = redm + 256;                               // [64]
-    float* fac = reinterpret_cast<float*>(smem + S::kFac);  // [64]
-    uint8_t* rows = smem + S::kPLo + sw * 1024;             // this warp's: 16 heads x 32 dims of the result
+    float* fac = reinterpret_cast<float*>(smem + S::kFac);  // [64]: references, then the factors of the result
+    uint8_t* rows = smem + S::kPLo + sw * 1024;             // this warp's, of the result: 16 heads x 32 dims, 64-byte swizzle
     int tile_ctr = 0, item_ctr = 0;
     bool ok = true;
     // A wait of this thread gave up: the eight warps leave together, at a
@@ -702,25 +698,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       // ---------------------------------------------------------- epilogue
       if (it + gridDim.x < p.n_items) next = get_item(p, it + gridDim.x, t_end);
       const float sink = p.sink && st < w.hv ? __ldg(p.sink + w.h0 + st) : -INFINITY;
-      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
-      // been waited for in turn, so the parity names that tile)
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr - 1) & 1, wt);
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr - 1) & 1, wt);
-      __syncwarp();
-      dsa::tc_fence_after();
+      // The sums' norm, while the last tile's MMA2 runs: over the four quarters
+      // in wmax, once everybody has read the last references there.
+      group_sync();
       if (quarter == 0 && lane < 4) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) mref[hb + h] = m[h];
+        for (int h = 0; h < 8; ++h) fac[hb + h] = m[h];
       }
-      red[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
-      if constexpr (kMax)
-        redm[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
+      wmax[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
       group_sync();
+      const float l = st < 64 ? wmax[st] + wmax[64 + st] + wmax[128 + st] + wmax[192 + st] : 0.f;
+      float m_max = 0.f;
+      if constexpr (kMax) {
+        group_sync();
+        wmax[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
+        group_sync();
+        if (st < 64) m_max = fmaxf(fmaxf(wmax[st], wmax[64 + st]), fmaxf(wmax[128 + st], wmax[192 + st]));
+      }
       const float unscale = ref * (1.f / kWeight);
       if (st < 64) {
-        const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
-        const float mc = mref[st];
-        const float m_max = kMax ? fmaxf(fmaxf(redm[st], redm[64 + st]), fmaxf(redm[128 + st], redm[192 + st])) : 0.f;
+        const float mc = fac[st];
         const bool any = l != 0.f;  // true for NaN too
         float f = unscale;
         if (p.splits > 1) {
@@ -745,51 +742,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         fac[st] = f;
       }
+      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
+      // been waited for in turn, so the parity names that tile)
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr - 1) & 1, wt);
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr - 1) & 1, wt);
       group_sync();
-      {
+      dsa::tc_fence_after();
+      const int hcount = min(32, w.hv - hh * 32);
+      const uint32_t tm_o = tmem_base + lane_off + kOCol + hh * 32;
+      if (hcount <= 0) {
+        // (no head of this half is real)
+      } else if (p.splits > 1) {
         const float* f32 = fac + hh * 32;
-        const int hcount = min(32, w.hv - hh * 32);
 #pragma unroll 1
         for (int mb = 0; mb < S::kNv; ++mb) {
-          if (hcount <= 0) break;
           uint32_t v[32];
           __syncwarp();
-          dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kHG + hh * 32, v);
+          dsa::tmem_ld32(tm_o + mb * kHG, v);
           dsa::tmem_wait_ld();
-          const int d = mb * 128 + quarter * 32;
-          if (p.splits > 1) {
-            float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + d + lane;
+          float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + mb * 128 + quarter * 32 + lane;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c < hcount) *o = __uint_as_float(v[c]) * f32[c];
-              o += static_cast<int64_t>(p.splits) * DV;
+          for (int c = 0; c < 32; ++c) {
+            if (c < hcount) *o = __uint_as_float(v[c]) * f32[c];
+            o += static_cast<int64_t>(p.splits) * DV;
+          }
+        }
+      } else {
+        // 16 heads x 32 dims at a time through shared memory, transposed by
+        // the store of 8 x 8 matrices: 64 consecutive bytes a head.  (Two
+        // bytes a lane straight to memory: 7K cycles an item, two bytes a
+        // lane to shared memory 5K.)
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 f2 = *reinterpret_cast<const float2*>(fac + hh * 32 + 8 * c + 2 * (lane & 3));
+          f[2 * c] = f2.x, f[2 * c + 1] = f2.y;
+        }
+        const uint32_t rows_at = dsa::smem_u32(rows);
+        const int mrow = 8 * (lane >> 4) + (lane & 7), munit = (lane >> 3) & 1;  // matrices: 8 heads x 8 dims
+        __nv_bfloat16* o0 = p.out + (orow + hh * 32 + (lane >> 2)) * DV + quarter * 32 + (lane & 3) * 8;
+#pragma unroll 1
+        for (int mb = 0; mb < S::kNv; ++mb) {
+#pragma unroll
+          for (int c0 = 0; c0 < 32; c0 += 16) {
+            uint32_t v[2][8];
+            __syncwarp();
+            dsa::tmem_ld16x256b_x2(tm_o + mb * kHG + c0, v[0]);
+            dsa::tmem_ld16x256b_x2(tm_o + mb * kHG + c0 + (16u << 16), v[1]);
+            dsa::tmem_wait_ld();
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint32_t r[4];
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {  // 8 heads n / 2, 8 dims n % 2
+                const float* fn = f + (c0 >> 2) + 2 * (n >> 1);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[g][2 * n]) * fn[0],
+                                                                __uint_as_float(v[g][2 * n + 1]) * fn[1]);
+                r[n] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              dsa::stmatrix_x4_trans(rows_at + sw64_offset(mrow, 2 * g + munit), r[0], r[1], r[2], r[3]);
             }
-          } else {
-            // through shared memory, 16 heads at a time: 64 consecutive bytes a
-            // head (two bytes a lane straight to memory: 7K cycles an item)
-            __nv_bfloat16* o = p.out + (orow + hh * 32 + (lane >> 2)) * DV + d + (lane & 3) * 8;
+            __syncwarp();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-              for (int c = 0; c < 16; c += 4) {
-                const float4 f4 = *reinterpret_cast<const float4*>(f32 + half * 16 + c);
-                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {  // (one conversion of two: they run at an eighth of the multiplies' rate)
-                  const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[half * 16 + c + e]) * f[e],
-                                                                 __uint_as_float(v[half * 16 + c + e + 1]) * f[e + 1]);
-                  reinterpret_cast<__nv_bfloat16*>(rows)[(c + e) * 32 + lane] = r.x;
-                  reinterpret_cast<__nv_bfloat16*>(rows)[(c + e + 1) * 32 + lane] = r.y;
-                }
-              }
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int c = half * 16 + k * 8;
-                if (c + (lane >> 2) < hcount)
-                  __stcs(reinterpret_cast<uint4*>(o + c * DV), reinterpret_cast<const uint4*>(rows)[k * 32 + lane]);
-              }
-              __syncwarp();
+            for (int k = 0; k < 2; ++k) {
+              const int h = k * 8 + (lane >> 2);
+              if (c0 + h < hcount)
+                __stcs(reinterpret_cast<uint4*>(o0 + mb * 128 + (c0 + k * 8) * DV),
+                       *reinterpret_cast<const uint4*>(rows + sw64_offset(h, lane & 3)));
             }
           }
         }
