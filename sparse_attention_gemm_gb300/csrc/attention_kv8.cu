@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   uint64_t* p_full = bars + 16;    // of the whole tile: its first half's products already meet rescaled sums
   uint64_t* q_full = bars + 17;
   uint64_t* q_empty = bars + 18;
+  uint64_t* q_read = bars + 19;    // the query's rows have been converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     dsa::mbar_init(p_full, kSoftWarps);
     dsa::mbar_init(q_full, kGatherWarps);
     dsa::mbar_init(q_empty, 1);
+    dsa::mbar_init(q_read, kGatherWarps);
     *abort_flag = 0;
     dsa::fence_barrier_init();
   }
@@ -226,29 +228,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv, meta_addr = dsa::smem_u32(smem) + S::kMeta;
     int half_ctr = 0, item_ctr = 0;  // (here a unit of work is half a tile)
     bool ok = true;
-    // The query: eight heads a warp, four threads a head, units (16 values)
-    // sub, sub + 4, ...; odd heads take the halves of a 128-byte row in the
-    // other order, so that eight lanes touch all banks once.  It is read twice,
-    // for the head's largest element while the item before still uses the
-    // operand, and for the terms: between the two items' scores stand only the
-    // conversions and what of the loads they do not hide.
+    // The query: its bf16 rows pass through a tile's buffer (ahead of the
+    // item's tiles, so that they are there when the item before leaves the
+    // operand); a warp copies and converts eight heads, four threads a head,
+    // units (16 values) sub, sub + 4, ...  Odd heads take the halves of a
+    // 128-byte row in the other order, and a head's 16-byte pieces lie in
+    // eights XOR-ed with it: eight lanes touch all banks once.
     const int hq = gt >> 2, sub = gt & 3;
-    constexpr int kUnits = DQK / 64;
-    constexpr int kAhead = 3;  // units loaded ahead of the one converted
+    constexpr int kUnits = DQK / 64, kPieces = DQK / 8;
+    static_assert(kHG * DQK * 2 <= S::kBuf, "a query fits a tile's buffer");
     // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
     // which gives each softmax thread eight consecutive heads
     const int qrow = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
+    auto raw_at = [&](int h, int c) { return h * (DQK * 2) + ((c & ~7) | ((c ^ h) & 7)) * 16; };
     auto unit_of = [&](int k) { return (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0); };
-    auto convert_query = [&](const Item& w, int n_item) {
-      const bool real = hq < w.hv;
-      // (a padding head: any)
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0 + (real ? hq : 0)) * DQK);
+    auto send_query = [&](const Item& w) {
+      const int b = (half_ctr >> 1) & 1;
+      const uint32_t ph = ((half_ctr >> 2) & 1) ^ 1, buf = kv_addr + b * S::kBuf;
+      if (!dsa::mbar_wait_warp(&kv_empty[2 * b], ph, wt) || !dsa::mbar_wait_warp(&kv_empty[2 * b + 1], ph, wt)) return false;
+      const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
+#pragma unroll 6
+      for (int k = 0; k < 8 * kPieces / 32; ++k) {
+        const int y = k * 32 + lane, h = warp * 8 + y / kPieces, c = y % kPieces;
+        const bool real = h < w.hv;
+        cp_async16(buf + raw_at(h, c), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u);
+      }
+      cp_async_arrive(&kv_full[2 * b]);
+      cp_async_arrive(&kv_full[2 * b + 1]);
+      half_ctr += 2;
+      return true;
+    };
+    auto convert_query = [&](int query_half, int n_item) {  // query_half: half_ctr of its buffer
+      const int b = (query_half >> 1) & 1;
+      const uint8_t* raw = smem + S::kKv + b * S::kBuf;
+      cp_async_wait_all();
+      __syncwarp();  // (the warp's own copies)
       uint32_t m = 0;
 #pragma unroll 3
       for (int k = 0; k < kUnits; ++k) {
         const int u = unit_of(k);
-        const uint4 v0 = __ldg(src + 2 * u), v1 = __ldg(src + 2 * u + 1);
-        m = dsa::amax_bf16x8(v1, dsa::amax_bf16x8(v0, m));
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u)), m);
+        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u + 1)), m);
       }
       m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
@@ -256,40 +276,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const bool finite = m < 0x7F80u;
       const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
       const float inv = dsa::pow2_inverse(s);
-      uint4 v[kAhead + 1][2];
-      auto load = [&](int k) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) v[k % (kAhead + 1)][e] = __ldg(src + 2 * unit_of(k) + e);
-      };
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) load(k);
       if (!dsa::mbar_wait_warp(q_empty, (n_item & 1) ^ 1, wt)) return false;
       if (sub == 0) qexp[(n_item % 3) * 64 + hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
-#pragma unroll
+#pragma unroll 3
       for (int k = 0; k < kUnits; ++k) {
-        if (k + kAhead < kUnits) load(k + kAhead);
         const int u = unit_of(k);
-        const uint4 v0 = v[k % (kAhead + 1)][0], v1 = v[k % (kAhead + 1)][1];
+        const uint4 v0 = *reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u));
+        const uint4 v1 = *reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u + 1));
         const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint16_t h2[2], l2[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) split_query(real ? wd[2 * j + e] : 0, inv, h2[e], l2[e]);
+          for (int e = 0; e < 2; ++e) split_query(wd[2 * j + e], inv, h2[e], l2[e]);
           hi[j] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
           lo[j] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
         }
         const bool tail = k >= S::kFull * 2;
-        const uint32_t at = tail ? S::kQTail + sw64_offset(qrow, u - S::kFull * 8)
+        const uint32_t to = tail ? S::kQTail + sw64_offset(qrow, u - S::kFull * 8)
                                  : (u >> 3) * kQChunkBytes + dsa::sw128_offset(qrow, (u & 7) * 16);
         // (64 rows on leaves either swizzle's phase as it is)
-        *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + at + kHG * (tail ? 64 : 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(smem + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + to + kHG * (tail ? 64 : 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       dsa::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) dsa::mbar_arrive(q_full);
+      if (lane == 0) {
+        dsa::mbar_arrive(q_full);
+        dsa::mbar_arrive(q_read);
+      }
+      if (warp == 0) {  // everybody has read the rows: the buffer goes back
+        if (!dsa::mbar_wait_warp(q_read, n_item & 1, wt)) return false;
+        if (lane == 0) {
+          dsa::mbar_arrive(&kv_empty[2 * b]);
+          dsa::mbar_arrive(&kv_empty[2 * b + 1]);
+        }
+        __syncwarp();
+      }
       return true;
     };
     // L2 prefetch of a later item's query and ids
@@ -325,9 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         id[kg] = load_id(2 * w.i0, kg);
         blk[kg] = load_block(id[kg]);
       }
-      // The query comes behind the first tile's copies, whose buffer does not
-      // wait for it; a CTA's first query behind those of half of it.
-      const int q_at = 2 * w.i0 + (item_ctr == 0 ? 0 : 1);
+      // The query comes before the first tile, and is converted before that is
+      // copied, whose buffer is not free sooner; a CTA's first query behind it.
+      const int query_half = half_ctr;
+      ok = send_query(w) && (item_ctr == 0 || convert_query(query_half, item_ctr));
+      if (!ok) break;
       for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
         const int stage = half_ctr & 3;
         int cur[kGatherSteps];
@@ -382,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
                        r >= 0 ? 16u : 0u);
         }
         cp_async_arrive(&kv_full[stage]);
-        if (i == q_at) {
-          if (!convert_query(w, item_ctr)) {
+        if (i == 2 * w.i0 + 1) {
+          if (item_ctr == 0 && !convert_query(query_half, 0)) {
             ok = false;
             break;
           }
@@ -411,17 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (w.i0 >= w.i1) continue;
         if (!dsa::mbar_wait_warp(q_full, item_ctr & 1, wt)) break;
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-          const int b = tile_ctr & 1;  // of the tile buffers and of those of S^T
-          const uint32_t par = (tile_ctr >> 1) & 1;
-          const bool got = dsa::mbar_wait(&s_empty[b], par ^ 1, wt) && dsa::mbar_wait(&kv_full[2 * b], par, wt) &&
-                           dsa::mbar_wait(&kv_full[2 * b + 1], par, wt);
+          const int sb = tile_ctr & 1, use = tile_ctr + item_ctr + 1, b = use & 1;  // use of the tile buffers
+          const uint32_t par = (use >> 1) & 1;
+          const bool got = dsa::mbar_wait(&s_empty[sb], ((tile_ctr >> 1) & 1) ^ 1, wt) &&
+                           dsa::mbar_wait(&kv_full[2 * b], par, wt) && dsa::mbar_wait(&kv_full[2 * b + 1], par, wt);
           // the gathered codes, before the tensor core reads them (MMA2's come
           // with the softmax warps' arrival, behind a fence of theirs)
           dsa::fence_proxy_async_smem();
           __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = kv_desc + b * (S::kBuf >> 4);
-          const uint32_t d = tmem_base + kSCol + b * 128;
+          const uint32_t d = tmem_base + kSCol + sb * 128;
 #pragma unroll
           for (int c = 0; c < S::kFull; ++c) {
             const uint64_t ac = a0 + c * (2 * kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
@@ -434,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) dsa::umma_f8_if(leader && got, d, at + kk * 2, qt_desc + kk * 2, idesc1, 1u);
           }
-          if (leader && got) dsa::umma_commit(&s_full[b]);
+          if (leader && got) dsa::umma_commit(&s_full[sb]);
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
@@ -449,16 +475,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       __syncwarp();
     } else {
       constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kHG) | (1u << 15) | (1u << 16);  // both MN-major
-      int half_ctr = 0;
+      int half_ctr = 0, tile_ctr = 0;
       const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, 2 * kChunkBytes, 1024, dsa::kSwizzle128B);
       // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
       const uint64_t ph_desc = dsa::smem_desc(base + S::kPHi, kPPart, 512, dsa::kSwizzle64B);
       const uint64_t pl_desc = dsa::smem_desc(base + S::kPLo, kPPart, 512, dsa::kSwizzle64B);
       for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
         const Item w = get_item(p, it, t_end);
+        if (w.i0 < w.i1) half_ctr += 2;  // the query's use of a buffer
         for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
           const int half = half_ctr & 1, b = (half_ctr >> 1) & 1;
-          const bool got = half == 1 || dsa::mbar_wait(p_full, b, wt);
+          const bool got = half == 1 || dsa::mbar_wait(p_full, tile_ctr++ & 1, wt);
           __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = v_desc + b * (S::kBuf >> 4) + half * (kChunkBytes >> 4);
@@ -501,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
     float* fac = reinterpret_cast<float*>(smem + S::kFac);  // [64]: references, then the factors of the result
     uint8_t* rows = smem + S::kPLo + sw * 1024;             // this warp's, of the result: 16 heads x 32 dims, 64-byte swizzle
-    int tile_ctr = 0, item_ctr = 0;
+    int tile_ctr = 0, n_item = 0;
     bool ok = true;
     // A wait of this thread gave up: the eight warps leave together, at a
     // point that reduces the flag (see the bf16 kernel).
@@ -527,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         continue;
       }
+      ++n_item;  // (with this one: each query used a tile's buffer)
       // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
       float m[8], l_part[8], qs[8];
       [[maybe_unused]] float top[8];
@@ -539,22 +567,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (kMax) top[h] = -INFINITY;
       }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-        const int b = tile_ctr & 1, stage = 2 * b + half;
-        const uint32_t par = (tile_ctr >> 1) & 1;
+        const int sb = tile_ctr & 1, use = tile_ctr + n_item, b = use & 1, stage = 2 * b + half;
         // the slots' scales come with the gathered tile
-        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], par, wt);
+        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (use >> 1) & 1, wt);
         const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep) + key0;
         float sk[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sk[k] = meta[8 * k] > 0.f ? meta[8 * k] : 0.f;
-        if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
+        if (!failed) failed = !dsa::mbar_wait(&s_full[sb], (tile_ctr >> 1) & 1, wt);
         __syncwarp();
         dsa::tc_fence_after();
         float x[32];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           uint32_t v[16], lo[16];
-          const uint32_t ta = tmem_base + lane_off + (static_cast<uint32_t>(g * 16) << 16) + kSCol + b * 128 + hh * 32;
+          const uint32_t ta = tmem_base + lane_off + (static_cast<uint32_t>(g * 16) << 16) + kSCol + sb * 128 + hh * 32;
           dsa::tmem_ld16x256b_x4(ta, v);
           dsa::tmem_ld16x256b_x4(ta + 64, lo);
           dsa::tmem_wait_ld();
@@ -562,15 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           for (int r = 0; r < 16; ++r) x[16 * g + r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
         }
         if (i == w.i0) {
-          const uint8_t* e = qexp + (item_ctr % 3) * 64 + hb;
+          const uint8_t* e = qexp + ((n_item - 1) % 3) * 64 + hb;
 #pragma unroll
           for (int h = 0; h < 8; ++h)  // (255: a head with infinity or NaN)
             qs[h] = __uint_as_float(static_cast<uint32_t>(e[h]) << 23) * (e[h] == 255 ? NAN : p.scale_log2);
-          ++item_ctr;
         }
         dsa::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
+        if (lane == 0) dsa::mbar_arrive(&s_empty[sb]);
         // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
