@@ -907,8 +907,10 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
 // Splits of each row's slots: the number that makes the longest CTA shortest,
 // counting a wave of CTAs as its tiles plus kItemTiles tiles for the query's
 // conversion, the first gather and the epilogue, and joining as kJoinTiles
-// tiles plus one per 16 splits.
-constexpr int kItemTiles = 3, kJoinTiles = 3;
+// tiles plus one per 16 splits.  Measured (rows of 576, 2048 slots, 128 heads;
+// microseconds with 1, 2, 4, 8, 16 splits): 16 rows 49, 34, 25, 31, 49; 32 rows 50,
+// 37, 42, 58, 85; 100 rows 96, 98, 118, 160, 248.
+constexpr int kItemTiles = 5, kJoinTiles = 3;
 
 int plan_splits(int64_t units, int K) {
   const int nt = (K + kTile - 1) / kTile;

@@ -694,9 +694,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 
 int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * ((H / Hc + kHG - 1) / kHG); }
 
-// Splits of each row's slots, one to eight: the number that makes the busiest SM's work shortest,
-// counting an item as its tiles plus kItemTiles for what happens once.
-constexpr int kItemTiles = 4;
+// Splits of each row's slots, one to eight CTAs of a cluster: the number that
+// makes the last CTA earliest, in fifths of a tile: kItemTiles for what an item
+// does once, 7 instead of 5 a tile where SMs have two CTAs, 13 and one per
+// split for the join.  Measured (2048 slots, latent rows of 576; microseconds
+// with 1, 2, 4, 8 splits): one row of 64 heads 35, 23, 14.8, 11.4; 8 rows of 128
+// heads 35, 24, 20.4, 28; 1024 rows of 16 heads of 512 180, 212, 260, 384.
+constexpr int kItemTiles = 5;
 
 int plan_splits(int64_t units, int K) {
   const int nt = (K + kKeys - 1) / kKeys;
@@ -704,7 +708,7 @@ int plan_splits(int64_t units, int K) {
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxCluster && s <= nt; s *= 2) {
     const int64_t waves = (units * s + 2 * kPlanSms - 1) / (2 * kPlanSms);
-    const int64_t c = 4 * waves * ((nt + s - 1) / s + kItemTiles) + (s > 1 ? 2 + s : 0);
+    const int64_t c = waves * ((nt + s - 1) / s + kItemTiles) * (units * s > kPlanSms ? 7 : 5) + (s > 1 ? 13 + s : 0);
     if (c < cost) cost = c, best = s;
   }
   return best;
@@ -742,7 +746,16 @@ int launch_form(const Params& p, cudaStream_t stream) {
 namespace dsa {
 namespace kv8_attn {
 
-bool narrow_takes(int T, int H, int Hc, int) { return H / Hc <= kHG || units_of(T, H, Hc) <= 16; }
+// KV heads of at most 16 query heads, and calls of little work: up to 10
+// tiles of 16 heads an SM, or 20 where the other kernel's 64 heads are at
+// least half padding.  Measured (microseconds, this kernel against the other):
+// 1024 rows of 16 heads of 512, 512 slots 63 / 102; 4 and 8 rows of 128 heads, 2048
+// slots 15.7 / 17.6 and 20.4 / 18.6; 64 and 128 rows of 64 heads, 256 slots 12.1 /
+// 14.3 and 22 / 15.4; 32 heads: 32 rows, 2048 slots 21.3 / 23.6, 1000 rows, 1000 slots 170 / 165.
+bool narrow_takes(int T, int H, int Hc, int K) {
+  const int groups = (H / Hc + kHG - 1) / kHG;
+  return groups == 1 || units_of(T, H, Hc) * ((K + kKeys - 1) / kKeys) <= (groups == 2 ? 20 : 10) * kPlanSms;
+}
 
 int launch_narrow(Params p, int T, int Dqk, cudaStream_t stream) {
   p.G = (p.H / p.Hc + kHG - 1) / kHG;
