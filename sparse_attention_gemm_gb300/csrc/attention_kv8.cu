@@ -556,14 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       }
       ++n_item;  // (with this one: each query used a tile's buffer)
       // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
-      float m[8], l_part[8], qs[8];
+      float nm[8], l_part[8], qs[8];  // (nm: the reference, negative)
       [[maybe_unused]] float top[8];
       bool unset = true;                        // no valid slot so far
       float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
       float inv = __uint_as_float(253u << 23);  // 2^-E
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        l_part[h] = 0.f, m[h] = 0.f;
+        l_part[h] = 0.f, nm[h] = 0.f;
         if (kMax) top[h] = -INFINITY;
       }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
@@ -586,7 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           dsa::tmem_ld16x256b_x4(ta + 64, lo);
           dsa::tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[16 * g + r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(v[r]));
+          for (int r = 0; r < 16; r += 2) {
+            const float2 y = fma2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
+                                  make_float2(__uint_as_float(v[r]), __uint_as_float(v[r + 1])));
+            x[16 * g + r] = y.x, x[16 * g + r + 1] = y.y;
+          }
         }
         if (i == w.i0) {
           const uint8_t* e = qexp + ((n_item - 1) % 3) * 64 + hb;
@@ -600,11 +604,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const bool valid = sk[k] > 0.f;
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            float& s = x[at(k, h)];
-            s = valid ? fmaf(s, qs[h] * sk[k], -m[h]) : -INFINITY;
+          for (int h = 0; h < 8; h += 2) {
+            const float2 c = mul2(make_float2(qs[h], qs[h + 1]), make_float2(sk[k], sk[k]));
+            const float2 y = fma2(make_float2(x[at(k, h)], x[at(k, h + 1)]), c, make_float2(nm[h], nm[h + 1]));
+            x[at(k, h)] = y.x, x[at(k, h + 1)] = y.y;
+          }
+        }
+        if (__any_sync(0xffffffffu, fminf(fminf(sk[0], sk[1]), fminf(sk[2], sk[3])) == 0.f)) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) x[at(k, h)] = sk[k] > 0.f ? x[at(k, h)] : -INFINITY;
           }
         }
         float most = x[0], sv_most = 0.f;
@@ -619,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         const bool ex = unset || most > kTheta || sv_most > ref;
         if constexpr (kMax) {
 #pragma unroll
-          for (int h = 0; h < 8; ++h) top[h] = fmaxf(top[h], most_of(x, h) + m[h]);
+          for (int h = 0; h < 8; ++h) top[h] = fmaxf(top[h], most_of(x, h) - nm[h]);
         }
         const bool first = i == w.i0;
         bool need_rescale = false;
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
               const float a = unset ? 1.f : ex2(-up);
               moved |= up != 0.f;
               l_part[h] *= a;
-              m[h] += up;
+              nm[h] -= up;
 #pragma unroll
               for (int k = 0; k < 4; ++k) x[at(k, h)] -= up;
               if (lane < 4) alpha[hb + h] = a * ratio;
@@ -685,9 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float p0 = ex2(x[at(k, 2 * j)]), p1 = ex2(x[at(k, 2 * j + 1)]);
-              l_part[2 * j] += p0;
-              l_part[2 * j + 1] += p1;
-              split_weights(p0 * wk, p1 * wk, hi[j], lo[j]);
+              const float2 l2 = add2(make_float2(l_part[2 * j], l_part[2 * j + 1]), make_float2(p0, p1));
+              l_part[2 * j] = l2.x, l_part[2 * j + 1] = l2.y;
+              const float2 p2 = mul2(make_float2(p0, p1), make_float2(wk, wk));
+              split_weights(p2.x, p2.y, hi[j], lo[j]);
             }
             const uint32_t to = sw64_offset(key0 + 8 * k, hb >> 4) + (hb & 8);
             *reinterpret_cast<uint2*>(ph + to) = pack4(hi);
@@ -729,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       group_sync();
       if (quarter == 0 && lane < 4) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) fac[hb + h] = m[h];
+        for (int h = 0; h < 8; ++h) fac[hb + h] = -nm[h];
       }
       wmax[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
       group_sync();
