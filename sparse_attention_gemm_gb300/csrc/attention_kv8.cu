@@ -15,19 +15,32 @@
 //   weights: w = C * exp(s_j - m) * v_scale / 2^E as hi + lo: relative error
 //            2^-8, what rounding to bf16 costs, and never less than 2^-10 / C
 //            (half the smaller term's smallest step).
-// Against the bf16 kernel a tile of 64 keys costs half the gather and 34
-// instructions instead of 52; hi and lo of the query are the two halves of
-// one N = 128 operand, hi and lo of the weights two instructions into the same sums.
 //
-// Work item = (token, KV head, group of 64 query heads, split of its slots).
-// Products ("swap AB"):
-//   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T   (M = 64 keys, N = 128)
-//   MMA2  O^T[dim, head] += V^T[dim, key] . (Phi + Plo)^T[key, head] (M = 128 dims, N = 64)
+// Work item = (token, KV head, group of 64 query heads, split of its slots);
+// calls with few heads per KV head or few rows go to attention_kv8_narrow.cu.
+// Products ("swap AB"), tiles of 128 keys:
+//   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T   (M = 128 keys, N = 128)
+//   MMA2  O^T[dim, head] += V^T[dim, key] . (Phi + Plo)^T[key, head] (M = 128 dims, N = 64),
+//         a half of the tile at a time: its buffer goes back that much sooner
 // S^T (two buffers) and O^T fill TMEM.  Tiles are gathered with cp.async into
-// 128-byte-swizzled rows by eight warps, two tiles in flight, three or four buffers.
+// 128-byte-swizzled rows, in two buffers of two halves; a copy's landing is its
+// own arrival at the half's barrier, so the gather never waits for one.
 // Softmax: as in the bf16 kernel, one reference maximum per head that moves
 // when a tile passes it by 2^kTheta, and a reference exponent E of the value
 // scales that moves when a block's scale passes 2^E; both move the running sums.
+//
+// What bounds it.  An M = 64 product takes the tensor core as long as an M =
+// 128 one (64 cycles a K step at N = 128), so tiles of 128 keys take 18 x 64 + 32 x 53 =
+// 2.85K cycles against 2 x 2.0K of tiles of 64.  The query's two terms take
+// 72 KB of shared memory, which leaves two buffers of 128 keys: a tile's way
+// through them (copies 2K cycles, scores 1.5-2K, softmax 3-4K, value product 2K)
+// is two tiles' time, 5.2K cycles a tile at 576 dims: latency, with the tensor
+// cores at 55%.  A row's end and the next one's start cost 10K more (query
+// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 618 us, 935
+// TFLOP/s of the formula's operations (half of the bf16 rate measured; 578 GFLOP).
+// Tried and slower: a look at the next query's largest element during this
+// item's tiles (its loads held the gather back, 2%), tiles of 64 keys in four
+// buffers (677 us), results from registers two bytes a lane (+25 us).
 //
 // Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
 // MMA1, 17 MMA2.
@@ -62,7 +75,7 @@ constexpr int kMaxSplits = 32;
 // A key row is kFull chunks of 128 codes (128-byte swizzle) and, at 576 dims,
 // a tail of 64 (64-byte swizzle).  MMA2 does not read the tail, so once a
 // tile's scores are done its space takes the first term of the tile's P^T; that is
-// what makes four buffers fit.
+// what makes two buffers of 128 keys fit beside the query's 72 KB.
 template <int DQK, int DV, bool SEP>
 struct Shape {
   static constexpr int kFull = DQK / 128;
@@ -636,10 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         bool need_rescale = false;
         float ratio = 1.f;  // of the old to the new 2^E
         if (first || group_any(ex || failed)) {
-          if (group_any(failed)) {  // the group leaves together
-            ok = false;
-            break;
-          }
           // move the references: the tile's maximum per head over its 64 keys
           float v[8];
 #pragma unroll
@@ -650,7 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
           if (lane == 0 && hh == 0) svm[quarter] = sv;
-          group_sync();
+          if (group_any(failed)) {  // the group leaves together
+            ok = false;
+            break;
+          }
           const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
           const float rn = fmaxf(ref, pow2_ceil(sv_max));
           inv = dsa::pow2_inverse(rn);

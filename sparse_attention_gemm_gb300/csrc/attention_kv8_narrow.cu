@@ -14,6 +14,13 @@
 // Splits of a row are the CTAs of a cluster: each leaves its sums in its own
 // shared memory, and each joins the dims of its rank from everyone's.  No
 // second kernel, no workspace, and the order of the sum is the ranks'.
+// What bounds it: 1.5K cycles of a pair of CTAs a tile (copies in flight), and
+// what an item does once, 10K cycles: first loads 4K (ids, table entries), first
+// tile 2K, softmax's first reference 1.6K, results 2.3K, join 4K.  Shared memory
+// (a tile of 64 keys 36 KB, two of them) holds two CTAs, not three.  96 rows of 2 x
+// 12 heads of 256 + 256, 1027 slots: 21 us, 4.2 TB/s, in its steady part the
+// memory's rate; 1024 rows of 16 heads of 512 over documents of 341: 39 us;
+// one row of 64 heads, 2048 slots: 11.4 us (the 64-head kernel and its join: 18.4).
 //
 // Warps: 0..3 gather, 4..7 query conversion, softmax and epilogue, 8 MMA1, 9 MMA2.
 #include "attention_kv8.cuh"
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   float* svm = reinterpret_cast<float*>(smem + S::kSvm);
   uint8_t* qexp = smem + S::kQexp;  // exponents of the query scales (biased; 255: not finite)
   float* part = reinterpret_cast<float*>(smem + S::kPart);
-  __nv_bfloat16* row16 = reinterpret_cast<__nv_bfloat16*>(smem + S::kPart);  // [16][DV]: the results of an undivided row
+  uint8_t* row16 = smem + S::kPart;  // [DV / 32] x 16 heads x 32 dims, 64-byte swizzle: the results of an undivided row
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* kv_full = bars;       // [3]
   uint64_t* kv_empty = bars + 3;  // [3]
@@ -488,10 +495,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       }
       bool need_rescale = false;
       if (i == i0 || group_any(ex || failed)) {
-        if (group_any(failed)) {  // the group leaves together
-          ok = false;
-          break;
-        }
         // move the references: the tile's maximum per head over its 64 keys
         wmax[quarter * kHG + hb + own_head(lane)] = fold4(v, lane, [](float a, float c) { return fmaxf(a, c); });
         float sv = fmaxf(svA, svB);
@@ -499,7 +502,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
         sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
         if (lane == 0) svm[quarter] = sv;
-        group_sync();
+        if (group_any(failed)) {  // the group leaves together
+          ok = false;
+          break;
+        }
         const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
         const float rn = fmaxf(ref, pow2_ceil(sv_max));
         inv = dsa::pow2_inverse(rn);
@@ -576,23 +582,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 
     // ---------------------------------------------------------- epilogue
     if (ok) {
-      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
-      // been waited for in turn, so the parity names that tile)
+      // The sums' norm, while the last tile's MMA2 runs.
       const float sink = p.sink && st < hv ? __ldg(p.sink + h0 + st) : -INFINITY;
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[(ctr - 1) & 1], ((ctr - 1) >> 1) & 1, wt);
-      __syncwarp();
-      dsa::tc_fence_after();
       red[quarter * kHG + hb + own_head(lane)] = fold4(l_part, lane, [](float a, float c) { return a + c; });
       redm[quarter * kHG + hb + own_head(lane)] = fold4(top, lane, [](float a, float c) { return fmaxf(a, c); });
       if (quarter == 0 && lane < 4) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) alpha[hb + h] = m[h];
+        for (int h = 0; h < 4; ++h) fac[hb + h] = m[h];
       }
       group_sync();
       const float unscale = ref * (1.f / kWeight);
       if (st < kHG) {
         const float l = red[st] + red[kHG + st] + red[2 * kHG + st] + red[3 * kHG + st];
-        const float mc = alpha[st];
+        const float mc = fac[st];
         const float mx = fmaxf(fmaxf(redm[st], redm[kHG + st]), fmaxf(redm[2 * kHG + st], redm[3 * kHG + st]));
         stats[st] = make_float4(mc, l, mx, sink);
         fac[st] = unscale;
@@ -606,34 +608,71 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
           }
         }
       }
+      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
+      // been waited for in turn, so the parity names that tile)
+      if (!failed) failed = !dsa::mbar_wait(&p_empty[(ctr - 1) & 1], ((ctr - 1) >> 1) & 1, wt);
       group_sync();
-      float f[kHG];
+      dsa::tc_fence_after();
+      const uint32_t tm_o = tmem_base + lane_off + kOCol;
+      if (p.splits > 1) {
+        float f[kHG];
 #pragma unroll
-      for (int h = 0; h < kHG; h += 4) {
-        const float4 f4 = *reinterpret_cast<const float4*>(fac + h);
-        f[h] = f4.x, f[h + 1] = f4.y, f[h + 2] = f4.z, f[h + 3] = f4.w;
-      }
+        for (int h = 0; h < kHG; h += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(fac + h);
+          f[h] = f4.x, f[h + 1] = f4.y, f[h + 2] = f4.z, f[h + 3] = f4.w;
+        }
 #pragma unroll 1
-      for (int mb = 0; mb < S::kNv; ++mb) {
-        uint32_t v[32];
-        __syncwarp();
-        dsa::tmem_ld32(tmem_base + lane_off + kOCol + mb * kCols, v);
-        dsa::tmem_wait_ld();
-        const int d = mb * 128 + quarter * 32 + lane;
-        if (p.splits > 1) {
+        for (int mb = 0; mb < S::kNv; ++mb) {
+          uint32_t v[32];
+          __syncwarp();
+          dsa::tmem_ld32(tm_o + mb * kCols, v);
+          dsa::tmem_wait_ld();
+          const int d = mb * 128 + quarter * 32 + lane;
 #pragma unroll
           for (int h = 0; h < kHG; ++h) part[h * DV + d] = (__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * f[h];
-        } else {
-#pragma unroll
-          for (int h = 0; h < kHG; ++h)
-            row16[h * DV + d] = __float2bfloat16_rn((__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * f[h]);
         }
-      }
-      if (p.splits == 1) {
-        // through shared memory: 16 bytes a lane (two bytes a lane straight to memory took 7K cycles of 16K)
-        group_sync();
-        uint4* o = reinterpret_cast<uint4*>(p.out + orow * DV);
-        for (int x = st; x < hv * (DV / 8); x += kSoftThreads) __stcs(o + x, reinterpret_cast<const uint4*>(row16)[x]);
+      } else {
+        // transposed by the store of 8 x 8 matrices, 16 heads x 32 dims at a
+        // time: 64 consecutive bytes a head (two bytes a lane straight to
+        // memory: 7K cycles of an item's 16K)
+        float f[4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 f2 = *reinterpret_cast<const float2*>(fac + 8 * c + 2 * (lane & 3));
+          f[2 * c] = f2.x, f[2 * c + 1] = f2.y;
+        }
+        const int mrow = 8 * (lane >> 4) + (lane & 7), munit = (lane >> 3) & 1;  // matrices: 8 heads x 8 dims
+        __nv_bfloat16* o0 = p.out + (orow + (lane >> 2)) * DV + quarter * 32 + (lane & 3) * 8;
+#pragma unroll
+        for (int mb = 0; mb < S::kNv; ++mb) {
+          uint8_t* rows = row16 + (mb * 4 + quarter) * 1024;
+          uint32_t v[2][16];
+          __syncwarp();
+          dsa::tmem_ld16x256b_x4(tm_o + mb * kCols, v[0]);
+          dsa::tmem_ld16x256b_x4(tm_o + mb * kCols + (16u << 16), v[1]);
+          dsa::tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t r[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {  // 8 heads n / 2, 8 dims n % 2
+              const float* fn = f + 2 * (n >> 1);
+              const float a = __uint_as_float(v[g][2 * n]) + __uint_as_float(v[g][8 + 2 * n]);
+              const float b = __uint_as_float(v[g][2 * n + 1]) + __uint_as_float(v[g][8 + 2 * n + 1]);
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(a * fn[0], b * fn[1]);
+              r[n] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            dsa::stmatrix_x4_trans(dsa::smem_u32(rows) + sw64_offset(mrow, 2 * g + munit), r[0], r[1], r[2], r[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int h = k * 8 + (lane >> 2);
+            if (h < hv)
+              __stcs(reinterpret_cast<uint4*>(o0 + mb * 128 + k * 8 * DV),
+                     *reinterpret_cast<const uint4*>(rows + sw64_offset(h, lane & 3)));
+          }
+        }
       }
       dsa::tc_fence_before();
     }
