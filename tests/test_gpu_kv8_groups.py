@@ -45,6 +45,7 @@ def same(a, b):
     (100, 64, 1, 260, 16, True, True),      # odd lengths, the last tile half empty
     (60, 128, 1, 290, 64, False, False),    # two full groups
     (40, 200, 2, 193, 32, True, True),      # groups of 64 and 36 heads, two KV heads
+    (50, 64, 1, 700, 64, True, False),      # three splits of a row
     (20, 64, 1, 2048, 64, False, True),     # slots split between CTAs, joined by the second kernel
     (400, 64, 1, 130, 4, True, False),      # several items a CTA, some empty
     (170, 33, 1, 300, 1, False, True),      # one head in the upper half of a group
@@ -164,7 +165,8 @@ def test_wide_offsets_beyond_32_bits():
 
 # (form, T, H, K): narrow undivided and in a cluster, wide undivided and in splits
 CALLS = [((576, 512), 300, 16, 256), ((512, 512), 2, 64, 1024), ((256, 256), 90, 12, 700), ((576, 512), 400, 64, 300),
-         ((512, 512), 300, 64, 300), ((256, 256), 300, 64, 300), ((576, 512), 20, 64, 2048)]
+         ((512, 512), 300, 64, 300), ((256, 256), 300, 64, 300), ((576, 512), 20, 64, 2048),
+         ((512, 512), 50, 64, 700), ((256, 256), 30, 64, 1200)]
 
 
 def made(form, T, H, K, seed=50):
