@@ -765,17 +765,18 @@ def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, s
             (lse is not None and lse.shape != (T, H))):
         _attn_refuse(q, kv8, kv_scale, idx, topk_length, sink, v8, v_scale, cu_seqlens, block_table, out, lse,
                      workspace)
+    device, empty = q.device, torch.empty
     if out is None:
-        out = q.new_empty((T, H, Dv))
+        out = empty((T, H, Dv), dtype=_BF16, device=device)
     if lse is None:
-        lse = kv_scale.new_empty((T, H))
-    lse_kv = kv_scale.new_empty((T, H)) if want_lse_kv else None
-    ml = kv_scale.new_empty((T, H)) if want_max_logits else None
+        lse = empty((T, H), dtype=_F32, device=device)
+    lse_kv = empty((T, H), dtype=_F32, device=device) if want_lse_kv else None
+    ml = empty((T, H), dtype=_F32, device=device) if want_max_logits else None
     L = _lib or lib()
     if workspace is None:
         need = L.dsa_sparse_attn_fwd_kv8_workspace_size(T, H, heads, Dqk, Dv, K)
         if need:
-            workspace = kv8.new_empty(need)
+            workspace = empty(need, dtype=_U8, device=device)
     rc = L.dsa_sparse_attn_fwd_kv8(
         q.data_ptr(), kv8.data_ptr(), kv_scale.data_ptr(), None if v8 is None else v8.data_ptr(),
         None if v8 is None else v_scale.data_ptr(), idx.data_ptr(),
