@@ -25,6 +25,11 @@ Cases (kernel to select with -k in parentheses):
   backward        dsa_sparse_attn_bwd on the fused top-k ids, dout ~ N(0, 1) * 0.1
                   (bwd_prep_kernel, bwd_dq_kernel, bwd_dkv_kernel, bwd_reduce_*);
                   with --atomic the variant whose dkv goes through fp32 atomics
+  kv8_write       dsa_kv8_write of T latent rows into pages of 64 tokens (kv8_write_kernel)
+  kv8_read        dsa_kv8_read of them                          (kv8_read_kernel)
+  attention_kv8   dsa_sparse_attn_fwd_kv8 over those pages, ids drawn evenly
+                  from the causal rows                          (attn_kv8_kernel)
+  attention_kv8_narrow  the same with H = 16                    (attn_kv8_narrow_kernel)
 """
 from __future__ import annotations
 
@@ -35,7 +40,8 @@ import sys
 import numpy as np
 import torch
 
-CASES = ("indexer_dense", "indexer_fused", "indexer_mxfp8", "select", "topk", "attention", "gqa", "backward")
+CASES = ("indexer_dense", "indexer_fused", "indexer_mxfp8", "select", "topk", "attention", "gqa", "backward",
+         "kv8_write", "kv8_read", "attention_kv8", "attention_kv8_narrow")
 
 
 def _bf16(shape, sigma, g, dev):
@@ -82,6 +88,26 @@ def main(argv=None) -> int:
         twice(lambda: ops.sparse_attn_fwd(q, k, idx, 1.0 / 16.0, v=v))
         print(f"gqa: B={B} S={S} Hq={Hq} D={D} width={idx.shape[1]}")
         return 0
+
+    if args.case in ("kv8_write", "kv8_read", "attention_kv8", "attention_kv8_narrow"):
+        pages = (T + 63) // 64
+        table = torch.randperm(pages, generator=g, device=dev).to(torch.int32)[None]
+        rows = _bf16((T, 1, 576), 1.0, g, dev)
+        kv8 = torch.zeros((pages, 64, 1, 576), dtype=torch.uint8, device=dev)
+        scale = torch.ones((pages, 1), device=dev)
+        ops.kv8_write(rows, kv8, scale, cu, block_table=table)
+        if args.case == "kv8_write":
+            twice(lambda: ops.kv8_write(rows, kv8, scale, cu, block_table=table))
+        elif args.case == "kv8_read":
+            twice(lambda: ops.kv8_read(kv8, scale, cu, T, block_table=table, out=rows))
+        else:
+            q = _bf16((T, 64 if args.case == "attention_kv8" else 16, 576), 1.0, g, dev)
+            u = torch.rand((T, K), generator=g, device=dev) * torch.arange(1, T + 1, device=dev)[:, None]
+            idx = u.to(torch.int32).sort(1)[0].contiguous()
+            twice(lambda: ops.sparse_attn_fwd_kv8(q, kv8, scale, idx, 1.0 / 24.0, cu_seqlens=cu, block_table=table))
+        status = ops.device_status(clear=True)
+        print(f"{args.case}: T={T} k={K} status={status:#x}")
+        return 1 if status else 0
 
     if args.case == "indexer_mxfp8":
         # E4M3 codes of N(0,1) draws with scale bytes around 2^-2 (no NaN codes)
