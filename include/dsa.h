@@ -543,6 +543,7 @@ int dsa_forward_host(const dsa_forward_buffers* b, int n_docs, int T, int Hi, in
 #define DSA_KV8_MAX_BLOCK 256
 #define DSA_KV8_MAX_DIM 1024
 #define DSA_KV8_MAX_HEADS 1024
+#define DSA_KV8_MAX_SLOTS (1 << 30)
 
 /* Quantises rows as they are written into the cache.
  *   src bf16 [T, Hc, D]; cache, scale (in, out).
@@ -597,7 +598,7 @@ int dsa_kv8_read(const void* cache, const float* scale, const int32_t* cu_seqlen
  *   entry; calls that may overlap need one each.
  * Accumulation is fp32.  Results are bitwise reproducible.
  * Shapes: (Dqk, Dv) in {(576, 512), (512, 512)} without v8, or (256, 256) with
- * it; H a multiple of Hc, H / Hc <= 128; K >= 0; scale finite > 0; q, kv8, v8,
+ * it; H a multiple of Hc, H / Hc <= 128; 0 <= K <= DSA_KV8_MAX_SLOTS; scale finite > 0; q, kv8, v8,
  * out 16-byte aligned.
  * Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
 size_t dsa_sparse_attn_fwd_kv8_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K);

@@ -950,7 +950,7 @@ int plan_splits(int64_t units, int K) {
 
 bool known_shape(int T, int H, int Hc, int Dqk, int Dv, int K) {
   const bool form = ((Dqk == 576 || Dqk == 512) && Dv == 512) || (Dqk == 256 && Dv == 256);
-  return form && T >= 1 && H >= 1 && Hc >= 1 && H % Hc == 0 && K >= 1;
+  return form && T >= 1 && H >= 1 && Hc >= 1 && H % Hc == 0 && K >= 1 && K <= DSA_KV8_MAX_SLOTS;
 }
 
 int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * ((H / Hc + kHG - 1) / kHG); }
@@ -1017,9 +1017,10 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   if (!latent && !separate)
     return dsa::set_error(
         DSA_ERR_VALUE, "%s: (Dqk, Dv) must be (576|512, 512) without v8 and v_scale or (256, 256) with both", fn);
-  if (T < 0 || H < 1 || Hc < 1 || Hc > DSA_KV8_MAX_HEADS || H % Hc != 0 || H / Hc > 128 || K < 0)
-    return dsa::set_error(DSA_ERR_VALUE, "%s: need T >= 0, K >= 0, 1 <= Hc <= %d, H a multiple of Hc, H / Hc <= 128", fn,
-                          DSA_KV8_MAX_HEADS);
+  if (T < 0 || H < 1 || Hc < 1 || Hc > DSA_KV8_MAX_HEADS || H % Hc != 0 || H / Hc > 128 || K < 0 ||
+      K > DSA_KV8_MAX_SLOTS)
+    return dsa::set_error(DSA_ERR_VALUE, "%s: need T >= 0, 0 <= K <= %d, 1 <= Hc <= %d, H a multiple of Hc, H / Hc <= 128",
+                          fn, DSA_KV8_MAX_SLOTS, DSA_KV8_MAX_HEADS);
   const int64_t units = T > 0 ? units_of(T, H, Hc) : 0;
   if (units * kMaxSplits > INT_MAX || static_cast<int64_t>(T) * H > INT_MAX)
     return dsa::set_error(DSA_ERR_VALUE, "%s: T * H exceeds the int32 range of work items", fn);

@@ -233,6 +233,13 @@ def check_attention(q, k, ks, idx, sm, **kw):
         assert np.array_equal(g[~fin], r[~fin]), n
         far = np.abs(g[fin] - r[fin]) - ref["lse_tol"][done][fin]
         assert not (far > 0).any(), f"{n}: {far.max():.3g} over its bound"
+    bare = ops.sparse_attn_fwd_kv8(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, topk_length=d["length"], sink=d["sink"],
+                                   v8=d["v8"], v_scale=d["v_scale"], cu_seqlens=d["cu"], block_table=d["table"])
+    o = bare["out"][dev(done)].float().cpu().numpy().astype(np.float64)
+    assert set(bare) == {"out", "lse"} and not (np.abs(o - ref["out"][done]) > ref["out_tol"][done]).any()
+    g, r = bare["lse"].cpu().numpy().astype(np.float64)[done], ref["lse"][done]
+    fin = np.isfinite(r)
+    assert np.array_equal(g[~fin], r[~fin]) and not (np.abs(g[fin] - r[fin]) > ref["lse_tol"][done][fin]).any()
     return got
 
 

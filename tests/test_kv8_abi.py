@@ -62,7 +62,7 @@ def test_read_refuses(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(H=0), dict(H=129), dict(H=64, Hc=3), dict(Hc=0), dict(K=-1), dict(Dqk=256), dict(Dv=256),
+    dict(T=-1), dict(H=0), dict(H=129), dict(H=64, Hc=3), dict(Hc=0), dict(K=-1), dict(K=(1 << 30) + 1), dict(K=(1 << 31) - 1), dict(Dqk=256), dict(Dv=256),
     dict(Dqk=256, Dv=256), dict(Dqk=256, Dv=256, v8=FAKE), dict(Dqk=256, Dv=256, v_scale=FAKE), dict(v8=FAKE, v_scale=FAKE),
     dict(v_scale=FAKE), dict(block=0), dict(block=3), dict(block=512), dict(n_blocks=0), dict(n_blocks=1 << 25),
     dict(scale=0.0), dict(scale=float("inf")), dict(scale=float("nan")), dict(q=NULL), dict(kv8=NULL), dict(kv_scale=NULL),
