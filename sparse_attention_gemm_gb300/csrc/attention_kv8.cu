@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       }
       ++n_item;  // (with this one: each query used a tile's buffer)
       // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
-      float nm[8], l_part[8], qs[8];  // (nm: the reference, negative)
+      float nm[8], l_part[8];  // (nm: the reference, negative)
       [[maybe_unused]] float top[8];
       bool unset = true;                        // no valid slot so far
       float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
@@ -605,21 +605,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             x[16 * g + r] = y.x, x[16 * g + r + 1] = y.y;
           }
         }
-        if (i == w.i0) {
-          const uint8_t* e = qexp + ((n_item - 1) % 3) * 64 + hb;
-#pragma unroll
-          for (int h = 0; h < 8; ++h)  // (255: a head with infinity or NaN)
-            qs[h] = __uint_as_float(static_cast<uint32_t>(e[h]) << 23) * (e[h] == 255 ? NAN : p.scale_log2);
-        }
+        const uint2 qe = *reinterpret_cast<const uint2*>(qexp + ((n_item - 1) % 3) * 64 + hb);
         dsa::tc_fence_before();
         __syncwarp();
         if (lane == 0) dsa::mbar_arrive(&s_empty[sb]);
         // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int h = 0; h < 8; h += 2) {
+          float2 q2;  // the query's scales times the softmax's (held as exponents: eight registers less)
+          q2.x = __uint_as_float(((h < 4 ? qe.x : qe.y) >> (8 * (h & 3)) & 255u) << 23);
+          q2.y = __uint_as_float(((h < 4 ? qe.x : qe.y) >> (8 * (h & 3) + 8) & 255u) << 23);
+          // (255: a head with infinity or NaN)
+          q2 = fma2(q2, make_float2(p.scale_log2, p.scale_log2), make_float2(q2.x - q2.x, q2.y - q2.y));
 #pragma unroll
-          for (int h = 0; h < 8; h += 2) {
-            const float2 c = mul2(make_float2(qs[h], qs[h + 1]), make_float2(sk[k], sk[k]));
+          for (int k = 0; k < 4; ++k) {
+            const float2 c = mul2(q2, make_float2(sk[k], sk[k]));
             const float2 y = fma2(make_float2(x[at(k, h)], x[at(k, h + 1)]), c, make_float2(nm[h], nm[h + 1]));
             x[at(k, h)] = y.x, x[at(k, h + 1)] = y.y;
           }
