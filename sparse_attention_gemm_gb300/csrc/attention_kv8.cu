@@ -36,8 +36,11 @@
 // through them (copies 2K cycles, scores 1.5-2K, softmax 3-4K, value product 2K)
 // is two tiles' time, 5.2K cycles a tile at 576 dims: latency, with the tensor
 // cores at 55%.  A row's end and the next one's start cost 10K more (query
-// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 618 us, 935
+// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 604 us, 957
 // TFLOP/s of the formula's operations (half of the bf16 rate measured; 578 GFLOP).
+// A CTA that has finished takes over the item of one that has not started: SMs
+// differ by up to 8% in speed, and with every 152nd item a CTA's own the slowest
+// ones' 14 items of 13.5 set the time (615 us).
 // Tried and slower: a look at the next query's largest element during this
 // item's tiles (its loads held the gather back, 2%), tiles of 64 keys in four
 // buffers (677 us), results from registers two bytes a lane (+25 us).
@@ -100,7 +103,8 @@ struct Shape {
   static constexpr uint32_t kQexp = kFac + 256;                        // uint8 [3][64]
   static constexpr uint32_t kSvm = kQexp + 192;                        // float [4]
   static constexpr uint32_t kBars = kSvm + 16;
-  static constexpr uint32_t kMisc = kBars + 20 * 8;
+  static constexpr uint32_t kSlots = kBars + 24 * 8;                   // 16 bytes [2]: answers to requests for items
+  static constexpr uint32_t kMisc = kSlots + 32;
   static constexpr uint32_t kTotal = kMisc + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
   static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kPLo % 1024 == 0, "alignment");
@@ -117,6 +121,28 @@ __device__ __forceinline__ void group_sync() {
 __device__ __forceinline__ bool group_any(bool x) {
   __syncwarp();
   return dsa::named_bar_any(1, kSoftThreads, x);
+}
+
+// Asks for the block index of a CTA of this grid that has not started and no
+// longer will; the answer (16 bytes) arrives at the barrier.
+__device__ __forceinline__ void take_cta(const void* slot, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   dsa::smem_u32(slot)),
+               "r"(dsa::smem_u32(bar))
+               : "memory");
+}
+// The answer: a block index, or -1 when all have started.
+__device__ __forceinline__ int taken_cta(const void* slot) {
+  const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(slot);
+  int x = -1;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n mov.b128 h, {%1, %2};\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}"
+      : "+r"(x)
+      : "l"(r.x), "l"(r.y)
+      : "memory");
+  return x;
 }
 
 // Combines v[0..7] (one value per head hb + i) over the 8 lanes that share
@@ -202,6 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   uint64_t* q_full = bars + 17;
   uint64_t* q_empty = bars + 18;
   uint64_t* q_read = bars + 19;    // the query's rows have been converted
+  uint64_t* sched_full = bars + 20;   // [2]: the answer to a request for an item is there
+  uint64_t* sched_empty = bars + 22;  // [2]: every warp has read it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
@@ -216,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       dsa::mbar_init(&s_empty[b], kSoftWarps);
       dsa::mbar_init(&p_empty[b], 1);
       dsa::mbar_init(&drain[b], 1);
+      dsa::mbar_init(&sched_full[b], 1);
+      dsa::mbar_init(&sched_empty[b], kThreads / 32);
     }
     dsa::mbar_init(p_full, kSoftWarps);
     dsa::mbar_init(q_full, kGatherWarps);
@@ -231,6 +261,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   const uint32_t tmem_base = *tmem_slot;
   const dsa::Waiter wt = dsa::make_waiter(abort_flag, p.status);
   const int t_end = p.g.table ? __ldg(p.g.cu + p.g.n_seqs) : INT_MAX;
+  // The item after this CTA's n-th, -1 if there is none: that of a CTA that has
+  // not started, which the request of the n-th item took over.  Taken in turn
+  // like this, slower SMs work fewer rows.  Every warp asks once per item;
+  // *heard = false if the wait gave up.
+  auto next_item = [&](int n, bool* heard) {
+    if (!p.steal) return -1;
+    *heard = dsa::mbar_wait_warp(&sched_full[n & 1], (n >> 1) & 1, wt);
+    if (!*heard) return -1;
+    const int got = taken_cta(smem + S::kSlots + (n & 1) * 16);
+    __syncwarp();
+    if (lane == 0) dsa::mbar_arrive(&sched_empty[n & 1]);
+    __syncwarp();
+    return got;
+  };
 
   if (warp < kGatherWarps) {
     // ------------------------------------------------------------ gather
@@ -331,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     };
     // L2 prefetch of a later item's query and ids
     auto prefetch_item = [&](int it) {
-      if (it >= p.n_items) return;
       const Item w = get_item(p, it, t_end);
       if (w.i0 >= w.i1) return;
       const uint8_t* q0 = reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK);
@@ -339,9 +382,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const int j = w.i0 * kTile + gt * 32;
       if (j < min(w.i1 * kTile, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
     };
-    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+    // The request for the item after the n-th goes out as that one begins (not
+    // again after the answer that there is none).
+    int requests = 0;
+    auto request = [&](int n) {
+      if (!p.steal) return true;
+      if (n >= 2 && !dsa::mbar_wait_warp(&sched_empty[n & 1], ((n >> 1) & 1) ^ 1, wt)) return false;
+      if (lane == 0) {
+        dsa::mbar_expect_tx(&sched_full[n & 1], 16);
+        take_cta(smem + S::kSlots + (n & 1) * 16, &sched_full[n & 1]);
+      }
+      __syncwarp();
+      ++requests;
+      return true;
+    };
+    int it = blockIdx.x;
+    for (int n = 0; it >= 0 && ok; ++n) {
+      if (warp == 0 && !request(n)) break;
       const Item w = get_item(p, it, t_end);
-      if (w.i0 >= w.i1) continue;
+      if (w.i0 >= w.i1) {
+        it = next_item(n, &ok);
+        continue;
+      }
       const int b = p.g.table ? dsa::kv8_seq_warp(p.g.cu, p.g.n_seqs, w.t) : 0;
       const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
       auto load_id = [&](int i, int kg) {
@@ -427,11 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             break;
           }
           ++item_ctr;
-          prefetch_item(it + gridDim.x);
+          it = next_item(n, &ok);
+          if (!ok) break;
+          if (it >= 0) prefetch_item(it);
         }
       }
     }
     cp_async_wait_all();  // nothing of this thread is in flight when it leaves
+    if (requests > 0 && lane == 0) dsa::mbar_drain(&sched_full[(requests - 1) & 1], ((requests - 1) >> 1) & 1, p.status);
+    __syncwarp();
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // Two warps, one per product, each converged with one elected issuer.
@@ -445,8 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const uint64_t qt_desc = dsa::smem_desc(base + S::kQTail, 16, 512, dsa::kSwizzle64B);
       const uint64_t kt_desc = dsa::smem_desc(base + S::kKv + S::kTailOff, 16, 512, dsa::kSwizzle64B);
       int tile_ctr = 0, item_ctr = 0;
-      for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+      int it = blockIdx.x;
+      for (int n = 0; it >= 0 && ok; ++n) {
         const Item w = get_item(p, it, t_end);
+        it = next_item(n, &ok);
+        if (!ok) break;
         if (w.i0 >= w.i1) continue;
         if (!dsa::mbar_wait_warp(q_full, item_ctr & 1, wt)) break;
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
@@ -493,8 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
       const uint64_t ph_desc = dsa::smem_desc(base + S::kPHi, kPPart, 512, dsa::kSwizzle64B);
       const uint64_t pl_desc = dsa::smem_desc(base + S::kPLo, kPPart, 512, dsa::kSwizzle64B);
-      for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+      int it = blockIdx.x;
+      for (int n = 0; it >= 0 && ok; ++n) {
         const Item w = get_item(p, it, t_end);
+        it = next_item(n, &ok);
+        if (!ok) break;
         if (w.i0 < w.i1) half_ctr += 2;  // the query's use of a buffer
         for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
           const int half = half_ctr & 1, b = (half_ctr >> 1) & 1;
@@ -547,10 +619,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     // point that reduces the flag (see the bf16 kernel).
     bool failed = false;
     Item next = get_item(p, blockIdx.x, t_end);
-    for (int it = blockIdx.x; it < p.n_items && ok; it += gridDim.x) {
+    int it = blockIdx.x;
+    for (int n = 0; it >= 0 && ok; ++n) {
       const Item w = next;
       const bool empty = w.dead || w.i0 >= w.i1;
-      if (empty && it + gridDim.x < p.n_items) next = get_item(p, it + gridDim.x, t_end);
+      if (empty) {
+        bool heard = true;
+        it = next_item(n, &heard);
+        failed |= !heard;
+        if (p.steal && group_any(failed)) {  // the group leaves together
+          ok = false;
+          break;
+        }
+        if (it >= 0) next = get_item(p, it, t_end);
+      }
       if (w.dead) continue;
       const int64_t orow = static_cast<int64_t>(w.t) * p.H + w.h0;
       if (empty) {
@@ -746,7 +828,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       if (!ok) break;
 
       // ---------------------------------------------------------- epilogue
-      if (it + gridDim.x < p.n_items) next = get_item(p, it + gridDim.x, t_end);
+      bool heard = true;
+      it = next_item(n, &heard);
+      failed |= !heard;
+      if (it >= 0) next = get_item(p, it, t_end);
       const float sink = p.sink && st < w.hv ? __ldg(p.sink + w.h0 + st) : -INFINITY;
       // The sums' norm, while the last tile's MMA2 runs: over the four quarters
       // in wmax, once everybody has read the last references there.
@@ -972,7 +1057,7 @@ int launch_form(const Params& p, int T, int sms, cudaStream_t stream) {
       return dsa::launch_error("attn_kv8_kernel smem attribute");
     ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
-  kernel<<<p.n_items < sms ? p.n_items : sms, kThreads, smem, stream>>>(p);
+  kernel<<<p.n_items, kThreads, smem, stream>>>(p);
   int rc = dsa::launch_error("attn_kv8_kernel");
   if (rc != DSA_OK || p.splits == 1) return rc;
   // launched while the splits' kernel drains, so that its start-up hides behind it
@@ -1066,6 +1151,7 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   p.splits = need > 0 ? plan_splits(units, K) : 1;
   p.n_items = static_cast<int>(units * p.splits);
   p.status = dsa::device_status_ptr();
+  p.steal = p.n_items > sms;
   p.scale_log2 = scale * kLog2e;
   if (narrow_takes(T, H, Hc, K)) return launch_narrow(p, T, Dqk, stream);
   if (need > 0) {

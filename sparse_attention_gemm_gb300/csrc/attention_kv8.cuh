@@ -42,6 +42,7 @@ struct Params {
   uint32_t* status;
   int H, Hc, G, K, splits, n_items;  // G: 64-head groups per KV head
   float scale_log2;
+  bool steal;  // more items than CTAs that fit: a CTA takes over those of CTAs not yet started
 };
 
 __device__ __forceinline__ float ex2(float x) {
