@@ -43,7 +43,9 @@
 // ones' 14 items of 13.5 set the time (615 us).
 // Tried and slower: a look at the next query's largest element during this
 // item's tiles (its loads held the gather back, 2%), tiles of 64 keys in four
-// buffers (677 us), results from registers two bytes a lane (+25 us).
+// buffers (677 us), results from registers two bytes a lane (+25 us), the vote on
+// moving references through a flag and a plain barrier (+25 us) or an mbarrier
+// (+18 us) instead of the reducing barrier, weights formed before the vote is in (+40 us).
 //
 // Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
 // MMA1, 17 MMA2.
@@ -65,8 +67,8 @@ constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
 constexpr int kMma2Warp = kMmaWarp + 1;
 constexpr int kThreads = (kMma2Warp + 1) * 32;
-// 18 warps: 96 registers a thread; moving some from the gather and MMA warps
-// to the softmax ones (setmaxnreg) is not needed: no role is short of any in its loop.
+// 18 warps: 96 registers a thread.  The softmax warps hold 32 scores, and keep
+// some values that an item needs once in local memory.
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
 constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T, 64 keys
 constexpr int kTile = 2 * kKeys;                  // keys per tile: M of the score product

@@ -19,8 +19,10 @@
 // tile 2K, softmax's first reference 1.6K, results 2.3K, join 4K.  Shared memory
 // (a tile of 64 keys 36 KB, two of them) holds two CTAs, not three.  96 rows of 2 x
 // 12 heads of 256 + 256, 1027 slots: 21 us, 4.2 TB/s, in its steady part the
-// memory's rate; 1024 rows of 16 heads of 512 over documents of 341: 39 us;
-// one row of 64 heads, 2048 slots: 11.4 us (the 64-head kernel and its join: 18.4).
+// memory's rate; 1024 rows of 16 heads of 512 over documents of 341: 36 us;
+// one row of 64 heads, 2048 slots: 11.3 us (the 64-head kernel and its join: 18.4).
+// Tried and slower: the first tile's copies or the query's conversion before the
+// set-up barrier (36.7 and 36.4 us instead of 36.1 for the packed rows).
 //
 // Warps: 0..3 gather, 4..7 query conversion, softmax and epilogue, 8 MMA1, 9 MMA2.
 #include "attention_kv8.cuh"
