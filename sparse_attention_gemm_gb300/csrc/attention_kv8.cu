@@ -36,7 +36,7 @@
 // through them (copies 2K cycles, scores 1.5-2K, softmax 3-4K, value product 2K)
 // is two tiles' time, 5.2K cycles a tile at 576 dims: latency, with the tensor
 // cores at 55%.  A row's end and the next one's start cost 10K more (query
-// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 604 us, 957
+// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 600 us, 963
 // TFLOP/s of the formula's operations (half of the bf16 rate measured; 578 GFLOP).
 // A CTA that has finished takes over the item of one that has not started: SMs
 // differ by up to 8% in speed, and with every 152nd item a CTA's own the slowest
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       const uint32_t ph = ((half_ctr >> 2) & 1) ^ 1, buf = kv_addr + b * S::kBuf;
       if (!dsa::mbar_wait_warp(&kv_empty[2 * b], ph, wt) || !dsa::mbar_wait_warp(&kv_empty[2 * b + 1], ph, wt)) return false;
       const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
-#pragma unroll 6
+#pragma unroll 3
       for (int k = 0; k < 8 * kPieces / 32; ++k) {
         const int y = k * 32 + lane, h = warp * 8 + y / kPieces, c = y % kPieces;
         const bool real = h < w.hv;
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         const uint32_t rows_at = dsa::smem_u32(rows);
         const int mrow = 8 * (lane >> 4) + (lane & 7), munit = (lane >> 3) & 1;  // matrices: 8 heads x 8 dims
         __nv_bfloat16* o0 = p.out + (orow + hh * 32 + (lane >> 2)) * DV + quarter * 32 + (lane & 3) * 8;
-#pragma unroll 1
+#pragma unroll 2
         for (int mb = 0; mb < S::kNv; ++mb) {
 #pragma unroll
           for (int c0 = 0; c0 < 32; c0 += 16) {
