@@ -36,7 +36,7 @@
 // through them (copies 2K cycles, scores 1.5-2K, softmax 3-4K, value product 2K)
 // is two tiles' time, 5.2K cycles a tile at 576 dims: latency, with the tensor
 // cores at 55%.  A row's end and the next one's start cost 10K more (query
-// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 600 us, 963
+// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 596 us, 970
 // TFLOP/s of the formula's operations (half of the bf16 rate measured; 578 GFLOP).
 // A CTA that has finished takes over the item of one that has not started: SMs
 // differ by up to 8% in speed, and with every 152nd item a CTA's own the slowest
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       cp_async_wait_all();
       __syncwarp();  // (the warp's own copies)
       uint32_t m = 0;
-#pragma unroll 3
+#pragma unroll 2
       for (int k = 0; k < kUnits; ++k) {
         const int u = unit_of(k);
         m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u)), m);
