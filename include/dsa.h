@@ -596,7 +596,8 @@ int dsa_kv8_read(const void* cache, const float* scale, const int32_t* cu_seqlen
  *   workspace: dsa_sparse_attn_fwd_kv8_workspace_size bytes (0 for many
  *   shapes: then it may be NULL), 256-byte aligned, contents ignored on
  *   entry; calls that may overlap need one each.
- * Accumulation is fp32.  Results are bitwise reproducible.
+ * Accumulation is fp32.  Results are bitwise reproducible; a row's last bits
+ * may differ between calls of different T, H or K, which choose the form.
  * Shapes: (Dqk, Dv) in {(576, 512), (512, 512)} without v8, or (256, 256) with
  * it; H a multiple of Hc, H / Hc <= 128; 0 <= K <= DSA_KV8_MAX_SLOTS; scale finite > 0; q, kv8, v8,
  * out 16-byte aligned.

@@ -241,3 +241,22 @@ def test_row_does_not_depend_on_its_batch():
     d = (whole["out"][:4].float() - alone["out"].float()).abs().cpu().numpy()
     assert not (d > 2 * ref["out_tol"]).any()
     assert math.isclose(float(whole["lse"][0, 0]), float(alone["lse"][0, 0]), rel_tol=1e-5, abs_tol=1e-4)
+
+
+@pytest.mark.parametrize("H,K", [(64, 64), (64, 200), (16, 64)])
+def test_thousands_of_short_rows(H, K):
+    """200 rows (a third of them empty) thirty times over: CTAs go from item to item; the copies have the same bits, and
+    they are those of the definition within its bounds (200 rows alone may take the other form: other bits)."""
+    rng = np.random.default_rng(80 + K + H)
+    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, 200, H, 1, K, 16, False)
+    kw["length"] = np.where(np.arange(200) % 3 == 0, 0, kw["length"]).astype(np.int32)
+    ref = R.attention(f64(q), k, ks, idx, sm, length=kw["length"])
+    many = call(np.tile(q, (30, 1, 1)), k, ks, np.tile(idx, (30, 1)), sm, length=np.tile(kw["length"], 30))()
+    for n in ("out", "lse", "lse_kv"):
+        copies = many[n].view(30, 200, *many[n].shape[1:])
+        assert bool((copies == copies[0]).all()), n
+    o = many["out"][:200].float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(o).all() and not (np.abs(o - ref["out"]) > ref["out_tol"]).any()
+    g, r = many["lse"][:200].cpu().numpy().astype(np.float64), ref["lse"]
+    fin = np.isfinite(r)
+    assert np.array_equal(g[~fin], r[~fin]) and not (np.abs(g[fin] - r[fin]) > ref["lse_tol"][fin]).any()
