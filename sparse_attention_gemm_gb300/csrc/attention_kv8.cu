@@ -5,50 +5,42 @@
 //   s_j = scale * k_scale[b_j] * (q . e4m3(kv8[r_j])),
 //   out = sum_j exp(s_j) v_scale[b_j] e4m3(v8[r_j]) / (sum_j exp(s_j) + exp(sink)).
 //
-// Both products run on the codes as they lie in the cache (kind::f8f6f4): a
-// block's scale is one number per key, so it multiplies the key's scores and
-// weights afterwards and no code is ever widened in shared memory.  The other
-// operand of each product is split into two E4M3 terms:
-//   query:   q / s = hi + lo / 16, s the power of two that brings the head's
-//            largest element to (224, 448].  A bf16 significand has 8 bits, two
-//            E4M3 terms hold 4 each: exact down to 2^-14 of the scaled units.
-//   weights: w = C * exp(s_j - m) * v_scale / 2^E as hi + lo: relative error
-//            2^-8, what rounding to bf16 costs, and never less than 2^-10 / C
-//            (half the smaller term's smallest step).
+// A code is a bf16 value exactly, and a block's scale is one number per key: it
+// multiplies the key's scores and weights, and no code is rounded.  Codes
+// are widened to bf16 on their way into shared memory, and both products run in bf16
+// (kind::f16) with fp32 sums.  The one rounding before out's is that of
+// the weights exp(s_j - m) * v_scale / 2^E to bf16, as in the bf16 call; bf16
+// has fp32's exponents, so small weights keep their relative precision.
 //
 // Work item = (token, KV head, group of 64 query heads, split of its slots);
 // calls with few heads per KV head or few rows go to attention_kv8_narrow.cu.
-// Products ("swap AB"), tiles of 128 keys:
-//   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T   (M = 128 keys, N = 128)
-//   MMA2  O^T[dim, head] += V^T[dim, key] . (Phi + Plo)^T[key, head] (M = 128 dims, N = 64),
-//         a half of the tile at a time: its buffer goes back that much sooner
-// S^T (two buffers) and O^T fill TMEM.  Tiles are gathered with cp.async into
-// 128-byte-swizzled rows, in two buffers of two halves; a copy's landing is its
-// own arrival at the half's barrier, so the gather never waits for one.
+// Products ("swap AB"), tiles of 64 keys:
+//   MMA1  S^T[key, head]  = K[key, :] . Q[head, :]^T           (M = 64 keys, N = 64)
+//   MMA2  O^T[dim, head] += V^T[dim, key] . P^T[key, head]     (M = 128 dims, N = 64)
+// S^T (two buffers) and O^T live in TMEM.  Two tile buffers; eight warps load a tile's
+// codes into registers while the tile before it is worked on.
 // Softmax: as in the bf16 kernel, one reference maximum per head that moves
-// when a tile passes it by 2^kTheta, and a reference exponent E of the value
+// when a tile passes it by 2^kMove, and a reference exponent E of the value
 // scales that moves when a block's scale passes 2^E; both move the running sums.
 //
-// What bounds it.  An M = 64 product takes the tensor core as long as an M =
-// 128 one (64 cycles a K step at N = 128), so tiles of 128 keys take 18 x 64 + 32 x 53 =
-// 2.85K cycles against 2 x 2.0K of tiles of 64.  The query's two terms take
-// 72 KB of shared memory, which leaves two buffers of 128 keys: a tile's way
-// through them (copies 2K cycles, scores 1.5-2K, softmax 3-4K, value product 2K)
-// is two tiles' time, 5.2K cycles a tile at 576 dims: latency, with the tensor
-// cores at 55%.  A row's end and the next one's start cost 10K more (query
-// 1.7K + 4.8K, results 4K).  2048 rows of 64 heads, 2048 slots, 576 dims: 596 us, 970
-// TFLOP/s of the formula's operations (half of the bf16 rate measured; 578 GFLOP).
+// What bounds it: shared memory.  A tile's products read 240 KB of operands (an
+// M = 64, N = 64 step takes its 4 KB at the memory's whole rate), its codes
+// arrive as 36 KB and are stored as 72: 350 KB, 2.7K of the 3.4K cycles
+// that a tile takes; the rest is the chain of two buffers (stores 1.3K, scores 2K, softmax 1K,
+// values 1.5K).  A row's end and the next one's start cost 8K more.  2048 rows
+// of 64 heads, 2048 slots, 576 dims: 800 us, 723 TFLOP/s (578 GFLOP); with the stores left
+// out 650 us, the loads 750 us; the bf16 call on the values read back: 676 us.
+// Both products on the codes as they lie in the cache (kind::f8f6f4, query and weights as
+// two E4M3 terms each) read half as much, 596 us, but E4M3 has a smallest step:
+// weights below 2^-13.8 of the largest weight times the largest value scale were lost, and
+// with them the output of rows whose largest weight meets a small value.
+// Tried and slower: 16 gather warps of one key a thread (925 us) or in two groups of a buffer
+// each (902 us), four of four keys (1157 us), each piece's next load behind its store (1105 us).
 // A CTA that has finished takes over the item of one that has not started: SMs
 // differ by up to 8% in speed, and with every 152nd item a CTA's own the slowest
-// ones' 14 items of 13.5 set the time (615 us).
-// Tried and slower: a look at the next query's largest element during this
-// item's tiles (its loads held the gather back, 2%), tiles of 64 keys in four
-// buffers (677 us), results from registers two bytes a lane (+25 us), the vote on
-// moving references through a flag and a plain barrier (+25 us) or an mbarrier
-// (+18 us) instead of the reducing barrier, weights formed before the vote is in (+40 us).
+// ones set the time.
 //
-// Warps: 0..7 gather and query conversion, 8..15 softmax and epilogue, 16
-// MMA1, 17 MMA2.
+// Warps: 0..7 gather and query, 8..15 softmax and epilogue, 16 MMA1, 17 MMA2.
 #include "attention_kv8.cuh"
 
 namespace {
@@ -56,60 +48,48 @@ namespace {
 using namespace dsa::kv8_attn;
 
 constexpr int kHG = 64;    // query heads per group
-constexpr int kGatherWarps = 8;
-constexpr int kGatherThreads = kGatherWarps * 32;
-constexpr int kGatherKeys = kGatherThreads / 8;   // keys one gather step covers
-constexpr int kGatherSteps = kKeys / kGatherKeys;
-static_assert(kGatherSteps == 2, "a thread gathers two keys of a tile");
-constexpr int kSoftWarp0 = kGatherWarps;
+constexpr int kGatherThreads = 256;
+constexpr int kSoftWarp0 = 8;
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
 constexpr int kMma2Warp = kMmaWarp + 1;
 constexpr int kThreads = (kMma2Warp + 1) * 32;
-// 18 warps: 96 registers a thread.  The softmax warps hold 32 scores, and keep
-// some values that an item needs once in local memory.
-constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 64 heads x 128 codes
-constexpr uint32_t kPPart = kKeys * kHG;          // one E4M3 term of P^T, 64 keys
-constexpr int kTile = 2 * kKeys;                  // keys per tile: M of the score product
+constexpr uint32_t kQChunkBytes = kHG * 128;      // 64 heads x 64 dims
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSCol = 0;    // S^T buffers at columns 0 and 128 (hi 64, lo 64)
-constexpr int kOCol = 256;  // O^T blocks at 256 + 64 m
+constexpr int kSCol = 0;    // S^T buffers at columns 0 and 64
+constexpr int kOCol = 128;  // O^T blocks at 128 + 64 m
 constexpr int kMaxSplits = 32;
+// A tile whose scores pass a head's reference by more than this (in powers of two) moves it.
+constexpr float kMove = 8.0f;
 
-// A key row is kFull chunks of 128 codes (128-byte swizzle) and, at 576 dims,
-// a tail of 64 (64-byte swizzle).  MMA2 does not read the tail, so once a
-// tile's scores are done its space takes the first term of the tile's P^T; that is
-// what makes two buffers of 128 keys fit beside the query's 72 KB.
+// A tile: key rows in chunks of 64 dims, then value rows where they are
+// separate.  MMA2 does not read the key's last chunk at 576 dims, so once
+// a tile's scores are done its space takes the tile's P^T.
 template <int DQK, int DV, bool SEP>
 struct Shape {
-  static constexpr int kFull = DQK / 128;
+  static constexpr int kNk = DQK / 64;
+  static constexpr int kNv = DV / 128;  // blocks of O^T
   static constexpr bool kTail = DQK % 128 != 0;
-  static_assert(DQK % 128 == 0 || DQK % 128 == 64, "tail of 64 codes");
-  static constexpr int kNv = DV / 128;
-  static constexpr uint32_t kVOff = SEP ? kFull * 2 * kChunkBytes : 0;  // V inside a tile buffer
-  static constexpr uint32_t kTailOff = kFull * 2 * kChunkBytes;
-  static constexpr uint32_t kBuf = 2 * ((kFull + (SEP ? kNv : 0)) * kChunkBytes + (kTail ? kKeys * 64 : 0));
-  static constexpr uint32_t kQTail = kFull * kQChunkBytes;
-  static constexpr uint32_t kQBytes = kQTail + (kTail ? 2 * kHG * 64 : 0);
-  static constexpr uint32_t kKv = kQBytes;                          // [2] tiles
-  static constexpr uint32_t kPLo = kKv + 2 * kBuf;                  // [2] halves of a tile
-  static constexpr uint32_t kPHi = kTail ? kKv + kTailOff : kPLo + 2 * kPPart;  // [2] halves; of each tile buffer, or
-  static constexpr uint32_t kPHiStep = kTail ? kBuf : 0;                        // of the one in turn
-  // scale of each slot's key and, behind them, value (one number where they are one), per half of a tile; 0: no slot
-  static constexpr uint32_t kMeta = kPLo + (kTail ? 2 : 4) * kPPart;
+  static constexpr uint32_t kVOff = SEP ? kNk * kChunkBytes : 0;  // V inside a tile buffer
+  static constexpr uint32_t kBuf = (kNk + (SEP ? 2 * kNv : 0)) * kChunkBytes;
+  static constexpr uint32_t kKv = kNk * kQChunkBytes;                              // [2] tiles, behind the query
+  static constexpr uint32_t kP = kTail ? kKv + DV / 64 * kChunkBytes : kKv + 2 * kBuf;  // [2] P^T
+  static constexpr uint32_t kPStep = kTail ? kBuf : kChunkBytes;
+  static constexpr uint32_t kRows = kKv + 2 * kBuf + (kTail ? 0 : 2 * kChunkBytes);  // results, 1 KB a softmax warp
+  // scale of each slot's key and, behind them, value (one number where they are one); 0: no slot
+  static constexpr uint32_t kMeta = kRows + kSoftWarps * 1024;         // [2]
   static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
-  static constexpr uint32_t kWmax = kMeta + 4 * kMetaStep;             // float [4][64]
+  static constexpr uint32_t kWmax = kMeta + 2 * kMetaStep;             // float [4][64]
   static constexpr uint32_t kAlpha = kWmax + 1024;                     // float [64]
   static constexpr uint32_t kFac = kAlpha + 256;                       // float [64]
-  static constexpr uint32_t kQexp = kFac + 256;                        // uint8 [3][64]
-  static constexpr uint32_t kSvm = kQexp + 192;                        // float [4]
+  static constexpr uint32_t kSvm = kFac + 256;                         // float [4]
   static constexpr uint32_t kBars = kSvm + 16;
-  static constexpr uint32_t kSlots = kBars + 24 * 8;                   // 16 bytes [2]: answers to requests for items
+  static constexpr uint32_t kSlots = kBars + 20 * 8;                   // 16 bytes [2]: answers to requests for items
   static constexpr uint32_t kMisc = kSlots + 32;
   static constexpr uint32_t kTotal = kMisc + 16;
   static_assert(kTotal <= 227 * 1024, "shared memory");
-  static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kPLo % 1024 == 0, "alignment");
+  static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kP % 1024 == 0 && kSlots % 16 == 0, "alignment");
 };
 
 // The softmax warps' barrier, plain and with an OR over the group.  The
@@ -164,11 +144,9 @@ __device__ __forceinline__ float fold8(float (&v)[8], int lane, F f) {
   return v[0];
 }
 
-// Index of a thread's score of its key k (0..3) and head h (0..7), and the largest of a head's.
-__device__ __forceinline__ constexpr int at(int k, int h) { return 16 * (k >> 1) + 4 * (h >> 1) + 2 * (k & 1) + (h & 1); }
-__device__ __forceinline__ float most_of(const float (&x)[32], int h) {
-  return fmaxf(fmaxf(x[at(0, h)], x[at(1, h)]), fmaxf(x[at(2, h)], x[at(3, h)]));
-}
+// Index of a thread's score of its key k (0, 1) and head h (0..7), and the larger of a head's.
+__device__ __forceinline__ constexpr int at(int k, int h) { return 4 * (h >> 1) + 2 * k + (h & 1); }
+__device__ __forceinline__ float most_of(const float (&x)[16], int h) { return fmaxf(x[at(0, h)], x[at(1, h)]); }
 
 // One work item: the tiles [i0, i1) of row t.
 struct Item {
@@ -196,7 +174,7 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
     len = len < 0 ? 0 : (len > p.K ? p.K : len);
   }
   if (w.dead) len = 0;
-  const int nt = (len + kTile - 1) / kTile;
+  const int nt = (len + kKeys - 1) / kKeys;
   w.len = len;
   // (nt <= 2^24 and at most 32 splits: the products fit)
   w.i0 = static_cast<int>(static_cast<uint32_t>(nt) * static_cast<uint32_t>(w.split) / static_cast<uint32_t>(p.splits));
@@ -208,51 +186,51 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
 template <int DQK, int DV, bool SEP, bool kMax>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
   using S = Shape<DQK, DV, SEP>;
+  using G = Gather<DQK, DV, SEP>;
+  static_assert(G::kThreads == kGatherThreads, "gather warps");
   extern __shared__ __align__(1024) uint8_t smem[];  // the kernel has no other shared memory
   if (dsa::smem_u32(smem) & 1023u) {                 // would break every swizzle
     if (threadIdx.x == 0) atomicOr(p.status, DSA_STATUS_CHECK_FAILED);
     return;
   }
   float* wmax = reinterpret_cast<float*>(smem + S::kWmax);  // [4 quarters][64 heads]
-  // Exponents of the query scales (biased; 255: not finite) of three items in turn: the gather
-  // warps convert item n + 3's query after MMA1 of item n + 2 has run, which
-  // needed the S buffer of item n, which the softmax hands back after reading these.
-  uint8_t* qexp = smem + S::kQexp;                        // [3][64]
-  float* svm = reinterpret_cast<float*>(smem + S::kSvm);  // [4]
+  float* svm = reinterpret_cast<float*>(smem + S::kSvm);    // [4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  uint64_t* kv_full = bars;        // [4]: halves of the two tile buffers
-  uint64_t* kv_empty = bars + 4;   // [4]
-  uint64_t* s_full = bars + 8;     // [2]
-  uint64_t* s_empty = bars + 10;   // [2]
-  uint64_t* p_empty = bars + 12;   // [2]: MMA2 of the half of a tile has run
-  uint64_t* drain = bars + 14;     // [2]: the MMA issuers' exit commits
-  uint64_t* p_full = bars + 16;    // of the whole tile: its first half's products already meet rescaled sums
-  uint64_t* q_full = bars + 17;
-  uint64_t* q_empty = bars + 18;
-  uint64_t* q_read = bars + 19;    // the query's rows have been converted
-  uint64_t* sched_full = bars + 20;   // [2]: the answer to a request for an item is there
-  uint64_t* sched_empty = bars + 22;  // [2]: every warp has read it
+  uint64_t* kv_full = bars;        // [2]
+  uint64_t* kv_empty = bars + 2;   // [2]: MMA2 of the tile has run
+  uint64_t* s_full = bars + 4;     // [2]
+  uint64_t* s_empty = bars + 6;    // [2]
+  uint64_t* p_full = bars + 8;     // [2]
+  uint64_t* drain = bars + 10;     // [2]: the MMA issuers' exit commits
+  uint64_t* sched_full = bars + 12;   // [2]: the answer to a request for an item is there
+  uint64_t* sched_empty = bars + 14;  // [2]: every warp has read it
+  uint64_t* q_full = bars + 16;
+  uint64_t* q_empty = bars + 17;
+  // Of each tile's MMA2, and of each item's last one: a wait for the last tile's
+  // phase of o_tile would also pass while the tile before it still runs.  For the
+  // rescale, which waits for tile i - 1 while working on tile i, MMA2 of tile i - 2
+  // has run: it released the buffer that tile i came into.
+  uint64_t* o_tile = bars + 18;
+  uint64_t* o_item = bars + 19;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < 4; ++b) {
-      dsa::mbar_init(&kv_full[b], kGatherThreads);
-      dsa::mbar_init(&kv_empty[b], 1);
-    }
     for (int b = 0; b < 2; ++b) {
+      dsa::mbar_init(&kv_full[b], G::kWarps);
+      dsa::mbar_init(&kv_empty[b], 1);
       dsa::mbar_init(&s_full[b], 1);
       dsa::mbar_init(&s_empty[b], kSoftWarps);
-      dsa::mbar_init(&p_empty[b], 1);
+      dsa::mbar_init(&p_full[b], kSoftWarps);
       dsa::mbar_init(&drain[b], 1);
       dsa::mbar_init(&sched_full[b], 1);
       dsa::mbar_init(&sched_empty[b], kThreads / 32);
     }
-    dsa::mbar_init(p_full, kSoftWarps);
-    dsa::mbar_init(q_full, kGatherWarps);
+    dsa::mbar_init(q_full, G::kWarps);
     dsa::mbar_init(q_empty, 1);
-    dsa::mbar_init(q_read, kGatherWarps);
+    dsa::mbar_init(o_tile, 1);
+    dsa::mbar_init(o_item, 1);
     *abort_flag = 0;
     dsa::fence_barrier_init();
   }
@@ -278,102 +256,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     return got;
   };
 
-  if (warp < kGatherWarps) {
+  if (warp < G::kWarps) {
     // ------------------------------------------------------------ gather
-    // Thread gt covers piece (gt & 7) (16 codes) of keys (gt >> 3) + 32 kg of
-    // every chunk.  A row's place depends on its id and the block table: ids
-    // are read two tiles ahead, the table one tile ahead.
-    const int gt = threadIdx.x, piece = gt & 7;
-    const uint32_t kv_addr = dsa::smem_u32(smem) + S::kKv, meta_addr = dsa::smem_u32(smem) + S::kMeta;
-    int half_ctr = 0, item_ctr = 0;  // (here a unit of work is half a tile)
+    // A row's place depends on its id and the block table, its codes on both:
+    // ids are read three tiles ahead, the table two, the codes one.
+    const int gt = threadIdx.x, piece = gt & 7, key0 = gt >> 3;
+    int tile_ctr = 0, item_ctr = 0;
     bool ok = true;
-    // The query: its bf16 rows pass through a tile's buffer (ahead of the
-    // item's tiles, so that they are there when the item before leaves the
-    // operand); a warp copies and converts eight heads, four threads a head,
-    // units (16 values) sub, sub + 4, ...  Odd heads take the halves of a
-    // 128-byte row in the other order, and a head's 16-byte pieces lie in
-    // eights XOR-ed with it: eight lanes touch all banks once.
-    const int hq = gt >> 2, sub = gt & 3;
-    constexpr int kUnits = DQK / 64, kPieces = DQK / 8;
-    static_assert(kHG * DQK * 2 <= S::kBuf, "a query fits a tile's buffer");
-    // head 32 a + 8 c + 2 j + e is row 32 a + 8 j + 2 c + e of the operand,
-    // which gives each softmax thread eight consecutive heads
-    const int qrow = (hq & 32) + ((hq & 6) << 2) + ((hq >> 2) & 6) + (hq & 1);
-    auto raw_at = [&](int h, int c) { return h * (DQK * 2) + ((c & ~7) | ((c ^ h) & 7)) * 16; };
-    auto unit_of = [&](int k) { return (sub + 4 * k) ^ (k < S::kFull * 2 ? (hq & 1) * 4 : 0); };
+    // The query's rows, without a stop on the way: head 32 a + 8 c + 2 j + e is
+    // row 32 a + 8 j + 2 c + e of the operand, which gives each softmax thread
+    // eight consecutive heads.
     auto send_query = [&](const Item& w) {
-      const int b = (half_ctr >> 1) & 1;
-      const uint32_t ph = ((half_ctr >> 2) & 1) ^ 1, buf = kv_addr + b * S::kBuf;
-      if (!dsa::mbar_wait_warp(&kv_empty[2 * b], ph, wt) || !dsa::mbar_wait_warp(&kv_empty[2 * b + 1], ph, wt)) return false;
       const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
+      const uint32_t q_addr = dsa::smem_u32(smem);
+      const int h = gt >> 2;  // four threads a head, pieces of 16 bytes sub, sub + 4, ...
+      const int row = (h & 32) + ((h & 6) << 2) + ((h >> 2) & 6) + (h & 1);
+      const bool real = h < w.hv;
 #pragma unroll 3
-      for (int k = 0; k < 8 * kPieces / 32; ++k) {
-        const int y = k * 32 + lane, h = warp * 8 + y / kPieces, c = y % kPieces;
-        const bool real = h < w.hv;
-        cp_async16(buf + raw_at(h, c), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u);
+      for (int k = 0; k < DQK / 32; ++k) {
+        const int c = (gt & 3) + 4 * k;
+        cp_async16(q_addr + (c >> 3) * kQChunkBytes + dsa::sw128_offset(row, (c & 7) * 16), src + (real ? h * DQK + c * 8 : 0),
+                   real ? 16u : 0u);
       }
-      cp_async_arrive(&kv_full[2 * b]);
-      cp_async_arrive(&kv_full[2 * b + 1]);
-      half_ctr += 2;
-      return true;
-    };
-    auto convert_query = [&](int query_half, int n_item) {  // query_half: half_ctr of its buffer
-      const int b = (query_half >> 1) & 1;
-      const uint8_t* raw = smem + S::kKv + b * S::kBuf;
-      cp_async_wait_all();
-      __syncwarp();  // (the warp's own copies)
-      uint32_t m = 0;
-#pragma unroll 2
-      for (int k = 0; k < kUnits; ++k) {
-        const int u = unit_of(k);
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u)), m);
-        m = dsa::amax_bf16x8(*reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u + 1)), m);
-      }
-      m = dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = dsa::larger_half(dsa::max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2)));
-      // a head with infinity or NaN: its scores are NaN
-      const bool finite = m < 0x7F80u;
-      const float s = finite ? dsa::kv8_scale_of(__uint_as_float(m << 16)) : 1.f;
-      const float inv = dsa::pow2_inverse(s);
-      if (!dsa::mbar_wait_warp(q_empty, (n_item & 1) ^ 1, wt)) return false;
-      if (sub == 0) qexp[(n_item % 3) * 64 + hq] = finite ? static_cast<uint8_t>(__float_as_uint(s) >> 23) : 255;
-#pragma unroll 3
-      for (int k = 0; k < kUnits; ++k) {
-        const int u = unit_of(k);
-        const uint4 v0 = *reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u));
-        const uint4 v1 = *reinterpret_cast<const uint4*>(raw + raw_at(hq, 2 * u + 1));
-        const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint16_t h2[2], l2[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) split_query(wd[2 * j + e], inv, h2[e], l2[e]);
-          hi[j] = h2[0] | (static_cast<uint32_t>(h2[1]) << 16);
-          lo[j] = l2[0] | (static_cast<uint32_t>(l2[1]) << 16);
-        }
-        const bool tail = k >= S::kFull * 2;
-        const uint32_t to = tail ? S::kQTail + sw64_offset(qrow, u - S::kFull * 8)
-                                 : (u >> 3) * kQChunkBytes + dsa::sw128_offset(qrow, (u & 7) * 16);
-        // (64 rows on leaves either swizzle's phase as it is)
-        *reinterpret_cast<uint4*>(smem + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + to + kHG * (tail ? 64 : 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      dsa::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        dsa::mbar_arrive(q_full);
-        dsa::mbar_arrive(q_read);
-      }
-      if (warp == 0) {  // everybody has read the rows: the buffer goes back
-        if (!dsa::mbar_wait_warp(q_read, n_item & 1, wt)) return false;
-        if (lane == 0) {
-          dsa::mbar_arrive(&kv_empty[2 * b]);
-          dsa::mbar_arrive(&kv_empty[2 * b + 1]);
-        }
-        __syncwarp();
-      }
-      return true;
     };
     // L2 prefetch of a later item's query and ids
     auto prefetch_item = [&](int it) {
@@ -381,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       if (w.i0 >= w.i1) return;
       const uint8_t* q0 = reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK);
       for (int o = gt * 128; o < w.hv * DQK * 2; o += kGatherThreads * 128) l2_prefetch(q0 + o);
-      const int j = w.i0 * kTile + gt * 32;
-      if (j < min(w.i1 * kTile, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
+      const int j = w.i0 * kKeys + gt * 32;
+      if (j < min(w.i1 * kKeys, w.len)) l2_prefetch(p.idx + static_cast<int64_t>(w.t) * p.K + j);
     };
     // The request for the item after the n-th goes out as that one begins (not
     // again after the answer that there is none).
@@ -408,88 +312,69 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       }
       const int b = p.g.table ? dsa::kv8_seq_warp(p.g.cu, p.g.n_seqs, w.t) : 0;
       const int32_t* irow = p.idx + static_cast<int64_t>(w.t) * p.K;
-      auto load_id = [&](int i, int kg) {
-        const int j = i * kKeys + kg * kGatherKeys + (gt >> 3);
-        return j < w.len ? __ldg(irow + j) : -1;
+      auto load_id = [&](int i, int s) {
+        const int j = i * kKeys + s * G::kStep + key0;
+        return i < w.i1 && j < w.len ? __ldg(irow + j) : -1;
       };
       const int32_t* trow = p.g.table ? p.g.table + static_cast<int64_t>(b) * p.g.max_blocks : nullptr;
       auto load_block = [&](int id) {  // as the table holds it; -1 beyond the table
         const int page = id >> p.g.lb;
         return !trow || id < 0 ? page : page < p.g.max_blocks ? __ldg(trow + page) : -1;
       };
-      // id of this tile's and the next tile's keys, table entry of this tile's:
-      // loaded one tile before they are looked at
-      int id[kGatherSteps], nid[kGatherSteps], blk[kGatherSteps];
+      auto row_of = [&](int id, int blk) {
+        return id >= 0 && blk >= 0 && blk < p.g.n_blocks ? (blk << p.g.lb) + (id & ((1 << p.g.lb) - 1)) : -1;
+      };
+      // codes of tile i, id and table entry of tile i + 1's keys, id of tile i + 2's
+      G codes;
+      int id[2], nid[2], blk[2], r[2];
 #pragma unroll
-      for (int kg = 0; kg < kGatherSteps; ++kg) {
-        nid[kg] = load_id(2 * w.i0 + 1, kg);
-        id[kg] = load_id(2 * w.i0, kg);
-        blk[kg] = load_block(id[kg]);
+      for (int s = 0; s < 2; ++s) {
+        r[s] = load_id(w.i0, s);
+        id[s] = load_id(w.i0 + 1, s);
+        nid[s] = load_id(w.i0 + 2, s);
       }
-      // The query comes before the first tile, and is converted before that is
-      // copied, whose buffer is not free sooner; a CTA's first query behind it.
-      const int query_half = half_ctr;
-      ok = send_query(w) && (item_ctr == 0 || convert_query(query_half, item_ctr));
-      if (!ok) break;
-      for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
-        const int stage = half_ctr & 3;
-        int cur[kGatherSteps];
 #pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) {
-          cur[kg] = id[kg] >= 0 && blk[kg] >= 0 && blk[kg] < p.g.n_blocks
-                        ? (blk[kg] << p.g.lb) + (id[kg] & ((1 << p.g.lb) - 1))
-                        : -1;
-          id[kg] = nid[kg];
-          blk[kg] = load_block(nid[kg]);
-          nid[kg] = i + 2 < 2 * w.i1 ? load_id(i + 2, kg) : -1;
-        }
-        if (!dsa::mbar_wait_warp(&kv_empty[stage], ((half_ctr >> 2) & 1) ^ 1, wt)) {
+      for (int s = 0; s < 2; ++s) blk[s] = load_block(r[s]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        r[s] = row_of(r[s], blk[s]);
+        blk[s] = load_block(id[s]);
+      }
+      codes.load_keys(p, r, w.kvh, piece);
+      if (SEP) codes.load_values(p, r, w.kvh, piece);
+      // MMA1 of the item before has read its query
+      if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) break;
+      send_query(w);
+      for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+        const int buf = tile_ctr & 1;
+        if (!dsa::mbar_wait_warp(&kv_empty[buf], ((tile_ctr >> 1) & 1) ^ 1, wt)) {
           ok = false;
           break;
         }
-        const uint32_t buf = kv_addr + (stage >> 1) * S::kBuf, half = stage & 1;
-        {
-          // the scales: lanes of even and odd pieces take the two keys' (with V, those of pieces 2, 3, 6, 7 the value's)
-          const int r = piece & 1 ? cur[1] : cur[0];
-          const int64_t at = static_cast<int64_t>((r >= 0 ? r : 0) >> p.g.lb) * p.Hc + w.kvh;
-          const bool value = SEP && (piece & 2);
-          if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
-            cp_async4(meta_addr + stage * S::kMetaStep + (value ? kKeys * 4 : 0) + ((piece & 1) * kGatherKeys + (gt >> 3)) * 4,
-                      (value ? p.v_scale : p.k_scale) + at, r >= 0 ? 4u : 0u);
+        uint8_t* tile = smem + S::kKv + buf * S::kBuf;
+        codes.store_keys(tile, reinterpret_cast<float*>(smem + S::kMeta + buf * S::kMetaStep), key0, piece);
+        if (SEP) codes.store_values(tile + S::kVOff, key0, piece);
+        const bool first = i == w.i0;
+        if (first) cp_async_wait_all();
+        dsa::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          dsa::mbar_arrive(&kv_full[buf]);
+          if (first) dsa::mbar_arrive(q_full);
         }
+        __syncwarp();
+        if (i + 1 < w.i1) {
 #pragma unroll
-        for (int kg = 0; kg < kGatherSteps; ++kg) {
-          const int key = kg * kGatherKeys + (gt >> 3);
-          const uint32_t nbytes = cur[kg] >= 0 ? 16u : 0u;
-          const int64_t rh = static_cast<int64_t>(cur[kg] >= 0 ? cur[kg] : 0) * p.Hc + w.kvh;
-          // checked build: the row is inside the cache
-          if (!dsa::check(cur[kg] < (p.g.n_blocks << p.g.lb), p.status)) continue;
-          const uint8_t* krow = p.k8 + rh * DQK + piece * 16;
-          const uint32_t dst = buf + half * kChunkBytes + dsa::sw128_offset(key, piece * 16);
-#pragma unroll
-          for (int c = 0; c < S::kFull; ++c) cp_async16(dst + c * 2 * kChunkBytes, krow + c * 128, nbytes);
-          if (SEP) {
-            const uint8_t* vrow = p.v8 + rh * DV + piece * 16;
-#pragma unroll
-            for (int c = 0; c < S::kNv; ++c)
-              cp_async16(dst + S::kVOff + c * 2 * kChunkBytes, vrow + c * 128, nbytes);
+          for (int s = 0; s < 2; ++s) {
+            r[s] = row_of(id[s], blk[s]);
+            id[s] = nid[s];
+            blk[s] = load_block(nid[s]);
+            nid[s] = load_id(i + 3, s);
           }
+          codes.load_keys(p, r, w.kvh, piece);
+          if (SEP) codes.load_values(p, r, w.kvh, piece);
         }
-        if (S::kTail) {
-          // the tail's four pieces: lanes with piece 0..3 take the first key's, the others the second's
-          const bool second = piece >= 4;
-          const int key = (second ? kGatherKeys : 0) + (gt >> 3), r = second ? cur[1] : cur[0];
-          const int64_t rh = static_cast<int64_t>(r >= 0 ? r : 0) * p.Hc + w.kvh;
-          if (dsa::check(r < (p.g.n_blocks << p.g.lb), p.status))
-            cp_async16(buf + S::kTailOff + half * (kKeys * 64) + sw64_offset(key, piece & 3), p.k8 + rh * DQK + S::kFull * 128 + (piece & 3) * 16,
-                       r >= 0 ? 16u : 0u);
-        }
-        cp_async_arrive(&kv_full[stage]);
-        if (i == 2 * w.i0 + 1) {
-          if (item_ctr == 0 && !convert_query(query_half, 0)) {
-            ok = false;
-            break;
-          }
+        if (first) {
           ++item_ctr;
           it = next_item(n, &ok);
           if (!ok) break;
@@ -507,11 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const uint32_t base = dsa::smem_u32(smem);
     bool ok = true;
     if (warp == kMmaWarp) {
-      constexpr uint32_t idesc1 = dsa::idesc_e4m3(kTile, 2 * kHG);
+      constexpr uint32_t idesc1 = dsa::idesc_bf16(kKeys, kHG, 0, 0);
       const uint64_t q_desc = dsa::smem_desc(base, 16, 1024, dsa::kSwizzle128B);
       const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
-      const uint64_t qt_desc = dsa::smem_desc(base + S::kQTail, 16, 512, dsa::kSwizzle64B);
-      const uint64_t kt_desc = dsa::smem_desc(base + S::kKv + S::kTailOff, 16, 512, dsa::kSwizzle64B);
       int tile_ctr = 0, item_ctr = 0;
       int it = blockIdx.x;
       for (int n = 0; it >= 0 && ok; ++n) {
@@ -521,30 +404,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (w.i0 >= w.i1) continue;
         if (!dsa::mbar_wait_warp(q_full, item_ctr & 1, wt)) break;
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-          const int sb = tile_ctr & 1, use = tile_ctr + item_ctr + 1, b = use & 1;  // use of the tile buffers
-          const uint32_t par = (use >> 1) & 1;
-          const bool got = dsa::mbar_wait(&s_empty[sb], ((tile_ctr >> 1) & 1) ^ 1, wt) &&
-                           dsa::mbar_wait(&kv_full[2 * b], par, wt) && dsa::mbar_wait(&kv_full[2 * b + 1], par, wt);
-          // the gathered codes, before the tensor core reads them (MMA2's come
-          // with the softmax warps' arrival, behind a fence of theirs)
-          dsa::fence_proxy_async_smem();
+          const int b = tile_ctr & 1;
+          const uint32_t par = (tile_ctr >> 1) & 1;
+          const bool got = dsa::mbar_wait(&s_empty[b], par ^ 1, wt) && dsa::mbar_wait(&kv_full[b], par, wt);
           __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = kv_desc + b * (S::kBuf >> 4);
-          const uint32_t d = tmem_base + kSCol + sb * 128;
+          const uint32_t d = tmem_base + kSCol + b * kHG;
 #pragma unroll
-          for (int c = 0; c < S::kFull; ++c) {
-            const uint64_t ac = a0 + c * (2 * kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
+          for (int c = 0; c < S::kNk; ++c) {
+            const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              dsa::umma_f8_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
+              dsa::umma_bf16_if(leader && got, d, ac + kk * 2, bc + kk * 2, idesc1, (c | kk) != 0);
           }
-          if (S::kTail) {
-            const uint64_t at = kt_desc + b * (S::kBuf >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) dsa::umma_f8_if(leader && got, d, at + kk * 2, qt_desc + kk * 2, idesc1, 1u);
-          }
-          if (leader && got) dsa::umma_commit(&s_full[sb]);
+          if (leader && got) dsa::umma_commit(&s_full[b]);
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
@@ -558,38 +432,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
       if (leader) dsa::umma_drain(&drain[0], p.status);
       __syncwarp();
     } else {
-      constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kHG) | (1u << 15) | (1u << 16);  // both MN-major
-      int half_ctr = 0, tile_ctr = 0;
-      const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, 2 * kChunkBytes, 1024, dsa::kSwizzle128B);
-      // P^T rows are 64 bytes (64 heads): 64-byte swizzle, groups of 8 keys 512 bytes apart
-      const uint64_t ph_desc = dsa::smem_desc(base + S::kPHi, kPPart, 512, dsa::kSwizzle64B);
-      const uint64_t pl_desc = dsa::smem_desc(base + S::kPLo, kPPart, 512, dsa::kSwizzle64B);
+      constexpr uint32_t idesc2 = dsa::idesc_bf16(128, kHG, 1, 1);  // both MN-major
+      int tile_ctr = 0;
+      const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
+      const uint64_t p_desc = dsa::smem_desc(base + S::kP, kChunkBytes, 1024, dsa::kSwizzle128B);
       int it = blockIdx.x;
       for (int n = 0; it >= 0 && ok; ++n) {
         const Item w = get_item(p, it, t_end);
         it = next_item(n, &ok);
         if (!ok) break;
-        if (w.i0 < w.i1) half_ctr += 2;  // the query's use of a buffer
-        for (int i = 2 * w.i0; i < 2 * w.i1; ++i, ++half_ctr) {
-          const int half = half_ctr & 1, b = (half_ctr >> 1) & 1;
-          const bool got = half == 1 || dsa::mbar_wait(p_full, tile_ctr++ & 1, wt);
+        for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
+          const int b = tile_ctr & 1;
+          const bool got = dsa::mbar_wait(&p_full[b], (tile_ctr >> 1) & 1, wt);
           __syncwarp();
           dsa::tc_fence_after();
-          const uint64_t a0 = v_desc + b * (S::kBuf >> 4) + half * (kChunkBytes >> 4);
-          const uint64_t bh = ph_desc + b * (S::kPHiStep >> 4) + half * (kPPart >> 4), bl = pl_desc + half * (kPPart >> 4);
+          const uint64_t a0 = v_desc + b * (S::kBuf >> 4), b0 = p_desc + b * (S::kPStep >> 4);
 #pragma unroll
           for (int mb = 0; mb < S::kNv; ++mb) {
             const uint32_t d = tmem_base + kOCol + mb * kHG;
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 32; ++kk) {
-              const uint64_t a = a0 + mb * (2 * kChunkBytes >> 4) + kk * (32 * 128 >> 4);
-              dsa::umma_f8_if(leader && got, d, a, bh + kk * (32 * kHG >> 4), idesc2, (i > 2 * w.i0 || kk > 0) ? 1u : 0u);
-              dsa::umma_f8_if(leader && got, d, a, bl + kk * (32 * kHG >> 4), idesc2, 1u);
-            }
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              dsa::umma_bf16_if(leader && got, d, a0 + mb * (2 * kChunkBytes >> 4) + kk * (16 * 128 >> 4),
+                                b0 + kk * (16 * 128 >> 4), idesc2, (i > w.i0 || kk > 0) ? 1u : 0u);
           }
           if (leader && got) {
-            dsa::umma_commit(&p_empty[half]);
-            dsa::umma_commit(&kv_empty[half_ctr & 3]);
+            dsa::umma_commit(o_tile);
+            dsa::umma_commit(&kv_empty[b]);
+            if (i + 1 == w.i1) dsa::umma_commit(o_item);
           }
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
@@ -607,15 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     const int quarter = warp & 3;  // TMEM lane quarter
     const int hh = sw >> 2;        // head half
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // Of S^T a thread holds four keys' scores of eight heads: key k of them is
-    // row key0 + 8 k of its half of the tile, head hb + 2j + e of it is x[16 (k / 2) + 4j + 2 (k % 2) + e]
-    const int half = quarter >> 1, key0 = (quarter & 1) * 32 + (lane >> 2);
+    // S^T of 64 keys lies in the first 16 lanes of each quarter.  Of it a thread holds two keys'
+    // scores of eight heads: key0 + 8 k (k = 0, 1), and head hb + 2j + e of it is x[4j + 2k + e].
+    const int key0 = quarter * 16 + (lane >> 2);
     const int hb = hh * 32 + 8 * (lane & 3);
     // factors of O^T per head (the four warps of a head half write the same ones)
     float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
     float* fac = reinterpret_cast<float*>(smem + S::kFac);  // [64]: references, then the factors of the result
-    uint8_t* rows = smem + S::kPLo + sw * 1024;             // this warp's, of the result: 16 heads x 32 dims, 64-byte swizzle
-    int tile_ctr = 0, n_item = 0;
+    uint8_t* rows = smem + S::kRows + sw * 1024;            // this warp's, of the result: 16 heads x 32 dims, 64-byte swizzle
+    int tile_ctr = 0, item_ctr = 0;
     bool ok = true;
     // A wait of this thread gave up: the eight warps leave together, at a
     // point that reduces the flag (see the bf16 kernel).
@@ -651,7 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         continue;
       }
-      ++n_item;  // (with this one: each query used a tile's buffer)
       // Per head hb + h: the reference, this thread's keys' sum and (for max_logits) maximum.
       float nm[8], l_part[8];  // (nm: the reference, negative)
       [[maybe_unused]] float top[8];
@@ -664,67 +532,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         if (kMax) top[h] = -INFINITY;
       }
       for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
-        const int sb = tile_ctr & 1, use = tile_ctr + n_item, b = use & 1, stage = 2 * b + half;
+        const int b = tile_ctr & 1;
+        const uint32_t par = (tile_ctr >> 1) & 1;
         // the slots' scales come with the gathered tile
-        if (!failed) failed = !dsa::mbar_wait(&kv_full[stage], (use >> 1) & 1, wt);
-        const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep) + key0;
-        float sk[4];
+        if (!failed) failed = !dsa::mbar_wait(&kv_full[b], par, wt);
+        const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + b * S::kMetaStep) + key0;
+        float sk[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sk[k] = meta[8 * k] > 0.f ? meta[8 * k] : 0.f;
-        if (!failed) failed = !dsa::mbar_wait(&s_full[sb], (tile_ctr >> 1) & 1, wt);
+        for (int k = 0; k < 2; ++k) sk[k] = meta[8 * k] > 0.f ? meta[8 * k] : 0.f;
+        if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
         __syncwarp();
         dsa::tc_fence_after();
-        float x[32];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t v[16], lo[16];
-          const uint32_t ta = tmem_base + lane_off + (static_cast<uint32_t>(g * 16) << 16) + kSCol + sb * 128 + hh * 32;
-          dsa::tmem_ld16x256b_x4(ta, v);
-          dsa::tmem_ld16x256b_x4(ta + 64, lo);
+        float x[16];
+        {
+          uint32_t v[16];
+          dsa::tmem_ld16x256b_x4(tmem_base + lane_off + kSCol + b * kHG + hh * 32, v);
           dsa::tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const float2 y = fma2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
-                                  make_float2(__uint_as_float(v[r]), __uint_as_float(v[r + 1])));
-            x[16 * g + r] = y.x, x[16 * g + r + 1] = y.y;
-          }
+          for (int r = 0; r < 16; ++r) x[r] = __uint_as_float(v[r]);
         }
-        const uint2 qe = *reinterpret_cast<const uint2*>(qexp + ((n_item - 1) % 3) * 64 + hb);
         dsa::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dsa::mbar_arrive(&s_empty[sb]);
+        if (lane == 0) dsa::mbar_arrive(&s_empty[b]);
         // scores in powers of two against the references; -inf where there is no slot
 #pragma unroll
-        for (int h = 0; h < 8; h += 2) {
-          float2 q2;  // the query's scales times the softmax's (held as exponents: eight registers less)
-          q2.x = __uint_as_float(((h < 4 ? qe.x : qe.y) >> (8 * (h & 3)) & 255u) << 23);
-          q2.y = __uint_as_float(((h < 4 ? qe.x : qe.y) >> (8 * (h & 3) + 8) & 255u) << 23);
-          // (255: a head with infinity or NaN)
-          q2 = fma2(q2, make_float2(p.scale_log2, p.scale_log2), make_float2(q2.x - q2.x, q2.y - q2.y));
+        for (int k = 0; k < 2; ++k) {
+          const float c = p.scale_log2 * sk[k];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 c = mul2(q2, make_float2(sk[k], sk[k]));
-            const float2 y = fma2(make_float2(x[at(k, h)], x[at(k, h + 1)]), c, make_float2(nm[h], nm[h + 1]));
-            x[at(k, h)] = y.x, x[at(k, h + 1)] = y.y;
-          }
-        }
-        if (__any_sync(0xffffffffu, fminf(fminf(sk[0], sk[1]), fminf(sk[2], sk[3])) == 0.f)) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-#pragma unroll
-            for (int h = 0; h < 8; ++h) x[at(k, h)] = sk[k] > 0.f ? x[at(k, h)] : -INFINITY;
+          for (int h = 0; h < 8; h += 2) {
+            const float2 y = fma2(make_float2(x[at(k, h)], x[at(k, h + 1)]), make_float2(c, c), make_float2(nm[h], nm[h + 1]));
+            x[at(k, h)] = sk[k] > 0.f ? y.x : -INFINITY, x[at(k, h + 1)] = sk[k] > 0.f ? y.y : -INFINITY;
           }
         }
         float most = x[0], sv_most = 0.f;
 #pragma unroll
-        for (int r = 1; r < 32; ++r) most = fmaxf(most, x[r]);
+        for (int r = 1; r < 16; ++r) most = fmaxf(most, x[r]);
         if (SEP) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sk[k] = sk[k] > 0.f ? meta[kKeys + 8 * k] : 0.f;  // from here on the values' scales
+          for (int k = 0; k < 2; ++k) sk[k] = sk[k] > 0.f ? meta[kKeys + 8 * k] : 0.f;  // from here on the values' scales
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sv_most = fmaxf(sv_most, sk[k]);
-        const bool ex = unset || most > kTheta || sv_most > ref;
+        sv_most = fmaxf(sk[0], sk[1]);
+        const bool ex = unset || most > kMove || sv_most > ref;
         if constexpr (kMax) {
 #pragma unroll
           for (int h = 0; h < 8; ++h) top[h] = fmaxf(top[h], most_of(x, h) - nm[h]);
@@ -763,48 +611,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
             }
             const float tm[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int h = 4 * g4 + n;
+            for (int m = 0; m < 4; ++m) {
+              const int h = 4 * g4 + m;
               // by how much the reference moves: to the tile's maximum, if that
-              // passes it by kTheta or is the first
-              const float up = (unset ? tm[n] > -INFINITY : tm[n] > kTheta) ? tm[n] : 0.f;
+              // passes it by kMove or is the first
+              const float up = (unset ? tm[m] > -INFINITY : tm[m] > kMove) ? tm[m] : 0.f;
               const float a = unset ? 1.f : ex2(-up);
               moved |= up != 0.f;
               l_part[h] *= a;
               nm[h] -= up;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) x[at(k, h)] -= up;
+              for (int k = 0; k < 2; ++k) x[at(k, h)] -= up;
               if (lane < 4) alpha[hb + h] = a * ratio;
             }
           }
           unset = unset && !(sv_max > 0.f);
           need_rescale = __any_sync(0xffffffffu, moved) && !first;
         }
-        // P^T rows key0 + 8 k, both terms: the thread's eight heads are bytes hb .. hb + 7 of the 64-byte rows
-        if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr & 1) ^ 1, wt);  // MMA2 of the tile before has read it
-        {
-          uint8_t* ph = smem + S::kPHi + b * S::kPHiStep + half * kPPart;
-          uint8_t* pl = smem + S::kPLo + half * kPPart;
+        // P^T rows key0 + 8 k: the thread's eight heads are one 16-byte unit of a row of 64.  MMA2 of
+        // the buffer's last tile has read it: this tile came into the buffer.
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float wk = sk[k] * inv * kWeight;  // (2^-E alone stays in range)
-            uint16_t hi[4], lo[4];
+        for (int k = 0; k < 2; ++k) {
+          const float wk = sk[k] * inv;  // (2^-E alone stays in range)
+          uint32_t u[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float p0 = ex2(x[at(k, 2 * j)]), p1 = ex2(x[at(k, 2 * j + 1)]);
-              const float2 l2 = add2(make_float2(l_part[2 * j], l_part[2 * j + 1]), make_float2(p0, p1));
-              l_part[2 * j] = l2.x, l_part[2 * j + 1] = l2.y;
-              const float2 p2 = mul2(make_float2(p0, p1), make_float2(wk, wk));
-              split_weights(p2.x, p2.y, hi[j], lo[j]);
-            }
-            const uint32_t to = sw64_offset(key0 + 8 * k, hb >> 4) + (hb & 8);
-            *reinterpret_cast<uint2*>(ph + to) = pack4(hi);
-            *reinterpret_cast<uint2*>(pl + to) = pack4(lo);
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = ex2(x[at(k, 2 * j)]), p1 = ex2(x[at(k, 2 * j + 1)]);
+            const float2 l2 = add2(make_float2(l_part[2 * j], l_part[2 * j + 1]), make_float2(p0, p1));
+            l_part[2 * j] = l2.x, l_part[2 * j + 1] = l2.y;
+            const float2 p2 = mul2(make_float2(p0, p1), make_float2(wk, wk));
+            u[j] = pack_bf16x2(p2.x, p2.y);
           }
+          *reinterpret_cast<uint4*>(smem + S::kP + b * S::kPStep + dsa::sw128_offset(key0 + 8 * k, hb * 2)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
         }
         if (need_rescale) {
           // MMA2 of the previous tile must have landed before O^T is scaled
-          if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr & 1) ^ 1, wt);
+          if (!failed) failed = !dsa::mbar_wait(o_tile, (tile_ctr - 1) & 1, wt);
           __syncwarp();
           dsa::tc_fence_after();
           __syncwarp();  // alpha, written by four lanes of this warp
@@ -825,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         dsa::fence_proxy_async_smem();
         dsa::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dsa::mbar_arrive(p_full);
+        if (lane == 0) dsa::mbar_arrive(&p_full[b]);
       }
       if (!ok) break;
 
@@ -852,22 +695,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         group_sync();
         if (st < 64) m_max = fmaxf(fmaxf(wmax[st], wmax[64 + st]), fmaxf(wmax[128 + st], wmax[192 + st]));
       }
-      const float unscale = ref * (1.f / kWeight);
       if (st < 64) {
         const float mc = fac[st];
         const bool any = l != 0.f;  // true for NaN too
-        float f = unscale;
+        float f = 0.f;
         if (p.splits > 1) {
+          // a split's mean value, which stays in range where the sum might not
+          if (any) f = ref / l;
           if (st < w.hv) p.part_s[(orow + st) * p.splits + w.split] = make_float4(mc, l, m_max, 0.f);
         } else {
           const float sk = sink * kLog2e;
           float lse_v = sink, lkv = INFINITY;
-          f = 0.f;
           if (any) {
             const float M = fmaxf(mc, sk);
             const float a = exp2f(mc - M);
             const float z = l * a + exp2f(sk - M);
-            f = a / z * unscale;
+            f = a / z * ref;
             lse_v = (M + log2f(z)) * kLn2;
             lkv = (mc + log2f(l)) * kLn2;
           }
@@ -879,10 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
         }
         fac[st] = f;
       }
-      // O^T is complete with the last tile's MMA2 (each phase of p_empty has
-      // been waited for in turn, so the parity names that tile)
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[half], (tile_ctr - 1) & 1, wt);
-      if (!failed) failed = !dsa::mbar_wait(&p_empty[half ^ 1], (tile_ctr - 1) & 1, wt);
+      // O^T is complete with the last tile's MMA2
+      if (!failed) failed = !dsa::mbar_wait(o_item, item_ctr & 1, wt);
+      ++item_ctr;
       group_sync();
       dsa::tc_fence_after();
       const int hcount = min(32, w.hv - hh * 32);
@@ -967,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
 }
 
 // Joins the splits of one (token, head) per CTA: with M the largest reference,
-// z = sum_s 2^(m_s - M) l_s + 2^(sink - M), out = sum_s 2^(m_s - M) O_s / z.
+// a_s = 2^(m_s - M) l_s and z = sum_s a_s + 2^(sink - M), out = sum_s a_s O_s / z of the splits' means O_s.
 template <int DV>
 __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
@@ -987,8 +829,8 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
   const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
   const bool any = __any_sync(0xffffffffu, have);
   const float M = fmaxf(m, sk);
-  const float a = have ? exp2f(s.x - M) : 0.f;
-  float l = have ? s.y * a : 0.f;
+  const float a = have ? s.y * exp2f(s.x - M) : 0.f;  // the split's share of the sum
+  float l = a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float z = any ? l + exp2f(sk - M) : 1.f;
@@ -1016,15 +858,15 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
 }
 
 // Splits of each row's slots: the number that makes the longest CTA shortest,
-// counting a wave of CTAs as its tiles plus kItemTiles tiles for the query's
-// conversion, the first gather and the epilogue, and joining as kJoinTiles
-// tiles plus one per 16 splits.  Measured (rows of 576, 2048 slots, 128 heads;
-// microseconds with 1, 2, 4, 8, 16 splits): 16 rows 49, 34, 25, 31, 49; 32 rows 50,
-// 37, 42, 58, 85; 100 rows 96, 98, 118, 160, 248.
-constexpr int kItemTiles = 5, kJoinTiles = 3;
+// counting a wave of CTAs as its tiles plus kItemTiles tiles for the first loads,
+// the query and the epilogue, and joining as kJoinTiles tiles plus one per 16
+// splits.  Measured (rows of 576, 2048 slots, 128 heads; microseconds with 1, 2, 4, 8, 16 splits):
+// 16 rows 64, 41, 28, 35, 49; 32 rows 74, 48, 52, 66; 100 rows 142, 133, 135 (the last with 3).
+// One row of 64 heads, 65536 slots: 1696, 854, 432, 221, 117, and 66 with 32.
+constexpr int kItemTiles = 6, kJoinTiles = 5;
 
 int plan_splits(int64_t units, int K) {
-  const int nt = (K + kTile - 1) / kTile;
+  const int nt = (K + kKeys - 1) / kKeys;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxSplits && s <= nt; ++s) {

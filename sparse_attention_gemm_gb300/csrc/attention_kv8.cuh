@@ -131,6 +131,99 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint16_t& hi, 
   lo = e4m3x2_h2(h2_bits(__hsub2(h, h2_of(h2_of_e4m3x2(hi)))));
 }
 
+// Two codes -> two bf16 values, exactly: a code's 4 significant bits leave
+// the lower half of its fp32 form zero, so the upper halves are the bf16 ones
+// (NaN too), and a byte permute takes them.
+__device__ __forceinline__ uint32_t bf2_of_e4m3x2(uint32_t c) {
+  const float2 f = f2_of_e4m3x2(static_cast<uint16_t>(c));
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The gather of a tile of 64 keys by eight warps: thread gt takes piece (gt &
+// 7) (16 codes) of keys (gt >> 3) and (gt >> 3) + 32 of every 128 dims.  The
+// codes of a tile are loaded into registers a tile ahead and widened as they
+// are stored: chunks of 64 dims, rows of 128 bytes, 128-byte swizzle.
+template <int DQK, int DV, bool SEP>
+struct Gather {
+  static constexpr int kWarps = 8, kThreads = kWarps * 32, kStep = kThreads / 8;
+  static constexpr int kFull = DQK / 128, kNv = SEP ? DV / 128 : 0;
+  static constexpr bool kTail = DQK % 128 != 0;
+  static_assert(2 * kStep == kKeys, "a thread gathers two keys of a tile");
+  uint4 k[kFull][2], v[SEP ? kNv : 1][2], tail;
+  float scale;  // of one of the two keys (pieces 0 and 1) or values (pieces 2 and 3)
+
+  // Rows r[0], r[1] of the cache (-1: none, zeros without reading).
+  __device__ __forceinline__ void load_keys(const Params& p, const int (&r)[2], int kvh, int piece) {
+    const int rows = p.g.n_blocks << p.g.lb;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bool have = r[s] >= 0 && dsa::check(r[s] < rows, p.status);
+      const uint8_t* src = p.k8 + (static_cast<int64_t>(have ? r[s] : 0) * p.Hc + kvh) * DQK + piece * 16;
+#pragma unroll
+      for (int c = 0; c < kFull; ++c)
+        k[c][s] = have ? __ldcg(reinterpret_cast<const uint4*>(src + c * 128)) : make_uint4(0, 0, 0, 0);
+    }
+    if (kTail) {  // its four pieces: threads with piece 0..3 take the first key's, the others the second's
+      const int x = piece >= 4 ? r[1] : r[0];
+      const bool have = x >= 0 && dsa::check(x < rows, p.status);
+      const uint8_t* src = p.k8 + (static_cast<int64_t>(have ? x : 0) * p.Hc + kvh) * DQK + kFull * 128 + (piece & 3) * 16;
+      tail = have ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    }
+    scale = 0.f;
+    if (piece < (SEP ? 4 : 2)) {
+      const int x = piece & 1 ? r[1] : r[0];
+      if (x >= 0 && dsa::check(x < rows, p.status))
+        scale = __ldg((SEP && piece >= 2 ? p.v_scale : p.k_scale) + static_cast<int64_t>(x >> p.g.lb) * p.Hc + kvh);
+    }
+  }
+  __device__ __forceinline__ void load_values(const Params& p, const int (&r)[2], int kvh, int piece) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bool have = r[s] >= 0 && dsa::check(r[s] < (p.g.n_blocks << p.g.lb), p.status);
+      const uint8_t* src = p.v8 + (static_cast<int64_t>(have ? r[s] : 0) * p.Hc + kvh) * DV + piece * 16;
+#pragma unroll
+      for (int c = 0; c < kNv; ++c)
+        v[c][s] = have ? __ldcg(reinterpret_cast<const uint4*>(src + c * 128)) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // 16 codes to two units of 16 bytes of a row.  Lanes of the upper pieces
+  // store the second unit first: eight lanes (a row) touch all banks once.
+  static __device__ __forceinline__ void widen(const uint4& c, uint8_t* chunk, int key, int piece) {
+    const bool up = (piece & 4) != 0;
+    const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      o[2 * n] = bf2_of_e4m3x2(w[n]);
+      o[2 * n + 1] = bf2_of_e4m3x2(w[n] >> 16);
+    }
+    const int unit = (piece & 3) * 2 + (up ? 1 : 0);
+    *reinterpret_cast<uint4*>(chunk + sw128_offset(key, unit * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(chunk + sw128_offset(key, (unit ^ 1) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  // meta: the scale of each slot's key and, behind them, value; 0: no slot.
+  __device__ __forceinline__ void store_keys(uint8_t* buf, float* meta, int key0, int piece) const {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int c = 0; c < kFull; ++c)
+        widen(k[c][s], buf + (2 * c + (piece >> 2)) * kChunkBytes, key0 + s * kStep, piece);
+    if (kTail) widen(tail, buf + 2 * kFull * kChunkBytes, key0 + (piece >> 2) * kStep, piece);
+    if (piece < (SEP ? 4 : 2)) meta[(piece >> 1) * kKeys + (piece & 1) * kStep + key0] = scale;
+  }
+  __device__ __forceinline__ void store_values(uint8_t* buf, int key0, int piece) const {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int c = 0; c < kNv; ++c)
+        widen(v[c][s], buf + (2 * c + (piece >> 2)) * kChunkBytes, key0 + s * kStep, piece);
+  }
+};
+
 // Attention in groups of 16 heads (attention_kv8_narrow.cu): whether it takes
 // a call, and the launch.
 bool narrow_takes(int T, int H, int Hc, int K);
