@@ -11,16 +11,9 @@ namespace dsa {
 namespace kv8_attn {
 
 constexpr int kKeys = 64;  // keys per tile
-constexpr uint32_t kChunkBytes = kKeys * 128;  // 64 keys x 128 codes
+constexpr uint32_t kChunkBytes = kKeys * 128;  // 64 keys x 64 dims
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Weights reach 2^kTheta before the reference moves; kWeight puts that at
-// E4M3's largest, 448, and leaves an error of 2^-10 / kWeight < 2^-13.8 of a
-// weight of 1 where the smaller term's step ends.  (kTheta = 4, kWeight = 16:
-// the reference of some head moved in a third of the tiles of the drawn
-// prompts, at 2K cycles a time.)
-constexpr float kTheta = 5.0f;
-constexpr float kWeight = 14.0f;
 constexpr int kPlanSms = 152;
 
 struct Params {
@@ -84,9 +77,7 @@ __device__ __forceinline__ bool elect_sync() {
   return is != 0;
 }
 
-// 16-byte global -> shared copy; src_bytes = 0 fills zeros without reading.  No
-// cache policy: it is a uniform operand of the instruction, and with the tail
-// copied by half a warp's lanes some builds stopped at an illegal instruction.
+// 16-byte global -> shared copy; src_bytes = 0 fills zeros without reading.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
@@ -124,12 +115,6 @@ __device__ __forceinline__ void split_query(uint32_t u, float inv, uint16_t& hi,
   hi = e4m3x2_h2(h2_bits(h));
   lo = e4m3x2_h2(h2_bits(__hmul2(__hsub2(h, h2_of(h2_of_e4m3x2(hi))), __float2half2_rn(16.f))));
 }
-// The two terms of a pair of weights.
-__device__ __forceinline__ void split_weights(float w0, float w1, uint16_t& hi, uint16_t& lo) {
-  const __half2 h = __floats2half2_rn(w0, w1);
-  hi = e4m3x2_h2(h2_bits(h));
-  lo = e4m3x2_h2(h2_bits(__hsub2(h, h2_of(h2_of_e4m3x2(hi)))));
-}
 
 // Two codes -> two bf16 values, exactly: a code's 4 significant bits leave
 // the lower half of its fp32 form zero, so the upper halves are the bf16 ones
@@ -141,6 +126,38 @@ __device__ __forceinline__ uint32_t bf2_of_e4m3x2(uint32_t c) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// A piece of 16 codes (of 8 in 128 dims, lane & 7) to two units of 16 bytes of
+// row `key` of a chunk of 64 dims.  Lanes of the upper pieces store the second
+// unit first: eight lanes (a row) touch all banks once.
+__device__ __forceinline__ void widen(const uint4& c, uint8_t* chunk, int key, int piece) {
+  const bool up = (piece & 4) != 0;
+  const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    o[2 * n] = bf2_of_e4m3x2(w[n]);
+    o[2 * n + 1] = bf2_of_e4m3x2(w[n] >> 16);
+  }
+  const int unit = (piece & 3) * 2 + (up ? 1 : 0);
+  *reinterpret_cast<uint4*>(chunk + sw128_offset(key, unit * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(chunk + sw128_offset(key, (unit ^ 1) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The two terms of a pair of weights: E4M3, and what it leaves in E5M2.
+__device__ __forceinline__ void split_weights(float w0, float w1, uint16_t& hi, uint16_t& lo) {
+  const __half2 h = __floats2half2_rn(w0, w1);
+  hi = e4m3x2_h2(h2_bits(h));
+  lo = e5m2x2_h2(h2_bits(__hsub2(h, h2_of(h2_of_e4m3x2(hi)))));
+}
+// x (> 0, finite) as 2^e * f, f in (1/2, 1].
+__device__ __forceinline__ float2 scale_parts(float x) {
+  const bool small = x < 1.17549435e-38f;  // below 2^-126
+  const uint32_t u = __float_as_uint(small ? x * 4294967296.f : x);
+  const bool one = (u & 0x7FFFFFu) == 0;
+  return make_float2(static_cast<float>(static_cast<int>(u >> 23) - (one ? 127 : 126) - (small ? 32 : 0)),
+                     __uint_as_float(one ? 0x3F800000u : 0x3F000000u | (u & 0x7FFFFFu)));
 }
 
 // The gather of a tile of 64 keys by eight warps: thread gt takes piece (gt &
@@ -189,21 +206,6 @@ struct Gather {
       for (int c = 0; c < kNv; ++c)
         v[c][s] = have ? __ldcg(reinterpret_cast<const uint4*>(src + c * 128)) : make_uint4(0, 0, 0, 0);
     }
-  }
-  // 16 codes to two units of 16 bytes of a row.  Lanes of the upper pieces
-  // store the second unit first: eight lanes (a row) touch all banks once.
-  static __device__ __forceinline__ void widen(const uint4& c, uint8_t* chunk, int key, int piece) {
-    const bool up = (piece & 4) != 0;
-    const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      o[2 * n] = bf2_of_e4m3x2(w[n]);
-      o[2 * n + 1] = bf2_of_e4m3x2(w[n] >> 16);
-    }
-    const int unit = (piece & 3) * 2 + (up ? 1 : 0);
-    *reinterpret_cast<uint4*>(chunk + sw128_offset(key, unit * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(chunk + sw128_offset(key, (unit ^ 1) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
   // meta: the scale of each slot's key and, behind them, value; 0: no slot.
   __device__ __forceinline__ void store_keys(uint8_t* buf, float* meta, int key0, int piece) const {

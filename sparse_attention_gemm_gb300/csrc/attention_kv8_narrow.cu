@@ -1,26 +1,43 @@
 // attention_kv8_narrow.cu -- sparse attention over the 8-bit block cache in
-// groups of 16 query heads: the mathematics of attention_kv8.cu (scores from
-// the codes, query and weights as two E4M3 terms, one moving reference), for
-// calls whose KV heads serve at most 16 query heads and for calls of few rows.
+// groups of 16 query heads, for calls whose KV heads serve at most 16 query
+// heads and for calls of few rows.
+//
+// Both products run on the codes as they lie in the cache (kind::f8f6f4): with
+// 16 heads, what counts is that two CTAs of two or three tiles each fit an
+// SM, and widened codes would not.  The other operands are sums of 8-bit terms.
+//   query:   q / s = hi + lo / 16 in E4M3, s the power of two that brings the head's
+//            largest element to (224, 448].  Exact (8 bits) down to 2^-14 of
+//            that, off by at most 2^-22 of it below.
+//   weights: w = 14 * 2^(x - R), x the score and the value's scale together in powers of two
+//            and R a reference of the head's x, one of two places: itself where it is
+//            2^-6 or more, else 2^14 times itself, each with an accumulator of its own.
+//            There it is an E4M3 term and, for what that leaves, one in E5M2: off by at
+//            most 2^-8 of itself, as bf16 would be, for 29 powers of two from the
+//            largest 448 down; below by at most 2^-31 of the largest that R stands for.
+//            (One place of two E4M3 terms ended at 2^-13.8 of the largest weight times the largest scale:
+//            rows whose largest weight meets a small value lost their output.)
+// The sum of exp(s_j) has a reference m of its own, since scales do not enter it.
+// Both are whole numbers: 2^(R - m), which joins them at the end, is exact.
 //
 // One work item (token, KV head, 16 heads, split of its slots) per CTA, two
-// CTAs on an SM: with 16 heads a tile's products, softmax and query are a
-// quarter of the 64-head kernel's, so an item is a chain of latencies (ids,
+// CTAs on an SM: an item is a chain of latencies (ids,
 // table, gather, scores, weights, sums), and what hides one CTA's is the other.
 //   MMA1  S^T[key, hi|lo head] = K[key, :] . Q[hi|lo head, :]^T  (M = 64 keys, N = 32)
-//   MMA2  O^T[dim, hi|lo head] += V^T[dim, key] . P^T[key, hi|lo head]  (M = 128 dims, N = 32)
-// Hi and lo of the weights are the two halves of one operand; the halves of O^T
-// are added when it is read, which costs 16 columns of TMEM instead of an instruction.
-// Splits of a row are the CTAs of a cluster: each leaves its sums in its own
+//   MMA2  O^T[dim, place|place head] += V^T[dim, key] . P^T[key, place|place head]
+//         (M = 128 dims, N = 32), once for each term
+// Splits of a row are the CTAs of a cluster: each leaves its mean value in its own
 // shared memory, and each joins the dims of its rank from everyone's.  No
 // second kernel, no workspace, and the order of the sum is the ranks'.
-// What bounds it: 1.5K cycles of a pair of CTAs a tile (copies in flight), and
+// What bounds it: 1.8K cycles of a pair of CTAs a tile (copies in flight, the weights' terms), and
 // what an item does once, 10K cycles: first loads 4K (ids, table entries), first
-// tile 2K, softmax's first reference 1.6K, results 2.3K, join 4K.  Shared memory
+// tile 2K, softmax's first references 1.6K, results 2.3K, join 4K.  Shared memory
 // (a tile of 64 keys 36 KB, two of them) holds two CTAs, not three.  96 rows of 2 x
-// 12 heads of 256 + 256, 1027 slots: 21 us, 4.2 TB/s, in its steady part the
-// memory's rate; 1024 rows of 16 heads of 512 over documents of 341: 36 us;
-// one row of 64 heads, 2048 slots: 11.3 us (the 64-head kernel and its join: 18.4).
+// 12 heads of 256 + 256, 1027 slots: 24.8 us, 3.6 TB/s; 1024 rows of 16 heads of 512 over
+// documents of 341: 41.4 us; one row of 64 heads, 2048 slots: 12.6 us (the 64-head
+// kernel and its join: 14.4).  With weights of one place of two E4M3 terms, which lost
+// small ones: 20.8, 36.2 and 11.2 us.  Codes widened to bf16, weights in bf16 (eight gather warps,
+// one tile buffer): 38.3, 56.8 and 15.5 us; only the values widened, a block of 128 dims at a
+// time: 31.8, 63.5 and 16.2.
 // Tried and slower: the first tile's copies or the query's conversion before the
 // set-up barrier (36.7 and 36.4 us instead of 36.1 for the packed rows).
 //
@@ -41,11 +58,16 @@ constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kGatherWarps + kSoftWarps;
 constexpr int kThreads = (kMmaWarp + 2) * 32;
 constexpr uint32_t kQChunkBytes = 2 * kHG * 128;  // hi and lo of 16 heads x 128 codes
-constexpr uint32_t kPBytes = kKeys * 2 * kHG;     // both E4M3 terms of P^T
+constexpr uint32_t kPBytes = kKeys * 2 * kHG;     // one term of P^T, both places
 constexpr uint32_t kSwizzle32B = 6;
 constexpr int kCols = 2 * kHG;  // TMEM columns of one S^T buffer or one block of O^T
 constexpr int kOCol = 2 * kCols;
 constexpr int kMaxCluster = 8;
+// A reference moves when a tile passes it by more than this (powers of two).
+// Weights then reach 14 * 2^5, E4M3's largest.
+constexpr float kMoveR = 5.0f, kMoveM = 16.0f;
+constexpr float kWeight = 14.0f;
+constexpr float kLow = 0.015625f, kLowScale = 16384.0f;  // weights below 2^-6 go to the second place, times 2^14
 
 template <int DQK, int DV, bool SEP>
 struct Shape {
@@ -60,24 +82,27 @@ struct Shape {
   static constexpr uint32_t kKv = 0;
   static constexpr uint32_t kQ = kStages * kBuf;
   static constexpr uint32_t kQTail = kQ + kFull * kQChunkBytes;
-  static constexpr uint32_t kP = kQTail + (kTail ? 2 * kHG * 64 : 0);  // [2]
+  static constexpr uint32_t kP = kQTail + (kTail ? 2 * kHG * 64 : 0);  // [kPBufs][2 terms]
+  static constexpr int kPBufs = SEP ? 1 : 2;
   // scale of each slot's key and, behind them, value (one number where they are one); 0: no slot
-  static constexpr uint32_t kMeta = kP + 2 * kPBytes;
+  static constexpr uint32_t kMeta = kP + kPBufs * 2 * kPBytes;
   static constexpr uint32_t kMetaStep = kKeys * (SEP ? 8 : 4);
   static constexpr uint32_t kWmax = kMeta + kStages * kMetaStep;  // float [4][16]
-  static constexpr uint32_t kRed = kWmax + 256;                   // float [4][16] sums
+  static constexpr uint32_t kYmax = kWmax + 256;                  // float [4][16]
+  static constexpr uint32_t kRed = kYmax + 256;                   // float [4][16] sums
   static constexpr uint32_t kRedM = kRed + 256;                   // float [4][16] maxima
   static constexpr uint32_t kAlpha = kRedM + 256;                 // float [16]
   static constexpr uint32_t kFac = kAlpha + 64;                   // float [16]
-  static constexpr uint32_t kStats = kFac + 64;                   // float4 [16]: reference, sum, maximum, sink
+  static constexpr uint32_t kFacR = kFac + 64;                    // float [16]
+  static constexpr uint32_t kStats = kFacR + 64;                  // float4 [16]: reference, sum, maximum, sink
   static constexpr uint32_t kSvm = kStats + 256;                  // float [4]
   static constexpr uint32_t kQexp = kSvm + 16;                    // uint8 [16]
   static constexpr uint32_t kBars = kQexp + 16;
   static constexpr uint32_t kMisc = kBars + 18 * 8;
   static constexpr uint32_t kTotal = kMisc + 16;
-  static constexpr uint32_t kPart = kKv;  // float [16][DV]: a split's sums, once its products have run
+  static constexpr uint32_t kPart = kKv;  // float [16][DV]: a split's mean value, once its products have run
   static_assert(kTotal <= (228 * 1024) / 2 - 1024, "two CTAs' shared memory");
-  static_assert(kHG * DV * 4 <= kStages * kBuf, "a split's sums fit");
+  static_assert(kHG * DV * 4 <= kStages * kBuf, "a split's mean value fits");
   static_assert(kBuf % 1024 == 0 && kQ % 1024 == 0 && kP % 1024 == 0, "alignment");
 };
 
@@ -164,10 +189,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
   const int i1 = static_cast<int>(static_cast<uint32_t>(nt) * (split + 1) / p.splits);
 
   float* wmax = reinterpret_cast<float*>(smem + S::kWmax);
+  float* ymax = reinterpret_cast<float*>(smem + S::kYmax);
   float* red = reinterpret_cast<float*>(smem + S::kRed);
   float* redm = reinterpret_cast<float*>(smem + S::kRedM);
   float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
   float* fac = reinterpret_cast<float*>(smem + S::kFac);
+  float* facr = reinterpret_cast<float*>(smem + S::kFacR);
   float4* stats = reinterpret_cast<float4*>(smem + S::kStats);
   float* svm = reinterpret_cast<float*>(smem + S::kSvm);
   uint8_t* qexp = smem + S::kQexp;  // exponents of the query scales (biased; 255: not finite)
@@ -364,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       if (leader) dsa::umma_drain(&drain[0], p.status);
       __syncwarp();
     } else {
-      constexpr uint32_t idesc2 = dsa::idesc_e4m3(128, kCols) | (1u << 15) | (1u << 16);  // both MN-major
+      constexpr uint32_t idesc_hi = dsa::idesc_e4m3(128, kCols) | (1u << 15) | (1u << 16);  // both MN-major
+      constexpr uint32_t idesc_lo = idesc_hi | (1u << 10);                                  // the weights' term in E5M2
       const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
       // P^T rows are 32 bytes (hi and lo of 16 heads): 32-byte swizzle, groups of 8 keys 256 bytes apart
       const uint64_t p_desc = dsa::smem_desc(base + S::kP, kPBytes, 256, kSwizzle32B);
@@ -373,14 +401,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
         const bool got = dsa::mbar_wait(&p_full[b], (ctr >> 1) & 1, wt);
         __syncwarp();
         dsa::tc_fence_after();
-        const uint64_t a0 = v_desc + stage * (S::kBuf >> 4), b0 = p_desc + b * (kPBytes >> 4);
+        const uint64_t a0 = v_desc + stage * (S::kBuf >> 4), b0 = p_desc + (S::kPBufs == 2 ? b : 0) * (2 * kPBytes >> 4);
 #pragma unroll
         for (int mb = 0; mb < S::kNv; ++mb) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk)
-            dsa::umma_f8_if(leader && got, tmem_base + kOCol + mb * kCols,
-                            a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4), b0 + kk * (32 * kCols >> 4), idesc2,
-                            (i > i0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kKeys / 32; ++kk) {
+            const uint32_t d = tmem_base + kOCol + mb * kCols;
+            const uint64_t av = a0 + mb * (kChunkBytes >> 4) + kk * (32 * 128 >> 4), bp = b0 + kk * (32 * kCols >> 4);
+            dsa::umma_f8_if(leader && got, d, av, bp, idesc_hi, (i > i0 || kk > 0) ? 1u : 0u);
+            dsa::umma_f8_if(leader && got, d, av, bp + (kPBytes >> 4), idesc_lo, 1u);
+          }
         }
         if (leader && got) {
           dsa::umma_commit(&p_empty[b]);
@@ -433,13 +463,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
     // S^T registers 4j + e (key kA) and 4j + 2 + e (key kB) hold head hb + 2j + e
     const int kA = quarter * 16 + (lane >> 2), kB = kA + 8;
     const int hb = 4 * (lane & 3);
-    // Per head hb + h: the reference, this thread's keys' sum and maximum.
-    float m[4], l_part[4], qs[4], top[4];
-    bool unset = true;                        // no valid slot so far
-    float ref = __uint_as_float(1u << 23);    // 2^E of the value scales so far
-    float inv = __uint_as_float(253u << 23);  // 2^-E
+    // Per head hb + h: the references (of the sum and of the weighted values), this thread's keys' sum and maximum.
+    float m[4], rr[4], l_part[4], qs[4], top[4];
+    bool unset = true;  // no valid slot so far
 #pragma unroll
-    for (int h = 0; h < 4; ++h) l_part[h] = 0.f, m[h] = 0.f, qs[h] = 0.f, top[h] = -INFINITY;
+    for (int h = 0; h < 4; ++h) l_part[h] = 0.f, m[h] = 0.f, rr[h] = 0.f, qs[h] = 0.f, top[h] = -INFINITY;
     bool ok = true;
     // A wait of this thread gave up: the four warps leave together, at a
     // point that reduces the flag (see the bf16 kernel).
@@ -453,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       const float* meta = reinterpret_cast<const float*>(smem + S::kMeta + stage * S::kMetaStep);
       const float skA = meta[kA], skB = meta[kB];
       const bool vA = skA > 0.f, vB = skB > 0.f;
-      const float svA = vA ? (SEP ? meta[kKeys + kA] : skA) : 0.f, svB = vB ? (SEP ? meta[kKeys + kB] : skB) : 0.f;
+      // the values' scales as 2^ek * fk, fk in (1/2, 1]
+      const float svA = SEP ? meta[kKeys + kA] : skA, svB = SEP ? meta[kKeys + kB] : skB;
+      const float2 eA = scale_parts(vA ? svA : 1.f), eB = scale_parts(vB ? svB : 1.f);
       if (!failed) failed = !dsa::mbar_wait(&s_full[b], par, wt);
       __syncwarp();
       dsa::tc_fence_after();
@@ -485,77 +515,84 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
           x[4 * j + 2 + e] = vB ? fmaf(x[4 * j + 2 + e], qs[h] * skB, -m[h]) : -INFINITY;
         }
       }
-      float most = x[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r) most = fmaxf(most, x[r]);
-      const bool ex = unset || most > kTheta || svA > ref || svB > ref;
-      float v[4];
+      // y: with the value's scale, against the other reference
+      float y[8], v[4], u[4], most = -INFINITY, most_y = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        v[h] = fmaxf(x[4 * (h >> 1) + (h & 1)], x[4 * (h >> 1) + 2 + (h & 1)]);
+        const int a = 4 * (h >> 1) + (h & 1);
+        const float d = m[h] - rr[h];
+        y[a] = x[a] + (d + eA.x), y[a + 2] = x[a + 2] + (d + eB.x);
+        v[h] = fmaxf(x[a], x[a + 2]), u[h] = fmaxf(y[a], y[a + 2]);
+        most = fmaxf(most, v[h]), most_y = fmaxf(most_y, u[h]);
         top[h] = fmaxf(top[h], v[h] + m[h]);
       }
+      const bool ex = unset || most > kMoveM || most_y > kMoveR;
       bool need_rescale = false;
       if (i == i0 || group_any(ex || failed)) {
-        // move the references: the tile's maximum per head over its 64 keys
-        wmax[quarter * kHG + hb + own_head(lane)] = fold4(v, lane, [](float a, float c) { return fmaxf(a, c); });
-        float sv = fmaxf(svA, svB);
-        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 4));
-        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
-        sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
-        if (lane == 0) svm[quarter] = sv;
+        // move the references: the tile's maxima per head over its 64 keys
+        const auto larger = [](float a, float c) { return fmaxf(a, c); };
+        wmax[quarter * kHG + hb + own_head(lane)] = fold4(v, lane, larger);
+        ymax[quarter * kHG + hb + own_head(lane)] = fold4(u, lane, larger);
+        const bool some = __any_sync(0xffffffffu, vA || vB);
+        if (lane == 0) svm[quarter] = some ? 1.f : 0.f;
         if (group_any(failed)) {  // the group leaves together
           ok = false;
           break;
         }
-        const float sv_max = fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3]));
-        const float rn = fmaxf(ref, pow2_ceil(sv_max));
-        inv = dsa::pow2_inverse(rn);
-        const float ratio = ref * inv;  // of the old to the new 2^E
-        ref = rn;
-        bool moved = ratio != 1.f;
-        float4 t4 = *reinterpret_cast<const float4*>(wmax + hb);
+        float4 t4 = *reinterpret_cast<const float4*>(wmax + hb), y4 = *reinterpret_cast<const float4*>(ymax + hb);
 #pragma unroll
         for (int q4 = 1; q4 < 4; ++q4) {
           const float4 o = *reinterpret_cast<const float4*>(wmax + q4 * kHG + hb);
           t4.x = fmaxf(t4.x, o.x), t4.y = fmaxf(t4.y, o.y), t4.z = fmaxf(t4.z, o.z), t4.w = fmaxf(t4.w, o.w);
+          const float4 r = *reinterpret_cast<const float4*>(ymax + q4 * kHG + hb);
+          y4.x = fmaxf(y4.x, r.x), y4.y = fmaxf(y4.y, r.y), y4.z = fmaxf(y4.z, r.z), y4.w = fmaxf(y4.w, r.w);
         }
-        const float tm[4] = {t4.x, t4.y, t4.z, t4.w};
+        const float tm[4] = {t4.x, t4.y, t4.z, t4.w}, ty[4] = {y4.x, y4.y, y4.z, y4.w};
+        bool moved = false;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          // by how much the reference moves: to the tile's maximum, if that
-          // passes it by kTheta or is the first
-          const float up = (unset ? tm[h] > -INFINITY : tm[h] > kTheta) ? tm[h] : 0.f;
-          const float a = unset ? 1.f : ex2(-up);
-          moved |= up != 0.f;
-          l_part[h] *= a;
-          m[h] += up;
-          x[4 * (h >> 1) + (h & 1)] -= up;
-          x[4 * (h >> 1) + 2 + (h & 1)] -= up;
-          if (lane < 4) alpha[hb + h] = a * ratio;  // (the four warps write the same ones)
+          // by how much each moves: to the next whole number above the tile's maximum, if
+          // that passes it by enough or is the first
+          const int a = 4 * (h >> 1) + (h & 1);
+          const float up = (unset ? tm[h] > -INFINITY : tm[h] > kMoveM) ? ceilf(tm[h]) : 0.f;
+          const float upr = (unset ? ty[h] > -INFINITY : ty[h] > kMoveR) ? ceilf(ty[h]) : 0.f;
+          moved |= upr != 0.f;
+          l_part[h] *= unset ? 1.f : ex2(-up);
+          m[h] += up, rr[h] += upr;
+          x[a] -= up, x[a + 2] -= up;
+          y[a] -= upr, y[a + 2] -= upr;
+          if (lane < 4) alpha[hb + h] = unset ? 1.f : ex2(-upr);  // (the four warps write the same ones)
         }
-        unset = unset && !(sv_max > 0.f);
+        unset = unset && !(fmaxf(fmaxf(svm[0], svm[1]), fmaxf(svm[2], svm[3])) > 0.f);
         need_rescale = __any_sync(0xffffffffu, moved) && i > i0;
       }
-      // P^T rows kA and kB, both terms: the thread's four heads are bytes hb .. hb + 3 of each half
+      // P^T rows kA and kB, both terms: the thread's four heads are bytes hb .. hb + 3 of each place
       if (!failed) failed = !dsa::mbar_wait(&p_empty[b], par ^ 1, wt);  // MMA2 of two tiles ago has read the buffer
+      if (S::kPBufs == 1 && i > i0 && !failed) failed = !dsa::mbar_wait(&p_empty[b ^ 1], ((ctr - 1) >> 1) & 1, wt);
       {
-        uint8_t* pb = smem + S::kP + b * kPBytes;
-        const float wA = svA * inv * kWeight, wB = svB * inv * kWeight;  // (2^-E alone stays in range)
+        uint8_t* pb = smem + S::kP + (S::kPBufs == 2 ? b : 0) * 2 * kPBytes;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int key = k ? kB : kA;
-          const float wk = k ? wB : wA;
+          const float fk = (k ? eB.y : eA.y) * kWeight;
           uint16_t hi[2], lo[2];
+          uint32_t low = 0;  // the bytes of the weights that go to the second place
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float p0 = ex2(x[4 * j + 2 * k]), p1 = ex2(x[4 * j + 2 * k + 1]);
-            l_part[2 * j] += p0;
-            l_part[2 * j + 1] += p1;
-            split_weights(p0 * wk, p1 * wk, hi[j], lo[j]);
+            const int a = 4 * j + 2 * k;
+            l_part[2 * j] += ex2(x[a]);
+            l_part[2 * j + 1] += ex2(x[a + 1]);
+            float w0 = ex2(y[a]) * fk, w1 = ex2(y[a + 1]) * fk;
+            if (w0 < kLow) w0 *= kLowScale, low |= 0xFFu << (16 * j);
+            if (w1 < kLow) w1 *= kLowScale, low |= 0xFFu << (16 * j + 8);
+            split_weights(w0, w1, hi[j], lo[j]);
           }
-          *reinterpret_cast<uint32_t*>(pb + sw32_offset(key, 0) + hb) = hi[0] | (static_cast<uint32_t>(hi[1]) << 16);
-          *reinterpret_cast<uint32_t*>(pb + sw32_offset(key, 1) + hb) = lo[0] | (static_cast<uint32_t>(lo[1]) << 16);
+          const uint32_t h4 = hi[0] | (static_cast<uint32_t>(hi[1]) << 16), l4 = lo[0] | (static_cast<uint32_t>(lo[1]) << 16);
+          const uint32_t at0 = sw32_offset(key, 0) + hb, at1 = sw32_offset(key, 1) + hb;
+          *reinterpret_cast<uint32_t*>(pb + at0) = h4 & ~low;
+          *reinterpret_cast<uint32_t*>(pb + at1) = h4 & low;
+          *reinterpret_cast<uint32_t*>(pb + kPBytes + at0) = l4 & ~low;
+          *reinterpret_cast<uint32_t*>(pb + kPBytes + at1) = l4 & low;
         }
       }
       if (need_rescale) {
@@ -590,19 +627,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       redm[quarter * kHG + hb + own_head(lane)] = fold4(top, lane, [](float a, float c) { return fmaxf(a, c); });
       if (quarter == 0 && lane < 4) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) fac[hb + h] = m[h];
+        for (int h = 0; h < 4; ++h) fac[hb + h] = m[h], facr[hb + h] = rr[h];
       }
       group_sync();
-      const float unscale = ref * (1.f / kWeight);
       if (st < kHG) {
         const float l = red[st] + red[kHG + st] + red[2 * kHG + st] + red[3 * kHG + st];
         const float mc = fac[st];
         const float mx = fmaxf(fmaxf(redm[st], redm[kHG + st]), fmaxf(redm[2 * kHG + st], redm[3 * kHG + st]));
         stats[st] = make_float4(mc, l, mx, sink);
-        fac[st] = unscale;
+        // (in two steps: 2^(R - m) alone may pass fp32's range)
+        const float half = floorf(0.5f * (facr[st] - mc)), e0 = exp2f(half) * (1.f / kWeight), e1 = exp2f(facr[st] - mc - half);
+        fac[st] = l != 0.f ? e0 / l * e1 : 0.f;  // of a split's mean value, which stays in range where the sum might not
         if (p.splits == 1) {
           const Norm n = norm_of(mc, l, sink);
-          fac[st] = n.f * unscale;
+          fac[st] = n.f * e0 * e1;
           if (st < hv) {
             p.lse[orow + st] = n.lse;
             if (p.lse_kv) p.lse_kv[orow + st] = n.lse_kv;
@@ -631,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
           dsa::tmem_wait_ld();
           const int d = mb * 128 + quarter * 32 + lane;
 #pragma unroll
-          for (int h = 0; h < kHG; ++h) part[h * DV + d] = (__uint_as_float(v[h]) + __uint_as_float(v[kHG + h])) * f[h];
+          for (int h = 0; h < kHG; ++h) part[h * DV + d] = fmaf(__uint_as_float(v[kHG + h]), 1.f / kLowScale, __uint_as_float(v[h])) * f[h];
         }
       } else {
         // transposed by the store of 8 x 8 matrices, 16 heads x 32 dims at a
@@ -659,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 #pragma unroll
             for (int n = 0; n < 4; ++n) {  // 8 heads n / 2, 8 dims n % 2
               const float* fn = f + 2 * (n >> 1);
-              const float a = __uint_as_float(v[g][2 * n]) + __uint_as_float(v[g][8 + 2 * n]);
-              const float b = __uint_as_float(v[g][2 * n + 1]) + __uint_as_float(v[g][8 + 2 * n + 1]);
+              const float a = fmaf(__uint_as_float(v[g][8 + 2 * n]), 1.f / kLowScale, __uint_as_float(v[g][2 * n]));
+              const float b = fmaf(__uint_as_float(v[g][8 + 2 * n + 1]), 1.f / kLowScale, __uint_as_float(v[g][2 * n + 1]));
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(a * fn[0], b * fn[1]);
               r[n] = *reinterpret_cast<const uint32_t*>(&b2);
             }
@@ -682,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 
   __syncwarp();
   if (p.splits > 1) {
-    // Joins the splits: with M the largest reference, out = sum_s 2^(m_s - M) O_s / z.
+    // Joins the splits: with M the largest reference and a_s = 2^(m_s - M) l_s, out = sum_s a_s O_s / z of their
+    // mean values O_s.
     cluster_arrive();
     cluster_wait();
     const int dims = DV / p.splits, quads = dims / 4, d0 = split * dims;
@@ -707,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) {
         if (sm[s].y == 0.f) continue;  // a split without a valid slot: it may have left no sums
-        const float a = exp2f(sm[s].x - M);
-        l = fmaf(sm[s].y, a, l);
+        const float a = sm[s].y * exp2f(sm[s].x - M);
+        l += a;
         acc.x = fmaf(a, o[s].x, acc.x), acc.y = fmaf(a, o[s].y, acc.y), acc.z = fmaf(a, o[s].z, acc.z), acc.w = fmaf(a, o[s].w, acc.w);
       }
       const Norm n = norm_of(M, l, sm[0].w);
@@ -739,8 +778,8 @@ int64_t units_of(int T, int H, int Hc) { return static_cast<int64_t>(T) * Hc * (
 // makes the last CTA earliest, in fifths of a tile: kItemTiles for what an item
 // does once, 7 instead of 5 a tile where SMs have two CTAs, 13 and one per
 // split for the join.  Measured (2048 slots, latent rows of 576; microseconds
-// with 1, 2, 4, 8 splits): one row of 64 heads 35, 23, 14.8, 11.4; 8 rows of 128
-// heads 35, 24, 20.4, 28; 1024 rows of 16 heads of 512 180, 212, 260, 384.
+// with 1, 2, 4, 8 splits): one row of 64 heads 43, 28, 17.2, 12.5; 64 rows of 32
+// heads 46.7, 39.2, 44.8, 61.7; 1024 rows of 16 heads of 512 220, 243.
 constexpr int kItemTiles = 5;
 
 int plan_splits(int64_t units, int K) {
@@ -787,15 +826,16 @@ int launch_form(const Params& p, cudaStream_t stream) {
 namespace dsa {
 namespace kv8_attn {
 
-// KV heads of at most 16 query heads, and calls of little work: up to 10
-// tiles of 16 heads an SM, or 20 where the other kernel's 64 heads are at
-// least half padding.  Measured (microseconds, this kernel against the other):
-// 1024 rows of 16 heads of 512, 512 slots 63 / 102; 4 and 8 rows of 128 heads, 2048
-// slots 15.7 / 17.6 and 20.4 / 18.6; 64 and 128 rows of 64 heads, 256 slots 12.1 /
-// 14.3 and 22 / 15.4; 32 heads: 32 rows, 2048 slots 21.3 / 23.6, 1000 rows, 1000 slots 170 / 165.
+// KV heads of at most 32 query heads, and calls of little work: up to 10 tiles
+// of 16 heads an SM.  Measured (microseconds, this kernel against the other):
+// 1024 rows of 16 heads of 512, 512 slots 68 / 125; 32 heads: 32 rows, 2048 slots 24.2 / 27.7,
+// 1000 rows, 1000 slots 218 / 261; 48 heads, 500 slots: 40 rows 15.4 / 17.6, 1000 rows 180 / 149;
+// 64 heads, 256 slots: 64 rows 13.3 / 14.7, 128 rows 23.5 / 17.6; 8 rows of 128 heads, 2048 slots
+// 23.0 / 18.7.  Rows of more than 2^20 slots go to the other kernel, whose weights have no
+// smallest step: here what lies below it could add up to 2^-10 of the largest.
 bool narrow_takes(int T, int H, int Hc, int K) {
   const int groups = (H / Hc + kHG - 1) / kHG;
-  return groups == 1 || units_of(T, H, Hc) * ((K + kKeys - 1) / kKeys) <= (groups == 2 ? 20 : 10) * kPlanSms;
+  return K <= (1 << 20) && (groups <= 2 || units_of(T, H, Hc) * ((K + kKeys - 1) / kKeys) <= 10 * kPlanSms);
 }
 
 int launch_narrow(Params p, int T, int Dqk, cudaStream_t stream) {

@@ -109,6 +109,12 @@ __device__ __forceinline__ uint16_t e4m3x2_h2(uint32_t h2) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
 }
+// The same to E5M2.
+__device__ __forceinline__ uint16_t e5m2x2_h2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
 // Two codes -> two halves, exactly.
 __device__ __forceinline__ uint32_t h2_of_e4m3x2(uint16_t c) {
   uint32_t r;

@@ -29,14 +29,18 @@ def _lib():
     assert ops.device_status(clear=True) == 0, "a kernel raised a device status flag"
 
 
-def definition(q, k, ks, count, sm, v8=None, v_scale=None, sink=None):
+def definition(q, k, ks, count, sm, v8=None, v_scale=None, sink=None, narrow=False):
     """out, lse and how far each may be off, in float64, for rows that select every cache row r count[t, r] times.
 
     Scores are fp32 sums of exact products of bf16 queries and codes: off by at most Dqk * 2^-24 of
     the products' magnitudes and 2^-21 of the score (scale, log2(e), the reference); d is the largest such error of a
     row's slots, and enters a weight and its norm: 2 d.  A weight is rounded to bf16 (2^-8).  The value product adds 16
     slots at a time to an fp32 sum, each time off by 2^-23 of it at most: n / 16 * 2^-23 over n slots.  2^-16:
-    exp and the fp32 operations of the norm.  out is rounded to bf16 (2^-8)."""
+    exp and the fp32 operations of the norm.  out is rounded to bf16 (2^-8).
+    In groups of 16 heads a query element is off by at most 2^-22 of its head's largest, and a
+    weight, held as 14 times itself against a reference less than a factor of two above the largest, is
+    an E4M3 and an E5M2 term of a half: off by 2^-8 + 2^-11, or by 2^-14 (half the last step where the E4M3
+    term has none) in the place of weights times 2^14: 2^-28 / 7 of the largest weight times its scale."""
     T, H, dqk = q.shape
     n_blocks, block, heads, _ = k.shape
     group, rows = H // heads, n_blocks * block
@@ -47,12 +51,17 @@ def definition(q, k, ks, count, sm, v8=None, v_scale=None, sink=None):
     for g in range(heads):
         hs = slice(g * group, (g + 1) * group)
         kk = R.VALUES[k.reshape(rows, heads, dqk)[:, g]] * ks[blk, g].astype(np.float64)[:, None]
-        vv = kk[:, :dv] if v8 is None else R.VALUES[v8.reshape(rows, heads, dv)[:, g]] * v_scale[blk, g].astype(np.float64)[:, None]
+        sv = (ks if v8 is None else v_scale)[blk, g].astype(np.float64)
+        code = R.VALUES[(k if v8 is None else v8).reshape(rows, heads, -1)[:, g, :dv]]
+        vv = code * sv[:, None]
         for t in range(T):
             used = count[t] > 0
             c = count[t, used].astype(np.float64)
             s = sm * (q[t, hs] @ kk[used].T)
-            d = (sm * dqk * 2.0 ** -24 * (np.abs(q[t, hs]) @ np.abs(kk[used]).T) + 2.0 ** -21 * np.abs(s)).max(1)
+            d = sm * dqk * 2.0 ** -24 * (np.abs(q[t, hs]) @ np.abs(kk[used]).T) + 2.0 ** -21 * np.abs(s)
+            if narrow:
+                d += sm * 2.0 ** -22 * np.abs(q[t, hs]).max(1)[:, None] * np.abs(kk[used]).sum(1)[None, :]
+            d = d.max(1)
             sk = np.full(s.shape[0], -np.inf) if sink is None else sink[hs].astype(np.float64)
             m = np.maximum(s.max(1), sk)
             e = np.exp(s - m[:, None]) * c
@@ -63,6 +72,9 @@ def definition(q, k, ks, count, sm, v8=None, v_scale=None, sink=None):
             n = c.sum()
             tol[t, hs] = (2.0 ** -8 * np.abs(out[t, hs]) +
                           (2.0 ** -8 + 2 * d[:, None] + n * 2.0 ** -27 + 2.0 ** -16) * (p @ np.abs(vv[used])))
+            if narrow:
+                tol[t, hs] += 2.0 ** -11 * (p @ np.abs(vv[used]))
+                tol[t, hs] += (2.0 ** -28 / 7) * ((p / c) * sv[used]).max(1)[:, None] * (c @ np.abs(code[used]))[None, :]
             ltol[t, hs] = d + n * 2.0 ** -28 + 2.0 ** -19 + 2.0 ** -21 * (np.abs(lse[t, hs]) + 16)
     return out, tol, lse, ltol
 
@@ -76,11 +88,11 @@ def finite_codes(rng, shape):
     return np.where((c & 127) == 127, c & 0x80, c).astype(np.uint8)
 
 
-def check(form, q, k, ks, idx, sm, table=False, **kw):
+def check(form, q, k, ks, idx, sm, table=False, narrow=False, **kw):
     dqk, dv = form
     rows = k.shape[0] * k.shape[1]
     count = np.stack([np.bincount(i, minlength=rows) for i in idx])
-    out, tol, lse, ltol = definition(f64(q), k, ks, count, sm, **kw)
+    out, tol, lse, ltol = definition(f64(q), k, ks, count, sm, narrow=narrow, **kw)
     d = {n: dev(a) for n, a in kw.items() if n != "sink"}
     if "sink" in kw:
         d["sink"] = dev(kw["sink"])
@@ -124,7 +136,8 @@ def peaked(rng, form, T, H, heads, K, block, n, small, where, lo=6.0, hi=28.0):
 
 
 # (T, H, heads, K): whole rows and rows in splits
-WIDE = [(40, 64, 1, 2048), (200, 40, 1, 512), (90, 128, 1, 300), (1, 64, 1, 131072)]
+WIDE = [(40, 64, 1, 2048), (200, 40, 1, 512), (90, 128, 1, 300), (1, 64, 1, 131072), (1, 16, 1, 1100000)]
+NARROW = [(1, 64, 1, 2048), (3, 16, 1, 16384), (2, 24, 2, 700), (5, 16, 1, 64), (300, 12, 1, 130), (1, 16, 1, 131072), (70, 32, 1, 512)]
 FORMS = [(576, 512), (512, 512), (256, 256)]
 
 
@@ -145,7 +158,24 @@ def test_unused_block_of_large_scale_wide(form, T, H, heads, K, up):
     unused_block(form, T, H, heads, K, up)
 
 
-def unused_block(form, T, H, heads, K, up):
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,H,heads,K", NARROW)
+def test_peaked_rows_narrow(form, T, H, heads, K, small, where):
+    rng = np.random.default_rng(K + H + T + form[0])
+    q, k, ks, idx, sm, kw = peaked(rng, form, T, H, heads, K, 16, 4096, small, where, hi=16.0)
+    check(form, q, k, ks, idx, sm, table=where == "middle", narrow=True, **kw)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("up", [8, 14, 40])
+@pytest.mark.parametrize("T,H,heads,K", NARROW[:5])
+def test_unused_block_of_large_scale_narrow(form, T, H, heads, K, up):
+    unused_block(form, T, H, heads, K, up, narrow=True)
+
+
+def unused_block(form, T, H, heads, K, up, narrow=False):
     """One block's scale is 2^up times the others', and its keys have no weight."""
     rng = np.random.default_rng(K + H + T + up)
     dqk, dv = form
@@ -167,4 +197,4 @@ def unused_block(form, T, H, heads, K, up):
         q[..., -1] *= 40  # 0 .. 120 nats, the block at -448
     idx = rng.integers(0, n_blocks * block, (T, K)).astype(np.int32)
     idx[:, 5] = 7 * block + 3
-    check(form, W.f32_to_bf16_bits(q.astype(np.float32)), k, ks, idx, sm, **kw)
+    check(form, W.f32_to_bf16_bits(q.astype(np.float32)), k, ks, idx, sm, narrow=narrow, **kw)
