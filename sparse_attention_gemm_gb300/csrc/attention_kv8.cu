@@ -106,7 +106,10 @@ __device__ __forceinline__ bool group_any(bool x) {
 }
 
 // Asks for the block index of a CTA of this grid that has not started and no
-// longer will; the answer (16 bytes) arrives at the barrier.
+// longer will; the answer (16 bytes) arrives at the barrier.  It is written
+// through the async proxy into a place whose last answer was read with ordinary
+// loads, so a proxy fence stands between those reads and the barrier that hands the
+// place back, and between that barrier and the request.
 __device__ __forceinline__ void take_cta(const void* slot, uint64_t* bar) {
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
                    dsa::smem_u32(slot)),
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     *heard = dsa::mbar_wait_warp(&sched_full[n & 1], (n >> 1) & 1, wt);
     if (!*heard) return -1;
     const int got = taken_cta(smem + S::kSlots + (n & 1) * 16);
+    dsa::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) dsa::mbar_arrive(&sched_empty[n & 1]);
     __syncwarp();
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const Params p) {
     auto request = [&](int n) {
       if (!p.steal) return true;
       if (n >= 2 && !dsa::mbar_wait_warp(&sched_empty[n & 1], ((n >> 1) & 1) ^ 1, wt)) return false;
+      dsa::fence_proxy_async_smem();
       if (lane == 0) {
         dsa::mbar_expect_tx(&sched_full[n & 1], 16);
         take_cta(smem + S::kSlots + (n & 1) * 16, &sched_full[n & 1]);
