@@ -557,7 +557,9 @@ int dsa_forward_host(const dsa_forward_buffers* b, int n_docs, int T, int Hi, in
  * two whenever every earlier scale was, and then reading back gives the bf16
  * of a code exactly.  Rows behind the new ones, blocks that receive none and
  * tokens whose position is not mapped are left alone.
- * Contract (not checked, device data): a block receives rows from one
+ * With neither block_table nor pos the batch's rows are one run of rows, as if of
+ * one sequence: a block may receive the end of one and the start of the next.
+ * Contract (not checked, device data): otherwise a block receives rows from one
  * sequence per call, through one table entry.  Other uses leave the codes and
  * the scale of that block unspecified.
  * Errors: DSA_ERR_VALUE. */

@@ -66,8 +66,8 @@ __device__ bool find_item(const dsa::Kv8Geom& g, int item, WriteItem* out) {
     int c0 = 0, n = 0, count = 0;
     int64_t p0 = 0;
     if (b < g.n_seqs) {
-      c0 = max(__ldg(g.cu + b), 0);
-      n = min(__ldg(g.cu + b + 1), g.T) - c0;
+      c0 = max(__ldg(g.cu + b * g.step), 0);
+      n = min(__ldg(g.cu + (b + 1) * g.step), g.T) - c0;
       p0 = kv8_pos0(g, b, c0);
       if (n > 0) count = static_cast<int>(((p0 + n - 1) >> g.lb) - (p0 >> g.lb)) + 1;
     }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Cache row of packed token t; -1 not mapped, -2 behind the last sequence.
 __device__ __forceinline__ int row_of_token(const dsa::Kv8Geom& g, int64_t t) {
-  if (t >= g.T || t < __ldg(g.cu) || t >= __ldg(g.cu + g.n_seqs)) return -2;
+  if (t >= g.T || t < __ldg(g.cu) || t >= __ldg(g.cu + g.n_seqs * g.step)) return -2;
   const int b = dsa::kv8_seq(g.cu, g.n_seqs, static_cast<int>(t));
   const int c = __ldg(g.cu + b);
   return dsa::kv8_row(g, b, kv8_pos0(g, b, c) + (t - c));
@@ -362,7 +362,8 @@ int check_args(const char* fn, const void* rows, const void* cache, const void* 
     return dsa::set_error(DSA_ERR_VALUE, "%s: the bf16 rows and the cache must be 16-byte aligned", fn);
   int lb = 0;
   while ((1 << lb) < block) ++lb;
-  *g = dsa::Kv8Geom{cu, pos, table, n_seqs, T, lb, n_blocks, max_blocks};
+  const bool one = !pos && !table;
+  *g = dsa::Kv8Geom{cu, pos, table, one ? 1 : n_seqs, T, lb, n_blocks, max_blocks, one ? n_seqs : 1};
   return DSA_OK;
 }
 
@@ -397,7 +398,7 @@ extern "C" int dsa_kv8_write(const void* src, const int32_t* cu_seqlens, const i
     return dsa::launch_error("kv8_write_rows_kernel");
   }
   // a sequence of n rows touches at most n / block + 2 blocks, and at most n
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(T, T / block + 2ll * n_seqs)), Hc);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(T, T / block + 2ll * g.n_seqs)), Hc);
   const int np = (D + 255) / 256;
   auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(x, g, Hc, D, c, scale); };
   if (block <= 16)

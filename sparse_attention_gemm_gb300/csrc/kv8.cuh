@@ -19,6 +19,10 @@ struct Kv8Geom {
   const int32_t* pos;    // NULL: 0 with a table, cu[b] without
   const int32_t* table;  // [n_seqs, max_blocks] or NULL
   int n_seqs, T, lb, n_blocks, max_blocks;
+  // Sequence b is cu[b * step] .. cu[(b + 1) * step] - 1.  With neither table nor pos, row t
+  // of the batch is row t of the cache whatever its sequence: n_seqs is 1 then, and
+  // step the number of sequences.
+  int step = 1;
 };
 
 // The sequence's first position.

@@ -34,3 +34,24 @@ def test_append_to_a_block_of_the_largest_scale(scale):
     codes, old = cache_of(rng, g.n_blocks, 16, 2, 32)
     old[:] = scale
     check_write(g, W.f32_to_bf16_bits(v), codes, old, 2, 32)
+
+
+@pytest.mark.parametrize("block", [2, 16, 256])
+def test_packed_rows_of_several_sequences_share_blocks(block):
+    """Neither table nor positions: row t of the batch is row t of the cache, and blocks hold the end of one sequence
+    and the start of the next; the same codes as of one sequence, call after call, and read back in place."""
+    rng = np.random.default_rng(91)
+    cu = cu_from_lengths([33, 16, 0, 1, 15, 2, 200, 7])
+    T = int(cu[-1]) + 5  # and padding
+    n_blocks = (T + block - 1) // block + 1
+    x = rows(rng, T, 2, 64, 6.0)
+    codes, scale = cache_of(rng, n_blocks, block, 2, 64, -14, -4)
+    want, ws = R.write(f64(x), codes, scale, np.array([0, cu[-1]], np.int32), None, None)
+    src = dev_bf16(x)
+    for _ in range(3):
+        c, s = dev(codes), dev(scale)
+        ops.kv8_write(src, c, s, dev(cu))
+        assert np.array_equal(s.cpu().numpy(), ws) and same_codes(c.cpu().numpy(), want)
+    got = ops.kv8_read(c, s, dev(cu), T)[:int(cu[-1])].float().cpu().numpy()
+    v = R.read(want, ws, np.array([0, cu[-1]], np.int32), T, None, None, np.zeros((T, 2, 64), np.float32))[:int(cu[-1])]
+    assert np.array_equal(got, torch.from_numpy(v).to(torch.bfloat16).float().numpy())
