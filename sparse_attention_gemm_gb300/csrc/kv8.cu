@@ -342,6 +342,9 @@ int tokens_per_cta(int T, int Hc, int D, int sms) {
   return n;
 }
 
+// (T + tokens may pass the int range)
+unsigned ctas_of(int T, int tokens) { return static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens); }
+
 // Checks of the two calls; fills the geometry.
 int check_args(const char* fn, const void* rows, const void* cache, const void* scale, const int32_t* cu,
                const int32_t* pos, const int32_t* table, int n_seqs, int T, int Hc, int D, int block, int n_blocks,
@@ -385,7 +388,7 @@ extern "C" int dsa_kv8_write(const void* src, const int32_t* cu_seqlens, const i
   auto* c = static_cast<uint8_t*>(cache);
   if (block == 1) {
     const int tokens = tokens_per_cta(T, Hc, D, sms);
-    const unsigned grid = static_cast<unsigned>((T + tokens - 1) / tokens);
+    const unsigned grid = ctas_of(T, tokens);
     const uint32_t magic = magic_of(Hc);
     if (D <= 128)
       kv8_write_rows_kernel<16, 1><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
@@ -421,7 +424,7 @@ extern "C" int dsa_kv8_read(const void* cache, const float* scale, const int32_t
   if (rc != DSA_OK) return rc;
   if (T == 0) return DSA_OK;
   const int tokens = tokens_per_cta(T, Hc, D, sms);
-  kv8_read_kernel<<<static_cast<unsigned>((T + tokens - 1) / tokens), kThreads, 0, stream>>>(
+  kv8_read_kernel<<<ctas_of(T, tokens), kThreads, 0, stream>>>(
       static_cast<const uint8_t*>(cache), scale, g, Hc, D, tokens, tokens == 1 ? 1 : magic_of(Hc * (D / 8)), magic_of(D / 8),
       static_cast<__nv_bfloat16*>(out));
   return dsa::launch_error("kv8_read_kernel");

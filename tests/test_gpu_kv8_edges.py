@@ -55,3 +55,27 @@ def test_packed_rows_of_several_sequences_share_blocks(block):
     got = ops.kv8_read(c, s, dev(cu), T)[:int(cu[-1])].float().cpu().numpy()
     v = R.read(want, ws, np.array([0, cu[-1]], np.int32), T, None, None, np.zeros((T, 2, 64), np.float32))[:int(cu[-1])]
     assert np.array_equal(got, torch.from_numpy(v).to(torch.bfloat16).float().numpy())
+
+
+def test_batches_of_nearly_2_to_the_31_rows():
+    """Rows counted up to the int32 limit, all but a few of them padding."""
+    T = 2 ** 31 - 10
+    if torch.cuda.mem_get_info()[0] < T * 32 + (8 << 30):
+        pytest.skip("needs 72 GB of device memory")
+    rng = np.random.default_rng(92)
+    x = rows(rng, 5, 1, 16)
+    big = torch.empty((T, 1, 16), dtype=torch.bfloat16, device=DEV)
+    big[:5] = dev_bf16(x)
+    big[T - 1] = 7.0
+    cu = dev(cu_from_lengths([2, 3]))
+    c = torch.full((8, 1, 1, 16), 9, dtype=torch.uint8, device=DEV)
+    s = torch.full((8, 1), 9.0, device=DEV)
+    ops.kv8_write(big, c, s, cu)
+    ref, rs = R.write(f64(x), np.full((8, 1, 1, 16), 9, np.uint8), np.full((8, 1), 9.0, np.float32), np.array([0, 5], np.int32), None, None)
+    assert same_codes(c.cpu().numpy(), ref) and np.array_equal(s.cpu().numpy(), rs)
+    ops.kv8_read(c, s, cu, T, out=big)
+    v = R.read(ref, rs, np.array([0, 5], np.int32), 5, None, None, np.zeros((5, 1, 16), np.float32))
+    assert np.array_equal(big[:5].float().cpu().numpy(), torch.from_numpy(v).to(torch.bfloat16).float().numpy())
+    assert bool((big[T - 1] == 7.0).all())
+    del big
+    torch.cuda.empty_cache()
