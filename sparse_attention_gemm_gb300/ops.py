@@ -649,7 +649,8 @@ def _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_nam
     if block_table is not None:
         _need(block_table, "block_table", _I32, 2)
         args.append((block_table, "block_table", _I32, 2, (n_seqs, block_table.shape[1])))
-    args.append((rows, rows_name, _BF16, 3, (T, heads, dim)))
+    _need(rows, rows_name, _BF16, 3)
+    args.append((rows, rows_name, _BF16, 3, (rows.shape[0] if T is None else T, heads, dim)))
     _refuse(device, *args)
 
 
@@ -661,14 +662,14 @@ def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
             _ok(cache_scale, _F32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev) and
             _ok(src, _BF16, 3, dev) and (pos is None or _ok(pos, _I32, 1, dev)) and
             (block_table is None or _ok(block_table, _I32, 2, dev))):
-        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", src.shape[0])
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", None)
     n_blocks, block, heads, dim = cache.shape
     T = src.shape[0]
     n_seqs = cu_seqlens.shape[0] - 1
     rows, width = (n_seqs, 0) if block_table is None else block_table.shape
     if (src.shape != (T, heads, dim) or cache_scale.shape != (n_blocks, heads) or rows != n_seqs or
             (pos is not None and pos.shape[0] != n_seqs)):
-        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", T)
+        _kv8_refuse(cache, cache_scale, cu_seqlens, pos, block_table, src, "src", None)
     rc = (_lib or lib()).dsa_kv8_write(src.data_ptr(), cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(),
                                        None if block_table is None else block_table.data_ptr(), n_seqs, T, heads, dim,
                                        block, n_blocks, width, cache.data_ptr(), cache_scale.data_ptr(),
