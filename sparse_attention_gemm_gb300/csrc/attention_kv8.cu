@@ -834,15 +834,16 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
   const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
   const bool any = __any_sync(0xffffffffu, have);
   const float M = fmaxf(m, sk);
-  const float a = have ? s.y * exp2f(s.x - M) : 0.f;  // the split's share of the sum
+  const float a = have ? s.y * exp2f(s.x - M) : 0.f;
   float l = a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float z = any ? l + exp2f(sk - M) : 1.f;
+  const float share = a / z;  // at most 1: a mean of means stays in range
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.splits * DV) + threadIdx.x;
   for (int k = 0; k < p.splits; ++k) {
-    const float ak = __shfl_sync(0xffffffffu, a, k);
+    const float ak = __shfl_sync(0xffffffffu, share, k);
     if (__shfl_sync(0xffffffffu, have, k)) {
       const float4 v = __ldcs(o + k * (DV / 4));
       acc.x = fmaf(ak, v.x, acc.x);
@@ -851,10 +852,7 @@ __global__ void __launch_bounds__(DV / 4) attn_kv8_join_kernel(const Params p) {
       acc.w = fmaf(ak, v.w, acc.w);
     }
   }
-  const float f = 1.f / z;
-  const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-  reinterpret_cast<uint2*>(p.out + row * DV)[threadIdx.x] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
+  reinterpret_cast<uint2*>(p.out + row * DV)[threadIdx.x] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   if (threadIdx.x == 0) {
     p.lse[row] = any ? (M + log2f(z)) * kLn2 : sink;
     if (p.lse_kv) p.lse_kv[row] = any ? (M + log2f(l)) * kLn2 : INFINITY;

@@ -742,19 +742,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s)
         if (sm[s].y != 0.f) M = fmaxf(M, sm[s].x), mx = fmaxf(mx, sm[s].z);
+      float share[kMaxCluster];
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s) {
+        share[s] = sm[s].y != 0.f ? sm[s].y * exp2f(sm[s].x - M) : 0.f;
+        l += share[s];
+      }
+      const Norm n = norm_of(M, l, sm[0].w);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) {
-        if (sm[s].y == 0.f) continue;  // a split without a valid slot: it may have left no sums
-        const float a = sm[s].y * exp2f(sm[s].x - M);
-        l += a;
+        if (sm[s].y == 0.f) continue;  // a split without a valid slot: it may have left no values
+        const float a = share[s] * n.f;  // at most 1: a mean of means stays in range
         acc.x = fmaf(a, o[s].x, acc.x), acc.y = fmaf(a, o[s].y, acc.y), acc.z = fmaf(a, o[s].z, acc.z), acc.w = fmaf(a, o[s].w, acc.w);
       }
-      const Norm n = norm_of(M, l, sm[0].w);
-      const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * n.f, acc.y * n.f),
-                           r1 = __floats2bfloat162_rn(acc.z * n.f, acc.w * n.f);
-      *reinterpret_cast<uint2*>(p.out + (orow + h) * DV + d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
+      *reinterpret_cast<uint2*>(p.out + (orow + h) * DV + d) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (d == 0) {
         p.lse[orow + h] = n.lse;
         if (p.lse_kv) p.lse_kv[orow + h] = n.lse_kv;

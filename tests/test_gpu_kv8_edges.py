@@ -8,6 +8,7 @@ import kv8_ref as R
 from sparse_attention_gemm_gb300 import ops
 from sparse_attention_gemm_gb300 import workloads as W
 from test_gpu_kv8 import Pages, cache_of, check_write, rows, same_codes
+from test_gpu_kv8_peaked import check
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,15 @@ def test_batches_of_nearly_2_to_the_31_rows():
     assert bool((big[T - 1] == 7.0).all())
     del big
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,H,K,narrow", [(200, 64, 130, False), (20, 64, 2048, False), (300, 12, 130, True), (1, 64, 2048, True)])
+def test_values_near_the_largest_float(T, H, K, narrow):
+    """Mean values fit where the sum of a row's, or of a split's, weighted values would not."""
+    rng = np.random.default_rng(93)
+    n_blocks, block = 40, 16
+    k, ks = cache_of(rng, n_blocks, block, 1, 256)
+    v, _ = cache_of(rng, n_blocks, block, 1, 256)
+    q = rows(rng, T, H, 256)
+    idx = rng.integers(0, n_blocks * block, (T, K)).astype(np.int32)
+    check((256, 256), q, k, ks, idx, 1 / 16, narrow=narrow, v8=v, v_scale=np.full((n_blocks, 1), 2.0 ** 118, np.float32))
