@@ -298,10 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // the tile is signalled with a plain release arrive once this thread's
-        // copies have landed (cp.async.mbarrier.arrive, which signals from the
-        // copy engine, gave stale tiles on GB300 when other warps arrived on
-        // other barriers meanwhile; waiting here costs nothing measurable,
-        // the next tile's buffer is not free before these copies land anyway)
+        // copies have landed; waiting here costs nothing measurable, the next
+        // tile's buffer is not free before these copies land anyway.  (An
+        // unshipped form with a barrier per group of chunks, signalled by
+        // cp.async.mbarrier.arrive, gave differing outputs.  Whether that signal
+        // was the cause is not established: the epilogue of the time had a race
+        // with the same symptom, mended since.  attention_kv8_narrow.cu signals
+        // its tiles so, with the proxy fence on the reader's side that MMA1 has
+        // here too, and repeats its bits.)
         cp_async_wait_all();
         dsa::mbar_arrive(&kv_full[b]);
       }

@@ -892,7 +892,7 @@ size_t part_bytes(int T, int H, int splits) {
 }
 
 template <int DQK, int DV, bool SEP, bool kMax>
-int launch_form(const Params& p, int T, int sms, cudaStream_t stream) {
+int launch_form(const Params& p, int T, cudaStream_t stream) {
   using S = Shape<DQK, DV, SEP>;
   constexpr int smem = S::kTotal;
   auto kernel = attn_kv8_kernel<DQK, DV, SEP, kMax>;
@@ -922,9 +922,9 @@ int launch_form(const Params& p, int T, int sms, cudaStream_t stream) {
 }
 
 template <int DQK, int DV, bool SEP>
-int launch(const Params& p, int T, int sms, cudaStream_t stream) {
-  return p.max_logits ? launch_form<DQK, DV, SEP, true>(p, T, sms, stream)
-                      : launch_form<DQK, DV, SEP, false>(p, T, sms, stream);
+int launch(const Params& p, int T, cudaStream_t stream) {
+  return p.max_logits ? launch_form<DQK, DV, SEP, true>(p, T, stream)
+                      : launch_form<DQK, DV, SEP, false>(p, T, stream);
 }
 
 }  // namespace
@@ -1005,6 +1005,6 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
     p.part_s = static_cast<float4*>(workspace);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(T, H, p.splits));
   }
-  if (separate) return launch<256, 256, true>(p, T, sms, stream);
-  return Dqk == 576 ? launch<576, 512, false>(p, T, sms, stream) : launch<512, 512, false>(p, T, sms, stream);
+  if (separate) return launch<256, 256, true>(p, T, stream);
+  return Dqk == 576 ? launch<576, 512, false>(p, T, stream) : launch<512, 512, false>(p, T, stream);
 }

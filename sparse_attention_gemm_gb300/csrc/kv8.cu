@@ -335,7 +335,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Tokens per CTA: enough for 16 KB of codes, fewer where the batch would not
-// fill the device twice, and few enough for 16-bit piece numbers.
+// fill the device twice.  What fast_div needs of them holds: several tokens have
+// 2048 pieces at most, and the 131072 that one token can have are divided by a
+// head's pieces alone, 128 at most.
 int tokens_per_cta(int T, int Hc, int D, int sms) {
   int n = std::max(1, std::min(kMaxTokens, 16384 / (Hc * D)));
   n = std::max(1, std::min(n, T / (2 * sms)));

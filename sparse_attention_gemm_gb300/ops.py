@@ -680,8 +680,9 @@ def kv8_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
 
 
 def kv8_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None, out=None):
-    """Rows of the 8-bit block cache back to packed bf16 [T, Hc, D] (rows of an
-    `out` that is given stay as they are behind the last sequence)."""
+    """Rows of the 8-bit block cache back to packed bf16 [T, Hc, D].  Rows behind the
+    last sequence are not written: an `out` that is given keeps them, a new one has
+    anything there."""
     dev = cache.get_device() if isinstance(cache, _Tensor) else -1
     if out is None and dev >= 0 and _ok(cache, _U8, 4, dev):
         out = torch.empty((T, cache.shape[2], cache.shape[3]), dtype=_BF16, device=cache.device)
@@ -741,7 +742,8 @@ def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, s
                         cu_seqlens=None, block_table=None, want_lse_kv: bool = False, want_max_logits: bool = False,
                         out=None, lse=None, workspace=None):
     """Sparse attention forward over the 8-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
-    idx holds cache rows, or, with block_table and cu_seqlens, positions in the row's sequence."""
+    idx holds cache rows, or, with block_table and cu_seqlens, positions in the row's sequence.  With a block_table,
+    rows behind the last sequence are not written: tensors that are given keep them, new ones have anything there."""
     dev = q.get_device() if isinstance(q, _Tensor) else -1
     paged = block_table is not None
     if not (dev >= 0 and dev == _current_device() and _ok(q, _BF16, 3, dev) and _ok(kv8, _U8, 4, dev) and
