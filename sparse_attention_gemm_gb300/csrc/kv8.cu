@@ -32,12 +32,12 @@ __device__ __forceinline__ uint32_t finite_max(uint4 v, uint32_t m) {
   return m;
 }
 
-// Codes of x / s: a product for a power of two s with an exact 1 / s (every scale that
-// the writer makes; a block may come with 2^127, or with no power of two), else divided.
+// Codes of x / s: a product for a power of two s (every scale that the writer makes), else
+// divided.  A block may come with a scale of 2^127, whose inverse is below the normal range.
 template <bool kPow2>
 __device__ __forceinline__ uint2 codes_of(uint4 v, float s) {
-  const bool exact = kPow2 || ((__float_as_uint(s) & 0x7FFFFFu) == 0 && s <= 0x1p126f);
-  const float inv = dsa::pow2_inverse(s);
+  const bool exact = kPow2 || (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  const float inv = kPow2 || s != 0x1p127f ? dsa::pow2_inverse(s) : 0x1p-127f;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint16_t o[4];
 #pragma unroll

@@ -198,3 +198,21 @@ def unused_block(form, T, H, heads, K, up, narrow=False):
     idx = rng.integers(0, n_blocks * block, (T, K)).astype(np.int32)
     idx[:, 5] = 7 * block + 3
     check(form, W.f32_to_bf16_bits(q.astype(np.float32)), k, ks, idx, sm, narrow=narrow, **kw)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,H,K,narrow", [(40, 64, 2048, False), (1, 64, 131072, False), (1, 64, 2048, True), (3, 16, 16384, True)])
+def test_peaked_rows_as_the_bf16_call_on_values_read_back(form, T, H, K, narrow):
+    """Powers of two as scales: the values read back are the cache's, and each call is within its bound of the same
+    definition (the bf16 call rounds what groups of 64 heads round)."""
+    rng = np.random.default_rng(K + H + T + form[0] + 1)
+    q, k, ks, idx, sm, kw = peaked(rng, form, T, H, 1, K, 16, 4096, True, "first", hi=16.0)
+    got, out, tol = check(form, q, k, ks, idx, sm, narrow=narrow, **kw)
+    n = k.shape[0] * k.shape[1]
+    cu = dev(cu_from_lengths([n]))
+    kv = ops.kv8_read(dev(k), dev(ks), cu, n).view(n, form[0])
+    v = ops.kv8_read(dev(kw["v8"]), dev(kw["v_scale"]), cu, n).view(n, form[1]) if kw else None
+    other = ops.sparse_attn_fwd(dev_bf16(q), kv, dev(idx), sm, v=v)
+    o = other["out"].float().cpu().numpy().astype(np.float64)
+    assert not (np.abs(o - out) > tol).any()
+    assert float((got["lse"] - other["lse"]).abs().max()) <= 2e-3
