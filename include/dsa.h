@@ -600,11 +600,12 @@ int dsa_kv8_read(const void* cache, const float* scale, const int32_t* cu_seqlen
  *   entry; calls that may overlap need one each.
  * Accumulation is fp32.  Roundings before out's: with H / Hc > 32 and more than a
  * few rows, or K > 2^20, the query enters as it is and a weight exp(s_j) * v_scale_j
- * is rounded to bf16 (2^-8 of itself, however small), as in dsa_sparse_attn_fwd.
+ * is rounded to bf16 (2^-8 of itself, down to 2^-126 of the largest s and v_scale of its
+ * row), as in dsa_sparse_attn_fwd.
  * Other calls hold both in 8-bit terms: s_j is off by at most scale * kv_scale_j *
  * 2^-22 * max_c |q[t,h,c]| * sum_c |e4m3(kv8[r_j, kvh, c])| more, and a weight by
- * 2^-8 + 2^-11 of itself or 2^-30 of the row's largest for that head, whichever is
- * the larger: over n slots, what is lost of small weights is at most n * 2^-30 of the largest.
+ * 2^-8 + 2^-11 of itself or 2^-29 of the row's largest for that head, whichever is
+ * the larger: over n slots, what is lost of small weights is at most n * 2^-29 of the largest.
  * Results are bitwise reproducible; a row's last bits may differ between calls of
  * different T, H or K, which choose the form.
  * Shapes: (Dqk, Dv) in {(576, 512), (512, 512)} without v8, or (256, 256) with

@@ -13,7 +13,8 @@
 //            2^-6 or more, else 2^14 times itself, each with an accumulator of its own.
 //            There it is an E4M3 term and, for what that leaves, one in E5M2: off by at
 //            most 2^-8 of itself, as bf16 would be, for 29 powers of two from the
-//            largest 448 down; below by at most 2^-31 of the largest that R stands for.
+//            largest 448 down; below by at most 2^-31 of 14, which the largest is
+//            within a factor of four of (two where scales are powers of two).
 //            (One place of two E4M3 terms ended at 2^-13.8 of the largest weight times the largest scale:
 //            rows whose largest weight meets a small value lost their output.)
 // The sum of exp(s_j) has a reference m of its own, since scales do not enter it.
@@ -834,7 +835,7 @@ namespace kv8_attn {
 // 1000 rows, 1000 slots 218 / 261; 48 heads, 500 slots: 40 rows 15.4 / 17.6, 1000 rows 180 / 149;
 // 64 heads, 256 slots: 64 rows 13.3 / 14.7, 128 rows 23.5 / 17.6; 8 rows of 128 heads, 2048 slots
 // 23.0 / 18.7.  Rows of more than 2^20 slots go to the other kernel, whose weights have no
-// smallest step: here what lies below it could add up to 2^-10 of the largest.
+// smallest step: here what lies below it could add up to 2^-9 of the largest.
 bool narrow_takes(int T, int H, int Hc, int K) {
   const int groups = (H / Hc + kHG - 1) / kHG;
   return K <= (1 << 20) && (groups <= 2 || units_of(T, H, Hc) * ((K + kKeys - 1) / kKeys) <= 10 * kPlanSms);

@@ -102,7 +102,7 @@ __device__ bool find_item(const dsa::Kv8Geom& g, int item, WriteItem* out) {
 // beyond what fits are read again).  NP: pieces of a lane and row, kRows: rows
 // that a warp keeps -- few for small blocks, so that more CTAs are resident.
 // Bound: memory, 3 bytes a value; with few blocks the chain cu_seqlens -> rows ->
-// maximum -> codes.  16384 latent rows in pages of 64: 9.8 us (256 CTAs, 2.9 TB/s), 64
+// maximum -> codes.  16384 latent rows in pages of 64: 9.6 us (264 CTAs, all resident, 2.9 TB/s), 64
 // single rows: 3.6 us.
 template <int NP, int kRows>
 __global__ void __launch_bounds__(kThreads)

@@ -38,7 +38,8 @@ def definition(q, k, ks, count, sm, v8=None, v_scale=None, sink=None, narrow=Fal
     slots at a time to an fp32 sum, each time off by 2^-23 of it at most: n / 16 * 2^-23 over n slots.  2^-16:
     exp and the fp32 operations of the norm.  out is rounded to bf16 (2^-8).
     In groups of 16 heads a query element is off by at most 2^-22 of its head's largest, and a
-    weight, held as 14 times itself against a reference less than a factor of two above the largest, is
+    weight, held as 14 times itself against a reference less than a factor of two above the largest (scales being
+    powers of two), is
     an E4M3 and an E5M2 term of a half: off by 2^-8 + 2^-11, or by 2^-14 (half the last step where the E4M3
     term has none) in the place of weights times 2^14: 2^-28 / 7 of the largest weight times its scale."""
     T, H, dqk = q.shape
