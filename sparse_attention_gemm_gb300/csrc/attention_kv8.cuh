@@ -30,7 +30,7 @@ struct Params {
   float* lse;
   float* lse_kv;
   float* max_logits;
-  float* part_o;   // [T, H, splits, Dv], splits > 1
+  float* part_o;   // [T, H, splits, Dv]: mean values of splits > 1
   float4* part_s;  // [T, H, splits]: reference, sum, maximum
   uint32_t* status;
   int H, Hc, G, K, splits, n_items;  // G: 64-head groups per KV head
