@@ -5,7 +5,7 @@
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every tensor argument is a caller-owned, contiguous, row-major DEVICE
- *    pointer on the current CUDA device.  bf16 tensors are passed as void*
+ *    pointer on the current CUDA device (a call that takes strides says so).  bf16 tensors are passed as void*
  *    (IEEE bfloat16 bit patterns), fp32 as float*, ids as int32_t*.
  *  - The library never allocates, frees or synchronises.  Work is enqueued
  *    on `stream` and the call returns immediately; scratch space is passed in
@@ -619,6 +619,152 @@ int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const float* kv_scal
                             int T, int H, int Hc, int Dqk, int Dv, int K, int block, int n_blocks, int max_blocks,
                             float scale, void* out, float* lse, float* lse_kv, float* max_logits,
                             void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- 4-bit block cache.  Keys and values kept as E2M1 codes (4 bits: a sign and
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one power of two per 32 elements of a
+ * row:
+ *   cache uint8 [n_blocks, block, Hc, D / 2], element 2i of a row in the low half
+ *   of its byte i; scale uint8 [n_blocks, block, Hc, D / 32], byte e standing
+ *   for 2^(e - 127) on elements 32 b .. 32 b + 31, 255 for NaN on all of them.
+ * A value is the code's times the scale; those beyond the bf16 range are infinite.
+ * Rows live where those of the 8-bit cache do: cu_seqlens, pos, block_table,
+ * n_seqs, max_blocks and what positions mean as there.  A row's codes
+ * and scales depend on nothing but the row, so a block may receive rows of several calls
+ * and sequences, in any order, as long as no two rows of a call go to one place.
+ * Shapes: D a multiple of 32 <= DSA_KV8_MAX_DIM; block, Hc, n_blocks as in
+ * the 8-bit cache; cache and bf16 rows 16-byte aligned. */
+
+/* Quantises rows as they are written into the cache.
+ *   src bf16 [T, Hc, D]; cache, scale (in, out).
+ * Per 32 elements, with a the largest |x| over their finite values: e the
+ * smallest integer with a <= 6 * 2^e, within [-126, 125] (values beyond 6 * 2^125
+ * become that), scale byte e + 127, codes e2m1(x / 2^e) to nearest even with
+ * the sign of x; infinities become +-6.  With a NaN among the 32 the byte is 255 and
+ * the codes 0.  Other rows and tokens whose position is not mapped are left alone.
+ * Errors: DSA_ERR_VALUE. */
+int dsa_kv4_write(const void* src, const int32_t* cu_seqlens, const int32_t* pos, const int32_t* block_table,
+                  int n_seqs, int T, int Hc, int D, int block, int n_blocks, int max_blocks, void* cache,
+                  uint8_t* scale, cudaStream_t stream);
+
+/* Reads rows back, packed: out bf16 [T, Hc, D] (out), the values exactly, 0
+ * where a token's position is not mapped.  Padding tokens' rows of out are left
+ * as they were.  Positions may be shared between sequences.  Errors: DSA_ERR_VALUE. */
+int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32_t* cu_seqlens, const int32_t* pos,
+                 const int32_t* block_table, int n_seqs, int T, int Hc, int D, int block, int n_blocks,
+                 int max_blocks, void* out, cudaStream_t stream);
+
+/* Sparse attention forward over the 4-bit cache: dsa_sparse_attn_fwd_kv8 with
+ *   s_j = scale * sum_c q[t,h,c] * k(r_j)[c],   V_j = v(r_j), or the first Dv values
+ * of the key row when v4 is NULL, of the cache's values k and v.
+ *   kv4 uint8 [n_blocks, block, Hc, Dqk / 2], kv_scale uint8 [n_blocks, block, Hc,
+ *   Dqk / 32]; v4 and v_scale likewise with Dv, or both NULL; other arguments,
+ *   results, empty rows, rows behind the last sequence and shapes as there (K at most
+ *   DSA_KV8_MAX_SLOTS).  Codes and scales of rows that no valid slot names are never used.
+ *   workspace: dsa_sparse_attn_fwd_kv4_workspace_size bytes (0 for many shapes:
+ *   then it may be NULL), 256-byte aligned, contents ignored on entry; calls
+ *   that may overlap need one each.
+ * Values are bf16 ones and the query enters as it is: weights exp(s_j) are rounded to
+ * bf16 before they meet the values, sums are fp32, as in dsa_sparse_attn_fwd.
+ * Results are bitwise reproducible; a row's last bits may differ between calls of
+ * different T, H or K, which choose the splits.
+ * Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
+size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K);
+int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uint8_t* kv_scale, const void* v4,
+                            const uint8_t* v_scale, const int32_t* idx, const int32_t* topk_length,
+                            const float* sink, const int32_t* cu_seqlens, const int32_t* block_table, int n_seqs,
+                            int T, int H, int Hc, int Dqk, int Dv, int K, int block, int n_blocks, int max_blocks,
+                            float scale, void* out, float* lse, float* lse_kv, float* max_logits,
+                            void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- What makes the rows: norm and rotary positions.  Rows of these calls may lie
+ * apart (strides in elements): part of a wider row, or a head of a token's heads. */
+
+/* Root-mean-square norm of T rows of D:
+ *   h = x + residual,  rstd = 1 / sqrt(mean_c h[c]^2 + eps),  y = h * rstd * weight,
+ * in fp32, each output rounded once.
+ *   x bf16, row t at x + t * ld_x; residual likewise or NULL (then h = x); weight
+ *   fp32 [D];
+ *   y (out), row t at y + t * ld_y, by fmt:
+ *     DSA_NORM_BF16   bf16; y_scale is ignored;
+ *     DSA_NORM_E4M3   E4M3 codes, y_scale fp32 [T, D / 128]: with rows of Hi heads of 128 the
+ *                     codes and descales that dsa_indexer_*_fp8 take;
+ *     DSA_NORM_MXFP8  E4M3 codes, y_scale uint8 [T, D / 32] (E8M0): those of
+ *                     dsa_indexer_*_mxfp8.
+ *     A scale is 2^e, e the smallest integer >= -126 with a <= 448 * 2^e of the largest
+ *     finite |y| a it stands for; codes are e4m3(y / 2^e) to nearest even; infinities become +-448,
+ *     NaN stays NaN.
+ *   sum bf16 (out), row t at sum + t * ld_sum, or NULL: h, the next residual;
+ *   rstd fp32 [T] (out) or NULL: for the backward pass.
+ * y and sum may each be x or residual itself (same rows, same stride), not overlap them otherwise.
+ * Shapes: T >= 0; D a multiple of 8 (E4M3: 128, MXFP8: 32), at most DSA_NORM_MAX_DIM;
+ * strides multiples of 8 and at least D; eps finite > 0; x, residual, weight, sum and
+ * y 16-byte aligned (8-bit y: 8).
+ * Errors: DSA_ERR_VALUE. */
+#define DSA_NORM_BF16 0
+#define DSA_NORM_E4M3 1
+#define DSA_NORM_MXFP8 2
+#define DSA_NORM_MAX_DIM 16384
+int dsa_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const float* weight, int T,
+                     int D, float eps, int fmt, void* y, int64_t ld_y, void* y_scale, void* sum, int64_t ld_sum,
+                     float* rstd, cudaStream_t stream);
+
+/* Its backward pass.  x is h as the forward pass stored it (sum, or x where there was
+ * no residual), rstd the forward's, dy bf16 the gradient of y, d_sum bf16 the gradient that
+ * reaches h on its other way, or NULL:
+ *   xh = x * rstd,  g = dy * weight,  dx = rstd * (g - xh * mean_c(g * xh)) + d_sum,
+ *   dweight[c] = sum_t dy[t, c] * xh[t, c].
+ *   dx bf16 (out): the gradient of x and of the residual alike; may be dy, x or
+ *   d_sum itself (same rows, same stride); dweight fp32 [D] (out) or NULL.
+ *   workspace: dsa_rms_norm_bwd_workspace_size(T, D) bytes, 256-byte aligned; not needed
+ *   without dweight.  Sums are fp32 in a fixed order: bitwise reproducible.
+ * Shapes as the forward's bf16 form.  Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
+size_t dsa_rms_norm_bwd_workspace_size(int T, int D);
+int dsa_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const float* weight,
+                     const float* rstd, const void* d_sum, int64_t ld_ds, int T, int D, void* dx, int64_t ld_dx,
+                     float* dweight, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Rotary positions.  Each of T tokens' H rows of R values (and, in the same call, H2 rows
+ * of a second tensor: queries and keys) is R / 2 pairs (a, b): elements (2i, 2i + 1)
+ * when interleaved != 0, (i, i + R / 2) otherwise.  At position p pair i becomes
+ *   mul * (a cos(p f_i) - b sin(p f_i), a sin(p f_i) + b cos(p f_i)),
+ * with inverse != 0 by the angle -p f_i: the adjoint, which takes the gradient of the
+ * result to that of the input.
+ *   x bf16, row (t, h) at x + t * x_token + h * x_head; y (out) likewise, x itself
+ *   (same strides) or apart from it; x2, y2 the same with H2 heads (H2 = 0: ignored).
+ *   Part of a head is rotated by passing that part: nothing beside the R values is read or written.
+ *   inv_freq fp64 [R / 2], device: f_i, e.g. from dsa_rotary_inv_freq.
+ *   Position of token t of sequence b (cu_seqlens int32 [n_seqs + 1], as in the block
+ *   caches): pos[b] + t - cu_seqlens[b], pos int32 [n_seqs] or NULL (0).  Rows of tokens
+ *   outside the sequences are left as they were.
+ * Angles are reduced to a turn before they are rounded to fp32, whatever the
+ * position (exact in p; f_i / (2 pi) to 2^-53); the rest is fp32, the result rounded once.
+ * Shapes: R a multiple of 16 <= DSA_ROTARY_MAX_DIM; H >= 1, H2 >= 0, H + H2 <=
+ * DSA_ROTARY_MAX_HEADS; strides multiples of 8; rows 16-byte aligned; mul finite.
+ * Errors: DSA_ERR_VALUE. */
+#define DSA_ROTARY_MAX_DIM 1024
+#define DSA_ROTARY_MAX_HEADS 1024
+int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H, const void* x2, int64_t x2_token,
+               int64_t x2_head, int H2, const double* inv_freq, const int32_t* cu_seqlens, const int32_t* pos,
+               int n_seqs, int T, int R, int interleaved, int inverse, float mul, void* y, int64_t y_token,
+               int64_t y_head, void* y2, int64_t y2_token, int64_t y2_head, cudaStream_t stream);
+
+/* Angles per position for dsa_rotary, on the host (no device is touched): inv_freq
+ * fp64 [R / 2] (out, HOST memory), mul (out): the factor that goes with them.  With f_i = base^(-2i / R):
+ *   DSA_ROTARY_PLAIN   f_i;
+ *   DSA_ROTARY_LINEAR  f_i / factor;
+ *   DSA_ROTARY_NTK     f_i of base * factor^(R / (R - 2));
+ *   DSA_ROTARY_YARN    pairs that make more than beta_fast turns over the first
+ *       `first` positions keep f_i, those of fewer than beta_slow take f_i / factor, those
+ *       between blend linearly in i; mul = 0.1 ln(factor) + 1 (1 in the other forms).
+ * factor is ignored by PLAIN, first and the betas by all but YARN.
+ * Shapes: R even in [2, DSA_ROTARY_MAX_DIM] (NTK: >= 4), base > 1, factor >= 1, first >= 1,
+ * beta_fast > beta_slow > 0, all finite.  Errors: DSA_ERR_VALUE. */
+#define DSA_ROTARY_PLAIN 0
+#define DSA_ROTARY_LINEAR 1
+#define DSA_ROTARY_NTK 2
+#define DSA_ROTARY_YARN 3
+int dsa_rotary_inv_freq(int R, double base, int scaling, double factor, int64_t first, double beta_fast,
+                        double beta_slow, double* inv_freq, float* mul);
 
 /* Route packing ([NeMo-QSA] _pack_indices): routes int32 [B, S, W] hold
  * batch-local ids; out int32 [B*S, Wp] with Wp = ceil(W/4)*4 receives

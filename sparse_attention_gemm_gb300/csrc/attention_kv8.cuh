@@ -22,6 +22,8 @@ struct Params {
   const float* k_scale;
   const uint8_t* v8;  // separate V, or unused
   const float* v_scale;
+  const uint8_t* k_exp;  // 4-bit cache: a scale byte per 32 elements of a row
+  const uint8_t* v_exp;
   const int32_t* idx;
   const int32_t* topk_length;
   const float* sink;

@@ -201,22 +201,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Cache row of packed token t; -1 not mapped, -2 behind the last sequence.
-__device__ __forceinline__ int row_of_token(const dsa::Kv8Geom& g, int64_t t) {
-  if (t >= g.T || t < __ldg(g.cu) || t >= __ldg(g.cu + g.n_seqs * g.step)) return -2;
-  const int b = dsa::kv8_seq(g.cu, g.n_seqs, static_cast<int>(t));
-  const int c = __ldg(g.cu + b);
-  return dsa::kv8_row(g, b, kv8_pos0(g, b, c) + (t - c));
-}
-
-// n / d for n * d < 2^32, magic = magic_of(d): n * (2^32 / d + 1) exceeds n / d *
-// 2^32 by at most n, less than the 2^32 / d that would reach the next quotient.
-// 0 stands for d = 1, and 1 gives 0 for every n.
-__device__ __forceinline__ int fast_div(int n, uint32_t magic) {
-  return magic ? static_cast<int>(__umulhi(n, magic)) : n;
-}
-uint32_t magic_of(int d) { return d == 1 ? 0 : static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(d)) + 1; }
-
 // block = 1: a (token, head) row has its own scale.  G lanes per row, NP pieces
 // each, kRowPieces / NP rows at a time; `tokens` tokens per CTA, whose cache
 // rows are looked up first.  Bound: memory, 3 bytes a value; 8192 x 64 rows of
@@ -230,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kRows = kRowPieces / NP, kGroups = kThreads / G;
   __shared__ int rows[kMaxTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  if (threadIdx.x < tokens) rows[threadIdx.x] = row_of_token(g, t0 + threadIdx.x);
+  if (threadIdx.x < tokens) rows[threadIdx.x] = dsa::row_of_token(g, t0 + threadIdx.x);
   __syncthreads();
   const int sub = threadIdx.x % G, p8 = D >> 3;
   const int n = min(static_cast<int64_t>(tokens), g.T - t0) * Hc;
@@ -266,7 +250,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int o = G / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       }
       if (i >= n) continue;
-      const int t = fast_div(i, magic_hc);
+      const int t = dsa::fast_div(i, magic_hc);
       const int row = rows[t];
       if (row < 0) continue;
       const float s = dsa::kv8_scale_of(__uint_as_float(m << 16));
@@ -292,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
                     int D, int tokens, uint32_t magic_row, uint32_t magic_head, __nv_bfloat16* __restrict__ out) {
   __shared__ int rows[kMaxTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  if (threadIdx.x < tokens) rows[threadIdx.x] = row_of_token(g, t0 + threadIdx.x);
+  if (threadIdx.x < tokens) rows[threadIdx.x] = dsa::row_of_token(g, t0 + threadIdx.x);
   __syncthreads();
   const int p8 = D >> 3, per = Hc * p8;
   const int64_t ld = static_cast<int64_t>(Hc) * D;
@@ -308,12 +292,12 @@ __global__ void __launch_bounds__(kThreads)
       v[j] = make_uint2(0, 0);
       s[j] = 0.f;
       if (i < n) {
-        const int k = fast_div(i, magic_row), c = i - k * per;
+        const int k = dsa::fast_div(i, magic_row), c = i - k * per;
         const int row = rows[k];
         if (row != -2) live |= 1u << j;
         if (row >= 0) {
           v[j] = __ldcs(reinterpret_cast<const uint2*>(cache + row * ld) + c);
-          s[j] = __ldg(scale + static_cast<int64_t>(row >> g.lb) * Hc + fast_div(c, magic_head));
+          s[j] = __ldg(scale + static_cast<int64_t>(row >> g.lb) * Hc + dsa::fast_div(c, magic_head));
         }
       }
     }
@@ -391,7 +375,7 @@ extern "C" int dsa_kv8_write(const void* src, const int32_t* cu_seqlens, const i
   if (block == 1) {
     const int tokens = tokens_per_cta(T, Hc, D, sms);
     const unsigned grid = ctas_of(T, tokens);
-    const uint32_t magic = magic_of(Hc);
+    const uint32_t magic = dsa::magic_of(Hc);
     if (D <= 128)
       kv8_write_rows_kernel<16, 1><<<grid, kThreads, 0, stream>>>(x, g, Hc, D, tokens, magic, c, scale);
     else if (D <= 256)
@@ -427,7 +411,7 @@ extern "C" int dsa_kv8_read(const void* cache, const float* scale, const int32_t
   if (T == 0) return DSA_OK;
   const int tokens = tokens_per_cta(T, Hc, D, sms);
   kv8_read_kernel<<<ctas_of(T, tokens), kThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(cache), scale, g, Hc, D, tokens, tokens == 1 ? 1 : magic_of(Hc * (D / 8)), magic_of(D / 8),
+      static_cast<const uint8_t*>(cache), scale, g, Hc, D, tokens, tokens == 1 ? 1 : dsa::magic_of(Hc * (D / 8)), dsa::magic_of(D / 8),
       static_cast<__nv_bfloat16*>(out));
   return dsa::launch_error("kv8_read_kernel");
 }

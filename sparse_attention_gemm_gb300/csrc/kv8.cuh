@@ -71,6 +71,22 @@ __device__ __forceinline__ int kv8_seq_warp(const int32_t* __restrict__ cu, int 
   return lo;
 }
 
+// Cache row of packed token t; -1 not mapped, -2 behind the last sequence.
+__device__ __forceinline__ int row_of_token(const Kv8Geom& g, int64_t t) {
+  if (t >= g.T || t < __ldg(g.cu) || t >= __ldg(g.cu + g.n_seqs * g.step)) return -2;
+  const int b = kv8_seq(g.cu, g.n_seqs, static_cast<int>(t));
+  const int c = __ldg(g.cu + b);
+  return kv8_row(g, b, kv8_pos0(g, b, c) + (t - c));
+}
+
+// n / d for n * d < 2^32, magic = magic_of(d): n * (2^32 / d + 1) exceeds n / d *
+// 2^32 by at most n, less than the 2^32 / d that would reach the next quotient.
+// 0 stands for d = 1, and 1 gives 0 for every n.
+__device__ __forceinline__ int fast_div(int n, uint32_t magic) {
+  return magic ? static_cast<int>(__umulhi(n, magic)) : n;
+}
+inline uint32_t magic_of(int d) { return d == 1 ? 0 : static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint32_t>(d)) + 1; }
+
 // Scale of values up to `amax` (>= 0, finite): 2^e with the smallest e that
 // keeps amax <= 448 * 2^e, at least 2^-126.  448 = 1.75 * 2^8, so e follows
 // from the exponent and from whether the significand exceeds 1.75.  Powers

@@ -1,0 +1,407 @@
+// rms_norm.cu -- root-mean-square norm of rows, with the residual's addition
+// and an output in 8 bits, and its backward pass.
+//
+// Forward, per row of D:
+//   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * w.
+// Backward, with xh = h * rstd and g = dy * w:
+//   dx = rstd * (g - xh * mean(g * xh)) + d_sum,  dw = sum over rows of dy * xh.
+//
+// A group of G threads holds a whole row in registers, NP pieces of 8 values
+// a thread, so that each value is read once; sums are fp32.
+#include <algorithm>
+#include <climits>
+
+#include "kv8.cuh"
+
+namespace {
+
+constexpr int kBf16 = 0, kE4m3 = 1, kMx = 2;  // forms of the output
+
+struct Piece {
+  float v[8];
+};
+
+__device__ __forceinline__ Piece unpack(uint4 u) {
+  Piece p;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p.v[2 * i] = __uint_as_float(w[i] << 16);
+    p.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return p;
+}
+__device__ __forceinline__ uint4 pack(const Piece& p) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.v[2 * i], p.v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Piece load_weight(const float* w) {
+  Piece p;
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  p.v[0] = a.x, p.v[1] = a.y, p.v[2] = a.z, p.v[3] = a.w;
+  p.v[4] = b.x, p.v[5] = b.y, p.v[6] = b.z, p.v[7] = b.w;
+  return p;
+}
+
+// Threads of a CTA: several groups where a group is a warp or less, else one.
+template <int G>
+struct Cta {
+  static constexpr int kThreads = G <= 32 ? 256 : G;
+  static constexpr int kGroups = kThreads / G;
+};
+
+// Sum over a group, the same in each of its threads.  `red`: one float per
+// warp; a CTA that calls this again in its next row takes another.
+template <int G>
+__device__ __forceinline__ float group_sum(float x, float* red) {
+#pragma unroll
+  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if constexpr (G > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < G / 32; ++w) x += red[w];
+  }
+  return x;
+}
+
+struct FwdParams {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* r;  // residual or NULL
+  const float* w;
+  __nv_bfloat16* sum;  // or NULL
+  void* y;
+  void* scale;
+  float* rstd;  // or NULL
+  int64_t ld_x, ld_r, ld_sum, ld_y;
+  int T, D;
+  float eps;
+};
+
+template <int G, int NP, int FMT>
+__global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdParams p) {
+  __shared__ float red[2][G > 32 ? G / 32 : 1];
+  const int sub = threadIdx.x % G, p8 = p.D >> 3;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * Cta<G>::kGroups + threadIdx.x / G;
+  const bool live = t < p.T;  // (all lanes take part in the reductions)
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 xr[NP], rr[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = k * G + sub;
+    xr[k] = live && c < p8 ? __ldcs(reinterpret_cast<const uint4*>(p.x + t * p.ld_x) + c) : zero;
+  }
+  if (p.r) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = k * G + sub;
+      rr[k] = live && c < p8 ? __ldcs(reinterpret_cast<const uint4*>(p.r + t * p.ld_r) + c) : zero;
+    }
+  }
+  Piece h[NP];
+  float sq = 0.f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    h[k] = unpack(xr[k]);
+    if (p.r) {
+      const Piece b = unpack(rr[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k].v[i] += b.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(h[k].v[i], h[k].v[i], sq);
+  }
+  sq = group_sum<G>(sq, red[0]);
+  float rstd = 1.f / sqrtf(sq / static_cast<float>(p.D) + p.eps);
+  // squares beyond fp32's range: again, of values 2^64 times smaller (eps is nothing beside them)
+  if (__any_sync(0xffffffffu, !(sq < INFINITY))) {
+    float small = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = h[k].v[i] * 0x1p-64f;
+        small = fmaf(v, v, small);
+      }
+    small = group_sum<G>(small, red[1]);
+    if (!(sq < INFINITY)) rstd = 0x1p-64f / sqrtf(small / static_cast<float>(p.D));
+  }
+  if (live && sub == 0 && p.rstd) p.rstd[t] = rstd;
+  if (live && p.sum) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = k * G + sub;
+      if (c < p8) reinterpret_cast<uint4*>(p.sum + t * p.ld_sum)[c] = pack(h[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = k * G + sub;
+    const bool have = live && c < p8;
+    if (have) {
+      const Piece w = load_weight(p.w + c * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k].v[i] = h[k].v[i] * rstd * w.v[i];
+    }
+    if constexpr (FMT == kBf16) {
+      if (have) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + t * p.ld_y)[c] = pack(h[k]);
+    } else {
+      // the largest finite magnitude of the lanes that share a scale
+      constexpr int kLanes = FMT == kE4m3 ? 16 : 4;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(h[k].v[i]) & 0x7FFFFFFFu;
+        m = max(m, have && u < 0x7F800000u ? u : 0u);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float s = dsa::kv8_scale_of(__uint_as_float(m)), inv = dsa::pow2_inverse(s);
+      uint32_t o[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        o[i] = dsa::e4m3x2(h[k].v[4 * i] * inv, h[k].v[4 * i + 1] * inv) |
+               (static_cast<uint32_t>(dsa::e4m3x2(h[k].v[4 * i + 2] * inv, h[k].v[4 * i + 3] * inv)) << 16);
+      if (have) {
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + t * p.ld_y)[c] = make_uint2(o[0], o[1]);
+        if (c % kLanes == 0) {
+          const int64_t at = t * (p8 / kLanes) + c / kLanes;
+          if (FMT == kE4m3)
+            static_cast<float*>(p.scale)[at] = s;
+          else
+            static_cast<uint8_t*>(p.scale)[at] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
+        }
+      }
+    }
+  }
+}
+
+struct BwdParams {
+  const __nv_bfloat16* dy;
+  const __nv_bfloat16* x;
+  const float* w;
+  const float* rstd;
+  const __nv_bfloat16* d_sum;  // or NULL
+  __nv_bfloat16* dx;
+  float* part;  // [CTAs, D] or NULL
+  int64_t ld_dy, ld_x, ld_ds, ld_dx;
+  int T, D;
+};
+
+// Groups go through the rows in steps of all groups of the grid; a thread keeps dw's
+// terms of its columns, the CTA adds its groups' and writes one row of `part`.
+template <int G, int NP>
+__global__ void __launch_bounds__(Cta<G>::kThreads) rms_bwd_kernel(const BwdParams p) {
+  constexpr int kGroups = Cta<G>::kGroups;
+  __shared__ float red[2][G > 32 ? G / 32 : 1];
+  extern __shared__ float cols[];  // [D], with several groups a CTA
+  const int sub = threadIdx.x % G, group = threadIdx.x / G, p8 = p.D >> 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  Piece dw[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k].v[i] = 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  int par = 0;
+  // all groups of a CTA make the same trips: their lanes meet in the reductions
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < p.T; t0 += step, par ^= 1) {
+    const int64_t t = t0 + group;
+    const bool live = t < p.T;
+    uint4 xr[NP], yr[NP], sr[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = k * G + sub;
+      const bool have = live && c < p8;
+      xr[k] = have ? __ldcs(reinterpret_cast<const uint4*>(p.x + t * p.ld_x) + c) : zero;
+      yr[k] = have ? __ldcs(reinterpret_cast<const uint4*>(p.dy + t * p.ld_dy) + c) : zero;
+      sr[k] = have && p.d_sum ? __ldcs(reinterpret_cast<const uint4*>(p.d_sum + t * p.ld_ds) + c) : zero;
+    }
+    const float rstd = live ? __ldg(p.rstd + t) : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = k * G + sub;
+      if (c < p8) {
+        const Piece x = unpack(xr[k]), y = unpack(yr[k]), w = load_weight(p.w + c * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xh = x.v[i] * rstd;
+          dot = fmaf(y.v[i] * w.v[i], xh, dot);
+          dw[k].v[i] = fmaf(y.v[i], xh, dw[k].v[i]);
+        }
+      }
+    }
+    const float mean = group_sum<G>(dot, red[par]) / static_cast<float>(p.D);
+    if (!live) continue;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = k * G + sub;
+      if (c >= p8) continue;
+      const Piece x = unpack(xr[k]), y = unpack(yr[k]), s = unpack(sr[k]), w = load_weight(p.w + c * 8);
+      Piece o;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.v[i] = fmaf(rstd, y.v[i] * w.v[i] - x.v[i] * rstd * mean, s.v[i]);
+      reinterpret_cast<uint4*>(p.dx + t * p.ld_dx)[c] = pack(o);
+    }
+  }
+  if (!p.part) return;
+  float* row = p.part + static_cast<int64_t>(blockIdx.x) * p.D;
+  for (int g = 0; g < kGroups; ++g) {  // in order, so that the sums are the same in every run
+    if (group == g) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = k * G + sub;
+        if (c >= p8) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float* at = cols + c * 8 + i;
+          const float v = dw[k].v[i] + (g > 0 ? *at : 0.f);
+          if (g + 1 < kGroups) *at = v;
+          else row[c * 8 + i] = v;
+        }
+      }
+    }
+    if (kGroups > 1) __syncthreads();
+  }
+}
+
+// dw = the sum of `n` rows of partial sums: a CTA takes 32 columns, its 8
+// warps every eighth row, added in a fixed order.
+__global__ void __launch_bounds__(256) rms_dw_kernel(const float* __restrict__ part, int n, int D,
+                                                     float* __restrict__ dw) {
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < D)
+    for (int i = warp; i < n; i += 8) v += part[static_cast<int64_t>(i) * D + c];
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < D) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += s[w][lane];
+    dw[c] = v;
+  }
+}
+
+// Threads a row and pieces a thread, by the row's length.
+template <class F>
+void by_width(int D, F f) {
+  using dsa_int = int;
+  if (D <= 64) f(std::integral_constant<dsa_int, 8>{}, std::integral_constant<dsa_int, 1>{});
+  else if (D <= 128) f(std::integral_constant<dsa_int, 16>{}, std::integral_constant<dsa_int, 1>{});
+  else if (D <= 256) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 1>{});
+  else if (D <= 512) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 2>{});
+  else if (D <= 1024) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 4>{});
+  else if (D <= 2048) f(std::integral_constant<dsa_int, 128>{}, std::integral_constant<dsa_int, 2>{});
+  else if (D <= 4096) f(std::integral_constant<dsa_int, 256>{}, std::integral_constant<dsa_int, 2>{});
+  else if (D <= 8192) f(std::integral_constant<dsa_int, 512>{}, std::integral_constant<dsa_int, 2>{});
+  else f(std::integral_constant<dsa_int, 512>{}, std::integral_constant<dsa_int, 4>{});
+}
+
+constexpr int kPlanSms = 152;
+
+// CTAs of the backward pass: what is resident at once, fewer for few rows.
+int bwd_ctas(int T, int D) {
+  const int groups = D <= 64 ? 32 : D <= 128 ? 16 : D <= 1024 ? 8 : 1;
+  const int per_sm = D <= 2048 ? 8 : D <= 4096 ? 4 : 2;
+  return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(T) + groups - 1) / groups, per_sm * kPlanSms));
+}
+
+bool width_ok(int D) { return D >= 8 && D <= DSA_NORM_MAX_DIM && D % 8 == 0; }
+bool stride_ok(int64_t ld, int D) { return ld >= D && ld % 8 == 0; }
+
+}  // namespace
+
+extern "C" int dsa_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const float* weight,
+                                int T, int D, float eps, int fmt, void* y, int64_t ld_y, void* y_scale, void* sum,
+                                int64_t ld_sum, float* rstd, cudaStream_t stream) {
+  dsa::clear_error();
+  const char* fn = "dsa_rms_norm_fwd";
+  if (fmt != DSA_NORM_BF16 && fmt != DSA_NORM_E4M3 && fmt != DSA_NORM_MXFP8)
+    return dsa::set_error(DSA_ERR_VALUE, "%s: fmt must be DSA_NORM_BF16, DSA_NORM_E4M3 or DSA_NORM_MXFP8", fn);
+  const int group = fmt == DSA_NORM_E4M3 ? 128 : fmt == DSA_NORM_MXFP8 ? 32 : 8;
+  if (T < 0 || !width_ok(D) || D % group != 0)
+    return dsa::set_error(DSA_ERR_VALUE, "%s: need T >= 0 and D a multiple of %d in [%d, %d]", fn, group, group,
+                          DSA_NORM_MAX_DIM);
+  if (!(eps > 0.f) || !(eps < INFINITY)) return dsa::set_error(DSA_ERR_VALUE, "%s: eps must be finite and > 0", fn);
+  if (!stride_ok(ld_x, D) || !stride_ok(ld_y, D) || (residual && !stride_ok(ld_r, D)) || (sum && !stride_ok(ld_sum, D)))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: row strides must be at least D and multiples of 8", fn);
+  if (T > 0 && ((y == x && (fmt != DSA_NORM_BF16 || ld_y != ld_x)) || (sum == x && sum && ld_sum != ld_x) ||
+      (residual && ((y == residual && (fmt != DSA_NORM_BF16 || ld_y != ld_r)) || (sum == residual && ld_sum != ld_r))) ||
+      (sum && y == sum)))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: in place, y or sum takes the rows and the stride of x or residual", fn);
+  if (!weight || (T > 0 && (!x || !y || (fmt != DSA_NORM_BF16 && !y_scale))))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: NULL pointer", fn);
+  if (!dsa::aligned(x, 16) || !dsa::aligned(residual, 16) || !dsa::aligned(weight, 16) || !dsa::aligned(sum, 16) ||
+      !dsa::aligned(y, fmt == DSA_NORM_BF16 ? 16 : 8) || !dsa::aligned(rstd, 4) ||
+      !dsa::aligned(y_scale, fmt == DSA_NORM_E4M3 ? 4 : 1))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: x, residual, weight, sum and y must be 16-byte aligned (8-bit y: 8)", fn);
+  int rc = dsa::check_device(nullptr);
+  if (rc != DSA_OK) return rc;
+  if (T == 0) return DSA_OK;
+  const FwdParams p{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(residual), weight,
+                    static_cast<__nv_bfloat16*>(sum), y, y_scale, rstd, ld_x, ld_r, ld_sum, ld_y, T, D, eps};
+  by_width(D, [&](auto g, auto np) {
+    constexpr int G = decltype(g)::value, NP = decltype(np)::value;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + Cta<G>::kGroups - 1) / Cta<G>::kGroups);
+    if (fmt == DSA_NORM_BF16)
+      rms_fwd_kernel<G, NP, kBf16><<<grid, Cta<G>::kThreads, 0, stream>>>(p);
+    else if (fmt == DSA_NORM_MXFP8)
+      rms_fwd_kernel<G, NP, kMx><<<grid, Cta<G>::kThreads, 0, stream>>>(p);
+    else if constexpr (G >= 16)
+      rms_fwd_kernel<G, NP, kE4m3><<<grid, Cta<G>::kThreads, 0, stream>>>(p);
+  });
+  return dsa::launch_error("rms_fwd_kernel");
+}
+
+extern "C" size_t dsa_rms_norm_bwd_workspace_size(int T, int D) {
+  if (T < 1 || !width_ok(D)) return 0;
+  return static_cast<size_t>(bwd_ctas(T, D)) * D * sizeof(float);
+}
+
+extern "C" int dsa_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const float* weight,
+                                const float* rstd, const void* d_sum, int64_t ld_ds, int T, int D, void* dx,
+                                int64_t ld_dx, float* dweight, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  dsa::clear_error();
+  const char* fn = "dsa_rms_norm_bwd";
+  if (T < 0 || !width_ok(D))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: need T >= 0 and D a multiple of 8 in [8, %d]", fn, DSA_NORM_MAX_DIM);
+  if (!stride_ok(ld_dy, D) || !stride_ok(ld_x, D) || !stride_ok(ld_dx, D) || (d_sum && !stride_ok(ld_ds, D)))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: row strides must be at least D and multiples of 8", fn);
+  if (T > 0 && ((dx == dy && ld_dx != ld_dy) || (dx == x && ld_dx != ld_x) || (dx == d_sum && ld_dx != ld_ds)))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: in place, dx takes the stride of its rows", fn);
+  if (!weight || (T > 0 && (!dy || !x || !rstd || !dx))) return dsa::set_error(DSA_ERR_VALUE, "%s: NULL pointer", fn);
+  if (!dsa::aligned(dy, 16) || !dsa::aligned(x, 16) || !dsa::aligned(weight, 16) || !dsa::aligned(d_sum, 16) ||
+      !dsa::aligned(dx, 16) || !dsa::aligned(rstd, 4) || !dsa::aligned(dweight, 4))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: dy, x, weight, d_sum and dx must be 16-byte aligned", fn);
+  const size_t need = dweight ? dsa_rms_norm_bwd_workspace_size(T, D) : 0;
+  if (need > 0 && (!workspace || ws_bytes < need || !dsa::aligned(workspace, 256)))
+    return dsa::set_error(DSA_ERR_WORKSPACE, "%s: needs a 256-byte aligned workspace of %zu bytes, got %zu", fn, need,
+                          workspace ? ws_bytes : static_cast<size_t>(0));
+  int rc = dsa::check_device(nullptr);
+  if (rc != DSA_OK) return rc;
+  if (T == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * sizeof(float), stream) != cudaSuccess)
+      return dsa::launch_error("dsa_rms_norm_bwd zero dweight");
+    return DSA_OK;
+  }
+  const int ctas = bwd_ctas(T, D);
+  const BwdParams p{static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(x), weight, rstd,
+                    static_cast<const __nv_bfloat16*>(d_sum), static_cast<__nv_bfloat16*>(dx),
+                    dweight ? static_cast<float*>(workspace) : nullptr, ld_dy, ld_x, ld_ds, ld_dx, T, D};
+  by_width(D, [&](auto g, auto np) {
+    constexpr int G = decltype(g)::value, NP = decltype(np)::value;
+    rms_bwd_kernel<G, NP><<<ctas, Cta<G>::kThreads, Cta<G>::kGroups > 1 ? D * sizeof(float) : 0, stream>>>(p);
+  });
+  rc = dsa::launch_error("rms_bwd_kernel");
+  if (rc != DSA_OK || !dweight) return rc;
+  rms_dw_kernel<<<(D + 31) / 32, 256, 0, stream>>>(p.part, ctas, D, dweight);
+  return dsa::launch_error("rms_dw_kernel");
+}

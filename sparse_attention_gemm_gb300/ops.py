@@ -40,6 +40,7 @@ P = ctypes.c_void_p
 I = ctypes.c_int
 I64 = ctypes.c_int64
 F = ctypes.c_float
+D = ctypes.c_double
 SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -75,6 +76,15 @@ _SIGNATURES = {
     "dsa_kv8_read": ([P, P, P, P, P, I, I, I, I, I, I, I, P, P], I),
     "dsa_sparse_attn_fwd_kv8_workspace_size": ([I, I, I, I, I, I], SZ),
     "dsa_sparse_attn_fwd_kv8": ([P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
+    "dsa_kv4_write": ([P, P, P, P, I, I, I, I, I, I, I, P, P, P], I),
+    "dsa_kv4_read": ([P, P, P, P, P, I, I, I, I, I, I, I, P, P], I),
+    "dsa_sparse_attn_fwd_kv4_workspace_size": ([I, I, I, I, I, I], SZ),
+    "dsa_sparse_attn_fwd_kv4": ([P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
+    "dsa_rms_norm_fwd": ([P, I64, P, I64, P, I, I, F, I, P, I64, P, P, I64, P, P], I),
+    "dsa_rms_norm_bwd_workspace_size": ([I, I], SZ),
+    "dsa_rms_norm_bwd": ([P, I64, P, I64, P, P, P, I64, I, I, P, I64, P, P, SZ, P], I),
+    "dsa_rotary": ([P, I64, I64, I, P, I64, I64, I, P, P, P, I, I, I, I, I, F, P, I64, I64, P, I64, I64, P], I),
+    "dsa_rotary_inv_freq": ([I, D, I, D, I64, D, D, P, P], I),
     "dsa_sparse_attn_bwd_ex": ([P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, I, P, SZ, P], I),
 }
 
@@ -797,3 +807,346 @@ def sparse_attn_fwd_kv8(q, kv8, kv_scale, idx, scale: float, topk_length=None, s
     if ml is not None:
         res["max_logits"] = ml
     return res
+
+
+def _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T):
+    _need(cache, "cache", _U8, 4)
+    _need(cu_seqlens, "cu_seqlens", _I32, 1)
+    n_blocks, block, heads, half = cache.shape
+    n_seqs = cu_seqlens.shape[0] - 1
+    args = [(cache, "cache", _U8, 4, None), (cache_scale, "cache_scale", _U8, 4, (n_blocks, block, heads, half // 16)),
+            (cu_seqlens, "cu_seqlens", _I32, 1, None)]
+    if pos is not None:
+        args.append((pos, "pos", _I32, 1, (n_seqs,)))
+    if block_table is not None:
+        _need(block_table, "block_table", _I32, 2)
+        args.append((block_table, "block_table", _I32, 2, (n_seqs, block_table.shape[1])))
+    _need(rows, rows_name, _BF16, 3)
+    args.append((rows, rows_name, _BF16, 3, (rows.shape[0] if T is None else T, heads, 2 * half)))
+    _refuse(cache.get_device(), *args)
+
+
+def _kv4_call(rows, rows_name, T, cache, cache_scale, cu_seqlens, pos, block_table):
+    """Checks what the writer and the reader share; their arguments from cu_seqlens to max_blocks."""
+    dev = cache.get_device() if isinstance(cache, _Tensor) else -1
+    if not (dev >= 0 and dev == _current_device() and _ok(cache, _U8, 4, dev) and _ok(cache_scale, _U8, 4, dev) and
+            _ok(cu_seqlens, _I32, 1, dev) and _ok(rows, _BF16, 3, dev) and (pos is None or _ok(pos, _I32, 1, dev)) and
+            (block_table is None or _ok(block_table, _I32, 2, dev))):
+        _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T)
+    n_blocks, block, heads, half = cache.shape
+    n_seqs = cu_seqlens.shape[0] - 1
+    n_rows, width = (n_seqs, 0) if block_table is None else block_table.shape
+    if (rows.shape != (rows.shape[0] if T is None else T, heads, 2 * half) or
+            cache_scale.shape != (n_blocks, block, heads, half // 16) or n_rows != n_seqs or
+            (pos is not None and pos.shape[0] != n_seqs)):
+        _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T)
+    return (cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(),
+            None if block_table is None else block_table.data_ptr(), n_seqs, rows.shape[0], heads, 2 * half, block,
+            n_blocks, width), dev
+
+
+def kv4_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
+    """Quantises the bf16 rows src [T, Hc, D] into the 4-bit block cache (codes uint8
+    [n_blocks, block, Hc, D / 2], scale uint8 [n_blocks, block, Hc, D / 32]), in place; returns both."""
+    args, dev = _kv4_call(src, "src", None, cache, cache_scale, cu_seqlens, pos, block_table)
+    rc = (_lib or lib()).dsa_kv4_write(src.data_ptr(), *args, cache.data_ptr(), cache_scale.data_ptr(),
+                                       _raw_stream(dev))
+    if rc:
+        _check("dsa_kv4_write", rc)
+    return cache, cache_scale
+
+
+def kv4_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None, out=None):
+    """Rows of the 4-bit block cache back to packed bf16 [T, Hc, D].  Rows behind the last
+    sequence are not written: an `out` that is given keeps them, a new one has anything there."""
+    if out is None and isinstance(cache, _Tensor) and cache.is_cuda and cache.dim() == 4:
+        out = torch.empty((T, cache.shape[2], 2 * cache.shape[3]), dtype=_BF16, device=cache.device)
+    args, dev = _kv4_call(out, "out", T, cache, cache_scale, cu_seqlens, pos, block_table)
+    rc = (_lib or lib()).dsa_kv4_read(cache.data_ptr(), cache_scale.data_ptr(), *args, out.data_ptr(),
+                                      _raw_stream(dev))
+    if rc:
+        _check("dsa_kv4_read", rc)
+    return out
+
+
+def sparse_attn_fwd_kv4_workspace_size(T: int, H: int, Hc: int, Dqk: int, Dv: int, K: int) -> int:
+    return int(lib().dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K))
+
+
+def _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse, workspace):
+    _need(q, "q", _BF16, 3)
+    _need(kv4, "kv4", _U8, 4)
+    T, H, Dqk = q.shape
+    n_blocks, block, heads, _ = kv4.shape
+    if (v4 is None) != (v_scale is None):
+        raise ValueError("v4 and v_scale go together")
+    if block_table is not None and cu_seqlens is None:
+        raise ValueError("block_table needs cu_seqlens")
+    args = [(q, "q", _BF16, 3, None), (kv4, "kv4", _U8, 4, (n_blocks, block, heads, Dqk // 2)),
+            (kv_scale, "kv_scale", _U8, 4, (n_blocks, block, heads, Dqk // 32))]
+    _need(idx, "idx", _I32, 2)
+    args.append((idx, "idx", _I32, 2, (T, idx.shape[1])))
+    Dv = 512
+    if v4 is not None:
+        _need(v4, "v4", _U8, 4)
+        Dv = 2 * v4.shape[3]
+        args += [(v4, "v4", _U8, 4, (n_blocks, block, heads, Dv // 2)),
+                 (v_scale, "v_scale", _U8, 4, (n_blocks, block, heads, Dv // 32))]
+    if block_table is not None:
+        _need(block_table, "block_table", _I32, 2)
+        args += [(block_table, "block_table", _I32, 2, None),
+                 (cu_seqlens, "cu_seqlens", _I32, 1, (block_table.shape[0] + 1,))]
+    args += [a for a in ((topk_length, "topk_length", _I32, 1, (T,)), (sink, "sink", _F32, 1, (H,)),
+                         (out, "out", _BF16, 3, (T, H, Dv)), (lse, "lse", _F32, 2, (T, H)),
+                         (workspace, "workspace", _U8, 1, None)) if a[0] is not None]
+    _refuse(q.get_device(), *args)
+
+
+def sparse_attn_fwd_kv4(q, kv4, kv_scale, idx, scale: float, topk_length=None, sink=None, v4=None, v_scale=None,
+                        cu_seqlens=None, block_table=None, want_lse_kv: bool = False, want_max_logits: bool = False,
+                        out=None, lse=None, workspace=None):
+    """Sparse attention forward over the 4-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
+    idx, block_table and rows behind the last sequence as in sparse_attn_fwd_kv8."""
+    dev = q.get_device() if isinstance(q, _Tensor) else -1
+    paged = block_table is not None
+    if not (dev >= 0 and dev == _current_device() and _ok(q, _BF16, 3, dev) and _ok(kv4, _U8, 4, dev) and
+            _ok(kv_scale, _U8, 4, dev) and
+            _ok(idx, _I32, 2, dev) and (topk_length is None or _ok(topk_length, _I32, 1, dev)) and
+            (sink is None or _ok(sink, _F32, 1, dev)) and
+            (v4 is None if v_scale is None else _ok(v4, _U8, 4, dev) and _ok(v_scale, _U8, 4, dev)) and
+            (not paged or _ok(block_table, _I32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev)) and
+            (out is None or _ok(out, _BF16, 3, dev)) and (lse is None or _ok(lse, _F32, 2, dev)) and
+            (workspace is None or _ok(workspace, _U8, 1, dev))):
+        _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse,
+                      workspace)
+    T, H, Dqk = q.shape
+    n_blocks, block, heads, half = kv4.shape
+    K = idx.shape[1]
+    Dv = 512 if v4 is None else 2 * v4.shape[3]
+    n_seqs, width = (0, 0) if not paged else block_table.shape
+    if (2 * half != Dqk or kv_scale.shape != (n_blocks, block, heads, half // 16) or idx.shape[0] != T or
+            (topk_length is not None and topk_length.shape[0] != T) or (sink is not None and sink.shape[0] != H) or
+            (v4 is not None and (v4.shape != (n_blocks, block, heads, Dv // 2) or
+                                 v_scale.shape != (n_blocks, block, heads, Dv // 32))) or
+            (paged and cu_seqlens.shape[0] != n_seqs + 1) or (out is not None and out.shape != (T, H, Dv)) or
+            (lse is not None and lse.shape != (T, H))):
+        _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse,
+                      workspace)
+    device, empty = q.device, torch.empty
+    if out is None:
+        out = empty((T, H, Dv), dtype=_BF16, device=device)
+    if lse is None:
+        lse = empty((T, H), dtype=_F32, device=device)
+    lse_kv = empty((T, H), dtype=_F32, device=device) if want_lse_kv else None
+    ml = empty((T, H), dtype=_F32, device=device) if want_max_logits else None
+    L = _lib or lib()
+    if workspace is None:
+        need = L.dsa_sparse_attn_fwd_kv4_workspace_size(T, H, heads, Dqk, Dv, K)
+        if need:
+            workspace = empty(need, dtype=_U8, device=device)
+    rc = L.dsa_sparse_attn_fwd_kv4(
+        q.data_ptr(), kv4.data_ptr(), kv_scale.data_ptr(), None if v4 is None else v4.data_ptr(),
+        None if v4 is None else v_scale.data_ptr(), idx.data_ptr(),
+        None if topk_length is None else topk_length.data_ptr(), None if sink is None else sink.data_ptr(),
+        cu_seqlens.data_ptr() if paged else None, block_table.data_ptr() if paged else None, n_seqs, T, H, heads, Dqk,
+        Dv, K, block, n_blocks, width, scale, out.data_ptr(), lse.data_ptr(),
+        None if lse_kv is None else lse_kv.data_ptr(), None if ml is None else ml.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
+        _raw_stream(dev))
+    if rc:
+        _check("dsa_sparse_attn_fwd_kv4", rc)
+    res = {"out": out, "lse": lse}
+    if lse_kv is not None:
+        res["lse_kv"] = lse_kv
+    if ml is not None:
+        res["max_logits"] = ml
+    return res
+
+
+# Norm and rotary positions: rows may lie apart, so what is asked of a tensor is
+# a last dimension without gaps; the C side checks the other strides.
+_NORM_FORMS = {"bf16": (0, 0), "e4m3": (1, 128), "mxfp8": (2, 32)}
+
+
+def _strided(t, dtype, shape, device):
+    """Whether t is a tensor of this kind, shape and device whose last dimension has no gaps."""
+    return (isinstance(t, _Tensor) and t.dtype == dtype and t.shape == shape and t.stride(-1) == 1 and
+            t.get_device() == device)
+
+
+def _strided_refuse(device, *args):
+    """Raises for the first of (tensor, name, dtype, shape, strided) that is not as it has to be."""
+    for t, name, dtype, shape, strided in args:
+        if not isinstance(t, _Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != device or device != _current_device():
+            raise ValueError(f"{name} is on {t.device}: the tensors of a call are on the current device, "
+                             f"cuda:{_current_device()}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not (t.stride(-1) == 1 if strided else t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if strided else ""))
+    raise ValueError("inconsistent arguments")
+
+
+def _ld(t):
+    """Row stride of a [T, D] tensor; that of a single row is nobody's business."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def rms_norm_fwd(x, weight, eps: float, residual=None, fmt: str = "bf16", out=None, sum_out=None, scale=None,
+                 want_rstd: bool = False):
+    """Root-mean-square norm of the rows of x [T, D] (plus residual): dict(out[, sum][, scale][, rstd]).
+    fmt "bf16": out bf16; "e4m3": out uint8 codes and scale fp32 [T, D / 128]; "mxfp8": codes and
+    scale uint8 [T, D / 32] (E8M0).  sum: x + residual in bf16, with a residual.  Rows of x, residual, out and
+    sum_out may lie apart; out and sum_out may be x or residual."""
+    if fmt not in _NORM_FORMS:
+        raise ValueError(f"fmt must be one of {sorted(_NORM_FORMS)}, got {fmt!r}")
+    if not isinstance(x, _Tensor) or x.dim() != 2:
+        raise TypeError("x must be a torch.Tensor of 2 dimensions")
+    form, group = _NORM_FORMS[fmt]
+    shape, dev = x.shape, x.get_device()
+    T, D = shape
+    y_type = _U8 if form else _BF16
+    s_type, s_shape = (_F32 if form == 1 else _U8), (T, D // group if form else 0)
+    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
+            _strided(weight, _F32, (D,), dev) and (residual is None or _strided(residual, _BF16, shape, dev)) and
+            (out is None or _strided(out, y_type, shape, dev)) and
+            (sum_out is None or _strided(sum_out, _BF16, shape, dev)) and
+            (scale is None or form and _strided(scale, s_type, s_shape, dev) and scale.is_contiguous())):
+        if scale is not None and not form:
+            raise ValueError("scale goes with the 8-bit forms")
+        _strided_refuse(dev, (x, "x", _BF16, shape, True), (weight, "weight", _F32, (D,), False),
+                        *[a for a in ((residual, "residual", _BF16, shape, True), (out, "out", y_type, shape, True),
+                                      (sum_out, "sum_out", _BF16, shape, True),
+                                      (scale, "scale", s_type, s_shape, False)) if a[0] is not None])
+    empty, device = torch.empty, x.device
+    if out is None:
+        out = empty(shape, dtype=y_type, device=device)
+    if sum_out is None and residual is not None:
+        sum_out = empty(shape, dtype=_BF16, device=device)
+    if form and scale is None:
+        scale = empty(s_shape, dtype=s_type, device=device)
+    rstd = empty((T,), dtype=_F32, device=device) if want_rstd else None
+    rc = (_lib or lib()).dsa_rms_norm_fwd(
+        x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(), 0 if residual is None else _ld(residual),
+        weight.data_ptr(), T, D, eps, form, out.data_ptr(), _ld(out), None if scale is None else scale.data_ptr(),
+        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else _ld(sum_out),
+        None if rstd is None else rstd.data_ptr(), _raw_stream(dev))
+    if rc:
+        _check("dsa_rms_norm_fwd", rc)
+    res = {"out": out}
+    if sum_out is not None:
+        res["sum"] = sum_out
+    if form:
+        res["scale"] = scale
+    if want_rstd:
+        res["rstd"] = rstd
+    return res
+
+
+def rms_norm_bwd_workspace_size(T: int, D: int) -> int:
+    return int(lib().dsa_rms_norm_bwd_workspace_size(T, D))
+
+
+def rms_norm_bwd(dy, x, weight, rstd, d_sum=None, want_dweight: bool = True, dx=None, workspace=None):
+    """Backward of rms_norm_fwd: dict(dx bf16 [T, D], dweight fp32 [D] or None).  x: the forward's sum (its x
+    without a residual); dx is the gradient of x and of the residual alike.  Rows may lie apart."""
+    if not isinstance(x, _Tensor) or x.dim() != 2:
+        raise TypeError("x must be a torch.Tensor of 2 dimensions")
+    shape, dev = x.shape, x.get_device()
+    T, D = shape
+    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
+            _strided(dy, _BF16, shape, dev) and _strided(weight, _F32, (D,), dev) and _ok(rstd, _F32, 1, dev) and
+            rstd.shape[0] == T and (d_sum is None or _strided(d_sum, _BF16, shape, dev)) and
+            (dx is None or _strided(dx, _BF16, shape, dev)) and (workspace is None or _ok(workspace, _U8, 1, dev))):
+        args = [(dy, "dy", _BF16, shape, True), (x, "x", _BF16, shape, True), (weight, "weight", _F32, (D,), False),
+                (rstd, "rstd", _F32, (T,), False)]
+        args += [a for a in ((d_sum, "d_sum", _BF16, shape, True), (dx, "dx", _BF16, shape, True)) if a[0] is not None]
+        if isinstance(workspace, _Tensor):
+            args.append((workspace, "workspace", _U8, (workspace.numel(),), False))
+        _strided_refuse(dev, *args)
+    if dx is None:
+        dx = torch.empty(shape, dtype=_BF16, device=x.device)
+    L = _lib or lib()
+    dweight = None
+    if want_dweight:
+        dweight = torch.empty((D,), dtype=_F32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty((L.dsa_rms_norm_bwd_workspace_size(T, D),), dtype=_U8, device=x.device)
+    rc = L.dsa_rms_norm_bwd(
+        dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), weight.data_ptr(), rstd.data_ptr(),
+        None if d_sum is None else d_sum.data_ptr(), 0 if d_sum is None else _ld(d_sum), T, D, dx.data_ptr(), _ld(dx),
+        None if dweight is None else dweight.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.shape[0], _raw_stream(dev))
+    if rc:
+        _check("dsa_rms_norm_bwd", rc)
+    return {"dx": dx, "dweight": dweight}
+
+
+_ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rotary_inv_freq(R: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, first: int = 4096,
+                    beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(inv_freq fp64 [R / 2] on `device`, mul) for rotary(); scaling "plain", "linear", "ntk" or "yarn"."""
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)}, got {scaling!r}")
+    freq, mul = torch.empty(max(R, 0) // 2, dtype=torch.float64), ctypes.c_float(0.0)
+    _check("dsa_rotary_inv_freq",
+           lib().dsa_rotary_inv_freq(R, base, _ROTARY_SCALINGS[scaling], factor, first, beta_fast, beta_slow,
+                                     freq.data_ptr(), ctypes.byref(mul)))
+    return freq.to(device or "cuda"), float(mul.value)
+
+
+def _rotary_strides(t):
+    """Strides of token and head; those of a single one are nobody's business."""
+    s = t.stride()
+    T, H, R = t.shape
+    return s[0] if T > 1 else H * R, s[1] if H > 1 else R
+
+
+def rotary(x, inv_freq, cu_seqlens, pos=None, x2=None, interleaved: bool = True, mul: float = 1.0,
+           inverse: bool = False, out=None, out2=None):
+    """Rotary positions of x bf16 [T, H, R] and, in the same call, x2 [T, H2, R]: (out, out2 or None).  Token t of
+    sequence b stands at pos[b] + t - cu_seqlens[b] (pos None: 0).  Part of a head is x[..., a:b], in place with out=x;
+    inverse: the adjoint, for gradients.  Rows of tokens outside the sequences are not written."""
+    if not isinstance(x, _Tensor) or x.dim() != 3:
+        raise TypeError("x must be a torch.Tensor of 3 dimensions")
+    if x2 is not None and (not isinstance(x2, _Tensor) or x2.dim() != 3):
+        raise TypeError("x2 must be a torch.Tensor of 3 dimensions")
+    if x2 is None and out2 is not None:
+        raise ValueError("out2 goes with x2")
+    shape, dev = x.shape, x.get_device()
+    T, H, R = shape
+    H2 = 0 if x2 is None else x2.shape[1]
+    shape2 = (T, H2, R)
+    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
+            _ok(inv_freq, torch.float64, 1, dev) and inv_freq.shape[0] == R // 2 and _ok(cu_seqlens, _I32, 1, dev) and
+            (pos is None or _ok(pos, _I32, 1, dev) and pos.shape[0] == cu_seqlens.shape[0] - 1) and
+            (x2 is None or _strided(x2, _BF16, shape2, dev)) and (out is None or _strided(out, _BF16, shape, dev)) and
+            (out2 is None or _strided(out2, _BF16, shape2, dev))):
+        _need(cu_seqlens, "cu_seqlens", _I32, 1)
+        args = [(x, "x", _BF16, shape, True), (inv_freq, "inv_freq", torch.float64, (R // 2,), False),
+                (cu_seqlens, "cu_seqlens", _I32, cu_seqlens.shape, False)]
+        args += [a for a in ((pos, "pos", _I32, (cu_seqlens.shape[0] - 1,), False), (x2, "x2", _BF16, shape2, True),
+                             (out, "out", _BF16, shape, True), (out2, "out2", _BF16, shape2, True)) if a[0] is not None]
+        _strided_refuse(dev, *args)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
+    if x2 is not None and out2 is None:
+        out2 = torch.empty(shape2, dtype=_BF16, device=x.device)
+    xs, ys = _rotary_strides(x), _rotary_strides(out)
+    xs2, ys2 = ((0, 0), (0, 0)) if x2 is None else (_rotary_strides(x2), _rotary_strides(out2))
+    rc = (_lib or lib()).dsa_rotary(
+        x.data_ptr(), xs[0], xs[1], H, None if x2 is None else x2.data_ptr(), xs2[0], xs2[1], H2, inv_freq.data_ptr(),
+        cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(), cu_seqlens.shape[0] - 1, T, R,
+        1 if interleaved else 0, 1 if inverse else 0, mul, out.data_ptr(), ys[0], ys[1],
+        None if x2 is None else out2.data_ptr(), ys2[0], ys2[1], _raw_stream(dev))
+    if rc:
+        _check("dsa_rotary", rc)
+    return out, out2
