@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   load(threadIdx.x);
-  if (threadIdx.x < tokens) rows[threadIdx.x] = dsa::row_of_token(g, t0 + threadIdx.x);
+  dsa::rows_of_tokens<kThreads>(g, t0, tokens, rows);
   __syncthreads();
   // (n is a multiple of 4: the four lanes of a scale are in or out together, and every lane of a
   // warp makes the same trips to the shuffles)
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
                     int D, int tokens, uint32_t magic_row, __nv_bfloat16* __restrict__ out) {
   __shared__ int rows[kMaxTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  if (threadIdx.x < tokens) rows[threadIdx.x] = dsa::row_of_token(g, t0 + threadIdx.x);
+  dsa::rows_of_tokens<kThreads>(g, t0, tokens, rows);
   __syncthreads();
   const int per = Hc * (D >> 3);
   const int n = static_cast<int>(min(static_cast<int64_t>(tokens), g.T - t0)) * per;
@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Tokens per CTA: four rounds of its threads' pieces, fewer where the batch would not
-// fill the device twice.  fast_div: several tokens have 4096 pieces at most.
+// Tokens per CTA: one round of its threads' pieces, fewer where the batch would not
+// fill the device twice.  fast_div: several tokens have 1024 pieces at most.
 int tokens_per_cta(int T, int Hc, int D, int sms) {
-  const int n = std::max(1, std::min(kMaxTokens, 4 * kThreads * kAhead / (Hc * (D / 8))));
+  const int n = std::max(1, std::min(kMaxTokens, kThreads * kAhead / (Hc * (D / 8))));
   return std::max(1, std::min(n, T / (2 * sms)));
 }
 

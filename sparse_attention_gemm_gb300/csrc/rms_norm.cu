@@ -194,13 +194,21 @@ struct BwdParams {
   int T, D;
 };
 
-// Groups go through the rows in steps of all groups of the grid; a thread keeps dw's
-// terms of its columns, the CTA adds its groups' and writes one row of `part`.
+// Groups go through the rows in steps of all groups of the grid, a row's loads
+// under way while the row before it is worked on; a thread keeps dw's terms of its
+// columns, the CTA adds its groups' and writes one row of `part`.
+// Resident CTAs an SM: what 64 registers a thread leave room for, 3 of 85 with two pieces a lane.
 template <int G, int NP>
-__global__ void __launch_bounds__(Cta<G>::kThreads) rms_bwd_kernel(const BwdParams p) {
+__host__ __device__ constexpr int bwd_per_sm() {
+  return G == 32 && NP == 2 ? 3 : 1024 / Cta<G>::kThreads;
+}
+
+template <int G, int NP>
+__global__ void __launch_bounds__(Cta<G>::kThreads, (bwd_per_sm<G, NP>())) rms_bwd_kernel(const BwdParams p) {
+  constexpr bool kAhead = NP * G <= 1024;  // two pieces of 1024 threads leave no registers for the next row
   constexpr int kGroups = Cta<G>::kGroups;
   __shared__ float red[2][G > 32 ? G / 32 : 1];
-  extern __shared__ float cols[];  // [D], with several groups a CTA
+  extern __shared__ float cols[];  // [groups][D], with several groups a CTA
   const int sub = threadIdx.x % G, group = threadIdx.x / G, p8 = p.D >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   Piece dw[NP];
@@ -209,109 +217,144 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_bwd_kernel(const BwdPara
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[k].v[i] = 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const float inv_d = 1.f / static_cast<float>(p.D);
   int par = 0;
-  // all groups of a CTA make the same trips: their lanes meet in the reductions
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < p.T; t0 += step, par ^= 1) {
-    const int64_t t = t0 + group;
-    const bool live = t < p.T;
-    uint4 xr[NP], yr[NP], sr[NP];
+  uint4 xr[NP], yr[NP], sr[NP];
+  float rstd = 0.f;
+  auto load = [&](int64_t t) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = k * G + sub;
-      const bool have = live && c < p8;
+      const bool have = t < p.T && c < p8;
       xr[k] = have ? __ldcs(reinterpret_cast<const uint4*>(p.x + t * p.ld_x) + c) : zero;
       yr[k] = have ? __ldcs(reinterpret_cast<const uint4*>(p.dy + t * p.ld_dy) + c) : zero;
       sr[k] = have && p.d_sum ? __ldcs(reinterpret_cast<const uint4*>(p.d_sum + t * p.ld_ds) + c) : zero;
     }
-    const float rstd = live ? __ldg(p.rstd + t) : 0.f;
+    rstd = t < p.T ? __ldg(p.rstd + t) : 0.f;
+  };
+  load(static_cast<int64_t>(blockIdx.x) * kGroups + group);
+  // all groups of a CTA make the same trips: their lanes meet in the reductions
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < p.T; t0 += step, par ^= 1) {
+    const int64_t t = t0 + group;
+    Piece x[NP], g[NP];  // x * rstd, and dy * w
+    uint4 s[NP];
+    const float r = rstd;
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = k * G + sub;
+      x[k] = unpack(xr[k]), g[k] = unpack(yr[k]), s[k] = sr[k];
       if (c < p8) {
-        const Piece x = unpack(xr[k]), y = unpack(yr[k]), w = load_weight(p.w + c * 8);
+        const Piece w = load_weight(p.w + c * 8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float xh = x.v[i] * rstd;
-          dot = fmaf(y.v[i] * w.v[i], xh, dot);
-          dw[k].v[i] = fmaf(y.v[i], xh, dw[k].v[i]);
+          x[k].v[i] *= r;
+          dw[k].v[i] = fmaf(g[k].v[i], x[k].v[i], dw[k].v[i]);
+          g[k].v[i] *= w.v[i];
+          dot = fmaf(g[k].v[i], x[k].v[i], dot);
         }
       }
     }
-    const float mean = group_sum<G>(dot, red[par]) / static_cast<float>(p.D);
-    if (!live) continue;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int c = k * G + sub;
-      if (c >= p8) continue;
-      const Piece x = unpack(xr[k]), y = unpack(yr[k]), s = unpack(sr[k]), w = load_weight(p.w + c * 8);
-      Piece o;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = fmaf(rstd, y.v[i] * w.v[i] - x.v[i] * rstd * mean, s.v[i]);
-      reinterpret_cast<uint4*>(p.dx + t * p.ld_dx)[c] = pack(o);
-    }
-  }
-  if (!p.part) return;
-  float* row = p.part + static_cast<int64_t>(blockIdx.x) * p.D;
-  for (int g = 0; g < kGroups; ++g) {  // in order, so that the sums are the same in every run
-    if (group == g) {
+    if (kAhead && t0 + step < p.T) load(t + step);
+    const float mean = group_sum<G>(dot, red[par]) * inv_d;
+    if (t < p.T) {
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int c = k * G + sub;
         if (c >= p8) continue;
+        Piece o = unpack(s[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float* at = cols + c * 8 + i;
-          const float v = dw[k].v[i] + (g > 0 ? *at : 0.f);
-          if (g + 1 < kGroups) *at = v;
-          else row[c * 8 + i] = v;
-        }
+        for (int i = 0; i < 8; ++i) o.v[i] = fmaf(r, fmaf(-mean, x[k].v[i], g[k].v[i]), o.v[i]);
+        reinterpret_cast<uint4*>(p.dx + t * p.ld_dx)[c] = pack(o);
       }
     }
-    if (kGroups > 1) __syncthreads();
+    if (!kAhead && t0 + step < p.T) load(t + step);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.part) return;
+  float* row = p.part + static_cast<int64_t>(blockIdx.x) * p.D;
+  float* to = kGroups > 1 ? cols + group * p.D : row;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = k * G + sub;
+    if (c >= p8) continue;
+    reinterpret_cast<float4*>(to + c * 8)[0] = make_float4(dw[k].v[0], dw[k].v[1], dw[k].v[2], dw[k].v[3]);
+    reinterpret_cast<float4*>(to + c * 8)[1] = make_float4(dw[k].v[4], dw[k].v[5], dw[k].v[6], dw[k].v[7]);
+  }
+  if (kGroups > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.D; c += Cta<G>::kThreads) {
+      float v = cols[c];
+      for (int g = 1; g < kGroups; ++g) v += cols[g * p.D + c];  // in order: the same sums in every run
+      row[c] = v;
+    }
   }
 }
 
-// dw = the sum of `n` rows of partial sums: a CTA takes 32 columns, its 8
-// warps every eighth row, added in a fixed order.
-__global__ void __launch_bounds__(256) rms_dw_kernel(const float* __restrict__ part, int n, int D,
-                                                     float* __restrict__ dw) {
-  __shared__ float s[8][33];
+// dw = the sum of `n` rows of partial sums: a CTA takes 32 columns, its 32
+// warps every 32nd row, added in a fixed order.
+__global__ void __launch_bounds__(1024) rms_dw_kernel(const float* __restrict__ part, int n, int D,
+                                                      float* __restrict__ dw) {
+  __shared__ float s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums' kernel has finished
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < D)
-    for (int i = warp; i < n; i += 8) v += part[static_cast<int64_t>(i) * D + c];
-  s[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0 && c < D) {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < D) {
+    for (int i = warp; i < n; i += 128) {
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += s[w][lane];
-    dw[c] = v;
+      for (int k = 0; k < 4; ++k)
+        if (i + 32 * k < n) v[k] += __ldcg(part + static_cast<int64_t>(i + 32 * k) * D + c);
+    }
   }
+  s[warp][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+  __syncthreads();
+  float x = s[lane][warp];  // column `warp` of the 32
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = x;
 }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 // Threads a row and pieces a thread, by the row's length.
 template <class F>
 void by_width(int D, F f) {
-  using dsa_int = int;
-  if (D <= 64) f(std::integral_constant<dsa_int, 8>{}, std::integral_constant<dsa_int, 1>{});
-  else if (D <= 128) f(std::integral_constant<dsa_int, 16>{}, std::integral_constant<dsa_int, 1>{});
-  else if (D <= 256) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 1>{});
-  else if (D <= 512) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 2>{});
-  else if (D <= 1024) f(std::integral_constant<dsa_int, 32>{}, std::integral_constant<dsa_int, 4>{});
-  else if (D <= 2048) f(std::integral_constant<dsa_int, 128>{}, std::integral_constant<dsa_int, 2>{});
-  else if (D <= 4096) f(std::integral_constant<dsa_int, 256>{}, std::integral_constant<dsa_int, 2>{});
-  else if (D <= 8192) f(std::integral_constant<dsa_int, 512>{}, std::integral_constant<dsa_int, 2>{});
-  else f(std::integral_constant<dsa_int, 512>{}, std::integral_constant<dsa_int, 4>{});
+  if (D <= 64) f(Int<8>{}, Int<1>{});
+  else if (D <= 128) f(Int<16>{}, Int<1>{});
+  else if (D <= 256) f(Int<32>{}, Int<1>{});
+  else if (D <= 512) f(Int<32>{}, Int<2>{});
+  else if (D <= 1024) f(Int<32>{}, Int<4>{});
+  else if (D <= 2048) f(Int<128>{}, Int<2>{});
+  else if (D <= 4096) f(Int<256>{}, Int<2>{});
+  else if (D <= 8192) f(Int<512>{}, Int<2>{});
+  else f(Int<512>{}, Int<4>{});
 }
 
 constexpr int kPlanSms = 152;
 
+// The backward pass keeps dw's terms and the next row beside a row: fewer pieces a thread.
+template <class F>
+void by_width_bwd(int D, F f) {
+  if (D <= 64) f(Int<8>{}, Int<1>{});
+  else if (D <= 128) f(Int<16>{}, Int<1>{});
+  else if (D <= 256) f(Int<32>{}, Int<1>{});
+  else if (D <= 512) f(Int<32>{}, Int<2>{});
+  else if (D <= 1024) f(Int<128>{}, Int<1>{});
+  else if (D <= 2048) f(Int<256>{}, Int<1>{});
+  else if (D <= 4096) f(Int<512>{}, Int<1>{});
+  else if (D <= 8192) f(Int<1024>{}, Int<1>{});
+  else f(Int<1024>{}, Int<2>{});
+}
+
 // CTAs of the backward pass: what is resident at once, fewer for few rows.
 int bwd_ctas(int T, int D) {
-  const int groups = D <= 64 ? 32 : D <= 128 ? 16 : D <= 1024 ? 8 : 1;
-  const int per_sm = D <= 2048 ? 8 : D <= 4096 ? 4 : 2;
-  return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(T) + groups - 1) / groups, per_sm * kPlanSms));
+  int n = 0;
+  by_width_bwd(D, [&](auto g, auto np) {
+    constexpr int G = decltype(g)::value, NP = decltype(np)::value, kGroups = Cta<G>::kGroups;
+    n = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(T) + kGroups - 1) / kGroups, bwd_per_sm<G, NP>() * kPlanSms));
+  });
+  return n;
 }
 
 bool width_ok(int D) { return D >= 8 && D <= DSA_NORM_MAX_DIM && D % 8 == 0; }
@@ -396,12 +439,24 @@ extern "C" int dsa_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* x, in
   const BwdParams p{static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(x), weight, rstd,
                     static_cast<const __nv_bfloat16*>(d_sum), static_cast<__nv_bfloat16*>(dx),
                     dweight ? static_cast<float*>(workspace) : nullptr, ld_dy, ld_x, ld_ds, ld_dx, T, D};
-  by_width(D, [&](auto g, auto np) {
+  by_width_bwd(D, [&](auto g, auto np) {
     constexpr int G = decltype(g)::value, NP = decltype(np)::value;
-    rms_bwd_kernel<G, NP><<<ctas, Cta<G>::kThreads, Cta<G>::kGroups > 1 ? D * sizeof(float) : 0, stream>>>(p);
+    rms_bwd_kernel<G, NP><<<ctas, Cta<G>::kThreads, Cta<G>::kGroups > 1 ? Cta<G>::kGroups * D * sizeof(float) : 0,
+                                                    stream>>>(p);
   });
   rc = dsa::launch_error("rms_bwd_kernel");
   if (rc != DSA_OK || !dweight) return rc;
-  rms_dw_kernel<<<(D + 31) / 32, 256, 0, stream>>>(p.part, ctas, D, dweight);
-  return dsa::launch_error("rms_dw_kernel");
+  // launched while the pass drains, so that its start-up hides behind it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((D + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, rms_dw_kernel, static_cast<const float*>(p.part), ctas, D, dweight) != cudaSuccess)
+    return dsa::launch_error("rms_dw_kernel");
+  return DSA_OK;
 }

@@ -6,8 +6,8 @@
 // and by the opposite angle in the adjoint, which is the gradient's pass.
 //
 // Angles: f_i / (2 pi) is taken as a fraction of a turn in 64-bit fixed point, so that
-// p times it modulo a turn is one integer product, and the angle of any
-// position is off by p * 2^-53 of a turn at most and 2^-25 of one when it becomes fp32.
+// p times it modulo a turn is one integer product: the angle of position p is off
+// by p * 2^-61 of f_i and p * 2^-64 of a turn, and by 2^-25 of half a turn when it becomes fp32.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -33,15 +33,30 @@ struct Params {
   dsa::Kv8Geom g;
   int H, H2, R, tokens;
   int per;               // units of a row
-  uint32_t m_token, m_row;  // of all rows of a token, and of one: dsa::fast_div
+  uint32_t m_token, m_row, m_half;  // dsa::fast_div by a token's units, a row's and R / 2
   float mul, sign;
 };
+
+// f / (2 pi) modulo 1, in units of 2^-64.  Of f = m 2^(e - 52): m times 2^11 / (2 pi), its
+// whole part, is shifted by e + 1 (FP64 units are few here, and this is exact to 2^-61 of f).
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+  const int e = static_cast<int>(bits >> 52 & 0x7FF) - 1023;
+  if (e == -1023) return 0;  // below 2^-1022
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (1ull << 52);
+  const uint64_t x = __umul64hi(m << 11, 0x28BE60DB9391054Aull);  // 2^64 / (2 pi)
+  const int s = e + 1;
+  const uint64_t r = s >= 64 || s <= -64 ? 0 : s >= 0 ? x << s : x >> -s;
+  return bits >> 63 ? 0 - r : r;
+}
 
 // A unit: 16 bytes of 4 pairs, or two times 16 bytes, half a row apart, of 8 pairs.
 template <bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
   constexpr int kWords = PAIRS ? 1 : 2;
-  __shared__ float2 turn[kMaxAngles];  // [token][pair]: mul * cos, mul * sin
+  // mul * cos, mul * sin of [token][pair of a unit][unit]: neighbouring units read neighbouring words
+  // (unit by unit they met in the same banks: R = 256 took 36 us where it takes 20)
+  __shared__ float2 turn[kMaxAngles];
   __shared__ int64_t place[kMaxTokens];  // position, or kNone
   constexpr int64_t kNone = INT64_MIN;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
@@ -72,25 +87,22 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
     }
   };
   load(threadIdx.x);  // under way while the angles are worked out
-  for (int k = threadIdx.x; k < n_tok; k += kThreads) {
-    const int64_t t = t0 + k;
-    int64_t pos = kNone;
-    if (t >= __ldg(p.g.cu) && t < __ldg(p.g.cu + p.g.n_seqs)) {
-      const int b = dsa::kv8_seq(p.g.cu, p.g.n_seqs, static_cast<int>(t));
-      pos = (p.g.pos ? __ldg(p.g.pos + b) : 0) + (t - __ldg(p.g.cu + b));
+  {
+    const dsa::SeqFinder seqs(p.g);
+    for (int k = threadIdx.x >> 5; k < n_tok; k += kThreads / 32) {
+      int b, c, pos;
+      const bool inside = seqs.find(p.g, t0 + k, &b, &c, &pos);
+      if ((threadIdx.x & 31) == 0) place[k] = inside ? pos + (t0 + k - c) : kNone;
     }
-    place[k] = pos;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
-    const int k = i / half, j = i - k * half;
-    double f = __ldg(p.f + j) * 0.15915494309189533577;  // 1 / (2 pi)
-    f -= floor(f);
-    const uint64_t step = static_cast<uint64_t>(f * 18446744073709551616.0);
-    const uint64_t angle = static_cast<uint64_t>(place[k]) * step + 0x80000000ull;
+    const int k = dsa::fast_div(i, p.m_half), j = i - k * half;
+    const uint64_t angle = static_cast<uint64_t>(place[k]) * turns_of(__ldg(p.f + j)) + 0x80000000ull;
     float sn, cs;  // the upper half as a signed number is the angle in 2^-31 half turns
     sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
-    turn[i] = make_float2(cs * p.mul, sn * p.mul * p.sign);
+    constexpr int kPairs = PAIRS ? 4 : 8;  // of a unit
+    turn[k * half + j % kPairs * p.per + j / kPairs] = make_float2(cs * p.mul, sn * p.mul * p.sign);
   }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kAhead) {
@@ -103,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
       const Side* s;
       where(i, &k, &u, &s, &h);
       if (place[k] == kNone) continue;
-      const float2* at = turn + k * half + u * (PAIRS ? 4 : 8);
+      const float2* at = turn + k * half + u;
       __nv_bfloat16* dst = s->y + (t0 + k) * s->yt + h * s->yh + u * 8;
       uint32_t* w0 = reinterpret_cast<uint32_t*>(&v[j][0]);
       auto pack2 = [](float lo, float hi) {
@@ -116,14 +128,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float a = lo(w0[e]), b = hi(w0[e]);
-          const float2 c = at[e];
+          const float2 c = at[e * p.per];
           w0[e] = pack2(a * c.x - b * c.y, a * c.y + b * c.x);
         }
       } else {
         uint32_t* w1 = reinterpret_cast<uint32_t*>(&v[j][kWords - 1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 c = at[2 * e], d = at[2 * e + 1];
+          const float2 c = at[2 * e * p.per], d = at[(2 * e + 1) * p.per];
           const float a0 = lo(w0[e]), a1 = hi(w0[e]), b0 = lo(w1[e]), b1 = hi(w1[e]);
           w0[e] = pack2(a0 * c.x - b0 * c.y, a1 * d.x - b1 * d.y);
           w1[e] = pack2(a0 * c.y + b0 * c.x, a1 * d.y + b1 * d.x);
@@ -229,13 +241,14 @@ extern "C" int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H,
   p.H = H, p.H2 = H2, p.R = R;
   p.per = interleaved ? R / 8 : R / 16;
   p.mul = mul, p.sign = inverse ? -1.f : 1.f;
-  // tokens of a CTA: about four rounds of its threads, and two CTAs an SM at least
+  // tokens of a CTA: one round of its threads, and two CTAs an SM at least
   const int per_token = (H + H2) * p.per;
-  int tokens = std::min({kMaxTokens, kMaxAngles / (R / 2), std::max(1, 4 * kAhead * kThreads / per_token)});
+  int tokens = std::min({kMaxTokens, kMaxAngles / (R / 2), std::max(1, kAhead * kThreads / per_token)});
   tokens = std::max(1, std::min(tokens, T / (2 * sms)));
   p.tokens = tokens;
   p.m_token = tokens == 1 ? 1 : dsa::magic_of(per_token);
   p.m_row = dsa::magic_of(p.per);
+  p.m_half = dsa::magic_of(R / 2);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens);
   if (interleaved)
     rotary_kernel<true><<<grid, kThreads, 0, stream>>>(p);
