@@ -657,7 +657,7 @@ int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32_t* cu_seql
  *   s_j = scale * sum_c q[t,h,c] * k(r_j)[c],   V_j = v(r_j), or the first Dv values
  * of the key row when v4 is NULL, of the cache's values k and v.
  *   kv4 uint8 [n_blocks, block, Hc, Dqk / 2], kv_scale uint8 [n_blocks, block, Hc,
- *   Dqk / 32]; v4 and v_scale likewise with Dv, or both NULL; other arguments,
+ *   Dqk / 32]; v4 and v_scale likewise with Dv, or both NULL (scales 16-byte aligned); other arguments,
  *   results, empty rows, rows behind the last sequence and shapes as there (K at most
  *   DSA_KV8_MAX_SLOTS).  Codes and scales of rows that no valid slot names are never used.
  *   workspace: dsa_sparse_attn_fwd_kv4_workspace_size bytes (0 for many shapes:

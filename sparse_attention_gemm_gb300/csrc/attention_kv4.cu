@@ -12,93 +12,201 @@ namespace {
 
 using namespace dsa::kv8_attn;
 
-// Sixteen codes (piece `piece` of 128 dims) to two units of 16 bytes of row `key`
-// of a chunk of 64 dims (lanes of the upper pieces store the second unit first,
-// as in dsa::kv8_attn::widen).
-__device__ __forceinline__ void widen4(uint2 c, uint32_t byte, uint8_t* chunk, int key, int piece) {
-  const bool up = (piece & 4) != 0;
-  const uint32_t f = dsa::bf2_of_scale(byte);
-  uint32_t a[4], b[4];
-  dsa::bf8_of_e2m1(up ? c.y : c.x, f, a);
-  dsa::bf8_of_e2m1(up ? c.x : c.y, f, b);
-  const int unit = (piece & 3) * 2 + (up ? 1 : 0);
-  *reinterpret_cast<uint4*>(chunk + dsa::sw128_offset(key, unit * 16)) = make_uint4(a[0], a[1], a[2], a[3]);
-  *reinterpret_cast<uint4*>(chunk + dsa::sw128_offset(key, (unit ^ 1) * 16)) = make_uint4(b[0], b[1], b[2], b[3]);
+// 32 codes with their scale byte, dims 32 * piece to 32 * piece + 31 of four chunks of 64 dims, to row `key` of the
+// piece's chunk.  Eight lanes (a key) hold two pieces of each chunk: a lane begins with the unit of 16 bytes that its chunk's
+// number says, so that they touch all banks once.  Of each eight dims, element i stands at place 2i and
+// element i + 4 behind it, as they come out of a word: neighbours would cost a third of the instructions more, and
+// integer ones, which an SM issues half as many of, are what a tile's conversion takes its time with.  The query's
+// elements lie in the same order (kPlaced), and results are put back as they are written.
+// direct: no byte of the warp's is above kMxDirect.
+__device__ __forceinline__ void widen8(uint32_t w, uint32_t f, uint32_t f2, bool direct, uint8_t* to) {
+  uint32_t x[4];
+  dsa::e2m1_raw(w, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = dsa::mul_bf16x2(x[i], f);
+  if (!direct) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = dsa::mul_bf16x2(x[i], f2);
+  }
+  *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+// Of a byte up to kMxDirect the second factor is 1.
+__device__ __forceinline__ uint32_t second_factor(uint32_t byte) { return byte > dsa::kMxDirect ? dsa::mx_factor2(byte) : 0x3F803F80u; }
+
+__device__ __forceinline__ void widen32(uint4 c, uint32_t byte, bool direct, uint8_t* chunks, int key, int piece) {
+  const int turn = piece >> 1;
+  const bool t1 = turn & 1, t2 = turn & 2;
+  const uint32_t a[4] = {t1 ? c.y : c.x, t1 ? c.z : c.y, t1 ? c.w : c.z, t1 ? c.x : c.w};
+  const uint32_t w[4] = {t2 ? a[2] : a[0], t2 ? a[3] : a[1], t2 ? a[0] : a[2], t2 ? a[1] : a[3]};
+  const uint32_t f = dsa::mx_factor(byte), f2 = direct ? 0 : second_factor(byte);
+  uint8_t* chunk = chunks + turn * kChunkBytes;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    widen8(w[j], f, f2, direct, chunk + dsa::sw128_offset(key, ((piece & 1) * 4 + ((j + turn) & 3)) * 16));
 }
 
-// The gather of a tile of 64 keys, as that of the 8-bit codes: thread gt takes
-// piece (gt & 7) (16 codes, 8 bytes) of keys (gt >> 3) and (gt >> 3) + 32 of every 128 dims.
-template <int DQK, int DV, bool SEP>
+// The gather of a tile of 64 keys by eight warps: thread gt takes piece (gt & 7) (32 codes, 16
+// bytes, one scale) of keys (gt >> 3) and (gt >> 3) + 32 of every 256 dims; of the last 64 of 576 the
+// threads with piece 0..3 take 16 codes each of the first key, the others of the second.
+// STAGES = 0: a tile's codes come into registers, a tile ahead.  Otherwise they are copied into as many
+// places behind the kernel's shared memory: plain loads in flight hold lines of what that leaves of L1
+// (a line for each key's 8 to 18 bytes of scales), and waited for each other.
+template <int DQK, int DV, bool SEP, int STAGES>
 struct Gather4 {
   static constexpr int kWarps = 8, kThreads = kWarps * 32, kStep = kThreads / 8;
-  static constexpr int kFull = DQK / 128, kNv = SEP ? DV / 128 : 0;
-  static constexpr bool kTail = DQK % 128 != 0;
+  static constexpr int kStages = STAGES;
+  static constexpr bool kScaled = false, kPlaced = true;
+  static constexpr int kM = DQK / 256;
+  static constexpr bool kTail = DQK % 256 != 0;
   static_assert(2 * kStep == kKeys, "a thread gathers two keys of a tile");
-  uint2 k[kFull][2], v[SEP ? kNv : 1][2], tail;
-  uint8_t ke[kFull][2], ve[SEP ? kNv : 1][2], tail_e;
-  float have_any[2];
+  static_assert(SEP ? kM == 1 && DV == 256 : kM == 2 && DV == 512, "pieces");
+  // A stage: each thread's pieces, the keys' last 32 bytes, their scales in 32 bytes each.
+  static constexpr uint32_t kUnits = 2 * (SEP ? 2 : kM);
+  static constexpr uint32_t kTailAt = kUnits * kThreads * 16, kScaleAt = kTailAt + (kTail ? kKeys * 32 : 0);
+  static constexpr uint32_t kStage = kScaleAt + kKeys * 32;
+  uint4 k[kM][2], v[2];
+  uint2 tail;
+  uint32_t ke[kM][2], ve[2], tail_e;
+  bool have[2];
 
+  // ---- through registers
   __device__ __forceinline__ void load_keys(const Params& p, const int (&r)[2], int kvh, int piece) {
     const int rows = p.g.n_blocks << p.g.lb;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const bool have = r[s] >= 0 && dsa::check(r[s] < rows, p.status);
-      const int64_t at = static_cast<int64_t>(have ? r[s] : 0) * p.Hc + kvh;
-      const uint8_t* src = p.k8 + at * (DQK / 2) + piece * 8;
-      const uint8_t* exp = p.k_exp + at * (DQK / 32) + (piece >> 1);
+      have[s] = r[s] >= 0 && dsa::check(r[s] < rows, p.status);
+      const int64_t at = static_cast<int64_t>(have[s] ? r[s] : 0) * p.Hc + kvh;
+      const uint8_t* src = p.k8 + at * (DQK / 2) + piece * 16;
+      const uint8_t* exp = p.k_exp + at * (DQK / 32) + piece;
 #pragma unroll
-      for (int c = 0; c < kFull; ++c) {
-        k[c][s] = have ? __ldcg(reinterpret_cast<const uint2*>(src + c * 64)) : make_uint2(0, 0);
-        ke[c][s] = have ? __ldg(exp + c * 4) : 127;
+      for (int m = 0; m < kM; ++m) {
+        k[m][s] = have[s] ? __ldcg(reinterpret_cast<const uint4*>(src + m * 128)) : make_uint4(0, 0, 0, 0);
+        ke[m][s] = have[s] ? __ldg(exp + m * 8) : 0;
       }
-      have_any[s] = have ? 1.f : 0.f;
     }
-    if (kTail) {  // its four pieces: threads with piece 0..3 take the first key's, the others the second's
-      const int x = piece >= 4 ? r[1] : r[0];
-      const bool have = x >= 0 && dsa::check(x < rows, p.status);
-      const int64_t at = static_cast<int64_t>(have ? x : 0) * p.Hc + kvh;
-      tail = have ? __ldcg(reinterpret_cast<const uint2*>(p.k8 + at * (DQK / 2) + kFull * 64 + (piece & 3) * 8))
-                  : make_uint2(0, 0);
-      tail_e = have ? __ldg(p.k_exp + at * (DQK / 32) + kFull * 4 + ((piece & 3) >> 1)) : 127;
+    if (kTail) {
+      const bool any = piece >= 4 ? have[1] : have[0];
+      const int64_t at = static_cast<int64_t>(any ? (piece >= 4 ? r[1] : r[0]) : 0) * p.Hc + kvh;
+      tail = any ? __ldcg(reinterpret_cast<const uint2*>(p.k8 + at * (DQK / 2) + kM * 128 + (piece & 3) * 8))
+                 : make_uint2(0, 0);
+      tail_e = any ? __ldg(p.k_exp + at * (DQK / 32) + kM * 8 + ((piece & 3) >> 1)) : 0;
     }
   }
   __device__ __forceinline__ void load_values(const Params& p, const int (&r)[2], int kvh, int piece) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const bool have = r[s] >= 0 && dsa::check(r[s] < (p.g.n_blocks << p.g.lb), p.status);
-      const int64_t at = static_cast<int64_t>(have ? r[s] : 0) * p.Hc + kvh;
+      const int64_t at = static_cast<int64_t>(have[s] ? r[s] : 0) * p.Hc + kvh;
+      v[s] = have[s] ? __ldcg(reinterpret_cast<const uint4*>(p.v8 + at * (DV / 2) + piece * 16)) : make_uint4(0, 0, 0, 0);
+      ve[s] = have[s] ? __ldg(p.v_exp + at * (DV / 32) + piece) : 0;
+    }
+  }
+
+  // ---- through stages.  copy: what take needs of a tile into the stage, without a stop on the way; bits: which of
+  // the thread's keys there are (0, 1) and where in their words their scales begin (2, 3: two bytes on).
+  __device__ __forceinline__ static uint32_t copy(const Params& p, const int (&r)[2], int kvh, int gt, uint32_t stage) {
+    const int rows = p.g.n_blocks << p.g.lb, piece = gt & 7, key0 = gt >> 3;
+    uint32_t bits = 0;
 #pragma unroll
-      for (int c = 0; c < kNv; ++c) {
-        v[c][s] = have ? __ldcg(reinterpret_cast<const uint2*>(p.v8 + at * (DV / 2) + c * 64 + piece * 8))
-                       : make_uint2(0, 0);
-        ve[c][s] = have ? __ldg(p.v_exp + at * (DV / 32) + c * 4 + (piece >> 1)) : 127;
+    for (int s = 0; s < 2; ++s) {
+      const bool any = r[s] >= 0 && dsa::check(r[s] < rows, p.status);
+      const int64_t at = static_cast<int64_t>(any ? r[s] : 0) * p.Hc + kvh;
+      const uint32_t n = any ? 16u : 0u;
+      bits |= any ? 1u << s : 0u;
+      const uint8_t* src = p.k8 + at * (DQK / 2) + piece * 16;
+#pragma unroll
+      for (int m = 0; m < kM; ++m) cp_async16(stage + ((2 * m + s) * kThreads + gt) * 16, src + m * 128, n);
+      if (SEP) cp_async16(stage + ((2 + s) * kThreads + gt) * 16, p.v8 + at * (DV / 2) + piece * 16, n);
+      const uint32_t to = stage + kScaleAt + (key0 + s * kStep) * 32;
+      if (DQK == 576) {
+        // 18 bytes from an even place on: the words that hold them, of the last one only what belongs to the row
+        const int64_t first = at * 18;
+        if (first & 2) bits |= 4u << s;
+        const int need = (first & 2 ? 20 : 18) - piece * 4;
+        if (piece < 5) cp_async4(to + piece * 4, p.k_exp + (first & ~int64_t{3}) + piece * 4, any ? min(need, 4) : 0);
+        if (piece >= 6)
+          cp_async16(stage + kTailAt + (key0 + s * kStep) * 32 + (piece - 6) * 16,
+                     p.k8 + at * (DQK / 2) + kM * 128 + (piece - 6) * 16, n);
+      } else if (DQK == 512) {
+        if (piece == 0) cp_async16(to, p.k_exp + at * 16, n);
+      } else {
+        if (piece == 0) cp_async8(to, p.k_exp + at * 8, n / 2);
+        if (piece == 1) cp_async8(to + 8, p.v_exp + at * 8, n / 2);
+      }
+    }
+    return bits;
+  }
+  __device__ __forceinline__ void take(const uint8_t* stage, uint32_t bits, int gt) {
+    const int piece = gt & 7, key0 = gt >> 3;
+    const uint4* units = reinterpret_cast<const uint4*>(stage) + gt;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      have[s] = bits >> s & 1;
+      const uint8_t* exp = stage + kScaleAt + (key0 + s * kStep) * 32 + (DQK == 576 && (bits >> s & 4) ? 2 : 0);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        k[m][s] = units[(2 * m + s) * kThreads];
+        ke[m][s] = exp[piece + m * 8];
+      }
+      if (SEP) v[s] = units[(2 + s) * kThreads], ve[s] = exp[piece + 8];
+      if (kTail && s == piece >> 2) {
+        tail = *reinterpret_cast<const uint2*>(stage + kTailAt + (key0 + s * kStep) * 32 + (piece & 3) * 8);
+        tail_e = exp[kM * 8 + ((piece & 3) >> 1)];
       }
     }
   }
-  // meta: 1 for each slot's key and, behind them, value; 0: no slot.
-  __device__ __forceinline__ void store_keys(uint8_t* buf, float* meta, int key0, int piece) const {
+
+  // Whether no byte of the warp's tile is above kMxDirect (values up to 12: the usual case).
+  __device__ __forceinline__ bool direct() const {
+    uint32_t m = kTail ? tail_e : 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int c = 0; c < kFull; ++c)
-        widen4(k[c][s], ke[c][s], buf + (2 * c + (piece >> 2)) * kChunkBytes, key0 + s * kStep, piece);
-    if (kTail) widen4(tail, tail_e, buf + 2 * kFull * kChunkBytes, key0 + (piece >> 2) * kStep, piece);
-    if (piece < (SEP ? 4 : 2)) meta[(piece >> 1) * kKeys + (piece & 1) * kStep + key0] = have_any[piece & 1];
+      for (int i = 0; i < kM; ++i) m = max(m, ke[i][s]);
+      if (SEP) m = max(m, ve[s]);
+    }
+    return !__any_sync(0xffffffffu, m > dsa::kMxDirect);
   }
-  __device__ __forceinline__ void store_values(uint8_t* buf, int key0, int piece) const {
+  // meta: 1 for each slot, 0: no slot.
+  __device__ __forceinline__ void store_keys(uint8_t* tile, float* meta, int key0, int piece) const {
+    const bool d = direct();
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int c = 0; c < kNv; ++c)
-        widen4(v[c][s], ve[c][s], buf + (2 * c + (piece >> 2)) * kChunkBytes, key0 + s * kStep, piece);
+      for (int m = 0; m < kM; ++m) widen32(k[m][s], ke[m][s], d, tile + m * 4 * kChunkBytes, key0 + s * kStep, piece);
+    if (kTail) {  // eight lanes hold four units of two keys' rows: upper ones store their second unit first
+      const bool up = (piece & 2) != 0;
+      const uint32_t f = dsa::mx_factor(tail_e), f2 = d ? 0 : second_factor(tail_e);
+      const int key = key0 + (piece >> 2) * kStep, unit = (piece & 3) * 2 + (up ? 1 : 0);
+      uint8_t* chunk = tile + 4 * kM * kChunkBytes;
+      widen8(up ? tail.y : tail.x, f, f2, d, chunk + dsa::sw128_offset(key, unit * 16));
+      widen8(up ? tail.x : tail.y, f, f2, d, chunk + dsa::sw128_offset(key, (unit ^ 1) * 16));
+    }
+    if (piece < 2) meta[piece * kStep + key0] = have[piece] ? 1.f : 0.f;
+  }
+  __device__ __forceinline__ void store_values(uint8_t* values, int key0, int piece) const {
+    const bool d = direct();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) widen32(v[s], ve[s], d, values, key0 + s * kStep, piece);
   }
 };
+
+// Heads of a group: 32 where a KV head has no more, which leaves out half of the products and the softmax.
+int heads_of_group(int H, int Hc) { return H / Hc <= 32 ? 32 : 64; }
+
+template <int HG>
+int launch_all(const Params& p, int T, int Dqk, bool separate, cudaStream_t stream) {
+  // as many stages as shared memory has room for
+  constexpr int n256 = HG == 32 ? 3 : 2, n512 = HG == 32 ? 2 : 0;
+  if (separate) return launch<Gather4<256, 256, true, n256>, HG, 256, 256, true>(p, T, stream);
+  return Dqk == 576 ? launch<Gather4<576, 512, false, n512>, HG, 576, 512, false>(p, T, stream)
+                    : launch<Gather4<512, 512, false, n512>, HG, 512, 512, false>(p, T, stream);
+}
 
 }  // namespace
 
 extern "C" size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
   if (!known_shape(T, H, Hc, Dqk, Dv, K)) return 0;
-  const int s = plan_splits(units_of(T, H, Hc), K);
+  const int s = plan_splits(units_of(T, H, Hc, heads_of_group(H, Hc)), K);
   return s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
 }
 
@@ -111,17 +219,19 @@ extern "C" int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uin
                                        cudaStream_t stream) {
   dsa::clear_error();
   const size_t need = dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K);
+  const int hg = H >= 1 && Hc >= 1 ? heads_of_group(H, Hc) : 64;
   Params p;
+  // (the scales of a row are copied in words)
+  if (!dsa::aligned(kv_scale, 16) || !dsa::aligned(v_scale, 16))
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd_kv4: kv_scale and v_scale must be 16-byte aligned");
   const int rc = fill(Call{"dsa_sparse_attn_fwd_kv4", "kv4", "v4", q, kv4, kv_scale, v4, v_scale, idx, topk_length,
                            sink, cu_seqlens, block_table, n_seqs, T, H, Hc, Dqk, Dv, K, block, n_blocks, max_blocks,
-                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need},
+                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, hg},
                       &p);
   if (rc != DSA_OK || T == 0) return rc;
   p.k8 = static_cast<const uint8_t*>(kv4);
   p.k_exp = kv_scale;
   p.v8 = static_cast<const uint8_t*>(v4);
   p.v_exp = v_scale;
-  if (v4) return launch<Gather4<256, 256, true>, 256, 256, true>(p, T, stream);
-  return Dqk == 576 ? launch<Gather4<576, 512, false>, 576, 512, false>(p, T, stream)
-                    : launch<Gather4<512, 512, false>, 512, 512, false>(p, T, stream);
+  return hg == 32 ? launch_all<32>(p, T, Dqk, v4 != nullptr, stream) : launch_all<64>(p, T, Dqk, v4 != nullptr, stream);
 }

@@ -86,6 +86,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // This thread's arrival at a barrier once its copies so far have landed.  (A tensor
 // core that reads them is behind a proxy fence of the thread that waited.)
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -170,6 +178,10 @@ __device__ __forceinline__ float2 scale_parts(float x) {
 template <int DQK, int DV, bool SEP>
 struct Gather {
   static constexpr int kWarps = 8, kThreads = kWarps * 32, kStep = kThreads / 8;
+  static constexpr int kStages = 0;        // places for codes under way, beside those in registers
+  static constexpr uint32_t kStage = 0;    // bytes of one
+  static constexpr bool kScaled = true;    // codes whose scales come beside the tile
+  static constexpr bool kPlaced = false;   // eight dims lie as 0, 4, 1, 5, 2, 6, 3, 7 in shared memory
   static constexpr int kFull = DQK / 128, kNv = SEP ? DV / 128 : 0;
   static constexpr bool kTail = DQK % 128 != 0;
   static_assert(2 * kStep == kKeys, "a thread gathers two keys of a tile");

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       uint32_t o[4];
-      dsa::bf8_of_e2m1(w[j], dsa::bf2_of_scale(e[j]), o);
+      dsa::bf8_of_e2m1(w[j], e[j], o);
       if (live >> j & 1) o0[i0 + j * kThreads] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }

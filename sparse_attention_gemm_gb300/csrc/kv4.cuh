@@ -42,25 +42,33 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The factor of a scale byte, twice, as bf16: 2^(byte - 127) (0x0040 for byte 0), NaN for kMxNan.
-__device__ __forceinline__ uint32_t bf2_of_scale(uint32_t byte) {
-  const uint32_t h = byte == kMxNan ? 0x7FC0u : max(byte << 7, 0x40u);
-  return h | (h << 16);
-}
-
-// Eight codes -> eight bf16 values times the factor, exactly.  A code's three
-// bits at bits 6..8 of a bf16 are its value times 2^-126: exponents 0 to 3, of which 0 is
-// subnormal in both.  Values 0 and 4, 1 and 5, ... of a word lie 16 bits apart; a byte
-// permute puts neighbours together.
-__device__ __forceinline__ void bf8_of_e2m1(uint32_t w, uint32_t factor, uint32_t (&o)[4]) {
-  constexpr uint32_t k126 = 0x7E807E80u;  // 2^126, twice
-  uint32_t x[4];
+// A code's three bits at bits 6..8 of a bf16 are its value times 2^-126: exponents 0 to 3, of which 0 is
+// subnormal in both.  Eight codes of a word as such: x[i] holds elements i and i + 4, which lie 16 bits apart.
+__device__ __forceinline__ void e2m1_raw(uint32_t w, uint32_t (&x)[4]) {
+  const uint32_t v = w >> 8;
   x[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);
   x[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);
-  x[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);
-  x[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);
+  x[2] = ((v << 6) & 0x01C001C0u) | ((w << 4) & 0x80008000u);
+  x[3] = ((v << 2) & 0x01C001C0u) | (w & 0x80008000u);
+}
+
+// Their factor, twice, as bf16: 2^126 times 2^(byte - 127), for bytes up to kMxDirect; of
+// larger ones it is 2^127 and another follows: 2^(byte - 128), NaN for kMxNan.
+constexpr uint32_t kMxDirect = 128;
+__device__ __forceinline__ uint32_t mx_factor(uint32_t byte) { return (min(byte, kMxDirect) + 126u) * 0x00800080u; }
+__device__ __forceinline__ uint32_t mx_factor2(uint32_t byte) {
+  return byte == kMxNan ? 0x7FC07FC0u : (max(byte, kMxDirect) - 1u) * 0x00800080u;
+}
+
+// Eight codes -> eight bf16 values, exactly, those beyond the range infinite; in order.
+__device__ __forceinline__ void bf8_of_e2m1(uint32_t w, uint32_t byte, uint32_t (&o)[4]) {
+  uint32_t x[4];
+  e2m1_raw(w, x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = mul_bf16x2(mul_bf16x2(x[i], k126), factor);
+  for (int i = 0; i < 4; ++i) {
+    x[i] = mul_bf16x2(x[i], mx_factor(byte));
+    if (byte > kMxDirect) x[i] = mul_bf16x2(x[i], mx_factor2(byte));
+  }
   o[0] = __byte_perm(x[0], x[1], 0x5410);
   o[1] = __byte_perm(x[2], x[3], 0x5410);
   o[2] = __byte_perm(x[0], x[1], 0x7632);

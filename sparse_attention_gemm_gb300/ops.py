@@ -828,21 +828,29 @@ def _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_nam
 
 def _kv4_call(rows, rows_name, T, cache, cache_scale, cu_seqlens, pos, block_table):
     """Checks what the writer and the reader share; their arguments from cu_seqlens to max_blocks."""
-    dev = cache.get_device() if isinstance(cache, _Tensor) else -1
-    if not (dev >= 0 and dev == _current_device() and _ok(cache, _U8, 4, dev) and _ok(cache_scale, _U8, 4, dev) and
-            _ok(cu_seqlens, _I32, 1, dev) and _ok(rows, _BF16, 3, dev) and (pos is None or _ok(pos, _I32, 1, dev)) and
-            (block_table is None or _ok(block_table, _I32, 2, dev))):
+    p_ptr = t_ptr = width = 0
+    try:
+        n_blocks, block, heads, half = cache.shape
+        n, dev = cu_seqlens.shape[0] - 1, cache.get_device()
+        t, h, d = rows.shape
+        ok = (cache.dtype is _U8 and dev == _get_device() and cache.is_contiguous() and cache_scale.dtype is _U8 and
+              cache_scale.shape == (n_blocks, block, heads, half // 16) and cache_scale.is_contiguous() and
+              cache_scale.get_device() == dev and cu_seqlens.dtype is _I32 and cu_seqlens.dim() == 1 and
+              cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev and rows.dtype is _BF16 and h == heads and
+              d == 2 * half and (T is None or t == T) and rows.is_contiguous() and rows.get_device() == dev)
+        if pos is not None:
+            ok = ok and pos.dtype is _I32 and pos.shape == (n,) and pos.is_contiguous() and pos.get_device() == dev
+            p_ptr = pos.data_ptr()
+        if block_table is not None:
+            m, width = block_table.shape
+            ok = (ok and block_table.dtype is _I32 and m == n and block_table.is_contiguous() and
+                  block_table.get_device() == dev)
+            t_ptr = block_table.data_ptr()
+    except (AttributeError, TypeError, ValueError, IndexError, RuntimeError):
+        ok = False
+    if not ok:
         _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T)
-    n_blocks, block, heads, half = cache.shape
-    n_seqs = cu_seqlens.shape[0] - 1
-    n_rows, width = (n_seqs, 0) if block_table is None else block_table.shape
-    if (rows.shape != (rows.shape[0] if T is None else T, heads, 2 * half) or
-            cache_scale.shape != (n_blocks, block, heads, half // 16) or n_rows != n_seqs or
-            (pos is not None and pos.shape[0] != n_seqs)):
-        _kv4_refuse(cache, cache_scale, cu_seqlens, pos, block_table, rows, rows_name, T)
-    return (cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(),
-            None if block_table is None else block_table.data_ptr(), n_seqs, rows.shape[0], heads, 2 * half, block,
-            n_blocks, width), dev
+    return (cu_seqlens.data_ptr(), p_ptr, t_ptr, n, t, heads, d, block, n_blocks, width), dev
 
 
 def kv4_write(src, cache, cache_scale, cu_seqlens, pos=None, block_table=None):
@@ -907,71 +915,87 @@ def sparse_attn_fwd_kv4(q, kv4, kv_scale, idx, scale: float, topk_length=None, s
                         out=None, lse=None, workspace=None):
     """Sparse attention forward over the 4-bit block cache; returns dict(out, lse[, lse_kv][, max_logits]).
     idx, block_table and rows behind the last sequence as in sparse_attn_fwd_kv8."""
-    dev = q.get_device() if isinstance(q, _Tensor) else -1
-    paged = block_table is not None
-    if not (dev >= 0 and dev == _current_device() and _ok(q, _BF16, 3, dev) and _ok(kv4, _U8, 4, dev) and
-            _ok(kv_scale, _U8, 4, dev) and
-            _ok(idx, _I32, 2, dev) and (topk_length is None or _ok(topk_length, _I32, 1, dev)) and
-            (sink is None or _ok(sink, _F32, 1, dev)) and
-            (v4 is None if v_scale is None else _ok(v4, _U8, 4, dev) and _ok(v_scale, _U8, 4, dev)) and
-            (not paged or _ok(block_table, _I32, 2, dev) and _ok(cu_seqlens, _I32, 1, dev)) and
-            (out is None or _ok(out, _BF16, 3, dev)) and (lse is None or _ok(lse, _F32, 2, dev)) and
-            (workspace is None or _ok(workspace, _U8, 1, dev))):
-        _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse,
-                      workspace)
-    T, H, Dqk = q.shape
-    n_blocks, block, heads, half = kv4.shape
-    K = idx.shape[1]
-    Dv = 512 if v4 is None else 2 * v4.shape[3]
-    n_seqs, width = (0, 0) if not paged else block_table.shape
-    if (2 * half != Dqk or kv_scale.shape != (n_blocks, block, heads, half // 16) or idx.shape[0] != T or
-            (topk_length is not None and topk_length.shape[0] != T) or (sink is not None and sink.shape[0] != H) or
-            (v4 is not None and (v4.shape != (n_blocks, block, heads, Dv // 2) or
-                                 v_scale.shape != (n_blocks, block, heads, Dv // 32))) or
-            (paged and cu_seqlens.shape[0] != n_seqs + 1) or (out is not None and out.shape != (T, H, Dv)) or
-            (lse is not None and lse.shape != (T, H))):
+    l_ptr = z_ptr = v_ptr = vs_ptr = c_ptr = t_ptr = n_seqs = width = w_ptr = w_bytes = 0
+    Dv = 512
+    try:
+        T, H, Dqk = q.shape
+        n_blocks, block, heads, half = kv4.shape
+        dev, (rows, K) = q.get_device(), idx.shape
+        ok = (q.dtype is _BF16 and dev == _get_device() and q.is_contiguous() and kv4.dtype is _U8 and
+              2 * half == Dqk and kv4.is_contiguous() and kv4.get_device() == dev and kv_scale.dtype is _U8 and
+              kv_scale.shape == (n_blocks, block, heads, half // 16) and kv_scale.is_contiguous() and
+              kv_scale.get_device() == dev and idx.dtype is _I32 and rows == T and idx.is_contiguous() and
+              idx.get_device() == dev)
+        if topk_length is not None:
+            ok = (ok and topk_length.dtype is _I32 and topk_length.shape == (T,) and topk_length.is_contiguous() and
+                  topk_length.get_device() == dev)
+            l_ptr = topk_length.data_ptr()
+        if sink is not None:
+            ok = (ok and sink.dtype is _F32 and sink.shape == (H,) and sink.is_contiguous() and
+                  sink.get_device() == dev)
+            z_ptr = sink.data_ptr()
+        if v4 is not None:
+            half = v4.shape[3]
+            Dv = 2 * half
+            ok = (ok and v4.dtype is _U8 and v4.shape == (n_blocks, block, heads, half) and v4.is_contiguous() and
+                  v4.get_device() == dev and v_scale.dtype is _U8 and
+                  v_scale.shape == (n_blocks, block, heads, half // 16) and v_scale.is_contiguous() and
+                  v_scale.get_device() == dev)
+            v_ptr, vs_ptr = v4.data_ptr(), v_scale.data_ptr()
+        elif v_scale is not None:
+            ok = False
+        if block_table is not None:
+            n_seqs, width = block_table.shape
+            ok = (ok and block_table.dtype is _I32 and block_table.is_contiguous() and
+                  block_table.get_device() == dev and cu_seqlens.dtype is _I32 and cu_seqlens.shape == (n_seqs + 1,) and
+                  cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev)
+            t_ptr, c_ptr = block_table.data_ptr(), cu_seqlens.data_ptr()
+        if out is not None:
+            ok = (ok and out.dtype is _BF16 and out.shape == (T, H, Dv) and out.is_contiguous() and
+                  out.get_device() == dev)
+        if lse is not None:
+            ok = ok and lse.dtype is _F32 and lse.shape == (T, H) and lse.is_contiguous() and lse.get_device() == dev
+        ok = ok and (workspace is None or _ok(workspace, _U8, 1, dev))
+    except (AttributeError, TypeError, ValueError, IndexError, RuntimeError):
+        ok = False
+    if not ok:
         _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse,
                       workspace)
     device, empty = q.device, torch.empty
+    res = {}
     if out is None:
         out = empty((T, H, Dv), dtype=_BF16, device=device)
     if lse is None:
         lse = empty((T, H), dtype=_F32, device=device)
-    lse_kv = empty((T, H), dtype=_F32, device=device) if want_lse_kv else None
-    ml = empty((T, H), dtype=_F32, device=device) if want_max_logits else None
+    res["out"], res["lse"] = out, lse
+    k_ptr = m_ptr = 0
+    if want_lse_kv:
+        res["lse_kv"] = lse_kv = empty((T, H), dtype=_F32, device=device)
+        k_ptr = lse_kv.data_ptr()
+    if want_max_logits:
+        res["max_logits"] = ml = empty((T, H), dtype=_F32, device=device)
+        m_ptr = ml.data_ptr()
     L = _lib or lib()
     if workspace is None:
         need = L.dsa_sparse_attn_fwd_kv4_workspace_size(T, H, heads, Dqk, Dv, K)
         if need:
-            workspace = empty(need, dtype=_U8, device=device)
-    rc = L.dsa_sparse_attn_fwd_kv4(
-        q.data_ptr(), kv4.data_ptr(), kv_scale.data_ptr(), None if v4 is None else v4.data_ptr(),
-        None if v4 is None else v_scale.data_ptr(), idx.data_ptr(),
-        None if topk_length is None else topk_length.data_ptr(), None if sink is None else sink.data_ptr(),
-        cu_seqlens.data_ptr() if paged else None, block_table.data_ptr() if paged else None, n_seqs, T, H, heads, Dqk,
-        Dv, K, block, n_blocks, width, scale, out.data_ptr(), lse.data_ptr(),
-        None if lse_kv is None else lse_kv.data_ptr(), None if ml is None else ml.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
-        _raw_stream(dev))
+            workspace = empty((need,), dtype=_U8, device=device)
+    if workspace is not None:
+        w_ptr, w_bytes = workspace.data_ptr(), workspace.shape[0]
+    rc = L.dsa_sparse_attn_fwd_kv4(q.data_ptr(), kv4.data_ptr(), kv_scale.data_ptr(), v_ptr, vs_ptr, idx.data_ptr(), l_ptr,
+                                   z_ptr, c_ptr, t_ptr, n_seqs, T, H, heads, Dqk, Dv, K, block, n_blocks, width, scale,
+                                   out.data_ptr(), lse.data_ptr(), k_ptr, m_ptr, w_ptr, w_bytes, _raw_stream(dev))
     if rc:
         _check("dsa_sparse_attn_fwd_kv4", rc)
-    res = {"out": out, "lse": lse}
-    if lse_kv is not None:
-        res["lse_kv"] = lse_kv
-    if ml is not None:
-        res["max_logits"] = ml
     return res
 
 
 # Norm and rotary positions: rows may lie apart, so what is asked of a tensor is
-# a last dimension without gaps; the C side checks the other strides.
+# a last dimension without gaps; the C side checks the other strides.  As above, one
+# condition a call, and a look at each argument only when it fails (or when one is no tensor).
 _NORM_FORMS = {"bf16": (0, 0), "e4m3": (1, 128), "mxfp8": (2, 32)}
-
-
-def _strided(t, dtype, shape, device):
-    """Whether t is a tensor of this kind, shape and device whose last dimension has no gaps."""
-    return (isinstance(t, _Tensor) and t.dtype == dtype and t.shape == shape and t.stride(-1) == 1 and
-            t.get_device() == device)
+_F64 = torch.float64
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _strided_refuse(device, *args):
@@ -993,9 +1017,25 @@ def _strided_refuse(device, *args):
     raise ValueError("inconsistent arguments")
 
 
-def _ld(t):
-    """Row stride of a [T, D] tensor; that of a single row is nobody's business."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _need_dim(t, name, dim):
+    if not isinstance(t, _Tensor) or t.dim() != dim:
+        raise TypeError(f"{name} must be a torch.Tensor of {dim} dimensions")
+    return t
+
+
+def _norm_refuse(x, weight, residual, fmt, out, sum_out, scale):
+    if fmt not in _NORM_FORMS:
+        raise ValueError(f"fmt must be one of {sorted(_NORM_FORMS)}, got {fmt!r}")
+    T, D = shape = _need_dim(x, "x", 2).shape
+    form, group = _NORM_FORMS[fmt]
+    if scale is not None and not form:
+        raise ValueError("scale goes with the 8-bit forms")
+    _strided_refuse(x.get_device(), (x, "x", _BF16, shape, True), (weight, "weight", _F32, (D,), False),
+                    *[a for a in ((residual, "residual", _BF16, shape, True),
+                                  (out, "out", _U8 if form else _BF16, shape, True),
+                                  (sum_out, "sum_out", _BF16, shape, True),
+                                  (scale, "scale", _F32 if form == 1 else _U8, (T, D // group if form else 0), False))
+                      if a[0] is not None])
 
 
 def rms_norm_fwd(x, weight, eps: float, residual=None, fmt: str = "bf16", out=None, sum_out=None, scale=None,
@@ -1004,48 +1044,61 @@ def rms_norm_fwd(x, weight, eps: float, residual=None, fmt: str = "bf16", out=No
     fmt "bf16": out bf16; "e4m3": out uint8 codes and scale fp32 [T, D / 128]; "mxfp8": codes and
     scale uint8 [T, D / 32] (E8M0).  sum: x + residual in bf16, with a residual.  Rows of x, residual, out and
     sum_out may lie apart; out and sum_out may be x or residual."""
-    if fmt not in _NORM_FORMS:
-        raise ValueError(f"fmt must be one of {sorted(_NORM_FORMS)}, got {fmt!r}")
-    if not isinstance(x, _Tensor) or x.dim() != 2:
-        raise TypeError("x must be a torch.Tensor of 2 dimensions")
-    form, group = _NORM_FORMS[fmt]
-    shape, dev = x.shape, x.get_device()
-    T, D = shape
-    y_type = _U8 if form else _BF16
-    s_type, s_shape = (_F32 if form == 1 else _U8), (T, D // group if form else 0)
-    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
-            _strided(weight, _F32, (D,), dev) and (residual is None or _strided(residual, _BF16, shape, dev)) and
-            (out is None or _strided(out, y_type, shape, dev)) and
-            (sum_out is None or _strided(sum_out, _BF16, shape, dev)) and
-            (scale is None or form and _strided(scale, s_type, s_shape, dev) and scale.is_contiguous())):
-        if scale is not None and not form:
-            raise ValueError("scale goes with the 8-bit forms")
-        _strided_refuse(dev, (x, "x", _BF16, shape, True), (weight, "weight", _F32, (D,), False),
-                        *[a for a in ((residual, "residual", _BF16, shape, True), (out, "out", y_type, shape, True),
-                                      (sum_out, "sum_out", _BF16, shape, True),
-                                      (scale, "scale", s_type, s_shape, False)) if a[0] is not None])
+    try:
+        form, group = _NORM_FORMS[fmt]
+        T, D = shape = x.shape
+        dev, xs = x.get_device(), x.stride()
+        ok = (x.dtype is _BF16 and xs[1] == 1 and dev == _get_device() and weight.dtype is _F32 and
+              weight.shape == (D,) and weight.stride(0) == 1 and weight.get_device() == dev)
+        r_ptr = r_ld = y_ptr = s_ptr = c_ptr = 0
+        if residual is not None:
+            st = residual.stride()
+            ok = (ok and residual.dtype is _BF16 and residual.shape == shape and st[1] == 1 and
+                  residual.get_device() == dev)
+            r_ptr, r_ld = residual.data_ptr(), st[0]
+        y_ld = s_ld = D
+        if out is not None:
+            st = out.stride()
+            ok = (ok and out.dtype is (_U8 if form else _BF16) and out.shape == shape and st[1] == 1 and
+                  out.get_device() == dev)
+            y_ld = st[0]
+        if sum_out is not None:
+            st = sum_out.stride()
+            ok = (ok and sum_out.dtype is _BF16 and sum_out.shape == shape and st[1] == 1 and
+                  sum_out.get_device() == dev)
+            s_ld = st[0]
+        if scale is not None:
+            ok = (ok and form and scale.dtype is (_F32 if form == 1 else _U8) and scale.shape == (T, D // group) and
+                  scale.is_contiguous() and scale.get_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError, RuntimeError):
+        ok = False
+    if not ok:
+        _norm_refuse(x, weight, residual, fmt, out, sum_out, scale)
     empty, device = torch.empty, x.device
+    res = {}
     if out is None:
-        out = empty(shape, dtype=y_type, device=device)
+        out = empty(shape, dtype=_U8 if form else _BF16, device=device)
+    res["out"], y_ptr = out, out.data_ptr()
     if sum_out is None and residual is not None:
         sum_out = empty(shape, dtype=_BF16, device=device)
-    if form and scale is None:
-        scale = empty(s_shape, dtype=s_type, device=device)
-    rstd = empty((T,), dtype=_F32, device=device) if want_rstd else None
-    rc = (_lib or lib()).dsa_rms_norm_fwd(
-        x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(), 0 if residual is None else _ld(residual),
-        weight.data_ptr(), T, D, eps, form, out.data_ptr(), _ld(out), None if scale is None else scale.data_ptr(),
-        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else _ld(sum_out),
-        None if rstd is None else rstd.data_ptr(), _raw_stream(dev))
+    if sum_out is not None:
+        res["sum"], s_ptr = sum_out, sum_out.data_ptr()
+    if form:
+        if scale is None:
+            scale = empty((T, D // group), dtype=_F32 if form == 1 else _U8, device=device)
+        res["scale"], c_ptr = scale, scale.data_ptr()
+    rstd_ptr = 0
+    if want_rstd:
+        res["rstd"] = rstd = empty((T,), dtype=_F32, device=device)
+        rstd_ptr = rstd.data_ptr()
+    if T <= 1:  # a row's stride to the next is nobody's business
+        x_ld = r_ld = y_ld = s_ld = D
+    else:
+        x_ld = xs[0]
+    rc = (_lib or lib()).dsa_rms_norm_fwd(x.data_ptr(), x_ld, r_ptr, r_ld, weight.data_ptr(), T, D, eps, form, y_ptr,
+                                          y_ld, c_ptr, s_ptr, s_ld, rstd_ptr, _raw_stream(dev))
     if rc:
         _check("dsa_rms_norm_fwd", rc)
-    res = {"out": out}
-    if sum_out is not None:
-        res["sum"] = sum_out
-    if form:
-        res["scale"] = scale
-    if want_rstd:
-        res["rstd"] = rstd
     return res
 
 
@@ -1056,33 +1109,49 @@ def rms_norm_bwd_workspace_size(T: int, D: int) -> int:
 def rms_norm_bwd(dy, x, weight, rstd, d_sum=None, want_dweight: bool = True, dx=None, workspace=None):
     """Backward of rms_norm_fwd: dict(dx bf16 [T, D], dweight fp32 [D] or None).  x: the forward's sum (its x
     without a residual); dx is the gradient of x and of the residual alike.  Rows may lie apart."""
-    if not isinstance(x, _Tensor) or x.dim() != 2:
-        raise TypeError("x must be a torch.Tensor of 2 dimensions")
-    shape, dev = x.shape, x.get_device()
-    T, D = shape
-    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
-            _strided(dy, _BF16, shape, dev) and _strided(weight, _F32, (D,), dev) and _ok(rstd, _F32, 1, dev) and
-            rstd.shape[0] == T and (d_sum is None or _strided(d_sum, _BF16, shape, dev)) and
-            (dx is None or _strided(dx, _BF16, shape, dev)) and (workspace is None or _ok(workspace, _U8, 1, dev))):
+    try:
+        T, D = shape = x.shape
+        dev, xs, ys = x.get_device(), x.stride(), dy.stride()
+        ok = (x.dtype is _BF16 and xs[1] == 1 and dev == _get_device() and dy.dtype is _BF16 and dy.shape == shape and
+              ys[1] == 1 and dy.get_device() == dev and weight.dtype is _F32 and weight.shape == (D,) and
+              weight.stride(0) == 1 and weight.get_device() == dev and rstd.dtype is _F32 and rstd.shape == (T,) and
+              rstd.is_contiguous() and rstd.get_device() == dev)
+        x_ld, y_ld, s_ptr, s_ld, o_ld = xs[0], ys[0], 0, 0, D
+        if d_sum is not None:
+            st = d_sum.stride()
+            ok = ok and d_sum.dtype is _BF16 and d_sum.shape == shape and st[1] == 1 and d_sum.get_device() == dev
+            s_ptr, s_ld = d_sum.data_ptr(), st[0]
+        if dx is not None:
+            st = dx.stride()
+            ok = ok and dx.dtype is _BF16 and dx.shape == shape and st[1] == 1 and dx.get_device() == dev
+            o_ld = st[0]
+        ok = ok and (workspace is None or _ok(workspace, _U8, 1, dev))
+    except (AttributeError, TypeError, ValueError, IndexError, RuntimeError):
+        ok = False
+    if not ok:
+        T, D = shape = _need_dim(x, "x", 2).shape
         args = [(dy, "dy", _BF16, shape, True), (x, "x", _BF16, shape, True), (weight, "weight", _F32, (D,), False),
                 (rstd, "rstd", _F32, (T,), False)]
         args += [a for a in ((d_sum, "d_sum", _BF16, shape, True), (dx, "dx", _BF16, shape, True)) if a[0] is not None]
-        if isinstance(workspace, _Tensor):
-            args.append((workspace, "workspace", _U8, (workspace.numel(),), False))
-        _strided_refuse(dev, *args)
+        if workspace is not None:
+            args.append((workspace, "workspace", _U8, (workspace.numel(),) if isinstance(workspace, _Tensor) else (), False))
+        _strided_refuse(x.get_device(), *args)
+    empty, device = torch.empty, x.device
     if dx is None:
-        dx = torch.empty(shape, dtype=_BF16, device=x.device)
+        dx = empty(shape, dtype=_BF16, device=device)
+    if T <= 1:  # a row's stride to the next is nobody's business
+        x_ld = y_ld = s_ld = o_ld = D
     L = _lib or lib()
-    dweight = None
+    dweight, w_ptr, ws_ptr, ws_bytes = None, 0, 0, 0
     if want_dweight:
-        dweight = torch.empty((D,), dtype=_F32, device=x.device)
+        dweight = empty((D,), dtype=_F32, device=device)
+        w_ptr = dweight.data_ptr()
         if workspace is None:
-            workspace = torch.empty((L.dsa_rms_norm_bwd_workspace_size(T, D),), dtype=_U8, device=x.device)
-    rc = L.dsa_rms_norm_bwd(
-        dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), weight.data_ptr(), rstd.data_ptr(),
-        None if d_sum is None else d_sum.data_ptr(), 0 if d_sum is None else _ld(d_sum), T, D, dx.data_ptr(), _ld(dx),
-        None if dweight is None else dweight.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.shape[0], _raw_stream(dev))
+            workspace = empty((L.dsa_rms_norm_bwd_workspace_size(T, D),), dtype=_U8, device=device)
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.shape[0]
+    rc = L.dsa_rms_norm_bwd(dy.data_ptr(), y_ld, x.data_ptr(), x_ld, weight.data_ptr(), rstd.data_ptr(), s_ptr, s_ld, T, D,
+                            dx.data_ptr(), o_ld, w_ptr, ws_ptr, ws_bytes, _raw_stream(dev))
     if rc:
         _check("dsa_rms_norm_bwd", rc)
     return {"dx": dx, "dweight": dweight}
@@ -1103,11 +1172,17 @@ def rotary_inv_freq(R: int, base: float = 10000.0, scaling: str = "plain", facto
     return freq.to(device or "cuda"), float(mul.value)
 
 
-def _rotary_strides(t):
-    """Strides of token and head; those of a single one are nobody's business."""
-    s = t.stride()
-    T, H, R = t.shape
-    return s[0] if T > 1 else H * R, s[1] if H > 1 else R
+def _rotary_refuse(x, inv_freq, cu_seqlens, pos, x2, out, out2):
+    T, _, R = shape = _need_dim(x, "x", 3).shape
+    if x2 is None and out2 is not None:
+        raise ValueError("out2 goes with x2")
+    shape2 = () if x2 is None else (T, _need_dim(x2, "x2", 3).shape[1], R)
+    _need(cu_seqlens, "cu_seqlens", _I32, 1)
+    args = [(x, "x", _BF16, shape, True), (inv_freq, "inv_freq", _F64, (R // 2,), False),
+            (cu_seqlens, "cu_seqlens", _I32, cu_seqlens.shape, False)]
+    args += [a for a in ((pos, "pos", _I32, (cu_seqlens.shape[0] - 1,), False), (x2, "x2", _BF16, shape2, True),
+                         (out, "out", _BF16, shape, True), (out2, "out2", _BF16, shape2, True)) if a[0] is not None]
+    _strided_refuse(x.get_device(), *args)
 
 
 def rotary(x, inv_freq, cu_seqlens, pos=None, x2=None, interleaved: bool = True, mul: float = 1.0,
@@ -1115,38 +1190,53 @@ def rotary(x, inv_freq, cu_seqlens, pos=None, x2=None, interleaved: bool = True,
     """Rotary positions of x bf16 [T, H, R] and, in the same call, x2 [T, H2, R]: (out, out2 or None).  Token t of
     sequence b stands at pos[b] + t - cu_seqlens[b] (pos None: 0).  Part of a head is x[..., a:b], in place with out=x;
     inverse: the adjoint, for gradients.  Rows of tokens outside the sequences are not written."""
-    if not isinstance(x, _Tensor) or x.dim() != 3:
-        raise TypeError("x must be a torch.Tensor of 3 dimensions")
-    if x2 is not None and (not isinstance(x2, _Tensor) or x2.dim() != 3):
-        raise TypeError("x2 must be a torch.Tensor of 3 dimensions")
-    if x2 is None and out2 is not None:
-        raise ValueError("out2 goes with x2")
-    shape, dev = x.shape, x.get_device()
-    T, H, R = shape
-    H2 = 0 if x2 is None else x2.shape[1]
-    shape2 = (T, H2, R)
-    if not (dev >= 0 and dev == _current_device() and _strided(x, _BF16, shape, dev) and
-            _ok(inv_freq, torch.float64, 1, dev) and inv_freq.shape[0] == R // 2 and _ok(cu_seqlens, _I32, 1, dev) and
-            (pos is None or _ok(pos, _I32, 1, dev) and pos.shape[0] == cu_seqlens.shape[0] - 1) and
-            (x2 is None or _strided(x2, _BF16, shape2, dev)) and (out is None or _strided(out, _BF16, shape, dev)) and
-            (out2 is None or _strided(out2, _BF16, shape2, dev))):
-        _need(cu_seqlens, "cu_seqlens", _I32, 1)
-        args = [(x, "x", _BF16, shape, True), (inv_freq, "inv_freq", torch.float64, (R // 2,), False),
-                (cu_seqlens, "cu_seqlens", _I32, cu_seqlens.shape, False)]
-        args += [a for a in ((pos, "pos", _I32, (cu_seqlens.shape[0] - 1,), False), (x2, "x2", _BF16, shape2, True),
-                             (out, "out", _BF16, shape, True), (out2, "out2", _BF16, shape2, True)) if a[0] is not None]
-        _strided_refuse(dev, *args)
+    H2 = a2 = b2 = c2 = d2 = x2_ptr = y2_ptr = p_ptr = 0
+    try:
+        T, H, R = shape = x.shape
+        dev = x.get_device()
+        a1, b1, last = x.stride()
+        n = cu_seqlens.shape[0] - 1
+        ok = (x.dtype is _BF16 and last == 1 and dev == _get_device() and inv_freq.dtype is _F64 and
+              inv_freq.shape == (R // 2,) and inv_freq.is_contiguous() and inv_freq.get_device() == dev and
+              cu_seqlens.dtype is _I32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and
+              cu_seqlens.get_device() == dev)
+        if pos is not None:
+            ok = ok and pos.dtype is _I32 and pos.shape == (n,) and pos.is_contiguous() and pos.get_device() == dev
+            p_ptr = pos.data_ptr()
+        c1, d1 = H * R, R
+        if out is not None:
+            c1, d1, last = out.stride()
+            ok = ok and out.dtype is _BF16 and out.shape == shape and last == 1 and out.get_device() == dev
+        if x2 is not None:
+            t2, H2, r2 = shape2 = x2.shape
+            a2, b2, last = x2.stride()
+            ok = ok and x2.dtype is _BF16 and t2 == T and r2 == R and last == 1 and x2.get_device() == dev
+            x2_ptr = x2.data_ptr()
+            c2, d2 = H2 * R, R
+            if out2 is not None:
+                c2, d2, last = out2.stride()
+                ok = ok and out2.dtype is _BF16 and out2.shape == shape2 and last == 1 and out2.get_device() == dev
+        elif out2 is not None:
+            ok = False
+    except (AttributeError, TypeError, ValueError, IndexError, RuntimeError):
+        ok = False
+    if not ok:
+        _rotary_refuse(x, inv_freq, cu_seqlens, pos, x2, out, out2)
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=x.device)
-    if x2 is not None and out2 is None:
-        out2 = torch.empty(shape2, dtype=_BF16, device=x.device)
-    xs, ys = _rotary_strides(x), _rotary_strides(out)
-    xs2, ys2 = ((0, 0), (0, 0)) if x2 is None else (_rotary_strides(x2), _rotary_strides(out2))
-    rc = (_lib or lib()).dsa_rotary(
-        x.data_ptr(), xs[0], xs[1], H, None if x2 is None else x2.data_ptr(), xs2[0], xs2[1], H2, inv_freq.data_ptr(),
-        cu_seqlens.data_ptr(), None if pos is None else pos.data_ptr(), cu_seqlens.shape[0] - 1, T, R,
-        1 if interleaved else 0, 1 if inverse else 0, mul, out.data_ptr(), ys[0], ys[1],
-        None if x2 is None else out2.data_ptr(), ys2[0], ys2[1], _raw_stream(dev))
+    if x2 is not None:
+        if out2 is None:
+            out2 = torch.empty(shape2, dtype=_BF16, device=x.device)
+        y2_ptr = out2.data_ptr()
+    if T <= 1:  # strides of a single token or head are nobody's business
+        a1, c1, a2, c2 = H * R, H * R, H2 * R, H2 * R
+    if H == 1:
+        b1 = d1 = R
+    if H2 == 1:
+        b2 = d2 = R
+    rc = (_lib or lib()).dsa_rotary(x.data_ptr(), a1, b1, H, x2_ptr, a2, b2, H2, inv_freq.data_ptr(),
+                                    cu_seqlens.data_ptr(), p_ptr, n, T, R, 1 if interleaved else 0, 1 if inverse else 0,
+                                    mul, out.data_ptr(), c1, d1, y2_ptr, c2, d2, _raw_stream(dev))
     if rc:
         _check("dsa_rotary", rc)
     return out, out2
