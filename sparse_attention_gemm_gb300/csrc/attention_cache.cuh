@@ -51,17 +51,15 @@
 namespace dsa {
 namespace kv8_attn {
 
+constexpr int kHG = 64;    // query heads per group
 constexpr int kGatherThreads = 256;
 constexpr int kSoftWarp0 = 8;
-// HG: query heads per group (64, or 32 with half the softmax warps).
-template <int HG>
-struct Roles {
-  static constexpr int kSoftWarps = HG / 8;
-  static constexpr int kSoftThreads = kSoftWarps * 32;
-  static constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
-  static constexpr int kThreads = (kMmaWarp + 2) * 32;
-  static constexpr uint32_t kQChunkBytes = HG * 128;  // the heads x 64 dims
-};
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kMmaWarp = kSoftWarp0 + kSoftWarps;
+constexpr int kMma2Warp = kMmaWarp + 1;
+constexpr int kThreads = (kMma2Warp + 1) * 32;
+constexpr uint32_t kQChunkBytes = kHG * 128;      // 64 heads x 64 dims
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 0;    // S^T buffers at columns 0 and 64
 constexpr int kOCol = 128;  // O^T blocks at 128 + 64 m
@@ -72,15 +70,14 @@ constexpr float kMove = 8.0f;
 // A tile: key rows in chunks of 64 dims, then value rows where they are
 // separate.  MMA2 does not read the key's last chunk at 576 dims, so once
 // a tile's scores are done its space takes the tile's P^T.
-template <int HG, int DQK, int DV, bool SEP>
+template <int DQK, int DV, bool SEP>
 struct Shape {
-  static constexpr int kSoftWarps = Roles<HG>::kSoftWarps;
   static constexpr int kNk = DQK / 64;
   static constexpr int kNv = DV / 128;  // blocks of O^T
   static constexpr bool kTail = DQK % 128 != 0;
   static constexpr uint32_t kVOff = SEP ? kNk * kChunkBytes : 0;  // V inside a tile buffer
   static constexpr uint32_t kBuf = (kNk + (SEP ? 2 * kNv : 0)) * kChunkBytes;
-  static constexpr uint32_t kKv = kNk * Roles<HG>::kQChunkBytes;                              // [2] tiles, behind the query
+  static constexpr uint32_t kKv = kNk * kQChunkBytes;                              // [2] tiles, behind the query
   static constexpr uint32_t kP = kTail ? kKv + DV / 64 * kChunkBytes : kKv + 2 * kBuf;  // [2] P^T
   static constexpr uint32_t kPStep = kTail ? kBuf : kChunkBytes;
   static constexpr uint32_t kRows = kKv + 2 * kBuf + (kTail ? 0 : 2 * kChunkBytes);  // results, 1 KB a softmax warp
@@ -95,23 +92,22 @@ struct Shape {
   static constexpr uint32_t kBars = kSvm + 16;
   static constexpr uint32_t kSlots = kBars + 20 * 8;                   // 16 bytes [2]: answers to requests for items
   static constexpr uint32_t kMisc = kSlots + 32;
-  static constexpr uint32_t kStages = kMisc + 16;                      // the gather's stages
-  static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kP % 1024 == 0 && kSlots % 16 == 0 && kStages % 16 == 0, "alignment");
+  static constexpr uint32_t kTotal = kMisc + 16;
+  static_assert(kTotal <= 227 * 1024, "shared memory");
+  static_assert(kKv % 1024 == 0 && kBuf % 1024 == 0 && kP % 1024 == 0 && kSlots % 16 == 0, "alignment");
 };
 
 // The softmax warps' barrier, plain and with an OR over the group.  The
 // instructions want converged warps (.aligned), and lanes part at waits and
 // at `if (lane == 0)` or `if (!valid)` before them: each warp is brought
 // together first.  The same goes for tcgen05.ld / st: __syncwarp before each.
-template <int HG>
 __device__ __forceinline__ void group_sync() {
   __syncwarp();
-  asm volatile("bar.sync 1, %0;" ::"n"(Roles<HG>::kSoftThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
 }
-template <int HG>
 __device__ __forceinline__ bool group_any(bool x) {
   __syncwarp();
-  return dsa::named_bar_any(1, Roles<HG>::kSoftThreads, x);
+  return dsa::named_bar_any(1, kSoftThreads, x);
 }
 
 // Asks for the block index of a CTA of this grid that has not started and no
@@ -177,7 +173,6 @@ struct Item {
   bool dead;           // a padding row of a batch with a block table
 };
 
-template <int HG>
 __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
   Item w;
   int u = p.n_items - 1 - it;  // longest rows first (they are the last of a packed prompt)
@@ -188,8 +183,8 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
   const int r = u - w.t * per;
   w.kvh = r / p.G;
   const int g = r - w.kvh * p.G;
-  w.h0 = w.kvh * group + g * HG;
-  w.hv = min(HG, group - g * HG);
+  w.h0 = w.kvh * group + g * kHG;
+  w.hv = min(kHG, group - g * kHG);
   w.dead = w.t >= t_end;
   int len = p.K;
   if (p.topk_length) {
@@ -206,12 +201,9 @@ __device__ __forceinline__ Item get_item(const Params& p, int it, int t_end) {
 }
 
 // G: how a tile comes into shared memory.  kMax: max_logits is asked for (eight registers a softmax thread).
-template <class G, int HG, int DQK, int DV, bool SEP, bool kMax>
-__global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(const Params p) {
-  using S = Shape<HG, DQK, DV, SEP>;
-  constexpr int kSoftWarps = Roles<HG>::kSoftWarps, kSoftThreads = Roles<HG>::kSoftThreads;
-  constexpr int kMmaWarp = Roles<HG>::kMmaWarp, kThreads = Roles<HG>::kThreads;
-  constexpr uint32_t kQChunkBytes = Roles<HG>::kQChunkBytes;
+template <class G, int DQK, int DV, bool SEP, bool kMax>
+__global__ void __launch_bounds__(kThreads, 1) attn_cache_kernel(const Params p) {
+  using S = Shape<DQK, DV, SEP>;
   static_assert(G::kThreads == kGatherThreads, "gather warps");
   extern __shared__ __align__(1024) uint8_t smem[];  // the kernel has no other shared memory
   if (dsa::smem_u32(smem) & 1023u) {                 // would break every swizzle
@@ -292,19 +284,18 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
     // The query's rows, without a stop on the way: head 32 a + 8 c + 2 j + e is
     // row 32 a + 8 j + 2 c + e of the operand, which gives each softmax thread
     // eight consecutive heads.
-    constexpr int kPer = kGatherThreads / HG;  // threads a head, units of 16 bytes sub, sub + kPer, ...
-    auto query_unit = [&](int c) {
-      const int h = gt / kPer;
+    auto query_unit = [&](int c) {  // four threads a head, units of 16 bytes sub, sub + 4, ...
+      const int h = gt >> 2;
       return (c >> 3) * kQChunkBytes + dsa::sw128_offset((h & 32) + ((h & 6) << 2) + ((h >> 2) & 6) + (h & 1), (c & 7) * 16);
     };
     auto send_query = [&](const Item& w) {
       const __nv_bfloat16* src = p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK;
       const uint32_t q_addr = dsa::smem_u32(smem);
-      const int h = gt / kPer;
+      const int h = gt >> 2;
       const bool real = h < w.hv;
 #pragma unroll 3
-      for (int k = 0; k < DQK / 8 / kPer; ++k) {
-        const int c = gt % kPer + kPer * k;
+      for (int k = 0; k < DQK / 32; ++k) {
+        const int c = (gt & 3) + 4 * k;
         cp_async16(q_addr + query_unit(c), src + (real ? h * DQK + c * 8 : 0), real ? 16u : 0u);
       }
     };
@@ -313,15 +304,15 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
       cp_async_wait_all();
       if constexpr (G::kPlaced) {
 #pragma unroll 3
-        for (int k = 0; k < DQK / 8 / kPer; ++k) {
-          uint4* u = reinterpret_cast<uint4*>(smem + query_unit(gt % kPer + kPer * k));
+        for (int k = 0; k < DQK / 32; ++k) {
+          uint4* u = reinterpret_cast<uint4*>(smem + query_unit((gt & 3) + 4 * k));
           *u = to_places(*u);
         }
       }
     };
     // L2 prefetch of a later item's query and ids
     auto prefetch_item = [&](int it) {
-      const Item w = get_item<HG>(p, it, t_end);
+      const Item w = get_item(p, it, t_end);
       if (w.i0 >= w.i1) return;
       const uint8_t* q0 = reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(w.t) * p.H + w.h0) * DQK);
       for (int o = gt * 128; o < w.hv * DQK * 2; o += kGatherThreads * 128) l2_prefetch(q0 + o);
@@ -346,7 +337,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
     int it = blockIdx.x;
     for (int n = 0; it >= 0 && ok; ++n) {
       if (warp == 0 && !request(n)) break;
-      const Item w = get_item<HG>(p, it, t_end);
+      const Item w = get_item(p, it, t_end);
       if (w.i0 >= w.i1) {
         it = next_item(n, &ok);
         continue;
@@ -365,60 +356,38 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
       auto row_of = [&](int id, int blk) {
         return id >= 0 && blk >= 0 && blk < p.g.n_blocks ? (blk << p.g.lb) + (id & ((1 << p.g.lb) - 1)) : -1;
       };
-      // The codes of kAhead tiles from the next on are under way (in registers or in stages), the id and
-      // the table entry of the keys of the one behind them, and the id of the one behind that.
-      constexpr int kAhead = G::kStages > 0 ? G::kStages : 1;
+      // codes of tile i, id and table entry of tile i + 1's keys, id of tile i + 2's
       G codes;
-      [[maybe_unused]] uint32_t bits[kAhead];
-      int id[2], nid[2], blk[2], r[kAhead][2], b0[kAhead][2];
-      [[maybe_unused]] auto copy_tile = [&](int stage, const int (&rows)[2]) {
-        uint32_t got = 0;
-        if constexpr (G::kStages > 0) got = G::copy(p, rows, w.kvh, gt, dsa::smem_u32(smem + S::kStages + stage * G::kStage));
-        cp_async_commit();
-        return got;
-      };
+      int id[2], nid[2], blk[2], r[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) r[d][s] = load_id(w.i0 + d, s);
-        id[s] = load_id(w.i0 + kAhead, s);
-        nid[s] = load_id(w.i0 + kAhead + 1, s);
+        r[s] = load_id(w.i0, s);
+        id[s] = load_id(w.i0 + 1, s);
+        nid[s] = load_id(w.i0 + 2, s);
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) b0[d][s] = load_block(r[d][s]);
+      for (int s = 0; s < 2; ++s) blk[s] = load_block(r[s]);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) r[d][s] = row_of(r[d][s], b0[d][s]);
+        r[s] = row_of(r[s], blk[s]);
         blk[s] = load_block(id[s]);
       }
-      if constexpr (G::kStages > 0) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) bits[d] = copy_tile(d, r[d]);
-      } else {
-        codes.load_keys(p, r[0], w.kvh, piece);
-        if (SEP) codes.load_values(p, r[0], w.kvh, piece);
-      }
+      codes.load_keys(p, r, w.kvh, piece);
+      if (SEP) codes.load_values(p, r, w.kvh, piece);
       // MMA1 of the item before has read its query
       if (!dsa::mbar_wait_warp(q_empty, (item_ctr & 1) ^ 1, wt)) break;
       send_query(w);
-      auto one_tile = [&](int i, int stage) {
+      for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
         const int buf = tile_ctr & 1;
-        const bool first = i == w.i0;
-        if constexpr (G::kStages > 0) {
-          // groups come in the order of their tiles; the first one's wait is for the query too
-          if (first) query_landed();
-          else cp_async_wait<kAhead - 1>();
-          __syncwarp();  // scales are copied by one lane for others
-          codes.take(smem + S::kStages + stage * G::kStage, bits[stage], gt);
+        if (!dsa::mbar_wait_warp(&kv_empty[buf], ((tile_ctr >> 1) & 1) ^ 1, wt)) {
+          ok = false;
+          break;
         }
-        if (!dsa::mbar_wait_warp(&kv_empty[buf], ((tile_ctr >> 1) & 1) ^ 1, wt)) return false;
         uint8_t* tile = smem + S::kKv + buf * S::kBuf;
         codes.store_keys(tile, reinterpret_cast<float*>(smem + S::kMeta + buf * S::kMetaStep), key0, piece);
         if (SEP) codes.store_values(tile + S::kVOff, key0, piece);
-        if (first && G::kStages == 0) query_landed();
+        const bool first = i == w.i0;
+        if (first) query_landed();
         dsa::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -426,37 +395,23 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           if (first) dsa::mbar_arrive(q_full);
         }
         __syncwarp();
-        if (i + kAhead < w.i1) {
-          int rn[2];
+        if (i + 1 < w.i1) {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            rn[s] = row_of(id[s], blk[s]);
+            r[s] = row_of(id[s], blk[s]);
             id[s] = nid[s];
             blk[s] = load_block(nid[s]);
-            nid[s] = load_id(i + kAhead + 2, s);
+            nid[s] = load_id(i + 3, s);
           }
-          if constexpr (G::kStages > 0) {
-            bits[stage] = copy_tile(stage, rn);
-          } else {
-            codes.load_keys(p, rn, w.kvh, piece);
-            if (SEP) codes.load_values(p, rn, w.kvh, piece);
-          }
-        } else if (G::kStages > 0) {
-          cp_async_commit();  // (an empty group: the waits count them)
+          codes.load_keys(p, r, w.kvh, piece);
+          if (SEP) codes.load_values(p, r, w.kvh, piece);
         }
         if (first) {
           ++item_ctr;
           it = next_item(n, &ok);
-          if (!ok) return false;
+          if (!ok) break;
           if (it >= 0) prefetch_item(it);
         }
-        ++tile_ctr;
-        return true;
-      };
-      for (int i = w.i0; i < w.i1 && ok; i += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d)
-          if (ok && i + d < w.i1) ok = one_tile(i + d, d);
       }
     }
     cp_async_wait_all();  // nothing of this thread is in flight when it leaves
@@ -469,13 +424,13 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
     const uint32_t base = dsa::smem_u32(smem);
     bool ok = true;
     if (warp == kMmaWarp) {
-      constexpr uint32_t idesc1 = dsa::idesc_bf16(kKeys, HG, 0, 0);
+      constexpr uint32_t idesc1 = dsa::idesc_bf16(kKeys, kHG, 0, 0);
       const uint64_t q_desc = dsa::smem_desc(base, 16, 1024, dsa::kSwizzle128B);
       const uint64_t kv_desc = dsa::smem_desc(base + S::kKv, 16, 1024, dsa::kSwizzle128B);
       int tile_ctr = 0, item_ctr = 0;
       int it = blockIdx.x;
       for (int n = 0; it >= 0 && ok; ++n) {
-        const Item w = get_item<HG>(p, it, t_end);
+        const Item w = get_item(p, it, t_end);
         it = next_item(n, &ok);
         if (!ok) break;
         if (w.i0 >= w.i1) continue;
@@ -487,7 +442,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           __syncwarp();
           dsa::tc_fence_after();
           const uint64_t a0 = kv_desc + b * (S::kBuf >> 4);
-          const uint32_t d = tmem_base + kSCol + b * 64;
+          const uint32_t d = tmem_base + kSCol + b * kHG;
 #pragma unroll
           for (int c = 0; c < S::kNk; ++c) {
             const uint64_t ac = a0 + c * (kChunkBytes >> 4), bc = q_desc + c * (kQChunkBytes >> 4);
@@ -509,13 +464,13 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
       if (leader) dsa::umma_drain(&drain[0], p.status);
       __syncwarp();
     } else {
-      constexpr uint32_t idesc2 = dsa::idesc_bf16(128, HG, 1, 1);  // both MN-major
+      constexpr uint32_t idesc2 = dsa::idesc_bf16(128, kHG, 1, 1);  // both MN-major
       int tile_ctr = 0;
       const uint64_t v_desc = dsa::smem_desc(base + S::kKv + S::kVOff, kChunkBytes, 1024, dsa::kSwizzle128B);
       const uint64_t p_desc = dsa::smem_desc(base + S::kP, kChunkBytes, 1024, dsa::kSwizzle128B);
       int it = blockIdx.x;
       for (int n = 0; it >= 0 && ok; ++n) {
-        const Item w = get_item<HG>(p, it, t_end);
+        const Item w = get_item(p, it, t_end);
         it = next_item(n, &ok);
         if (!ok) break;
         for (int i = w.i0; i < w.i1; ++i, ++tile_ctr) {
@@ -526,7 +481,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           const uint64_t a0 = v_desc + b * (S::kBuf >> 4), b0 = p_desc + b * (S::kPStep >> 4);
 #pragma unroll
           for (int mb = 0; mb < S::kNv; ++mb) {
-            const uint32_t d = tmem_base + kOCol + mb * 64;
+            const uint32_t d = tmem_base + kOCol + mb * kHG;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
               dsa::umma_bf16_if(leader && got, d, a0 + mb * (2 * kChunkBytes >> 4) + kk * (16 * 128 >> 4),
@@ -566,7 +521,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
     // A wait of this thread gave up: the eight warps leave together, at a
     // point that reduces the flag (see the bf16 kernel).
     bool failed = false;
-    Item next = get_item<HG>(p, blockIdx.x, t_end);
+    Item next = get_item(p, blockIdx.x, t_end);
     int it = blockIdx.x;
     for (int n = 0; it >= 0 && ok; ++n) {
       const Item w = next;
@@ -575,11 +530,11 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
         bool heard = true;
         it = next_item(n, &heard);
         failed |= !heard;
-        if (p.steal && group_any<HG>(failed)) {  // the group leaves together
+        if (p.steal && group_any(failed)) {  // the group leaves together
           ok = false;
           break;
         }
-        if (it >= 0) next = get_item<HG>(p, it, t_end);
+        if (it >= 0) next = get_item(p, it, t_end);
       }
       if (w.dead) continue;
       const int64_t orow = static_cast<int64_t>(w.t) * p.H + w.h0;
@@ -623,7 +578,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
         float x[16];
         {
           uint32_t v[16];
-          dsa::tmem_ld16x256b_x4(tmem_base + lane_off + kSCol + b * 64 + hh * 32, v);
+          dsa::tmem_ld16x256b_x4(tmem_base + lane_off + kSCol + b * kHG + hh * 32, v);
           dsa::tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[r] = __uint_as_float(v[r]);
@@ -657,7 +612,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
         const bool first = i == w.i0;
         bool need_rescale = false;
         float ratio = 1.f;  // of the old to the new 2^E
-        if (first || group_any<HG>(ex || failed)) {
+        if (first || group_any(ex || failed)) {
           // move the references: the tile's maximum per head over its 64 keys
           float v[8];
 #pragma unroll
@@ -668,7 +623,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 8));
           sv = fmaxf(sv, __shfl_xor_sync(0xffffffffu, sv, 16));
           if (lane == 0 && hh == 0) svm[quarter] = sv;
-          if (group_any<HG>(failed)) {  // the group leaves together
+          if (group_any(failed)) {  // the group leaves together
             ok = false;
             break;
           }
@@ -731,7 +686,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           const float* a32 = alpha + hh * 32;
 #pragma unroll 1
           for (int mb = 0; mb < S::kNv; ++mb) {
-            const uint32_t ta = tmem_base + lane_off + kOCol + mb * 64 + hh * 32;
+            const uint32_t ta = tmem_base + lane_off + kOCol + mb * kHG + hh * 32;
             uint32_t v[32];
             __syncwarp();
             dsa::tmem_ld32(ta, v);
@@ -753,26 +708,26 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
       bool heard = true;
       it = next_item(n, &heard);
       failed |= !heard;
-      if (it >= 0) next = get_item<HG>(p, it, t_end);
+      if (it >= 0) next = get_item(p, it, t_end);
       const float sink = p.sink && st < w.hv ? __ldg(p.sink + w.h0 + st) : -INFINITY;
       // The sums' norm, while the last tile's MMA2 runs: over the four quarters
       // in wmax, once everybody has read the last references there.
-      group_sync<HG>();
+      group_sync();
       if (quarter == 0 && lane < 4) {
 #pragma unroll
         for (int h = 0; h < 8; ++h) fac[hb + h] = -nm[h];
       }
       wmax[quarter * 64 + hb + own_head(lane)] = fold8(l_part, lane, [](float a, float c) { return a + c; });
-      group_sync<HG>();
-      const float l = st < HG ? wmax[st] + wmax[64 + st] + wmax[128 + st] + wmax[192 + st] : 0.f;
+      group_sync();
+      const float l = st < 64 ? wmax[st] + wmax[64 + st] + wmax[128 + st] + wmax[192 + st] : 0.f;
       float m_max = 0.f;
       if constexpr (kMax) {
-        group_sync<HG>();
+        group_sync();
         wmax[quarter * 64 + hb + own_head(lane)] = fold8(top, lane, [](float a, float c) { return fmaxf(a, c); });
-        group_sync<HG>();
-        if (st < HG) m_max = fmaxf(fmaxf(wmax[st], wmax[64 + st]), fmaxf(wmax[128 + st], wmax[192 + st]));
+        group_sync();
+        if (st < 64) m_max = fmaxf(fmaxf(wmax[st], wmax[64 + st]), fmaxf(wmax[128 + st], wmax[192 + st]));
       }
-      if (st < HG) {
+      if (st < 64) {
         const float mc = fac[st];
         const bool any = l != 0.f;  // true for NaN too
         float f = 0.f;
@@ -802,7 +757,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
       // O^T is complete with the last tile's MMA2
       if (!failed) failed = !dsa::mbar_wait(o_item, item_ctr & 1, wt);
       ++item_ctr;
-      group_sync<HG>();
+      group_sync();
       dsa::tc_fence_after();
       const int hcount = min(32, w.hv - hh * 32);
       const uint32_t tm_o = tmem_base + lane_off + kOCol + hh * 32;
@@ -815,7 +770,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
         for (int mb = 0; mb < S::kNv; ++mb) {
           uint32_t v[32];
           __syncwarp();
-          dsa::tmem_ld32(tm_o + mb * 64, v);
+          dsa::tmem_ld32(tm_o + mb * kHG, v);
           dsa::tmem_wait_ld();
           float* o = p.part_o + ((orow + hh * 32) * p.splits + w.split) * DV + mb * 128 + quarter * 32 + dim;
 #pragma unroll
@@ -844,8 +799,8 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
           for (int c0 = 0; c0 < 32; c0 += 16) {
             uint32_t v[2][8];
             __syncwarp();
-            dsa::tmem_ld16x256b_x2(tm_o + mb * 64 + c0, v[0]);
-            dsa::tmem_ld16x256b_x2(tm_o + mb * 64 + c0 + (16u << 16), v[1]);
+            dsa::tmem_ld16x256b_x2(tm_o + mb * kHG + c0, v[0]);
+            dsa::tmem_ld16x256b_x2(tm_o + mb * kHG + c0 + (16u << 16), v[1]);
             dsa::tmem_wait_ld();
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -873,7 +828,7 @@ __global__ void __launch_bounds__(Roles<HG>::kThreads, 1) attn_cache_kernel(cons
         }
       }
       dsa::tc_fence_before();
-      if (group_any<HG>(failed)) {  // the item's last barrier: the group leaves together
+      if (group_any(failed)) {  // the item's last barrier: the group leaves together
         ok = false;
         break;
       }
@@ -967,23 +922,8 @@ inline size_t part_bytes(int T, int H, int splits) {
   return (static_cast<size_t>(T) * H * splits * sizeof(float4) + 255) / 256 * 256;
 }
 
-template <class G, int HG, int DQK, int DV, bool SEP, bool kMax>
-int launch_form(const Params& p, int T, cudaStream_t stream) {
-  using S = Shape<HG, DQK, DV, SEP>;
-  constexpr int smem = S::kStages + G::kStages * G::kStage;
-  static_assert(smem <= 227 * 1024, "shared memory");
-  auto kernel = attn_cache_kernel<G, HG, DQK, DV, SEP, kMax>;
-  static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
-  int dev = 0;
-  cudaGetDevice(&dev);  // below 64: check_device
-  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return dsa::launch_error("attn_cache_kernel smem attribute");
-    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-  }
-  kernel<<<p.n_items, Roles<HG>::kThreads, smem, stream>>>(p);
-  int rc = dsa::launch_error("attn_cache_kernel");
-  if (rc != DSA_OK || p.splits == 1) return rc;
+template <int DV>
+int launch_join(const Params& p, int T, cudaStream_t stream) {
   // launched while the splits' kernel drains, so that its start-up hides behind it
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(T) * p.H);
@@ -998,10 +938,29 @@ int launch_form(const Params& p, int T, cudaStream_t stream) {
   return DSA_OK;
 }
 
-template <class G, int HG, int DQK, int DV, bool SEP>
+template <class G, int DQK, int DV, bool SEP, bool kMax>
+int launch_form(const Params& p, int T, cudaStream_t stream) {
+  using S = Shape<DQK, DV, SEP>;
+  constexpr int smem = S::kTotal;
+  auto kernel = attn_cache_kernel<G, DQK, DV, SEP, kMax>;
+  static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
+  int dev = 0;
+  cudaGetDevice(&dev);  // below 64: check_device
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return dsa::launch_error("attn_cache_kernel smem attribute");
+    ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
+  kernel<<<p.n_items, kThreads, smem, stream>>>(p);
+  int rc = dsa::launch_error("attn_cache_kernel");
+  if (rc != DSA_OK || p.splits == 1) return rc;
+  return launch_join<DV>(p, T, stream);
+}
+
+template <class G, int DQK, int DV, bool SEP>
 int launch(const Params& p, int T, cudaStream_t stream) {
-  return p.max_logits ? launch_form<G, HG, DQK, DV, SEP, true>(p, T, stream)
-                      : launch_form<G, HG, DQK, DV, SEP, false>(p, T, stream);
+  return p.max_logits ? launch_form<G, DQK, DV, SEP, true>(p, T, stream)
+                      : launch_form<G, DQK, DV, SEP, false>(p, T, stream);
 }
 
 // What a call hands over, under the names of its own entry point.
@@ -1023,7 +982,7 @@ struct Call {
   float *lse, *lse_kv, *max_logits;
   void* workspace;
   size_t ws_bytes, need;
-  int hg;  // heads of a group
+  int hg, splits;  // heads of a group, splits of a row's slots
 };
 
 // Checks a call and fills the kernels' arguments, but for the codes and scales.
@@ -1075,7 +1034,7 @@ inline int fill(const Call& c, Params* out) {
   p.Hc = c.Hc;
   p.K = c.K;
   p.G = (c.H / c.Hc + c.hg - 1) / c.hg;
-  p.splits = c.need > 0 ? plan_splits(units, c.K) : 1;
+  p.splits = c.splits;
   p.n_items = static_cast<int>(units * p.splits);
   p.status = device_status_ptr();
   p.steal = p.n_items > sms;

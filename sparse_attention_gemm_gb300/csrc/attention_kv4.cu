@@ -6,7 +6,7 @@
 // attention_cache.cuh run on it as on a bf16 cache: the roundings are those of the bf16
 // call.  A row of 576 comes as 306 bytes.
 #include "attention_cache.cuh"
-#include "kv4.cuh"
+#include "attention_kv4.cuh"
 
 namespace {
 
@@ -30,15 +30,12 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t f, uint32_t f2, bool
   }
   *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
 }
-// Of a byte up to kMxDirect the second factor is 1.
-__device__ __forceinline__ uint32_t second_factor(uint32_t byte) { return byte > dsa::kMxDirect ? dsa::mx_factor2(byte) : 0x3F803F80u; }
-
 __device__ __forceinline__ void widen32(uint4 c, uint32_t byte, bool direct, uint8_t* chunks, int key, int piece) {
   const int turn = piece >> 1;
   const bool t1 = turn & 1, t2 = turn & 2;
   const uint32_t a[4] = {t1 ? c.y : c.x, t1 ? c.z : c.y, t1 ? c.w : c.z, t1 ? c.x : c.w};
   const uint32_t w[4] = {t2 ? a[2] : a[0], t2 ? a[3] : a[1], t2 ? a[0] : a[2], t2 ? a[1] : a[3]};
-  const uint32_t f = dsa::mx_factor(byte), f2 = direct ? 0 : second_factor(byte);
+  const uint32_t f = dsa::mx_factor(byte), f2 = direct ? 0 : dsa::mx_second(byte);
   uint8_t* chunk = chunks + turn * kChunkBytes;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -48,28 +45,19 @@ __device__ __forceinline__ void widen32(uint4 c, uint32_t byte, bool direct, uin
 // The gather of a tile of 64 keys by eight warps: thread gt takes piece (gt & 7) (32 codes, 16
 // bytes, one scale) of keys (gt >> 3) and (gt >> 3) + 32 of every 256 dims; of the last 64 of 576 the
 // threads with piece 0..3 take 16 codes each of the first key, the others of the second.
-// STAGES = 0: a tile's codes come into registers, a tile ahead.  Otherwise they are copied into as many
-// places behind the kernel's shared memory: plain loads in flight hold lines of what that leaves of L1
-// (a line for each key's 8 to 18 bytes of scales), and waited for each other.
-template <int DQK, int DV, bool SEP, int STAGES>
+template <int DQK, int DV, bool SEP>
 struct Gather4 {
   static constexpr int kWarps = 8, kThreads = kWarps * 32, kStep = kThreads / 8;
-  static constexpr int kStages = STAGES;
   static constexpr bool kScaled = false, kPlaced = true;
   static constexpr int kM = DQK / 256;
   static constexpr bool kTail = DQK % 256 != 0;
   static_assert(2 * kStep == kKeys, "a thread gathers two keys of a tile");
   static_assert(SEP ? kM == 1 && DV == 256 : kM == 2 && DV == 512, "pieces");
-  // A stage: each thread's pieces, the keys' last 32 bytes, their scales in 32 bytes each.
-  static constexpr uint32_t kUnits = 2 * (SEP ? 2 : kM);
-  static constexpr uint32_t kTailAt = kUnits * kThreads * 16, kScaleAt = kTailAt + (kTail ? kKeys * 32 : 0);
-  static constexpr uint32_t kStage = kScaleAt + kKeys * 32;
   uint4 k[kM][2], v[2];
   uint2 tail;
   uint32_t ke[kM][2], ve[2], tail_e;
   bool have[2];
 
-  // ---- through registers
   __device__ __forceinline__ void load_keys(const Params& p, const int (&r)[2], int kvh, int piece) {
     const int rows = p.g.n_blocks << p.g.lb;
 #pragma unroll
@@ -101,60 +89,6 @@ struct Gather4 {
     }
   }
 
-  // ---- through stages.  copy: what take needs of a tile into the stage, without a stop on the way; bits: which of
-  // the thread's keys there are (0, 1) and where in their words their scales begin (2, 3: two bytes on).
-  __device__ __forceinline__ static uint32_t copy(const Params& p, const int (&r)[2], int kvh, int gt, uint32_t stage) {
-    const int rows = p.g.n_blocks << p.g.lb, piece = gt & 7, key0 = gt >> 3;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const bool any = r[s] >= 0 && dsa::check(r[s] < rows, p.status);
-      const int64_t at = static_cast<int64_t>(any ? r[s] : 0) * p.Hc + kvh;
-      const uint32_t n = any ? 16u : 0u;
-      bits |= any ? 1u << s : 0u;
-      const uint8_t* src = p.k8 + at * (DQK / 2) + piece * 16;
-#pragma unroll
-      for (int m = 0; m < kM; ++m) cp_async16(stage + ((2 * m + s) * kThreads + gt) * 16, src + m * 128, n);
-      if (SEP) cp_async16(stage + ((2 + s) * kThreads + gt) * 16, p.v8 + at * (DV / 2) + piece * 16, n);
-      const uint32_t to = stage + kScaleAt + (key0 + s * kStep) * 32;
-      if (DQK == 576) {
-        // 18 bytes from an even place on: the words that hold them, of the last one only what belongs to the row
-        const int64_t first = at * 18;
-        if (first & 2) bits |= 4u << s;
-        const int need = (first & 2 ? 20 : 18) - piece * 4;
-        if (piece < 5) cp_async4(to + piece * 4, p.k_exp + (first & ~int64_t{3}) + piece * 4, any ? min(need, 4) : 0);
-        if (piece >= 6)
-          cp_async16(stage + kTailAt + (key0 + s * kStep) * 32 + (piece - 6) * 16,
-                     p.k8 + at * (DQK / 2) + kM * 128 + (piece - 6) * 16, n);
-      } else if (DQK == 512) {
-        if (piece == 0) cp_async16(to, p.k_exp + at * 16, n);
-      } else {
-        if (piece == 0) cp_async8(to, p.k_exp + at * 8, n / 2);
-        if (piece == 1) cp_async8(to + 8, p.v_exp + at * 8, n / 2);
-      }
-    }
-    return bits;
-  }
-  __device__ __forceinline__ void take(const uint8_t* stage, uint32_t bits, int gt) {
-    const int piece = gt & 7, key0 = gt >> 3;
-    const uint4* units = reinterpret_cast<const uint4*>(stage) + gt;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      have[s] = bits >> s & 1;
-      const uint8_t* exp = stage + kScaleAt + (key0 + s * kStep) * 32 + (DQK == 576 && (bits >> s & 4) ? 2 : 0);
-#pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        k[m][s] = units[(2 * m + s) * kThreads];
-        ke[m][s] = exp[piece + m * 8];
-      }
-      if (SEP) v[s] = units[(2 + s) * kThreads], ve[s] = exp[piece + 8];
-      if (kTail && s == piece >> 2) {
-        tail = *reinterpret_cast<const uint2*>(stage + kTailAt + (key0 + s * kStep) * 32 + (piece & 3) * 8);
-        tail_e = exp[kM * 8 + ((piece & 3) >> 1)];
-      }
-    }
-  }
-
   // Whether no byte of the warp's tile is above kMxDirect (values up to 12: the usual case).
   __device__ __forceinline__ bool direct() const {
     uint32_t m = kTail ? tail_e : 0;
@@ -175,7 +109,7 @@ struct Gather4 {
       for (int m = 0; m < kM; ++m) widen32(k[m][s], ke[m][s], d, tile + m * 4 * kChunkBytes, key0 + s * kStep, piece);
     if (kTail) {  // eight lanes hold four units of two keys' rows: upper ones store their second unit first
       const bool up = (piece & 2) != 0;
-      const uint32_t f = dsa::mx_factor(tail_e), f2 = d ? 0 : second_factor(tail_e);
+      const uint32_t f = dsa::mx_factor(tail_e), f2 = d ? 0 : dsa::mx_second(tail_e);
       const int key = key0 + (piece >> 2) * kStep, unit = (piece & 3) * 2 + (up ? 1 : 0);
       uint8_t* chunk = tile + 4 * kM * kChunkBytes;
       widen8(up ? tail.y : tail.x, f, f2, d, chunk + dsa::sw128_offset(key, unit * 16));
@@ -190,24 +124,25 @@ struct Gather4 {
   }
 };
 
-// Heads of a group: 32 where a KV head has no more, which leaves out half of the products and the softmax.
-int heads_of_group(int H, int Hc) { return H / Hc <= 32 ? 32 : 64; }
-
-template <int HG>
-int launch_all(const Params& p, int T, int Dqk, bool separate, cudaStream_t stream) {
-  // as many stages as shared memory has room for
-  constexpr int n256 = HG == 32 ? 3 : 2, n512 = HG == 32 ? 2 : 0;
-  if (separate) return launch<Gather4<256, 256, true, n256>, HG, 256, 256, true>(p, T, stream);
-  return Dqk == 576 ? launch<Gather4<576, 512, false, n512>, HG, 576, 512, false>(p, T, stream)
-                    : launch<Gather4<512, 512, false, n512>, HG, 512, 512, false>(p, T, stream);
+// How a call of a known shape is worked: heads of a group and splits of a row's slots.
+struct Plan {
+  bool narrow;
+  int heads, splits;
+};
+Plan plan_of(int T, int H, int Hc, int K) {
+  const bool narrow = dsa::kv4_attn::narrow_takes(T, H, Hc, K);
+  const int heads = narrow ? dsa::kv4_attn::narrow_heads(T, H, Hc) : kHG;
+  const int64_t units = units_of(T, H, Hc, heads);
+  return Plan{narrow, heads, narrow ? dsa::kv4_attn::narrow_splits(units, heads, K) : plan_splits(units, K)};
 }
 
 }  // namespace
 
 extern "C" size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
   if (!known_shape(T, H, Hc, Dqk, Dv, K)) return 0;
-  const int s = plan_splits(units_of(T, H, Hc, heads_of_group(H, Hc)), K);
-  return s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
+  const Plan plan = plan_of(T, H, Hc, K);
+  const int s = plan.splits;
+  return s == 1 || plan.narrow ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
 }
 
 extern "C" int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uint8_t* kv_scale, const void* v4,
@@ -219,19 +154,22 @@ extern "C" int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uin
                                        cudaStream_t stream) {
   dsa::clear_error();
   const size_t need = dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K);
-  const int hg = H >= 1 && Hc >= 1 ? heads_of_group(H, Hc) : 64;
-  Params p;
+  const Plan plan = known_shape(T, H, Hc, Dqk, Dv, K) ? plan_of(T, H, Hc, K) : Plan{false, kHG, 1};
   // (the scales of a row are copied in words)
   if (!dsa::aligned(kv_scale, 16) || !dsa::aligned(v_scale, 16))
     return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd_kv4: kv_scale and v_scale must be 16-byte aligned");
+  Params p;
   const int rc = fill(Call{"dsa_sparse_attn_fwd_kv4", "kv4", "v4", q, kv4, kv_scale, v4, v_scale, idx, topk_length,
                            sink, cu_seqlens, block_table, n_seqs, T, H, Hc, Dqk, Dv, K, block, n_blocks, max_blocks,
-                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, hg},
+                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, plan.heads, plan.splits},
                       &p);
   if (rc != DSA_OK || T == 0) return rc;
   p.k8 = static_cast<const uint8_t*>(kv4);
   p.k_exp = kv_scale;
   p.v8 = static_cast<const uint8_t*>(v4);
   p.v_exp = v_scale;
-  return hg == 32 ? launch_all<32>(p, T, Dqk, v4 != nullptr, stream) : launch_all<64>(p, T, Dqk, v4 != nullptr, stream);
+  if (plan.narrow) return dsa::kv4_attn::launch_narrow(p, T, plan.heads, Dqk, v4 != nullptr, stream);
+  if (v4) return launch<Gather4<256, 256, true>, 256, 256, true>(p, T, stream);
+  return Dqk == 576 ? launch<Gather4<576, 512, false>, 576, 512, false>(p, T, stream)
+                    : launch<Gather4<512, 512, false>, 512, 512, false>(p, T, stream);
 }

@@ -5,10 +5,6 @@
 
 using namespace dsa::kv8_attn;
 
-namespace {
-constexpr int kHG = 64;  // query heads per group
-}
-
 extern "C" size_t dsa_sparse_attn_fwd_kv8_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
   if (!known_shape(T, H, Hc, Dqk, Dv, K) || narrow_takes(T, H, Hc, K)) return 0;
   const int s = plan_splits(units_of(T, H, Hc, kHG), K);
@@ -27,7 +23,7 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   Params p;
   const int rc = fill(Call{"dsa_sparse_attn_fwd_kv8", "kv8", "v8", q, kv8, kv_scale, v8, v_scale, idx, topk_length,
                            sink, cu_seqlens, block_table, n_seqs, T, H, Hc, Dqk, Dv, K, block, n_blocks, max_blocks,
-                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, kHG},
+                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, kHG, need > 0 ? plan_splits(units_of(T, H, Hc, kHG), K) : 1},
                       &p);
   if (rc != DSA_OK || T == 0) return rc;
   p.k8 = static_cast<const uint8_t*>(kv8);
@@ -35,7 +31,7 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   p.v8 = static_cast<const uint8_t*>(v8 ? v8 : kv8);
   p.v_scale = v8 ? v_scale : kv_scale;
   if (narrow_takes(T, H, Hc, K)) return launch_narrow(p, T, Dqk, stream);
-  if (v8) return launch<Gather<256, 256, true>, kHG, 256, 256, true>(p, T, stream);
-  return Dqk == 576 ? launch<Gather<576, 512, false>, kHG, 576, 512, false>(p, T, stream)
-                    : launch<Gather<512, 512, false>, kHG, 512, 512, false>(p, T, stream);
+  if (v8) return launch<Gather<256, 256, true>, 256, 256, true>(p, T, stream);
+  return Dqk == 576 ? launch<Gather<576, 512, false>, 576, 512, false>(p, T, stream)
+                    : launch<Gather<512, 512, false>, 512, 512, false>(p, T, stream);
 }

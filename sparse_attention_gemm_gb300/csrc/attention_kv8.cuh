@@ -178,10 +178,8 @@ __device__ __forceinline__ float2 scale_parts(float x) {
 template <int DQK, int DV, bool SEP>
 struct Gather {
   static constexpr int kWarps = 8, kThreads = kWarps * 32, kStep = kThreads / 8;
-  static constexpr int kStages = 0;        // places for codes under way, beside those in registers
-  static constexpr uint32_t kStage = 0;    // bytes of one
-  static constexpr bool kScaled = true;    // codes whose scales come beside the tile
-  static constexpr bool kPlaced = false;   // eight dims lie as 0, 4, 1, 5, 2, 6, 3, 7 in shared memory
+  static constexpr bool kScaled = true;   // codes whose scales come beside the tile
+  static constexpr bool kPlaced = false;  // eight dims lie as 0, 4, 1, 5, 2, 6, 3, 7 in shared memory
   static constexpr int kFull = DQK / 128, kNv = SEP ? DV / 128 : 0;
   static constexpr bool kTail = DQK % 128 != 0;
   static_assert(2 * kStep == kKeys, "a thread gathers two keys of a tile");
