@@ -660,15 +660,18 @@ int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32_t* cu_seql
  *   Dqk / 32]; v4 and v_scale likewise with Dv, or both NULL (scales 16-byte aligned); other arguments,
  *   results, empty rows, rows behind the last sequence and shapes as there (K at most
  *   DSA_KV8_MAX_SLOTS).  Codes and scales of rows that no valid slot names are never used.
- *   workspace: dsa_sparse_attn_fwd_kv4_workspace_size bytes (0 for many shapes:
- *   then it may be NULL), 256-byte aligned, contents ignored on entry; calls
- *   that may overlap need one each.
+ *   workspace: dsa_sparse_attn_fwd_kv4_workspace_size bytes (paged: whether there is a block
+ *   table; 0 for many shapes: then it may be NULL), 256-byte aligned, contents ignored on entry; calls
+ *   that may overlap need one each.  With one KV head and many slots beside the cache's rows it holds the
+ *   cache's values in bf16 (at most 2^30 bytes) and the slots' rows: a call that reads each row
+ *   often widens them once.
  * Values are bf16 ones and the query enters as it is: weights exp(s_j) are rounded to
  * bf16 before they meet the values, sums are fp32, as in dsa_sparse_attn_fwd.
  * Results are bitwise reproducible; a row's last bits may differ between calls of
- * different T, H or K, which choose the splits.
+ * different T, H, K or n_blocks * block, which choose the form and the splits.
  * Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
-size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K);
+size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K, int block, int n_blocks,
+                                              int paged);
 int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uint8_t* kv_scale, const void* v4,
                             const uint8_t* v_scale, const int32_t* idx, const int32_t* topk_length,
                             const float* sink, const int32_t* cu_seqlens, const int32_t* block_table, int n_seqs,

@@ -99,6 +99,7 @@ struct AttnParams {
   int p_alias;   // chunk whose space holds P^T, or -1 (separate buffers)
   int kv_row_bytes, v_row_bytes;
   float scale_log2;
+  const int32_t* t_end;  // or NULL: rows from *t_end on are left alone
 };
 
 struct Layout {
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.misc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_units = p.T * p.G;
+  const int n_units = (p.t_end ? max(0, min(p.T, __ldg(p.t_end))) : p.T) * p.G;
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -742,33 +743,15 @@ done:
 
 }  // namespace
 
-extern "C" int dsa_sparse_attn_fwd_ex(const void* q, const void* kv, const void* v, const int32_t* idx,
-                                      const int32_t* topk_length, const float* sink, int T, int Tkv, int H, int Dqk,
-                                      int Dv, int K, float scale, void* out, float* lse, float* lse_kv,
-                                      float* max_logits, int indexer_topk, float* lse_indexer, cudaStream_t stream) {
-  dsa::clear_error();
-  if (indexer_topk < 0 || indexer_topk % 64 != 0 || indexer_topk > K)
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: indexer_topk must be a multiple of 64 in [0, K]");
-  if (indexer_topk > 0 && T > 0 && !lse_indexer)
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: lse_indexer is NULL while indexer_topk > 0");
-  const bool latent = (Dqk == 576 || Dqk == 512) && Dv == 512 && v == nullptr;
-  const bool separate = Dqk == 256 && Dv == 256 && v != nullptr;
-  if (!latent && !separate)
-    return dsa::set_error(DSA_ERR_VALUE,
-                          "dsa_sparse_attn_fwd: (Dqk, Dv) must be (576|512, 512) with v == NULL or (256, 256) with v");
-  if (T < 0 || Tkv < 1 || H < 1 || H > 128 || K < 0)
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: need T >= 0, Tkv >= 1, 1 <= H <= 128, K >= 0");
-  if (!(scale > 0.f) || !(scale < INFINITY))
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: scale must be finite and > 0");
-  if (T > 0 && (!q || !kv || !out || !lse || (K > 0 && !idx)))
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: NULL pointer");
-  if (!dsa::aligned(q, 16) || !dsa::aligned(kv, 16) || (v && !dsa::aligned(v, 16)) || !dsa::aligned(out, 16))
-    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: q, kv, v and out must be 16-byte aligned");
-  int sms = 0;
-  int rc = dsa::check_device(&sms);
-  if (rc != DSA_OK) return rc;
-  if (T == 0) return DSA_OK;
+namespace dsa {
 
+// The launch of a call whose arguments are checked.
+int sparse_attn_launch(const void* q, const void* kv, const void* v, const int32_t* idx, const int32_t* topk_length,
+                       const float* sink, int T, int Tkv, int H, int Dqk, int Dv, int K, float scale, void* out, float* lse,
+                       float* lse_kv, float* max_logits, int indexer_topk, float* lse_indexer, const int32_t* t_end, int sms,
+                       cudaStream_t stream) {
+  int rc = DSA_OK;
+  const bool latent = v == nullptr;
   AttnParams p{};
   p.idx = idx;
   p.topk_length = topk_length;
@@ -782,6 +765,7 @@ extern "C" int dsa_sparse_attn_fwd_ex(const void* q, const void* kv, const void*
   p.lse_indexer = indexer_topk > 0 ? lse_indexer : nullptr;
   p.snap_tiles = indexer_topk / kKeys;
   p.status = dsa::device_status_ptr();
+  p.t_end = t_end;
   p.T = T;
   p.Tkv = Tkv;
   p.H = H;
@@ -823,6 +807,38 @@ extern "C" int dsa_sparse_attn_fwd_ex(const void* q, const void* kv, const void*
   const int grid = units < sms ? units : sms;
   sparse_attn_kernel<<<grid, kThreads, smem, stream>>>(mq, p);
   return dsa::launch_error("sparse_attn_kernel");
+}
+
+}  // namespace dsa
+
+extern "C" int dsa_sparse_attn_fwd_ex(const void* q, const void* kv, const void* v, const int32_t* idx,
+                                      const int32_t* topk_length, const float* sink, int T, int Tkv, int H, int Dqk,
+                                      int Dv, int K, float scale, void* out, float* lse, float* lse_kv,
+                                      float* max_logits, int indexer_topk, float* lse_indexer, cudaStream_t stream) {
+  dsa::clear_error();
+  if (indexer_topk < 0 || indexer_topk % 64 != 0 || indexer_topk > K)
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: indexer_topk must be a multiple of 64 in [0, K]");
+  if (indexer_topk > 0 && T > 0 && !lse_indexer)
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: lse_indexer is NULL while indexer_topk > 0");
+  const bool latent = (Dqk == 576 || Dqk == 512) && Dv == 512 && v == nullptr;
+  const bool separate = Dqk == 256 && Dv == 256 && v != nullptr;
+  if (!latent && !separate)
+    return dsa::set_error(DSA_ERR_VALUE,
+                          "dsa_sparse_attn_fwd: (Dqk, Dv) must be (576|512, 512) with v == NULL or (256, 256) with v");
+  if (T < 0 || Tkv < 1 || H < 1 || H > 128 || K < 0)
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: need T >= 0, Tkv >= 1, 1 <= H <= 128, K >= 0");
+  if (!(scale > 0.f) || !(scale < INFINITY))
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: scale must be finite and > 0");
+  if (T > 0 && (!q || !kv || !out || !lse || (K > 0 && !idx)))
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: NULL pointer");
+  if (!dsa::aligned(q, 16) || !dsa::aligned(kv, 16) || (v && !dsa::aligned(v, 16)) || !dsa::aligned(out, 16))
+    return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd: q, kv, v and out must be 16-byte aligned");
+  int sms = 0;
+  int rc = dsa::check_device(&sms);
+  if (rc != DSA_OK) return rc;
+  if (T == 0) return DSA_OK;
+  return dsa::sparse_attn_launch(q, kv, v, idx, topk_length, sink, T, Tkv, H, Dqk, Dv, K, scale, out, lse, lse_kv, max_logits,
+                                 indexer_topk, lse_indexer, nullptr, sms, stream);
 }
 
 extern "C" int dsa_sparse_attn_fwd(const void* q, const void* kv, const void* v, const int32_t* idx,

@@ -963,6 +963,12 @@ int launch(const Params& p, int T, cudaStream_t stream) {
                       : launch_form<G, DQK, DV, SEP, false>(p, T, stream);
 }
 
+// The workspace of rows in several splits.
+inline void take_workspace(Params& p, int T, void* workspace) {
+  p.part_s = static_cast<float4*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(T, p.H, p.splits));
+}
+
 // What a call hands over, under the names of its own entry point.
 struct Call {
   const char *fn, *codes, *values;  // names of the entry point and of its code arguments
@@ -986,7 +992,7 @@ struct Call {
 };
 
 // Checks a call and fills the kernels' arguments, but for the codes and scales.
-inline int fill(const Call& c, Params* out) {
+inline int fill(const Call& c, Params* out, int* sm_count = nullptr) {
   const char* fn = c.fn;
   const bool separate = c.Dqk == 256 && c.Dv == 256 && c.v && c.v_scale;
   const bool latent = (c.Dqk == 576 || c.Dqk == 512) && c.Dv == 512 && !c.v && !c.v_scale;
@@ -1017,6 +1023,7 @@ inline int fill(const Call& c, Params* out) {
                      c.workspace ? c.ws_bytes : static_cast<size_t>(0));
   int sms = 0;
   const int rc = check_device(&sms);
+  if (sm_count) *sm_count = sms;
   if (rc != DSA_OK || c.T == 0) return rc;
   int lb = 0;
   while ((1 << lb) < c.block) ++lb;
@@ -1039,10 +1046,6 @@ inline int fill(const Call& c, Params* out) {
   p.status = device_status_ptr();
   p.steal = p.n_items > sms;
   p.scale_log2 = c.scale * kLog2e;
-  if (c.need > 0) {
-    p.part_s = static_cast<float4*>(c.workspace);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + part_bytes(c.T, c.H, p.splits));
-  }
   *out = p;
   return DSA_OK;
 }

@@ -124,25 +124,108 @@ struct Gather4 {
   }
 };
 
-// How a call of a known shape is worked: heads of a group and splits of a row's slots.
-struct Plan {
-  bool narrow;
-  int heads, splits;
+// ---- the cache widened once, and the attention over bf16 rows on that
+constexpr int kWideThreads = 256, kWidePieces = 4;
+
+// Codes of 8 values a piece, with their scale bytes, to bf16 in the order in which they lie.
+__global__ void __launch_bounds__(kWideThreads) kv4_widen_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scale,
+                                                                 int64_t n, uint4* __restrict__ out) {
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kWideThreads * kWidePieces) + threadIdx.x;
+  uint32_t w[kWidePieces], e[kWidePieces];
+#pragma unroll
+  for (int j = 0; j < kWidePieces; ++j) {
+    const int64_t i = i0 + j * kWideThreads;
+    w[j] = i < n ? __ldcs(codes + i) : 0;
+    e[j] = i < n ? __ldg(scale + (i >> 2)) : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kWidePieces; ++j) {
+    uint32_t o[4];
+    dsa::bf8_of_e2m1(w[j], e[j], o);
+    const int64_t i = i0 + j * kWideThreads;
+    if (i < n) out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// Cache rows of positions: one CTA a query row, whose sequence each warp looks up.
+__global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* __restrict__ idx, const dsa::Kv8Geom g, int K,
+                                                                int32_t* __restrict__ rows) {
+  const int t = blockIdx.x;
+  if (t >= __ldg(g.cu + g.n_seqs)) return;
+  const int b = dsa::kv8_seq_warp(g.cu, g.n_seqs, t);
+  const int64_t at = static_cast<int64_t>(t) * K;
+  for (int j = threadIdx.x; j < K; j += kWideThreads) {
+    const int id = __ldcs(idx + at + j);
+    rows[at + j] = id < 0 ? -1 : dsa::kv8_row(g, b, id);
+  }
+}
+
+struct WideSizes {
+  size_t k, v, rows;  // bytes of the widened keys, the values and the ids
 };
-Plan plan_of(int T, int H, int Hc, int K) {
-  const bool narrow = dsa::kv4_attn::narrow_takes(T, H, Hc, K);
-  const int heads = narrow ? dsa::kv4_attn::narrow_heads(T, H, Hc) : kHG;
-  const int64_t units = units_of(T, H, Hc, heads);
-  return Plan{narrow, heads, narrow ? dsa::kv4_attn::narrow_splits(units, heads, K) : plan_splits(units, K)};
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+WideSizes widened_sizes(int T, int Dqk, int Dv, int K, int64_t cache_rows, bool paged) {
+  return WideSizes{up256(static_cast<size_t>(cache_rows) * Dqk * 2), Dqk == 256 ? up256(static_cast<size_t>(cache_rows) * Dv * 2) : 0,
+                   paged ? up256(static_cast<size_t>(T) * K * 4) : 0};
+}
+
+// Whether the cache is widened once for the call.  Measured (576 dims, 64 heads, a slot each): the tiles'
+// own conversion costs 0.05 ns a slot and group of 64 heads over the bf16 kernel, widening 0.27 ns a cache row
+// and the launches 8 us; taken where the first is twice the second, up to 2^30 bytes.
+bool widens(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows) {
+  const double slots = static_cast<double>(T) * K * ((H + kHG - 1) / kHG);
+  return Hc == 1 && slots >= 10.8 * cache_rows + 320e3 && cache_rows * (Dqk == 256 ? Dqk + Dv : Dqk) <= (int64_t{1} << 29);
+}
+
+int launch_widened(const Params& p, const void* q, int T, int Dqk, int Dv, float scale, int sms, void* workspace, cudaStream_t stream) {
+  const int64_t cache_rows = static_cast<int64_t>(p.g.n_blocks) << p.g.lb;
+  const bool separate = Dqk == 256, paged = p.g.table != nullptr;
+  const WideSizes size = widened_sizes(T, Dqk, Dv, p.K, cache_rows, paged);
+  auto* ws = static_cast<uint8_t*>(workspace);
+  auto widen = [&](const uint8_t* codes, const uint8_t* exp, int dim, uint8_t* to) {
+    const int64_t n = cache_rows * (dim / 8);
+    const unsigned grid = static_cast<unsigned>((n + kWideThreads * kWidePieces - 1) / (kWideThreads * kWidePieces));
+    kv4_widen_kernel<<<grid, kWideThreads, 0, stream>>>(reinterpret_cast<const uint32_t*>(codes), exp, n, reinterpret_cast<uint4*>(to));
+    return dsa::launch_error("kv4_widen_kernel");
+  };
+  int rc = widen(p.k8, p.k_exp, Dqk, ws);
+  if (rc == DSA_OK && separate) rc = widen(p.v8, p.v_exp, Dv, ws + size.k);
+  const int32_t* rows = p.idx;
+  if (rc == DSA_OK && paged) {
+    auto* to = reinterpret_cast<int32_t*>(ws + size.k + size.v);
+    kv4_rows_kernel<<<T, kWideThreads, 0, stream>>>(p.idx, p.g, p.K, to);
+    rc = dsa::launch_error("kv4_rows_kernel");
+    rows = to;
+  }
+  if (rc != DSA_OK) return rc;
+  return dsa::sparse_attn_launch(q, ws, separate ? ws + size.k : nullptr, rows, p.topk_length, p.sink, T, static_cast<int>(cache_rows),
+                                 p.H, Dqk, Dv, p.K, scale, p.out, p.lse, p.lse_kv, p.max_logits, 0, nullptr,
+                                 paged ? p.g.cu + p.g.n_seqs : nullptr, sms, stream);
+}
+
+// How a call of a known shape is worked: heads of a group, splits of a row's slots and the workspace's bytes.
+struct Plan {
+  enum { kTiles, kNarrow, kWidened } form;
+  int heads, splits;
+  size_t bytes;
+};
+Plan plan_of(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows, bool paged) {
+  if (dsa::kv4_attn::narrow_takes(T, H, Hc, Dqk, K))
+    return Plan{Plan::kNarrow, 16, dsa::kv4_attn::narrow_splits(units_of(T, H, Hc, 16), K), 0};
+  if (widens(T, H, Hc, Dqk, Dv, K, cache_rows)) {
+    const WideSizes s = widened_sizes(T, Dqk, Dv, K, cache_rows, paged);
+    return Plan{Plan::kWidened, kHG, 1, s.k + s.v + s.rows};
+  }
+  const int s = plan_splits(units_of(T, H, Hc, kHG), K);
+  return Plan{Plan::kTiles, kHG, s, s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float)};
 }
 
 }  // namespace
 
-extern "C" size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K) {
-  if (!known_shape(T, H, Hc, Dqk, Dv, K)) return 0;
-  const Plan plan = plan_of(T, H, Hc, K);
-  const int s = plan.splits;
-  return s == 1 || plan.narrow ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float);
+extern "C" size_t dsa_sparse_attn_fwd_kv4_workspace_size(int T, int H, int Hc, int Dqk, int Dv, int K, int block,
+                                                         int n_blocks, int paged) {
+  if (!known_shape(T, H, Hc, Dqk, Dv, K) || block < 1 || n_blocks < 1) return 0;
+  return plan_of(T, H, Hc, Dqk, Dv, K, static_cast<int64_t>(n_blocks) * block, paged != 0).bytes;
 }
 
 extern "C" int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uint8_t* kv_scale, const void* v4,
@@ -153,22 +236,26 @@ extern "C" int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uin
                                        float* lse_kv, float* max_logits, void* workspace, size_t ws_bytes,
                                        cudaStream_t stream) {
   dsa::clear_error();
-  const size_t need = dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K);
-  const Plan plan = known_shape(T, H, Hc, Dqk, Dv, K) ? plan_of(T, H, Hc, K) : Plan{false, kHG, 1};
+  const Plan plan = known_shape(T, H, Hc, Dqk, Dv, K) && block >= 1 && n_blocks >= 1
+                        ? plan_of(T, H, Hc, Dqk, Dv, K, static_cast<int64_t>(n_blocks) * block, block_table != nullptr)
+                        : Plan{Plan::kTiles, kHG, 1, 0};
   // (the scales of a row are copied in words)
   if (!dsa::aligned(kv_scale, 16) || !dsa::aligned(v_scale, 16))
     return dsa::set_error(DSA_ERR_VALUE, "dsa_sparse_attn_fwd_kv4: kv_scale and v_scale must be 16-byte aligned");
   Params p;
+  int sms = 0;
   const int rc = fill(Call{"dsa_sparse_attn_fwd_kv4", "kv4", "v4", q, kv4, kv_scale, v4, v_scale, idx, topk_length,
                            sink, cu_seqlens, block_table, n_seqs, T, H, Hc, Dqk, Dv, K, block, n_blocks, max_blocks,
-                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, need, plan.heads, plan.splits},
-                      &p);
+                           scale, out, lse, lse_kv, max_logits, workspace, ws_bytes, plan.bytes, plan.heads, plan.splits},
+                      &p, &sms);
   if (rc != DSA_OK || T == 0) return rc;
   p.k8 = static_cast<const uint8_t*>(kv4);
   p.k_exp = kv_scale;
   p.v8 = static_cast<const uint8_t*>(v4);
   p.v_exp = v_scale;
-  if (plan.narrow) return dsa::kv4_attn::launch_narrow(p, T, plan.heads, Dqk, v4 != nullptr, stream);
+  if (plan.form == Plan::kNarrow) return dsa::kv4_attn::launch_narrow(p, T, Dqk, stream);
+  if (plan.form == Plan::kWidened) return launch_widened(p, q, T, Dqk, Dv, scale, sms, workspace, stream);
+  if (plan.bytes > 0) take_workspace(p, T, workspace);
   if (v4) return launch<Gather4<256, 256, true>, 256, 256, true>(p, T, stream);
   return Dqk == 576 ? launch<Gather4<576, 512, false>, 576, 512, false>(p, T, stream)
                     : launch<Gather4<512, 512, false>, 512, 512, false>(p, T, stream);

@@ -5,14 +5,20 @@
 #include "kv4.cuh"
 
 namespace dsa {
+
+// The attention over bf16 rows (attention.cu) of a call whose arguments are checked; rows from *t_end on are left alone.
+int sparse_attn_launch(const void* q, const void* kv, const void* v, const int32_t* idx, const int32_t* topk_length,
+                       const float* sink, int T, int Tkv, int H, int Dqk, int Dv, int K, float scale, void* out, float* lse,
+                       float* lse_kv, float* max_logits, int indexer_topk, float* lse_indexer, const int32_t* t_end, int sms,
+                       cudaStream_t stream);
+
 namespace kv4_attn {
 
-// Attention in groups of 16 or 32 heads (attention_kv4_narrow.cu): whether it takes a
-// call, the heads of a group, the splits of a row's slots, and the launch.
-bool narrow_takes(int T, int H, int Hc, int K);
-int narrow_heads(int T, int H, int Hc);
-int narrow_splits(int64_t units, int heads, int K);
-int launch_narrow(const kv8_attn::Params& p, int T, int heads, int Dqk, bool separate, cudaStream_t stream);
+// Attention in groups of 16 heads (attention_kv4_narrow.cu): whether it takes a call, the splits of
+// a row's slots, and the launch.
+bool narrow_takes(int T, int H, int Hc, int Dqk, int K);
+int narrow_splits(int64_t units, int K);
+int launch_narrow(const kv8_attn::Params& p, int T, int Dqk, cudaStream_t stream);
 
 }  // namespace kv4_attn
 }  // namespace dsa

@@ -14,7 +14,7 @@
 // running maximum of each head) is agreed on through shared memory, and a warp adds up 64 value dims
 // (of 256 dims: of one half of the keys).  Raw codes arrive by cp.async, two tiles ahead.
 //
-// Work item = (token, KV head, group of 16 MT heads, split of its slots); a row's splits are the CTAs of a
+// Work item = (token, KV head, group of 16 heads, split of its slots); a row's splits are the CTAs of a
 // cluster and are joined there.
 #include "attention_kv4.cuh"
 
@@ -26,11 +26,11 @@ constexpr int kTile = 64;  // keys
 constexpr int kWarps = 8, kBlock = kWarps * 32;
 static_assert(kTile == 8 * kWarps, "a warp scores eight keys");
 constexpr int kRowRing = 4;
-constexpr int kMaxCluster = 8;  // splits of a row's slots are the CTAs of a cluster
+constexpr int kMaxCluster = 16;  // splits of a row's slots are the CTAs of a cluster
 
-template <int DQK, int DV, bool SEP, int MT>
+template <int DQK, int DV, bool SEP>
 struct Narrow {
-  static constexpr int kHeads = 16 * MT;
+  static constexpr int kHeads = 16;
   static constexpr uint32_t kQPitch = DQK * 2 + 16;  // an odd number of 16-byte units: ldmatrix without conflicts
   // a key's codes, 32 bytes on from a multiple of 128: scores read 64 bytes of keys two apart at a time, values 32 of four in a
   // row, and neither meet in a bank
@@ -54,7 +54,7 @@ struct Narrow {
   static constexpr uint32_t kShares = kStats + kHeads * 16;  // float [heads][kMaxCluster]
   static constexpr uint32_t kTotal = kShares + kHeads * kMaxCluster * 4;
   static_assert(kHeads * DV * 4 <= kFactors, "mean values");
-  static constexpr int kPerSm = kTotal <= 75 * 1024 && MT == 1 ? 3 : kTotal <= 113 * 1024 ? 2 : 1;
+  static constexpr int kPerSm = kTotal <= 75 * 1024 ? 3 : kTotal <= 113 * 1024 ? 2 : 1;
   static_assert(kTotal <= 227 * 1024 && kStage % 16 == 0 && kStages % 16 == 0 && kP % 16 == 0, "shared memory");
   // value dims: 64 a warp; with 256, two halves of the keys
   static constexpr int kSlices = DV / 64, kHalves = kWarps / kSlices;
@@ -107,9 +107,9 @@ __device__ __forceinline__ void with_direct(bool direct, F f) {
 __device__ __forceinline__ constexpr int key_of(int col) { return (col & 4) + ((col >> 1) & 1) + 2 * (col & 1); }
 __device__ __forceinline__ constexpr int place_of(int key) { return 2 * (key & 3) + (key >> 2); }
 
-template <int DQK, int DV, bool SEP, int MT>
-__global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) attn_kv4_narrow_kernel(const Params p) {
-  using N = Narrow<DQK, DV, SEP, MT>;
+template <int DQK, int DV, bool SEP>
+__global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_kv4_narrow_kernel(const Params p) {
+  using N = Narrow<DQK, DV, SEP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const uint32_t base = dsa::smem_u32(smem);
@@ -231,17 +231,12 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
   }
 
   // ---- state of the softmax: heads 16 m + g and 16 m + g + 8, the same in every warp
-  float m_run[MT][2], l_part[MT][2];
-  float acc[MT][8][4];
+  float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
+  float acc[8][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int j = 0; j < 8; ++j)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m_run[m][e] = -INFINITY, l_part[m][e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
   float* wmax = reinterpret_cast<float*>(smem + N::kWmax);
   const int slice = warp % N::kSlices, half = warp / N::kSlices;  // value dims 64 slice .., keys of this half
   const uint32_t q_addr = base + ((lane & 7) + 8 * ((lane >> 3) & 1)) * N::kQPitch + (lane >> 4) * 16;
@@ -281,11 +276,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
     byte[kSuper] = DQK == 576 ? exp_at[16 + (c >> 1)] : 0;
     const bool direct = !__any_sync(0xffffffffu, max(top_byte, byte[kSuper]) > dsa::kMxDirect);
     // (two sums each, of alternating steps: a product does not wait for the one before)
-    float s_acc[MT][4], s_two[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s_acc[m][e] = s_two[m][e] = 0.f;
+    float s_acc[4] = {0.f, 0.f, 0.f, 0.f}, s_two[4] = {0.f, 0.f, 0.f, 0.f};
     with_direct(direct, [&](auto d) {
       // NW words, two steps each
       auto words = [&](auto nw, const uint32_t* w, uint32_t f, uint32_t f2, int step) {
@@ -293,16 +284,13 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
         uint32_t x[NW][4];
 #pragma unroll
         for (int k = 0; k < NW; ++k) widen_word<decltype(d)::value>(w[k], f, f2, x[k]);
+        uint32_t a[2 * NW][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t a[2 * NW][4];
+        for (int k = 0; k < 2 * NW; ++k) ldmatrix4(a[k], q_addr + (step + k) * 32);
 #pragma unroll
-          for (int k = 0; k < 2 * NW; ++k) ldmatrix4(a[k], q_addr + m * 16 * N::kQPitch + (step + k) * 32);
-#pragma unroll
-          for (int k = 0; k < NW; ++k) {
-            mma16816(s_acc[m], a[2 * k], x[k][0], x[k][1]);
-            mma16816(s_two[m], a[2 * k + 1], x[k][2], x[k][3]);
-          }
+        for (int k = 0; k < NW; ++k) {
+          mma16816(s_acc, a[2 * k], x[k][0], x[k][1]);
+          mma16816(s_two, a[2 * k + 1], x[k][2], x[k][3]);
         }
       };
 #pragma unroll
@@ -320,39 +308,35 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
 
     // ---- softmax: in powers of two, against the running maximum of each head
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < 2; ++e) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float& s = s_acc[m][2 * e + k];
-          s = valid[k] ? (s + s_two[m][2 * e + k]) * p.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s);
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (c == 0) wmax[warp * N::kHeads + m * 16 + e * 8 + g] = mx;
+      for (int k = 0; k < 2; ++k) {
+        float& s = s_acc[2 * e + k];
+        s = valid[k] ? (s + s_two[2 * e + k]) * p.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, s);
       }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if (c == 0) wmax[warp * N::kHeads + e * 8 + g] = mx;
+    }
     const bool all_direct = !__syncthreads_or(!direct);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < 2; ++e) {
+      float mx = m_run[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = m_run[m][e];
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wmax[w * N::kHeads + e * 8 + g]);
+      const float ref = mx == -INFINITY ? 0.f : mx;  // (no valid slot so far)
+      const float alpha = ex2(m_run[e] - ref);
+      m_run[e] = mx;
+      const float p0 = ex2(s_acc[2 * e] - ref), p1 = ex2(s_acc[2 * e + 1] - ref);
+      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(smem + N::kP + (e * 8 + g) * N::kPPitch) + key0;
+      to[place_of(key_of(2 * c))] = __float2bfloat16_rn(p0);
+      to[place_of(key_of(2 * c + 1))] = __float2bfloat16_rn(p1);
+      l_part[e] = fmaf(l_part[e], alpha, p0 + p1);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wmax[w * N::kHeads + m * 16 + e * 8 + g]);
-        const float ref = mx == -INFINITY ? 0.f : mx;  // (no valid slot so far)
-        const float alpha = ex2(m_run[m][e] - ref);
-        m_run[m][e] = mx;
-        const float p0 = ex2(s_acc[m][2 * e] - ref), p1 = ex2(s_acc[m][2 * e + 1] - ref);
-        __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(smem + N::kP + (m * 16 + e * 8 + g) * N::kPPitch) + key0;
-        to[place_of(key_of(2 * c))] = __float2bfloat16_rn(p0);
-        to[place_of(key_of(2 * c + 1))] = __float2bfloat16_rn(p1);
-        l_part[m][e] = fmaf(l_part[m][e], alpha, p0 + p1);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[m][j][2 * e] *= alpha, acc[m][j][2 * e + 1] *= alpha;
-      }
+      for (int j = 0; j < 8; ++j) acc[j][2 * e] *= alpha, acc[j][2 * e + 1] *= alpha;
+    }
     __syncthreads();
 
     // ---- values: 64 dims of this warp's keys; of eight weights, place 2 i is key i's and place 2 i + 1 key i + 4's
@@ -373,9 +357,8 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
       load(0);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        uint32_t a[MT][4], x[4][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) ldmatrix4(a[m], p_addr + m * 16 * N::kPPitch + k * 32);
+        uint32_t a[4], x[4][4];
+        ldmatrix4(a, p_addr + k * 32);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           uint32_t f2 = 0;
@@ -390,11 +373,8 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
         for (int j = 0; j < 4; ++j) {
           const uint32_t lo0 = __byte_perm(x[0][j], x[1][j], 0x5410), lo1 = __byte_perm(x[2][j], x[3][j], 0x5410);
           const uint32_t hi0 = __byte_perm(x[0][j], x[1][j], 0x7632), hi1 = __byte_perm(x[2][j], x[3][j], 0x7632);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma16816(acc[m][j], a[m], lo0, lo1);
-            mma16816(acc[m][j + 4], a[m], hi0, hi1);
-          }
+          mma16816(acc[j], a, lo0, lo1);
+          mma16816(acc[j + 4], a, hi0, hi1);
         }
       }
     });
@@ -405,87 +385,79 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
 
   // ---- the sums' norm, over lanes and warps, and the two halves' values
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = l_part[m][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (c == 0) wmax[warp * N::kHeads + m * 16 + e * 8 + g] = l;
-    }
+  for (int e = 0; e < 2; ++e) {
+    float l = l_part[e];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (c == 0) wmax[warp * N::kHeads + e * 8 + g] = l;
+  }
   __syncthreads();  // (and every thread's copies have ended)
   if constexpr (N::kHalves == 2) {
     float* other = reinterpret_cast<float*>(smem + N::kStages);
     if (half == 1) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) other[((slice * MT + m) * 32 + j * 4 + e) * 32 + lane] = acc[m][j][e];
+        for (int e = 0; e < 4; ++e) other[(slice * 32 + j * 4 + e) * 32 + lane] = acc[j][e];
     }
     __syncthreads();
     if (half == 0) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] += other[((slice * MT + m) * 32 + j * 4 + e) * 32 + lane];
+        for (int e = 0; e < 4; ++e) acc[j][e] += other[(slice * 32 + j * 4 + e) * 32 + lane];
     }
     __syncthreads();
   }
   const bool split_up = p.splits > 1;
   if (half == 0) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < 2; ++e) {
+      const int h = e * 8 + g;
+      float l = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = m * 16 + e * 8 + g;
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += wmax[w * N::kHeads + h];
-        if (h >= hv) continue;
-        const float mc = m_run[m][e] == -INFINITY ? 0.f : m_run[m][e];
-        const bool any = l != 0.f;  // true for NaN too
-        const bool first = slice == 0 && c == 0;
-        float f = 0.f;
-        if (split_up) {
-          if (any) f = 1.f / l;  // a split's mean value, which stays in range where the sum might not
-          if (first) *reinterpret_cast<float4*>(smem + N::kStats + h * 16) = make_float4(mc, l, m_run[m][e], 0.f);
-        } else {
-          const float sink = p.sink ? __ldg(p.sink + h0 + h) : -INFINITY, sk = sink * kLog2e;
-          float lse_v = sink, lkv = INFINITY;
-          if (any) {
-            const float M = fmaxf(mc, sk);
-            const float a = exp2f(mc - M);
-            const float z = l * a + exp2f(sk - M);
-            f = a / z;
-            lse_v = (M + log2f(z)) * kLn2;
-            lkv = (mc + log2f(l)) * kLn2;
-          }
-          if (first) {
-            p.lse[orow + h] = lse_v;
-            if (p.lse_kv) p.lse_kv[orow + h] = lkv;
-            if (p.max_logits) p.max_logits[orow + h] = any ? m_run[m][e] * kLn2 : -INFINITY;
-          }
+      for (int w = 0; w < kWarps; ++w) l += wmax[w * N::kHeads + h];
+      if (h >= hv) continue;
+      const float mc = m_run[e] == -INFINITY ? 0.f : m_run[e];
+      const bool any = l != 0.f;  // true for NaN too
+      const bool first = slice == 0 && c == 0;
+      float f = 0.f;
+      if (split_up) {
+        if (any) f = 1.f / l;  // a split's mean value, which stays in range where the sum might not
+        if (first) *reinterpret_cast<float4*>(smem + N::kStats + h * 16) = make_float4(mc, l, m_run[e], 0.f);
+      } else {
+        const float sink = p.sink ? __ldg(p.sink + h0 + h) : -INFINITY, sk = sink * kLog2e;
+        float lse_v = sink, lkv = INFINITY;
+        if (any) {
+          const float M = fmaxf(mc, sk);
+          const float a = exp2f(mc - M);
+          const float z = l * a + exp2f(sk - M);
+          f = a / z;
+          lse_v = (M + log2f(z)) * kLn2;
+          lkv = (mc + log2f(l)) * kLn2;
         }
-        // this lane's dims: 64 slice + 8 (2c + k) + j
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int d = slice * 64 + (2 * c + k) * 8;
-          float o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = any ? acc[m][j][2 * e + k] * f : 0.f;
-          if (split_up) {
-            float4* to = reinterpret_cast<float4*>(smem) + (h * DV + d) / 4;
-            to[0] = make_float4(o[0], o[1], o[2], o[3]), to[1] = make_float4(o[4], o[5], o[6], o[7]);
-          } else {
-            __stcs(reinterpret_cast<uint4*>(p.out + (orow + h) * DV + d),
-                   make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])));
-          }
+        if (first) {
+          p.lse[orow + h] = lse_v;
+          if (p.lse_kv) p.lse_kv[orow + h] = lkv;
+          if (p.max_logits) p.max_logits[orow + h] = any ? m_run[e] * kLn2 : -INFINITY;
         }
       }
+      // this lane's dims: 64 slice + 8 (2c + k) + j
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int d = slice * 64 + (2 * c + k) * 8;
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = any ? acc[j][2 * e + k] * f : 0.f;
+        if (split_up) {
+          float4* to = reinterpret_cast<float4*>(smem) + (h * DV + d) / 4;
+          to[0] = make_float4(o[0], o[1], o[2], o[3]), to[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+          __stcs(reinterpret_cast<uint4*>(p.out + (orow + h) * DV + d),
+                 make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])));
+        }
+      }
+    }
   }
   if (!split_up) return;
 
@@ -493,8 +465,8 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
   // the splits' means O_s.  Each CTA takes its part of the values.
   cluster_sync();
   float* shares = reinterpret_cast<float*>(smem + N::kShares);
-  if (tid < N::kHeads * kMaxCluster) {
-    const int h = tid / kMaxCluster, s = tid % kMaxCluster;  // eight lanes a head
+  for (int y = tid; y < N::kHeads * kMaxCluster; y += kBlock) {
+    const int h = y / kMaxCluster, s = y % kMaxCluster;  // sixteen lanes a head
     const float4 v = s < p.splits && h < hv ? ld_cluster(base + N::kStats + h * 16, s) : make_float4(0.f, 0.f, 0.f, 0.f);
     const bool have = v.y != 0.f;
     float mm = have ? v.x : -INFINITY, mx = have ? v.z : -INFINITY;
@@ -512,7 +484,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
 #pragma unroll
     for (int o = 1; o < kMaxCluster; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float z = any ? l + exp2f(sk - M) : 1.f;
-    shares[tid] = a / z;  // at most 1: a mean of means stays in range
+    shares[y] = a / z;  // at most 1: a mean of means stays in range
     if (split == 0 && s == 0 && h < hv) {
       p.lse[orow + h] = any ? (M + log2f(z)) * kLn2 : sink;
       if (p.lse_kv) p.lse_kv[orow + h] = any ? (M + log2f(l)) * kLn2 : INFINITY;
@@ -521,33 +493,29 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP, MT>::kPerSm)) at
   }
   __syncthreads();
   for (int y = split * kBlock + tid; y < hv * (DV / 4); y += p.splits * kBlock) {
-    const int h = y / (DV / 4);
-    float4 v[kMaxCluster];
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s)
-      if (s < p.splits) v[s] = ld_cluster(base + y * 16, s);
+    const float* share = shares + y / (DV / 4) * kMaxCluster;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s) {
-      if (s < p.splits) {
-        const float a = shares[h * kMaxCluster + s];
-        o.x = fmaf(a, v[s].x, o.x), o.y = fmaf(a, v[s].y, o.y), o.z = fmaf(a, v[s].z, o.z), o.w = fmaf(a, v[s].w, o.w);
-      }
+#pragma unroll 8
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 v = ld_cluster(base + y * 16, s);
+      const float a = share[s];
+      o.x = fmaf(a, v.x, o.x), o.y = fmaf(a, v.y, o.y), o.z = fmaf(a, v.z, o.z), o.w = fmaf(a, v.w, o.w);
     }
     reinterpret_cast<uint2*>(p.out + orow * DV)[y] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
   cluster_sync();  // the others have read this CTA's values
 }
 
-template <int DQK, int DV, bool SEP, int MT>
-int launch_narrow_form(const Params& p, int T, cudaStream_t stream) {
-  using N = Narrow<DQK, DV, SEP, MT>;
-  auto kernel = attn_kv4_narrow_kernel<DQK, DV, SEP, MT>;
+template <int DQK, int DV, bool SEP>
+int launch_form(const Params& p, cudaStream_t stream) {
+  using N = Narrow<DQK, DV, SEP>;
+  auto kernel = attn_kv4_narrow_kernel<DQK, DV, SEP>;
   static std::atomic<uint64_t> ready{0};  // devices where the kernel's shared memory is allowed
   int dev = 0;
   cudaGetDevice(&dev);  // below 64: check_device
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, N::kTotal) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, N::kTotal) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return dsa::launch_error("attn_kv4_narrow_kernel smem attribute");
     ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
@@ -566,30 +534,22 @@ int launch_narrow_form(const Params& p, int T, cudaStream_t stream) {
   return DSA_OK;
 }
 
-template <int MT>
-int launch_heads(const Params& p, int T, int Dqk, bool separate, cudaStream_t stream) {
-  if (separate) return launch_narrow_form<256, 256, true, MT>(p, T, stream);
-  return Dqk == 576 ? launch_narrow_form<576, 512, false, MT>(p, T, stream)
-                    : launch_narrow_form<512, 512, false, MT>(p, T, stream);
-}
-
 }  // namespace
 
 namespace dsa {
 namespace kv4_attn {
 
-bool narrow_takes(int T, int H, int Hc, int K) {
+bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
   const int64_t units = static_cast<int64_t>(T) * Hc * ((H / Hc + 15) / 16);
-  if (units * kMaxCluster < kv8_attn::kPlanSms && K > 5120) return false;
-  return H / Hc <= 32 || units <= 16;
+  if (units * kMaxCluster < kv8_attn::kPlanSms && K > 6144) return false;
+  if (units <= 4) return true;
+  return H / Hc <= 16 && (Dqk == 256 || K <= 1024 || units <= 64);
 }
-
-int narrow_heads(int T, int H, int Hc) { return H / Hc <= 16 || static_cast<int64_t>(T) * H <= 256 ? 16 : 32; }
 
 constexpr int kItemTiles = 2;
 
-int narrow_splits(int64_t units, int heads, int K) {
-  const int nt = (K + kTile - 1) / kTile, slots = (heads == 16 ? 3 : 2) * kv8_attn::kPlanSms;
+int narrow_splits(int64_t units, int K) {
+  const int nt = (K + kTile - 1) / kTile, slots = 3 * kv8_attn::kPlanSms;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxCluster && s <= nt; s *= 2) {
@@ -600,8 +560,9 @@ int narrow_splits(int64_t units, int heads, int K) {
   return best;
 }
 
-int launch_narrow(const kv8_attn::Params& p, int T, int heads, int Dqk, bool separate, cudaStream_t stream) {
-  return heads == 16 ? launch_heads<1>(p, T, Dqk, separate, stream) : launch_heads<2>(p, T, Dqk, separate, stream);
+int launch_narrow(const kv8_attn::Params& p, int T, int Dqk, cudaStream_t stream) {
+  if (Dqk == 256) return launch_form<256, 256, true>(p, stream);
+  return Dqk == 576 ? launch_form<576, 512, false>(p, stream) : launch_form<512, 512, false>(p, stream);
 }
 
 }  // namespace kv4_attn

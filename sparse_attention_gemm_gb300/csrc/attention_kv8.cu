@@ -31,6 +31,7 @@ extern "C" int dsa_sparse_attn_fwd_kv8(const void* q, const void* kv8, const flo
   p.v8 = static_cast<const uint8_t*>(v8 ? v8 : kv8);
   p.v_scale = v8 ? v_scale : kv_scale;
   if (narrow_takes(T, H, Hc, K)) return launch_narrow(p, T, Dqk, stream);
+  if (need > 0) take_workspace(p, T, workspace);
   if (v8) return launch<Gather<256, 256, true>, 256, 256, true>(p, T, stream);
   return Dqk == 576 ? launch<Gather<576, 512, false>, 576, 512, false>(p, T, stream)
                     : launch<Gather<512, 512, false>, 512, 512, false>(p, T, stream);

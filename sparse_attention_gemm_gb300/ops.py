@@ -78,7 +78,7 @@ _SIGNATURES = {
     "dsa_sparse_attn_fwd_kv8": ([P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
     "dsa_kv4_write": ([P, P, P, P, I, I, I, I, I, I, I, P, P, P], I),
     "dsa_kv4_read": ([P, P, P, P, P, I, I, I, I, I, I, I, P, P], I),
-    "dsa_sparse_attn_fwd_kv4_workspace_size": ([I, I, I, I, I, I], SZ),
+    "dsa_sparse_attn_fwd_kv4_workspace_size": ([I, I, I, I, I, I, I, I, I], SZ),
     "dsa_sparse_attn_fwd_kv4": ([P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
     "dsa_rms_norm_fwd": ([P, I64, P, I64, P, I, I, F, I, P, I64, P, P, I64, P, P], I),
     "dsa_rms_norm_bwd_workspace_size": ([I, I], SZ),
@@ -877,8 +877,9 @@ def kv4_read(cache, cache_scale, cu_seqlens, T: int, pos=None, block_table=None,
     return out
 
 
-def sparse_attn_fwd_kv4_workspace_size(T: int, H: int, Hc: int, Dqk: int, Dv: int, K: int) -> int:
-    return int(lib().dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K))
+def sparse_attn_fwd_kv4_workspace_size(T: int, H: int, Hc: int, Dqk: int, Dv: int, K: int, block: int, n_blocks: int,
+                                       paged: bool = False) -> int:
+    return int(lib().dsa_sparse_attn_fwd_kv4_workspace_size(T, H, Hc, Dqk, Dv, K, block, n_blocks, 1 if paged else 0))
 
 
 def _attn4_refuse(q, kv4, kv_scale, idx, topk_length, sink, v4, v_scale, cu_seqlens, block_table, out, lse, workspace):
@@ -977,7 +978,7 @@ def sparse_attn_fwd_kv4(q, kv4, kv_scale, idx, scale: float, topk_length=None, s
         m_ptr = ml.data_ptr()
     L = _lib or lib()
     if workspace is None:
-        need = L.dsa_sparse_attn_fwd_kv4_workspace_size(T, H, heads, Dqk, Dv, K)
+        need = L.dsa_sparse_attn_fwd_kv4_workspace_size(T, H, heads, Dqk, Dv, K, block, n_blocks, 1 if t_ptr else 0)
         if need:
             workspace = empty((need,), dtype=_U8, device=device)
     if workspace is not None:

@@ -372,6 +372,67 @@ def test_repeated_calls_give_the_same_bits(H):
         assert torch.equal(first["out"], again["out"]) and torch.equal(first["lse"], again["lse"])
 
 
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("H,table", [(40, True), (64, False), (128, True)])
+def test_attention_over_a_cache_widened_once(dqk, dv, H, table):
+    """Many slots of a small cache: its values go through bf16 rows.  Lengths, holes, a padded batch; a few rows against
+    their definition, every row against the tiles' own conversion (the same call on a part of the rows)."""
+    rng = np.random.default_rng(dqk + H)
+    T, K, block = 700, 700, 16
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, block, table, n=900)
+    ks.reshape(-1)[rng.integers(0, ks.size, 5)] = 131  # a few blocks of large values
+    assert ops.sparse_attn_fwd_kv4_workspace_size(T, H, 1, dqk, dv, K, block, k.shape[0], table) >= k.shape[0] * block * dqk * 2
+    if table:
+        kw["cu"] = cu_from_lengths([300, 350])  # 50 padding rows
+    kw["sink"] = rng.standard_normal(H).astype(np.float32)
+    d = {n: (dev(kw[n]) if n in kw else None) for n in ("v4", "v_scale", "cu", "table", "sink")}
+    out = torch.full((T, H, dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, H), 7.0, device=DEV)
+    args = dict(v4=d["v4"], v_scale=d["v_scale"], sink=d["sink"], block_table=d["table"])
+    got = ops.sparse_attn_fwd_kv4(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, topk_length=dev(kw["length"]), cu_seqlens=d["cu"],
+                                  want_lse_kv=True, want_max_logits=True, out=out, lse=lse, **args)
+    done = int(kw["cu"][-1]) if table else T
+    assert bool((out[done:] == 7.0).all()) and bool((lse[done:] == 7.0).all())
+    rows = np.array([0, 1, 5, 299, 300, T // 2, 600, 649])
+    seq = np.searchsorted(kw["cu"], rows, side="right") - 1 if table else None
+    for i, t in enumerate(rows):
+        part = {n: kw[n] for n in ("sink", "v4", "v_scale") if n in kw}
+        if table:
+            part.update(table=kw["table"][seq[i]:seq[i] + 1], cu=np.array([0, 1], np.int32))
+        ref = R.attention(f64(q[t:t + 1]), k, ks, idx[t:t + 1], sm, length=kw["length"][t:t + 1], **part)
+        assert not (np.abs(got["out"][t].double().cpu().numpy() - ref["out"][0]) > ref["out_tol"][0]).any(), t
+        for n in ("lse", "lse_kv", "max_logits"):
+            g, want = got[n][t].double().cpu().numpy(), ref[n][0]
+            fin = np.isfinite(want)
+            # (an empty row's lse is the sink, which this form takes to powers of two and back: two products and two
+            # rounded constants, 4 * 2^-24 of it)
+            tol = np.maximum(ref["lse_tol"][0], 2.0 ** -22 * np.abs(kw["sink"]))
+            assert np.array_equal(g[~fin], want[~fin]) and not (np.abs(g[fin] - want[fin]) > tol[fin]).any(), (n, t)
+    # rows 100..139 alone: too few slots to widen the cache for
+    part = slice(100, 140)
+    few = ops.sparse_attn_fwd_kv4(dev_bf16(q[part]), dev(k), dev(ks), dev(idx[part]), sm, topk_length=dev(kw["length"][part]),
+                                  cu_seqlens=dev(cu_from_lengths([40, 0])) if table else None, **args)
+    a, b = got["out"][part].float(), few["out"].float()
+    assert float((a - b).norm() / b.norm()) <= 4 * 2.0 ** -8  # each rounds weights and out (2^-8)
+    fin = torch.isfinite(few["lse"])
+    assert torch.equal(fin, torch.isfinite(got["lse"][part])) and float((few["lse"] - got["lse"][part])[fin].abs().max()) <= 1e-3
+    again = ops.sparse_attn_fwd_kv4(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, topk_length=dev(kw["length"]), cu_seqlens=d["cu"], **args)
+    assert torch.equal(again["out"][:done], got["out"][:done]) and torch.equal(again["lse"][:done], got["lse"][:done])
+
+
+def test_widened_cache_never_uses_unselected_rows():
+    rng = np.random.default_rng(70)
+    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, 650, 64, 1, 640, 1, False, n=1300)
+    idx[(idx >= 0) & (idx % 7 == 3)] = 4
+    spoilt = ks.copy()
+    spoilt[np.arange(k.shape[0]) % 7 == 3] = 255
+    a = [dev_bf16(q), dev(k)]
+    assert ops.sparse_attn_fwd_kv4_workspace_size(650, 64, 1, 576, 512, 640, 1, k.shape[0]) > 0
+    x = ops.sparse_attn_fwd_kv4(*a, dev(ks), dev(idx), sm, topk_length=dev(kw["length"]))
+    y = ops.sparse_attn_fwd_kv4(*a, dev(spoilt), dev(idx), sm, topk_length=dev(kw["length"]))
+    assert torch.equal(x["out"], y["out"]) and torch.equal(x["lse"], y["lse"]) and bool(torch.isfinite(y["out"]).all())
+
+
 def test_empty_calls():
     k, ks = cache_of(np.random.default_rng(1), 2, 4, 1, 576)
     c, s = dev(k), dev(ks)
@@ -420,7 +481,7 @@ def test_captured_steps_with_their_own_workspaces():
         q, k, ks, idx, sm, _ = attention_case(rng, 576, 512, T, H, 1, K, 32, False, holes=False)
         st = {"q": dev_bf16(q), "k": dev(k), "s": dev(ks), "idx": dev(idx), "cu": dev(cu_from_lengths([T])),
               "pos": dev(np.array([37], np.int32)), "src": dev_bf16(rows(rng, T, 1, 576))}
-        n = ops.sparse_attn_fwd_kv4_workspace_size(T, H, 1, 576, 512, K)
+        n = ops.sparse_attn_fwd_kv4_workspace_size(T, H, 1, 576, 512, K, 32, k.shape[0])
         st["ws"] = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
 
         def step(st=st, sm=sm):

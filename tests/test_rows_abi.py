@@ -149,17 +149,36 @@ def test_cache_attention_refuses(lib, bad):
     assert b"dsa_sparse_attn_fwd_kv4" in lib.dsa_last_error()
 
 
-@pytest.mark.parametrize("shape", [(32, 128, 1, 576, 512, 2048), (20, 64, 1, 512, 512, 2048), (1, 64, 1, 576, 512, 131072)])
-def test_cache_attention_workspace(lib, shape):
-    need = lib.dsa_sparse_attn_fwd_kv4_workspace_size(*shape)
+# (shape, block, blocks, paged, fewest bytes): rows in splits leave a mean value and its sums each; a cache that
+# is widened once takes its rows in bf16, and the slots' rows with a block table
+@pytest.mark.parametrize("shape,block,n_blocks,paged,least", [
+    ((32, 128, 1, 576, 512, 2048), 64, 10, False, 2 * 32 * 128 * 516 * 4),
+    ((20, 64, 1, 512, 512, 2048), 64, 10, False, 2 * 20 * 64 * 516 * 4),
+    ((1, 64, 1, 576, 512, 131072), 64, 4096, False, 2 * 64 * 516 * 4),
+    ((2048, 64, 1, 576, 512, 2048), 64, 256, False, 64 * 256 * 576 * 2),
+    ((2048, 64, 1, 576, 512, 2048), 64, 256, True, 64 * 256 * 576 * 2 + 2048 * 2048 * 4),
+    ((2048, 20, 1, 256, 256, 2048), 16, 1000, False, 16 * 1000 * 512 * 2),
+])
+def test_cache_attention_workspace(lib, shape, block, n_blocks, paged, least):
+    need = lib.dsa_sparse_attn_fwd_kv4_workspace_size(*shape, block, n_blocks, 1 if paged else 0)
+    assert need >= least
     T, H, Hc, Dqk, Dv, K = shape
-    assert need >= 2 * T * H * (Dv + 4) * 4  # two splits at least: a mean value and its sums each
-    a = dict(T=T, H=H, Hc=Hc, Dqk=Dqk, Dv=Dv, K=K)
+    a = dict(T=T, H=H, Hc=Hc, Dqk=Dqk, Dv=Dv, K=K, block=block, n_blocks=n_blocks)
+    if paged:
+        a.update(table=FAKE, cu=FAKE, n_seqs=2, max_blocks=4)
+    if Dqk == 256:
+        a.update(v8=FAKE, v_scale=FAKE)
     for bad in (dict(ws_bytes=need - 1), dict(ws_bytes=0), dict(workspace=NULL),
                 dict(workspace=ctypes.c_void_p(4096 + 128))):
         assert lib.dsa_sparse_attn_fwd_kv4(*attn_args(**{**a, "ws_bytes": need, **bad})) == ops.DSA_ERR_WORKSPACE
         assert str(need).encode() in lib.dsa_last_error()
-    assert lib.dsa_sparse_attn_fwd_kv4_workspace_size(2048, 64, 1, 576, 512, 2048) == 0
+
+
+@pytest.mark.parametrize("shape,block,n_blocks", [
+    ((1, 64, 1, 576, 512, 2048), 64, 1024), ((2048, 64, 1, 576, 512, 2048), 64, 20000), ((96, 24, 2, 256, 256, 1027), 16, 9999),
+    ((0, 64, 1, 576, 512, 64), 64, 10), ((4, 64, 1, 576, 512, 0), 64, 10), ((4, 64, 3, 576, 512, 64), 64, 10)])
+def test_cache_attention_needs_no_workspace(lib, shape, block, n_blocks):
+    assert lib.dsa_sparse_attn_fwd_kv4_workspace_size(*shape, block, n_blocks, 1) == 0
 
 
 @pytest.mark.parametrize("bad", [None, [[0.0]], 3, torch.tensor(1.0, dtype=torch.bfloat16)])
