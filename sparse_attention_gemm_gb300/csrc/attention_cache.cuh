@@ -8,15 +8,16 @@
 // How a tile of codes becomes bf16 values in shared memory is the business of a Gather
 // (attention_kv8.cuh, attention_kv4.cu); the rest is here.
 //
-// A code is a bf16 value exactly, and a block's scale is one number per key: it
-// multiplies the key's scores and weights, and no code is rounded.  Codes
-// are widened to bf16 on their way into shared memory, and both products run in bf16
+// A code is a bf16 value exactly.  An 8-bit block's scale is one number per key: it
+// multiplies the key's scores and weights, and no code is rounded.  A 4-bit code
+// times its scale is a bf16 value again (kScaled = false).  Codes are widened to bf16 on their way into shared memory, and both products run in bf16
 // (kind::f16) with fp32 sums.  The one rounding before out's is that of
 // the weights exp(s_j - m) * v_scale / 2^E to bf16, as in the bf16 call; bf16
 // has fp32's exponents, so small weights keep their relative precision.
 //
 // Work item = (token, KV head, group of 64 query heads, split of its slots);
-// calls with few heads per KV head or few rows go to attention_kv8_narrow.cu.
+// calls with few heads per KV head or few rows go to attention_kv8_narrow.cu and
+// attention_kv4_narrow.cu.
 // Products ("swap AB"), tiles of 64 keys:
 //   MMA1  S^T[key, head]  = K[key, :] . Q[head, :]^T           (M = 64 keys, N = 64)
 //   MMA2  O^T[dim, head] += V^T[dim, key] . P^T[key, head]     (M = 128 dims, N = 64)
@@ -26,7 +27,7 @@
 // when a tile passes it by 2^kMove, and a reference exponent E of the value
 // scales that moves when a block's scale passes 2^E; both move the running sums.
 //
-// What bounds it: shared memory.  A tile's products read 240 KB of operands (an
+// What bounds it, over E4M3 codes: shared memory.  A tile's products read 240 KB of operands (an
 // M = 64, N = 64 step takes its 4 KB at the memory's whole rate), its codes
 // arrive as 36 KB and are stored as 72: 350 KB, 2.7K of the 3.4K cycles
 // that a tile takes; the rest is the chain of two buffers (stores 1.3K, scores 2K, softmax 1K,

@@ -5,6 +5,17 @@
 // way into shared memory, scales and all, and the products and the softmax of
 // attention_cache.cuh run on it as on a bf16 cache: the roundings are those of the bf16
 // call.  A row of 576 comes as 306 bytes.
+//
+// Three forms, by rules on the call's sizes (narrow_takes, widens):
+// * tiles: groups of 64 heads, each row's codes widened on their way (attention_cache.cuh).
+//   2048 rows of 64 heads, 2048 slots, 576 dims: 889 us, 657 TFLOP/s.  The gather bounds it: a
+//   warp's conversion of its part of a tile takes 1.5K cycles and its loads' issue 1.8K, where the products take 2.2K.
+//   Slower: two hand-overs a tile (977 where 938), the loads two tiles ahead (1042), scale bytes by
+//   shuffles (987 where 890), loads past L1 (900 to 926).
+// * narrow: groups of 16 heads, warp products (attention_kv4_narrow.cu).
+// * widened: a cache whose rows are read often is written out in bf16 once and the call is the
+//   bf16 one (attention.cu), which such a call comes close to: the same 2048 rows over 16,384 cache rows
+//   703 us, 831 TFLOP/s, of which widening takes 4 and the positions' rows 10.
 #include "attention_cache.cuh"
 #include "attention_kv4.cuh"
 
@@ -147,16 +158,29 @@ __global__ void __launch_bounds__(kWideThreads) kv4_widen_kernel(const uint32_t*
   }
 }
 
-// Cache rows of positions: one CTA a query row, whose sequence each warp looks up.
+// Cache rows of positions: one CTA a query row, whose sequence each warp looks up.  Eight ids of a
+// thread are under way at a time: their pages are loads that wait for loads.
 __global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* __restrict__ idx, const dsa::Kv8Geom g, int K,
                                                                 int32_t* __restrict__ rows) {
   const int t = blockIdx.x;
   if (t >= __ldg(g.cu + g.n_seqs)) return;
   const int b = dsa::kv8_seq_warp(g.cu, g.n_seqs, t);
   const int64_t at = static_cast<int64_t>(t) * K;
-  for (int j = threadIdx.x; j < K; j += kWideThreads) {
-    const int id = __ldcs(idx + at + j);
-    rows[at + j] = id < 0 ? -1 : dsa::kv8_row(g, b, id);
+  constexpr int kAhead = 8;
+  for (int j0 = threadIdx.x; j0 < K; j0 += kWideThreads * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = j0 + k * kWideThreads;
+      id[k] = j < K ? __ldcs(idx + at + j) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) id[k] = id[k] < 0 ? -1 : dsa::kv8_row(g, b, id[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int j = j0 + k * kWideThreads;
+      if (j < K) rows[at + j] = id[k];
+    }
   }
 }
 
@@ -169,9 +193,10 @@ WideSizes widened_sizes(int T, int Dqk, int Dv, int K, int64_t cache_rows, bool 
                    paged ? up256(static_cast<size_t>(T) * K * 4) : 0};
 }
 
-// Whether the cache is widened once for the call.  Measured (576 dims, 64 heads, a slot each): the tiles'
-// own conversion costs 0.05 ns a slot and group of 64 heads over the bf16 kernel, widening 0.27 ns a cache row
-// and the launches 8 us; taken where the first is twice the second, up to 2^30 bytes.
+// Whether the cache is widened once for the call.  Measured (576 dims, 64 heads): the tiles' own
+// conversion costs 0.05 ns a slot and group of 64 heads over the bf16 kernel (2048 rows of 2048 slots 889 us
+// against 703), widening 0.27 ns a cache row and the launches 8 us; taken where the first is
+// twice the second, for a widened cache of at most 2^30 bytes.
 bool widens(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows) {
   const double slots = static_cast<double>(T) * K * ((H + kHG - 1) / kHG);
   return Hc == 1 && slots >= 10.8 * cache_rows + 320e3 && cache_rows * (Dqk == 256 ? Dqk + Dv : Dqk) <= (int64_t{1} << 29);

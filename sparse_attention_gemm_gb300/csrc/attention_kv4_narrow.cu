@@ -14,8 +14,15 @@
 // running maximum of each head) is agreed on through shared memory, and a warp adds up 64 value dims
 // (of 256 dims: of one half of the keys).  Raw codes arrive by cp.async, two tiles ahead.
 //
+// Why warp products: 16 heads fill a quarter of the tcgen05 tile's columns (N = 64), whose operands
+// have to be stored and read all the same.  What bounds it is the issue of instructions (65%, the tensor
+// pipe 25%): a tile of 64 keys is widened by integer and bf16 arithmetic.  96 rows of 2 x 12 heads, 1027
+// slots, 256 dims: 41 us, 1.2 TB/s of codes; on the tiles of 64 heads 59.  One row of 16 heads, 2048 slots, 576
+// dims: 12.8 us; on the tiles 15.8.  Slower: tiles of 128 keys (73 us where 46), two CTAs an SM (51 where 41),
+// loops that are not unrolled; groups of 32 heads were never ahead of the tiles.
+//
 // Work item = (token, KV head, group of 16 heads, split of its slots); a row's splits are the CTAs of a
-// cluster and are joined there.
+// cluster and are joined there: no workspace, no second launch, nothing that waits on another cluster.
 #include "attention_kv4.cuh"
 
 namespace {
@@ -54,6 +61,7 @@ struct Narrow {
   static constexpr uint32_t kShares = kStats + kHeads * 16;  // float [heads][kMaxCluster]
   static constexpr uint32_t kTotal = kShares + kHeads * kMaxCluster * 4;
   static_assert(kHeads * DV * 4 <= kFactors, "mean values");
+  // CTAs of an SM, by their shared memory (228 KB of it, 1 KB of each the system's)
   static constexpr int kPerSm = kTotal <= 75 * 1024 ? 3 : kTotal <= 113 * 1024 ? 2 : 1;
   static_assert(kTotal <= 227 * 1024 && kStage % 16 == 0 && kStages % 16 == 0 && kP % 16 == 0, "shared memory");
   // value dims: 64 a warp; with 256, two halves of the keys
@@ -539,6 +547,14 @@ int launch_form(const Params& p, cudaStream_t stream) {
 namespace dsa {
 namespace kv4_attn {
 
+// Measured, in us, groups of 16 heads here against the tiles of 64 (rows x heads x slots):
+//   one row of 16 heads    2048 slots 12.8 / 15.8, 8192 27.5 / 21.4, 65,536 165 / 72:
+//                          sixteen CTAs a unit are all there are, the tiles' 32 splits win long rows
+//   one row of 64 heads    512 9.5 / 14.3, 2048 13.2 / 17.0 (four units); of 128 2048 18.7 / 17.3
+//   four rows of 64 heads  2048 24.6 / 17.9: a group's keys are widened once for 16 heads, there for 64
+//   rows of 16 heads       64 x 2048 41.1 / 40.8, 300 x 2048 162 / 131, 1024 x 512 119 / 135
+//   256 dims               96 x (2 x 12) x 1027 39.8 / 58.8, 1000 x 12 x 1027 168 / 193,
+//                          16 x 32 x 1027 15.4 / 14.2
 bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
   const int64_t units = static_cast<int64_t>(T) * Hc * ((H / Hc + 15) / 16);
   if (units * kMaxCluster < kv8_attn::kPlanSms && K > 6144) return false;
@@ -546,8 +562,12 @@ bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
   return H / Hc <= 16 && (Dqk == 256 || K <= 1024 || units <= 64);
 }
 
+// The time of a work item besides its tiles, in tiles: the query's way and the join.
 constexpr int kItemTiles = 2;
 
+// A power of two, at most a cluster's CTAs: the fewest waves of (tiles of an item + kItemTiles), with
+// kPerSm = 3 as most forms have it; of equal ones the fewest splits.  96 rows of 2 x 12 heads, 1027 slots:
+// two splits 41 us, four 48; one row of 16 heads, 2048 slots: sixteen.
 int narrow_splits(int64_t units, int K) {
   const int nt = (K + kTile - 1) / kTile, slots = 3 * kv8_attn::kPlanSms;
   int best = 1;

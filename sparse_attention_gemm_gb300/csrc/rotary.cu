@@ -8,6 +8,12 @@
 // Angles: f_i / (2 pi) is taken as a fraction of a turn in 64-bit fixed point, so that
 // p times it modulo a turn is one integer product: the angle of position p is off
 // by p * 2^-61 of f_i and p * 2^-64 of a turn, and by 2^-25 of half a turn when it becomes fp32.
+//
+// A CTA works out its tokens' cosines and sines once, for all their heads, while the first loads
+// are under way.  The rows' bytes bound it: 16,384 tokens of 64 + 1 rows of 64, halves, 272 MB, take
+// 45 us (6.1 TB/s), pairs 47; rows that are the last 64 of 576 the same 48 and 50; 4096 tokens of
+// 24 + 2 heads of 256 21 us (5.2 TB/s).  64 tokens take 3.4 us: the chain from the sequence's
+// offsets to the angles, not the bytes.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -55,7 +61,7 @@ template <bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
   constexpr int kWords = PAIRS ? 1 : 2;
   // mul * cos, mul * sin of [token][pair of a unit][unit]: neighbouring units read neighbouring words
-  // (unit by unit they met in the same banks: R = 256 took 36 us where it takes 20)
+  // (unit by unit they met in the same banks: R = 256 took 36 us where it takes 21)
   __shared__ float2 turn[kMaxAngles];
   __shared__ int64_t place[kMaxTokens];  // position, or kNone
   constexpr int64_t kNone = INT64_MIN;
@@ -241,9 +247,13 @@ extern "C" int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H,
   p.H = H, p.H2 = H2, p.R = R;
   p.per = interleaved ? R / 8 : R / 16;
   p.mul = mul, p.sign = inverse ? -1.f : 1.f;
-  // tokens of a CTA: one round of its threads, and two CTAs an SM at least
-  const int per_token = (H + H2) * p.per;
-  int tokens = std::min({kMaxTokens, kMaxAngles / (R / 2), std::max(1, kAhead * kThreads / per_token)});
+  // Tokens of a CTA: one round of its threads' units, or two rounds where one token takes more than
+  // half of one (16,384 tokens of 65 rows of 64, pairs: 47 us, and 57 with one token a CTA; rounds
+  // of 20 rows, where three tokens share one, gain nothing from two: 17.0 us), and two CTAs an SM at
+  // least.
+  const int per_token = (H + H2) * p.per, round = kAhead * kThreads;
+  const int units = per_token > round / 2 ? 2 * round : round;
+  int tokens = std::min({kMaxTokens, kMaxAngles / (R / 2), std::max(1, units / per_token)});
   tokens = std::max(1, std::min(tokens, T / (2 * sms)));
   p.tokens = tokens;
   p.m_token = tokens == 1 ? 1 : dsa::magic_of(per_token);

@@ -28,8 +28,17 @@ Cases (kernel to select with -k in parentheses):
   kv8_write       dsa_kv8_write of T latent rows into pages of 64 tokens (kv8_write_kernel)
   kv8_read        dsa_kv8_read of them                          (kv8_read_kernel)
   attention_kv8   dsa_sparse_attn_fwd_kv8 over those pages, ids drawn evenly
-                  from the causal rows                          (attn_kv8_kernel)
+                  from the causal rows                          (attn_cache_kernel)
   attention_kv8_narrow  the same with H = 16                    (attn_kv8_narrow_kernel)
+  rms_norm        dsa_rms_norm_fwd of T rows of 4096, residual added (rms_fwd_kernel)
+  rms_norm_bwd    dsa_rms_norm_bwd of them                      (rms_bwd_kernel, rms_dw_kernel)
+  rotary          dsa_rotary of the last 64 of H heads of 576   (rotary_kernel)
+  kv4_write       dsa_kv4_write of T latent rows into pages of 64 tokens (kv4_write_kernel)
+  kv4_read        dsa_kv4_read of them                          (kv4_read_kernel)
+  attention_kv4   dsa_sparse_attn_fwd_kv4 over a cache of T * k / 8 rows, ids drawn
+                  evenly: too many rows to be widened once      (attn_cache_kernel)
+  attention_kv4_widened  the same over T rows                   (kv4_widen_kernel, kv4_rows_kernel, sparse_attn_kernel)
+  attention_kv4_narrow   the first with H = 16 heads, k at most 1024 (attn_kv4_narrow_kernel)
 """
 from __future__ import annotations
 
@@ -41,7 +50,8 @@ import numpy as np
 import torch
 
 CASES = ("indexer_dense", "indexer_fused", "indexer_mxfp8", "select", "topk", "attention", "gqa", "backward",
-         "kv8_write", "kv8_read", "attention_kv8", "attention_kv8_narrow")
+         "kv8_write", "kv8_read", "attention_kv8", "attention_kv8_narrow", "rms_norm", "rms_norm_bwd", "rotary", "kv4_write",
+         "kv4_read", "attention_kv4", "attention_kv4_widened", "attention_kv4_narrow")
 
 
 def _bf16(shape, sigma, g, dev):
@@ -105,6 +115,45 @@ def main(argv=None) -> int:
             u = torch.rand((T, K), generator=g, device=dev) * torch.arange(1, T + 1, device=dev)[:, None]
             idx = u.to(torch.int32).sort(1)[0].contiguous()
             twice(lambda: ops.sparse_attn_fwd_kv8(q, kv8, scale, idx, 1.0 / 24.0, cu_seqlens=cu, block_table=table))
+        status = ops.device_status(clear=True)
+        print(f"{args.case}: T={T} k={K} status={status:#x}")
+        return 1 if status else 0
+
+    if args.case in ("rms_norm", "rms_norm_bwd", "rotary"):
+        if args.case == "rotary":
+            q, k = _bf16((T, H, 576), 1.0, g, dev), _bf16((T, 1, 576), 1.0, g, dev)
+            f, mul = ops.rotary_inv_freq(64, scaling="yarn", factor=40.0, device=dev)
+            twice(lambda: ops.rotary(q[..., 512:], f, cu, x2=k[..., 512:], mul=mul, out=q[..., 512:], out2=k[..., 512:]))
+        else:
+            x, r, dy = (_bf16((T, 4096), 1.0, g, dev) for _ in range(3))
+            weight = torch.ones(4096, device=dev)
+            fwd = ops.rms_norm_fwd(x, weight, 1e-6, residual=r, want_rstd=True)
+            if args.case == "rms_norm":
+                twice(lambda: ops.rms_norm_fwd(x, weight, 1e-6, residual=r, want_rstd=True))
+            else:
+                twice(lambda: ops.rms_norm_bwd(dy, fwd["sum"], weight, fwd["rstd"], d_sum=r))
+        torch.cuda.synchronize()
+        print(f"{args.case}: T={T}")
+        return 0
+
+    if args.case in ("kv4_write", "kv4_read", "attention_kv4", "attention_kv4_widened", "attention_kv4_narrow"):
+        narrow = args.case == "attention_kv4_narrow"
+        K = min(K, 1024) if narrow else K
+        n = T * K // 8 if args.case in ("attention_kv4", "attention_kv4_narrow") else T
+        pages = (n + 63) // 64
+        table = torch.randperm(pages, generator=g, device=dev).to(torch.int32)[None]
+        kv4 = torch.randint(0, 256, (pages, 64, 1, 288), generator=g, device=dev, dtype=torch.int32).to(torch.uint8)
+        scale = torch.full((pages, 64, 1, 18), 125, dtype=torch.uint8, device=dev)
+        if args.case in ("kv4_write", "kv4_read"):
+            rows = _bf16((T, 1, 576), 1.0, g, dev)
+            if args.case == "kv4_write":
+                twice(lambda: ops.kv4_write(rows, kv4, scale, cu, block_table=table))
+            else:
+                twice(lambda: ops.kv4_read(kv4, scale, cu, T, block_table=table, out=rows))
+        else:
+            q = _bf16((T, 16 if narrow else 64, 576), 1.0, g, dev)
+            idx = torch.randint(0, n, (T, K), generator=g, device=dev, dtype=torch.int32).sort(1)[0].contiguous()
+            twice(lambda: ops.sparse_attn_fwd_kv4(q, kv4, scale, idx, 1.0 / 24.0, cu_seqlens=cu, block_table=table))
         status = ops.device_status(clear=True)
         print(f"{args.case}: T={T} k={K} status={status:#x}")
         return 1 if status else 0

@@ -241,6 +241,15 @@ def test_attention_many_rows(dqk, dv, H):
     check_attention(q, k, ks, idx, sm, **kw)
 
 
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,table", [(1, 16, 8192, True), (2, 5, 6200, False), (80, 12, 1100, True), (9, 40, 1500, False)])
+def test_attention_long_rows_of_few_heads(dqk, dv, T, H, K, table):
+    """Few heads and rows too long for a cluster, and more rows of few heads than clusters: groups of 64 heads, and of 16."""
+    rng = np.random.default_rng(K + dqk)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 32, table, n=3000, holes=T > 2)
+    check_attention(q, k, ks, idx, sm, sink=rng.standard_normal(H).astype(np.float32), **kw)
+
+
 @pytest.mark.parametrize("lo,hi", [(-60, -50), (-30, 4), (40, 60), (-100, 60), (-126, -90)])
 def test_attention_values_of_every_size(lo, hi):
     """Value scales that differ by many powers of two (keys of one size, so that scores stay finite)."""

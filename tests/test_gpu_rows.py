@@ -216,6 +216,7 @@ def part(rng, T, H, R_, ld, lead):
     (1024, 2, 1, [9, 4], [-3, 77], 3, 1032, 8),
     (32, 1, 0, [5000], None, 11, 40, 8),
     (48, 5, 3, [257], [100000], 0, 64, 16),
+    (64, 64, 1, [900, 1400], [0, 77], 3, 72, 8),
 ])
 def test_rotary(pairs, R_, H, H2, lens, pos, pad, ld, lead):
     rng = np.random.default_rng(R_ + H + len(lens))
