@@ -15,11 +15,12 @@
 // (of 256 dims: of one half of the keys).  Raw codes arrive by cp.async, two tiles ahead.
 //
 // Why warp products: 16 heads fill a quarter of the tcgen05 tile's columns (N = 64), whose operands
-// have to be stored and read all the same.  What bounds it is the issue of instructions (65%, the tensor
-// pipe 25%): a tile of 64 keys is widened by integer and bf16 arithmetic.  96 rows of 2 x 12 heads, 1027
-// slots, 256 dims: 41 us, 1.2 TB/s of codes; on the tiles of 64 heads 59.  One row of 16 heads, 2048 slots, 576
-// dims: 12.8 us; on the tiles 15.8.  Slower: tiles of 128 keys (73 us where 46), two CTAs an SM (51 where 41),
-// loops that are not unrolled; groups of 32 heads were never ahead of the tiles.
+// have to be stored and read all the same.  What bounds it is the issue of instructions (58 to 65%, the
+// tensor pipe 16 to 25%): eight codes take 17 to become bf16 values.  96 rows of 2 x 12 heads, 1027 slots,
+// 256 dims: 37 us, 1.3 TB/s of codes, of which SMs with three CTAs work all the time and those with two 4/5
+// of it; on the tiles of 64 heads 59.  One row of 16 heads, 2048 slots, 576 dims: 12.8 us; on the tiles 15.8.
+// Slower: tiles of 128 keys (73 us where 46), two CTAs an SM (51 where 41), loops that are not unrolled, pairing
+// values instead of codes (39.8 where 38.9); groups of 32 heads were never ahead of the tiles.
 //
 // Work item = (token, KV head, group of 16 heads, split of its slots); a row's splits are the CTAs of a
 // cluster and are joined there: no workspace, no second launch, nothing that waits on another cluster.
@@ -49,21 +50,24 @@ struct Narrow {
   static constexpr uint32_t kStage = kMetaAt + kTile;
   static constexpr uint32_t kStages = kHeads * kQPitch;                 // [2], behind the query
   static constexpr int kBlocksV = DV / 32;
-  static constexpr uint32_t kFPitch = kBlocksV * 4 + 4;                 // factors of a key's value blocks
-  static constexpr uint32_t kFactors = kStages + 2 * kStage;
+  static constexpr uint32_t kFPitch = kTile * 2 + 16;                   // factors of a value block's keys (bf16), in
+  static constexpr uint32_t kFactors = kStages + 2 * kStage;            // the order of the weights
   static constexpr uint32_t kPPitch = kTile * 2 + 16;
-  static constexpr uint32_t kP = (kFactors + kTile * kFPitch + 15) / 16 * 16;  // weights [heads][keys]
+  static constexpr uint32_t kP = (kFactors + kBlocksV * kFPitch + 15) / 16 * 16;  // weights [heads][keys]
   static constexpr uint32_t kRows = kP + kHeads * kPPitch;              // int [kRowRing][kTile]
-  static constexpr uint32_t kWmax = kRows + kRowRing * kTile * 4;       // float [warps][heads]
+  // float [heads][warps], of which eight lanes at a time read 16 bytes each, of eight heads: kWPitch floats a
+  // head, and no two of them in a bank
+  static constexpr uint32_t kWmax = kRows + kRowRing * kTile * 4;
+  static constexpr int kWPitch = 12;
   // what a CTA of a cluster leaves for the others: mean values [heads][DV] over the query and the stages, and
   // float4 [heads]: reference, sum, maximum
-  static constexpr uint32_t kStats = (kWmax + kWarps * kHeads * 4 + 15) / 16 * 16;
+  static constexpr uint32_t kStats = kWmax + kHeads * kWPitch * 4;
   static constexpr uint32_t kShares = kStats + kHeads * 16;  // float [heads][kMaxCluster]
   static constexpr uint32_t kTotal = kShares + kHeads * kMaxCluster * 4;
   static_assert(kHeads * DV * 4 <= kFactors, "mean values");
   // CTAs of an SM, by their shared memory (228 KB of it, 1 KB of each the system's)
   static constexpr int kPerSm = kTotal <= 75 * 1024 ? 3 : kTotal <= 113 * 1024 ? 2 : 1;
-  static_assert(kTotal <= 227 * 1024 && kStage % 16 == 0 && kStages % 16 == 0 && kP % 16 == 0, "shared memory");
+  static_assert(kTotal <= 227 * 1024 && kStage % 16 == 0 && kStages % 16 == 0 && kP % 16 == 0 && kWmax % 16 == 0, "shared memory");
   // value dims: 64 a warp; with 256, two halves of the keys
   static constexpr int kSlices = DV / 64, kHalves = kWarps / kSlices;
   static_assert(kHalves == 1 || kHeads * DV * 4 <= 2 * kStage, "the halves' sums meet in the stages");
@@ -110,6 +114,9 @@ __device__ __forceinline__ void with_direct(bool direct, F f) {
   if (direct) f(std::true_type{});
   else f(std::false_type{});
 }
+
+// A tile whose scores pass a head's reference by more than this (in powers of two) moves it.
+constexpr float kMove = 8.0f;
 
 // The key (of eight) of a score's column, and the place of a key's weight: see kKPitch.
 __device__ __forceinline__ constexpr int key_of(int col) { return (col & 4) + ((col >> 1) & 1) + 2 * (col & 1); }
@@ -183,35 +190,39 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
   }
   __syncthreads();
 
+  // where a key's scales begin in its 32 bytes
+  auto shift_of = [](const uint8_t* st, int key) { return DQK == 576 ? st[N::kMetaAt + key] & 2 : 0; };
   // ---- copies of a tile: eight lanes a key, so that they cover 128 bytes of its row
   const int rows = p.g.n_blocks << p.g.lb;
+  const int piece = tid & 7;
+  const uint8_t* const k_from = p.k8 + kvh * (DQK / 2) + piece * 16;
+  const uint8_t* const v_from = SEP ? p.v8 + kvh * (DV / 2) + piece * 16 : nullptr;
   auto copy_tile = [&](int i, int stage) {
     const uint32_t st = base + N::kStages + stage * N::kStage;
-    const int piece = tid & 7;
+    const int* ring = row_ring + (i & (kRowRing - 1)) * kTile;
 #pragma unroll
     for (int s = 0; s < kTile / (kBlock / 8); ++s) {
       const int key = (tid >> 3) + s * (kBlock / 8);
-      const int row = i < i1 ? row_ring[(i & (kRowRing - 1)) * kTile + key] : -1;
+      const int row = i < i1 ? ring[key] : -1;
       const bool any = row >= 0 && dsa::check(row < rows, p.status);
-      const int64_t at = static_cast<int64_t>(any ? row : 0) * p.Hc + kvh;
-      const uint32_t n = any ? 16u : 0u, to = st + key * N::kKPitch, sc = st + N::kScaleAt + key * 32;
-      const uint8_t* src = p.k8 + at * (DQK / 2);
+      const int64_t r = any ? row : 0;
+      const uint32_t n = any ? 16u : 0u, to = st + key * N::kKPitch + piece * 16, sc = st + N::kScaleAt + key * 32;
+      const uint8_t* src = k_from + r * (p.Hc * (DQK / 2));
 #pragma unroll
-      for (int m = 0; m < DQK / 256; ++m) cp_async16(to + (piece + 8 * m) * 16, src + (piece + 8 * m) * 16, n);
-      if (SEP) cp_async16(st + N::kVAt + key * N::kVPitch + piece * 16, p.v8 + at * (DV / 2) + piece * 16, n);
+      for (int m = 0; m < DQK / 256; ++m) cp_async16(to + m * 128, src + m * 128, n);
+      if (SEP) cp_async16(st + N::kVAt + key * N::kVPitch + piece * 16, v_from + r * (p.Hc * (DV / 2)), n);
       uint32_t meta = any ? 1u : 0u;
       if (DQK == 576) {
-        if (piece < 2) cp_async16(to + (16 + piece) * 16, src + (16 + piece) * 16, n);
+        if (piece < 2) cp_async16(to + 256, src + 256, n);
         // 18 bytes from an even place on: the words that hold them, of the last one only what belongs to the row
-        const int64_t first = at * 18;
+        const int64_t first = (r * p.Hc + kvh) * 18;
         if (first & 2) meta |= 2u;
         const int need = (first & 2 ? 20 : 18) - (piece - 3) * 4;
         if (piece >= 3) cp_async4(sc + (piece - 3) * 4, p.k_exp + (first & ~int64_t{3}) + (piece - 3) * 4, any ? min(need, 4) : 0);
       } else if (DQK == 512) {
-        if (piece == 0) cp_async16(sc, p.k_exp + at * 16, n);
+        if (piece == 0) cp_async16(sc, p.k_exp + (r * p.Hc + kvh) * 16, n);
       } else {
-        if (piece == 0) cp_async8(sc, p.k_exp + at * 8, n / 2);
-        if (piece == 1) cp_async8(sc + 8, p.v_exp + at * 8, n / 2);
+        if (piece < 2) cp_async8(sc + piece * 8, (piece ? p.v_exp : p.k_exp) + (r * p.Hc + kvh) * 8, n / 2);
       }
       if (piece == 0) smem[N::kStages + stage * N::kStage + N::kMetaAt + key] = static_cast<uint8_t>(meta);
     }
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
   }
 
   // ---- state of the softmax: heads 16 m + g and 16 m + g + 8, the same in every warp
-  float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
+  float m_run[2] = {-INFINITY, -INFINITY}, m_max[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
   float acc[8][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -254,17 +265,17 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
     cp_async_wait<1>();  // this thread's copies of tile i
     __syncthreads();     // and everybody's (the first time: the query too)
     const uint8_t* st = smem + N::kStages + stage * N::kStage;
-    // rows of tile i + 3
-    put_row(i + 3, id_a, blk_a);
-    id_a = id_b;
-    blk_a = load_block(id_b);
-    id_b = load_id(i + 5);
+    if (DQK != 256 || tid < kTile) {  // rows of tile i + 3 (at more dims registers are short for the branch)
+      put_row(i + 3, id_a, blk_a);
+      id_a = id_b;
+      blk_a = load_block(id_b);
+      id_b = load_id(i + 5);
+    }
 
     // ---- scores of the warp's eight keys (column n of the products is key key_of(n))
     const int key0 = warp * 8;
     const uint8_t* key_at = st + (key0 + key_of(g)) * N::kKPitch;
-    const uint8_t meta = st[N::kMetaAt + key0 + key_of(g)];
-    const uint8_t* exp_at = st + N::kScaleAt + (key0 + key_of(g)) * 32 + (meta & 2);
+    const uint8_t* exp_at = st + N::kScaleAt + (key0 + key_of(g)) * 32 + shift_of(st, key0 + key_of(g));
     // of this lane's columns 2 c and 2 c + 1
     const bool valid[2] = {static_cast<bool>(st[N::kMetaAt + key0 + key_of(2 * c)] & 1),
                            static_cast<bool>(st[N::kMetaAt + key0 + key_of(2 * c + 1)] & 1)};
@@ -273,9 +284,10 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
 #pragma unroll
     for (int y = lane; y < 8 * N::kBlocksV; y += 32) {
       const int key = key0 + y / N::kBlocksV, blk = y % N::kBlocksV;
-      const uint32_t byte = st[N::kScaleAt + key * 32 + (st[N::kMetaAt + key] & 2) + (SEP ? 8 : 0) + blk];
+      const uint32_t byte = st[N::kScaleAt + key * 32 + shift_of(st, key) + (SEP ? 8 : 0) + blk];
       top_byte = max(top_byte, byte);
-      *reinterpret_cast<uint32_t*>(smem + N::kFactors + key * N::kFPitch + blk * 4) = dsa::mx_factor(byte);
+      *reinterpret_cast<uint16_t*>(smem + N::kFactors + blk * N::kFPitch + (key0 + place_of(y / N::kBlocksV)) * 2) =
+          static_cast<uint16_t>(dsa::mx_factor(byte));
     }
     constexpr int kSuper = DQK / 128;  // whole super-steps
     uint32_t byte[kSuper + 1];
@@ -314,7 +326,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
       }
     });
 
-    // ---- softmax: in powers of two, against the running maximum of each head
+    // ---- softmax: in powers of two, against a running reference of each head
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float mx = -INFINITY;
@@ -326,24 +338,35 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (c == 0) wmax[warp * N::kHeads + e * 8 + g] = mx;
+      if (c == 0) wmax[(e * 8 + g) * N::kWPitch + warp] = mx;
     }
     const bool all_direct = !__syncthreads_or(!direct);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float mx = m_run[e];
+      const float4 w0 = *reinterpret_cast<const float4*>(wmax + (e * 8 + g) * N::kWPitch);
+      const float4 w1 = *reinterpret_cast<const float4*>(wmax + (e * 8 + g) * N::kWPitch + 4);
+      m_max[e] = fmaxf(m_max[e], fmaxf(fmaxf(fmaxf(w0.x, w0.y), fmaxf(w0.z, w0.w)), fmaxf(fmaxf(w1.x, w1.y), fmaxf(w1.z, w1.w))));
+    }
+    if (__any_sync(0xffffffffu, m_max[0] > m_run[0] + kMove || m_max[1] > m_run[1] + kMove)) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wmax[w * N::kHeads + e * 8 + g]);
-      const float ref = mx == -INFINITY ? 0.f : mx;  // (no valid slot so far)
-      const float alpha = ex2(m_run[e] - ref);
-      m_run[e] = mx;
+      for (int e = 0; e < 2; ++e) {
+        if (m_max[e] > m_run[e] + kMove) {
+          const float alpha = ex2(m_run[e] - m_max[e]);
+          m_run[e] = m_max[e];
+          l_part[e] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j][2 * e] *= alpha, acc[j][2 * e + 1] *= alpha;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ref = m_run[e] == -INFINITY ? 0.f : m_run[e];  // (no valid slot so far)
       const float p0 = ex2(s_acc[2 * e] - ref), p1 = ex2(s_acc[2 * e + 1] - ref);
       __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(smem + N::kP + (e * 8 + g) * N::kPPitch) + key0;
       to[place_of(key_of(2 * c))] = __float2bfloat16_rn(p0);
       to[place_of(key_of(2 * c + 1))] = __float2bfloat16_rn(p1);
-      l_part[e] = fmaf(l_part[e], alpha, p0 + p1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j][2 * e] *= alpha, acc[j][2 * e + 1] *= alpha;
+      l_part[e] += p0 + p1;
     }
     __syncthreads();
 
@@ -351,39 +374,37 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
     constexpr int kSteps = kTile / 16 / N::kHalves;
     const int first = half * kSteps * 16 + c;
     const uint8_t* v0 = st + N::kVAt + first * N::kVPitch + slice * 32 + g * 4;
-    const uint32_t* f0 = reinterpret_cast<const uint32_t*>(smem + N::kFactors + first * N::kFPitch) + slice * 2 + (g >> 2);
+    const uint8_t* f0 = smem + N::kFactors + (slice * 2 + (g >> 2)) * N::kFPitch + (half * kSteps * 16 + 2 * c) * 2;
     const uint32_t p_addr = base + N::kP + ((lane & 7) + 8 * ((lane >> 3) & 1)) * N::kPPitch + (half * kSteps * 16 + (lane >> 4) * 8) * 2;
     with_direct(all_direct, [&](auto d) {
-      uint32_t w[4], f[4];  // of the next step: keys c, c + 4, c + 8, c + 12 of its sixteen
+      uint32_t w[4], f[2];  // of the next step: keys c, c + 4, c + 8, c + 12 of its sixteen
       auto load = [&](int k) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          w[y] = *reinterpret_cast<const uint32_t*>(v0 + (k * 16 + 4 * y) * N::kVPitch);
-          f[y] = f0[(k * 16 + 4 * y) * (N::kFPitch / 4)];
-        }
+        for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint32_t*>(v0 + (k * 16 + 4 * y) * N::kVPitch);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) f[y] = *reinterpret_cast<const uint32_t*>(f0 + (k * 16 + 8 * y) * 2);
       };
       load(0);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        uint32_t a[4], x[4][4];
+        uint32_t a[4], x[2][2][4];  // of two keys: dims 0..3 and 4..7, the first key's in the low half
         ldmatrix4(a, p_addr + k * 32);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < 2; ++y) {
           uint32_t f2 = 0;
           if (!decltype(d)::value) {
-            const int key = first + k * 16 + 4 * y;
-            f2 = dsa::mx_second(st[N::kScaleAt + key * 32 + (st[N::kMetaAt + key] & 2) + (SEP ? 8 : 0) + slice * 2 + (g >> 2)]);
+            auto second = [&](int key) {
+              return dsa::mx_second(st[N::kScaleAt + key * 32 + shift_of(st, key) + (SEP ? 8 : 0) + slice * 2 + (g >> 2)]);
+            };
+            const int key = first + k * 16 + 8 * y;
+            f2 = __byte_perm(second(key), second(key + 4), 0x5410);
           }
-          widen_word<decltype(d)::value>(w[y], f[y], f2, x[y]);
+          widen_word<decltype(d)::value>(__byte_perm(w[2 * y], w[2 * y + 1], 0x5410), f[y], f2, x[y][0]);
+          widen_word<decltype(d)::value>(__byte_perm(w[2 * y], w[2 * y + 1], 0x7632), f[y], f2, x[y][1]);
         }
         if (k + 1 < kSteps) load(k + 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo0 = __byte_perm(x[0][j], x[1][j], 0x5410), lo1 = __byte_perm(x[2][j], x[3][j], 0x5410);
-          const uint32_t hi0 = __byte_perm(x[0][j], x[1][j], 0x7632), hi1 = __byte_perm(x[2][j], x[3][j], 0x7632);
-          mma16816(acc[j], a, lo0, lo1);
-          mma16816(acc[j + 4], a, hi0, hi1);
-        }
+        for (int j = 0; j < 8; ++j) mma16816(acc[j], a, x[0][j >> 2][j & 3], x[1][j >> 2][j & 3]);
       }
     });
     __syncthreads();  // the stage is free
@@ -397,7 +418,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
     float l = l_part[e];
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (c == 0) wmax[warp * N::kHeads + e * 8 + g] = l;
+    if (c == 0) wmax[(e * 8 + g) * N::kWPitch + warp] = l;
   }
   __syncthreads();  // (and every thread's copies have ended)
   if constexpr (N::kHalves == 2) {
@@ -424,7 +445,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
       const int h = e * 8 + g;
       float l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) l += wmax[w * N::kHeads + h];
+      for (int w = 0; w < kWarps; ++w) l += wmax[h * N::kWPitch + w];
       if (h >= hv) continue;
       const float mc = m_run[e] == -INFINITY ? 0.f : m_run[e];
       const bool any = l != 0.f;  // true for NaN too
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
       float f = 0.f;
       if (split_up) {
         if (any) f = 1.f / l;  // a split's mean value, which stays in range where the sum might not
-        if (first) *reinterpret_cast<float4*>(smem + N::kStats + h * 16) = make_float4(mc, l, m_run[e], 0.f);
+        if (first) *reinterpret_cast<float4*>(smem + N::kStats + h * 16) = make_float4(mc, l, m_max[e], 0.f);
       } else {
         const float sink = p.sink ? __ldg(p.sink + h0 + h) : -INFINITY, sk = sink * kLog2e;
         float lse_v = sink, lkv = INFINITY;
@@ -447,7 +468,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
         if (first) {
           p.lse[orow + h] = lse_v;
           if (p.lse_kv) p.lse_kv[orow + h] = lkv;
-          if (p.max_logits) p.max_logits[orow + h] = any ? m_run[e] * kLn2 : -INFINITY;
+          if (p.max_logits) p.max_logits[orow + h] = any ? m_max[e] * kLn2 : -INFINITY;
         }
       }
       // this lane's dims: 64 slice + 8 (2c + k) + j
@@ -547,13 +568,13 @@ int launch_form(const Params& p, cudaStream_t stream) {
 namespace dsa {
 namespace kv4_attn {
 
-// Measured, in us, groups of 16 heads here against the tiles of 64 (rows x heads x slots):
-//   one row of 16 heads    2048 slots 12.8 / 15.8, 8192 27.5 / 21.4, 65,536 165 / 72:
-//                          sixteen CTAs a unit are all there are, the tiles' 32 splits win long rows
-//   one row of 64 heads    512 9.5 / 14.3, 2048 13.2 / 17.0 (four units); of 128 2048 18.7 / 17.3
-//   four rows of 64 heads  2048 24.6 / 17.9: a group's keys are widened once for 16 heads, there for 64
-//   rows of 16 heads       64 x 2048 41.1 / 40.8, 300 x 2048 162 / 131, 1024 x 512 119 / 135
-//   256 dims               96 x (2 x 12) x 1027 39.8 / 58.8, 1000 x 12 x 1027 168 / 193,
+// Measured, in us, groups of 16 heads here against the tiles of 64:
+//   one row of 16 heads    2048 slots 12.8 / 15.8, 8192 27.5 / 21.4, 65,536 165 / 72: sixteen CTAs a unit
+//                          are all there are, the tiles' 32 splits win long rows
+//   one row of 64 heads    512 9.3 / 14.3, 2048 13.0 / 17.0 (four units); of 128 heads 2048 18.7 / 17.3
+//   four rows of 64 heads  2048 24.6 / 17.7: a key is widened once for 16 heads here, there for 64
+//   rows of 16 heads       64 x 2048 39.4 / 40.8, 300 x 2048 160 / 132, 1024 x 512 114 / 135
+//   256 dims               96 x (2 x 12) x 1027 36.9 / 58.8, 1000 x 12 x 1027 155 / 193,
 //                          16 x 32 x 1027 15.4 / 14.2
 bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
   const int64_t units = static_cast<int64_t>(T) * Hc * ((H / Hc + 15) / 16);
@@ -567,7 +588,7 @@ constexpr int kItemTiles = 2;
 
 // A power of two, at most a cluster's CTAs: the fewest waves of (tiles of an item + kItemTiles), with
 // kPerSm = 3 as most forms have it; of equal ones the fewest splits.  96 rows of 2 x 12 heads, 1027 slots:
-// two splits 41 us, four 48; one row of 16 heads, 2048 slots: sixteen.
+// two splits 41 us, four 48 (and now 37 with two); one row of 16 heads, 2048 slots: sixteen.
 int narrow_splits(int64_t units, int K) {
   const int nt = (K + kTile - 1) / kTile, slots = 3 * kv8_attn::kPlanSms;
   int best = 1;
