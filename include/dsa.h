@@ -718,8 +718,8 @@ int dsa_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t 
  *   dweight[c] = sum_t dy[t, c] * xh[t, c].
  *   dx bf16 (out): the gradient of x and of the residual alike; may be dy, x or
  *   d_sum itself (same rows, same stride); dweight fp32 [D] (out) or NULL.
- *   workspace: dsa_rms_norm_bwd_workspace_size(T, D) bytes, 256-byte aligned; not needed
- *   without dweight.  Sums are fp32 in a fixed order: bitwise reproducible.
+ *   workspace: dsa_rms_norm_bwd_workspace_size(T, D) bytes, 256-byte aligned, contents ignored on
+ *   entry; not needed without dweight; calls that may overlap need one each.  Sums are fp32 in a fixed order: bitwise reproducible.
  * Shapes as the forward's bf16 form.  Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
 size_t dsa_rms_norm_bwd_workspace_size(int T, int D);
 int dsa_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const float* weight,
@@ -733,7 +733,8 @@ int dsa_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
  * with inverse != 0 by the angle -p f_i: the adjoint, which takes the gradient of the
  * result to that of the input.
  *   x bf16, row (t, h) at x + t * x_token + h * x_head; y (out) likewise, x itself
- *   (same strides) or apart from it; x2, y2 the same with H2 heads (H2 = 0: ignored).
+ *   (same strides) or apart from it; x2, y2 the same with H2 heads (H2 = 0: ignored).  y and
+ *   y2 have no value in common, and neither is the other tensor's input.
  *   Part of a head is rotated by passing that part: nothing beside the R values is read or written.
  *   inv_freq fp64 [R / 2], device: f_i, e.g. from dsa_rotary_inv_freq.
  *   Position of token t of sequence b (cu_seqlens int32 [n_seqs + 1], as in the block

@@ -12,7 +12,7 @@
 // A CTA works out its tokens' cosines and sines once, for all their heads, while the first loads
 // are under way.  The rows' bytes bound it: 16,384 tokens of 64 + 1 rows of 64, halves, 272 MB, take
 // 45 us (6.1 TB/s), pairs 47; rows that are the last 64 of 576 the same 48 and 50; 4096 tokens of
-// 24 + 2 heads of 256 21 us (5.2 TB/s).  64 tokens take 3.4 us: the chain from the sequence's
+// 24 + 1 heads of 256 21 us (4.9 TB/s).  64 tokens take 3.4 us: the chain from the sequence's
 // offsets to the angles, not the bytes.
 #include <algorithm>
 #include <climits>
