@@ -99,7 +99,7 @@ struct AttnParams {
   int p_alias;   // chunk whose space holds P^T, or -1 (separate buffers)
   int kv_row_bytes, v_row_bytes;
   float scale_log2;
-  const int32_t* t_end;  // or NULL: rows from *t_end on are left alone
+  const int32_t* t_end;  // or NULL: rows from *t_end on, which have no slots, are left alone
 };
 
 struct Layout {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.misc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_units = (p.t_end ? max(0, min(p.T, __ldg(p.t_end))) : p.T) * p.G;
+  const int n_units = p.T * p.G;
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = (len + kKeys - 1) / kKeys;
       const int64_t orow = static_cast<int64_t>(t) * p.H + g * kHG;
       if (nt == 0) {
+        if (p.t_end && t >= __ldg(p.t_end)) continue;
         for (int h = 0; h < hv; ++h)
           for (int d = st; d < p.Dv; d += kSoftThreads) p.out[(orow + h) * p.Dv + d] = __float2bfloat16_rn(0.f);
         if (st < hv) {

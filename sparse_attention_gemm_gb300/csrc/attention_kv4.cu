@@ -15,7 +15,7 @@
 // * narrow: groups of 16 heads, warp products (attention_kv4_narrow.cu).
 // * widened: a cache whose rows are read often is written out in bf16 once and the call is the
 //   bf16 one (attention.cu), which such a call comes close to: the same 2048 rows over 16,384 cache rows
-//   703 us, 831 TFLOP/s, of which widening takes 4 and the positions' rows 10.
+//   681 us, 857 TFLOP/s, of which widening takes 4 and the positions' rows 10.
 #include "attention_cache.cuh"
 #include "attention_kv4.cuh"
 
@@ -158,12 +158,15 @@ __global__ void __launch_bounds__(kWideThreads) kv4_widen_kernel(const uint32_t*
   }
 }
 
-// Cache rows of positions: one CTA a query row, whose sequence each warp looks up.  Eight ids of a
+// Cache rows of positions and the rows' lengths, 0 for padding: one CTA a query row, whose sequence each warp looks up.  Eight ids of a
 // thread are under way at a time: their pages are loads that wait for loads.
 __global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* __restrict__ idx, const dsa::Kv8Geom g, int K,
-                                                                int32_t* __restrict__ rows) {
+                                                                const int32_t* __restrict__ topk_length,
+                                                                int32_t* __restrict__ rows, int32_t* __restrict__ length) {
   const int t = blockIdx.x;
-  if (t >= __ldg(g.cu + g.n_seqs)) return;
+  const bool padding = t >= __ldg(g.cu + g.n_seqs);
+  if (threadIdx.x == 0) length[t] = padding ? 0 : topk_length ? __ldg(topk_length + t) : K;
+  if (padding) return;
   const int b = dsa::kv8_seq_warp(g.cu, g.n_seqs, t);
   const int64_t at = static_cast<int64_t>(t) * K;
   constexpr int kAhead = 8;
@@ -185,17 +188,17 @@ __global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* _
 }
 
 struct WideSizes {
-  size_t k, v, rows;  // bytes of the widened keys, the values and the ids
+  size_t k, v, rows, length;  // bytes of the widened keys, the values, the ids and the rows' lengths
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 WideSizes widened_sizes(int T, int Dqk, int Dv, int K, int64_t cache_rows, bool paged) {
   return WideSizes{up256(static_cast<size_t>(cache_rows) * Dqk * 2), Dqk == 256 ? up256(static_cast<size_t>(cache_rows) * Dv * 2) : 0,
-                   paged ? up256(static_cast<size_t>(T) * K * 4) : 0};
+                   paged ? up256(static_cast<size_t>(T) * K * 4) : 0, paged ? up256(static_cast<size_t>(T) * 4) : 0};
 }
 
 // Whether the cache is widened once for the call.  Measured (576 dims, 64 heads): the tiles' own
 // conversion costs 0.05 ns a slot and group of 64 heads over the bf16 kernel (2048 rows of 2048 slots 889 us
-// against 703), widening 0.27 ns a cache row and the launches 8 us; taken where the first is
+// against 681), widening 0.27 ns a cache row and the launches 8 us; taken where the first is
 // twice the second, for a widened cache of at most 2^30 bytes.
 bool widens(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows) {
   const double slots = static_cast<double>(T) * K * ((H + kHG - 1) / kHG);
@@ -215,15 +218,16 @@ int launch_widened(const Params& p, const void* q, int T, int Dqk, int Dv, float
   };
   int rc = widen(p.k8, p.k_exp, Dqk, ws);
   if (rc == DSA_OK && separate) rc = widen(p.v8, p.v_exp, Dv, ws + size.k);
-  const int32_t* rows = p.idx;
+  const int32_t *rows = p.idx, *length = p.topk_length;
   if (rc == DSA_OK && paged) {
     auto* to = reinterpret_cast<int32_t*>(ws + size.k + size.v);
-    kv4_rows_kernel<<<T, kWideThreads, 0, stream>>>(p.idx, p.g, p.K, to);
+    auto* len = reinterpret_cast<int32_t*>(ws + size.k + size.v + size.rows);
+    kv4_rows_kernel<<<T, kWideThreads, 0, stream>>>(p.idx, p.g, p.K, p.topk_length, to, len);
     rc = dsa::launch_error("kv4_rows_kernel");
-    rows = to;
+    rows = to, length = len;
   }
   if (rc != DSA_OK) return rc;
-  return dsa::sparse_attn_launch(q, ws, separate ? ws + size.k : nullptr, rows, p.topk_length, p.sink, T, static_cast<int>(cache_rows),
+  return dsa::sparse_attn_launch(q, ws, separate ? ws + size.k : nullptr, rows, length, p.sink, T, static_cast<int>(cache_rows),
                                  p.H, Dqk, Dv, p.K, scale, p.out, p.lse, p.lse_kv, p.max_logits, 0, nullptr,
                                  paged ? p.g.cu + p.g.n_seqs : nullptr, sms, stream);
 }
@@ -239,7 +243,7 @@ Plan plan_of(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows, b
     return Plan{Plan::kNarrow, 16, dsa::kv4_attn::narrow_splits(units_of(T, H, Hc, 16), K), 0};
   if (widens(T, H, Hc, Dqk, Dv, K, cache_rows)) {
     const WideSizes s = widened_sizes(T, Dqk, Dv, K, cache_rows, paged);
-    return Plan{Plan::kWidened, kHG, 1, s.k + s.v + s.rows};
+    return Plan{Plan::kWidened, kHG, 1, s.k + s.v + s.rows + s.length};
   }
   const int s = plan_splits(units_of(T, H, Hc, kHG), K);
   return Plan{Plan::kTiles, kHG, s, s == 1 ? 0 : part_bytes(T, H, s) + static_cast<size_t>(T) * H * s * Dv * sizeof(float)};

@@ -6,7 +6,8 @@
 
 namespace dsa {
 
-// The attention over bf16 rows (attention.cu) of a call whose arguments are checked; rows from *t_end on are left alone.
+// The attention over bf16 rows (attention.cu) of a call whose arguments are checked.  t_end: NULL, or rows from
+// *t_end on are left alone; their topk_length is 0 (asked in the loops of all rows the end cost the bf16 call 2%).
 int sparse_attn_launch(const void* q, const void* kv, const void* v, const int32_t* idx, const int32_t* topk_length,
                        const float* sink, int T, int Tkv, int H, int Dqk, int Dv, int K, float scale, void* out, float* lse,
                        float* lse_kv, float* max_logits, int indexer_topk, float* lse_indexer, const int32_t* t_end, int sms,
