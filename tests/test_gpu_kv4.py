@@ -2,6 +2,7 @@
 bit, untouched bytes included), reading back (bit for bit) and sparse attention over
 it (within bounds that kv4_ref derives per element)."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -515,6 +516,54 @@ def test_captured_steps_with_their_own_workspaces():
             out, lse = st["res"]["out"].clone(), st["res"]["lse"].clone()
             eager = step()
             assert torch.equal(out, eager["out"]) and torch.equal(lse, eager["lse"])
+
+
+def test_threads_with_streams_of_their_own():
+    """Calls of several host threads at once, each on a stream of its own: the results of one after another."""
+    rng = np.random.default_rng(43)
+    f, _ = ops.rotary_inv_freq(64)
+    calls = []
+    for T, H, heads, K, d, v in ((3, 128, 1, 900, 576, 512), (1, 16, 1, 2048, 512, 512), (30, 12, 1, 300, 256, 256),
+                                 (400, 64, 1, 1024, 576, 512), (2, 64, 1, 7000, 576, 512)):
+        q, k, ks, idx, sm, kw = attention_case(rng, d, v, T, H, heads, K, 32, T == 400, n=2000, holes=False)
+        args = (dev_bf16(q), dev(k), dev(ks), dev(idx), sm)
+        kw = {("cu_seqlens" if n == "cu" else "block_table" if n == "table" else n): dev(a) for n, a in kw.items()}
+        x, g = dev_bf16(rows(rng, 500, 1, 264))[:, 0], dev_bf16(rows(rng, 500, 1, 264))[:, 0]
+        w, cu = torch.ones(264, device=DEV), dev(cu_from_lengths([100, 400]))
+        turned = dev_bf16(rows(rng, 500, 9, 64))
+
+        def call(args=args, kw=kw, x=x, g=g, w=w, cu=cu, turned=turned):
+            a = ops.sparse_attn_fwd_kv4(*args, **kw)
+            n = ops.rms_norm_fwd(x, w, 1e-6, residual=g, want_rstd=True)
+            b = ops.rms_norm_bwd(g, n["sum"], w, n["rstd"])
+            r = ops.rotary(turned, f, cu, x2=turned[:, :1])
+            c, s = torch.zeros(8, 64, 9, 32, dtype=torch.uint8, device=DEV), torch.zeros(8, 64, 9, 2, dtype=torch.uint8, device=DEV)
+            ops.kv4_write(r[0], c, s, cu)
+            return [a["out"], a["lse"], n["out"], b["dx"], b["dweight"], r[0], r[1], c, s, ops.kv4_read(c, s, cu, 500)]
+        calls.append(call)
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for r in range(12):
+                    j = (i + r) % len(calls)
+                    got = calls[j]()
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[j])):
+                        failed.append((i, r, j))
+        except Exception as e:  # (reported by the test's own thread)
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
 
 
 def test_a_layers_step_together():
