@@ -899,13 +899,13 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
 // One row of 64 heads, 65536 slots: 1696, 854, 432, 221, 117, and 66 with 32.
 constexpr int kItemTiles = 6, kJoinTiles = 5;
 
-inline int plan_splits(int64_t units, int K) {
+inline int plan_splits(int64_t units, int K, int join_tiles = kJoinTiles) {
   const int nt = (K + kKeys - 1) / kKeys;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= kMaxSplits && s <= nt; ++s) {
     const int64_t waves = (units * s + kPlanSms - 1) / kPlanSms;
-    const int64_t c = 16 * (waves * ((nt + s - 1) / s + kItemTiles) + (s > 1 ? kJoinTiles : 0)) + (s > 1 ? s : 0);
+    const int64_t c = 16 * (waves * ((nt + s - 1) / s + kItemTiles) + (s > 1 ? join_tiles : 0)) + (s > 1 ? s : 0);
     if (c < cost) cost = c, best = s;
   }
   return best;

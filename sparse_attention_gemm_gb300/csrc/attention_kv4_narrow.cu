@@ -24,6 +24,8 @@
 //
 // Work item = (token, KV head, group of 16 heads, split of its slots); a row's splits are the CTAs of a
 // cluster and are joined there: no workspace, no second launch, nothing that waits on another cluster.
+#include <algorithm>
+
 #include "attention_kv4.cuh"
 
 namespace {
@@ -568,37 +570,56 @@ int launch_form(const Params& p, cudaStream_t stream) {
 namespace dsa {
 namespace kv4_attn {
 
-// Measured, in us, groups of 16 heads here against the tiles of 64:
-//   one row of 16 heads    2048 slots 12.8 / 15.8, 8192 27.5 / 21.4, 65,536 165 / 72: sixteen CTAs a unit
-//                          are all there are, the tiles' 32 splits win long rows
-//   one row of 64 heads    512 9.3 / 14.3, 2048 13.0 / 17.0 (four units); of 128 heads 2048 18.7 / 17.3
-//   four rows of 64 heads  2048 24.6 / 17.7: a key is widened once for 16 heads here, there for 64
-//   rows of 16 heads       64 x 2048 39.4 / 40.8, 300 x 2048 160 / 132, 1024 x 512 114 / 135
-//   256 dims               96 x (2 x 12) x 1027 36.9 / 58.8, 1000 x 12 x 1027 155 / 193,
-//                          16 x 32 x 1027 15.4 / 14.2
+// Clusters of 1 to 16 CTAs that are resident at once, with three CTAs an SM, as the runtime's occupancy query
+// says (a cluster stays within a group of SMs).
+constexpr int kResident[kMaxCluster] = {456, 228, 148, 110, 87, 74, 59, 51, 46, 43, 36, 36, 28, 26, 26, 21};
+
+// A call's time with s splits a row, in tenths of what a tile takes on a busy SM (1.65 us at 576 dims, 1.0 at 256).  Items of
+// one SM take their tiles more or less one after the other, so layers of one CTA an SM count; a tile takes 1.45 times as
+// long where there is one and 1.15 where there are two, and items that are not resident at once cost a
+// tenth more (96 rows of 2 x 12 heads with shorter and longer contexts: 37.6 us with two splits, 44.8 with three).  An item is its tiles and 1.1 for the query and
+// the results, 0.3 for its part of a join, whose latency is 2.1.  Measured, 576 dims (1.7 us beside it): one to three
+// tiles 6.8, 9.4, 11.8 us in one layer, 9.7, 13.4, 17.3 in two; sixteen splits of two tiles 12.8, 17.6, 23.5 in one to
+// three; 100 rows of 22 tiles 57.6 us in one layer, 43.7 with four splits.
+int64_t cost_of(int64_t units, int nt, int s) {
+  const int64_t layers = (3 * units + kResident[s - 1] - 1) / kResident[s - 1];
+  const int64_t item = 10 * ((nt + s - 1) / s) + (s > 1 ? 14 : 11);
+  return layers * item * (layers == 1 ? 29 : layers == 2 ? 23 : layers == 3 ? 20 : 22) / 20 + (s > 1 ? 21 : 0);
+}
+int best_splits(int64_t units, int K, int64_t* cost) {
+  const int nt = (K + kTile - 1) / kTile;
+  int best = 1;
+  *cost = INT64_MAX;
+  for (int s = 1; s <= kMaxCluster && s <= nt; ++s) {
+    const int64_t c = cost_of(units, nt, s);
+    if (c < *cost) *cost = c, best = s;
+  }
+  return best;
+}
+
+// Where groups of 16 heads take less time than the tiles of 64.  Measured, in us, here / there, 576 dims:
+//   slots                  64          180          350          700         1400         2048
+//   1 row of 64 heads   6.8 / 11.3   9.7 / 14.8  10.5 / 14.6  10.3 / 15.6  12.5 / 17.1  13.0 / 17.2
+//   10 rows             6.8 / 11.3  10.1 / 14.8  12.6 / 15.2  17.5 / 16.7  25.0 / 18.4  33.1 / 20.1
+//   40 rows             9.5 / 11.5  17.1 / 14.8  27.3 / 19.0  44.2 / 22.8  72.1 / 29.8  89.2 / 35.1
+//   16 rows of 16 heads 7.0 / 10.5   9.9 / 14.0  10.7 / 14.2  13.2 / 16.0  20.3 / 17.7  23.9 / 19.7
+//   100 rows            7.0 / 10.9  11.9 / 14.4  19.1 / 19.9  27.3 / 28.7  43.7 / 48.8  55.0 / 62.1
+// (a key is widened once for 16 heads here, there for 64; tiles a quarter full cost what full ones do).  300 rows
+// of 16 heads x 2048 slots 160 / 132; one of 8192 slots 27.5 / 21.4, of 65,536 165 / 72: sixteen CTAs a unit are all there
+// are.  256 dims: 96 rows of 2 x 12 heads x 1027 slots 37 / 59, 1000 of 12 135 / 193, 16 of 64 heads x 700 14.6 / 14.0.
 bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
   const int64_t units = static_cast<int64_t>(T) * Hc * ((H / Hc + 15) / 16);
   if (units * kMaxCluster < kv8_attn::kPlanSms && K > 6144) return false;
-  if (units <= 4) return true;
-  return H / Hc <= 16 && (Dqk == 256 || K <= 1024 || units <= 64);
+  if (H / Hc <= 16 && (Dqk == 256 || K <= 1024 || (units >= 24 && units <= 100))) return true;
+  const int nt = (K + kTile - 1) / kTile;
+  int64_t cost;
+  best_splits(units, K, &cost);
+  return cost <= 50 + 10 * std::min(nt, 3) + std::min(std::max(nt - 3, 0), 12) * 5 / 4;
 }
 
-// The time of a work item besides its tiles, in tiles: the query's way and the join.
-constexpr int kItemTiles = 2;
-
-// A power of two, at most a cluster's CTAs: the fewest waves of (tiles of an item + kItemTiles), with
-// kPerSm = 3 as most forms have it; of equal ones the fewest splits.  96 rows of 2 x 12 heads, 1027 slots:
-// two splits 41 us, four 48 (and now 37 with two); one row of 16 heads, 2048 slots: sixteen.
 int narrow_splits(int64_t units, int K) {
-  const int nt = (K + kTile - 1) / kTile, slots = 3 * kv8_attn::kPlanSms;
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  for (int s = 1; s <= kMaxCluster && s <= nt; s *= 2) {
-    const int64_t waves = (units * s + slots - 1) / slots;
-    const int64_t c = 16 * waves * ((nt + s - 1) / s + kItemTiles) + s;
-    if (c < cost) cost = c, best = s;
-  }
-  return best;
+  int64_t cost;
+  return best_splits(units, K, &cost);
 }
 
 int launch_narrow(const kv8_attn::Params& p, int T, int Dqk, cudaStream_t stream) {

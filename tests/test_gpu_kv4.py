@@ -251,23 +251,45 @@ def test_attention_long_rows_of_few_heads(dqk, dv, T, H, K, table):
     check_attention(q, k, ks, idx, sm, sink=rng.standard_normal(H).astype(np.float32), **kw)
 
 
+# (110 rows of more than 16 heads: groups of 64 heads, whole; a dozen of many slots: the same in splits)
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,heads,K,block,table,sink", [
+    (110, 100, 1, 150, 16, True, True),
+    (90, 48, 1, 350, 64, False, True),
+    (60, 130, 2, 200, 4, True, False),
+    (160, 64, 1, 64, 32, True, True),
+    (40, 64, 1, 350, 16, True, False),
+    (12, 128, 1, 1500, 64, True, True),
+    (9, 40, 1, 2000, 1, False, False),
+    (50, 17, 1, 65, 1, False, True),
+    (170, 17, 1, 1, 1, False, True),
+])
+def test_attention_in_groups_of_64(dqk, dv, T, H, heads, K, block, table, sink):
+    rng = np.random.default_rng(T * 1000 + H + K + dqk)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, heads, K, block, table)
+    if sink:
+        kw["sink"] = rng.standard_normal(H).astype(np.float32)
+    check_attention(q, k, ks, idx, sm, **kw)
+
+
+@pytest.mark.parametrize("T,H", [(6, 12), (110, 64), (10, 128)])
 @pytest.mark.parametrize("lo,hi", [(-60, -50), (-30, 4), (40, 60), (-100, 60), (-126, -90)])
-def test_attention_values_of_every_size(lo, hi):
+def test_attention_values_of_every_size(lo, hi, T, H):
     """Value scales that differ by many powers of two (keys of one size, so that scores stay finite)."""
     rng = np.random.default_rng(200 + hi)
-    q, k, ks, idx, sm, kw = attention_case(rng, 256, 256, 6, 12, 1, 200, 4, False, holes=False)
+    q, k, ks, idx, sm, kw = attention_case(rng, 256, 256, T, H, 1, 1500 if T == 10 else 200, 4, False, holes=False)
     kw["v_scale"] = (rng.integers(lo, hi + 1, kw["v_scale"].shape) + 127).astype(np.uint8)
     check_attention(q, k, ks, idx, sm, **kw)
 
 
 @pytest.mark.parametrize("dqk,dv", FORMS)
-@pytest.mark.parametrize("H", [12, 64])
-def test_attention_rising_and_falling_scores(dqk, dv, H):
+@pytest.mark.parametrize("T,H,K", [(4, 12, 512), (4, 64, 512), (100, 64, 512), (12, 64, 1500)])
+def test_attention_rising_and_falling_scores(dqk, dv, T, H, K):
     """The running maximum moves in many tiles: keys in order of their scores, up and down."""
     rng = np.random.default_rng(dqk)
-    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, 4, H, 1, 512, 1, False, holes=False)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 1, False, holes=False)
     s = f64(q)[:, 0] @ R.values(k[:, 0, 0], ks[:, 0, 0]).T
-    for t in range(4):
+    for t in range(T):
         order = np.argsort(s[t])[:: 1 if t % 2 else -1]
         idx[t] = order[np.linspace(0, order.size - 1, idx.shape[1]).astype(int)]
     check_attention(q, k, ks, idx, 4 * sm, **kw)
@@ -276,8 +298,8 @@ def test_attention_rising_and_falling_scores(dqk, dv, H):
 def test_attention_peaked_row():
     """One key far above the rest whose value is tiny, the others' large: nothing of the small weights is lost."""
     rng = np.random.default_rng(90)
-    for H in (12, 64):
-        q, k, ks, idx, sm, kw = attention_case(rng, 256, 256, 3, H, 1, 150, 1, False, holes=False)
+    for T, H in ((3, 12), (3, 64), (130, 64)):
+        q, k, ks, idx, sm, kw = attention_case(rng, 256, 256, T, H, 1, 150, 1, False, holes=False)
         q[:] = W.f32_to_bf16_bits(np.ones(q.shape, np.float32))
         k[:], ks[:] = 0, 127
         k[5] = 0x22                    # the value 1 in every element: a score of 256 sm = 16
@@ -289,13 +311,13 @@ def test_attention_peaked_row():
 
 
 @pytest.mark.parametrize("dqk,dv", FORMS)
-@pytest.mark.parametrize("H", [20, 60])
-def test_attention_never_uses_unselected_rows(dqk, dv, H):
+@pytest.mark.parametrize("T,H", [(6, 20), (6, 60), (120, 60)])
+def test_attention_never_uses_unselected_rows(dqk, dv, T, H):
     """NaN scales in rows that no valid slot names, the slots behind topk_length among them."""
     rng = np.random.default_rng(dqk + 3)
-    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, 6, H, 1, 90, 1, False, n=400)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, 90, 1, False, n=400 if T == 6 else 12000)
     used = np.zeros(k.shape[0], bool)
-    for t in range(6):
+    for t in range(T):
         i = idx[t, :max(0, min(int(kw["length"][t]), 90))]
         used[i[(i >= 0) & (i < k.shape[0])]] = True
     assert not used.all()
@@ -310,11 +332,11 @@ def test_attention_never_uses_unselected_rows(dqk, dv, H):
     assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
 
 
-@pytest.mark.parametrize("H", [16, 64])
-def test_attention_nan_reaches_only_its_rows(H):
+@pytest.mark.parametrize("T,H", [(4, 16), (4, 64), (130, 64)])
+def test_attention_nan_reaches_only_its_rows(T, H):
     """A NaN scale in a selected row, and a query head with NaN or infinity, give NaN there and nowhere else."""
     rng = np.random.default_rng(21)
-    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, 4, H, 1, 70, 1, False, holes=False)
+    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, T, H, 1, 70, 1, False, holes=False)
     hit = idx[0, 5]
     idx[1:][idx[1:] == hit] = (hit + 1) % k.shape[0]
     clean = ops.sparse_attn_fwd_kv4(dev_bf16(q), dev(k), dev(ks), dev(idx), sm)["out"]
@@ -325,16 +347,16 @@ def test_attention_nan_reaches_only_its_rows(H):
     q2 = dev_bf16(q)
     q2[2, 7, 3], q2[3, 9, 500] = float("nan"), float("inf")
     got = ops.sparse_attn_fwd_kv4(q2, dev(k), dev(ks), dev(idx), sm)["out"]
-    hit = torch.zeros(4, H, dtype=torch.bool, device=DEV)
+    hit = torch.zeros(T, H, dtype=torch.bool, device=DEV)
     hit[2, 7] = hit[3, 9] = True
     assert bool(got[hit].isnan().all()) and torch.equal(got[~hit], clean[~hit])
 
 
-@pytest.mark.parametrize("H", [16, 64])
-def test_attention_is_that_of_the_bf16_call_on_values_read_back(H):
+@pytest.mark.parametrize("T,H", [(30, 16), (30, 64), (130, 64)])
+def test_attention_is_that_of_the_bf16_call_on_values_read_back(T, H):
     """The cache's values are bf16 ones: both calls round weights (2^-8) and out (2^-8), nothing else."""
     rng = np.random.default_rng(30)
-    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, 30, H, 1, 200, 16, False)
+    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, T, H, 1, 200, 16, False)
     n = k.shape[0] * 16
     kv = ops.kv4_read(dev(k), dev(ks), dev(cu_from_lengths([n])), n).view(n, 576)
     a = ops.sparse_attn_fwd_kv4(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, topk_length=dev(kw["length"]))
@@ -355,12 +377,12 @@ def test_attention_offsets_beyond_32_bits():
     at = [0, 1, n_blocks - 2, n_blocks - 1]
     for i, b in enumerate(at):
         cache[b], scale[b] = dev(k[i]), dev(ks[i])
-    idx = rng.integers(0, 4 * block, (3, 150)).astype(np.int32)
+    idx = rng.integers(0, 4 * block, (130, 150)).astype(np.int32)
     far = (np.array(at)[idx // block] * block + idx % block).astype(np.int32)
-    for H in (16, 64):
-        q = dev_bf16(rand_bf16_bits(rng, (3, H, 576)))
-        a = ops.sparse_attn_fwd_kv4(q, cache, scale, dev(far), 0.04)
-        b = ops.sparse_attn_fwd_kv4(q, dev(k), dev(ks), dev(idx), 0.04)
+    for T, H in ((3, 16), (3, 64), (130, 64)):  # (groups of 16 heads, and of 64)
+        q = dev_bf16(rand_bf16_bits(rng, (T, H, 576)))
+        a = ops.sparse_attn_fwd_kv4(q, cache, scale, dev(far[:T]), 0.04)
+        b = ops.sparse_attn_fwd_kv4(q, dev(k), dev(ks), dev(idx[:T]), 0.04)
         assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
     table, pos = dev(np.array([at], np.int32)), dev(np.array([40], np.int32))
     cu = dev(cu_from_lengths([200]))
@@ -371,10 +393,10 @@ def test_attention_offsets_beyond_32_bits():
     assert torch.equal(ops.kv4_read(cache, scale, cu, 200, pos=pos, block_table=table), want)
 
 
-@pytest.mark.parametrize("H", [16, 128])
-def test_repeated_calls_give_the_same_bits(H):
+@pytest.mark.parametrize("T,H", [(33, 16), (33, 128), (150, 128)])
+def test_repeated_calls_give_the_same_bits(T, H):
     rng = np.random.default_rng(32)
-    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, 33, H, 1, 300, 16, False)
+    q, k, ks, idx, sm, kw = attention_case(rng, 576, 512, T, H, 1, 300, 16, False)
     a = [dev_bf16(q), dev(k), dev(ks), dev(idx), sm]
     first = ops.sparse_attn_fwd_kv4(*a, topk_length=dev(kw["length"]))
     for _ in range(20):
