@@ -6,7 +6,7 @@
 // attention_cache.cuh run on it as on a bf16 cache: the roundings are those of the bf16
 // call.  A row of 576 comes as 306 bytes.
 //
-// Three forms, by rules on the call's sizes (narrow_takes, widens):
+// Three forms, by rules on the call's sizes (narrow_splits, widens):
 // * tiles: groups of 64 heads, each row's codes widened on their way (attention_cache.cuh).
 //   2048 rows of 64 heads, 2048 slots, 576 dims: 889 us, 657 TFLOP/s.  The gather bounds it: a
 //   warp's conversion of its part of a tile takes 1.5K cycles and its loads' issue 1.8K, where the products take 2.2K.
@@ -243,8 +243,7 @@ struct Plan {
   size_t bytes;
 };
 Plan plan_of(int T, int H, int Hc, int Dqk, int Dv, int K, int64_t cache_rows, bool paged) {
-  if (dsa::kv4_attn::narrow_takes(T, H, Hc, Dqk, K))
-    return Plan{Plan::kNarrow, 16, dsa::kv4_attn::narrow_splits(units_of(T, H, Hc, 16), K), 0};
+  if (const int n = dsa::kv4_attn::narrow_splits(T, H, Hc, Dqk, K)) return Plan{Plan::kNarrow, 16, n, 0};
   if (widens(T, H, Hc, Dqk, Dv, K, cache_rows)) {
     const WideSizes s = widened_sizes(T, Dqk, Dv, K, cache_rows, paged);
     return Plan{Plan::kWidened, kHG, 1, s.k + s.v + s.rows + s.length};

@@ -15,10 +15,9 @@ int sparse_attn_launch(const void* q, const void* kv, const void* v, const int32
 
 namespace kv4_attn {
 
-// Attention in groups of 16 heads (attention_kv4_narrow.cu): whether it takes a call, the splits of
-// a row's slots, and the launch.
-bool narrow_takes(int T, int H, int Hc, int Dqk, int K);
-int narrow_splits(int64_t units, int K);
+// Attention in groups of 16 heads (attention_kv4_narrow.cu): the splits of a row's slots in a call that it
+// takes, 0 in others, and the launch.
+int narrow_splits(int T, int H, int Hc, int Dqk, int K);
 int launch_narrow(const kv8_attn::Params& p, int T, int Dqk, cudaStream_t stream);
 
 }  // namespace kv4_attn

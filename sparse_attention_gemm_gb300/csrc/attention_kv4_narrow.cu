@@ -581,23 +581,13 @@ constexpr int kResident[kMaxCluster] = {456, 228, 148, 110, 87, 74, 59, 51, 46, 
 // the results, 0.3 for its part of a join, whose latency is 2.1.  Measured, 576 dims (1.7 us beside it): one to three
 // tiles 6.8, 9.4, 11.8 us in one layer, 9.7, 13.4, 17.3 in two; sixteen splits of two tiles 12.8, 17.6, 23.5 in one to
 // three; 100 rows of 22 tiles 57.6 us in one layer, 43.7 with four splits.
-int64_t cost_of(int64_t units, int nt, int s) {
+int64_t cost_of(int units, int nt, int s) {
   const int64_t layers = (3 * units + kResident[s - 1] - 1) / kResident[s - 1];
-  const int64_t item = 10 * ((nt + s - 1) / s) + (s > 1 ? 14 : 11);
+  const int item = 10 * ((nt + s - 1) / s) + (s > 1 ? 14 : 11);
   return layers * item * (layers == 1 ? 29 : layers == 2 ? 23 : layers == 3 ? 20 : 22) / 20 + (s > 1 ? 21 : 0);
 }
-int best_splits(int64_t units, int K, int64_t* cost) {
-  const int nt = (K + kTile - 1) / kTile;
-  int best = 1;
-  *cost = INT64_MAX;
-  for (int s = 1; s <= kMaxCluster && s <= nt; ++s) {
-    const int64_t c = cost_of(units, nt, s);
-    if (c < *cost) *cost = c, best = s;
-  }
-  return best;
-}
 
-// Where groups of 16 heads take less time than the tiles of 64.  Measured, in us, here / there, 576 dims:
+// The splits of a row's slots where groups of 16 heads take less time than the tiles of 64, else 0.  Measured, in us, here / there, 576 dims:
 //   slots                  64          180          350          700         1400         2048
 //   1 row of 64 heads   6.8 / 11.3   9.7 / 14.8  10.5 / 14.6  10.3 / 15.6  12.5 / 17.1  13.0 / 17.2
 //   10 rows             6.8 / 11.3  10.1 / 14.8  12.6 / 15.2  17.5 / 16.7  25.0 / 18.4  33.1 / 20.1
@@ -607,19 +597,19 @@ int best_splits(int64_t units, int K, int64_t* cost) {
 // (a key is widened once for 16 heads here, there for 64; tiles a quarter full cost what full ones do).  300 rows
 // of 16 heads x 2048 slots 160 / 132; one of 8192 slots 27.5 / 21.4, of 65,536 165 / 72: sixteen CTAs a unit are all there
 // are.  256 dims: 96 rows of 2 x 12 heads x 1027 slots 37 / 59, 1000 of 12 135 / 193, 16 of 64 heads x 700 14.6 / 14.0.
-bool narrow_takes(int T, int H, int Hc, int Dqk, int K) {
+int narrow_splits(int T, int H, int Hc, int Dqk, int K) {
   const int64_t units = static_cast<int64_t>(T) * Hc * ((H / Hc + 15) / 16);
-  if (units * kMaxCluster < kv8_attn::kPlanSms && K > 6144) return false;
-  if (H / Hc <= 16 && (Dqk == 256 || K <= 1024 || (units >= 24 && units <= 100))) return true;
+  if (units * kMaxCluster < kv8_attn::kPlanSms && K > 6144) return 0;
   const int nt = (K + kTile - 1) / kTile;
-  int64_t cost;
-  best_splits(units, K, &cost);
-  return cost <= 50 + 10 * std::min(nt, 3) + std::min(std::max(nt - 3, 0), 12) * 5 / 4;
-}
-
-int narrow_splits(int64_t units, int K) {
-  int64_t cost;
-  return best_splits(units, K, &cost);
+  const bool few = H / Hc <= 16 && (Dqk == 256 || K <= 1024 || (units >= 24 && units <= 100));
+  if (units > 10 * kv8_attn::kPlanSms) return few ? 1 : 0;  // (many layers: splits only add to an item)
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= kMaxCluster && s <= nt; ++s) {
+    const int64_t c = cost_of(static_cast<int>(units), nt, s);
+    if (c < cost) cost = c, best = s;
+  }
+  return few || cost <= 50 + 10 * std::min(nt, 3) + std::min(std::max(nt - 3, 0), 12) * 5 / 4 ? best : 0;
 }
 
 int launch_narrow(const kv8_attn::Params& p, int T, int Dqk, cudaStream_t stream) {

@@ -203,10 +203,12 @@ struct BwdParams {
 // Groups go through the rows in steps of all groups of the grid, a row's loads
 // under way while the row before it is worked on; a thread keeps dw's terms of its
 // columns, the CTA adds its groups' and writes one row of `part`.
-// Resident CTAs an SM: what 64 registers a thread leave room for, 3 of 85 with two pieces a lane.
+// Resident CTAs an SM: what 64 registers a thread leave room for, 2 of 128 with two pieces a lane (3 of 85
+// spill: 24,000 rows of 288 took 23.9 us where they take 12.9), 3 with groups of 8 (4 spill: 5.1 us for 24,000
+// rows of 40, and 4.7 with 3).
 template <int G, int NP>
 __host__ __device__ constexpr int bwd_per_sm() {
-  return G == 32 && NP == 2 ? 3 : 1024 / Cta<G>::kThreads;
+  return G == 8 ? 3 : G == 32 && NP == 2 ? 2 : 1024 / Cta<G>::kThreads;
 }
 
 template <int G, int NP>

@@ -12,7 +12,7 @@
 // A CTA works out its tokens' cosines and sines once, for all their heads, while the first loads
 // are under way.  The rows' bytes bound it: 16,384 tokens of 64 + 1 rows of 64, halves, 272 MB, take
 // 45 us (6.1 TB/s), pairs 47; rows that are the last 64 of 576 the same 48 and 50; 4096 tokens of
-// 24 + 1 heads of 256 21 us (4.9 TB/s).  64 tokens take 3.4 us: the chain from the sequence's
+// 24 + 1 heads of 256 21 us (4.9 TB/s).  32 tokens take 2.6 us: the chain from the sequence's
 // offsets to the angles, not the bytes.
 #include <algorithm>
 #include <climits>
@@ -38,6 +38,7 @@ struct Params {
   const double* f;
   dsa::Kv8Geom g;
   int H, H2, R, tokens;
+  int rows;              // of a token, that a CTA takes: all of them, or with one token a part
   int per;               // units of a row
   uint32_t m_token, m_row, m_half;  // dsa::fast_div by a token's units, a row's and R / 2
   float mul, sign;
@@ -66,15 +67,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
   __shared__ int64_t place[kMaxTokens];  // position, or kNone
   constexpr int64_t kNone = INT64_MIN;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
-  const int half = p.R >> 1, rows = p.H + p.H2;
+  const int half = p.R >> 1, row0 = blockIdx.y * p.rows, rows = min(p.rows, p.H + p.H2 - row0);
   const int n_tok = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.g.T - t0));
   const int n = n_tok * rows * p.per;
   uint4 v[kAhead][kWords];
   auto where = [&](int i, int* token, int* u, const Side** s, int* h) {
     const int k = dsa::fast_div(i, p.m_token), rest = i - k * rows * p.per;
-    const int r = dsa::fast_div(rest, p.m_row);
+    const int in = dsa::fast_div(rest, p.m_row), r = row0 + in;
     *token = k;
-    *u = rest - r * p.per;
+    *u = rest - in * p.per;
     *s = r < p.H ? &p.a : &p.b;
     *h = r < p.H ? r : r - p.H;
   };
@@ -256,10 +257,17 @@ extern "C" int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H,
   int tokens = std::min({kMaxTokens, kMaxAngles / (R / 2), std::max(1, units / per_token)});
   tokens = std::max(1, std::min(tokens, T / (2 * sms)));
   p.tokens = tokens;
+  // Few tokens: a token's rows go to several CTAs, a unit a thread, up to four CTAs an SM (32 tokens of 129
+  // rows of 64, pairs: 2.6 us, and 3.5 in one CTA a token; 19 of 129 rows of 256: 2.8, and 6.8; 150 of them: 5.1,
+  // with one or eight CTAs an SM 6.9 and 6.2).
+  int parts = 1;
+  if (tokens == 1) parts = std::max(1, std::min(per_token / kThreads, 4 * sms / T));
+  p.rows = (H + H2 + parts - 1) / parts;
   p.m_token = tokens == 1 ? 1 : dsa::magic_of(per_token);
   p.m_row = dsa::magic_of(p.per);
   p.m_half = dsa::magic_of(R / 2);
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens),
+                  static_cast<unsigned>((H + H2 + p.rows - 1) / p.rows));
   if (interleaved)
     rotary_kernel<true><<<grid, kThreads, 0, stream>>>(p);
   else

@@ -217,6 +217,9 @@ def part(rng, T, H, R_, ld, lead):
     (32, 1, 0, [5000], None, 11, 40, 8),
     (48, 5, 3, [257], [100000], 0, 64, 16),
     (64, 64, 1, [900, 1400], [0, 77], 3, 72, 8),
+    (256, 120, 5, [3, 0, 20], [5, 0, 999], 2, 256, 0),
+    (1024, 7, 1, [1], [65535], 0, 1024, 0),
+    (16, 1000, 24, [130], [7], 4, 16, 0),
 ])
 def test_rotary(pairs, R_, H, H2, lens, pos, pad, ld, lead):
     rng = np.random.default_rng(R_ + H + len(lens))
