@@ -667,6 +667,8 @@ int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32_t* cu_seql
  *   often widens them once.
  * Values are bf16 ones and the query enters as it is: weights exp(s_j) are rounded to
  * bf16 before they meet the values, sums are fp32, as in dsa_sparse_attn_fwd.
+ * Weights times values are summed before they are divided by the weights' sum, a weight being at most 2^8:
+ * values beyond 2^119 / K may make infinities of them.
  * Results are bitwise reproducible; a row's last bits may differ between calls of
  * different T, H, K or n_blocks * block, which choose the form and the splits.
  * Errors: DSA_ERR_VALUE, DSA_ERR_WORKSPACE. */
