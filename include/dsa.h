@@ -388,6 +388,7 @@ int dsa_indexer_topk_noalloc(const void* qi, const void* ki, const float* w, con
  *   lse_kv fp32 [T, H] or NULL (out): log sum_j exp(s_j), KV only (empty
  *       row: +inf) -- the cuDNN "lse" statistic;
  *   max_logits fp32 [T, H] or NULL (out): max_j s_j (empty row: -inf).
+ * A head of a row that meets NaN or a score of +inf has NaN in out and in every statistic.
  * Shapes: (Dqk, Dv) in {(576, 512), (512, 512)} with v == NULL, or
  * (256, 256) with a separate v; 1 <= H <= 128; K >= 0; scale finite > 0;
  * q, kv, v, out 16-byte aligned.

@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar(1, kSoftThreads);
           if (st < hv) {
             const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
-            p.lse_indexer[orow + st] = l > 0.f ? (mref[st] + log2f(l)) * kLn2 : INFINITY;
+            p.lse_indexer[orow + st] = l != 0.f ? (mref[st] + log2f(l)) * kLn2 : INFINITY;
           }
           named_bar(1, kSoftThreads);  // red is read before the epilogue reuses it
         }
@@ -686,14 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mc = mref[st];
         const float sk = (p.sink && st < hv) ? __ldg(p.sink + g * kHG + st) * kLog2e : -INFINITY;
         float f = 0.f, lse_v, lkv, mlog = -INFINITY;
-        if (l > 0.f) {
+        if (l != 0.f) {  // true for NaN too, which reaches every statistic
           const float M = fmaxf(mc, sk);
           const float a = exp2f(mc - M);
           const float z = l * a + exp2f(sk - M);
           f = a / z;
           lse_v = (M + log2f(z)) * kLn2;
           lkv = (mc + log2f(l)) * kLn2;
-          if (want_max) mlog = m_max * kLn2;  // x = s*log2(e), so max s = max x * ln(2)
+          if (want_max) mlog = l == l ? m_max * kLn2 : l;  // x = s*log2(e), so max s = max x * ln(2)
         } else {
           lse_v = sk * kLn2;
           lkv = INFINITY;

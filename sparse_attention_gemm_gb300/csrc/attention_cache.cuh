@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_kernel(const Params p)
           if (st < w.hv) {
             p.lse[orow + st] = lse_v;
             if (p.lse_kv) p.lse_kv[orow + st] = lkv;
-            if (kMax) p.max_logits[orow + st] = any ? m_max * kLn2 : -INFINITY;
+            if (kMax) p.max_logits[orow + st] = max_logit_of(l, m_max);
           }
         }
         fac[st] = f;
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
   if (threadIdx.x == 0) {
     p.lse[row] = any ? (M + log2f(z)) * kLn2 : sink;
     if (p.lse_kv) p.lse_kv[row] = any ? (M + log2f(l)) * kLn2 : INFINITY;
-    if (p.max_logits) p.max_logits[row] = any ? mx * kLn2 : -INFINITY;
+    if (p.max_logits) p.max_logits[row] = !any ? -INFINITY : l == l ? mx * kLn2 : l;
   }
 }
 

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
         if (first) {
           p.lse[orow + h] = lse_v;
           if (p.lse_kv) p.lse_kv[orow + h] = lkv;
-          if (p.max_logits) p.max_logits[orow + h] = any ? m_max[e] * kLn2 : -INFINITY;
+          if (p.max_logits) p.max_logits[orow + h] = max_logit_of(l, m_max[e]);
         }
       }
       // this lane's dims: 64 slice + 8 (2c + k) + j
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
     if (split == 0 && s == 0 && h < hv) {
       p.lse[orow + h] = any ? (M + log2f(z)) * kLn2 : sink;
       if (p.lse_kv) p.lse_kv[orow + h] = any ? (M + log2f(l)) * kLn2 : INFINITY;
-      if (p.max_logits) p.max_logits[orow + h] = any ? mx * kLn2 : -INFINITY;
+      if (p.max_logits) p.max_logits[orow + h] = any ? (l == l ? mx * kLn2 : l) : -INFINITY;
     }
   }
   __syncthreads();

@@ -1,0 +1,121 @@
+"""Rows of sparse attention that meet NaN, that have no slot, or whose cache rows have large scales, in every
+form of the calls."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as R
+import test_gpu_kv8 as kv8
+from gpu_util import DEV, dev, dev_bf16, rand_bf16_bits
+from sparse_attention_gemm_gb300 import ops
+from test_gpu_kv4 import FORMS, attention_case, check_attention
+
+pytestmark = pytest.mark.gpu
+
+STATISTICS = ("lse", "lse_kv", "max_logits")
+# 16 heads whole and in splits; 64 heads whole and in splits; a cache that is widened once
+SHAPES = [(4, 16, 70, None), (4, 16, 1500, None), (130, 64, 70, None), (12, 64, 1500, None), (700, 64, 700, 900)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    ops.device_status(clear=True)
+    yield
+    torch.cuda.synchronize()
+    assert ops.device_status(clear=True) == 0, "a kernel raised a device status flag"
+
+
+def kv4_call(q, k, ks, idx, sm, kw, **more):
+    d = {n: dev(kw[n]) for n in ("v4", "v_scale", "sink") if n in kw}
+    if "length" in kw:
+        d["topk_length"] = dev(kw["length"])
+    return ops.sparse_attn_fwd_kv4(q, dev(k), dev(ks), dev(idx), sm, want_lse_kv=True, want_max_logits=True, **d, **more)
+
+
+def assert_widened(T, H, dqk, dv, K, k, n):
+    if n:
+        need = ops.sparse_attn_fwd_kv4_workspace_size(T, H, 1, dqk, dv, K, k.shape[1], k.shape[0])
+        assert need >= k.shape[0] * k.shape[1] * dqk * 2
+
+
+def assert_nan_only(got, clean, hit, names):
+    """Every result of the (row, head) pairs in `hit` is NaN, the others' bits are those of `clean`."""
+    for n in names:
+        assert bool(got[n][hit].isnan().all()), f"{n}: not NaN"
+        assert torch.equal(got[n][~hit], clean[n][~hit]), n
+
+
+def pairs(T, H, *hits):
+    m = torch.zeros(T, H, dtype=torch.bool, device=DEV)
+    for t, h in hits:
+        m[t, h] = True
+    return m
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,n", SHAPES)
+def test_nan_reaches_every_result_of_its_rows(dqk, dv, T, H, K, n):
+    rng = np.random.default_rng(dqk + T + K)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 1, False, n=n, holes=False)
+    assert_widened(T, H, dqk, dv, K, k, n)
+    kw["sink"] = rng.standard_normal(H).astype(np.float32)
+    hit = idx[0, 5]
+    idx[1:][idx[1:] == hit] = (hit + 1) % k.shape[0]
+    names = ("out", *STATISTICS)
+    clean = kv4_call(dev_bf16(q), k, ks, idx, sm, kw)
+    bad = ks.copy()
+    bad[hit, 0, 0, 2] = 255
+    assert_nan_only(kv4_call(dev_bf16(q), k, bad, idx, sm, kw), clean, pairs(T, H, (0, slice(None))), names)
+    q2 = dev_bf16(q)
+    q2[2, 7, 3], q2[3, 9, 200] = float("nan"), float("inf")
+    assert_nan_only(kv4_call(q2, k, ks, idx, sm, kw), clean, pairs(T, H, (2, 7), (3, 9)), names)
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H", [(5, 64), (200, 20)])
+def test_nan_over_bf16_rows(dqk, dv, T, H):
+    """The call over bf16 rows, with the statistic of the first slots: NaN from a key and from a query's head."""
+    rng = np.random.default_rng(dqk + T)
+    K, n = 200, 900
+    q, kv = dev_bf16(rand_bf16_bits(rng, (T, H, dqk))), dev_bf16(rand_bf16_bits(rng, (n, dqk)))
+    idx = rng.integers(0, n, (T, K)).astype(np.int32)
+    hit, late = idx[0, 5], idx[1, 150]
+    idx[1:][idx[1:] == hit] = (hit + 1) % n
+    idx[idx == late] = (late + 1) % n
+    idx[0, 5], idx[1, 150] = hit, late
+    args = dict(sink=dev(rng.standard_normal(H).astype(np.float32)), want_lse_kv=True, want_max_logits=True, indexer_topk=64,
+                v=dev_bf16(rand_bf16_bits(rng, (n, dv))) if dqk == 256 else None)
+    clean = ops.sparse_attn_fwd(q, kv, dev(idx), 0.05, **args)
+    bad = kv.clone()
+    bad[int(hit), 40] = float("nan")
+    names = ("out", "lse_indexer", *STATISTICS)
+    assert_nan_only(ops.sparse_attn_fwd(q, bad, dev(idx), 0.05, **args), clean, pairs(T, H, (0, slice(None))), names)
+    bad = kv.clone()
+    bad[int(late), 40] = float("nan")  # behind the first slots: their statistic stays
+    got = ops.sparse_attn_fwd(q, bad, dev(idx), 0.05, **args)
+    assert_nan_only(got, clean, pairs(T, H, (1, slice(None))), ("out", *STATISTICS))
+    assert torch.equal(got["lse_indexer"], clean["lse_indexer"])
+    q2 = q.clone()
+    q2[2, 7, 3], q2[3, 9, 200] = float("nan"), float("inf")
+    assert_nan_only(ops.sparse_attn_fwd(q2, kv, dev(idx), 0.05, **args), clean, pairs(T, H, (2, 7), (3, 9)), names)
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K", [(4, 16, 70), (4, 64, 1500), (200, 64, 70), (100, 128, 700)])
+def test_nan_over_the_8_bit_cache(dqk, dv, T, H, K):
+    rng = np.random.default_rng(dqk + T + K)
+    q, k, ks, idx, sm, kw = kv8.attention_case(rng, dqk, dv, T, H, 1, K, 1, False, holes=False)
+    args = dict(sink=dev(rng.standard_normal(H).astype(np.float32)), want_lse_kv=True, want_max_logits=True,
+                **{n: dev(kw[n]) for n in ("v8", "v_scale") if n in kw})
+    hit = idx[0, 5]
+    idx[1:][idx[1:] == hit] = (hit + 1) % k.shape[0]
+    clean = ops.sparse_attn_fwd_kv8(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, **args)
+    bad = k.copy()
+    bad[hit, 0, 0, 40] = 127
+    got = ops.sparse_attn_fwd_kv8(dev_bf16(q), dev(bad), dev(ks), dev(idx), sm, **args)
+    assert_nan_only(got, clean, pairs(T, H, (0, slice(None))), ("out", *STATISTICS))
