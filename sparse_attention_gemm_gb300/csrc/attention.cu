@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (st < 64) {
         const float l = red[st] + red[64 + st] + red[128 + st] + red[192 + st];
         const float mc = mref[st];
-        const float sk = (p.sink && st < hv) ? __ldg(p.sink + g * kHG + st) * kLog2e : -INFINITY;
+        const float sink = (p.sink && st < hv) ? __ldg(p.sink + g * kHG + st) : -INFINITY, sk = sink * kLog2e;
         float f = 0.f, lse_v, lkv, mlog = -INFINITY;
         if (l != 0.f) {  // true for NaN too, which reaches every statistic
           const float M = fmaxf(mc, sk);
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lkv = (mc + log2f(l)) * kLn2;
           if (want_max) mlog = l == l ? m_max * kLn2 : l;  // x = s*log2(e), so max s = max x * ln(2)
         } else {
-          lse_v = sk * kLn2;
+          lse_v = sink;  // the sink itself, as for a row without tiles
           lkv = INFINITY;
         }
         fac[st] = f;

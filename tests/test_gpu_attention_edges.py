@@ -119,3 +119,37 @@ def test_nan_over_the_8_bit_cache(dqk, dv, T, H, K):
     bad[hit, 0, 0, 40] = 127
     got = ops.sparse_attn_fwd_kv8(dev_bf16(q), dev(bad), dev(ks), dev(idx), sm, **args)
     assert_nan_only(got, clean, pairs(T, H, (0, slice(None))), ("out", *STATISTICS))
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,n", SHAPES)
+@pytest.mark.parametrize("sink", [True, False])
+def test_rows_without_slots_give_the_sink_itself(dqk, dv, T, H, K, n, sink):
+    """Rows whose slots are all unmapped: lse is the sink's own bits (-inf without one), not the sink taken to powers of
+    two and back."""
+    rng = np.random.default_rng(dqk + T + K + 1)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 1, False, n=n, holes=False)
+    assert_widened(T, H, dqk, dv, K, k, n)
+    idx[0], idx[2], idx[3, ::2], idx[3, 1::2] = -1, 1 << 30, -7, k.shape[0]
+    kw["length"] = np.full(T, K, np.int32)
+    kw["length"][1] = 0
+    want = torch.full((4, H), -math.inf, device=DEV)
+    if sink:
+        kw["sink"] = (3 * rng.standard_normal(H)).astype(np.float32)
+        want = dev(kw["sink"]).expand(4, H)
+    got = kv4_call(dev_bf16(q), k, ks, idx, sm, kw)
+    assert bool((got["out"][:4] == 0).all()) and torch.equal(got["lse"][:4], want)
+    assert bool((got["lse_kv"][:4] == math.inf).all()) and bool((got["max_logits"][:4] == -math.inf).all())
+
+
+@pytest.mark.parametrize("T,H", [(5, 64), (200, 20)])
+def test_bf16_rows_without_slots_give_the_sink_itself(T, H):
+    rng = np.random.default_rng(T)
+    q, kv = dev_bf16(rand_bf16_bits(rng, (T, H, 576))), dev_bf16(rand_bf16_bits(rng, (300, 576)))
+    idx = torch.full((T, 130), -1, dtype=torch.int32, device=DEV)
+    idx[1:] = 300
+    sink = dev((3 * rng.standard_normal(H)).astype(np.float32))
+    got = ops.sparse_attn_fwd(q, kv, idx, 0.05, sink=sink, want_lse_kv=True, want_max_logits=True, indexer_topk=64)
+    assert bool((got["out"] == 0).all()) and torch.equal(got["lse"], sink.expand(T, H))
+    assert bool((got["lse_kv"] == math.inf).all()) and bool((got["max_logits"] == -math.inf).all())
+    assert bool((got["lse_indexer"] == math.inf).all())
