@@ -844,8 +844,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_kernel(const Params p)
   }
 }
 
-// Joins the splits of one (token, head) per CTA: with M the largest reference,
-// a_s = 2^(m_s - M) l_s and z = sum_s a_s + 2^(sink - M), out = sum_s a_s O_s / z of the splits' means O_s.
+// Joins the splits of one (token, head) per CTA: with m the largest reference, a_s = 2^(m_s - m) l_s, l = sum_s a_s,
+// M the larger of m and the sink and z = 2^(m - M) l + 2^(sink - M), out = sum_s a_s 2^(m - M) O_s / z of the splits' means
+// O_s.  (l is lse_kv's, of the slots alone: against M it is nothing under a sink far above the scores.)
 template <int DV>
 __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
@@ -865,12 +866,12 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
   const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
   const bool any = __any_sync(0xffffffffu, have);
   const float M = fmaxf(m, sk);
-  const float a = have ? s.y * exp2f(s.x - M) : 0.f;
+  const float a = have ? s.y * exp2f(s.x - m) : 0.f, down = any ? exp2f(m - M) : 0.f;
   float l = a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float z = any ? l + exp2f(sk - M) : 1.f;
-  const float share = a / z;  // at most 1: a mean of means stays in range
+  const float z = any ? l * down + exp2f(sk - M) : 1.f;
+  const float share = a * down / z;  // at most 1: a mean of means stays in range
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.splits * DV) + threadIdx.x;
   for (int k = 0; k < p.splits; ++k) {
@@ -886,8 +887,8 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
   reinterpret_cast<uint2*>(p.out + row * DV)[threadIdx.x] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   if (threadIdx.x == 0) {
     p.lse[row] = any ? (M + log2f(z)) * kLn2 : sink;
-    if (p.lse_kv) p.lse_kv[row] = any ? (M + log2f(l)) * kLn2 : INFINITY;
-    if (p.max_logits) p.max_logits[row] = !any ? -INFINITY : l == l ? mx * kLn2 : l;
+    if (p.lse_kv) p.lse_kv[row] = any ? (m + log2f(l)) * kLn2 : INFINITY;
+    if (p.max_logits) p.max_logits[row] = max_logit_of(l, mx);
   }
 }
 

@@ -153,3 +153,31 @@ def test_bf16_rows_without_slots_give_the_sink_itself(T, H):
     assert bool((got["out"] == 0).all()) and torch.equal(got["lse"], sink.expand(T, H))
     assert bool((got["lse_kv"] == math.inf).all()) and bool((got["max_logits"] == -math.inf).all())
     assert bool((got["lse_indexer"] == math.inf).all())
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,n", SHAPES + [(32, 128, 2048, None)])
+@pytest.mark.parametrize("cache", ["4 bits", "8 bits"])
+def test_statistics_under_a_sink_far_above_the_scores(dqk, dv, T, H, K, n, cache):
+    """lse_kv and max_logits know nothing of the sink; lse is the sink's, out next to nothing."""
+    rng = np.random.default_rng(dqk + T + K + 2)
+    if cache == "4 bits":
+        q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 1, False, n=n, holes=False)
+
+        def call(sink):
+            return kv4_call(dev_bf16(q), k, ks, idx, sm, dict(kw, sink=sink))
+    else:
+        q, k, ks, idx, sm, kw = kv8.attention_case(rng, dqk, dv, T, H, 1, K, 1, False, n=n, holes=False)
+        args = {m: dev(kw[m]) for m in ("v8", "v_scale") if m in kw}
+
+        def call(sink):
+            return ops.sparse_attn_fwd_kv8(dev_bf16(q), dev(k), dev(ks), dev(idx), sm, sink=dev(sink), want_lse_kv=True,
+                                           want_max_logits=True, **args)
+    low = call(np.full(H, -100.0, np.float32))
+    sink = (90 + 60 * rng.random(H)).astype(np.float32)
+    high = call(sink)
+    # (a product with ln 2 and, of both, a sum and a logarithm: a few roundings of numbers below 2^8)
+    tol = 8 * 2.0 ** -24 * 256
+    assert bool(((high["lse_kv"] - low["lse_kv"]).abs() <= tol).all()), "lse_kv"
+    assert torch.equal(high["max_logits"], low["max_logits"])
+    assert bool(((high["lse"] - dev(sink)).abs() <= tol).all()) and bool((high["out"].abs() <= 1e-20).all())
