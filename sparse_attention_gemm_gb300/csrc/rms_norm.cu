@@ -125,18 +125,19 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdPara
   }
   sq = group_sum<G>(sq, red[0]);
   float rstd = 1.f / sqrtf(sq / static_cast<float>(p.D) + p.eps);
-  // squares beyond fp32's range: again, of values 2^64 times smaller (eps is nothing beside them)
+  // A sum of squares beyond fp32's range: again, of values 2^100 times smaller.  Of 16,384 values below 2^128 the squares'
+  // sum is then below 2^70; those that underflow are below 2^26 beside one of 2^57 at least, and eps is nothing beside it.
   if (__any_sync(0xffffffffu, !(sq < INFINITY))) {
     float small = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = h[k].v[i] * 0x1p-64f;
+        const float v = h[k].v[i] * 0x1p-100f;
         small = fmaf(v, v, small);
       }
     small = group_sum<G>(small, red[1]);
-    if (!(sq < INFINITY)) rstd = 0x1p-64f / sqrtf(small / static_cast<float>(p.D));
+    if (!(sq < INFINITY)) rstd = 0x1p-100f / sqrtf(small / static_cast<float>(p.D));
   }
   if (live && sub == 0 && p.rstd) p.rstd[t] = rstd;
   if (live && p.sum) {

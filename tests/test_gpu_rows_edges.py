@@ -1,0 +1,65 @@
+"""Norm and rotary positions of rows and positions at the ends of their ranges, against their 64-bit definitions."""
+import numpy as np
+import pytest
+import torch
+
+import rows_ref as R
+from gpu_util import DEV, dev
+from sparse_attention_gemm_gb300 import ops
+from test_gpu_rows import EPS, f64, near
+
+pytestmark = pytest.mark.gpu
+
+MOST = 3.3895313892515355e38  # the largest bf16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    yield
+    torch.cuda.synchronize()
+
+
+def bf16(a):
+    return torch.from_numpy(np.asarray(a, np.float64)).to(torch.bfloat16).to(DEV)
+
+
+def check_norm(x, w, eps, residual=None):
+    h, rstd, y = R.norm(f64(x), w.astype(np.float64), float(np.float32(eps)), None if residual is None else f64(residual))
+    ts, tr, ty = R.norm_bounds(h, rstd, y)
+    got = ops.rms_norm_fwd(x, dev(w), eps, residual=residual, want_rstd=True)
+    # (below 2^-126 rstd is a multiple of 2^-149, at least 2^-128: off by 2^-22 of itself, which the bounds leave room for;
+    # results below 2^-126 are multiples of 2^-133, sums of the residual are in range)
+    near(got["rstd"], rstd, tr + 2.0 ** -150, "rstd")
+    near(got["out"], y, ty + 2.0 ** -134, "out")
+    if residual is not None:
+        near(got["sum"], h, ts, "sum")
+    if x.shape[1] % 128 == 0:
+        for fmt, group in (("e4m3", 128), ("mxfp8", 32)):
+            q = ops.rms_norm_fwd(x, dev(w), eps, residual=residual, fmt=fmt)
+            s = q["scale"].cpu().numpy()
+            s = s.astype(np.float64) if fmt == "e4m3" else np.exp2(s.astype(np.float64) - 127)
+            R.check_codes(q["out"].cpu().numpy(), s, y, group)
+
+
+@pytest.mark.parametrize("D", [8, 64, 128, 256, 512, 1024, 1032, 4096, 8200, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_rows_up_to_the_largest_values(D, residual):
+    """Squares and their sums beyond fp32's range, beside ordinary rows: every finite row has its norm."""
+    rng = np.random.default_rng(D)
+    x = rng.standard_normal((14, D))
+    size = 2.0 ** np.array([0, 40, 60, 63, 64, 70, 90, 110, 118, 122, 125])
+    x[:11] *= size[:, None] / np.abs(x[:11]).max(1, keepdims=True)
+    x[11] = MOST * np.sign(x[11])
+    x[12] = 0
+    x[12, D // 2] = -MOST
+    x[13] *= 2.0 ** rng.uniform(-120, 120, D)
+    x[13] = np.clip(x[13], -MOST, MOST)
+    r = None
+    if residual:
+        r = rng.standard_normal((14, D))
+        r[:11] *= size[:, None] / 16
+        r[11] = -np.sign(x[11]) * MOST / 2
+    check_norm(bf16(x), rng.standard_normal(D).astype(np.float32), EPS, None if r is None else bf16(r))
