@@ -124,20 +124,27 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdPara
     for (int i = 0; i < 8; ++i) sq = fmaf(h[k].v[i], h[k].v[i], sq);
   }
   sq = group_sum<G>(sq, red[0]);
-  float rstd = 1.f / sqrtf(sq / static_cast<float>(p.D) + p.eps);
-  // A sum of squares beyond fp32's range: again, of values 2^100 times smaller.  Of 16,384 values below 2^128 the squares'
-  // sum is then below 2^70; those that underflow are below 2^26 beside one of 2^57 at least, and eps is nothing beside it.
-  if (__any_sync(0xffffffffu, !(sq < INFINITY))) {
-    float small = 0.f;
+  const float mean = sq / static_cast<float>(p.D) + p.eps;
+  float rstd = 1.f / sqrtf(mean);
+  // Out of fp32's range the squares are summed again, of values 2^100 times smaller or larger.
+  // * beyond it: of 16,384 values below 2^128 the sum is then below 2^70; those whose squares underflow are below 2^26
+  //   beside one of 2^57 at least, and eps is nothing beside it;
+  // * below it: a mean and an eps that together are under 2^-100 leave a sum under 2^114, and squares that would have
+  //   lost bits (under 2^-126) are whole.  From 2^-100 on what they lose is under 2^-49 of the mean.
+  const bool high = !(sq < INFINITY), low = mean < 0x1p-100f;
+  if (__any_sync(0xffffffffu, high || low)) {
+    const float by = high ? 0x1p-100f : 0x1p100f;
+    float again = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = h[k].v[i] * 0x1p-100f;
-        small = fmaf(v, v, small);
+        const float v = h[k].v[i] * by;
+        again = fmaf(v, v, again);
       }
-    small = group_sum<G>(small, red[1]);
-    if (!(sq < INFINITY)) rstd = 0x1p-100f / sqrtf(small / static_cast<float>(p.D));
+    again = group_sum<G>(again, red[1]) / static_cast<float>(p.D);
+    if (high) rstd = by / sqrtf(again);
+    else if (low) rstd = by / sqrtf(again + p.eps * by * by);
   }
   if (live && sub == 0 && p.rstd) p.rstd[t] = rstd;
   if (live && p.sum) {

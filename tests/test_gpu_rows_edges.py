@@ -63,3 +63,13 @@ def test_norm_of_rows_up_to_the_largest_values(D, residual):
         r[:11] *= size[:, None] / 16
         r[11] = -np.sign(x[11]) * MOST / 2
     check_norm(bf16(x), rng.standard_normal(D).astype(np.float32), EPS, None if r is None else bf16(r))
+
+
+@pytest.mark.parametrize("D", [8, 64, 256, 512, 1032, 4096, 16384])
+@pytest.mark.parametrize("eps", [1e-45, 1e-43, 1e-38, 1e-31])
+def test_norm_with_an_eps_below_small_squares(D, eps):
+    """Squares below fp32's range that count beside an eps of their size."""
+    rng = np.random.default_rng(D)
+    x = rng.standard_normal((9, D)) * 10.0 ** np.array([-22, -22.5, -21, -20, -19, -16, -23, 0, 30])[:, None]
+    x[6] = 0
+    check_norm(bf16(x), rng.standard_normal(D).astype(np.float32), eps)
