@@ -634,10 +634,21 @@ def _ok(t, dtype, dim, device):
             t.get_device() == device)
 
 
+# Sizes are 32-bit in the library, and ctypes takes larger ones modulo 2^32: the norm's, rotary's and the 4-bit
+# cache's calls refuse them.
+_MOST = 2 ** 31 - 1
+
+
+def _need_size(t, name):
+    if t.dim() > 1 and max(t.shape) > _MOST:
+        raise ValueError(f"{name} is {list(t.shape)}: sizes are signed numbers of 32 bits")
+
+
 def _refuse(device, *args):
     """Raises for the first of (tensor, name, dtype, dim, shape or None) that is not as it has to be."""
     for t, name, dtype, dim, shape in args:
         _need(t, name, dtype, dim)
+        _need_size(t, name)
         if t.get_device() != device or device != _current_device():
             raise ValueError(f"{name} is on {t.device}: the tensors of a call are on the current device, "
                              f"cuda:{_current_device()}")
@@ -837,14 +848,15 @@ def _kv4_call(rows, rows_name, T, cache, cache_scale, cu_seqlens, pos, block_tab
               cache_scale.shape == (n_blocks, block, heads, half // 16) and cache_scale.is_contiguous() and
               cache_scale.get_device() == dev and cu_seqlens.dtype is _I32 and cu_seqlens.dim() == 1 and
               cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev and rows.dtype is _BF16 and h == heads and
-              d == 2 * half and (T is None or t == T) and rows.is_contiguous() and rows.get_device() == dev)
+              d == 2 * half and (T is None or t == T) and rows.is_contiguous() and rows.get_device() == dev and
+              max(n_blocks, n, t) <= _MOST)
         if pos is not None:
             ok = ok and pos.dtype is _I32 and pos.shape == (n,) and pos.is_contiguous() and pos.get_device() == dev
             p_ptr = pos.data_ptr()
         if block_table is not None:
             m, width = block_table.shape
             ok = (ok and block_table.dtype is _I32 and m == n and block_table.is_contiguous() and
-                  block_table.get_device() == dev)
+                  block_table.get_device() == dev and width <= _MOST)
             t_ptr = block_table.data_ptr()
     except (AttributeError, TypeError, ValueError, IndexError, RuntimeError):
         ok = False
@@ -926,7 +938,7 @@ def sparse_attn_fwd_kv4(q, kv4, kv_scale, idx, scale: float, topk_length=None, s
               2 * half == Dqk and kv4.is_contiguous() and kv4.get_device() == dev and kv_scale.dtype is _U8 and
               kv_scale.shape == (n_blocks, block, heads, half // 16) and kv_scale.is_contiguous() and
               kv_scale.get_device() == dev and idx.dtype is _I32 and rows == T and idx.is_contiguous() and
-              idx.get_device() == dev)
+              idx.get_device() == dev and max(T, K, n_blocks) <= _MOST)
         if topk_length is not None:
             ok = (ok and topk_length.dtype is _I32 and topk_length.shape == (T,) and topk_length.is_contiguous() and
                   topk_length.get_device() == dev)
@@ -949,7 +961,7 @@ def sparse_attn_fwd_kv4(q, kv4, kv_scale, idx, scale: float, topk_length=None, s
             n_seqs, width = block_table.shape
             ok = (ok and block_table.dtype is _I32 and block_table.is_contiguous() and
                   block_table.get_device() == dev and cu_seqlens.dtype is _I32 and cu_seqlens.shape == (n_seqs + 1,) and
-                  cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev)
+                  cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev and max(n_seqs, width) <= _MOST)
             t_ptr, c_ptr = block_table.data_ptr(), cu_seqlens.data_ptr()
         if out is not None:
             ok = (ok and out.dtype is _BF16 and out.shape == (T, H, Dv) and out.is_contiguous() and
@@ -1008,6 +1020,7 @@ def _strided_refuse(device, *args):
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+        _need_size(t, name)
         if t.get_device() != device or device != _current_device():
             raise ValueError(f"{name} is on {t.device}: the tensors of a call are on the current device, "
                              f"cuda:{_current_device()}")
@@ -1050,7 +1063,7 @@ def rms_norm_fwd(x, weight, eps: float, residual=None, fmt: str = "bf16", out=No
         T, D = shape = x.shape
         dev, xs = x.get_device(), x.stride()
         ok = (x.dtype is _BF16 and xs[1] == 1 and dev == _get_device() and weight.dtype is _F32 and
-              weight.shape == (D,) and weight.stride(0) == 1 and weight.get_device() == dev)
+              weight.shape == (D,) and weight.stride(0) == 1 and weight.get_device() == dev and max(T, D) <= _MOST)
         r_ptr = r_ld = y_ptr = s_ptr = c_ptr = 0
         if residual is not None:
             st = residual.stride()
@@ -1116,7 +1129,7 @@ def rms_norm_bwd(dy, x, weight, rstd, d_sum=None, want_dweight: bool = True, dx=
         ok = (x.dtype is _BF16 and xs[1] == 1 and dev == _get_device() and dy.dtype is _BF16 and dy.shape == shape and
               ys[1] == 1 and dy.get_device() == dev and weight.dtype is _F32 and weight.shape == (D,) and
               weight.stride(0) == 1 and weight.get_device() == dev and rstd.dtype is _F32 and rstd.shape == (T,) and
-              rstd.is_contiguous() and rstd.get_device() == dev)
+              rstd.is_contiguous() and rstd.get_device() == dev and max(T, D) <= _MOST)
         x_ld, y_ld, s_ptr, s_ld, o_ld = xs[0], ys[0], 0, 0, D
         if d_sum is not None:
             st = d_sum.stride()
@@ -1200,7 +1213,7 @@ def rotary(x, inv_freq, cu_seqlens, pos=None, x2=None, interleaved: bool = True,
         ok = (x.dtype is _BF16 and last == 1 and dev == _get_device() and inv_freq.dtype is _F64 and
               inv_freq.shape == (R // 2,) and inv_freq.is_contiguous() and inv_freq.get_device() == dev and
               cu_seqlens.dtype is _I32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and
-              cu_seqlens.get_device() == dev)
+              cu_seqlens.get_device() == dev and max(T, H, R, n) <= _MOST)
         if pos is not None:
             ok = ok and pos.dtype is _I32 and pos.shape == (n,) and pos.is_contiguous() and pos.get_device() == dev
             p_ptr = pos.data_ptr()
@@ -1211,7 +1224,7 @@ def rotary(x, inv_freq, cu_seqlens, pos=None, x2=None, interleaved: bool = True,
         if x2 is not None:
             t2, H2, r2 = shape2 = x2.shape
             a2, b2, last = x2.stride()
-            ok = ok and x2.dtype is _BF16 and t2 == T and r2 == R and last == 1 and x2.get_device() == dev
+            ok = ok and x2.dtype is _BF16 and t2 == T and r2 == R and last == 1 and x2.get_device() == dev and H2 <= _MOST
             x2_ptr = x2.data_ptr()
             c2, d2 = H2 * R, R
             if out2 is not None:

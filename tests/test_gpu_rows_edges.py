@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import rows_ref as R
-from gpu_util import DEV, dev
+from gpu_util import DEV, cu_from_lengths, dev
 from sparse_attention_gemm_gb300 import ops
 from test_gpu_rows import EPS, f64, near
 
@@ -73,3 +73,23 @@ def test_norm_with_an_eps_below_small_squares(D, eps):
     x = rng.standard_normal((9, D)) * 10.0 ** np.array([-22, -22.5, -21, -20, -19, -16, -23, 0, 30])[:, None]
     x[6] = 0
     check_norm(bf16(x), rng.standard_normal(D).astype(np.float32), eps)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The library's sizes are 32-bit: a larger one does not come in modulo 2^32."""
+    far = 1 << 32
+    x = torch.zeros(1, 1, 16, dtype=torch.bfloat16, device=DEV).expand(far, 1, 16)
+    f, _ = ops.rotary_inv_freq(16)
+    cu, w = dev(cu_from_lengths([1])), torch.ones(8, device=DEV)
+    rows = torch.zeros(1, 8, dtype=torch.bfloat16, device=DEV).expand(far, 8)
+    rstd = torch.ones(1, device=DEV).expand(far)
+    src, empty = torch.zeros(3, 0, 32, dtype=torch.bfloat16, device=DEV), torch.zeros(far + 1, 1, 0, 16, dtype=torch.uint8, device=DEV)
+    scale = torch.zeros(far + 1, 1, 0, 1, dtype=torch.uint8, device=DEV)
+    q, idx = torch.zeros(1, 4, 576, dtype=torch.bfloat16, device=DEV), torch.zeros(1, 8, dtype=torch.int32, device=DEV)
+    wide = torch.zeros(far + 1, 1, 0, 288, dtype=torch.uint8, device=DEV)
+    for bad in (lambda: ops.rotary(x, f, cu, out=x), lambda: ops.rms_norm_fwd(rows, w, EPS, out=rows),
+                lambda: ops.rms_norm_bwd(rows, rows, w, rstd, dx=rows, want_dweight=False),
+                lambda: ops.kv4_write(src, empty, scale, cu), lambda: ops.kv4_read(empty, scale, cu, 3, out=src),
+                lambda: ops.sparse_attn_fwd_kv4(q, wide, wide[..., :18], idx, 0.1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            bad()
