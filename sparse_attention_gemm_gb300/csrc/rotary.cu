@@ -193,6 +193,7 @@ extern "C" int dsa_rotary_inv_freq(int R, double base, int scaling, double facto
     };
     lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
     hi = std::min(std::ceil(pair_of(beta_slow)), static_cast<double>(R - 1));
+    if (pair_of(beta_slow) < 0.0) lo = hi = -1.0;  // no pair makes as many turns: the blend ends before the first
   }
   for (int i = 0; i < half; ++i) {
     const double f = std::pow(b, -static_cast<double>(i) / half);
