@@ -233,6 +233,8 @@ extern "C" int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H,
   if ((x == y && (x_token != y_token || x_head != y_head)) ||
       (H2 > 0 && x2 == y2 && (x2_token != y2_token || x2_head != y2_head)))
     return dsa::set_error(DSA_ERR_VALUE, "%s: in place, the strides of both sides must be equal", fn);
+  if (H2 > 0 && T > 0 && (y == y2 || y == x2 || y2 == x))
+    return dsa::set_error(DSA_ERR_VALUE, "%s: y and y2 must not be one tensor, nor the other tensor's input", fn);
   if (!dsa::aligned(x, 16) || !dsa::aligned(y, 16) || !dsa::aligned(inv_freq, 8) ||
       (H2 > 0 && (!dsa::aligned(x2, 16) || !dsa::aligned(y2, 16))))
     return dsa::set_error(DSA_ERR_VALUE, "%s: rows must be 16-byte aligned, inv_freq 8-byte aligned", fn);

@@ -4,6 +4,8 @@ import pytest
 
 from sparse_attention_gemm_gb300 import build as dsa_build
 from sparse_attention_gemm_gb300 import ops
+from test_kv8_abi import FAKE
+from test_rows_abi import FAR, FAR2, rotary_args
 
 
 @pytest.fixture(scope="module")
@@ -25,3 +27,13 @@ def test_angles_of_pairs_beyond_the_blend(lib, first, R, base, slow):
     ratio = f.numpy() / plain.numpy()
     # (the blend runs from pair floor(lo) to pair ceil(hi): those outside turns' bounds are outside it)
     assert np.allclose(ratio[few], 1 / factor, rtol=1e-13) and np.allclose(ratio[many], 1, rtol=1e-13)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x2=FAR2, y2=FAR), dict(x2=FAR, y2=FAR2), dict(x2=FAR2, y2=FAKE), dict(x2=FAKE, y=FAKE, y2=FAKE),
+    dict(x2=FAKE, y=FAKE, y2=FAR2)])
+def test_rotary_refuses_one_tensor_in_two_places(lib, bad):
+    """y and y2 in one place, or either in the place of the other tensor's input."""
+    a = rotary_args(**{"H2": 8, "x2_token": 512, "x2_head": 64, "y2_token": 512, "y2_head": 64, **bad})
+    assert lib.dsa_rotary(*a) == ops.DSA_ERR_VALUE
+    assert b"dsa_rotary" in lib.dsa_last_error()
