@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kWideThreads) kv4_widen_kernel(const uint32_t*
 // thread are under way at a time: their pages are loads that wait for loads.
 __global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* __restrict__ idx, const dsa::Kv8Geom g, int K,
                                                                 const int32_t* __restrict__ topk_length,
-                                                                int32_t* __restrict__ rows, int32_t* __restrict__ length) {
+                                                                int32_t* __restrict__ rows, int32_t* __restrict__ length,
+                                                                uint32_t* status) {
   const int t = blockIdx.x;
   const bool padding = t >= __ldg(g.cu + g.n_seqs);
   if (threadIdx.x == 0) length[t] = padding ? 0 : topk_length ? __ldg(topk_length + t) : K;
@@ -178,7 +179,10 @@ __global__ void __launch_bounds__(kWideThreads) kv4_rows_kernel(const int32_t* _
       id[k] = j < K ? __ldcs(idx + at + j) : -1;
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) id[k] = id[k] < 0 ? -1 : dsa::kv8_row(g, b, id[k]);
+    for (int k = 0; k < kAhead; ++k) {
+      id[k] = id[k] < 0 ? -1 : dsa::kv8_row(g, b, id[k]);
+      if (!dsa::check(id[k] < (g.n_blocks << g.lb), status)) id[k] = -1;
+    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int j = j0 + k * kWideThreads;
@@ -222,7 +226,7 @@ int launch_widened(const Params& p, const void* q, int T, int Dqk, int Dv, float
   if (rc == DSA_OK && paged) {
     auto* to = reinterpret_cast<int32_t*>(ws + size.k + size.v);
     auto* len = reinterpret_cast<int32_t*>(ws + size.k + size.v + size.rows);
-    kv4_rows_kernel<<<T, kWideThreads, 0, stream>>>(p.idx, p.g, p.K, p.topk_length, to, len);
+    kv4_rows_kernel<<<T, kWideThreads, 0, stream>>>(p.idx, p.g, p.K, p.topk_length, to, len, p.status);
     rc = dsa::launch_error("kv4_rows_kernel");
     rows = to, length = len;
   }

@@ -24,7 +24,7 @@ constexpr int kMaxTokens = 64;
 
 __global__ void __launch_bounds__(kThreads)
     kv4_write_kernel(const __nv_bfloat16* __restrict__ src, const dsa::Kv8Geom g, int Hc, int D, int tokens,
-                     uint32_t magic_row, uint8_t* __restrict__ cache, uint8_t* __restrict__ scale) {
+                     uint32_t magic_row, uint8_t* __restrict__ cache, uint8_t* __restrict__ scale, uint32_t* status) {
   constexpr int kAhead = 2;  // pieces here are 16 values: two lanes have a scale's 32
   __shared__ int rows[kMaxTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
@@ -74,8 +74,9 @@ __global__ void __launch_bounds__(kThreads)
       }
       if (i >= n) continue;
       const int t = dsa::fast_div(i, magic_row);
+      if (!dsa::check(t < tokens, status)) continue;
       const int row = rows[t];
-      if (row < 0) continue;
+      if (row < 0 || !dsa::check(row < (g.n_blocks << g.lb), status)) continue;
       const uint32_t e = dsa::kv4_scale_of(m);
       const float inv = dsa::kv4_inverse(e);
       const int64_t at = static_cast<int64_t>(row) * per + (i - t * per);
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(const uint8_t* __restrict__ cache, const uint8_t* __restrict__ scale, const dsa::Kv8Geom g, int Hc,
-                    int D, int tokens, uint32_t magic_row, __nv_bfloat16* __restrict__ out) {
+                    int D, int tokens, uint32_t magic_row, __nv_bfloat16* __restrict__ out, uint32_t* status) {
   __shared__ int rows[kMaxTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
   dsa::rows_of_tokens<kThreads>(g, t0, tokens, rows);
@@ -103,9 +104,9 @@ __global__ void __launch_bounds__(kThreads)
       const int i = i0 + j * kThreads;
       w[j] = 0, e[j] = 127;
       if (i < n) {
-        const int t = dsa::fast_div(i, magic_row), row = rows[t];
+        const int t = dsa::fast_div(i, magic_row), row = dsa::check(t < tokens, status) ? rows[t] : -2;
         if (row != -2) live |= 1u << j;
-        if (row >= 0) {
+        if (row >= 0 && dsa::check(row < (g.n_blocks << g.lb), status)) {
           const int64_t at = static_cast<int64_t>(row) * per + (i - t * per);
           w[j] = __ldcs(reinterpret_cast<const uint32_t*>(cache) + at);
           e[j] = __ldg(scale + (at >> 2));
@@ -173,7 +174,7 @@ extern "C" int dsa_kv4_write(const void* src, const int32_t* cu_seqlens, const i
   const int tokens = tokens_per_cta(T, Hc, D, sms);
   kv4_write_kernel<<<ctas_of(T, tokens), kThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(src), g, Hc, D, tokens, tokens == 1 ? 1 : dsa::magic_of(Hc * (D / 16)),
-      static_cast<uint8_t*>(cache), scale);
+      static_cast<uint8_t*>(cache), scale, dsa::device_status_ptr());
   return dsa::launch_error("kv4_write_kernel");
 }
 
@@ -192,6 +193,6 @@ extern "C" int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32
   const int tokens = tokens_per_cta(T, Hc, D, sms);
   kv4_read_kernel<<<ctas_of(T, tokens), kThreads, 0, stream>>>(
       static_cast<const uint8_t*>(cache), scale, g, Hc, D, tokens, tokens == 1 ? 1 : dsa::magic_of(Hc * (D / 8)),
-      static_cast<__nv_bfloat16*>(out));
+      static_cast<__nv_bfloat16*>(out), dsa::device_status_ptr());
   return dsa::launch_error("kv4_read_kernel");
 }

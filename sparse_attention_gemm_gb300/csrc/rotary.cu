@@ -42,6 +42,7 @@ struct Params {
   int per;               // units of a row
   uint32_t m_token, m_row, m_half;  // dsa::fast_div by a token's units, a row's and R / 2
   float mul, sign;
+  uint32_t* status;
 };
 
 // f / (2 pi) modulo 1, in units of 2^-64.  Of f = m 2^(e - 52): m times 2^11 / (2 pi), its
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
     for (int k = threadIdx.x >> 5; k < n_tok; k += kThreads / 32) {
       int b, c, pos;
       const bool inside = seqs.find(p.g, t0 + k, &b, &c, &pos);
-      if ((threadIdx.x & 31) == 0) place[k] = inside ? pos + (t0 + k - c) : kNone;
+      if ((threadIdx.x & 31) == 0 && dsa::check(k < kMaxTokens, p.status)) place[k] = inside ? pos + (t0 + k - c) : kNone;
     }
   }
   __syncthreads();
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
     float sn, cs;  // the upper half as a signed number is the angle in 2^-31 half turns
     sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
     constexpr int kPairs = PAIRS ? 4 : 8;  // of a unit
-    turn[k * half + j % kPairs * p.per + j / kPairs] = make_float2(cs * p.mul, sn * p.mul * p.sign);
+    if (dsa::check(k < n_tok && (k + 1) * half <= kMaxAngles && j / kPairs < p.per, p.status))
+      turn[k * half + j % kPairs * p.per + j / kPairs] = make_float2(cs * p.mul, sn * p.mul * p.sign);
   }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kAhead) {
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
       int k, u, h;
       const Side* s;
       where(i, &k, &u, &s, &h);
-      if (place[k] == kNone) continue;
+      if (!dsa::check(k < n_tok && u < p.per && h < (s == &p.a ? p.H : p.H2), p.status) || place[k] == kNone) continue;
       const float2* at = turn + k * half + u;
       __nv_bfloat16* dst = s->y + (t0 + k) * s->yt + h * s->yh + u * 8;
       uint32_t* w0 = reinterpret_cast<uint32_t*>(&v[j][0]);
@@ -251,6 +253,7 @@ extern "C" int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H,
   p.H = H, p.H2 = H2, p.R = R;
   p.per = interleaved ? R / 8 : R / 16;
   p.mul = mul, p.sign = inverse ? -1.f : 1.f;
+  p.status = dsa::device_status_ptr();
   // Tokens of a CTA: one round of its threads' units, or two rounds where one token takes more than
   // half of one (16,384 tokens of 65 rows of 64, pairs: 47 us, and 57 with one token a CTA; rounds
   // of 20 rows, where three tokens share one, gain nothing from two: 17.0 us), and two CTAs an SM at
