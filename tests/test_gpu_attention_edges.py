@@ -181,3 +181,22 @@ def test_statistics_under_a_sink_far_above_the_scores(dqk, dv, T, H, K, n, cache
     assert bool(((high["lse_kv"] - low["lse_kv"]).abs() <= tol).all()), "lse_kv"
     assert torch.equal(high["max_logits"], low["max_logits"])
     assert bool(((high["lse"] - dev(sink)).abs() <= tol).all()) and bool((high["out"].abs() <= 1e-20).all())
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,heads,K,block", [(6, 12, 1, 130, 1), (4, 16, 1, 1500, 16), (3, 24, 2, 65, 4), (2, 64, 1, 700, 64)])
+@pytest.mark.parametrize("hi", [129, 134])
+def test_large_scales_in_groups_of_16_heads(dqk, dv, T, H, heads, K, block, hi):
+    """Bytes above 128, whose factor takes two products: alone in a tile and among small ones, in rows whose scales begin
+    at either half of a word, in the first and the last of a row's blocks, in keys and values; whole and in splits."""
+    rng = np.random.default_rng(dqk + T + K + hi)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, heads, K, block, False)
+    assert ops.sparse_attn_fwd_kv4_workspace_size(T, H, heads, dqk, dv, K, block, k.shape[0]) == 0
+    flat = ks.reshape(-1, heads, dqk // 32)
+    many = rng.choice(flat.shape[0], flat.shape[0] // 3, replace=False)
+    flat[many, 0, rng.integers(0, dqk // 32, many.size)] = rng.integers(129, hi + 1, many.size)
+    flat[many[::2], heads - 1, 0], flat[many[1::2], heads - 1, dqk // 32 - 1] = hi, hi
+    if dqk == 256:
+        vs = kw["v_scale"].reshape(-1, heads, dv // 32)
+        vs[many, 0, rng.integers(0, dv // 32, many.size)] = rng.integers(129, hi + 1, many.size)
+    check_attention(q, k, ks, idx, sm * 2.0 ** (127 - hi), sink=rng.standard_normal(H).astype(np.float32), **kw)

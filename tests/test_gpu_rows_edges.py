@@ -1,4 +1,6 @@
 """Norm and rotary positions of rows and positions at the ends of their ranges, against their 64-bit definitions."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -6,7 +8,7 @@ import torch
 import rows_ref as R
 from gpu_util import DEV, cu_from_lengths, dev
 from sparse_attention_gemm_gb300 import ops
-from test_gpu_rows import EPS, f64, near
+from test_gpu_rows import EPS, apart, f64, near
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +95,73 @@ def test_sizes_beyond_32_bits_are_refused():
                 lambda: ops.sparse_attn_fwd_kv4(q, wide, wide[..., :18], idx, 0.1)):
         with pytest.raises(ValueError, match="32 bits"):
             bad()
+
+
+@pytest.mark.parametrize("fmt,group", [("e4m3", 128), ("mxfp8", 32)])
+@pytest.mark.parametrize("T,D", [(300001, 128), (9001, 1024)])
+def test_norm_in_8_bits_of_a_prompts_rows(fmt, group, T, D):
+    """As many rows as a prompt's indexer heads are."""
+    rng = np.random.default_rng(T)
+    x = apart(bf16(rng.standard_normal((T, D)) * np.exp2(rng.uniform(-6, 6, (T, 1)))), 64)
+    w = (rng.standard_normal(D) * np.exp2(rng.integers(-6, 6, D))).astype(np.float32)
+    _, _, y = R.norm(f64(x), w.astype(np.float64), EPS)
+    got = ops.rms_norm_fwd(x, dev(w), EPS, fmt=fmt)
+    s = got["scale"].cpu().numpy()
+    s = s.astype(np.float64) if fmt == "e4m3" else np.exp2(s.astype(np.float64) - 127)
+    g = y.reshape(T, D // group, group)
+    most = np.abs(g).max(2)
+    # a <= 448 * 2^e for the smallest e, where 448 = 1.75 * 2^8; either power within the norm's own error of a border
+    lo, hi = (np.exp2(np.ceil(np.log2(most * (1 + k * 4 * R.RSTD_REL) / 448))) for k in (-1, 1))
+    assert ((s == lo) | (s == hi)).all(), "scales"
+    v = torch.from_numpy(got["out"].cpu().numpy()).view(torch.float8_e4m3fn).double().numpy().reshape(g.shape) * s[:, :, None]
+    # E4M3: half a step is 2^-4 of the value, or half of 2^-9 below the normal range
+    tol = np.abs(g) * (2.0 ** -4 + 4 * R.RSTD_REL) + 2.0 ** -10 * s[:, :, None]
+    assert (np.abs(v - g) <= tol).all(), "codes"
+
+
+def inverse_pi(bits):
+    """1 / (2 pi) in units of 2^-bits, by Machin's formula: pi = 16 atan(1/5) - 4 atan(1/239)."""
+    one = 1 << (bits + 64)
+
+    def atan(n):
+        term, total, k = one // n, 0, 0
+        while term:
+            total += (-term if k & 1 else term) // (2 * k + 1)
+            term //= n * n
+            k += 1
+        return total
+    return (one << bits) // (2 * (16 * atan(5) - 4 * atan(239)))
+
+
+def exact_angle(p, f, turn=inverse_pi(320)):
+    """p * f modulo 2 pi in [-pi, pi], from the exact product of the integer and the double."""
+    part = (Fraction(int(p)) * Fraction(float(f)) * Fraction(turn, 1 << 320)) % 1
+    return 2 * np.pi * float(part - 1 if part > Fraction(1, 2) else part)
+
+
+@pytest.mark.parametrize("pairs", [True, False])
+@pytest.mark.parametrize("R_", [16, 64, 256])
+def test_rotary_angles_at_far_positions(R_, pairs):
+    """Positions whose product with f_i is itself rounded in 64 bits: the definition takes whole turns off exactly."""
+    assert exact_angle(1, 1.0) == 1.0 and abs(exact_angle(10 ** 9, 1.0) - np.arctan2(np.sin(1e9), np.cos(1e9))) < 1e-12
+    rng = np.random.default_rng(R_)
+    lens, pos = [4, 3, 5, 6, 2], [2 ** 31 - 1 - 3, -2 ** 31, 1 << 30, 131071, 987654321]
+    T, H, cu = sum(lens), 3, cu_from_lengths(lens)
+    at = [pos[b] + i for b, n in enumerate(lens) for i in range(n)]
+    x = bf16(rng.standard_normal((T, H, R_)))
+    first = np.arange(0, R_, 2) if pairs else np.arange(R_ // 2)
+    second = first + 1 if pairs else first + R_ // 2
+    x[:, 0, first], x[:, 0, second] = 1.0, 0.0  # cosines and sines themselves
+    f, _ = ops.rotary_inv_freq(R_)
+    for inverse in (False, True):
+        got = f64(ops.rotary(x, f, dev(cu), pos=dev(np.array(pos, np.int32)), interleaved=pairs, inverse=inverse)[0])
+        for t, p in enumerate(at):
+            theta = np.array([exact_angle(p, v) for v in f64(f)]) * (-1 if inverse else 1)
+            c, s = np.cos(theta), np.sin(theta)
+            a, b = f64(x[t])[:, first], f64(x[t])[:, second]
+            # the angle: 2^-25 of half a turn in fp32 and, of the fixed point, 2^-33 of a turn and p * 2^-61 of f_i
+            # (both below 2^-29); cosine, sine and products a few 2^-24 each
+            e = np.pi * 2.0 ** -25 + 2.0 ** -28 + 8 * R.F32
+            for want, i in ((a * c - b * s, first), (a * s + b * c, second)):
+                tol = e * (np.abs(a) + np.abs(b)) + R.BF16 * np.abs(want)
+                assert (np.abs(got[t][:, i] - want) <= tol).all(), (p, inverse)

@@ -4,7 +4,7 @@ import pytest
 
 from sparse_attention_gemm_gb300 import build as dsa_build
 from sparse_attention_gemm_gb300 import ops
-from test_kv8_abi import FAKE
+from test_kv8_abi import FAKE, ODD, attn_args
 from test_rows_abi import FAR, FAR2, rotary_args
 
 
@@ -37,3 +37,11 @@ def test_rotary_refuses_one_tensor_in_two_places(lib, bad):
     a = rotary_args(**{"H2": 8, "x2_token": 512, "x2_head": 64, "y2_token": 512, "y2_head": 64, **bad})
     assert lib.dsa_rotary(*a) == ops.DSA_ERR_VALUE
     assert b"dsa_rotary" in lib.dsa_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(kv_scale=ODD), dict(Dqk=256, Dv=256, v8=FAKE, v_scale=ODD),
+                                 dict(Dqk=256, Dv=256, v8=FAKE, v_scale=FAKE, kv_scale=ODD)])
+def test_cache_attention_refuses_misaligned_scales(lib, bad):
+    """A row's scale bytes are copied in words of up to 16 bytes."""
+    assert lib.dsa_sparse_attn_fwd_kv4(*attn_args(**bad)) == ops.DSA_ERR_VALUE
+    assert b"v_scale" in lib.dsa_last_error() and b"16-byte" in lib.dsa_last_error()
