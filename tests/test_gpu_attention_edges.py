@@ -10,7 +10,7 @@ import kv4_ref as R
 import test_gpu_kv8 as kv8
 from gpu_util import DEV, dev, dev_bf16, rand_bf16_bits
 from sparse_attention_gemm_gb300 import ops
-from test_gpu_kv4 import FORMS, attention_case, check_attention
+from test_gpu_kv4 import FORMS, attention_case, cache_of, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +200,59 @@ def test_large_scales_in_groups_of_16_heads(dqk, dv, T, H, heads, K, block, hi):
         vs = kw["v_scale"].reshape(-1, heads, dv // 32)
         vs[many, 0, rng.integers(0, dv // 32, many.size)] = rng.integers(129, hi + 1, many.size)
     check_attention(q, k, ks, idx, sm * 2.0 ** (127 - hi), sink=rng.standard_normal(H).astype(np.float32), **kw)
+
+
+def many_sequences(rng, T, n_seqs, pad, block, n_blocks, width):
+    """cu (empty sequences among them, `pad` rows behind the last), and a table with unmapped and foreign pages."""
+    cuts = np.sort(rng.integers(0, T - pad + 1, n_seqs - 1))
+    cu = np.concatenate([[0], cuts, [T - pad]]).astype(np.int32)
+    table = rng.integers(0, n_blocks, (n_seqs, width)).astype(np.int32)
+    table[rng.random(table.shape) < 0.1] = -1
+    table[rng.random(table.shape) < 0.05] = n_blocks + 3
+    return cu, table
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,n_seqs,pad", [(60, 16, 70, 50, 7), (5, 16, 1500, 40, 2), (3, 64, 2000, 2, 2), (150, 64, 70, 1100, 20),
+                                              (14, 64, 1500, 33, 3), (40, 12, 130, 3, 40)])
+def test_batches_of_many_sequences(dqk, dv, T, H, K, n_seqs, pad):
+    """More sequences than a warp looks up at once, empty ones, padding behind them (or nothing else), rows in splits."""
+    rng = np.random.default_rng(dqk + T + K + 3)
+    q, k, ks, idx, sm, kw = attention_case(rng, dqk, dv, T, H, 1, K, 16, False, n=600)
+    kw["cu"], kw["table"] = many_sequences(rng, T, n_seqs, pad, 16, k.shape[0], 20)
+    idx %= 20 * 16 + 40  # positions behind the table among them
+    check_attention(q, k, ks, idx, sm, sink=rng.standard_normal(H).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("dqk,dv", FORMS)
+@pytest.mark.parametrize("T,H,K,n_seqs,pad", [(700, 64, 700, 300, 45), (14000, 17, 33, 40, 700), (600, 100, 900, 1, 0), (330000, 20, 1, 9, 11)])
+def test_a_widened_cache_gives_the_bits_of_the_bf16_call(dqk, dv, T, H, K, n_seqs, pad):
+    rng = np.random.default_rng(dqk + T + K + 4)
+    block = 16
+    n = 600
+    n_blocks = n // block + 2
+    k, ks = (dev(a) for a in cache_of(rng, n_blocks, block, 1, dqk))
+    v, vs = (dev(a) for a in cache_of(rng, n_blocks, block, 1, dv)) if dqk == 256 else (None, None)
+    cu, table = many_sequences(rng, T, n_seqs, pad, block, n_blocks, 20)
+    q = torch.randn(T, H, dqk, device=DEV, generator=torch.Generator(DEV).manual_seed(T)).to(torch.bfloat16)
+    idx = rng.integers(-30, 20 * block + 40, (T, K)).astype(np.int32)
+    length = rng.integers(-3, K + 9, T).astype(np.int32)
+    sink = dev(rng.standard_normal(H).astype(np.float32))
+    need = ops.sparse_attn_fwd_kv4_workspace_size(T, H, 1, dqk, dv, K, block, n_blocks, True)
+    assert need >= n_blocks * block * dqk * 2 + T * K * 4
+    out, lse = torch.full((T, H, dv), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((T, H), 7.0, device=DEV)
+    got = ops.sparse_attn_fwd_kv4(q, k, ks, dev(idx), 0.05, topk_length=dev(length), sink=sink, v4=v, v_scale=vs, cu_seqlens=dev(cu),
+                                  block_table=dev(table), want_lse_kv=True, want_max_logits=True, out=out, lse=lse)
+    done = T - pad
+    assert bool((out[done:] == 7.0).all()) and bool((lse[done:] == 7.0).all())
+    seq = np.searchsorted(cu, np.arange(done), side="right") - 1
+    page = idx[:done] // block
+    there = (idx[:done] >= 0) & (page < table.shape[1])
+    blk = table[seq[:, None], np.where(there, page, 0)]
+    row = np.where(there & (blk >= 0) & (blk < n_blocks), blk * block + idx[:done] % block, -1).astype(np.int32)
+    every = dev(np.array([0, n_blocks * block], np.int32))
+    wide = [None if c is None else ops.kv4_read(c, s, every, n_blocks * block)[:, 0] for c, s in ((k, ks), (v, vs))]
+    want = ops.sparse_attn_fwd(q[:done], wide[0], dev(row), 0.05, topk_length=dev(length[:done]), sink=sink, v=wide[1], want_lse_kv=True,
+                               want_max_logits=True)
+    for name in ("out", *STATISTICS):
+        assert torch.equal(got[name][:done], want[name]), name
