@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_kernel(const Params p)
           if (st < w.hv) {
             p.lse[orow + st] = lse_v;
             if (p.lse_kv) p.lse_kv[orow + st] = lkv;
-            if (kMax) p.max_logits[orow + st] = max_logit_of(l, m_max);
+            if (kMax) p.max_logits[orow + st] = any ? max_logit(l, m_max) : -INFINITY;
           }
         }
         fac[st] = f;
@@ -844,9 +844,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_cache_kernel(const Params p)
   }
 }
 
-// Joins the splits of one (token, head) per CTA: with m the largest reference, a_s = 2^(m_s - m) l_s, l = sum_s a_s,
-// M the larger of m and the sink and z = 2^(m - M) l + 2^(sink - M), out = sum_s a_s 2^(m - M) O_s / z of the splits' means
-// O_s.  (l is lse_kv's, of the slots alone: against M it is nothing under a sink far above the scores.)
+// Joins the splits of one (token, head) per CTA: with M the largest of the references and the sink, a_s = 2^(m_s - M) l_s
+// and z = sum_s a_s + 2^(sink - M), out = sum_s a_s O_s / z of the splits' means O_s.  lse_kv is the slots' alone, whose
+// sum against a sink far above them is nothing: under a sink it is taken again against the largest reference.
 template <int DV>
 __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
@@ -866,12 +866,13 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
   const float sink = p.sink ? __ldg(p.sink + h) : -INFINITY, sk = sink * kLog2e;
   const bool any = __any_sync(0xffffffffu, have);
   const float M = fmaxf(m, sk);
-  const float a = have ? s.y * exp2f(s.x - m) : 0.f, down = any ? exp2f(m - M) : 0.f;
+  const float a = have ? s.y * exp2f(s.x - M) : 0.f;
   float l = a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float z = any ? l * down + exp2f(sk - M) : 1.f;
-  const float share = a * down / z;  // at most 1: a mean of means stays in range
+  const float z = any ? l + exp2f(sk - M) : 1.f;
+  const float share = a / z;  // at most 1: a mean of means stays in range
+  const bool under = p.lse_kv && any && sk > m;  // (the same in all lanes)
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.splits * DV) + threadIdx.x;
   for (int k = 0; k < p.splits; ++k) {
@@ -887,8 +888,19 @@ __global__ void __launch_bounds__(DV / 4) attn_cache_join_kernel(const Params p)
   reinterpret_cast<uint2*>(p.out + row * DV)[threadIdx.x] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   if (threadIdx.x == 0) {
     p.lse[row] = any ? (M + log2f(z)) * kLn2 : sink;
-    if (p.lse_kv) p.lse_kv[row] = any ? (m + log2f(l)) * kLn2 : INFINITY;
-    if (p.max_logits) p.max_logits[row] = max_logit_of(l, mx);
+    if (p.lse_kv && !under) p.lse_kv[row] = any ? (M + log2f(l)) * kLn2 : INFINITY;
+    if (p.max_logits) p.max_logits[row] = any ? max_logit(l, mx) : -INFINITY;
+  }
+  // (read again: kept beside the values, the sums would cost eight registers and with those a quarter of the CTAs)
+  if (under && threadIdx.x < 32) {
+    const float4 r = lane < p.splits ? p.part_s[row * p.splits + lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    float top = r.y != 0.f ? r.x : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float l_kv = r.y != 0.f ? r.y * exp2f(r.x - top) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l_kv += __shfl_xor_sync(0xffffffffu, l_kv, o);
+    if (lane == 0) p.lse_kv[row] = (top + log2f(l_kv)) * kLn2;
   }
 }
 

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
         if (first) {
           p.lse[orow + h] = lse_v;
           if (p.lse_kv) p.lse_kv[orow + h] = lkv;
-          if (p.max_logits) p.max_logits[orow + h] = max_logit_of(l, m_max[e]);
+          if (p.max_logits) p.max_logits[orow + h] = any ? max_logit(l, m_max[e]) : -INFINITY;
         }
       }
       // this lane's dims: 64 slice + 8 (2c + k) + j
@@ -495,9 +495,9 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
   }
   if (!split_up) return;
 
-  // ---- joined: with m the largest reference, a_s = 2^(m_s - m) l_s, l = sum_s a_s, M the larger of m and the sink and
-  // z = 2^(m - M) l + 2^(sink - M), out = sum_s a_s 2^(m - M) O_s / z of the splits' means O_s.  (l is lse_kv's, of the slots
-  // alone: against M it is nothing under a sink far above the scores.)  Each CTA takes its part of the values.
+  // ---- joined: with M the largest of the references and the sink, a_s = 2^(m_s - M) l_s and z = sum_s a_s + 2^(sink - M),
+  // out = sum_s a_s O_s / z of the splits' means O_s.  Each CTA takes its part of the values.  lse_kv is the slots' alone, whose
+  // sum against a sink far above them is nothing: under a sink it is taken again against the largest reference.
   cluster_sync();
   float* shares = reinterpret_cast<float*>(smem + N::kShares);
   for (int y = tid; y < N::kHeads * kMaxCluster; y += kBlock) {
@@ -514,16 +514,22 @@ __global__ void __launch_bounds__(kBlock, (Narrow<DQK, DV, SEP>::kPerSm)) attn_k
     }
     const float sink = p.sink && h < hv ? __ldg(p.sink + h0 + h) : -INFINITY, sk = sink * kLog2e;
     const float M = fmaxf(mm, sk);
-    const float a = have ? v.y * exp2f(v.x - mm) : 0.f, down = any ? exp2f(mm - M) : 0.f;
+    const float a = have ? v.y * exp2f(v.x - M) : 0.f;
     float l = a;
 #pragma unroll
     for (int o = 1; o < kMaxCluster; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float z = any ? l * down + exp2f(sk - M) : 1.f;
-    shares[y] = a * down / z;  // at most 1: a mean of means stays in range
+    const float z = any ? l + exp2f(sk - M) : 1.f;
+    shares[y] = a / z;  // at most 1: a mean of means stays in range
+    float l_kv = l;
+    if (p.lse_kv && __any_sync(0xffffffffu, sk > mm)) {
+      l_kv = have ? v.y * exp2f(v.x - mm) : 0.f;
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o <<= 1) l_kv += __shfl_xor_sync(0xffffffffu, l_kv, o);
+    }
     if (split == 0 && s == 0 && h < hv) {
       p.lse[orow + h] = any ? (M + log2f(z)) * kLn2 : sink;
-      if (p.lse_kv) p.lse_kv[orow + h] = any ? (mm + log2f(l)) * kLn2 : INFINITY;
-      if (p.max_logits) p.max_logits[orow + h] = max_logit_of(l, mx);
+      if (p.lse_kv) p.lse_kv[orow + h] = any ? (mm + log2f(l_kv)) * kLn2 : INFINITY;
+      if (p.max_logits) p.max_logits[orow + h] = any ? max_logit(l, mx) : -INFINITY;
     }
   }
   __syncthreads();

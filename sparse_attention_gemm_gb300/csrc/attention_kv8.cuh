@@ -162,11 +162,9 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint16_t& hi, 
   hi = e4m3x2_h2(h2_bits(h));
   lo = e5m2x2_h2(h2_bits(__hsub2(h, h2_of(h2_of_e4m3x2(hi)))));
 }
-// max_logits of a head whose weights' sum is l and whose largest score is mx (in powers of two; a
-// maximum passes over NaN): -inf without a slot, NaN where the sum is.
-__device__ __forceinline__ float max_logit_of(float l, float mx) {
-  return l != l ? l : l != 0.f ? mx * kLn2 : -INFINITY;
-}
+// max_logits of a head with slots, whose weights' sum is l and whose largest score is mx (in powers of two; a
+// maximum passes over NaN): NaN where the sum is.
+__device__ __forceinline__ float max_logit(float l, float mx) { return l == l ? mx * kLn2 : l; }
 
 // x (> 0, finite) as 2^e * f, f in (1/2, 1].
 __device__ __forceinline__ float2 scale_parts(float x) {

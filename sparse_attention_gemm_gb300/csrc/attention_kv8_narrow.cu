@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
           if (st < hv) {
             p.lse[orow + st] = n.lse;
             if (p.lse_kv) p.lse_kv[orow + st] = n.lse_kv;
-            if (p.max_logits) p.max_logits[orow + st] = max_logit_of(l, mx);
+            if (p.max_logits) p.max_logits[orow + st] = l != 0.f ? max_logit(l, mx) : -INFINITY;
           }
         }
       }
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_narrow_kernel(const Para
       if (d == 0) {
         p.lse[orow + h] = n.lse;
         if (p.lse_kv) p.lse_kv[orow + h] = n.lse_kv;
-        if (p.max_logits) p.max_logits[orow + h] = max_logit_of(l, mx);
+        if (p.max_logits) p.max_logits[orow + h] = l != 0.f ? max_logit(l, mx) : -INFINITY;
       }
     }
   }
