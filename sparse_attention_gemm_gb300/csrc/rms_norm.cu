@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdPara
   //   beside one of 2^57 at least, and eps is nothing beside it;
   // * below it: a mean and an eps that together are under 2^-100 leave a sum under 2^114, and squares that would have
   //   lost bits (under 2^-126) are whole.  From 2^-100 on what they lose is under 2^-49 of the mean.
-  const bool high = !(sq < INFINITY), low = mean < 0x1p-100f;
-  if (__any_sync(0xffffffffu, high || low)) {
+  // (one comparison for both and NaN: bits from those of 2^-100 on, below infinity's)
+  constexpr uint32_t kLow = 27u << 23;
+  if (__any_sync(0xffffffffu, __float_as_uint(mean) - kLow >= 0x7F800000u - kLow)) {
+    const bool high = !(sq < INFINITY), low = mean < 0x1p-100f;
     const float by = high ? 0x1p-100f : 0x1p100f;
     float again = 0.f;
 #pragma unroll
