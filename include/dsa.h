@@ -664,8 +664,9 @@ int dsa_kv4_read(const void* cache, const uint8_t* scale, const int32_t* cu_seql
  *   workspace: dsa_sparse_attn_fwd_kv4_workspace_size bytes (paged: whether there is a block
  *   table; 0 for many shapes: then it may be NULL), 256-byte aligned, contents ignored on entry; calls
  *   that may overlap need one each.  With one KV head and many slots beside the cache's rows it holds the
- *   cache's values in bf16 (at most 2^30 bytes) and the slots' rows: a call that reads each row
- *   often widens them once.
+ *   cache's values in bf16 (at most 2^30 bytes) and, with a block table, the slots' rows (4 T (K + 1) bytes
+ *   beside them, which nothing bounds): a call that reads each row often widens them once.  All n_blocks * block
+ *   rows count, not those that the batch's table names: a pool that is large beside the batch's slots is not widened.
  * Values are bf16 ones and the query enters as it is: weights exp(s_j) are rounded to
  * bf16 before they meet the values, sums are fp32, as in dsa_sparse_attn_fwd.
  * Weights times values are summed before they are divided by the weights' sum, a weight being at most 2^8:
@@ -696,11 +697,15 @@ int dsa_sparse_attn_fwd_kv4(const void* q, const void* kv4, const uint8_t* kv_sc
  *                     codes and descales that dsa_indexer_*_fp8 take;
  *     DSA_NORM_MXFP8  E4M3 codes, y_scale uint8 [T, D / 32] (E8M0): those of
  *                     dsa_indexer_*_mxfp8.
+ *     (Indexer rows that are rotated after their norm are normed to bf16, turned by dsa_rotary and
+ *     quantised by dsa_kv8_write with blocks of one row, a descale each; no call makes MXFP8 of those.)
  *     A scale is 2^e, e the smallest integer >= -126 with a <= 448 * 2^e of the largest
  *     finite |y| a it stands for; codes are e4m3(y / 2^e) to nearest even; infinities become +-448,
  *     NaN stays NaN.
  *   sum bf16 (out), row t at sum + t * ld_sum, or NULL: h, the next residual;
  *   rstd fp32 [T] (out) or NULL: for the backward pass.
+ * Finite h have their norm whatever their size: where the sum of squares leaves fp32's range it is taken again,
+ * scaled.  (x + residual beyond that range is infinite: rstd 0, NaN in its place and 0 in the row's others.)
  * y and sum may each be x or residual itself (same rows, same stride), not overlap them otherwise.
  * Shapes: T >= 0; D a multiple of 8 (E4M3: 128, MXFP8: 32), at most DSA_NORM_MAX_DIM;
  * strides multiples of 8 and at least D; eps finite > 0; x, residual, weight, sum and
@@ -762,7 +767,9 @@ int dsa_rotary(const void* x, int64_t x_token, int64_t x_head, int H, const void
  *   DSA_ROTARY_NTK     f_i of base * factor^(R / (R - 2));
  *   DSA_ROTARY_YARN    pairs that make more than beta_fast turns over the first
  *       `first` positions keep f_i, those of fewer than beta_slow take f_i / factor, those
- *       between blend linearly in i; mul = 0.1 ln(factor) + 1 (1 in the other forms).
+ *       between blend linearly in i; mul = 0.1 ln(factor) + 1 (1 in the other forms).  With whole heads rotated,
+ *       queries and keys, it scales scores by mul^2.  Where only a part of a head is rotated it would scale that
+ *       part of a score alone: pass 1 to dsa_rotary there and multiply the attention's scale by mul^2.
  * factor is ignored by PLAIN, first and the betas by all but YARN.
  * Shapes: R even in [2, DSA_ROTARY_MAX_DIM] (NTK: >= 4), base > 1, factor >= 1, first >= 1,
  * beta_fast > beta_slow > 0, all finite.  Errors: DSA_ERR_VALUE. */

@@ -599,11 +599,12 @@ int64_t cost_of(int units, int nt, int s) {
 
 // The splits of a row's slots where groups of 16 heads take less time than the tiles of 64, else 0.  Measured, in us, here / there, 576 dims:
 //   slots                  64          180          350          700         1400         2048
-//   1 row of 64 heads   6.8 / 11.3   9.7 / 14.8  10.5 / 14.6  10.3 / 15.6  12.5 / 17.1  13.0 / 17.2
+//   1 row of 64 heads   6.8 / 11.3   9.7 / 14.8  10.5 / 14.6  10.3 / 15.6  12.5 / 17.1  13.0 / 17.2 (*)
 //   10 rows             6.8 / 11.3  10.1 / 14.8  12.6 / 15.2  17.5 / 16.7  25.0 / 18.4  33.1 / 20.1
 //   40 rows             9.5 / 11.5  17.1 / 14.8  27.3 / 19.0  44.2 / 22.8  72.1 / 29.8  89.2 / 35.1
 //   16 rows of 16 heads 7.0 / 10.5   9.9 / 14.0  10.7 / 14.2  13.2 / 16.0  20.3 / 17.7  23.9 / 19.7
 //   100 rows            7.0 / 10.9  11.9 / 14.4  19.1 / 19.9  27.3 / 28.7  43.7 / 48.8  55.0 / 62.1
+// (* 12.5 to 13.4 by where the ids lie, and 13.9 in a decode step with lengths and a sink over 65,536 positions.)
 // (a key is widened once for 16 heads here, there for 64; tiles a quarter full cost what full ones do).  300 rows
 // of 16 heads x 2048 slots 160 / 132; one of 8192 slots 27.5 / 21.4, of 65,536 165 / 72: sixteen CTAs a unit are all there
 // are.  256 dims: 96 rows of 2 x 12 heads x 1027 slots 37 / 59, 1000 of 12 135 / 193, 16 of 64 heads x 700 14.6 / 14.0.

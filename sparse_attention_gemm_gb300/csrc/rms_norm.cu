@@ -10,10 +10,12 @@
 // a thread, so that each value is read once; sums are fp32.
 //
 // The bytes bound it.  16,384 rows of 4096 with a residual: 82 us, 6.6 TB/s.  64 rows of 4096
-// to 8 bits: 2.7 us, the chain of a load, two barriers and a store.  Backward, 8192 rows of 4096:
+// to 8 bits: 2.7 us, the chain of a load, two barriers and a store; 1,048,576 rows of 128 to 8 bits 125 us, 3.3 TB/s, where
+// the issue of instructions bounds it (70% of the slots).  Backward, 8192 rows of 4096:
 // 45 us, 5.9 TB/s, of which the join of dw's partial sums (one row of them a CTA, added in a fixed
 // order) takes 6; 24,216 rows of 256 9.4 us.  One row ahead is under way while a row is summed (66 us
-// without it, 53 with more CTAs than are resident).
+// without it, 53 with more CTAs than are resident).  Above 8192 wide it spills and loads no row ahead (2048 rows of
+// 16,384: 96 us, 2.1 TB/s).
 #include <algorithm>
 #include <climits>
 

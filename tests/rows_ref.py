@@ -74,7 +74,7 @@ def rotary(x, f, positions, pairs, inverse=False, mul=1.0):
     for t, p in enumerate(positions):
         if p is None:
             continue
-        # angle in turns with the integer part taken off exactly: p * f / (2 pi) in extended steps
+        # p * f in one rounded product, modulo the 64-bit 2 pi: what that leaves out is in e below
         theta = np.array([math.fmod(float(p) * float(v), 2 * math.pi) for v in f])
         if inverse:
             theta = -theta
