@@ -130,14 +130,14 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdPara
   float rstd = 1.f / sqrtf(mean);
   // Out of fp32's range the squares are summed again, of values 2^100 times smaller or larger.
   // * beyond it: of 16,384 values below 2^128 the sum is then below 2^70; those whose squares underflow are below 2^26
-  //   beside one of 2^57 at least, and eps is nothing beside it;
+  //   beside one of 2^57 at least (or an eps of the size);
   // * below it: a mean and an eps that together are under 2^-100 leave a sum under 2^114, and squares that would have
   //   lost bits (under 2^-126) are whole.  From 2^-100 on what they lose is under 2^-49 of the mean.
   // (one comparison for both and NaN: bits from those of 2^-100 on, below infinity's)
   constexpr uint32_t kLow = 27u << 23;
-  if (__any_sync(0xffffffffu, __float_as_uint(mean) - kLow >= 0x7F800000u - kLow)) {
-    const bool high = !(sq < INFINITY), low = mean < 0x1p-100f;
-    const float by = high ? 0x1p-100f : 0x1p100f;
+  const bool out = __float_as_uint(mean) - kLow >= 0x7F800000u - kLow;
+  if (__any_sync(0xffffffffu, out)) {
+    const float by = mean < INFINITY ? 0x1p100f : 0x1p-100f;
     float again = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k)
@@ -147,8 +147,7 @@ __global__ void __launch_bounds__(Cta<G>::kThreads) rms_fwd_kernel(const FwdPara
         again = fmaf(v, v, again);
       }
     again = group_sum<G>(again, red[1]) / static_cast<float>(p.D);
-    if (high) rstd = by / sqrtf(again);
-    else if (low) rstd = by / sqrtf(again + p.eps * by * by);
+    if (out) rstd = by / sqrtf(again + p.eps * by * by);
   }
   if (live && sub == 0 && p.rstd) p.rstd[t] = rstd;
   if (live && p.sum) {

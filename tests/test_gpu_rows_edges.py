@@ -77,6 +77,13 @@ def test_norm_with_an_eps_below_small_squares(D, eps):
     check_norm(bf16(x), rng.standard_normal(D).astype(np.float32), eps)
 
 
+@pytest.mark.parametrize("D", [8, 64, 512, 4096])
+def test_norm_with_an_eps_near_the_largest_number(D):
+    """Squares and an eps that are in fp32's range while their sum is not."""
+    x = np.random.default_rng(D).standard_normal((7, D)) * 10.0 ** np.array([19.2, 19, 18.5, 18, 25, 0, 37])[:, None]
+    check_norm(bf16(x), np.ones(D, np.float32), 3e38)
+
+
 def test_sizes_beyond_32_bits_are_refused():
     """The library's sizes are 32-bit: a larger one does not come in modulo 2^32."""
     far = 1 << 32
